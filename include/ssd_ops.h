@@ -143,6 +143,101 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
                                   int32_t max_seq, const void* wk, const void* wv, int32_t w_rows,
                                   int32_t H, int32_t Hkv, int32_t dh, void* out, void* stream);
 
+/* ---- Decoding with a tree of drafts: attention of the tree over the cache,
+ * eviction from the cache by accumulated attention weight, beam selection
+ * and the reordering of the beams' caches.  These calls allocate nothing:
+ * where a call needs scratch memory, the caller gives a workspace of device
+ * memory (256-byte aligned, at least what the call's _workspace function
+ * returns for the current device; fewer bytes are SSD_ERR_CAPACITY).  Its
+ * contents need no initialisation and mean nothing afterwards; calls that may
+ * overlap on the GPU need one each.  Each call can be captured into a CUDA
+ * graph.  Inputs that these calls read from device memory (parents, done)
+ * may hold any values, with the meanings below. */
+
+/* Attention of T drafted nodes over a cache of n_ctx rows.  1 <= T <= 1024,
+ * n_ctx >= 0, n_ctx + T <= max_seq, pos0 >= 0; dh 64 or 128.
+ * parents (device int32 [T]): parents[t] is the node that t follows,
+ * 0 <= parents[t] < t, or -1 where t follows the context itself.  Any other
+ * value makes t absent, and with it every node below it: padding rows.
+ * qkv fp32 [T][(H + 2 Hkv) dh] holds the raw projections (q, k, v rows,
+ * before RoPE; what ssd_op_linear_rows stores).  The call rotates q and k by
+ * rotate-half RoPE (base theta) to position pos0 + depth(t), depth(t) = the
+ * number of nodes above t, stores bf16(k), bf16(v) into row n_ctx + t of
+ * k_cache / v_cache ([Hkv][max_seq][dh] bf16; zeros for an absent node), and
+ * writes
+ *   out[t][h dh ..] = bf16(softmax(q K^T / sqrt(dh)) V)      (bf16 [T][H dh])
+ * over cache rows 0..n_ctx-1, the nodes above t, and t itself; query head h
+ * reads K/V head h / (H/Hkv).  An absent node's row is zeros.  Keys that a
+ * row does not see take no part in it, whatever they hold.  n_ctx and pos0
+ * differ when rows have been evicted.  Cache rows >= n_ctx + T are neither
+ * read nor written.
+ * weight_out (fp32 [Hkv][max_seq], nullable): the attention weight that each
+ * key received, summed over the present rows and the query heads of its
+ * group: rows j < n_ctx get weight_in[j] (fp32 [Hkv][max_seq]; NULL: zeros;
+ * may be weight_out itself) plus this call's sum, rows n_ctx..n_ctx+T-1 this
+ * call's sum alone; other rows stay as they are.
+ * Scores keep fp32 accuracy (q is split into two bf16 parts); probabilities
+ * are rounded to bf16 for the product with V.  The result of a call does not
+ * depend on timing (no floating-point atomics). */
+size_t ssd_op_tree_attention_workspace(int32_t T, int32_t n_ctx, int32_t H, int32_t Hkv,
+                                       int32_t dh);
+ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32_t T,
+                                 int32_t n_ctx, int32_t pos0, void* k_cache, void* v_cache,
+                                 int32_t max_seq, int32_t H, int32_t Hkv, int32_t dh, float theta,
+                                 const float* weight_in, float* weight_out, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction from a cache by accumulated attention weight: of rows 0..n-1 of
+ * each K/V head, keeps the first `sinks`, the last `recent` and, of those
+ * between, the ones with the largest weight (ties: the lower row; NaN counts
+ * as -infinity), `keep` rows in all, in their order:
+ *   kept[h][j]       the j-th kept row's index        (int32 [Hkv][keep])
+ *   k_out[h][j], v_out[h][j], weight_out[h][j] = its K, V and weight.
+ * sinks, recent >= 0; sinks + recent <= keep <= n <= max_seq;
+ * 1 <= keep <= max_out.  k, v [Hkv][max_seq][dh] and weight fp32
+ * [Hkv][max_seq]; k_out, v_out [Hkv][max_out][dh] and weight_out fp32
+ * [Hkv][max_out] (nullable), no overlap with the inputs; rows >= keep of the
+ * outputs stay as they are.  dtype: SSD_DTYPE_BF16 or SSD_DTYPE_FP32, the
+ * element type of the four caches; a row's bytes are a multiple of 16. */
+ssd_status ssd_op_cache_evict(const void* k, const void* v, const float* weight, int32_t n,
+                              int32_t keep, int32_t sinks, int32_t recent, int32_t max_seq,
+                              int32_t Hkv, int32_t dh, int32_t dtype, void* k_out, void* v_out,
+                              float* weight_out, int32_t max_out, int32_t* kept, void* stream);
+
+/* Beam selection: the W best candidates (b, v) of B beams by
+ *   scores[b] + (logits[b][v] - lse[b])
+ * (computed in 64 bits, so that no rounding reorders them; within a beam by
+ * logit; ties: the lower beam, then the lower token), best first:
+ *   tokens[w] = v, parents[w] = b, scores_out[w] = the score in fp32.
+ * logits fp32 [B][V]; lse: row b's log sum exp at lse[b * lse_stride]
+ * (&stats[0].lse with a stride of 12 reads ssd_row_stats records), NULL
+ * where logits are log-probabilities already.  done (int32 [B], nullable):
+ * beam b with done[b] != 0 has ended and stands for itself, one candidate
+ * with token end_id and score scores[b]; its logits are not read.
+ * done_out (int32 [W], nullable): 1 where the token is end_id (or nothing was
+ * left), else 0.  NaN and -infinity scores are no candidates; where fewer
+ * than W are left, the rest is tokens = parents = -1, scores_out = -infinity.
+ * 1 <= B <= 256, 1 <= W <= 256, V >= 1, -1 <= end_id < V, and end_id >= 0
+ * with done; logits, lse and scores 4-byte aligned, no other alignment. */
+size_t ssd_op_beam_select_workspace(int32_t B, int32_t V, int32_t W);
+ssd_status ssd_op_beam_select(const float* logits, int32_t B, int32_t V, const float* lse,
+                              int32_t lse_stride, const float* scores, const int32_t* done,
+                              int32_t end_id, int32_t W, int32_t* tokens, int32_t* parents,
+                              float* scores_out, int32_t* done_out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Reordering of the beams' caches after a selection: state w of the output
+ * takes rows start..stop-1 of every group of state parents[w] of the input.
+ * k, v [B][groups][max_seq][row_bytes] (groups = layers x K/V heads; v and
+ * v_out may both be NULL), k_out, v_out [W][groups][max_seq][row_bytes], no
+ * overlap; row_bytes a multiple of 16.  0 <= start <= stop <= max_seq; all
+ * other rows stay as they are, and so does state w where parents[w] (device
+ * int32 [W]) is outside 0..B-1. */
+ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* parents, int32_t B,
+                               int32_t W, int32_t groups, int32_t max_seq, int32_t start,
+                               int32_t stop, int32_t row_bytes, void* k_out, void* v_out,
+                               void* stream);
+
 /* Description of the most recent failed op call on this host thread. */
 const char* ssd_ops_last_error(void);
 

@@ -163,3 +163,85 @@ def resample_gap(P: np.ndarray, Q: np.ndarray, a: int, T: float, seed: int, rnd:
     g = -np.log(-np.log(uniforms(seed, n + a, rnd, 2, P.shape[1])))
     s = np.sort(logw + g)
     return float(s[-1] - s[-2])
+
+
+def tree_paths(parents):
+    """Per node the list of the nodes above it and itself, in order; None for
+    an absent node (its chain of parents does not end in -1)."""
+    paths = []
+    for t, p in enumerate(parents):
+        above = [] if p == -1 else (paths[p] if 0 <= p < t else None)
+        paths.append(None if above is None else above + [t])
+    return paths
+
+
+def tree_rows(qkv, parents, pos0, H, Hkv, dh, theta):
+    """(q [T, H, dh], k, v [T, Hkv, dh]) of a tree's nodes, rotated to
+    pos0 + depth, unrounded; zeros for absent nodes."""
+    m = OracleModel.__new__(OracleModel)
+    m.s = _shape(H, Hkv, dh, theta)
+    m.inv_freq = theta ** (-2.0 * np.arange(dh // 2, dtype=np.float64) / dh)
+    T = len(parents)
+    q, k, v = np.zeros((T, H, dh)), np.zeros((T, Hkv, dh)), np.zeros((T, Hkv, dh))
+    for t, path in enumerate(tree_paths(parents)):
+        if path is None:
+            continue
+        pos = pos0 + len(path) - 1
+        q[t] = m.rope(qkv[t, : H * dh].reshape(H, dh), pos)
+        k[t] = m.rope(qkv[t, H * dh:(H + Hkv) * dh].reshape(Hkv, dh), pos)
+        v[t] = qkv[t, (H + Hkv) * dh:].reshape(Hkv, dh)
+    return q, k, v
+
+
+def tree_attention(q, parents, n: int, K, V):
+    """Attention of a tree's nodes (q [T, H, dh], rotated) over a cache whose
+    rows 0..n-1 are the context and n + t node t's (K, V [Hkv, >= n + T, dh]):
+    node t sees the context, the nodes above it and itself.  Returns
+    (out [T, H, dh], mass [Hkv, n + T]: the attention weight of each key,
+    summed over nodes and the heads of a group, spread [T, H, dh]: sum p |v|)."""
+    T, H, dh = q.shape
+    Hkv = K.shape[0]
+    out, spread, mass = np.zeros((T, H, dh)), np.zeros((T, H, dh)), np.zeros((Hkv, n + T))
+    for t, path in enumerate(tree_paths(parents)):
+        if path is None:
+            continue
+        keys = np.concatenate([np.arange(n), n + np.array(path)]).astype(int)
+        for kvh in range(Hkv):
+            hs = slice(kvh * (H // Hkv), (kvh + 1) * (H // Hkv))
+            with np.errstate(all="ignore"):
+                s = q[t, hs] @ K[kvh, keys].T / np.sqrt(dh)
+                e = np.exp(s - s.max(axis=1, keepdims=True))
+                p = e / e.sum(axis=1, keepdims=True)
+                out[t, hs] = p @ V[kvh, keys]
+                spread[t, hs] = p @ np.abs(V[kvh, keys])
+            mass[kvh, keys] += p.sum(axis=0)
+    return out, mass, spread
+
+
+def cache_evict(weight, n: int, keep: int, sinks: int, recent: int) -> np.ndarray:
+    """Kept rows [Hkv, keep]: the first sinks, the last recent, and the
+    heaviest between (NaN as -inf, ties to the lower row), in order."""
+    kept = []
+    for row in np.asarray(weight, dtype=np.float64)[:, :n]:
+        w = np.where(np.isnan(row), -np.inf, row)
+        mid = sorted(range(sinks, n - recent), key=lambda i: (-w[i], i))
+        mid = sorted(mid[: keep - sinks - recent])
+        kept.append(list(range(sinks)) + mid + list(range(n - recent, n)))
+    return np.array(kept)
+
+
+def beam_select(logits, lse, scores, done, end_id: int, W: int):
+    """The W best of score_b + (z_bv - lse_b): a list of (token, parent,
+    score, ended), filled with (-1, -1, -inf, 1)."""
+    found = []
+    for b, z in enumerate(np.asarray(logits, dtype=np.float64)):
+        if done is not None and done[b]:
+            if scores[b] > -np.inf:
+                found.append((-float(scores[b]), b, 0.0, end_id))
+            continue
+        with np.errstate(invalid="ignore"):
+            s = float(scores[b]) + (z - float(lse[b]))
+        found += [(-s[v], b, -z[v], v) for v in range(len(z)) if s[v] > -np.inf]
+    found.sort()
+    got = [(v, b, -s, int(v == end_id)) for s, b, _, v in found[:W]]
+    return got + [(-1, -1, -np.inf, 1)] * (W - len(got))

@@ -10,6 +10,7 @@ PyTorch fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from typing import Dict, List, Optional, Sequence, Tuple
 
@@ -419,6 +420,135 @@ class _Ops:
                                                   _ptr(out),
                                                   stream_handle()))
         return out
+
+    @staticmethod
+    def _want(t: Optional[torch.Tensor], name: str, dtype, shape, device=None):
+        """Checks one tensor of a tree-decoding call (the library sees bare
+        pointers): type, shape (None: any extent) and device."""
+        if t is None:
+            return
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_cuda or (device is not None and t.device != device):
+            raise ValueError(f"{name}: expected a tensor on {device or 'a CUDA device'}")
+
+    @staticmethod
+    def _on(device: torch.device):
+        """The tensors' device made current where it is not (the call's stream
+        is that device's current stream)."""
+        if device.index == torch.cuda.current_device():
+            return contextlib.nullcontext()
+        return torch.cuda.device(device)
+
+    def tree_attention(self, qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv, dh, theta,
+                       weights=None, weights_out=None, out=None) -> torch.Tensor:
+        """Attention of a tree of drafted nodes over a cache of n_ctx rows
+        (ssd_op_tree_attention): qkv fp32 [T, (H + 2 Hkv) dh] raw projections,
+        parents int32 [T] (-1: follows the context), k_cache / v_cache bf16
+        [Hkv, max_seq, dh], whose rows n_ctx .. n_ctx + T - 1 are written.
+        Returns bf16 [T, H dh].  weights_out fp32 [Hkv, max_seq] receives
+        weights plus the attention weight of each key in this call; pass the
+        same tensor twice to accumulate in place."""
+        T, dev = qkv.shape[0], qkv.device
+        max_seq = k_cache.shape[1]
+        self._want(qkv, "qkv", torch.float32, (T, (H + 2 * Hkv) * dh))
+        self._want(parents, "parents", torch.int32, (T,), dev)
+        self._want(k_cache, "k_cache", torch.bfloat16, (Hkv, None, dh), dev)
+        self._want(v_cache, "v_cache", torch.bfloat16, (Hkv, max_seq, dh), dev)
+        self._want(weights, "weights", torch.float32, (Hkv, max_seq), dev)
+        self._want(weights_out, "weights_out", torch.float32, (Hkv, max_seq), dev)
+        with self._on(dev):
+            need = _lib().ssd_op_tree_attention_workspace(T, n_ctx, H, Hkv, dh)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            if out is None:
+                out = torch.empty(T, H * dh, dtype=torch.bfloat16, device=dev)
+            self._want(out, "out", torch.bfloat16, (T, H * dh), dev)
+            self._check(_lib().ssd_op_tree_attention(
+                _ptr(qkv), _ptr(parents), T, n_ctx, pos0, _ptr(k_cache), _ptr(v_cache), max_seq, H,
+                Hkv, dh, theta, _ptr(weights), _ptr(weights_out), _ptr(out), ws.data_ptr(), need,
+                stream_handle()))
+        return out
+
+    CACHE_DTYPES = {torch.bfloat16: _abi.SSD_DTYPE_BF16, torch.float32: _abi.SSD_DTYPE_FP32}
+
+    def cache_evict(self, k, v, weights, n, keep, k_out, v_out, weights_out=None, sinks=0,
+                    recent=0) -> torch.Tensor:
+        """Eviction by accumulated attention weight (ssd_op_cache_evict): of
+        rows 0 .. n-1 of every K/V head the first ``sinks``, the last
+        ``recent`` and the heaviest others go to k_out / v_out / weights_out in
+        their order, ``keep`` in all.  k, v [Hkv, max_seq, dh] bf16 or fp32,
+        weights fp32 [Hkv, max_seq].  Returns the kept rows, int32
+        [Hkv, keep]."""
+        if k.dtype not in self.CACHE_DTYPES or k.dim() != 3:
+            raise ValueError("k: expected a bf16 or fp32 tensor [Hkv, max_seq, dh]")
+        Hkv, max_seq, dh = k.shape
+        dev, max_out = k.device, k_out.shape[1]
+        self._want(v, "v", k.dtype, k.shape, dev)
+        self._want(weights, "weights", torch.float32, (Hkv, max_seq), dev)
+        self._want(k_out, "k_out", k.dtype, (Hkv, None, dh), dev)
+        self._want(v_out, "v_out", k.dtype, (Hkv, max_out, dh), dev)
+        self._want(weights_out, "weights_out", torch.float32, (Hkv, max_out), dev)
+        with self._on(dev):
+            kept = torch.empty(Hkv, max(keep, 0), dtype=torch.int32, device=dev)
+            self._check(_lib().ssd_op_cache_evict(
+                _ptr(k), _ptr(v), _ptr(weights), n, keep, sinks, recent, max_seq, Hkv, dh,
+                self.CACHE_DTYPES[k.dtype], _ptr(k_out), _ptr(v_out), _ptr(weights_out), max_out,
+                _ptr(kept), stream_handle()))
+        return kept
+
+    def beam_select(self, logits, scores, width, lse=None, done=None, end_id=-1):
+        """Beam selection (ssd_op_beam_select): the ``width`` best (beam,
+        token) by scores[b] + (logits[b, v] - lse[b]).  logits fp32 [B, V];
+        lse fp32 [B] (any stride), or the int32 [B, 12] row records of
+        lm_head, or None for log-probabilities; done int32 [B] marks ended
+        beams.  Returns (tokens, parents, scores, done) of the selected, best
+        first."""
+        B, V = logits.shape
+        dev = logits.device
+        self._want(logits, "logits", torch.float32, (B, V))
+        self._want(scores, "scores", torch.float32, (B,), dev)
+        self._want(done, "done", torch.int32, (B,), dev)
+        if lse is not None and lse.dtype == torch.int32:
+            self._want(lse, "lse", torch.int32, (B, 12), dev)
+            lse = lse.view(torch.float32)[:, 6]
+        self._want(lse, "lse", torch.float32, (B,), dev)
+        with self._on(dev):
+            need = _lib().ssd_op_beam_select_workspace(B, V, width)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            got = torch.empty(4, max(width, 0), dtype=torch.int32, device=dev)
+            tokens, parents, sc, ended = got[0], got[1], got[2].view(torch.float32), got[3]
+            self._check(_lib().ssd_op_beam_select(
+                _ptr(logits), B, V, None if lse is None else lse.data_ptr(),
+                1 if lse is None or B == 1 else lse.stride(0), _ptr(scores), _ptr(done), end_id,
+                width, _ptr(tokens), _ptr(parents), _ptr(sc), _ptr(ended), ws.data_ptr(), need,
+                stream_handle()))
+        return tokens, parents, sc, ended
+
+    def beam_reorder(self, k, v, parents, start, stop, k_out, v_out):
+        """Reordering of the beams' caches (ssd_op_beam_reorder): state w of
+        k_out / v_out takes rows start .. stop-1 of state parents[w].  k, v
+        [B, ..., max_seq, dh] (any dims between: layers, heads), k_out, v_out
+        [W, ..., max_seq, dh]; v and v_out may be None."""
+        dev, W = k.device, k_out.shape[0]
+        if k.dim() < 3:
+            raise ValueError("k: expected [B, ..., max_seq, dh]")
+        self._want(k, "k", k.dtype, k.shape)
+        self._want(k_out, "k_out", k.dtype, (W, *k.shape[1:]), dev)
+        if (v is None) != (v_out is None):
+            raise ValueError("v and v_out go together")
+        self._want(v, "v", k.dtype, k.shape, dev)
+        self._want(v_out, "v_out", k.dtype, k_out.shape, dev)
+        self._want(parents, "parents", torch.int32, (W,), dev)
+        groups = 1
+        for d in k.shape[1:-2]:
+            groups *= d
+        with self._on(dev):
+            self._check(_lib().ssd_op_beam_reorder(
+                _ptr(k), _ptr(v), _ptr(parents), k.shape[0], W, groups, k.shape[-2], start, stop,
+                k.shape[-1] * k.element_size(), _ptr(k_out), _ptr(v_out), stream_handle()))
+        return k_out, v_out
 
     def wait_selftest(self, polls: int = 4096) -> int:
         """Device bounded waits made to run out (ssd_op_wait_selftest);

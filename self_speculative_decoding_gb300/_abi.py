@@ -134,6 +134,13 @@ _SIGS = {
     "ssd_op_linear_rows": [_P, _P, _I, _I, _P, _I, _I, _P, _P, _P],
     "ssd_op_score_attention": [_P, _P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P],
     "ssd_op_linear_noalloc_last_error": [],
+    "ssd_op_tree_attention_workspace": [_I, _I, _I, _I, _I],
+    "ssd_op_tree_attention": [_P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, C.c_float, _P, _P, _P,
+                              _P, C.c_size_t, _P],
+    "ssd_op_cache_evict": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P],
+    "ssd_op_beam_select_workspace": [_I, _I, _I],
+    "ssd_op_beam_select": [_P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, C.c_size_t, _P],
+    "ssd_op_beam_reorder": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P],
 }
 
 EXPORTED = tuple(_SIGS)
@@ -151,7 +158,8 @@ def load(path: Optional[str] = None) -> C.CDLL:
     for name, args in _SIGS.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = C.c_char_p if name.endswith("last_error") else C.c_int
+        fn.restype = (C.c_char_p if name.endswith("last_error") else
+                      C.c_size_t if name.endswith("_workspace") else C.c_int)
     return lib
 
 

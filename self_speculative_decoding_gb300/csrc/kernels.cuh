@@ -350,4 +350,46 @@ cudaError_t launch_wait_selftest(const unsigned* never, int polls, int32_t* code
 // the norm-fused GEMV from an arbitrary x).
 cudaError_t launch_ss_partials(const float* x, int M, int D, float* ss, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Tree decoding beside the attention of tree.cuh: eviction from a cache
+// (evict.cu), beam selection and the reordering of the beams' caches (beam.cu).
+
+struct EvictArgs {
+  const uint4* k = nullptr;        // [Hkv][max_seq][units] 16-byte units
+  const uint4* v = nullptr;
+  const float* weight = nullptr;   // [Hkv][max_seq]
+  uint4* k_out = nullptr;          // [Hkv][max_out][units]
+  uint4* v_out = nullptr;
+  float* weight_out = nullptr;     // [Hkv][max_out], nullable
+  int32_t* kept = nullptr;         // [Hkv][keep]
+  int n = 0, keep = 0, sinks = 0, recent = 0, max_seq = 0, max_out = 0, Hkv = 0, units = 0;
+};
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
+
+struct BeamArgs {
+  const float* logits = nullptr;   // [B][V]
+  const float* lse = nullptr;      // row b at lse[b * lse_stride]; nullable: 0
+  int lse_stride = 1;
+  const float* scores = nullptr;   // [B]
+  const int32_t* done = nullptr;   // [B], nullable
+  int B = 0, V = 0, W = 0, end_id = -1;
+  uint64_t* lists = nullptr;       // workspace
+  int32_t* tokens = nullptr;       // [W]
+  int32_t* parents = nullptr;
+  float* scores_out = nullptr;
+  int32_t* done_out = nullptr;     // nullable
+};
+size_t beam_select_workspace(int B, int V, int W);
+cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s);
+
+struct ReorderArgs {
+  const uint4* k = nullptr;        // [B][groups][max_seq][units]
+  const uint4* v = nullptr;        // nullable
+  const int32_t* parents = nullptr;  // [W]
+  uint4* k_out = nullptr;          // [W][groups][max_seq][units]
+  uint4* v_out = nullptr;
+  int B = 0, W = 0, groups = 0, max_seq = 0, start = 0, stop = 0, units = 0;
+};
+cudaError_t launch_beam_reorder(const ReorderArgs& a, cudaStream_t s);
+
 }  // namespace ssd

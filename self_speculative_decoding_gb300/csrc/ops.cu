@@ -8,6 +8,7 @@
 
 #include "../../include/ssd_ops.h"
 #include "kernels.cuh"
+#include "tree.cuh"
 
 using namespace ssd;
 
@@ -85,6 +86,29 @@ ssd_status launch_norm_fused(int epi, LinearArgs a, cudaStream_t s, Scratch& xn,
   a.ss = nullptr;
   a.gain = nullptr;
   return cu(launch_gemv(IN_BF16, epi, a, s, false), what);
+}
+
+bool al4(const void* p) { return p && ((uintptr_t)p & 3u) == 0; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y ? x + na > y : y + nb > x;
+}
+
+ssd_status check_tree_sizes(int T, int n_ctx, int H, int Hkv, int dh) {
+  if (T < 1 || T > kTreeMaxNodes || n_ctx < 0 || H < 1 || Hkv < 1 || H % Hkv || H > 4096 ||
+      (dh != 64 && dh != 128))
+    return op_fail(SSD_ERR_INVALID_ARG, "tree_attention sizes");
+  return SSD_OK;
+}
+
+void tree_sizes(TreeArgs& a, int T, int n_ctx, int H, int Hkv, int dh) {
+  a.T = T;
+  a.n = n_ctx;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.dh = dh;
 }
 
 }  // namespace
@@ -395,6 +419,154 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
   a.out = (bf16*)out;
   a.w_rows = w_rows;
   return cu(launch_score_attn(a, n_cand, (cudaStream_t)stream), "score_attention");
+}
+
+size_t ssd_op_tree_attention_workspace(int32_t T, int32_t n_ctx, int32_t H, int32_t Hkv,
+                                       int32_t dh) {
+  if (check_tree_sizes(T, n_ctx, H, Hkv, dh) != SSD_OK) return 0;
+  TreeArgs a;
+  tree_sizes(a, T, n_ctx, H, Hkv, dh);
+  return tree_workspace(a, nullptr);
+}
+
+ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32_t T,
+                                 int32_t n_ctx, int32_t pos0, void* k_cache, void* v_cache,
+                                 int32_t max_seq, int32_t H, int32_t Hkv, int32_t dh, float theta,
+                                 const float* weight_in, float* weight_out, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  ssd_status r = check_tree_sizes(T, n_ctx, H, Hkv, dh);
+  if (r != SSD_OK) return r;
+  if (max_seq <= 0 || n_ctx > max_seq - T || pos0 < 0 || pos0 > INT32_MAX - T || !(theta > 0.f) ||
+      !std::isfinite(theta))
+    return op_fail(SSD_ERR_INVALID_ARG, "tree_attention: max_seq / pos0 / theta");
+  if (!al16(qkv) || !al4(parents) || !al16(k_cache) || !al16(v_cache) || !al16(out) ||
+      ((uintptr_t)workspace & 255u) || !workspace)
+    return op_fail(SSD_ERR_INVALID_ARG, "tree_attention pointers");
+  if ((weight_in && (!weight_out || !al4(weight_in))) || (weight_out && !al4(weight_out)))
+    return op_fail(SSD_ERR_INVALID_ARG, "tree_attention: weight_in needs weight_out");
+  TreeArgs a;
+  tree_sizes(a, T, n_ctx, H, Hkv, dh);
+  if (tree_workspace(a, workspace) > workspace_bytes)
+    return op_fail(SSD_ERR_CAPACITY, "tree_attention: workspace too small");
+  a.qkv = qkv;
+  a.parents = parents;
+  a.pos0 = pos0;
+  a.max_seq = max_seq;
+  a.kc = (bf16*)k_cache;
+  a.vc = (bf16*)v_cache;
+  a.w_in = weight_in;
+  a.w_out = weight_out;
+  a.out = (bf16*)out;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)dh));
+  for (int i = 0; i < dh / 2; ++i)
+    a.inv_freq[i] = std::pow((double)theta, -2.0 * i / dh) / 3.14159265358979323846;
+  return cu(launch_tree_attention(a, (cudaStream_t)stream), "tree_attention");
+}
+
+ssd_status ssd_op_cache_evict(const void* k, const void* v, const float* weight, int32_t n,
+                              int32_t keep, int32_t sinks, int32_t recent, int32_t max_seq,
+                              int32_t Hkv, int32_t dh, int32_t dtype, void* k_out, void* v_out,
+                              float* weight_out, int32_t max_out, int32_t* kept, void* stream) {
+  if (n < 1 || n > max_seq || keep < 1 || keep > n || keep > max_out || sinks < 0 || recent < 0 ||
+      sinks > keep || recent > keep - sinks || Hkv < 1 || Hkv > 65535 || dh < 1 || dh > 65536 ||
+      (dtype != SSD_DTYPE_BF16 && dtype != SSD_DTYPE_FP32))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_evict sizes");
+  const size_t row = (size_t)dh * (dtype == SSD_DTYPE_BF16 ? 2 : 4);
+  if (row % 16) return op_fail(SSD_ERR_INVALID_ARG, "cache_evict: a row's bytes must be a multiple of 16");
+  if (!al16(k) || !al16(v) || !al4(weight) || !al16(k_out) || !al16(v_out) || !al4(kept) ||
+      (weight_out && !al4(weight_out)))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_evict pointers");
+  const size_t in = row * Hkv * max_seq, o = row * Hkv * max_out;
+  const size_t win = (size_t)4 * Hkv * max_seq, wo = (size_t)4 * Hkv * max_out;
+  if (overlap(k, in, k_out, o) || overlap(k, in, v_out, o) || overlap(v, in, k_out, o) ||
+      overlap(v, in, v_out, o) || overlap(k_out, o, v_out, o) ||
+      (weight_out && overlap(weight, win, weight_out, wo)))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_evict: outputs overlap");
+  EvictArgs a;
+  a.k = (const uint4*)k;
+  a.v = (const uint4*)v;
+  a.weight = weight;
+  a.k_out = (uint4*)k_out;
+  a.v_out = (uint4*)v_out;
+  a.weight_out = weight_out;
+  a.kept = kept;
+  a.n = n;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.max_seq = max_seq;
+  a.max_out = max_out;
+  a.Hkv = Hkv;
+  a.units = (int)(row / 16);
+  return cu(launch_cache_evict(a, (cudaStream_t)stream), "cache_evict");
+}
+
+size_t ssd_op_beam_select_workspace(int32_t B, int32_t V, int32_t W) {
+  if (B < 1 || B > 256 || W < 1 || W > 256 || V < 1) return 0;
+  return beam_select_workspace(B, V, W);
+}
+
+ssd_status ssd_op_beam_select(const float* logits, int32_t B, int32_t V, const float* lse,
+                              int32_t lse_stride, const float* scores, const int32_t* done,
+                              int32_t end_id, int32_t W, int32_t* tokens, int32_t* parents,
+                              float* scores_out, int32_t* done_out, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (B < 1 || B > 256 || W < 1 || W > 256 || V < 1 || end_id < -1 || end_id >= V ||
+      (done && end_id < 0) || (lse && lse_stride < 1))
+    return op_fail(SSD_ERR_INVALID_ARG, "beam_select sizes");
+  if (!al4(logits) || !al4(scores) || (lse && !al4(lse)) || (done && !al4(done)) ||
+      !al4(tokens) || !al4(parents) || !al4(scores_out) || (done_out && !al4(done_out)) ||
+      !workspace || ((uintptr_t)workspace & 255u))
+    return op_fail(SSD_ERR_INVALID_ARG, "beam_select pointers");
+  if (workspace_bytes < beam_select_workspace(B, V, W))
+    return op_fail(SSD_ERR_CAPACITY, "beam_select: workspace too small");
+  BeamArgs a;
+  a.logits = logits;
+  a.lse = lse;
+  a.lse_stride = lse_stride;
+  a.scores = scores;
+  a.done = done;
+  a.B = B;
+  a.V = V;
+  a.W = W;
+  a.end_id = end_id;
+  a.lists = (uint64_t*)workspace;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.scores_out = scores_out;
+  a.done_out = done_out;
+  return cu(launch_beam_select(a, (cudaStream_t)stream), "beam_select");
+}
+
+ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* parents, int32_t B,
+                               int32_t W, int32_t groups, int32_t max_seq, int32_t start,
+                               int32_t stop, int32_t row_bytes, void* k_out, void* v_out,
+                               void* stream) {
+  if (B < 1 || W < 1 || groups < 1 || max_seq < 1 || start < 0 || stop < start || stop > max_seq ||
+      row_bytes < 16 || row_bytes % 16)
+    return op_fail(SSD_ERR_INVALID_ARG, "beam_reorder sizes");
+  if (!al16(k) || !al16(k_out) || !al4(parents) || (!v) != (!v_out) || (v && (!al16(v) || !al16(v_out))))
+    return op_fail(SSD_ERR_INVALID_ARG, "beam_reorder pointers");
+  const size_t state = (size_t)groups * max_seq * row_bytes, in = state * B, o = state * W;
+  if (overlap(k, in, k_out, o) ||
+      (v && (overlap(k, in, v_out, o) || overlap(v, in, k_out, o) || overlap(v, in, v_out, o) ||
+             overlap(k_out, o, v_out, o))))
+    return op_fail(SSD_ERR_INVALID_ARG, "beam_reorder: outputs overlap");
+  if (start == stop) return SSD_OK;
+  ReorderArgs a;
+  a.k = (const uint4*)k;
+  a.v = (const uint4*)v;
+  a.parents = parents;
+  a.k_out = (uint4*)k_out;
+  a.v_out = (uint4*)v_out;
+  a.B = B;
+  a.W = W;
+  a.groups = groups;
+  a.max_seq = max_seq;
+  a.start = start;
+  a.stop = stop;
+  a.units = row_bytes / 16;
+  return cu(launch_beam_reorder(a, (cudaStream_t)stream), "beam_reorder");
 }
 
 }  // extern "C"

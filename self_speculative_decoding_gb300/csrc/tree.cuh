@@ -1,0 +1,46 @@
+// Attention of a tree of drafted tokens over a cache: arguments, the layout
+// of the caller's workspace and the launches (tree.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace ssd {
+
+constexpr int kTreeMaxNodes = 1024;  // nodes (rows) of one tree
+constexpr int kTreeKeys = 128;       // keys per block
+constexpr int kTreeMaxHalf = 64;     // dh / 2 at most
+
+struct TreeArgs {
+  const float* qkv = nullptr;        // [T][(H + 2 Hkv) dh] raw projections
+  const int32_t* parents = nullptr;  // [T]
+  int T = 0, n = 0, pos0 = 0, H = 0, Hkv = 0, G = 0, dh = 0, max_seq = 0;
+  bf16* kc = nullptr;                // [Hkv][max_seq][dh]
+  bf16* vc = nullptr;
+  const float* w_in = nullptr;       // [Hkv][max_seq], nullable
+  float* w_out = nullptr;            // nullable: no weights
+  bf16* out = nullptr;               // [T][H dh]
+  float scale_log2 = 0.f;            // log2(e) / sqrt(dh)
+  // workspace
+  uint32_t* anc = nullptr;           // [T][anc_words] ancestors-and-self bits
+  int32_t* depth = nullptr;          // [T] ancestors above the node, -1 absent
+  uint8_t* vbad = nullptr;           // [Hkv][T] the node's V row holds inf or NaN
+  bf16* q = nullptr;                 // [2][Hkv][T G][dh]: the rotated query's high and low part
+  bf16* kt = nullptr;                // [Hkv][T][dh] the tree's K rows
+  bf16* vt = nullptr;                // [Hkv][T][dh] its V rows, inf and NaN as 0
+  float* lse = nullptr;              // [Hkv][T G] base-2 log-sum-exp of a row's scores
+  int anc_words = 0;
+  double inv_freq[kTreeMaxHalf];     // theta^(-2 i / dh) / pi
+};
+
+SSD_HD int tree_anc_words(int T) { return 4 * ((T + kTreeKeys - 1) / kTreeKeys); }
+
+// Sets the workspace pointers of `a` (sizes already set) from base and
+// returns the bytes used; with base NULL only the size is computed.
+size_t tree_workspace(TreeArgs& a, void* base);
+cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
+
+}  // namespace ssd

@@ -1,0 +1,113 @@
+"""The tree-decoding calls refuse what they do not document, on the host and
+before any launch (no GPU needed)."""
+
+import pytest
+
+INVALID, CAPACITY = 1, 3
+P = 0x10000  # 256-byte aligned addresses that are never read here
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from self_speculative_decoding_gb300 import build as b
+    b.build()
+    from self_speculative_decoding_gb300 import _abi
+    return _abi.load()
+
+
+TREE = dict(qkv=P, parents=P, T=4, n=10, pos0=10, k=P, v=P, max_seq=64, H=4, Hkv=2, dh=64,
+            theta=1e4, w_in=None, w_out=None, out=P, ws=P, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(T=0), dict(T=1025), dict(n=-1), dict(n=61), dict(n=2**31 - 1), dict(pos0=-1),
+    dict(pos0=2**31 - 2), dict(max_seq=0), dict(H=0), dict(Hkv=0), dict(H=3), dict(dh=96),
+    dict(theta=0.0), dict(theta=float("nan")), dict(theta=float("inf")), dict(qkv=None),
+    dict(qkv=P + 4), dict(parents=None), dict(parents=P + 2), dict(k=None), dict(v=P + 8),
+    dict(out=None), dict(ws=None), dict(ws=P + 16), dict(w_in=P), dict(w_out=P + 2),
+    dict(w_in=P + 1, w_out=P)])
+def test_tree_attention(lib, change):
+    a = {**TREE, **change}
+    assert lib.ssd_op_tree_attention(*a.values()) == INVALID
+    assert b"tree_attention" in lib.ssd_ops_last_error()
+
+
+def test_small_workspaces(lib):
+    need = lib.ssd_op_tree_attention_workspace(4, 10, 4, 2, 64)
+    assert need > 0
+    assert lib.ssd_op_tree_attention(*{**TREE, "ws_bytes": need - 1}.values()) == CAPACITY
+    assert lib.ssd_op_tree_attention_workspace(0, 10, 4, 2, 64) == 0
+    assert lib.ssd_op_tree_attention_workspace(4, 10, 4, 3, 64) == 0
+    need = lib.ssd_op_beam_select_workspace(4, 1000, 4)
+    assert need > 0
+    assert lib.ssd_op_beam_select(*{**SELECT, "ws_bytes": need - 1}.values()) == CAPACITY
+    assert lib.ssd_op_beam_select_workspace(4, 0, 4) == 0
+
+
+MB = 1 << 20
+EVICT = dict(k=16 * MB, v=32 * MB, w=P, n=50, keep=20, sinks=2, recent=5, max_seq=64, Hkv=2, dh=64,
+             dtype=0, k_out=48 * MB, v_out=64 * MB, w_out=80 * MB, max_out=32, kept=P, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(n=0), dict(n=65), dict(keep=0), dict(keep=51, max_out=64), dict(keep=33), dict(sinks=-1),
+    dict(recent=-1), dict(sinks=16), dict(sinks=2**31 - 1), dict(Hkv=0), dict(Hkv=65536),
+    dict(dh=4), dict(dh=0), dict(dtype=2), dict(k=None), dict(v=32 * MB + 8), dict(w=None),
+    dict(w=P + 2), dict(kept=None), dict(k_out=None), dict(v_out=None), dict(w_out=80 * MB + 1),
+    dict(k_out=16 * MB), dict(v_out=48 * MB + 1024), dict(k_out=32 * MB + 4096), dict(w_out=P)])
+def test_cache_evict(lib, change):
+    assert lib.ssd_op_cache_evict(*{**EVICT, **change}.values()) == INVALID
+    assert b"cache_evict" in lib.ssd_ops_last_error()
+
+
+SELECT = dict(logits=P, B=4, V=1000, lse=P, stride=1, scores=P, done=P, end_id=2, W=4, tokens=P,
+              parents=P, scores_out=P, done_out=P, ws=P, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(B=0), dict(B=257), dict(V=0), dict(W=0), dict(W=257), dict(stride=0), dict(end_id=-2),
+    dict(end_id=1000), dict(end_id=-1), dict(logits=None), dict(logits=P + 2), dict(scores=None),
+    dict(lse=P + 1), dict(done=P + 1), dict(tokens=None), dict(parents=None),
+    dict(scores_out=None), dict(done_out=P + 1), dict(ws=None), dict(ws=P + 8)])
+def test_beam_select(lib, change):
+    assert lib.ssd_op_beam_select(*{**SELECT, **change}.values()) == INVALID
+    assert b"beam_select" in lib.ssd_ops_last_error()
+
+
+REORDER = dict(k=16 * MB, v=32 * MB, parents=P, B=2, W=2, groups=4, max_seq=64, start=3, stop=9,
+               row_bytes=128, k_out=48 * MB, v_out=64 * MB, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(B=0), dict(W=0), dict(groups=0), dict(max_seq=0), dict(start=-1), dict(start=10),
+    dict(stop=65), dict(row_bytes=0), dict(row_bytes=24), dict(k=None), dict(k_out=None),
+    dict(v=None), dict(v_out=None), dict(v=32 * MB + 8), dict(parents=None), dict(parents=P + 1),
+    dict(k_out=16 * MB + 4096), dict(v_out=32 * MB), dict(v_out=48 * MB), dict(k_out=32 * MB)])
+def test_beam_reorder(lib, change):
+    assert lib.ssd_op_beam_reorder(*{**REORDER, **change}.values()) == INVALID
+    assert b"beam_reorder" in lib.ssd_ops_last_error()
+
+
+def test_an_empty_range_is_no_call(lib):
+    assert lib.ssd_op_beam_reorder(*{**REORDER, "start": 9}.values()) == 0
+
+
+def test_binding_refuses_tensors_it_cannot_take():
+    import torch
+    from self_speculative_decoding_gb300 import ops
+    f, i = torch.zeros(4, 8 * 64), torch.zeros(4, dtype=torch.int32)
+    c = torch.zeros(2, 64, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):       # host tensors
+        ops.tree_attention(f, i, c, c, 10, 10, 4, 2, 64, 1e4)
+    with pytest.raises(ValueError):       # parents of another type
+        ops.tree_attention(f, i.long(), c, c, 10, 10, 4, 2, 64, 1e4)
+    with pytest.raises(ValueError):       # too few columns
+        ops.tree_attention(f[:, :-1], i, c, c, 10, 10, 4, 2, 64, 1e4)
+    with pytest.raises(ValueError):
+        ops.cache_evict(c.half(), c, torch.zeros(2, 64), 10, 5, c, c)
+    with pytest.raises(ValueError):
+        ops.cache_evict(c, c, torch.zeros(2, 63), 10, 5, c, c)
+    with pytest.raises(ValueError):
+        ops.beam_select(f, torch.zeros(3), 4)
+    with pytest.raises(ValueError):
+        ops.beam_reorder(c, None, i, 0, 4, c, c)
