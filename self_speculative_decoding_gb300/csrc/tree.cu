@@ -26,7 +26,9 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
   __shared__ uint32_t bits[kTreeMaxNodes / 32];
   __shared__ int s_depth;
   __shared__ int bad[kPrepHeads];
+  pdl_trigger();
   const int t = blockIdx.x, tid = threadIdx.x;
+  if (t == 0 && blockIdx.y == 0 && tid == 0) *a.err = 0;
   for (int i = tid; i <= t; i += kPrepThreads) par[i] = a.parents[i];
   for (int i = tid; i < kTreeMaxNodes / 32; i += kPrepThreads) bits[i] = 0u;
   if (tid < kPrepHeads) bad[tid] = 0;
@@ -106,108 +108,6 @@ SSD_DI bool sees(const TreeArgs& a, int t, int node) {
   return (a.anc[(size_t)t * a.anc_words + (node >> 5)] >> (node & 31)) & 1u;
 }
 
-constexpr int kRowsPerCta = 8;
-constexpr int kTile = 64;
-
-// One warp per (row, query head), keys in tiles of 64 shared by eight rows of
-// a K/V head: each lane scores two keys, the running maximum and sum are
-// those of the warp, and each lane sums dh / 32 output columns.
-template <int DH>
-__global__ void __launch_bounds__(kRowsPerCta * 32)
-    tree_attn_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int kPad = DH + 2;  // one 4-byte bank further per key
-  constexpr int kCols = DH / 32;
-  __shared__ bf16 sk[kTile * kPad], sv[kTile * kPad];
-  __shared__ float sq[kRowsPerCta][DH];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y, rows = a.T * a.G;
-  const int r = blockIdx.x * kRowsPerCta + warp;
-  const bool live = r < rows;
-  const int t = live ? r / a.G : 0;
-  const bool present = live && a.depth[t] >= 0;
-  const size_t plane = (size_t)a.Hkv * rows * DH;
-  if (live) {
-    const bf16* q = a.q + ((size_t)kvh * rows + r) * DH;
-    for (int i = lane; i < DH; i += 32)
-      sq[warp][i] = __bfloat162float(q[i]) + __bfloat162float(q[plane + i]);
-  }
-  float m = -INFINITY, l = 0.f, o[kCols] = {};
-  const int total = a.n + a.T;
-  for (int k0 = 0; k0 < total; k0 += kTile) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < kTile * DH; e += blockDim.x) {
-      const int kk = k0 + e / DH, i = e % DH;
-      bf16 kx = __float2bfloat16(0.f), vx = kx;
-      if (kk < a.n) {
-        kx = a.kc[((size_t)kvh * a.max_seq + kk) * DH + i];
-        vx = a.vc[((size_t)kvh * a.max_seq + kk) * DH + i];
-      } else if (kk < total) {
-        kx = a.kt[((size_t)kvh * a.T + kk - a.n) * DH + i];
-        vx = a.vt[((size_t)kvh * a.T + kk - a.n) * DH + i];
-      }
-      sk[(e / DH) * kPad + i] = kx;
-      sv[(e / DH) * kPad + i] = vx;
-    }
-    __syncthreads();
-    if (!present) continue;
-    float s[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = lane + 32 * u, kk = k0 + key;
-      float acc = 0.f;
-      for (int i = 0; i < DH; ++i) acc = fmaf(sq[warp][i], __bfloat162float(sk[key * kPad + i]), acc);
-      const bool vis = kk < a.n || (kk < total && sees(a, t, kk - a.n));
-      s[u] = vis ? acc * a.scale_log2 : -INFINITY;
-    }
-    float bm = fmaxf(s[0], s[1]);
-    for (int w = 16; w; w >>= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, w));
-    const float mn = fmaxf(m, bm), base = mn == -INFINITY ? 0.f : mn;
-    const float corr = exp2f(m - base);  // m = -inf: 0 times an empty sum
-    l *= corr;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) o[c] *= corr;
-    m = mn;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float p = exp2f(s[u] - base);
-      float ps = p;
-      for (int w = 16; w; w >>= 1) ps += __shfl_xor_sync(~0u, ps, w);
-      l += ps;
-      for (int j = 0; j < 32; ++j) {
-        const float pj = __shfl_sync(~0u, p, j);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          o[c] = fmaf(pj, __bfloat162float(sv[(u * 32 + j) * kPad + c * 32 + lane]), o[c]);
-      }
-    }
-  }
-  if (!live) return;
-  const float lse = l > 0.f || isnan(l) ? m + log2f(l) : INFINITY;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) o[c] *= inv;
-  if (present) {
-    // inf and NaN of the V rows that this row sees (left out above)
-    for (int j = 0; j <= t; ++j) {
-      if (!a.vbad[(size_t)kvh * a.T + j] || !sees(a, t, j)) continue;
-      float acc = 0.f;
-      for (int i = 0; i < DH; ++i)
-        acc = fmaf(sq[warp][i], __bfloat162float(a.kt[((size_t)kvh * a.T + j) * DH + i]), acc);
-      const float p = exp2f(acc * a.scale_log2 - lse);
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const float v = __bfloat162float(a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + c * 32 + lane]);
-        if (!isfinite(v)) o[c] += p * v;
-      }
-    }
-  }
-  const int h = kvh * a.G + r % a.G;
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    a.out[((size_t)t * a.H + h) * DH + c * 32 + lane] = __float2bfloat16(o[c]);
-  if (lane == 0) a.lse[(size_t)kvh * rows + r] = present ? lse : INFINITY;
-}
-
 // Weights: thread = key; w_out = w_in + the sum over the group's rows of
 // 2^(score - lse), added in row order (the same bits on every call).
 template <int DH>
@@ -253,6 +153,8 @@ size_t tree_workspace(TreeArgs& a, void* base) {
     return base ? (void*)((char*)base + at) : nullptr;
   };
   const size_t rows = (size_t)a.T * a.G;
+  tree_split(a);
+  const size_t slots = (size_t)tree_slots(a);
   a.anc_words = tree_anc_words(a.T);
   a.anc = (uint32_t*)take((size_t)a.T * a.anc_words * 4);
   a.depth = (int32_t*)take((size_t)a.T * 4);
@@ -261,20 +163,19 @@ size_t tree_workspace(TreeArgs& a, void* base) {
   a.kt = (bf16*)take((size_t)a.Hkv * a.T * a.dh * sizeof(bf16));
   a.vt = (bf16*)take((size_t)a.Hkv * a.T * a.dh * sizeof(bf16));
   a.lse = (float*)take(a.Hkv * rows * 4);
+  a.part_o = (float*)take(slots * a.dh * 128 * 4);
+  a.part_m = (float*)take(slots * 128 * 4);
+  a.part_l = (float*)take(slots * 128 * 4);
+  a.err = (int*)take(4);
   return off;
 }
 
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
-  const int heads = a.H + 2 * a.Hkv, rows = a.T * a.G;
+  const int heads = a.H + 2 * a.Hkv;
   tree_prep_kernel<<<dim3(a.T, (heads + kPrepHeads - 1) / kPrepHeads), kPrepThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, a.Hkv);
-  if (a.dh == 128)
-    tree_attn_kernel<128><<<grid, kRowsPerCta * 32, 0, s>>>(a);
-  else
-    tree_attn_kernel<64><<<grid, kRowsPerCta * 32, 0, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.w_out) return e;
+  if ((e = launch_tree_attn_tc(a, s)) != cudaSuccess || !a.w_out) return e;
   const dim3 wgrid((a.n + a.T + kTreeKeys - 1) / kTreeKeys, a.Hkv);
   if (a.dh == 128)
     tree_weight_kernel<128><<<wgrid, kTreeKeys, 0, s>>>(a);

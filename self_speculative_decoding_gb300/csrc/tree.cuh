@@ -32,15 +32,27 @@ struct TreeArgs {
   bf16* kt = nullptr;                // [Hkv][T][dh] the tree's K rows
   bf16* vt = nullptr;                // [Hkv][T][dh] its V rows, inf and NaN as 0
   float* lse = nullptr;              // [Hkv][T G] base-2 log-sum-exp of a row's scores
+  float* part_o = nullptr;           // [slots][dh / 4][128 rows][4] unnormalised outputs
+  float* part_m = nullptr;           // [slots][128] base-2 maximum of the row's scores
+  float* part_l = nullptr;           // [slots][128] sum of 2^(score - maximum)
+  int* err = nullptr;                // non-zero: a bounded wait gave up
   int anc_words = 0;
+  // the rows in tiles of 128, the keys in blocks of 128 (the context's, then
+  // the tree's); a unit = (head, split, item): a run of key blocks for one tile
+  // (two = 0: blocks in turn to two streams) or a pair of tiles (two = 1: one
+  // stream each)
+  int tiles = 0, two = 0, items = 0, nb_ctx = 0, nb = 0, splits = 0, units = 0, ctas = 0;
   double inv_freq[kTreeMaxHalf];     // theta^(-2 i / dh) / pi
 };
 
 SSD_HD int tree_anc_words(int T) { return 4 * ((T + kTreeKeys - 1) / kTreeKeys); }
 
-// Sets the workspace pointers of `a` (sizes already set) from base and
-// returns the bytes used; with base NULL only the size is computed.
+// Sets the work split and the workspace pointers of `a` (sizes already set)
+// from base and returns the bytes used; with base NULL only the size.
 size_t tree_workspace(TreeArgs& a, void* base);
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
+void tree_split(TreeArgs& a);        // tree_attn_tc.cu
+int tree_slots(const TreeArgs& a);
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace ssd

@@ -1,0 +1,598 @@
+// Tree attention on the 5th-generation tensor cores: a tile of 128 query rows
+// (row = node G + head of the group) against blocks of 128 keys.
+//
+//   S = (Q_hi + Q_lo) K^T   tcgen05, fp32 in tensor memory
+//   P = 2^(S c - m)         one thread per row, bf16 over S's columns
+//   O += P V                tcgen05, P from tensor memory, V as it lies in the
+//                           cache (key-major: the MN-major operand form)
+//
+// Two streams of (S, P, O) share the matrix pipe: while one stream's softmax
+// runs, the other's products are issued.  With up to 128 rows the streams
+// take the key blocks in turn (both of the one tile); with more, each takes a
+// tile of its own and the pair reads every key block once.  m is raised, and
+// O rescaled, only when a block's maximum passes it by 8 (a factor of 256,
+// which fp32 sums and bf16 probabilities carry without loss).  The keys are
+// split into units over the SMs; a second kernel joins the units' partial
+// results in a fixed order.
+//
+// Warps 0-3 and 4-7: the streams' softmax; warp 8: TMA copies; warp 9: MMA.
+// Every wait is bounded: one that gives up sets the CTA's flag, every role
+// runs out, and the results become NaN.
+#include "tc_dev.cuh"
+#include "tree.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 320;
+constexpr int kPolls = 1 << 22;
+constexpr int kRegion = 128 * 128;              // [128 rows][64] bf16, 128-byte swizzle
+constexpr int kTileSmem = 224 * 1024;           // Q tiles, then the ring of K / V blocks
+constexpr int kMaxStages = 12;
+constexpr uint32_t kColO = 256;                 // TMEM: S0, S1 (P over each), O0, O1
+constexpr float kRaise = 8.f;
+
+SSD_DI bool flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
+SSD_DI float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+SSD_DI void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// V block [128 keys][dh] in 64-column regions as the MN-major B operand: 64
+// contiguous columns per atom (next atom one region on), 8 keys per 1024 bytes.
+SSD_DI uint64_t mn_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kRegion >> 4) << 16;           // leading offset: next 64 columns
+  d |= (uint64_t)(1024 >> 4) << 32;              // stride offset: next 8 keys
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;                        // 128-byte swizzle
+  return d;
+}
+__host__ __device__ constexpr uint32_t idesc_pv(int N) {
+  return idesc_bf16(128, N) | (1u << 16);        // B is MN-major
+}
+// D += A B with A in tensor memory.
+SSD_DI void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Block range of a unit and its place.
+struct Unit {
+  int kvh, item, split, b0, nb;
+};
+SSD_DI Unit unit_of(const TreeArgs& a, int u) {
+  Unit x;
+  // items fastest, then splits: CTAs that run together read the same keys
+  x.item = u % a.items;
+  const int r = u / a.items;
+  x.split = r % a.splits;
+  x.kvh = r / a.splits;
+  x.b0 = (int)((long long)x.split * a.nb / a.splits);
+  x.nb = (int)((long long)(x.split + 1) * a.nb / a.splits) - x.b0;
+  return x;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ,
+                        const __grid_constant__ CUtensorMap mK,
+                        const __grid_constant__ CUtensorMap mV,
+                        const __grid_constant__ CUtensorMap mTK,
+                        const __grid_constant__ CUtensorMap mTV,
+                        const __grid_constant__ TreeArgs a) {
+  constexpr int kRegs = DH / 64;                 // 64-column regions per row block
+  constexpr int kItem = kRegs * kRegion;         // bytes of a K or V block, or a Q plane
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kTileSmem);
+  uint64_t* qfull = bars;
+  uint64_t* qfree = bars + 1;
+  uint64_t* sfull = bars + 2;                    // [2] S written
+  uint64_t* pready = bars + 4;                   // [2] P written, O rescaled
+  uint64_t* ofull = bars + 6;                    // [2] the unit's last product done
+  uint64_t* mdone = bars + 8;
+  uint64_t* full = bars + 9;                     // [stages]
+  uint64_t* empty = full + kMaxStages;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kMaxStages);
+  int* fail = reinterpret_cast<int*>(tslot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qtiles = a.two ? 2 : 1;
+  const int stages = min(kMaxStages, (kTileSmem - qtiles * 2 * kItem) / kItem);
+  unsigned char* ring = sm + qtiles * 2 * kItem;
+
+  if (tid == 0) {
+    mbar_init(qfull, 1);
+    mbar_init(qfree, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&pready[s], 128);
+      mbar_init(&ofull[s], 1);
+    }
+    mbar_init(mdone, 1);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    *fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const int lag = a.two ? 1 : 2;                 // K blocks ahead of their V block
+
+  if (warp == 8) {
+    if (lane == 0) {
+      // ---- copies, in the order in which the products use them: K of the
+      // first `lag` blocks, then V of block i and K of block i + lag in turn
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mQ) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mK) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mV) : "memory");
+      int issued = 0, units = 0;                 // copies / units so far
+      bool ok = true, waited = false;
+      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
+        const Unit x = unit_of(a, u);
+        const int pro = min(lag, x.nb), mid = 2 * (x.nb - pro), total = 2 * x.nb;
+        bool q_sent = false;
+        auto send_q = [&]() {
+          if (!waited) {
+            pdl_wait();                          // the rows come from the preparation
+            waited = true;
+          }
+          if (units > 0 && !mbar_wait_n(qfree, (uint32_t)((units - 1) & 1), kPolls)) return false;
+          mbar_arrive_expect_tx(qfull, (uint32_t)(qtiles * 2 * kItem));
+          for (int t = 0; t < qtiles; ++t)
+            for (int p = 0; p < 2; ++p)
+              for (int r = 0; r < kRegs; ++r)
+                tma_load_3d(sm + (t * 2 + p) * kItem + r * kRegion, &mQ, r * 64,
+                            (x.item * qtiles + t) * 128, p * a.Hkv + x.kvh, qfull);
+          q_sent = true;
+          return true;
+        };
+        for (int i = 0; ok && i < total; ++i) {
+          int b;
+          bool is_v;
+          if (i < pro) {
+            b = i;
+            is_v = false;
+          } else if (i - pro < mid) {
+            is_v = ((i - pro) & 1) == 0;
+            b = (i - pro) / 2 + (is_v ? 0 : lag);
+          } else {
+            is_v = true;
+            b = mid / 2 + (i - pro - mid);
+          }
+          b += x.b0;
+          const bool ctx = b < a.nb_ctx;
+          const int st = issued % stages, use = issued / stages;
+          // the CTA's first copies of context blocks go out before the rows are
+          // ready; a later unit's first blocks before its rows are free (the
+          // slots they wait for need no query of this unit)
+          if (!q_sent && (units > 0 ? i >= lag : !ctx || use > 0)) ok = send_q();
+          if (ok && use > 0) ok = mbar_wait_n(&empty[st], (uint32_t)((use - 1) & 1), kPolls);
+          if (!ok || flagged(fail)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[st], (uint32_t)kItem);
+          const CUtensorMap* m = ctx ? (is_v ? &mV : &mK) : (is_v ? &mTV : &mTK);
+          const int row = (ctx ? b : b - a.nb_ctx) * kTreeKeys;
+          for (int r = 0; r < kRegs; ++r)
+            tma_load_3d(ring + (size_t)st * kItem + r * kRegion, m, r * 64, row, x.kvh, &full[st]);
+          ++issued;
+        }
+        if (ok && !q_sent) ok = send_q();
+        if (!q_sent) break;
+      }
+      if (!ok) atomicExch(fail, 1);
+      // what is still in flight lands before the memory is released
+      for (int i = max(0, issued - stages); i < issued; ++i)
+        mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
+      if (units > 0) mbar_wait_n(qfull, (uint32_t)((units - 1) & 1), ok ? kPolls : 1 << 16);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---- products
+      const uint32_t ids = idesc_bf16(128, 128), idp = idesc_pv(DH);
+      const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
+      int taken = 0, units = 0;
+      int np[2] = {0, 0};                        // P tiles taken per stream
+      bool ok = true;
+      // the ring slot in turn, landed
+      auto slot = [&](int i) {
+        ok = ok && mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
+        tc_fence_after();
+        return ra + (uint32_t)(i % stages) * kItem;
+      };
+      auto scores = [&](int s, uint32_t kb) {
+        const uint32_t q = qa + (uint32_t)(a.two ? s : 0) * 2 * kItem;
+#pragma unroll
+        for (int p = 1; p >= 0; --p)             // the low part first
+#pragma unroll
+          for (int ks = 0; ks < DH / 16; ++ks) {
+            const uint32_t rg = (uint32_t)(ks >> 2) * kRegion;
+            mma_bf16_tc(tmem + (uint32_t)s * 128, sw128_desc(q + p * kItem + rg) + 2 * (ks & 3),
+                        sw128_desc(kb + rg) + 2 * (ks & 3), ids, (p == 0 || ks > 0) ? 1u : 0u);
+          }
+        mma_commit(&sfull[s]);
+      };
+      auto values = [&](int s, uint32_t vb, bool first) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(tmem + kColO + (uint32_t)s * 128, tmem + (uint32_t)s * 128 + 8 * ks,
+                 mn_desc(vb + ks * 2048), idp, (!first || ks > 0) ? 1u : 0u);
+      };
+      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
+        const Unit x = unit_of(a, u);
+        ok = mbar_wait_n(qfull, (uint32_t)(units & 1), kPolls);
+        tc_fence_after();
+        // streams' block counts; a pair's second tile may lie beyond the rows
+        int cnt[2];
+        cnt[0] = a.two ? x.nb : (x.nb + 1) / 2;
+        cnt[1] = a.two ? (x.item * 2 + 1 < a.tiles ? x.nb : 0) : x.nb / 2;
+        int kslot = taken;
+        for (int s = 0; ok && s < 2; ++s)
+          if (cnt[s]) {
+            const uint32_t kb = slot(kslot);
+            if (!ok) break;
+            scores(s, kb);
+            if (!a.two || s == 1 || !cnt[1]) mma_commit(&empty[kslot++ % stages]);
+          }
+        taken = kslot;
+        for (int j = 0; ok && j < cnt[0]; ++j) {
+          // two tiles: V of block j and K of block j + 1 stay for both streams
+          const int v0 = taken;
+          for (int s = 0; ok && s < 2; ++s) {
+            if (j >= cnt[s]) continue;
+            const bool last_user = !a.two || s == 1 || !cnt[1];
+            const int vs = a.two ? v0 : taken;
+            const uint32_t vb = slot(vs);
+            ok = ok && mbar_wait_n(&pready[s], (uint32_t)(np[s]++ & 1), kPolls) && !flagged(fail);
+            if (!ok) break;
+            tc_fence_after();
+            values(s, vb, j == 0);
+            if (last_user) mma_commit(&empty[vs % stages]);
+            const bool more = j + 1 < cnt[s];
+            if (!more) mma_commit(&ofull[s]);
+            if (more) {
+              const int ks = vs + 1;
+              const uint32_t kb = slot(ks);
+              if (!ok) break;
+              scores(s, kb);
+              if (last_user) mma_commit(&empty[ks % stages]);
+            }
+            if (last_user) taken = vs + (more ? 2 : 1);
+          }
+        }
+        mma_commit(qfree);
+      }
+      if (!ok) atomicExch(fail, 1);
+      mma_commit(mdone);
+      mbar_wait_n(mdone, 0u, kPolls);
+    }
+  } else {
+    // ---- softmax: stream s, one thread per row of its tile
+    pdl_wait();
+    const int s = warp >> 2, r = tid & 127;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t col_s = (uint32_t)s * 128, col_o = kColO + (uint32_t)s * 128;
+    const float scale = a.scale_log2;
+    const int rows = a.T * a.G;
+    int n_s = 0, n_o = 0;
+    auto wait_w = [&](uint64_t* bar, uint32_t parity) -> bool {
+      bool okw = !flagged(fail) && mbar_wait_n(bar, parity, kPolls);
+      okw = __all_sync(0xffffffffu, okw);
+      if (!okw && lane == 0) atomicExch(fail, 1);
+      return okw;
+    };
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+      const Unit x = unit_of(a, u);
+      const int tile = a.two ? x.item * 2 + s : x.item;
+      const int cnt = a.two ? (tile < a.tiles ? x.nb : 0) : (x.nb + 1 - s) / 2;
+      const int row = tile * 128 + r;
+      const bool live = row < rows;
+      const bool warp_live = tile * 128 + (r & ~31) < rows;
+      const int t = live ? row / a.G : 0;
+      const uint32_t* anc = a.anc + (size_t)t * a.anc_words;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < cnt; ++j) {
+        ok = wait_w(&sfull[s], (uint32_t)(n_s++ & 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
+          const int b = x.b0 + (a.two ? j : 2 * j + s);
+          const int left = a.n - b * kTreeKeys;  // context keys from this block on
+          const bool whole = b < a.nb_ctx && left >= kTreeKeys;
+          uint4 mask = make_uint4(~0u, ~0u, ~0u, ~0u);
+          if (!whole) {
+            if (b >= a.nb_ctx) {
+              mask = live ? *reinterpret_cast<const uint4*>(anc + 4 * (b - a.nb_ctx))
+                          : make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              auto low = [&](int w) {
+                const int k = left - 32 * w;
+                return k >= 32 ? ~0u : (k > 0 ? (1u << k) - 1u : 0u);
+              };
+              mask = make_uint4(low(0), low(1), low(2), low(3));
+            }
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_pin32(sr[q]);
+          if (!whole) {
+            const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((mw[q] >> e) & 1u)) sr[q][e] = 0xff800000u;  // -infinity
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sr[q][e]));
+          const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float corr = raise ? ex2(m - bm) : 1.f;
+            if (raise) m = bm;
+            l *= corr;
+            if (j > 0) {  // the stream's products so far are done: S followed them
+#pragma unroll 1
+              for (int q = 0; q < DH / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16_nw(trow + col_o + q * 16, o);
+                tmem_wait_ld();
+                tmem_pin16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st16(trow + col_o + q * 16, o);
+              }
+            }
+          }
+          const float nm = m == -INFINITY ? 0.f : -m;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2(fmaf(__uint_as_float(sr[q][2 * e]), scale, nm));
+              const float p1 = ex2(fmaf(__uint_as_float(sr[q][2 * e + 1]), scale, nm));
+              ls[e & 3] += p0 + p1;
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(trow + col_s + q * 16, pk);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive_cta(&pready[s]);
+      }
+      if (!ok) break;
+      // ---- the unit's partial result
+      if (cnt > 0) {
+        ok = wait_w(&ofull[s], (uint32_t)(n_o++ & 1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const int slot = a.two ? (x.kvh * a.splits + x.split) * (a.items * 2) + tile
+                             : (x.kvh * a.splits + x.split) * 2 + s;
+      if (warp_live) {
+        float* po = a.part_o + (size_t)slot * DH * 128 + (size_t)r * 4;
+        if (cnt > 0) {
+#pragma unroll
+          for (int q = 0; q < DH / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32_nw(trow + col_o + q * 32, o);
+            tmem_wait_ld();
+            tmem_pin32(o);
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(po + (size_t)(q * 8 + e) * 512) =
+                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+        }
+        if (live) {
+          a.part_m[(size_t)slot * 128 + r] = m;
+          a.part_l[(size_t)slot * 128 + r] = l;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && flagged(fail)) atomicExch(a.err, 1);
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the units' partial results: warp = 32 rows of one K/V head, four
+// output columns per lane and row; the slots are added in order.
+constexpr int kJoinWarps = 8;
+template <int DH>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = a.T * a.G, kvh = blockIdx.y;
+  const int row = blockIdx.x * 32 + lane, c = blockIdx.z * kJoinWarps + warp;  // 16-byte chunk
+  if (row >= rows) return;
+  const int tile = row >> 7, r = row & 127, t = row / a.G;
+  const int per = a.two ? a.items * 2 : 2;       // slots per (head, split)
+  const int step = a.two ? per : 1, count = a.two ? a.splits : 2 * a.splits;
+  const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
+  const bool present = a.depth[t] >= 0, bad = *a.err != 0;
+  float m = -INFINITY;
+  for (int i = 0; i < count; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * step) * 128 + r]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < count; ++i) {
+    const size_t sl = s0 + (size_t)i * step;
+    const float pm = a.part_m[sl * 128 + r], pl = a.part_l[sl * 128 + r];
+    if (pl == 0.f) continue;                     // saw no key: its columns were not written
+    const float w = exp2f(pm - base);
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 + (size_t)c * 512 + r * 4);
+    l += pl * w;
+    o.x += v.x * w;
+    o.y += v.y * w;
+    o.z += v.z * w;
+    o.w += v.w * w;
+  }
+  const float lse = l != 0.f ? m + log2f(l) : INFINITY;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  if (present) {
+    // inf and NaN of the V rows that this row sees (left out of the products)
+    const uint8_t* flags = a.vbad + (size_t)kvh * a.T;
+    for (int j = 0; j <= t; ++j) {
+      if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+      const size_t plane = (size_t)a.Hkv * rows * DH;
+      const bf16* q = a.q + ((size_t)kvh * rows + row) * DH;
+      const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
+      float acc = 0.f;
+      for (int i = 0; i < DH; ++i)
+        acc = fmaf(__bfloat162float(q[i]) + __bfloat162float(q[plane + i]), __bfloat162float(k[i]), acc);
+      const float p = exp2f(acc * a.scale_log2 - lse);
+      for (int e = 0; e < 4; ++e) {
+        const float x = __bfloat162float(a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + c * 4 + e]);
+        if (!isfinite(x)) v[e] += p * x;
+      }
+    }
+  } else {
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+  }
+  if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
+  const int h = kvh * a.G + row % a.G;
+  uint2 packed = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.H + h) * DH + c * 4) = packed;
+  if (c == 0) a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
+}
+
+int sm_count() {
+  static int cached[kDeviceSlots] = {0};
+  const int dv = device_slot();
+  if (dv >= 0 && cached[dv]) return cached[dv];
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  else if (dv >= 0)
+    cached[dv] = sms;
+  return sms;
+}
+
+template <int DH>
+cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
+  EncodeTiled enc = tma_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const int rows = a.T * a.G;
+  auto map3 = [&](CUtensorMap* m, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t s2) {
+    const cuuint64_t row = DH * sizeof(bf16);
+    const cuuint64_t dims[3] = {DH, d1, d2};
+    const cuuint64_t strides[2] = {row, row * s2};
+    const cuuint32_t box[3] = {64, 128, 1};      // rows beyond d1 read as zero
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  CUtensorMap mQ, mK, mV, mTK, mTV;
+  const cuuint64_t n = a.n ? a.n : 1;            // no context: never read
+  if (!map3(&mQ, a.q, rows, 2 * a.Hkv, rows) || !map3(&mK, a.kc, n, a.Hkv, a.max_seq) ||
+      !map3(&mV, a.vc, n, a.Hkv, a.max_seq) || !map3(&mTK, a.kt, a.T, a.Hkv, a.T) ||
+      !map3(&mTV, a.vt, a.T, a.Hkv, a.T))
+    return cudaErrorInvalidValue;
+  const size_t smem = (size_t)kTileSmem + 1024 + 512;
+  static bool ready[kDeviceSlots] = {};
+  const int dv = device_slot();
+  if (dv < 0 || !ready[dv]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        tree_attn_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dv >= 0) ready[dv] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(a.ctas);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH>, mQ, mK, mV, mTK, mTV, a);
+  if (e != cudaSuccess) return e;
+  lc.gridDim = dim3((rows + 31) / 32, a.Hkv, DH / 4 / kJoinWarps);
+  lc.blockDim = dim3(kJoinWarps * 32);
+  lc.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&lc, tree_join_kernel<DH>, a);
+}
+
+}  // namespace
+
+// Splits the key blocks so that the units of all heads and row tiles fill the
+// SMs in as few block steps as possible: a wave of units takes as long as its
+// longest run of blocks plus about three for the start and the hand-over.
+void tree_split(TreeArgs& a) {
+  const int rows = a.T * a.G, sms = sm_count();
+  a.tiles = (rows + 127) / 128;
+  a.two = a.tiles > 1;
+  a.items = a.two ? (a.tiles + 1) / 2 : 1;
+  a.nb_ctx = (a.n + kTreeKeys - 1) / kTreeKeys;
+  a.nb = a.nb_ctx + (a.T + kTreeKeys - 1) / kTreeKeys;
+  const long long lanes = (long long)a.Hkv * a.items;
+  long long best = -1;
+  for (int s = 1; s <= a.nb && s <= 160; ++s) {
+    const long long waves = (lanes * s + sms - 1) / sms;
+    // a stream takes every other block of a single tile's run
+    const long long len = (a.nb + s - 1) / s, steps = a.two ? len : (len + 1) / 2;
+    const long long cost = waves * (steps + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.splits = s;
+    }
+  }
+  a.units = (int)(lanes * a.splits);
+  a.ctas = a.units < sms ? a.units : sms;
+}
+
+int tree_slots(const TreeArgs& a) { return a.Hkv * a.splits * (a.two ? a.items * 2 : 2); }
+
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s) {
+  return a.dh == 128 ? launch<128>(a, s) : launch<64>(a, s);
+}
+
+}  // namespace ssd
