@@ -104,45 +104,6 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
     if (h >= a.H + a.Hkv) a.vbad[(size_t)(h - a.H - a.Hkv) * a.T + t] = (uint8_t)bad[h - h0];
 }
 
-SSD_DI bool sees(const TreeArgs& a, int t, int node) {
-  return (a.anc[(size_t)t * a.anc_words + (node >> 5)] >> (node & 31)) & 1u;
-}
-
-// Weights: thread = key; w_out = w_in + the sum over the group's rows of
-// 2^(score - lse), added in row order (the same bits on every call).
-template <int DH>
-__global__ void __launch_bounds__(kTreeKeys) tree_weight_kernel(const __grid_constant__ TreeArgs a) {
-  __shared__ float sq[DH];
-  const int kvh = blockIdx.y, kk = blockIdx.x * kTreeKeys + threadIdx.x;
-  const int total = a.n + a.T, rows = a.T * a.G;
-  const size_t plane = (size_t)a.Hkv * rows * DH;
-  float kx[DH];
-  if (kk < total) {
-    const bf16* k = kk < a.n ? a.kc + ((size_t)kvh * a.max_seq + kk) * DH
-                             : a.kt + ((size_t)kvh * a.T + kk - a.n) * DH;
-#pragma unroll
-    for (int i = 0; i < DH; ++i) kx[i] = __bfloat162float(k[i]);
-  }
-  float sum = 0.f;
-  for (int r = 0; r < rows; ++r) {
-    const bf16* q = a.q + ((size_t)kvh * rows + r) * DH;
-    __syncthreads();
-    for (int i = threadIdx.x; i < DH; i += kTreeKeys)
-      sq[i] = __bfloat162float(q[i]) + __bfloat162float(q[plane + i]);
-    __syncthreads();
-    const float lse = a.lse[(size_t)kvh * rows + r];
-    if (kk >= total || (kk >= a.n && !sees(a, r / a.G, kk - a.n))) continue;
-    float acc = 0.f;
-#pragma unroll
-    for (int i = 0; i < DH; ++i) acc = fmaf(sq[i], kx[i], acc);
-    if (lse != INFINITY) sum += exp2f(acc * a.scale_log2 - lse);
-  }
-  if (kk < total) {
-    const size_t o = (size_t)kvh * a.max_seq + kk;
-    a.w_out[o] = kk < a.n && a.w_in ? a.w_in[o] + sum : sum;
-  }
-}
-
 }  // namespace
 
 size_t tree_workspace(TreeArgs& a, void* base) {
@@ -176,12 +137,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if ((e = launch_tree_attn_tc(a, s)) != cudaSuccess || !a.w_out) return e;
-  const dim3 wgrid((a.n + a.T + kTreeKeys - 1) / kTreeKeys, a.Hkv);
-  if (a.dh == 128)
-    tree_weight_kernel<128><<<wgrid, kTreeKeys, 0, s>>>(a);
-  else
-    tree_weight_kernel<64><<<wgrid, kTreeKeys, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_tree_weight_tc(a, tree_sms(), s);
 }
 
 }  // namespace ssd

@@ -2,6 +2,7 @@
 // of the caller's workspace and the launches (tree.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -53,6 +54,11 @@ size_t tree_workspace(TreeArgs& a, void* base);
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 void tree_split(TreeArgs& a);        // tree_attn_tc.cu
 int tree_slots(const TreeArgs& a);
+int tree_sms();                      // SMs of the current device
+// Tensor map of 128-row boxes of [d2][stride rows][dh] bf16, d1 rows of each
+// seen (the others read as zero).
+bool tree_map(CUtensorMap* m, const void* base, int dh, int d1, int d2, int stride);
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_weight_tc(const TreeArgs& a, int sms, cudaStream_t s);
 
 }  // namespace ssd

@@ -444,6 +444,7 @@ template <int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     tree_join_kernel(const __grid_constant__ TreeArgs a) {
   pdl_wait();
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = a.T * a.G, kvh = blockIdx.y;
   const int row = blockIdx.x * 32 + lane, c = blockIdx.z * kJoinWarps + warp;  // 16-byte chunk
@@ -500,39 +501,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (c == 0) a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
 }
 
-int sm_count() {
-  static int cached[kDeviceSlots] = {0};
-  const int dv = device_slot();
-  if (dv >= 0 && cached[dv]) return cached[dv];
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    cudaGetLastError();
-  else if (dv >= 0)
-    cached[dv] = sms;
-  return sms;
-}
-
 template <int DH>
 cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
-  EncodeTiled enc = tma_encoder();
-  if (!enc) return cudaErrorNotSupported;
   const int rows = a.T * a.G;
-  auto map3 = [&](CUtensorMap* m, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t s2) {
-    const cuuint64_t row = DH * sizeof(bf16);
-    const cuuint64_t dims[3] = {DH, d1, d2};
-    const cuuint64_t strides[2] = {row, row * s2};
-    const cuuint32_t box[3] = {64, 128, 1};      // rows beyond d1 read as zero
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
   CUtensorMap mQ, mK, mV, mTK, mTV;
-  const cuuint64_t n = a.n ? a.n : 1;            // no context: never read
-  if (!map3(&mQ, a.q, rows, 2 * a.Hkv, rows) || !map3(&mK, a.kc, n, a.Hkv, a.max_seq) ||
-      !map3(&mV, a.vc, n, a.Hkv, a.max_seq) || !map3(&mTK, a.kt, a.T, a.Hkv, a.T) ||
-      !map3(&mTV, a.vt, a.T, a.Hkv, a.T))
+  const int n = a.n ? a.n : 1;                   // no context: never read
+  if (!tree_map(&mQ, a.q, DH, rows, 2 * a.Hkv, rows) || !tree_map(&mK, a.kc, DH, n, a.Hkv, a.max_seq) ||
+      !tree_map(&mV, a.vc, DH, n, a.Hkv, a.max_seq) || !tree_map(&mTK, a.kt, DH, a.T, a.Hkv, a.T) ||
+      !tree_map(&mTV, a.vt, DH, a.T, a.Hkv, a.T))
     return cudaErrorInvalidValue;
   const size_t smem = (size_t)kTileSmem + 1024 + 512;
   static bool ready[kDeviceSlots] = {};
@@ -563,11 +539,37 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+int tree_sms() {
+  static int cached[kDeviceSlots] = {0};
+  const int dv = device_slot();
+  if (dv >= 0 && cached[dv]) return cached[dv];
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  else if (dv >= 0)
+    cached[dv] = sms;
+  return sms;
+}
+
+bool tree_map(CUtensorMap* m, const void* base, int dh, int d1, int d2, int stride) {
+  EncodeTiled enc = tma_encoder();
+  const cuuint64_t row = dh * sizeof(bf16);
+  const cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)d1, (cuuint64_t)d2};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)stride};
+  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Splits the key blocks so that the units of all heads and row tiles fill the
 // SMs in as few block steps as possible: a wave of units takes as long as its
 // longest run of blocks plus about three for the start and the hand-over.
 void tree_split(TreeArgs& a) {
-  const int rows = a.T * a.G, sms = sm_count();
+  const int rows = a.T * a.G, sms = tree_sms();
   a.tiles = (rows + 127) / 128;
   a.two = a.tiles > 1;
   a.items = a.two ? (a.tiles + 1) / 2 : 1;

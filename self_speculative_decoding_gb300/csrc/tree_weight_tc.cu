@@ -1,0 +1,322 @@
+// Attention weight received by each key of a tree attention, on the
+// 5th-generation tensor cores:
+//   w_out[key] = w_in[key] + sum over the group's rows of 2^(s c - lse_row).
+// The scores are computed again, transposed (S^T = K Q^T: one key per tensor
+// memory lane, one row per column), so that a key's sum is one thread's sum
+// over its columns: no exchange between threads and a fixed order.
+//
+// Unit = two blocks of 128 keys of one K/V head; warps 0-3 and 4-7 take a
+// block each, every tile of 128 rows passes both (a Q tile read from L2
+// serves 256 keys).  Up to two Q tiles stay in shared memory for all of a
+// CTA's units of a head.  Warp 8: TMA copies, warp 9: MMA.  Waits are bounded;
+// one that gives up makes the CTA's weights NaN.
+#include "tc_dev.cuh"
+#include "tree.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 320;
+constexpr int kPolls = 1 << 22;
+constexpr int kRegion = 128 * 128;
+constexpr int kTileSmem = 224 * 1024;            // Q tiles (hi, lo), then the ring of K blocks
+constexpr int kMaxStages = 12;
+
+SSD_DI bool flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
+SSD_DI float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Barrier of one stream's 128 threads; true if any of them passed true.
+SSD_DI bool stream_any(int s, bool x) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(s + 1), "r"(128), "r"((int)x)
+      : "memory");
+  return r != 0;
+}
+
+SSD_DI void stream_sync(int s) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(s + 1), "r"(128) : "memory");
+}
+
+struct Range {
+  int u0, u1;
+};
+SSD_DI Range my_units(const TreeArgs& a) {
+  const long long total = (long long)a.Hkv * ((a.nb + 1) / 2);
+  return {(int)(blockIdx.x * total / gridDim.x), (int)((blockIdx.x + 1) * total / gridDim.x)};
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_weight_tc_kernel(const __grid_constant__ CUtensorMap mQ,
+                          const __grid_constant__ CUtensorMap mK,
+                          const __grid_constant__ CUtensorMap mTK,
+                          const __grid_constant__ TreeArgs a) {
+  constexpr int kRegs = DH / 64;
+  constexpr int kItem = kRegs * kRegion;
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  float* nlse = reinterpret_cast<float*>(sm + kTileSmem);  // [stream][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(nlse + 256);
+  uint64_t* qfull = bars;                        // [2]
+  uint64_t* qempty = bars + 2;                   // [2]
+  uint64_t* sfull = bars + 4;                    // [stream][buffer]
+  uint64_t* sfree = bars + 8;
+  uint64_t* mdone = bars + 12;
+  uint64_t* full = bars + 13;
+  uint64_t* empty = full + kMaxStages;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kMaxStages);
+  int* fail = reinterpret_cast<int*>(tslot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = a.T * a.G;
+  const int qslots = a.tiles > 1 ? 2 : 1;
+  const bool resident = a.tiles <= qslots;       // Q stays for all units of a head
+  const int stages = min(kMaxStages, (kTileSmem - qslots * 2 * kItem) / kItem);
+  unsigned char* ring = sm + qslots * 2 * kItem;
+  const int pairs = (a.nb + 1) / 2;
+  const Range rg = my_units(a);
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qempty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sfree[s], 128);
+    }
+    mbar_init(mdone, 1);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    *fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int issued = 0, qissued = 0;
+      bool ok = true;
+      auto send_q = [&](int kvh, int tile) {
+        const int sl = qissued % qslots, use = qissued / qslots;
+        if (use > 0 && !mbar_wait_n(&qempty[sl], (uint32_t)((use - 1) & 1), kPolls)) return false;
+        mbar_arrive_expect_tx(&qfull[sl], 2u * kItem);
+        for (int p = 0; p < 2; ++p)
+          for (int r = 0; r < kRegs; ++r)
+            tma_load_3d(sm + (sl * 2 + p) * kItem + r * kRegion, &mQ, r * 64, tile * 128,
+                        p * a.Hkv + kvh, &qfull[sl]);
+        ++qissued;
+        return true;
+      };
+      for (int u = rg.u0; ok && u < rg.u1; ++u) {
+        const int kvh = u / pairs, b0 = (u - kvh * pairs) * 2, nblk = min(2, a.nb - b0);
+        if (u == rg.u0) pdl_wait();              // Q and the tree's K rows
+        // Q of a new head before its keys: its slots wait for the old head's
+        // products only, and these for nothing of this unit
+        if (resident && (u == rg.u0 || u % pairs == 0))
+          for (int t = 0; ok && t < a.tiles; ++t) ok = send_q(kvh, t);
+        for (int s = 0; ok && s < nblk; ++s) {
+          const int b = b0 + s, st = issued % stages, use = issued / stages;
+          if (use > 0) ok = mbar_wait_n(&empty[st], (uint32_t)((use - 1) & 1), kPolls);
+          if (!ok || flagged(fail)) {
+            ok = false;
+            break;
+          }
+          const bool ctx = b < a.nb_ctx;
+          mbar_arrive_expect_tx(&full[st], (uint32_t)kItem);
+          for (int r = 0; r < kRegs; ++r)
+            tma_load_3d(ring + (size_t)st * kItem + r * kRegion, ctx ? &mK : &mTK, r * 64,
+                        (ctx ? b : b - a.nb_ctx) * kTreeKeys, kvh, &full[st]);
+          ++issued;
+        }
+        if (!resident)
+          for (int t = 0; ok && t < a.tiles; ++t) ok = !flagged(fail) && send_q(kvh, t);
+      }
+      if (!ok) atomicExch(fail, 1);
+      for (int i = max(0, issued - stages); i < issued; ++i)
+        mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
+      for (int i = max(0, qissued - qslots); i < qissued; ++i)
+        mbar_wait_n(&qfull[i % qslots], (uint32_t)((i / qslots) & 1), kPolls);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
+      int taken = 0, qtaken = 0;
+      int cs[2] = {0, 0};                        // score tiles per stream
+      bool ok = true;
+      for (int u = rg.u0; ok && u < rg.u1; ++u) {
+        const int kvh = u / pairs, b0 = (u - kvh * pairs) * 2, nblk = min(2, a.nb - b0);
+        for (int s = 0; ok && s < nblk; ++s) {
+          const int i = taken + s;
+          ok = mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
+        }
+        for (int t = 0; ok && t < a.tiles; ++t) {
+          const int qi = qtaken + t, sl = qi % qslots;
+          ok = mbar_wait_n(&qfull[sl], (uint32_t)((qi / qslots) & 1), kPolls);
+          const int cols = min(128, (rows - t * 128 + 15) / 16 * 16);
+          const uint32_t id = idesc_bf16(128, cols);
+          for (int s = 0; ok && s < nblk; ++s) {
+            const int c = cs[s]++, buf = c & 1;
+            if (c >= 2) ok = mbar_wait_n(&sfree[s * 2 + buf], (uint32_t)((c / 2 - 1) & 1), kPolls);
+            if (!ok || flagged(fail)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t kb = ra + (uint32_t)((taken + s) % stages) * kItem;
+            const uint32_t qb = qa + (uint32_t)sl * 2 * kItem;
+#pragma unroll
+            for (int p = 1; p >= 0; --p)
+#pragma unroll
+              for (int ks = 0; ks < DH / 16; ++ks) {
+                const uint32_t o = (uint32_t)(ks >> 2) * kRegion;
+                mma_bf16_tc(tmem + (uint32_t)(s * 256 + buf * 128), sw128_desc(kb + o) + 2 * (ks & 3),
+                            sw128_desc(qb + p * kItem + o) + 2 * (ks & 3), id,
+                            (p == 0 || ks > 0) ? 1u : 0u);
+              }
+            mma_commit(&sfull[s * 2 + buf]);
+          }
+          if (ok && !resident) mma_commit(&qempty[sl]);
+        }
+        for (int s = 0; ok && s < nblk; ++s) mma_commit(&empty[(taken + s) % stages]);
+        taken += nblk;
+        if (!resident) {
+          qtaken += a.tiles;
+        } else if ((u + 1) % pairs == 0) {       // the head's last unit
+          for (int t = 0; ok && t < a.tiles; ++t) mma_commit(&qempty[(qtaken + t) % qslots]);
+          qtaken += a.tiles;
+        }
+      }
+      if (!ok) atomicExch(fail, 1);
+      mma_commit(mdone);
+      mbar_wait_n(mdone, 0u, kPolls);
+    }
+  } else {
+    // one key per thread.  Every thread passes every barrier: a wait that
+    // gives up only turns the sums into NaN.
+    pdl_wait();
+    const int s = warp >> 2, r = tid & 127;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)s * 256;
+    const float scale = a.scale_log2;
+    int c = 0;
+    bool ok = true;
+    for (int u = rg.u0; u < rg.u1; ++u) {
+      const int kvh = u / pairs, b = (u - kvh * pairs) * 2 + s;
+      if (b >= a.nb) continue;
+      const bool ctx = b < a.nb_ctx;
+      const int key = ctx ? b * kTreeKeys + r : a.n + (b - a.nb_ctx) * kTreeKeys + r;
+      const bool live = key < (ctx ? a.n : a.n + a.T);
+      const size_t o = (size_t)kvh * a.max_seq + key;
+      const float before = live && ctx && a.w_in ? a.w_in[o] : 0.f;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < a.tiles; ++t, ++c) {
+        const int buf = c & 1, cols = min(128, rows - t * 128);
+        float* nl = nlse + s * 128;
+        // rows that are absent, or beyond the last, take no part
+        const float x = r < cols ? -a.lse[(size_t)kvh * rows + t * 128 + r] : -INFINITY;
+        stream_sync(s);                          // the tile before has been read
+        nl[r] = x;
+        const bool some = stream_any(s, x == -INFINITY);
+        ok = ok && !flagged(fail) && mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
+        const bool all_ok = __all_sync(0xffffffffu, ok);
+        if (!all_ok) {
+          if (lane == 0) atomicExch(fail, 1);
+          ok = false;
+        } else {
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q * 32 < cols; ++q) {
+            uint32_t v[32];
+            tmem_ld32_nw(trow + (uint32_t)(buf * 128 + q * 32), v);
+            tmem_wait_ld();
+            tmem_pin32(v);
+            if (ctx && !some) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 n4 = *reinterpret_cast<const float4*>(nl + q * 32 + e);
+                sum[0] += ex2(fmaf(__uint_as_float(v[e]), scale, n4.x));
+                sum[1] += ex2(fmaf(__uint_as_float(v[e + 1]), scale, n4.y));
+                sum[2] += ex2(fmaf(__uint_as_float(v[e + 2]), scale, n4.z));
+                sum[3] += ex2(fmaf(__uint_as_float(v[e + 3]), scale, n4.w));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float n1 = nl[q * 32 + e];
+                bool on = n1 != -INFINITY;       // NaN stays: its row is NaN
+                if (!ctx && on) {
+                  const int node = (t * 128 + q * 32 + e) / a.G;
+                  const uint32_t w = a.anc[(size_t)node * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
+                  on = (w >> lane) & 1u;
+                }
+                if (on) sum[e & 3] += ex2(fmaf(__uint_as_float(v[e]), scale, n1));
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive_cta(&sfree[s * 2 + buf]);
+      }
+      if (live) a.w_out[o] = ok ? before + ((sum[0] + sum[1]) + (sum[2] + sum[3])) : NAN;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int DH>
+cudaError_t launch(const TreeArgs& a, int sms, cudaStream_t st) {
+  CUtensorMap mQ, mK, mTK;
+  const int rows = a.T * a.G;
+  if (!tree_map(&mQ, a.q, DH, rows, 2 * a.Hkv, rows) ||
+      !tree_map(&mK, a.kc, DH, a.n ? a.n : 1, a.Hkv, a.max_seq) ||
+      !tree_map(&mTK, a.kt, DH, a.T, a.Hkv, a.T))
+    return cudaErrorInvalidValue;
+  const size_t smem = (size_t)kTileSmem + 1024 + 1024 + 512;
+  static bool ready[kDeviceSlots] = {};
+  const int dv = device_slot();
+  if (dv < 0 || !ready[dv]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        tree_weight_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dv >= 0) ready[dv] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  const long long units = (long long)a.Hkv * ((a.nb + 1) / 2);
+  lc.gridDim = dim3((unsigned)(units < sms ? units : sms));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, tree_weight_tc_kernel<DH>, mQ, mK, mTK, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_weight_tc(const TreeArgs& a, int sms, cudaStream_t s) {
+  return a.dh == 128 ? launch<128>(a, sms, s) : launch<64>(a, sms, s);
+}
+
+}  // namespace ssd
