@@ -11,10 +11,11 @@
 namespace ssd {
 namespace {
 
-constexpr int kPieceThreads = 256;
-constexpr int kPieceItems = 16;
-constexpr int kPiece = kPieceThreads * kPieceItems;  // logits per CTA
+constexpr int kPieceThreads = 512;
+constexpr int kPieceItems = 32;
+constexpr int kPieceMax = kPieceThreads * kPieceItems;  // logits per CTA at most
 constexpr int kMergeThreads = 1024;
+constexpr int kList = 1024;         // candidates over the threshold that are ranked at once
 
 // (logit, token) as one key: larger logit first, then lower token; 0 stands
 // for no candidate (NaN and -infinity are none).
@@ -30,36 +31,102 @@ SSD_DI float key_logit(uint64_t k) {
 }
 SSD_DI int key_token(uint64_t k) { return (int)~(uint32_t)k; }
 
-// CTA = (piece of a row, beam): the piece's W largest keys, by W maxima.
-__global__ void __launch_bounds__(kPieceThreads) beam_piece_kernel(const BeamArgs a) {
-  __shared__ uint64_t best[kPieceThreads / 32];
-  const int b = blockIdx.y, tid = threadIdx.x;
-  uint64_t* list = a.lists + ((size_t)b * gridDim.x + blockIdx.x) * a.W;
-  if (a.done && a.done[b]) {
-    for (int i = tid; i < a.W; i += kPieceThreads) list[i] = 0;
-    return;
+// The W-th largest of G group maxima (W <= G; equal ones ordered by group):
+// at least W values are at or over it, and few more.  All threads of the
+// block call it with their group's maximum (threads of a group are adjacent)
+// and get it; each group's rank is counted by its threads together.
+template <int G, int kThreads>
+SSD_DI float group_cut(float gmax, int W, float* gm, float* cut) {
+  constexpr int kPer = kThreads / G;             // threads of a group
+  static_assert(kPer >= 1 && kPer <= 32 && (G / kPer) % 4 == 0, "group shape");
+  const int g = threadIdx.x / kPer, q = threadIdx.x % kPer;
+  if (q == 0) gm[g] = gmax;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll 4
+  for (int i = q * (G / kPer); i < (q + 1) * (G / kPer); i += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(gm + i);
+    rank += (o.x > gmax || (o.x == gmax && i < g)) + (o.y > gmax || (o.y == gmax && i + 1 < g)) +
+            (o.z > gmax || (o.z == gmax && i + 2 < g)) + (o.w > gmax || (o.w == gmax && i + 3 < g));
   }
-  uint64_t key[kPieceItems];
-  const float* z = a.logits + (size_t)b * a.V;
+#pragma unroll
+  for (int d = 1; d < kPer; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
+  if (q == 0 && rank == W - 1) *cut = gmax;
+  __syncthreads();
+  return *cut;
+}
+
+// CTA = (piece of a row, beam): the piece's W largest keys, largest first.
+// The row's logits stay in registers; what lies at or over the W-th largest
+// of G group maxima is listed and ranked.
+template <int G>
+__global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
+  __shared__ uint64_t list[kList];
+  __shared__ __align__(16) float gm[G];
+  __shared__ float s_cut;
+  __shared__ int s_n;
+  pdl_trigger();
+  const int b = blockIdx.y, tid = threadIdx.x;
+  if (a.done && a.done[b]) return;               // the merge does not read its lists
+  uint64_t* out = a.lists + ((size_t)b * gridDim.x + blockIdx.x) * a.W;
+  const int v0 = blockIdx.x * len, n = min(len, a.V - v0);
+  const float* row = a.logits + (size_t)b * a.V + v0;
+  float z[kPieceItems];
+  float mx = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPieceItems; ++i) {
-    const int v = blockIdx.x * kPiece + i * kPieceThreads + tid;
-    key[i] = v < a.V ? logit_key(z[v], v) : 0;
+    const int v = i * kPieceThreads + tid;
+    z[i] = v < n ? __ldcs(row + v) : -INFINITY;
   }
-  for (int w = 0; w < a.W; ++w) {
-    uint64_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kPieceItems; ++i) m = max(m, key[i]);
-    for (int d = 16; d; d >>= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
-    if ((tid & 31) == 0) best[tid >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < kPieceThreads / 32; ++i) m = max(m, best[i]);
-    __syncthreads();
-    if (tid == 0) list[w] = m;
+  for (int i = 0; i < kPieceItems; ++i) mx = fmaxf(mx, z[i]);  // ignores NaN
 #pragma unroll
-    for (int i = 0; i < kPieceItems; ++i)
-      if (key[i] == m) key[i] = 0;
+  for (int d = 1; d < kPieceThreads / G; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+  if (tid == 0) s_n = 0;
+  const float cut = group_cut<G, kPieceThreads>(mx, a.W, gm, &s_cut);
+#pragma unroll
+  for (int i = 0; i < kPieceItems; ++i)
+    if (z[i] >= cut && z[i] > -INFINITY) {
+      const int at = atomicAdd(&s_n, 1);
+      if (at < kList) list[at] = logit_key(z[i], v0 + i * kPieceThreads + tid);
+    }
+  __syncthreads();
+  int cnt = s_n;
+  if (cnt > kList) {
+    // many equal logits, or few finite ones: the W-th largest key bit by bit
+    uint64_t t = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const uint64_t c = t | (1ull << bit);
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < kPieceItems; ++i) k += logit_key(z[i], v0 + i * kPieceThreads + tid) >= c;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) k += __shfl_xor_sync(~0u, k, d);
+      if (tid == 0) s_n = 0;
+      __syncthreads();
+      if ((tid & 31) == 0) atomicAdd(&s_n, k);
+      __syncthreads();
+      if (s_n >= a.W) t = c;
+      __syncthreads();
+    }
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPieceItems; ++i) {
+      const uint64_t k = logit_key(z[i], v0 + i * kPieceThreads + tid);
+      if (k >= t && k) list[atomicAdd(&s_n, 1)] = k;  // keys differ: exactly W
+    }
+    __syncthreads();
+    cnt = s_n;
   }
+  // keys differ, so each key's rank is its place
+  for (int i = tid; i < cnt; i += kPieceThreads) {
+    const uint64_t k = list[i];
+    int rank = 0;
+    for (int j = 0; j < cnt; ++j) rank += list[j] > k;
+    if (rank < a.W) out[rank] = k;
+  }
+  for (int i = cnt + tid; i < a.W; i += kPieceThreads) out[i] = 0;
 }
 
 struct Cand {
@@ -73,27 +140,76 @@ SSD_DI bool before(const Cand& x, const Cand& y) {
   return x.k > y.k;
 }
 
-// One CTA: W maxima over all lists.
+// Candidate i of the lists, W per piece; s = -infinity where there is none.
+SSD_DI Cand candidate(const BeamArgs& a, int i, int per) {
+  const int b = i / per;
+  const bool ended = a.done && a.done[b];
+  Cand x;
+  x.b = b;
+  x.k = ended ? (i == b * per ? 1u : 0u) : a.lists[i];
+  x.s = -INFINITY;
+  if (x.k) {
+    const double sc = (double)a.scores[b];
+    x.s = ended ? sc : sc + ((double)key_logit(x.k) - (a.lse ? (double)a.lse[(size_t)b * a.lse_stride] : 0.0));
+    if (!(x.s > -INFINITY)) x.s = -INFINITY;     // NaN
+  }
+  return x;
+}
+
+SSD_DI void put(const BeamArgs& a, int w, const Cand& c, bool got) {
+  const bool ended = got && a.done && a.done[c.b];
+  const int token = !got ? -1 : ended ? a.end_id : key_token(c.k);
+  a.tokens[w] = token;
+  a.parents[w] = got ? c.b : -1;
+  a.scores_out[w] = got ? (float)c.s : -INFINITY;
+  if (a.done_out) a.done_out[w] = !got || token == a.end_id;
+}
+
+// One CTA: the W best of all lists.  Scores rounded to 32 bits keep their
+// order, so a threshold on them passes every candidate at or over it; what
+// passes is ranked by the whole order.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArgs a, int pieces) {
-  __shared__ double bs[kMergeThreads / 32];
-  __shared__ uint64_t bk[kMergeThreads / 32];
-  __shared__ int bb[kMergeThreads / 32];
+  constexpr int kGroups = 256;
+  __shared__ Cand list[kList];
+  __shared__ __align__(16) float gm[kGroups];
+  __shared__ float s_cut;
+  __shared__ int s_n;
+  pdl_wait();
   const int tid = threadIdx.x, per = pieces * a.W, n = a.B * per;
+  float mx = -INFINITY;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kMergeThreads) mx = fmaxf(mx, (float)candidate(a, i, per).s);
+#pragma unroll
+  for (int d = 1; d < kMergeThreads / kGroups; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+  if (tid == 0) s_n = 0;
+  const float cut = group_cut<kGroups, kMergeThreads>(mx, a.W, gm, &s_cut);
+#pragma unroll 4
+  for (int i = tid; i < n; i += kMergeThreads) {
+    const Cand c = candidate(a, i, per);
+    if (c.s > -INFINITY && (float)c.s >= cut) {
+      const int at = atomicAdd(&s_n, 1);
+      if (at < kList) list[at] = c;
+    }
+  }
+  __syncthreads();
+  const int cnt = s_n;
+  if (cnt <= kList) {
+    if (tid < cnt) {
+      const Cand c = list[tid];
+      int rank = 0;
+      for (int j = 0; j < cnt; ++j) rank += before(list[j], c);
+      if (rank < a.W) put(a, rank, c, true);
+    }
+    for (int w = cnt + tid; w < a.W; w += kMergeThreads) put(a, w, Cand{}, false);
+    return;
+  }
+  // many equal scores: W maxima in turn, each below the one before
   const Cand none = {-INFINITY, 0, 1 << 30};
-  Cand last = {INFINITY, ~0ull, -1};  // the candidate taken before
+  Cand last = {INFINITY, ~0ull, -1};
   for (int w = 0; w < a.W; ++w) {
     Cand c = none;
     for (int i = tid; i < n; i += kMergeThreads) {
-      const int b = i / per;
-      const bool ended = a.done && a.done[b];
-      const uint64_t k = ended ? (i == b * per ? (uint64_t)1 : 0) : a.lists[i];
-      if (!k) continue;
-      Cand x;
-      x.s = ended ? (double)a.scores[b]
-                  : (double)a.scores[b] +
-                        ((double)key_logit(k) - (a.lse ? (double)a.lse[(size_t)b * a.lse_stride] : 0.0));
-      x.k = k;
-      x.b = b;
+      const Cand x = candidate(a, i, per);
       if (x.s > -INFINITY && before(last, x) && before(x, c)) c = x;
     }
     for (int d = 16; d; d >>= 1) {
@@ -103,26 +219,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
       x.b = __shfl_xor_sync(~0u, c.b, d);
       if (before(x, c)) c = x;
     }
-    if ((tid & 31) == 0) {
-      bs[tid >> 5] = c.s;
-      bk[tid >> 5] = c.k;
-      bb[tid >> 5] = c.b;
-    }
     __syncthreads();
-    for (int i = 0; i < kMergeThreads / 32; ++i) {
-      const Cand x = {bs[i], bk[i], bb[i]};
-      if (before(x, c)) c = x;
-    }
+    if ((tid & 31) == 0) list[tid >> 5] = c;
     __syncthreads();
-    if (tid == 0) {
-      const bool got = c.k != 0;
-      const bool ended = got && a.done && a.done[c.b];
-      const int token = !got ? -1 : ended ? a.end_id : key_token(c.k);
-      a.tokens[w] = token;
-      a.parents[w] = got ? c.b : -1;
-      a.scores_out[w] = got ? (float)c.s : -INFINITY;
-      if (a.done_out) a.done_out[w] = !got || token == a.end_id;
-    }
+    for (int i = 0; i < kMergeThreads / 32; ++i)
+      if (before(list[i], c)) c = list[i];
+    if (tid == 0) put(a, w, c, c.k != 0);
     last = c;
   }
 }
@@ -145,17 +247,40 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const ReorderArgs a) 
 
 }  // namespace
 
+// Pieces per row, and their length: as few as hold a row in registers, and
+// more while they leave SMs idle and a piece is over 2048 logits.
+static int beam_pieces(int B, int V, int& len) {
+  int p = (V + kPieceMax - 1) / kPieceMax;
+  while ((long long)B * p < 152 && V / (2 * p) >= 2048) p *= 2;
+  len = (V + p - 1) / p;
+  return p;
+}
+
 size_t beam_select_workspace(int B, int V, int W) {
-  return (size_t)B * ((V + kPiece - 1) / kPiece) * W * sizeof(uint64_t);
+  int len;
+  return (size_t)B * beam_pieces(B, V, len) * W * sizeof(uint64_t);
 }
 
 cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s) {
-  const int pieces = (a.V + kPiece - 1) / kPiece;
-  beam_piece_kernel<<<dim3(pieces, a.B), kPieceThreads, 0, s>>>(a);
+  int len;
+  const int pieces = beam_pieces(a.B, a.V, len);
+  const dim3 grid(pieces, a.B);
+  if (a.W <= 64)
+    beam_piece_kernel<128><<<grid, kPieceThreads, 0, s>>>(a, len);
+  else
+    beam_piece_kernel<256><<<grid, kPieceThreads, 0, s>>>(a, len);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  beam_merge_kernel<<<1, kMergeThreads, 0, s>>>(a, pieces);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(1);
+  lc.blockDim = dim3(kMergeThreads);
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, beam_merge_kernel, a, pieces);
 }
 
 cudaError_t launch_beam_reorder(const ReorderArgs& a, cudaStream_t s) {
