@@ -10,8 +10,8 @@ PyTorch fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
+import math
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -66,6 +66,13 @@ def _lib():
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
+
+
+# The current device's index, and a device's current stream as the C calls take
+# it, without building Python stream objects (several microseconds a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: int(torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -422,25 +429,18 @@ class _Ops:
         return out
 
     @staticmethod
-    def _want(t: Optional[torch.Tensor], name: str, dtype, shape, device=None):
-        """Checks one tensor of a tree-decoding call (the library sees bare
-        pointers): type, shape (None: any extent) and device."""
-        if t is None:
-            return
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_cuda or (device is not None and t.device != device):
-            raise ValueError(f"{name}: expected a tensor on {device or 'a CUDA device'}")
-
-    @staticmethod
-    def _on(device: torch.device):
-        """The tensors' device made current where it is not (the call's stream
-        is that device's current stream)."""
-        if device.index == torch.cuda.current_device():
-            return contextlib.nullcontext()
-        return torch.cuda.device(device)
+    def _arg(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+        """The address of one tensor of a tree-decoding call (the library sees
+        bare pointers), its type, shape, device and layout checked."""
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0
+                and t.is_contiguous()):
+            return t.data_ptr()
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                             f"shape {tuple(t.shape)}")
+        if not t.is_cuda or t.get_device() != device:
+            raise ValueError(f"{name}: expected a tensor on CUDA device {device}, got {t.device}")
+        raise ValueError(f"{name}: expected a contiguous tensor")
 
     def tree_attention(self, qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv, dh, theta,
                        weights=None, weights_out=None, out=None) -> torch.Tensor:
@@ -451,24 +451,28 @@ class _Ops:
         Returns bf16 [T, H dh].  weights_out fp32 [Hkv, max_seq] receives
         weights plus the attention weight of each key in this call; pass the
         same tensor twice to accumulate in place."""
-        T, dev = qkv.shape[0], qkv.device
-        max_seq = k_cache.shape[1]
-        self._want(qkv, "qkv", torch.float32, (T, (H + 2 * Hkv) * dh))
-        self._want(parents, "parents", torch.int32, (T,), dev)
-        self._want(k_cache, "k_cache", torch.bfloat16, (Hkv, None, dh), dev)
-        self._want(v_cache, "v_cache", torch.bfloat16, (Hkv, max_seq, dh), dev)
-        self._want(weights, "weights", torch.float32, (Hkv, max_seq), dev)
-        self._want(weights_out, "weights_out", torch.float32, (Hkv, max_seq), dev)
-        with self._on(dev):
-            need = _lib().ssd_op_tree_attention_workspace(T, n_ctx, H, Hkv, dh)
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            if out is None:
-                out = torch.empty(T, H * dh, dtype=torch.bfloat16, device=dev)
-            self._want(out, "out", torch.bfloat16, (T, H * dh), dev)
-            self._check(_lib().ssd_op_tree_attention(
-                _ptr(qkv), _ptr(parents), T, n_ctx, pos0, _ptr(k_cache), _ptr(v_cache), max_seq, H,
-                Hkv, dh, theta, _ptr(weights), _ptr(weights_out), _ptr(out), ws.data_ptr(), need,
-                stream_handle()))
+        dev = qkv.get_device()
+        if dev >= 0 and dev != _current_device():
+            with torch.cuda.device(dev):
+                return self.tree_attention(qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv, dh,
+                                           theta, weights, weights_out, out)
+        T, max_seq = qkv.shape[0], k_cache.shape[1]
+        cache, per_key = (Hkv, max_seq, dh), (Hkv, max_seq)
+        args = (self._arg(qkv, "qkv", torch.float32, (T, (H + 2 * Hkv) * dh), dev),
+                self._arg(parents, "parents", torch.int32, (T,), dev), T, n_ctx, pos0,
+                self._arg(k_cache, "k_cache", torch.bfloat16, cache, dev),
+                self._arg(v_cache, "v_cache", torch.bfloat16, cache, dev), max_seq, H, Hkv, dh, theta,
+                None if weights is None else self._arg(weights, "weights", torch.float32, per_key, dev),
+                None if weights_out is None else
+                self._arg(weights_out, "weights_out", torch.float32, per_key, dev))
+        if out is None:
+            out = torch.empty((T, H * dh), dtype=torch.bfloat16, device=qkv.device)
+        lib = _lib()
+        need = lib.ssd_op_tree_attention_workspace(T, n_ctx, H, Hkv, dh)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=qkv.device)
+        self._check(lib.ssd_op_tree_attention(
+            *args, self._arg(out, "out", torch.bfloat16, (T, H * dh), dev), ws.data_ptr(), need,
+            _raw_stream(dev)))
         return out
 
     CACHE_DTYPES = {torch.bfloat16: _abi.SSD_DTYPE_BF16, torch.float32: _abi.SSD_DTYPE_FP32}
@@ -481,21 +485,25 @@ class _Ops:
         their order, ``keep`` in all.  k, v [Hkv, max_seq, dh] bf16 or fp32,
         weights fp32 [Hkv, max_seq].  Returns the kept rows, int32
         [Hkv, keep]."""
-        if k.dtype not in self.CACHE_DTYPES or k.dim() != 3:
+        dt = k.dtype
+        if dt not in self.CACHE_DTYPES or k.dim() != 3:
             raise ValueError("k: expected a bf16 or fp32 tensor [Hkv, max_seq, dh]")
+        dev = k.get_device()
+        if dev >= 0 and dev != _current_device():
+            with torch.cuda.device(dev):
+                return self.cache_evict(k, v, weights, n, keep, k_out, v_out, weights_out, sinks,
+                                        recent)
         Hkv, max_seq, dh = k.shape
-        dev, max_out = k.device, k_out.shape[1]
-        self._want(v, "v", k.dtype, k.shape, dev)
-        self._want(weights, "weights", torch.float32, (Hkv, max_seq), dev)
-        self._want(k_out, "k_out", k.dtype, (Hkv, None, dh), dev)
-        self._want(v_out, "v_out", k.dtype, (Hkv, max_out, dh), dev)
-        self._want(weights_out, "weights_out", torch.float32, (Hkv, max_out), dev)
-        with self._on(dev):
-            kept = torch.empty(Hkv, max(keep, 0), dtype=torch.int32, device=dev)
-            self._check(_lib().ssd_op_cache_evict(
-                _ptr(k), _ptr(v), _ptr(weights), n, keep, sinks, recent, max_seq, Hkv, dh,
-                self.CACHE_DTYPES[k.dtype], _ptr(k_out), _ptr(v_out), _ptr(weights_out), max_out,
-                _ptr(kept), stream_handle()))
+        max_out = k_out.shape[1]
+        shape, kept_rows = (Hkv, max_out, dh), (Hkv, max_out)
+        args = (self._arg(k, "k", dt, k.shape, dev), self._arg(v, "v", dt, k.shape, dev),
+                self._arg(weights, "weights", torch.float32, (Hkv, max_seq), dev), n, keep, sinks,
+                recent, max_seq, Hkv, dh, self.CACHE_DTYPES[dt],
+                self._arg(k_out, "k_out", dt, shape, dev), self._arg(v_out, "v_out", dt, shape, dev),
+                None if weights_out is None else
+                self._arg(weights_out, "weights_out", torch.float32, kept_rows, dev), max_out)
+        kept = torch.empty((Hkv, max(keep, 0)), dtype=torch.int32, device=k.device)
+        self._check(_lib().ssd_op_cache_evict(*args, kept.data_ptr(), _raw_stream(dev)))
         return kept
 
     def beam_select(self, logits, scores, width, lse=None, done=None, end_id=-1):
@@ -505,49 +513,54 @@ class _Ops:
         lm_head, or None for log-probabilities; done int32 [B] marks ended
         beams.  Returns (tokens, parents, scores, done) of the selected, best
         first."""
+        dev = logits.get_device()
+        if dev >= 0 and dev != _current_device():
+            with torch.cuda.device(dev):
+                return self.beam_select(logits, scores, width, lse, done, end_id)
         B, V = logits.shape
-        dev = logits.device
-        self._want(logits, "logits", torch.float32, (B, V))
-        self._want(scores, "scores", torch.float32, (B,), dev)
-        self._want(done, "done", torch.int32, (B,), dev)
+        step, lse_at = 1, None
         if lse is not None and lse.dtype == torch.int32:
-            self._want(lse, "lse", torch.int32, (B, 12), dev)
-            lse = lse.view(torch.float32)[:, 6]
-        self._want(lse, "lse", torch.float32, (B,), dev)
-        with self._on(dev):
-            need = _lib().ssd_op_beam_select_workspace(B, V, width)
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            got = torch.empty(4, max(width, 0), dtype=torch.int32, device=dev)
-            tokens, parents, sc, ended = got[0], got[1], got[2].view(torch.float32), got[3]
-            self._check(_lib().ssd_op_beam_select(
-                _ptr(logits), B, V, None if lse is None else lse.data_ptr(),
-                1 if lse is None or B == 1 else lse.stride(0), _ptr(scores), _ptr(done), end_id,
-                width, _ptr(tokens), _ptr(parents), _ptr(sc), _ptr(ended), ws.data_ptr(), need,
-                stream_handle()))
-        return tokens, parents, sc, ended
+            # ssd_row_stats records: lse is their seventh word
+            step, lse_at = 12, self._arg(lse, "lse", torch.int32, (B, 12), dev) + 24
+        elif lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != (B,) or lse.get_device() != dev:
+                raise ValueError(f"lse: expected fp32 [{B}] on CUDA device {dev}")
+            step, lse_at = lse.stride(0) if B > 1 else 1, lse.data_ptr()
+        args = (self._arg(logits, "logits", torch.float32, (B, V), dev), B, V, lse_at, step,
+                self._arg(scores, "scores", torch.float32, (B,), dev),
+                None if done is None else self._arg(done, "done", torch.int32, (B,), dev), end_id,
+                width)
+        lib = _lib()
+        need = lib.ssd_op_beam_select_workspace(B, V, width)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=logits.device)
+        got = torch.empty((3, max(width, 0)), dtype=torch.int32, device=logits.device)
+        best = torch.empty(max(width, 0), dtype=torch.float32, device=logits.device)
+        at = got.data_ptr()
+        self._check(lib.ssd_op_beam_select(*args, at, at + 4 * width, best.data_ptr(),
+                                           at + 8 * width, ws.data_ptr(), need, _raw_stream(dev)))
+        tokens, parents, ended = got.unbind(0)
+        return tokens, parents, best, ended
 
     def beam_reorder(self, k, v, parents, start, stop, k_out, v_out):
         """Reordering of the beams' caches (ssd_op_beam_reorder): state w of
         k_out / v_out takes rows start .. stop-1 of state parents[w].  k, v
         [B, ..., max_seq, dh] (any dims between: layers, heads), k_out, v_out
         [W, ..., max_seq, dh]; v and v_out may be None."""
-        dev, W = k.device, k_out.shape[0]
-        if k.dim() < 3:
+        shape, dt, dev, W = k.shape, k.dtype, k.get_device(), k_out.shape[0]
+        if len(shape) < 3:
             raise ValueError("k: expected [B, ..., max_seq, dh]")
-        self._want(k, "k", k.dtype, k.shape)
-        self._want(k_out, "k_out", k.dtype, (W, *k.shape[1:]), dev)
         if (v is None) != (v_out is None):
             raise ValueError("v and v_out go together")
-        self._want(v, "v", k.dtype, k.shape, dev)
-        self._want(v_out, "v_out", k.dtype, k_out.shape, dev)
-        self._want(parents, "parents", torch.int32, (W,), dev)
-        groups = 1
-        for d in k.shape[1:-2]:
-            groups *= d
-        with self._on(dev):
-            self._check(_lib().ssd_op_beam_reorder(
-                _ptr(k), _ptr(v), _ptr(parents), k.shape[0], W, groups, k.shape[-2], start, stop,
-                k.shape[-1] * k.element_size(), _ptr(k_out), _ptr(v_out), stream_handle()))
+        if dev >= 0 and dev != _current_device():
+            with torch.cuda.device(dev):
+                return self.beam_reorder(k, v, parents, start, stop, k_out, v_out)
+        to = (W, *shape[1:])
+        self._check(_lib().ssd_op_beam_reorder(
+            self._arg(k, "k", dt, shape, dev), None if v is None else self._arg(v, "v", dt, shape, dev),
+            self._arg(parents, "parents", torch.int32, (W,), dev), shape[0], W,
+            math.prod(shape[1:-2]), shape[-2], start, stop, shape[-1] * k.element_size(),
+            self._arg(k_out, "k_out", dt, to, dev),
+            None if v_out is None else self._arg(v_out, "v_out", dt, to, dev), _raw_stream(dev)))
         return k_out, v_out
 
     def wait_selftest(self, polls: int = 4096) -> int:

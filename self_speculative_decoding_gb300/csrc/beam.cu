@@ -12,7 +12,7 @@ namespace ssd {
 namespace {
 
 constexpr int kPieceThreads = 512;
-constexpr int kPieceItems = 32;
+constexpr int kPieceItems = 40;
 constexpr int kPieceMax = kPieceThreads * kPieceItems;  // logits per CTA at most
 constexpr int kMergeThreads = 1024;
 constexpr int kList = 1024;         // candidates over the threshold that are ranked at once
@@ -56,6 +56,36 @@ SSD_DI float group_cut(float gmax, int W, float* gm, float* cut) {
   return *cut;
 }
 
+// The W largest of n logits by bisection of the W-th largest key, bit by bit
+// (many equal logits, or few finite ones); keys differ, so there are exactly W.
+__device__ __noinline__ int piece_bisect(const float* row, int v0, int n, int W, uint64_t* list,
+                                         int* s_n) {
+  const int tid = threadIdx.x;
+  uint64_t t = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t c = t | (1ull << bit);
+    int k = 0;
+    for (int v = tid; v < n; v += kPieceThreads) k += logit_key(row[v], v0 + v) >= c;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) k += __shfl_xor_sync(~0u, k, d);
+    __syncthreads();
+    if (tid == 0) *s_n = 0;
+    __syncthreads();
+    if ((tid & 31) == 0) atomicAdd(s_n, k);
+    __syncthreads();
+    if (*s_n >= W) t = c;
+  }
+  __syncthreads();
+  if (tid == 0) *s_n = 0;
+  __syncthreads();
+  for (int v = tid; v < n; v += kPieceThreads) {
+    const uint64_t k = logit_key(row[v], v0 + v);
+    if (k >= t && k) list[atomicAdd(s_n, 1)] = k;
+  }
+  __syncthreads();
+  return *s_n;
+}
+
 // CTA = (piece of a row, beam): the piece's W largest keys, largest first.
 // The row's logits stay in registers; what lies at or over the W-th largest
 // of G group maxima is listed and ranked.
@@ -92,33 +122,7 @@ __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const Beam
     }
   __syncthreads();
   int cnt = s_n;
-  if (cnt > kList) {
-    // many equal logits, or few finite ones: the W-th largest key bit by bit
-    uint64_t t = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t c = t | (1ull << bit);
-      int k = 0;
-#pragma unroll
-      for (int i = 0; i < kPieceItems; ++i) k += logit_key(z[i], v0 + i * kPieceThreads + tid) >= c;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) k += __shfl_xor_sync(~0u, k, d);
-      if (tid == 0) s_n = 0;
-      __syncthreads();
-      if ((tid & 31) == 0) atomicAdd(&s_n, k);
-      __syncthreads();
-      if (s_n >= a.W) t = c;
-      __syncthreads();
-    }
-    if (tid == 0) s_n = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPieceItems; ++i) {
-      const uint64_t k = logit_key(z[i], v0 + i * kPieceThreads + tid);
-      if (k >= t && k) list[atomicAdd(&s_n, 1)] = k;  // keys differ: exactly W
-    }
-    __syncthreads();
-    cnt = s_n;
-  }
+  if (cnt > kList) cnt = piece_bisect(row, v0, n, a.W, list, &s_n);
   // keys differ, so each key's rank is its place
   for (int i = tid; i < cnt; i += kPieceThreads) {
     const uint64_t k = list[i];
@@ -140,24 +144,28 @@ SSD_DI bool before(const Cand& x, const Cand& y) {
   return x.k > y.k;
 }
 
-// Candidate i of the lists, W per piece; s = -infinity where there is none.
-SSD_DI Cand candidate(const BeamArgs& a, int i, int per) {
-  const int b = i / per;
-  const bool ended = a.done && a.done[b];
+// What the scores of a beam's candidates share, in shared memory.
+struct Beam {
+  double score, lse;
+  int ended;
+};
+
+// Entry d of list i; s = -infinity where there is no candidate.
+SSD_DI Cand candidate(const BeamArgs& a, const Beam* beams, int pieces, int i, int d) {
   Cand x;
-  x.b = b;
-  x.k = ended ? (i == b * per ? 1u : 0u) : a.lists[i];
+  x.b = i / pieces;
+  const Beam& m = beams[x.b];
+  x.k = m.ended ? (uint64_t)(d == 0 && i == x.b * pieces) : a.lists[(size_t)i * a.W + d];
   x.s = -INFINITY;
   if (x.k) {
-    const double sc = (double)a.scores[b];
-    x.s = ended ? sc : sc + ((double)key_logit(x.k) - (a.lse ? (double)a.lse[(size_t)b * a.lse_stride] : 0.0));
+    x.s = m.ended ? m.score : m.score + ((double)key_logit(x.k) - m.lse);
     if (!(x.s > -INFINITY)) x.s = -INFINITY;     // NaN
   }
   return x;
 }
 
-SSD_DI void put(const BeamArgs& a, int w, const Cand& c, bool got) {
-  const bool ended = got && a.done && a.done[c.b];
+SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool got) {
+  const bool ended = got && beams[c.b].ended;
   const int token = !got ? -1 : ended ? a.end_id : key_token(c.k);
   a.tokens[w] = token;
   a.parents[w] = got ? c.b : -1;
@@ -165,30 +173,55 @@ SSD_DI void put(const BeamArgs& a, int w, const Cand& c, bool got) {
   if (a.done_out) a.done_out[w] = !got || token == a.end_id;
 }
 
-// One CTA: the W best of all lists.  Scores rounded to 32 bits keep their
-// order, so a threshold on them passes every candidate at or over it; what
-// passes is ranked by the whole order.
+// One CTA: the W best of all lists, which are sorted.  The lists' first
+// entries (their first few, where there are fewer lists than W) are W
+// candidates at least, so the W-th largest of them, or of their maxima over
+// 256 groups, is a threshold that W candidates reach; what lies before it in
+// each list is collected and ranked by the whole order.  The threshold is on
+// scores rounded to 32 bits, which keeps their order.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArgs a, int pieces) {
   constexpr int kGroups = 256;
   __shared__ Cand list[kList];
+  __shared__ Beam beams[256];
   __shared__ __align__(16) float gm[kGroups];
   __shared__ float s_cut;
   __shared__ int s_n;
+  const int tid = threadIdx.x, lists = a.B * pieces;
   pdl_wait();
-  const int tid = threadIdx.x, per = pieces * a.W, n = a.B * per;
+  if (tid < a.B) {
+    beams[tid].score = (double)a.scores[tid];
+    beams[tid].lse = a.lse ? (double)a.lse[(size_t)tid * a.lse_stride] : 0.0;
+    beams[tid].ended = a.done && a.done[tid];
+  }
+  if (tid == 0) s_n = 0;
+  __syncthreads();
+  // sample j: entry j / lists of list j % lists; 256 in a row go to 256 groups
+  const int deep = min(a.W, (a.W + lists - 1) / lists), samples = lists * deep;
   float mx = -INFINITY;
 #pragma unroll 4
-  for (int i = tid; i < n; i += kMergeThreads) mx = fmaxf(mx, (float)candidate(a, i, per).s);
+  for (int j = (tid >> 2) + kGroups * (tid & 3); j < samples; j += kMergeThreads) {
+    const int d = j / lists;
+    mx = fmaxf(mx, (float)candidate(a, beams, pieces, j - d * lists, d).s);
+  }
 #pragma unroll
   for (int d = 1; d < kMergeThreads / kGroups; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-  if (tid == 0) s_n = 0;
   const float cut = group_cut<kGroups, kMergeThreads>(mx, a.W, gm, &s_cut);
-#pragma unroll 4
-  for (int i = tid; i < n; i += kMergeThreads) {
-    const Cand c = candidate(a, i, per);
-    if (c.s > -INFINITY && (float)c.s >= cut) {
-      const int at = atomicAdd(&s_n, 1);
-      if (at < kList) list[at] = c;
+  // eight lanes walk a list together
+  for (int i = tid >> 3; i < lists; i += kMergeThreads / 8) {
+    for (int d0 = 0; d0 < a.W; d0 += 8) {
+      const int d = d0 + (tid & 7);
+      bool in = false;
+      Cand c;
+      if (d < a.W) {
+        c = candidate(a, beams, pieces, i, d);
+        in = c.s > -INFINITY && (float)c.s >= cut;
+      }
+      if (in) {
+        const int at = atomicAdd(&s_n, 1);
+        if (at < kList) list[at] = c;
+      }
+      const unsigned group = 0xffu << (tid & 24);
+      if (__ballot_sync(group, in) != group) break;
     }
   }
   __syncthreads();
@@ -198,9 +231,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
       const Cand c = list[tid];
       int rank = 0;
       for (int j = 0; j < cnt; ++j) rank += before(list[j], c);
-      if (rank < a.W) put(a, rank, c, true);
+      if (rank < a.W) put(a, beams, rank, c, true);
     }
-    for (int w = cnt + tid; w < a.W; w += kMergeThreads) put(a, w, Cand{}, false);
+    for (int w = cnt + tid; w < a.W; w += kMergeThreads) put(a, beams, w, Cand{}, false);
     return;
   }
   // many equal scores: W maxima in turn, each below the one before
@@ -208,10 +241,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   Cand last = {INFINITY, ~0ull, -1};
   for (int w = 0; w < a.W; ++w) {
     Cand c = none;
-    for (int i = tid; i < n; i += kMergeThreads) {
-      const Cand x = candidate(a, i, per);
-      if (x.s > -INFINITY && before(last, x) && before(x, c)) c = x;
-    }
+    for (int i = tid; i < lists; i += kMergeThreads)
+      for (int d = 0; d < a.W; ++d) {
+        const Cand x = candidate(a, beams, pieces, i, d);
+        if (!(x.s > -INFINITY)) break;           // the list's end
+        if (!before(last, x)) continue;
+        if (before(x, c)) c = x;
+        break;                                   // the rest of the list comes after
+      }
     for (int d = 16; d; d >>= 1) {
       Cand x;
       x.s = __shfl_xor_sync(~0u, c.s, d);
@@ -224,7 +261,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
     __syncthreads();
     for (int i = 0; i < kMergeThreads / 32; ++i)
       if (before(list[i], c)) c = list[i];
-    if (tid == 0) put(a, w, c, c.k != 0);
+    if (tid == 0) put(a, beams, w, c, c.k != 0);
     last = c;
   }
 }

@@ -111,6 +111,21 @@ void tree_sizes(TreeArgs& a, int T, int n_ctx, int H, int Hkv, int dh) {
   a.dh = dh;
 }
 
+// theta^(-2 i / dh) / pi.  The table of the thread's last (theta, dh) is kept:
+// 64 powers cost a small call several microseconds.
+void tree_frequencies(float theta, int dh, double* out) {
+  thread_local float last_theta = 0.f;
+  thread_local int last_dh = 0;
+  thread_local double table[kTreeMaxHalf];
+  if (theta != last_theta || dh != last_dh) {
+    for (int i = 0; i < dh / 2; ++i)
+      table[i] = std::pow((double)theta, -2.0 * i / dh) / 3.14159265358979323846;
+    last_theta = theta;
+    last_dh = dh;
+  }
+  std::memcpy(out, table, sizeof(double) * (dh / 2));
+}
+
 }  // namespace
 
 extern "C" {
@@ -458,8 +473,7 @@ ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32
   a.w_out = weight_out;
   a.out = (bf16*)out;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)dh));
-  for (int i = 0; i < dh / 2; ++i)
-    a.inv_freq[i] = std::pow((double)theta, -2.0 * i / dh) / 3.14159265358979323846;
+  tree_frequencies(theta, dh, a.inv_freq);
   return cu(launch_tree_attention(a, (cudaStream_t)stream), "tree_attention");
 }
 

@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
   __shared__ uint32_t bits[kTreeMaxNodes / 32];
   __shared__ int s_depth;
   __shared__ int bad[kPrepHeads];
+  __shared__ float2 turn[kTreeMaxHalf];  // (cos, sin) of the node's position
   pdl_trigger();
   const int t = blockIdx.x, tid = threadIdx.x;
   if (t == 0 && blockIdx.y == 0 && tid == 0) *a.err = 0;
@@ -55,6 +56,12 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
       a.anc[(size_t)t * a.anc_words + w] = d >= 0 ? bits[w] : 0u;
     if (tid == 0) a.depth[t] = d;
   }
+  if (tid < (a.dh >> 1)) {
+    double x = (double)(a.pos0 + max(d, 0)) * a.inv_freq[tid];  // angle / pi
+    x -= 2.0 * rint(0.5 * x);
+    sincospif((float)x, &turn[tid].y, &turn[tid].x);
+  }
+  __syncthreads();
   const int half = a.dh >> 1, heads = a.H + 2 * a.Hkv;
   const int h0 = blockIdx.y * kPrepHeads, h1 = min(h0 + kPrepHeads, heads);
   const float* row = a.qkv + (size_t)t * heads * a.dh;
@@ -64,10 +71,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
     float x = row[(size_t)h * a.dh + i], y = row[(size_t)h * a.dh + half + i];
     if (d < 0) x = y = 0.f;
     if (h < a.H + a.Hkv) {
-      double turn = (double)(a.pos0 + max(d, 0)) * a.inv_freq[i];  // angle / pi
-      turn -= 2.0 * rint(0.5 * turn);
-      float sn, cs;
-      sincospif((float)turn, &sn, &cs);
+      const float cs = turn[i].x, sn = turn[i].y;
       const float rx = x * cs - y * sn, ry = y * cs + x * sn;
       x = rx;
       y = ry;

@@ -407,7 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                              : (x.kvh * a.splits + x.split) * 2 + s;
       if (warp_live) {
         float* po = a.part_o + (size_t)slot * DH * 128 + (size_t)r * 4;
-        if (cnt > 0) {
+        if (cnt == 0) {
+          for (int e = 0; live && e < DH / 4; ++e)
+            *reinterpret_cast<uint4*>(po + (size_t)e * 512) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
 #pragma unroll
           for (int q = 0; q < DH / 32; ++q) {
             uint32_t o[32];
@@ -437,40 +440,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the units' partial results: warp = 32 rows of one K/V head, four
-// output columns per lane and row; the slots are added in order.
+// Joins the units' partial results: lane = row of one K/V head, warp = four
+// output columns; the slots are added in order.  Where there are many, `ways`
+// warps of the CTA share the columns and each adds every ways-th slot.
 constexpr int kJoinWarps = 8;
 template <int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    tree_join_kernel(const __grid_constant__ TreeArgs a) {
+    tree_join_kernel(const __grid_constant__ TreeArgs a, int ways) {
+  __shared__ float4 s_o[kJoinWarps][32];
+  __shared__ float s_l[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = warp % ways;
   const int rows = a.T * a.G, kvh = blockIdx.y;
-  const int row = blockIdx.x * 32 + lane, c = blockIdx.z * kJoinWarps + warp;  // 16-byte chunk
-  if (row >= rows) return;
+  const int row = min(blockIdx.x * 32 + lane, rows - 1);
+  const int c = blockIdx.z * (kJoinWarps / ways) + warp / ways;  // 16-byte chunk
   const int tile = row >> 7, r = row & 127, t = row / a.G;
   const int per = a.two ? a.items * 2 : 2;       // slots per (head, split)
   const int step = a.two ? per : 1, count = a.two ? a.splits : 2 * a.splits;
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
   const bool present = a.depth[t] >= 0, bad = *a.err != 0;
   float m = -INFINITY;
+#pragma unroll 8
   for (int i = 0; i < count; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * step) * 128 + r]);
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < count; ++i) {
+#pragma unroll 4
+  for (int i = way; i < count; i += ways) {
     const size_t sl = s0 + (size_t)i * step;
-    const float pm = a.part_m[sl * 128 + r], pl = a.part_l[sl * 128 + r];
-    if (pl == 0.f) continue;                     // saw no key: its columns were not written
-    const float w = exp2f(pm - base);
+    const float w = exp2f(a.part_m[sl * 128 + r] - base);
     const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 + (size_t)c * 512 + r * 4);
-    l += pl * w;
-    o.x += v.x * w;
-    o.y += v.y * w;
-    o.z += v.z * w;
-    o.w += v.w * w;
+    l = fmaf(a.part_l[sl * 128 + r], w, l);
+    o.x = fmaf(v.x, w, o.x);
+    o.y = fmaf(v.y, w, o.y);
+    o.z = fmaf(v.z, w, o.z);
+    o.w = fmaf(v.w, w, o.w);
   }
+  if (ways > 1) {
+    s_o[warp][lane] = o;
+    s_l[warp][lane] = l;
+    __syncthreads();
+    if (way) return;
+    for (int i = 1; i < ways; ++i) {
+      const float4 v = s_o[warp + i][lane];
+      l += s_l[warp + i][lane];
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
+    }
+  }
+  if (blockIdx.x * 32 + lane >= rows) return;
   const float lse = l != 0.f ? m + log2f(l) : INFINITY;
   const float inv = l != 0.f ? 1.f / l : 0.f;
   float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
@@ -531,10 +552,11 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
   lc.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH>, mQ, mK, mV, mTK, mTV, a);
   if (e != cudaSuccess) return e;
-  lc.gridDim = dim3((rows + 31) / 32, a.Hkv, DH / 4 / kJoinWarps);
+  const int ways = (a.two ? a.splits : 2 * a.splits) >= 16 ? kJoinWarps : 1;
+  lc.gridDim = dim3((rows + 31) / 32, a.Hkv, DH / 4 / (kJoinWarps / ways));
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, tree_join_kernel<DH>, a);
+  return cudaLaunchKernelEx(&lc, tree_join_kernel<DH>, a, ways);
 }
 
 }  // namespace
@@ -577,14 +599,17 @@ void tree_split(TreeArgs& a) {
   a.nb = a.nb_ctx + (a.T + kTreeKeys - 1) / kTreeKeys;
   const long long lanes = (long long)a.Hkv * a.items;
   long long best = -1;
-  for (int s = 1; s <= a.nb && s <= 160; ++s) {
-    const long long waves = (lanes * s + sms - 1) / sms;
+  // of the splits that take the same number of waves the most is the best
+  for (long long waves = 1; waves <= 8; ++waves) {
+    long long n = waves * sms / lanes;
+    if (n < 1 && (waves < 8 || best >= 0)) continue;
+    n = n < 1 ? 1 : n > a.nb ? a.nb : n > 160 ? 160 : n;
     // a stream takes every other block of a single tile's run
-    const long long len = (a.nb + s - 1) / s, steps = a.two ? len : (len + 1) / 2;
-    const long long cost = waves * (steps + 3);
+    const long long len = (a.nb + n - 1) / n, steps = a.two ? len : (len + 1) / 2;
+    const long long cost = ((lanes * n + sms - 1) / sms) * (steps + 3);
     if (best < 0 || cost < best) {
       best = cost;
-      a.splits = s;
+      a.splits = (int)n;
     }
   }
   a.units = (int)(lanes * a.splits);

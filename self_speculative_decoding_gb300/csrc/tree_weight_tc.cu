@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  float* nlse = reinterpret_cast<float*>(sm + kTileSmem);  // [stream][128]
+  float* nlse = reinterpret_cast<float*>(sm + kTileSmem);  // [stream][128], -lse
   uint64_t* bars = reinterpret_cast<uint64_t*>(nlse + 256);
   uint64_t* qfull = bars;                        // [2]
   uint64_t* qempty = bars + 2;                   // [2]
@@ -242,31 +242,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q * 32 < cols; ++q) {
-            uint32_t v[32];
-            tmem_ld32_nw(trow + (uint32_t)(buf * 128 + q * 32), v);
+          for (int q = 0; q < cols; q += 64) {
+            uint32_t v[2][32];
+            tmem_ld32_nw(trow + (uint32_t)(buf * 128 + q), v[0]);
+            if (q + 32 < cols) tmem_ld32_nw(trow + (uint32_t)(buf * 128 + q + 32), v[1]);
             tmem_wait_ld();
-            tmem_pin32(v);
-            if (ctx && !some) {
+            tmem_pin32(v[0]);
+            tmem_pin32(v[1]);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 n4 = *reinterpret_cast<const float4*>(nl + q * 32 + e);
-                sum[0] += ex2(fmaf(__uint_as_float(v[e]), scale, n4.x));
-                sum[1] += ex2(fmaf(__uint_as_float(v[e + 1]), scale, n4.y));
-                sum[2] += ex2(fmaf(__uint_as_float(v[e + 2]), scale, n4.z));
-                sum[3] += ex2(fmaf(__uint_as_float(v[e + 3]), scale, n4.w));
-              }
-            } else {
+            for (int hlf = 0; hlf < 2; ++hlf) {
+              if (q + hlf * 32 >= cols) break;
+              const int q0 = q + hlf * 32;
+              if (some) {
+                // a row without part may meet inf or NaN among the keys: its
+                // score is made 0, and its 2^(0 - inf) is 0
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float n1 = nl[q * 32 + e];
-                bool on = n1 != -INFINITY;       // NaN stays: its row is NaN
-                if (!ctx && on) {
-                  const int node = (t * 128 + q * 32 + e) / a.G;
-                  const uint32_t w = a.anc[(size_t)node * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
-                  on = (w >> lane) & 1u;
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 n4 = *reinterpret_cast<const float4*>(nl + q0 + e);
+                  if (n4.x == -INFINITY) v[hlf][e] = 0u;
+                  if (n4.y == -INFINITY) v[hlf][e + 1] = 0u;
+                  if (n4.z == -INFINITY) v[hlf][e + 2] = 0u;
+                  if (n4.w == -INFINITY) v[hlf][e + 3] = 0u;
                 }
-                if (on) sum[e & 3] += ex2(fmaf(__uint_as_float(v[e]), scale, n1));
+              }
+              if (ctx) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 n4 = *reinterpret_cast<const float4*>(nl + q0 + e);
+                  sum[0] += ex2(fmaf(__uint_as_float(v[hlf][e]), scale, n4.x));
+                  sum[1] += ex2(fmaf(__uint_as_float(v[hlf][e + 1]), scale, n4.y));
+                  sum[2] += ex2(fmaf(__uint_as_float(v[hlf][e + 2]), scale, n4.z));
+                  sum[3] += ex2(fmaf(__uint_as_float(v[hlf][e + 3]), scale, n4.w));
+                }
+              } else {
+                // a tree block: lane e holds the ancestor word of row q0 + e
+                const int row = min(t * 128 + q0 + lane, rows - 1);
+                const uint32_t mine =
+                    a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const uint32_t w = __shfl_sync(0xffffffffu, mine, e);
+                  const float p = ex2(fmaf(__uint_as_float(v[hlf][e]), scale, nl[q0 + e]));
+                  if ((w >> lane) & 1u) sum[e & 3] += p;
+                }
               }
             }
           }
