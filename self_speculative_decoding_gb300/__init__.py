@@ -533,12 +533,15 @@ class _Ops:
         lib = _lib()
         need = lib.ssd_op_beam_select_workspace(B, V, width)
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=logits.device)
-        got = torch.empty((3, max(width, 0)), dtype=torch.int32, device=logits.device)
-        best = torch.empty(max(width, 0), dtype=torch.float32, device=logits.device)
-        at = got.data_ptr()
-        self._check(lib.ssd_op_beam_select(*args, at, at + 4 * width, best.data_ptr(),
-                                           at + 8 * width, ws.data_ptr(), need, _raw_stream(dev)))
-        tokens, parents, ended = got.unbind(0)
+        # (rows of one tensor would cost more than four small tensors)
+        n, at = max(width, 0), logits.device
+        tokens = torch.empty(n, dtype=torch.int32, device=at)
+        parents = torch.empty(n, dtype=torch.int32, device=at)
+        best = torch.empty(n, dtype=torch.float32, device=at)
+        ended = torch.empty(n, dtype=torch.int32, device=at)
+        self._check(lib.ssd_op_beam_select(*args, tokens.data_ptr(), parents.data_ptr(),
+                                           best.data_ptr(), ended.data_ptr(), ws.data_ptr(), need,
+                                           _raw_stream(dev)))
         return tokens, parents, best, ended
 
     def beam_reorder(self, k, v, parents, start, stop, k_out, v_out):

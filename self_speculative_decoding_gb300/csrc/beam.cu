@@ -6,6 +6,8 @@
 // the order is that of the logits, so each piece of a row is cut down to its
 // W largest logits first; the pieces' lists are then merged by score.  Ties
 // go to the lower beam, then to the lower token.
+#include <cooperative_groups.h>
+
 #include "kernels.cuh"
 
 namespace ssd {
@@ -15,6 +17,7 @@ constexpr int kPieceThreads = 512;
 constexpr int kPieceItems = 40;
 constexpr int kPieceMax = kPieceThreads * kPieceItems;  // logits per CTA at most
 constexpr int kMergeThreads = 1024;
+constexpr int kMaxCluster = 8;      // portable cluster size
 constexpr int kList = 1024;         // candidates over the threshold that are ranked at once
 
 // (logit, token) as one key: larger logit first, then lower token; 0 stands
@@ -86,20 +89,19 @@ __device__ __noinline__ int piece_bisect(const float* row, int v0, int n, int W,
   return *s_n;
 }
 
-// CTA = (piece of a row, beam): the piece's W largest keys, largest first.
-// The row's logits stay in registers; what lies at or over the W-th largest
+// Piece `piece` of row b: its W largest keys to its list, largest first.  The
+// logits stay in registers; what lies at or over the W-th largest
 // of G group maxima is listed and ranked.
 template <int G>
-__global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
+SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int pieces, int b) {
   __shared__ uint64_t list[kList];
   __shared__ __align__(16) float gm[G];
   __shared__ float s_cut;
   __shared__ int s_n;
-  pdl_trigger();
-  const int b = blockIdx.y, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   if (a.done && a.done[b]) return;               // the merge does not read its lists
-  uint64_t* out = a.lists + ((size_t)b * gridDim.x + blockIdx.x) * a.W;
-  const int v0 = blockIdx.x * len, n = min(len, a.V - v0);
+  uint64_t* out = a.lists + ((size_t)b * pieces + piece) * a.W;
+  const int v0 = piece * len, n = min(len, a.V - v0);
   const float* row = a.logits + (size_t)b * a.V + v0;
   float z[kPieceItems];
   float mx = -INFINITY;
@@ -131,6 +133,13 @@ __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const Beam
     if (rank < a.W) out[rank] = k;
   }
   for (int i = cnt + tid; i < a.W; i += kPieceThreads) out[i] = 0;
+}
+
+// CTA = (piece of a row, beam).
+template <int G>
+__global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
+  pdl_trigger();
+  piece_body<G>(a, len, blockIdx.x, gridDim.x, blockIdx.y);
 }
 
 struct Cand {
@@ -179,15 +188,15 @@ SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool
 // 256 groups, is a threshold that W candidates reach; what lies before it in
 // each list is collected and ranked by the whole order.  The threshold is on
 // scores rounded to 32 bits, which keeps their order.
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArgs a, int pieces) {
-  constexpr int kGroups = 256;
+template <int kThreads>
+SSD_DI void merge_body(const BeamArgs& a, int pieces) {
+  constexpr int kGroups = 256, kPer = kThreads / kGroups;
   __shared__ Cand list[kList];
   __shared__ Beam beams[256];
   __shared__ __align__(16) float gm[kGroups];
   __shared__ float s_cut;
   __shared__ int s_n;
   const int tid = threadIdx.x, lists = a.B * pieces;
-  pdl_wait();
   if (tid < a.B) {
     beams[tid].score = (double)a.scores[tid];
     beams[tid].lse = a.lse ? (double)a.lse[(size_t)tid * a.lse_stride] : 0.0;
@@ -199,15 +208,15 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   const int deep = min(a.W, (a.W + lists - 1) / lists), samples = lists * deep;
   float mx = -INFINITY;
 #pragma unroll 4
-  for (int j = (tid >> 2) + kGroups * (tid & 3); j < samples; j += kMergeThreads) {
+  for (int j = tid / kPer + kGroups * (tid % kPer); j < samples; j += kThreads) {
     const int d = j / lists;
     mx = fmaxf(mx, (float)candidate(a, beams, pieces, j - d * lists, d).s);
   }
 #pragma unroll
-  for (int d = 1; d < kMergeThreads / kGroups; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-  const float cut = group_cut<kGroups, kMergeThreads>(mx, a.W, gm, &s_cut);
+  for (int d = 1; d < kThreads / kGroups; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+  const float cut = group_cut<kGroups, kThreads>(mx, a.W, gm, &s_cut);
   // eight lanes walk a list together
-  for (int i = tid >> 3; i < lists; i += kMergeThreads / 8) {
+  for (int i = tid >> 3; i < lists; i += kThreads / 8) {
     for (int d0 = 0; d0 < a.W; d0 += 8) {
       const int d = d0 + (tid & 7);
       bool in = false;
@@ -227,13 +236,13 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   __syncthreads();
   const int cnt = s_n;
   if (cnt <= kList) {
-    if (tid < cnt) {
-      const Cand c = list[tid];
+    for (int i = tid; i < cnt; i += kThreads) {
+      const Cand c = list[i];
       int rank = 0;
       for (int j = 0; j < cnt; ++j) rank += before(list[j], c);
       if (rank < a.W) put(a, beams, rank, c, true);
     }
-    for (int w = cnt + tid; w < a.W; w += kMergeThreads) put(a, beams, w, Cand{}, false);
+    for (int w = cnt + tid; w < a.W; w += kThreads) put(a, beams, w, Cand{}, false);
     return;
   }
   // many equal scores: W maxima in turn, each below the one before
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   Cand last = {INFINITY, ~0ull, -1};
   for (int w = 0; w < a.W; ++w) {
     Cand c = none;
-    for (int i = tid; i < lists; i += kMergeThreads)
+    for (int i = tid; i < lists; i += kThreads)
       for (int d = 0; d < a.W; ++d) {
         const Cand x = candidate(a, beams, pieces, i, d);
         if (!(x.s > -INFINITY)) break;           // the list's end
@@ -259,11 +268,25 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
     __syncthreads();
     if ((tid & 31) == 0) list[tid >> 5] = c;
     __syncthreads();
-    for (int i = 0; i < kMergeThreads / 32; ++i)
+    for (int i = 0; i < kThreads / 32; ++i)
       if (before(list[i], c)) c = list[i];
     if (tid == 0) put(a, beams, w, c, c.k != 0);
     last = c;
   }
+}
+
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArgs a, int pieces) {
+  pdl_wait();
+  merge_body<kMergeThreads>(a, pieces);
+}
+
+// Few pieces: one cluster holds them all, and its first CTA merges (one launch
+// instead of two).
+template <int G>
+__global__ void __launch_bounds__(kPieceThreads, 1) beam_cluster_kernel(const BeamArgs a, int len) {
+  piece_body<G>(a, len, blockIdx.x, gridDim.x, blockIdx.y);
+  cooperative_groups::this_cluster().sync();
+  if (blockIdx.x == 0 && blockIdx.y == 0) merge_body<kPieceThreads>(a, gridDim.x);
 }
 
 // Units of 16 bytes of the rows start .. stop-1 of every group of every state.
@@ -301,21 +324,28 @@ size_t beam_select_workspace(int B, int V, int W) {
 cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s) {
   int len;
   const int pieces = beam_pieces(a.B, a.V, len);
-  const dim3 grid(pieces, a.B);
-  if (a.W <= 64)
-    beam_piece_kernel<128><<<grid, kPieceThreads, 0, s>>>(a, len);
-  else
-    beam_piece_kernel<256><<<grid, kPieceThreads, 0, s>>>(a, len);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(1);
-  lc.blockDim = dim3(kMergeThreads);
+  lc.gridDim = dim3(pieces, a.B);
+  lc.blockDim = dim3(kPieceThreads);
   lc.stream = s;
   lc.attrs = attr;
+  if (pieces * a.B <= kMaxCluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pieces;
+    attr[0].val.clusterDim.y = a.B;
+    attr[0].val.clusterDim.z = 1;
+    lc.numAttrs = 1;
+    return a.W <= 64 ? cudaLaunchKernelEx(&lc, beam_cluster_kernel<128>, a, len)
+                     : cudaLaunchKernelEx(&lc, beam_cluster_kernel<256>, a, len);
+  }
+  cudaError_t e = a.W <= 64 ? cudaLaunchKernelEx(&lc, beam_piece_kernel<128>, a, len)
+                            : cudaLaunchKernelEx(&lc, beam_piece_kernel<256>, a, len);
+  if (e != cudaSuccess) return e;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = dim3(1);
+  lc.blockDim = dim3(kMergeThreads);
   lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, beam_merge_kernel, a, pieces);
 }

@@ -7,8 +7,9 @@
 //
 // Unit = two blocks of 128 keys of one K/V head; warps 0-3 and 4-7 take a
 // block each, every tile of 128 rows passes both (a Q tile read from L2
-// serves 256 keys).  Up to two Q tiles stay in shared memory for all of a
-// CTA's units of a head.  Warp 8: TMA copies, warp 9: MMA.  Waits are bounded;
+// serves 256 keys), plane by plane (low part, high part).  Up to two Q tiles
+// stay in shared memory for all of a CTA's units of a head; more stream
+// through three slots of a plane each.  Warp 8: TMA copies, warp 9: MMA.  Waits are bounded;
 // one that gives up makes the CTA's weights NaN.
 #include "tc_dev.cuh"
 #include "tree.cuh"
@@ -23,6 +24,7 @@ constexpr int kPolls = 1 << 22;
 constexpr int kRegion = 128 * 128;
 constexpr int kTileSmem = 224 * 1024;            // Q tiles (hi, lo), then the ring of K blocks
 constexpr int kMaxStages = 12;
+constexpr int kMaxPlanes = 4;
 
 SSD_DI bool flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
 SSD_DI float ex2(float x) {
@@ -69,26 +71,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   float* nlse = reinterpret_cast<float*>(sm + kTileSmem);  // [stream][128], -lse
   uint64_t* bars = reinterpret_cast<uint64_t*>(nlse + 256);
-  uint64_t* qfull = bars;                        // [2]
-  uint64_t* qempty = bars + 2;                   // [2]
-  uint64_t* sfull = bars + 4;                    // [stream][buffer]
-  uint64_t* sfree = bars + 8;
-  uint64_t* mdone = bars + 12;
-  uint64_t* full = bars + 13;
+  uint64_t* qfull = bars;                        // [planes]
+  uint64_t* qempty = bars + kMaxPlanes;
+  uint64_t* sfull = bars + 2 * kMaxPlanes;       // [stream][buffer]
+  uint64_t* sfree = sfull + 4;
+  uint64_t* mdone = sfull + 8;
+  uint64_t* full = sfull + 9;
   uint64_t* empty = full + kMaxStages;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kMaxStages);
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G;
-  const int qslots = a.tiles > 1 ? 2 : 1;
-  const bool resident = a.tiles <= qslots;       // Q stays for all units of a head
-  const int stages = min(kMaxStages, (kTileSmem - qslots * 2 * kItem) / kItem);
-  unsigned char* ring = sm + qslots * 2 * kItem;
+  const bool resident = a.tiles <= 2;            // Q stays for all units of a head
+  const int qslots = resident ? 2 * a.tiles : 3;
+  const int stages = min(kMaxStages, kTileSmem / kItem - qslots);
+  unsigned char* ring = sm + qslots * kItem;
   const int pairs = (a.nb + 1) / 2;
   const Range rg = my_units(a);
 
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kMaxPlanes; ++s) {
       mbar_init(&qfull[s], 1);
       mbar_init(&qempty[s], 1);
     }
@@ -115,14 +117,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0, qissued = 0;
       bool ok = true;
       auto send_q = [&](int kvh, int tile) {
-        const int sl = qissued % qslots, use = qissued / qslots;
-        if (use > 0 && !mbar_wait_n(&qempty[sl], (uint32_t)((use - 1) & 1), kPolls)) return false;
-        mbar_arrive_expect_tx(&qfull[sl], 2u * kItem);
-        for (int p = 0; p < 2; ++p)
+        for (int p = 1; p >= 0; --p) {
+          const int sl = qissued % qslots, use = qissued / qslots;
+          if (use > 0 && !mbar_wait_n(&qempty[sl], (uint32_t)((use - 1) & 1), kPolls)) return false;
+          mbar_arrive_expect_tx(&qfull[sl], (uint32_t)kItem);
           for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(sm + (sl * 2 + p) * kItem + r * kRegion, &mQ, r * 64, tile * 128,
-                        p * a.Hkv + kvh, &qfull[sl]);
-        ++qissued;
+            tma_load_3d(sm + sl * kItem + r * kRegion, &mQ, r * 64, tile * 128, p * a.Hkv + kvh,
+                        &qfull[sl]);
+          ++qissued;
+        }
         return true;
       };
       for (int u = rg.u0; ok && u < rg.u1; ++u) {
@@ -168,40 +171,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
         }
         for (int t = 0; ok && t < a.tiles; ++t) {
-          const int qi = qtaken + t, sl = qi % qslots;
-          ok = mbar_wait_n(&qfull[sl], (uint32_t)((qi / qslots) & 1), kPolls);
           const int cols = min(128, (rows - t * 128 + 15) / 16 * 16);
           const uint32_t id = idesc_bf16(128, cols);
-          for (int s = 0; ok && s < nblk; ++s) {
-            const int c = cs[s]++, buf = c & 1;
-            if (c >= 2) ok = mbar_wait_n(&sfree[s * 2 + buf], (uint32_t)((c / 2 - 1) & 1), kPolls);
-            if (!ok || flagged(fail)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t kb = ra + (uint32_t)((taken + s) % stages) * kItem;
-            const uint32_t qb = qa + (uint32_t)sl * 2 * kItem;
-#pragma unroll
-            for (int p = 1; p >= 0; --p)
+          for (int p = 1; ok && p >= 0; --p) {   // the low part first
+            const int qi = qtaken + 2 * t + (1 - p), sl = qi % qslots;
+            ok = mbar_wait_n(&qfull[sl], (uint32_t)((qi / qslots) & 1), kPolls);
+            for (int s = 0; ok && s < nblk; ++s) {
+              const int buf = cs[s] & 1;
+              if (p && cs[s] >= 2)
+                ok = mbar_wait_n(&sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1), kPolls);
+              if (!ok || flagged(fail)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t kb = ra + (uint32_t)((taken + s) % stages) * kItem;
+              const uint32_t qb = qa + (uint32_t)sl * kItem;
 #pragma unroll
               for (int ks = 0; ks < DH / 16; ++ks) {
                 const uint32_t o = (uint32_t)(ks >> 2) * kRegion;
                 mma_bf16_tc(tmem + (uint32_t)(s * 256 + buf * 128), sw128_desc(kb + o) + 2 * (ks & 3),
-                            sw128_desc(qb + p * kItem + o) + 2 * (ks & 3), id,
-                            (p == 0 || ks > 0) ? 1u : 0u);
+                            sw128_desc(qb + o) + 2 * (ks & 3), id, (p == 0 || ks > 0) ? 1u : 0u);
               }
-            mma_commit(&sfull[s * 2 + buf]);
+              if (p == 0) {
+                mma_commit(&sfull[s * 2 + buf]);
+                ++cs[s];
+              }
+            }
+            if (ok && !resident) mma_commit(&qempty[sl]);
           }
-          if (ok && !resident) mma_commit(&qempty[sl]);
         }
         for (int s = 0; ok && s < nblk; ++s) mma_commit(&empty[(taken + s) % stages]);
         taken += nblk;
         if (!resident) {
-          qtaken += a.tiles;
+          qtaken += 2 * a.tiles;
         } else if ((u + 1) % pairs == 0) {       // the head's last unit
-          for (int t = 0; ok && t < a.tiles; ++t) mma_commit(&qempty[(qtaken + t) % qslots]);
-          qtaken += a.tiles;
+          for (int i = 0; ok && i < 2 * a.tiles; ++i) mma_commit(&qempty[(qtaken + i) % qslots]);
+          qtaken += 2 * a.tiles;
         }
       }
       if (!ok) atomicExch(fail, 1);
@@ -217,9 +223,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = a.scale_log2;
     int c = 0;
     bool ok = true;
+    // -lse of row r of a tile; rows that are absent, or beyond the last, take
+    // no part
+    auto row_lse = [&](int kvh, int t) {
+      return t * 128 + r < rows ? -a.lse[(size_t)kvh * rows + t * 128 + r] : -INFINITY;
+    };
+    float next = rg.u0 < rg.u1 ? row_lse(rg.u0 / pairs, 0) : 0.f;
     for (int u = rg.u0; u < rg.u1; ++u) {
       const int kvh = u / pairs, b = (u - kvh * pairs) * 2 + s;
-      if (b >= a.nb) continue;
+      if (b >= a.nb) {                           // an odd last block: no second one
+        if (u + 1 < rg.u1) next = row_lse((u + 1) / pairs, 0);
+        continue;
+      }
       const bool ctx = b < a.nb_ctx;
       const int key = ctx ? b * kTreeKeys + r : a.n + (b - a.nb_ctx) * kTreeKeys + r;
       const bool live = key < (ctx ? a.n : a.n + a.T);
@@ -229,11 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < a.tiles; ++t, ++c) {
         const int buf = c & 1, cols = min(128, rows - t * 128);
         float* nl = nlse + s * 128;
-        // rows that are absent, or beyond the last, take no part
-        const float x = r < cols ? -a.lse[(size_t)kvh * rows + t * 128 + r] : -INFINITY;
+        const float x = next;
         stream_sync(s);                          // the tile before has been read
         nl[r] = x;
         const bool some = stream_any(s, x == -INFINITY);
+        // the next tile's, or the next unit's first, ahead of its use
+        if (t + 1 < a.tiles)
+          next = row_lse(kvh, t + 1);
+        else if (u + 1 < rg.u1)
+          next = row_lse((u + 1) / pairs, 0);
         ok = ok && !flagged(fail) && mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
         const bool all_ok = __all_sync(0xffffffffu, ok);
         if (!all_ok) {
