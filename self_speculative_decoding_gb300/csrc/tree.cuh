@@ -61,4 +61,74 @@ bool tree_map(CUtensorMap* m, const void* base, int dh, int d1, int d2, int stri
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_tree_weight_tc(const TreeArgs& a, int sms, cudaStream_t s);
 
+// ---- device helpers of the two tensor-core kernels
+
+// A ring's slot and the parity of its use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  SSD_DI Ring next() const {
+    Ring r = *this;
+    if (++r.slot == N) {
+      r.slot = 0;
+      r.phase ^= 1u;
+    }
+    return r;
+  }
+};
+
+SSD_DI bool tree_flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
+
+// 2^x on the special-function unit (relative error about 2^-22).
+SSD_DI float tree_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The matrix instructions are issued by one elected lane of a warp that runs
+// its loop together: the operands are then uniform values, which one lane's
+// own branch would have to move into uniform registers for every instruction
+// (measured: 95 cycles per instruction instead of 64).
+SSD_DI uint32_t tree_elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// D += A B, both operands in shared memory / A in tensor memory.
+SSD_DI void tree_mma_ss(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                        uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+SSD_DI void tree_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                        uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+SSD_DI void tree_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(lead)
+      : "memory");
+}
+
 }  // namespace ssd

@@ -30,16 +30,13 @@ constexpr int kThreads = 320;
 constexpr int kPolls = 1 << 22;
 constexpr int kRegion = 128 * 128;              // [128 rows][64] bf16, 128-byte swizzle
 constexpr int kTileSmem = 224 * 1024;           // Q tiles, then the ring of K / V blocks
-constexpr int kMaxStages = 12;
+// K / V blocks in flight beside the Q tiles (two planes each).
+__host__ __device__ constexpr int ring_stages(int dh, bool two) {
+  const int item = dh / 64 * kRegion, n = kTileSmem / item - (two ? 4 : 2);
+  return n < 12 ? n : 12;
+}
 constexpr uint32_t kColO = 256;                 // TMEM: S0, S1 (P over each), O0, O1
 constexpr float kRaise = 8.f;
-
-SSD_DI bool flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
-SSD_DI float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 SSD_DI void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -64,16 +61,6 @@ SSD_DI uint64_t mn_desc(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t idesc_pv(int N) {
   return idesc_bf16(128, N) | (1u << 16);        // B is MN-major
 }
-// D += A B with A in tensor memory.
-SSD_DI void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 // Block range of a unit and its place.
 struct Unit {
   int kvh, item, split, b0, nb;
@@ -90,7 +77,7 @@ SSD_DI Unit unit_of(const TreeArgs& a, int u) {
   return x;
 }
 
-template <int DH>
+template <int DH, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ,
                         const __grid_constant__ CUtensorMap mK,
@@ -100,6 +87,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ TreeArgs a) {
   constexpr int kRegs = DH / 64;                 // 64-column regions per row block
   constexpr int kItem = kRegs * kRegion;         // bytes of a K or V block, or a Q plane
+  constexpr int kTiles = TWO ? 2 : 1;            // Q tiles of a unit
+  constexpr int kStages = ring_stages(DH, TWO);
+  constexpr int kLag = TWO ? 1 : 2;              // K blocks ahead of their V block
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
@@ -111,13 +101,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* ofull = bars + 6;                    // [2] the unit's last product done
   uint64_t* mdone = bars + 8;
   uint64_t* full = bars + 9;                     // [stages]
-  uint64_t* empty = full + kMaxStages;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kMaxStages);
+  uint64_t* empty = full + kStages;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kStages);
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int qtiles = a.two ? 2 : 1;
-  const int stages = min(kMaxStages, (kTileSmem - qtiles * 2 * kItem) / kItem);
-  unsigned char* ring = sm + qtiles * 2 * kItem;
+  unsigned char* ring = sm + kTiles * 2 * kItem;
 
   if (tid == 0) {
     mbar_init(qfull, 1);
@@ -128,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ofull[s], 1);
     }
     mbar_init(mdone, 1);
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -140,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  const int lag = a.two ? 1 : 2;                 // K blocks ahead of their V block
 
   if (warp == 8) {
     if (lane == 0) {
@@ -149,11 +136,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("prefetch.tensormap [%0];" ::"l"(&mQ) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&mK) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&mV) : "memory");
+      Ring<kStages> at;
       int issued = 0, units = 0;                 // copies / units so far
       bool ok = true, waited = false;
       for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
         const Unit x = unit_of(a, u);
-        const int pro = min(lag, x.nb), mid = 2 * (x.nb - pro), total = 2 * x.nb;
+        const int pro = min(kLag, x.nb), mid = 2 * (x.nb - pro), total = 2 * x.nb;
         bool q_sent = false;
         auto send_q = [&]() {
           if (!waited) {
@@ -161,12 +149,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             waited = true;
           }
           if (units > 0 && !mbar_wait_n(qfree, (uint32_t)((units - 1) & 1), kPolls)) return false;
-          mbar_arrive_expect_tx(qfull, (uint32_t)(qtiles * 2 * kItem));
-          for (int t = 0; t < qtiles; ++t)
+          mbar_arrive_expect_tx(qfull, (uint32_t)(kTiles * 2 * kItem));
+          for (int t = 0; t < kTiles; ++t)
             for (int p = 0; p < 2; ++p)
               for (int r = 0; r < kRegs; ++r)
                 tma_load_3d(sm + (t * 2 + p) * kItem + r * kRegion, &mQ, r * 64,
-                            (x.item * qtiles + t) * 128, p * a.Hkv + x.kvh, qfull);
+                            (x.item * kTiles + t) * 128, p * a.Hkv + x.kvh, qfull);
           q_sent = true;
           return true;
         };
@@ -178,119 +166,126 @@ __global__ void __launch_bounds__(kThreads, 1)
             is_v = false;
           } else if (i - pro < mid) {
             is_v = ((i - pro) & 1) == 0;
-            b = (i - pro) / 2 + (is_v ? 0 : lag);
+            b = (i - pro) / 2 + (is_v ? 0 : kLag);
           } else {
             is_v = true;
             b = mid / 2 + (i - pro - mid);
           }
           b += x.b0;
           const bool ctx = b < a.nb_ctx;
-          const int st = issued % stages, use = issued / stages;
           // the CTA's first copies of context blocks go out before the rows are
           // ready; a later unit's first blocks before its rows are free (the
           // slots they wait for need no query of this unit)
-          if (!q_sent && (units > 0 ? i >= lag : !ctx || use > 0)) ok = send_q();
-          if (ok && use > 0) ok = mbar_wait_n(&empty[st], (uint32_t)((use - 1) & 1), kPolls);
-          if (!ok || flagged(fail)) {
+          if (!q_sent && (units > 0 ? i >= kLag : !ctx || issued >= kStages)) ok = send_q();
+          if (ok && issued >= kStages) ok = mbar_wait_n(&empty[at.slot], at.phase ^ 1u, kPolls);
+          if (!ok || tree_flagged(fail)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[st], (uint32_t)kItem);
+          mbar_arrive_expect_tx(&full[at.slot], (uint32_t)kItem);
           const CUtensorMap* m = ctx ? (is_v ? &mV : &mK) : (is_v ? &mTV : &mTK);
           const int row = (ctx ? b : b - a.nb_ctx) * kTreeKeys;
           for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(ring + (size_t)st * kItem + r * kRegion, m, r * 64, row, x.kvh, &full[st]);
+            tma_load_3d(ring + at.slot * kItem + r * kRegion, m, r * 64, row, x.kvh, &full[at.slot]);
           ++issued;
+          at = at.next();
         }
         if (ok && !q_sent) ok = send_q();
         if (!q_sent) break;
       }
       if (!ok) atomicExch(fail, 1);
       // what is still in flight lands before the memory is released
-      for (int i = max(0, issued - stages); i < issued; ++i)
-        mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        mbar_wait_n(&full[i % kStages], (uint32_t)((i / kStages) & 1), kPolls);
       if (units > 0) mbar_wait_n(qfull, (uint32_t)((units - 1) & 1), ok ? kPolls : 1 << 16);
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      // ---- products
-      const uint32_t ids = idesc_bf16(128, 128), idp = idesc_pv(DH);
-      const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
-      int taken = 0, units = 0;
-      int np[2] = {0, 0};                        // P tiles taken per stream
-      bool ok = true;
-      // the ring slot in turn, landed
-      auto slot = [&](int i) {
-        ok = ok && mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
-        tc_fence_after();
-        return ra + (uint32_t)(i % stages) * kItem;
-      };
-      auto scores = [&](int s, uint32_t kb) {
-        const uint32_t q = qa + (uint32_t)(a.two ? s : 0) * 2 * kItem;
+    // ---- products: the warp runs together, one lane issues
+    const uint32_t lead = tree_elect();
+    constexpr uint32_t ids = idesc_bf16(128, 128), idp = idesc_pv(DH);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
+    Ring<kStages> at;                            // the next K or V block
+    int units = 0;
+    uint32_t pphase[2] = {0, 0};                 // of the streams' P tiles
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, phase, kPolls));
+      tc_fence_after();
+    };
+    auto landed = [&](const Ring<kStages>& r) {
+      wait(&full[r.slot], r.phase);
+      return ra + (uint32_t)r.slot * kItem;
+    };
+    auto scores = [&](int s, uint32_t kb) {
+      const uint32_t q = qa + (uint32_t)(TWO ? s : 0) * 2 * kItem;
 #pragma unroll
-        for (int p = 1; p >= 0; --p)             // the low part first
+      for (int p = 1; p >= 0; --p)               // the low part first
 #pragma unroll
-          for (int ks = 0; ks < DH / 16; ++ks) {
-            const uint32_t rg = (uint32_t)(ks >> 2) * kRegion;
-            mma_bf16_tc(tmem + (uint32_t)s * 128, sw128_desc(q + p * kItem + rg) + 2 * (ks & 3),
-                        sw128_desc(kb + rg) + 2 * (ks & 3), ids, (p == 0 || ks > 0) ? 1u : 0u);
-          }
-        mma_commit(&sfull[s]);
-      };
-      auto values = [&](int s, uint32_t vb, bool first) {
+        for (int ks = 0; ks < DH / 16; ++ks) {
+          const uint32_t rg = (uint32_t)(ks >> 2) * kRegion;
+          tree_mma_ss(lead, tm + (uint32_t)s * 128, sw128_desc(q + p * kItem + rg) + 2 * (ks & 3),
+                      sw128_desc(kb + rg) + 2 * (ks & 3), ids, (p == 0 || ks > 0) ? 1u : 0u);
+        }
+      tree_commit(lead, &sfull[s]);
+    };
+    auto values = [&](int s, uint32_t vb, uint32_t acc) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + kColO + (uint32_t)s * 128, tmem + (uint32_t)s * 128 + 8 * ks,
-                 mn_desc(vb + ks * 2048), idp, (!first || ks > 0) ? 1u : 0u);
-      };
-      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
-        const Unit x = unit_of(a, u);
-        ok = mbar_wait_n(qfull, (uint32_t)(units & 1), kPolls);
-        tc_fence_after();
-        // streams' block counts; a pair's second tile may lie beyond the rows
-        int cnt[2];
-        cnt[0] = a.two ? x.nb : (x.nb + 1) / 2;
-        cnt[1] = a.two ? (x.item * 2 + 1 < a.tiles ? x.nb : 0) : x.nb / 2;
-        int kslot = taken;
-        for (int s = 0; ok && s < 2; ++s)
-          if (cnt[s]) {
-            const uint32_t kb = slot(kslot);
-            if (!ok) break;
-            scores(s, kb);
-            if (!a.two || s == 1 || !cnt[1]) mma_commit(&empty[kslot++ % stages]);
-          }
-        taken = kslot;
-        for (int j = 0; ok && j < cnt[0]; ++j) {
+      for (int ks = 0; ks < 8; ++ks)
+        tree_mma_ts(lead, tm + kColO + (uint32_t)s * 128, tm + (uint32_t)s * 128 + 8 * ks,
+                    mn_desc(vb + ks * 2048), idp, ks > 0 ? 1u : acc);
+    };
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
+      const Unit x = unit_of(a, u);
+      wait(qfull, (uint32_t)(units & 1));
+      // the streams' block counts; a pair's second tile may lie beyond the rows
+      const int cnt0 = TWO ? x.nb : (x.nb + 1) / 2;
+      const int cnt1 = TWO ? (x.item * 2 + 1 < a.tiles ? x.nb : 0) : x.nb / 2;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok || !(s ? cnt1 : cnt0)) continue;
+        const uint32_t kb = landed(at);
+        if (!ok) continue;
+        scores(s, kb);
+        if (!TWO || s == 1 || !cnt1) {
+          tree_commit(lead, &empty[at.slot]);
+          at = at.next();
+        }
+      }
+      for (int j = 0; ok && j < cnt0; ++j) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int cnt = s ? cnt1 : cnt0;
+          if (!ok || j >= cnt) continue;
           // two tiles: V of block j and K of block j + 1 stay for both streams
-          const int v0 = taken;
-          for (int s = 0; ok && s < 2; ++s) {
-            if (j >= cnt[s]) continue;
-            const bool last_user = !a.two || s == 1 || !cnt[1];
-            const int vs = a.two ? v0 : taken;
-            const uint32_t vb = slot(vs);
-            ok = ok && mbar_wait_n(&pready[s], (uint32_t)(np[s]++ & 1), kPolls) && !flagged(fail);
-            if (!ok) break;
-            tc_fence_after();
-            values(s, vb, j == 0);
-            if (last_user) mma_commit(&empty[vs % stages]);
-            const bool more = j + 1 < cnt[s];
-            if (!more) mma_commit(&ofull[s]);
-            if (more) {
-              const int ks = vs + 1;
-              const uint32_t kb = slot(ks);
-              if (!ok) break;
-              scores(s, kb);
-              if (last_user) mma_commit(&empty[ks % stages]);
-            }
-            if (last_user) taken = vs + (more ? 2 : 1);
+          const bool last_user = !TWO || s == 1 || !cnt1, more = j + 1 < cnt;
+          const Ring<kStages> v = at, k = at.next();
+          const uint32_t vb = landed(v);
+          wait(&pready[s], pphase[s]);
+          pphase[s] ^= 1u;
+          ok = __all_sync(0xffffffffu, ok && !tree_flagged(fail));
+          if (!ok) continue;
+          values(s, vb, j > 0 ? 1u : 0u);
+          if (last_user) tree_commit(lead, &empty[v.slot]);
+          if (!more) {
+            tree_commit(lead, &ofull[s]);
+            if (last_user) at = k;
+            continue;
+          }
+          const uint32_t kb = landed(k);
+          if (!ok) continue;
+          scores(s, kb);
+          if (last_user) {
+            tree_commit(lead, &empty[k.slot]);
+            at = k.next();
           }
         }
-        mma_commit(qfree);
       }
-      if (!ok) atomicExch(fail, 1);
-      mma_commit(mdone);
-      mbar_wait_n(mdone, 0u, kPolls);
+      tree_commit(lead, qfree);
     }
+    if (!ok && lane == 0) atomicExch(fail, 1);
+    tree_commit(lead, mdone);
+    mbar_wait_n(mdone, 0u, kPolls);
   } else {
     // ---- softmax: stream s, one thread per row of its tile
     pdl_wait();
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = a.T * a.G;
     int n_s = 0, n_o = 0;
     auto wait_w = [&](uint64_t* bar, uint32_t parity) -> bool {
-      bool okw = !flagged(fail) && mbar_wait_n(bar, parity, kPolls);
+      bool okw = !tree_flagged(fail) && mbar_wait_n(bar, parity, kPolls);
       okw = __all_sync(0xffffffffu, okw);
       if (!okw && lane == 0) atomicExch(fail, 1);
       return okw;
@@ -309,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
       const Unit x = unit_of(a, u);
-      const int tile = a.two ? x.item * 2 + s : x.item;
-      const int cnt = a.two ? (tile < a.tiles ? x.nb : 0) : (x.nb + 1 - s) / 2;
+      const int tile = TWO ? x.item * 2 + s : x.item;
+      const int cnt = TWO ? (tile < a.tiles ? x.nb : 0) : (x.nb + 1 - s) / 2;
       const int row = tile * 128 + r;
       const bool live = row < rows;
       const bool warp_live = tile * 128 + (r & ~31) < rows;
@@ -325,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t sr[4][32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
-          const int b = x.b0 + (a.two ? j : 2 * j + s);
+          const int b = x.b0 + (TWO ? j : 2 * j + s);
           const int left = a.n - b * kTreeKeys;  // context keys from this block on
           const bool whole = b < a.nb_ctx && left >= kTreeKeys;
           uint4 mask = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -360,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
-            const float corr = raise ? ex2(m - bm) : 1.f;
+            const float corr = raise ? tree_ex2(m - bm) : 1.f;
             if (raise) m = bm;
             l *= corr;
             if (j > 0) {  // the stream's products so far are done: S followed them
@@ -383,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(__uint_as_float(sr[q][2 * e]), scale, nm));
-              const float p1 = ex2(fmaf(__uint_as_float(sr[q][2 * e + 1]), scale, nm));
+              const float p0 = tree_ex2(fmaf(__uint_as_float(sr[q][2 * e]), scale, nm));
+              const float p1 = tree_ex2(fmaf(__uint_as_float(sr[q][2 * e + 1]), scale, nm));
               ls[e & 3] += p0 + p1;
               pk[e] = pack_bf16x2(p0, p1);
             }
@@ -403,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      const int slot = a.two ? (x.kvh * a.splits + x.split) * (a.items * 2) + tile
+      const int slot = TWO ? (x.kvh * a.splits + x.split) * (a.items * 2) + tile
                              : (x.kvh * a.splits + x.split) * 2 + s;
       if (warp_live) {
         float* po = a.part_o + (size_t)slot * DH * 128 + (size_t)r * 4;
@@ -436,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && flagged(fail)) atomicExch(a.err, 1);
+  if (tid == 0 && tree_flagged(fail)) atomicExch(a.err, 1);
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -522,7 +517,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (c == 0) a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
 }
 
-template <int DH>
+template <int DH, bool TWO>
 cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
   const int rows = a.T * a.G;
   CUtensorMap mQ, mK, mV, mTK, mTV;
@@ -536,7 +531,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        tree_attn_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        tree_attn_tc_kernel<DH, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
@@ -550,7 +545,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
   lc.stream = st;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH>, mQ, mK, mV, mTK, mTV, a);
+  cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH, TWO>, mQ, mK, mV, mTK, mTV, a);
   if (e != cudaSuccess) return e;
   const int ways = (a.two ? a.splits : 2 * a.splits) >= 16 ? kJoinWarps : 1;
   lc.gridDim = dim3((rows + 31) / 32, a.Hkv, DH / 4 / (kJoinWarps / ways));
@@ -619,7 +614,8 @@ void tree_split(TreeArgs& a) {
 int tree_slots(const TreeArgs& a) { return a.Hkv * a.splits * (a.two ? a.items * 2 : 2); }
 
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s) {
-  return a.dh == 128 ? launch<128>(a, s) : launch<64>(a, s);
+  if (a.dh == 128) return a.two ? launch<128, true>(a, s) : launch<128, false>(a, s);
+  return a.two ? launch<64, true>(a, s) : launch<64, false>(a, s);
 }
 
 }  // namespace ssd

@@ -26,12 +26,6 @@ constexpr int kTileSmem = 224 * 1024;            // Q tiles (hi, lo), then the r
 constexpr int kMaxStages = 12;
 constexpr int kMaxPlanes = 4;
 
-SSD_DI bool flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
-SSD_DI float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Barrier of one stream's 128 threads; true if any of them passed true.
 SSD_DI bool stream_any(int s, bool x) {
   int r;
@@ -138,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; ok && s < nblk; ++s) {
           const int b = b0 + s, st = issued % stages, use = issued / stages;
           if (use > 0) ok = mbar_wait_n(&empty[st], (uint32_t)((use - 1) & 1), kPolls);
-          if (!ok || flagged(fail)) {
+          if (!ok || tree_flagged(fail)) {
             ok = false;
             break;
           }
@@ -150,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
         }
         if (!resident)
-          for (int t = 0; ok && t < a.tiles; ++t) ok = !flagged(fail) && send_q(kvh, t);
+          for (int t = 0; ok && t < a.tiles; ++t) ok = !tree_flagged(fail) && send_q(kvh, t);
       }
       if (!ok) atomicExch(fail, 1);
       for (int i = max(0, issued - stages); i < issued; ++i)
@@ -159,61 +153,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_n(&qfull[i % qslots], (uint32_t)((i / qslots) & 1), kPolls);
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
-      int taken = 0, qtaken = 0;
-      int cs[2] = {0, 0};                        // score tiles per stream
-      bool ok = true;
-      for (int u = rg.u0; ok && u < rg.u1; ++u) {
-        const int kvh = u / pairs, b0 = (u - kvh * pairs) * 2, nblk = min(2, a.nb - b0);
-        for (int s = 0; ok && s < nblk; ++s) {
-          const int i = taken + s;
-          ok = mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
-        }
-        for (int t = 0; ok && t < a.tiles; ++t) {
-          const int cols = min(128, (rows - t * 128 + 15) / 16 * 16);
-          const uint32_t id = idesc_bf16(128, cols);
-          for (int p = 1; ok && p >= 0; --p) {   // the low part first
-            const int qi = qtaken + 2 * t + (1 - p), sl = qi % qslots;
-            ok = mbar_wait_n(&qfull[sl], (uint32_t)((qi / qslots) & 1), kPolls);
-            for (int s = 0; ok && s < nblk; ++s) {
-              const int buf = cs[s] & 1;
-              if (p && cs[s] >= 2)
-                ok = mbar_wait_n(&sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1), kPolls);
-              if (!ok || flagged(fail)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t kb = ra + (uint32_t)((taken + s) % stages) * kItem;
-              const uint32_t qb = qa + (uint32_t)sl * kItem;
+    // the warp runs together, one lane issues
+    const uint32_t lead = tree_elect();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
+    int k0 = 0, kslot[2];                        // K slots of the unit
+    uint32_t kphase = 0;
+    int qslot = 0;
+    uint32_t qphase = 0;
+    int cs[2] = {0, 0};                          // score tiles per stream
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, phase, kPolls));
+      tc_fence_after();
+    };
+    for (int u = rg.u0; ok && u < rg.u1; ++u) {
+      const int kvh = u / pairs, b0 = (u - kvh * pairs) * 2, nblk = min(2, a.nb - b0);
 #pragma unroll
-              for (int ks = 0; ks < DH / 16; ++ks) {
-                const uint32_t o = (uint32_t)(ks >> 2) * kRegion;
-                mma_bf16_tc(tmem + (uint32_t)(s * 256 + buf * 128), sw128_desc(kb + o) + 2 * (ks & 3),
-                            sw128_desc(qb + o) + 2 * (ks & 3), id, (p == 0 || ks > 0) ? 1u : 0u);
-              }
-              if (p == 0) {
-                mma_commit(&sfull[s * 2 + buf]);
-                ++cs[s];
-              }
-            }
-            if (ok && !resident) mma_commit(&qempty[sl]);
+      for (int s = 0; s < 2; ++s)
+        if (s < nblk) {
+          wait(&full[k0], kphase);
+          kslot[s] = k0;
+          if (++k0 == stages) {
+            k0 = 0;
+            kphase ^= 1u;
           }
         }
-        for (int s = 0; ok && s < nblk; ++s) mma_commit(&empty[(taken + s) % stages]);
-        taken += nblk;
-        if (!resident) {
-          qtaken += 2 * a.tiles;
-        } else if ((u + 1) % pairs == 0) {       // the head's last unit
-          for (int i = 0; ok && i < 2 * a.tiles; ++i) mma_commit(&qempty[(qtaken + i) % qslots]);
-          qtaken += 2 * a.tiles;
+      const int q0 = qslot;
+      const uint32_t qp0 = qphase;
+      for (int t = 0; ok && t < a.tiles; ++t) {
+        const int cols = min(128, (rows - t * 128 + 15) / 16 * 16);
+        const uint32_t id = idesc_bf16(128, cols);
+#pragma unroll
+        for (int p = 1; p >= 0; --p) {           // the low part first
+          wait(&qfull[qslot], qphase);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok || s >= nblk) continue;
+            const int buf = cs[s] & 1;
+            if (p && cs[s] >= 2) wait(&sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1));
+            ok = __all_sync(0xffffffffu, ok && !tree_flagged(fail));
+            if (!ok) continue;
+            const uint32_t kb = ra + (uint32_t)kslot[s] * kItem;
+            const uint32_t qb = qa + (uint32_t)qslot * kItem;
+            const uint32_t acc = tm + (uint32_t)(s * 256 + buf * 128);
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks) {
+              const uint32_t o = (uint32_t)(ks >> 2) * kRegion;
+              tree_mma_ss(lead, acc, sw128_desc(kb + o) + 2 * (ks & 3),
+                          sw128_desc(qb + o) + 2 * (ks & 3), id, (p == 0 || ks > 0) ? 1u : 0u);
+            }
+            if (p == 0) {
+              tree_commit(lead, &sfull[s * 2 + buf]);
+              ++cs[s];
+            }
+          }
+          if (!resident) tree_commit(lead, &qempty[qslot]);
+          if (++qslot == qslots) {
+            qslot = 0;
+            qphase ^= 1u;
+          }
         }
       }
-      if (!ok) atomicExch(fail, 1);
-      mma_commit(mdone);
-      mbar_wait_n(mdone, 0u, kPolls);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s < nblk) tree_commit(lead, &empty[kslot[s]]);
+      if (resident) {
+        if ((u + 1) % pairs == 0) {              // the head's last unit
+          for (int i = 0; i < 2 * a.tiles; ++i) tree_commit(lead, &qempty[i]);
+        } else {                                 // the same planes again
+          qslot = q0;
+          qphase = qp0;
+        }
+      }
     }
+    if (!ok && lane == 0) atomicExch(fail, 1);
+    tree_commit(lead, mdone);
+    mbar_wait_n(mdone, 0u, kPolls);
   } else {
     // one key per thread.  Every thread passes every barrier: a wait that
     // gives up only turns the sums into NaN.
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           next = row_lse(kvh, t + 1);
         else if (u + 1 < rg.u1)
           next = row_lse((u + 1) / pairs, 0);
-        ok = ok && !flagged(fail) && mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
+        ok = ok && !tree_flagged(fail) && mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
         const bool all_ok = __all_sync(0xffffffffu, ok);
         if (!all_ok) {
           if (lane == 0) atomicExch(fail, 1);
@@ -288,10 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                   const float4 n4 = *reinterpret_cast<const float4*>(nl + q0 + e);
-                  sum[0] += ex2(fmaf(__uint_as_float(v[hlf][e]), scale, n4.x));
-                  sum[1] += ex2(fmaf(__uint_as_float(v[hlf][e + 1]), scale, n4.y));
-                  sum[2] += ex2(fmaf(__uint_as_float(v[hlf][e + 2]), scale, n4.z));
-                  sum[3] += ex2(fmaf(__uint_as_float(v[hlf][e + 3]), scale, n4.w));
+                  sum[0] += tree_ex2(fmaf(__uint_as_float(v[hlf][e]), scale, n4.x));
+                  sum[1] += tree_ex2(fmaf(__uint_as_float(v[hlf][e + 1]), scale, n4.y));
+                  sum[2] += tree_ex2(fmaf(__uint_as_float(v[hlf][e + 2]), scale, n4.z));
+                  sum[3] += tree_ex2(fmaf(__uint_as_float(v[hlf][e + 3]), scale, n4.w));
                 }
               } else {
                 // a tree block: lane e holds the ancestor word of row q0 + e
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   const uint32_t w = __shfl_sync(0xffffffffu, mine, e);
-                  const float p = ex2(fmaf(__uint_as_float(v[hlf][e]), scale, nl[q0 + e]));
+                  const float p = tree_ex2(fmaf(__uint_as_float(v[hlf][e]), scale, nl[q0 + e]));
                   if ((w >> lane) & 1u) sum[e & 3] += p;
                 }
               }
