@@ -14,7 +14,7 @@ namespace ssd {
 namespace {
 
 constexpr int kPieceThreads = 512;
-constexpr int kPieceItems = 40;
+constexpr int kPieceItems = 44;
 constexpr int kPieceMax = kPieceThreads * kPieceItems;  // logits per CTA at most
 constexpr int kMergeThreads = 1024;
 constexpr int kMaxCluster = 8;      // portable cluster size
@@ -142,8 +142,11 @@ __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const Beam
   piece_body<G>(a, len, blockIdx.x, gridDim.x, blockIdx.y);
 }
 
+// A candidate in the whole order: the 64-bit score as an ordered integer
+// (64-bit arithmetic runs at a 64th of the 32-bit rate: it is kept to the few
+// candidates over the threshold, and comparisons are integers').
 struct Cand {
-  double s;
+  uint64_t s;
   uint64_t k;
   int b;
 };
@@ -152,25 +155,46 @@ SSD_DI bool before(const Cand& x, const Cand& y) {
   if (x.b != y.b) return x.b < y.b;
   return x.k > y.k;
 }
+SSD_DI uint64_t ordered(double s) {
+  const uint64_t u = (uint64_t)__double_as_longlong(s + 0.0);
+  return (u >> 63) ? ~u : (u | (1ull << 63));
+}
+SSD_DI double unordered(uint64_t o) {
+  return __longlong_as_double((long long)((o >> 63) ? (o & ~(1ull << 63)) : ~o));
+}
 
 // What the scores of a beam's candidates share, in shared memory.
 struct Beam {
-  double score, lse;
+  float score, lse;
   int ended;
 };
 
-// Entry d of list i; s = -infinity where there is no candidate.
-SSD_DI Cand candidate(const BeamArgs& a, const Beam* beams, int pieces, int i, int d) {
-  Cand x;
-  x.b = i / pieces;
-  const Beam& m = beams[x.b];
-  x.k = m.ended ? (uint64_t)(d == 0 && i == x.b * pieces) : a.lists[(size_t)i * a.W + d];
-  x.s = -INFINITY;
-  if (x.k) {
-    x.s = m.ended ? m.score : m.score + ((double)key_logit(x.k) - m.lse);
-    if (!(x.s > -INFINITY)) x.s = -INFINITY;     // NaN
-  }
-  return x;
+// Entry d of list i, 0 where there is none (an ended beam has one entry, 1).
+SSD_DI uint64_t entry(const BeamArgs& a, const Beam* beams, int pieces, int i, int d) {
+  const int b = i / pieces;
+  if (beams[b].ended) return (uint64_t)(d == 0 && i == b * pieces);
+  return a.lists[(size_t)i * a.W + d];
+}
+
+// The candidate of an entry; false where its score is NaN or -infinity.
+SSD_DI bool score(const Beam& m, uint64_t k, int b, Cand& c) {
+  const double sc = (double)m.score;
+  const double s = m.ended ? sc : sc + ((double)key_logit(k) - (double)m.lse);
+  c.s = ordered(s);
+  c.k = k;
+  c.b = b;
+  return s > -INFINITY;
+}
+
+// Bounds of that score in 32-bit arithmetic: the two sums are off by half a
+// step each, 2^-24 of |z| + |lse| and of the whole.  Overflow to an infinity
+// bounds from one side only; NaN (inf - inf) gives no bound.
+SSD_DI void score_bounds(const Beam& m, uint64_t k, float& lower, float& upper) {
+  const float z = key_logit(k);
+  const float f = m.ended ? m.score : m.score + (z - m.lse);
+  const float e = m.ended ? 0.f : (fabsf(z) + fabsf(m.lse) + fabsf(m.score)) * 2.4e-7f;
+  lower = fabsf(f) < INFINITY && e < INFINITY ? f - e : f > 0.f ? 3e38f : -INFINITY;
+  upper = fabsf(f) < INFINITY && e < INFINITY ? f + e : f == -INFINITY ? -3e38f : INFINITY;
 }
 
 SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool got) {
@@ -178,16 +202,16 @@ SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool
   const int token = !got ? -1 : ended ? a.end_id : key_token(c.k);
   a.tokens[w] = token;
   a.parents[w] = got ? c.b : -1;
-  a.scores_out[w] = got ? (float)c.s : -INFINITY;
+  a.scores_out[w] = got ? (float)unordered(c.s) : -INFINITY;
   if (a.done_out) a.done_out[w] = !got || token == a.end_id;
 }
 
 // One CTA: the W best of all lists, which are sorted.  The lists' first
 // entries (their first few, where there are fewer lists than W) are W
-// candidates at least, so the W-th largest of them, or of their maxima over
-// 256 groups, is a threshold that W candidates reach; what lies before it in
-// each list is collected and ranked by the whole order.  The threshold is on
-// scores rounded to 32 bits, which keeps their order.
+// candidates at least, so the W-th largest of their lower bounds, or of the
+// bounds' maxima over 256 groups, is a threshold that W candidates reach; the
+// entries of each list whose upper bound reaches it are collected and ranked
+// by the whole order.
 template <int kThreads>
 SSD_DI void merge_body(const BeamArgs& a, int pieces) {
   constexpr int kGroups = 256, kPer = kThreads / kGroups;
@@ -198,8 +222,8 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
   __shared__ int s_n;
   const int tid = threadIdx.x, lists = a.B * pieces;
   if (tid < a.B) {
-    beams[tid].score = (double)a.scores[tid];
-    beams[tid].lse = a.lse ? (double)a.lse[(size_t)tid * a.lse_stride] : 0.0;
+    beams[tid].score = a.scores[tid];
+    beams[tid].lse = a.lse ? a.lse[(size_t)tid * a.lse_stride] : 0.f;
     beams[tid].ended = a.done && a.done[tid];
   }
   if (tid == 0) s_n = 0;
@@ -207,10 +231,13 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
   // sample j: entry j / lists of list j % lists; 256 in a row go to 256 groups
   const int deep = min(a.W, (a.W + lists - 1) / lists), samples = lists * deep;
   float mx = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
   for (int j = tid / kPer + kGroups * (tid % kPer); j < samples; j += kThreads) {
-    const int d = j / lists;
-    mx = fmaxf(mx, (float)candidate(a, beams, pieces, j - d * lists, d).s);
+    const int d = j / lists, i = j - d * lists;
+    const uint64_t k = entry(a, beams, pieces, i, d);
+    float lo, up;
+    score_bounds(beams[i / pieces], k, lo, up);
+    if (k) mx = fmaxf(mx, lo);
   }
 #pragma unroll
   for (int d = 1; d < kThreads / kGroups; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
@@ -220,14 +247,16 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
     for (int d0 = 0; d0 < a.W; d0 += 8) {
       const int d = d0 + (tid & 7);
       bool in = false;
-      Cand c;
-      if (d < a.W) {
-        c = candidate(a, beams, pieces, i, d);
-        in = c.s > -INFINITY && (float)c.s >= cut;
-      }
-      if (in) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kList) list[at] = c;
+      const uint64_t k = d < a.W ? entry(a, beams, pieces, i, d) : 0;
+      if (k) {
+        float lo, up;
+        score_bounds(beams[i / pieces], k, lo, up);
+        Cand c;
+        in = up >= cut;
+        if (in && score(beams[i / pieces], k, i / pieces, c)) {
+          const int at = atomicAdd(&s_n, 1);
+          if (at < kList) list[at] = c;
+        }
       }
       const unsigned group = 0xffu << (tid & 24);
       if (__ballot_sync(group, in) != group) break;
@@ -246,14 +275,15 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
     return;
   }
   // many equal scores: W maxima in turn, each below the one before
-  const Cand none = {-INFINITY, 0, 1 << 30};
-  Cand last = {INFINITY, ~0ull, -1};
+  const Cand none = {0, 0, 1 << 30};
+  Cand last = {~0ull, ~0ull, -1};
   for (int w = 0; w < a.W; ++w) {
     Cand c = none;
     for (int i = tid; i < lists; i += kThreads)
       for (int d = 0; d < a.W; ++d) {
-        const Cand x = candidate(a, beams, pieces, i, d);
-        if (!(x.s > -INFINITY)) break;           // the list's end
+        const uint64_t k = entry(a, beams, pieces, i, d);
+        Cand x;
+        if (!k || !score(beams[i / pieces], k, i / pieces, x)) break;  // the list's end
         if (!before(last, x)) continue;
         if (before(x, c)) c = x;
         break;                                   // the rest of the list comes after

@@ -175,7 +175,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
           if ((u >> above) == (cut >> above)) atomicAdd(&sum[(u >> shift) & mask], 1);
         }
       }
-      cluster.sync();
+      if (nc > 1)
+        cluster.sync();
+      else
+        __syncthreads();
       // thread t takes the bins 2047 - 2 t and 2046 - 2 t, so that lower
       // threads hold larger keys
       const int b1 = kBins - 1 - 2 * tid;
@@ -242,12 +245,11 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const int middle = a.n - a.sinks - a.recent, want = a.keep - a.sinks - a.recent;
   // Few rows that stay: the selecting CTA copies them (one launch).
   const bool few = (long long)a.keep * a.units <= kFusedUnits && a.keep <= kFusedRows;
-  // A CTA per 1024 middle rows up to the portable cluster size, while all
-  // heads' clusters fit the SMs.
+  // A CTA per 8192 middle rows up to the portable cluster size: the exchange
+  // of histograms costs a cluster more than a CTA's longer runs (40 heads of
+  // 4095 rows: 12 us with one CTA per head, 25 us with four).
   int nc = 1;
-  while (nc < kMaxCluster && middle > kRankKeys && (long long)nc * 1024 < middle &&
-         2LL * nc * a.Hkv <= 304)
-    nc *= 2;
+  while (nc < kMaxCluster && (long long)nc * 8192 < middle) nc *= 2;
   const bool fused = few && nc == 1;
   const int share = (middle + nc - 1) / nc;
   const bool ranked = want == 0 || (nc == 1 && share <= kRankKeys);

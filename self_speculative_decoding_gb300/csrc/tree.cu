@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
   }
   __syncthreads();
   for (int h = h0 + tid; h < h1; h += kPrepThreads)
-    if (h >= a.H + a.Hkv) a.vbad[(size_t)(h - a.H - a.Hkv) * a.T + t] = (uint8_t)bad[h - h0];
+    if (h >= a.H + a.Hkv) a.vbad[(size_t)(h - a.H - a.Hkv) * tree_vbad_stride(a.T) + t] = (uint8_t)bad[h - h0];
 }
 
 }  // namespace
@@ -123,7 +123,7 @@ size_t tree_workspace(TreeArgs& a, void* base) {
   a.anc_words = tree_anc_words(a.T);
   a.anc = (uint32_t*)take((size_t)a.T * a.anc_words * 4);
   a.depth = (int32_t*)take((size_t)a.T * 4);
-  a.vbad = (uint8_t*)take((size_t)a.Hkv * a.T);
+  a.vbad = (uint8_t*)take((size_t)a.Hkv * tree_vbad_stride(a.T));
   a.q = (bf16*)take(2 * a.Hkv * rows * a.dh * sizeof(bf16));
   a.kt = (bf16*)take((size_t)a.Hkv * a.T * a.dh * sizeof(bf16));
   a.vt = (bf16*)take((size_t)a.Hkv * a.T * a.dh * sizeof(bf16));

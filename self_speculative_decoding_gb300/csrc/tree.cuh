@@ -28,7 +28,7 @@ struct TreeArgs {
   // workspace
   uint32_t* anc = nullptr;           // [T][anc_words] ancestors-and-self bits
   int32_t* depth = nullptr;          // [T] ancestors above the node, -1 absent
-  uint8_t* vbad = nullptr;           // [Hkv][T] the node's V row holds inf or NaN
+  uint8_t* vbad = nullptr;           // [Hkv][T rounded up to 4] the node's V row holds inf or NaN
   bf16* q = nullptr;                 // [2][Hkv][T G][dh]: the rotated query's high and low part
   bf16* kt = nullptr;                // [Hkv][T][dh] the tree's K rows
   bf16* vt = nullptr;                // [Hkv][T][dh] its V rows, inf and NaN as 0
@@ -47,6 +47,8 @@ struct TreeArgs {
 };
 
 SSD_HD int tree_anc_words(int T) { return 4 * ((T + kTreeKeys - 1) / kTreeKeys); }
+
+SSD_HD size_t tree_vbad_stride(int T) { return ((size_t)T + 3) & ~(size_t)3; }
 
 // Sets the work split and the workspace pointers of `a` (sizes already set)
 // from base and returns the bytes used; with base NULL only the size.

@@ -61,6 +61,31 @@ SSD_DI uint64_t mn_desc(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t idesc_pv(int N) {
   return idesc_bf16(128, N) | (1u << 16);        // B is MN-major
 }
+// Pairs of fp32 values in one instruction, and the maximum of three.
+SSD_DI uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+SSD_DI void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+SSD_DI uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+SSD_DI uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SSD_DI float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Block range of a unit and its place.
 struct Unit {
   int kvh, item, split, b0, nb;
@@ -319,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp_live) {
           uint32_t sr[4][32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
+          for (int q = 0; q < 2; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
           const int b = x.b0 + (TWO ? j : 2 * j + s);
           const int left = a.n - b * kTreeKeys;  // context keys from this block on
           const bool whole = b < a.nb_ctx && left >= kTreeKeys;
@@ -336,23 +361,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               mask = make_uint4(low(0), low(1), low(2), low(3));
             }
           }
+          // the second half loads while the first half's maximum is taken
           tmem_wait_ld();
+          tmem_pin32(sr[0]);
+          tmem_pin32(sr[1]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_pin32(sr[q]);
-          if (!whole) {
-            const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((mw[q] >> e) & 1u)) sr[q][e] = 0xff800000u;  // -infinity
-          }
+          for (int q = 2; q < 4; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
+          const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int hlf = 0; hlf < 2; ++hlf) {
+            if (hlf == 1) {
+              tmem_wait_ld();
+              tmem_pin32(sr[2]);
+              tmem_pin32(sr[3]);
+            }
+            if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sr[q][e]));
-          const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+              for (int q = 2 * hlf; q < 2 * hlf + 2; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((mw[q] >> e) & 1u)) sr[q][e] = 0xff800000u;  // -infinity
+            }
+#pragma unroll
+            for (int q = 2 * hlf; q < 2 * hlf + 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[q][e]),
+                                        __uint_as_float(sr[q][e + 1]));
+          }
+          const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
           const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
             const float corr = raise ? tree_ex2(m - bm) : 1.f;
@@ -372,20 +410,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float nm = m == -INFINITY ? 0.f : -m;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
+          const uint64_t nm2 = pack2(__float_as_uint(nm), __float_as_uint(nm));
+          uint64_t ls2[2] = {0, 0};              // pairs of partial sums
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = tree_ex2(fmaf(__uint_as_float(sr[q][2 * e]), scale, nm));
-              const float p1 = tree_ex2(fmaf(__uint_as_float(sr[q][2 * e + 1]), scale, nm));
-              ls[e & 3] += p0 + p1;
+              float p0, p1;
+              unpack2(fma2(pack2(sr[q][2 * e], sr[q][2 * e + 1]), sc2, nm2), p0, p1);
+              p0 = tree_ex2(p0);
+              p1 = tree_ex2(p1);
+              ls2[e & 1] = add2(ls2[e & 1], pack2(__float_as_uint(p0), __float_as_uint(p1)));
               pk[e] = pack_bf16x2(p0, p1);
             }
             tmem_st16(trow + col_s + q * 16, pk);
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          float l0, l1;
+          unpack2(add2(ls2[0], ls2[1]), l0, l1);
+          l += l0 + l1;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -435,86 +479,117 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the units' partial results: lane = row of one K/V head, warp = four
-// output columns; the slots are added in order.  Where there are many, `ways`
-// warps of the CTA share the columns and each adds every ways-th slot.
+// Joins the units' partial results: CTA = 32 rows of one K/V head, lane = row;
+// the slots are added in order.  With WAYS = 1 each warp has an eighth of the
+// columns; with WAYS = 8 (many slots, few rows) a CTA has one 16-byte column
+// and each warp every eighth slot.  Rows leave through shared memory, so that
+// stores are whole rows.
 constexpr int kJoinWarps = 8;
-template <int DH>
+template <int DH, int WAYS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    tree_join_kernel(const __grid_constant__ TreeArgs a, int ways) {
-  __shared__ float4 s_o[kJoinWarps][32];
+    tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kChunks = WAYS > 1 ? 1 : DH / 4 / kJoinWarps;  // 16-byte columns per warp
+  __shared__ float4 s_o[kJoinWarps * kChunks][33];
   __shared__ float s_l[kJoinWarps][32];
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = warp % ways;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = WAYS > 1 ? warp : 0;
   const int rows = a.T * a.G, kvh = blockIdx.y;
   const int row = min(blockIdx.x * 32 + lane, rows - 1);
-  const int c = blockIdx.z * (kJoinWarps / ways) + warp / ways;  // 16-byte chunk
+  const int c0 = WAYS > 1 ? blockIdx.z : warp * kChunks;
   const int tile = row >> 7, r = row & 127, t = row / a.G;
   const int per = a.two ? a.items * 2 : 2;       // slots per (head, split)
   const int step = a.two ? per : 1, count = a.two ? a.splits : 2 * a.splits;
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
+  pdl_wait();
+  pdl_trigger();
   const bool present = a.depth[t] >= 0, bad = *a.err != 0;
   float m = -INFINITY;
 #pragma unroll 8
   for (int i = 0; i < count; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * step) * 128 + r]);
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 o[kChunks];
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = way; i < count; i += ways) {
+  for (int i = way; i < count; i += WAYS) {
     const size_t sl = s0 + (size_t)i * step;
     const float w = exp2f(a.part_m[sl * 128 + r] - base);
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 + (size_t)c * 512 + r * 4);
     l = fmaf(a.part_l[sl * 128 + r], w, l);
-    o.x = fmaf(v.x, w, o.x);
-    o.y = fmaf(v.y, w, o.y);
-    o.z = fmaf(v.z, w, o.z);
-    o.w = fmaf(v.w, w, o.w);
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 +
+                                                        (size_t)(c0 + q) * 512 + r * 4);
+      o[q].x = fmaf(v.x, w, o[q].x);
+      o[q].y = fmaf(v.y, w, o[q].y);
+      o[q].z = fmaf(v.z, w, o[q].z);
+      o[q].w = fmaf(v.w, w, o[q].w);
+    }
   }
-  if (ways > 1) {
-    s_o[warp][lane] = o;
+  if (WAYS > 1) {
+    s_o[warp][lane] = o[0];
     s_l[warp][lane] = l;
     __syncthreads();
     if (way) return;
-    for (int i = 1; i < ways; ++i) {
-      const float4 v = s_o[warp + i][lane];
-      l += s_l[warp + i][lane];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
+    for (int i = 1; i < WAYS; ++i) {
+      const float4 v = s_o[i][lane];
+      l += s_l[i][lane];
+      o[0].x += v.x;
+      o[0].y += v.y;
+      o[0].z += v.z;
+      o[0].w += v.w;
     }
   }
-  if (blockIdx.x * 32 + lane >= rows) return;
   const float lse = l != 0.f ? m + log2f(l) : INFINITY;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  if (present) {
-    // inf and NaN of the V rows that this row sees (left out of the products)
-    const uint8_t* flags = a.vbad + (size_t)kvh * a.T;
-    for (int j = 0; j <= t; ++j) {
-      if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
-      const size_t plane = (size_t)a.Hkv * rows * DH;
-      const bf16* q = a.q + ((size_t)kvh * rows + row) * DH;
-      const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
-      float acc = 0.f;
-      for (int i = 0; i < DH; ++i)
-        acc = fmaf(__bfloat162float(q[i]) + __bfloat162float(q[plane + i]), __bfloat162float(k[i]), acc);
-      const float p = exp2f(acc * a.scale_log2 - lse);
-      for (int e = 0; e < 4; ++e) {
-        const float x = __bfloat162float(a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + c * 4 + e]);
-        if (!isfinite(x)) v[e] += p * x;
+  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) {
+    float v[4] = {o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv};
+    if (present) {
+      // inf and NaN of the V rows that this row sees (left out of the products)
+      for (int j0 = 0; j0 <= t; j0 += 4) {
+        if (j0 + 3 < a.T && *reinterpret_cast<const uint32_t*>(flags + j0) == 0u) continue;
+        for (int j = j0; j <= t && j < j0 + 4; ++j) {
+          if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+          const size_t plane = (size_t)a.Hkv * rows * DH;
+          const bf16* qr = a.q + ((size_t)kvh * rows + row) * DH;
+          const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
+          float acc = 0.f;
+          for (int i = 0; i < DH; ++i)
+            acc = fmaf(__bfloat162float(qr[i]) + __bfloat162float(qr[plane + i]),
+                       __bfloat162float(k[i]), acc);
+          const float p = exp2f(acc * a.scale_log2 - lse);
+          for (int e = 0; e < 4; ++e) {
+            const float x = __bfloat162float(
+                a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + (c0 + q) * 4 + e]);
+            if (!isfinite(x)) v[e] += p * x;
+          }
+        }
       }
+    } else {
+      v[0] = v[1] = v[2] = v[3] = 0.f;
     }
-  } else {
-    v[0] = v[1] = v[2] = v[3] = 0.f;
+    if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
+    const uint2 packed = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    if (WAYS > 1) {
+      if (blockIdx.x * 32 + lane < rows)
+        *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.H + kvh * a.G + row % a.G) * DH + c0 * 4) =
+            packed;
+    } else {
+      reinterpret_cast<uint2*>(&s_o[warp * kChunks + q][lane])[0] = packed;
+    }
   }
-  if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
-  const int h = kvh * a.G + row % a.G;
-  uint2 packed = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-  *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.H + h) * DH + c * 4) = packed;
-  if (c == 0) a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
+  if (c0 == 0 && blockIdx.x * 32 + lane < rows)
+    a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
+  if (WAYS > 1) return;
+  __syncthreads();
+  // DH / 4 consecutive lanes write a row
+  for (int e = threadIdx.x; e < 32 * (DH / 4); e += kJoinWarps * 32) {
+    const int i = e / (DH / 4), c = e % (DH / 4), rw = blockIdx.x * 32 + i;
+    if (rw < rows)
+      *reinterpret_cast<uint2*>(a.out + ((size_t)(rw / a.G) * a.H + kvh * a.G + rw % a.G) * DH +
+                                c * 4) = *reinterpret_cast<const uint2*>(&s_o[c][i]);
+  }
 }
 
 template <int DH, bool TWO>
@@ -547,11 +622,12 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
   lc.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH, TWO>, mQ, mK, mV, mTK, mTV, a);
   if (e != cudaSuccess) return e;
-  const int ways = (a.two ? a.splits : 2 * a.splits) >= 16 ? kJoinWarps : 1;
-  lc.gridDim = dim3((rows + 31) / 32, a.Hkv, DH / 4 / (kJoinWarps / ways));
+  const bool many = (a.two ? a.splits : 2 * a.splits) >= 16;
+  lc.gridDim = dim3((rows + 31) / 32, a.Hkv, many ? DH / 4 : 1);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, tree_join_kernel<DH>, a, ways);
+  return many ? cudaLaunchKernelEx(&lc, tree_join_kernel<DH, kJoinWarps>, a)
+              : cudaLaunchKernelEx(&lc, tree_join_kernel<DH, 1>, a);
 }
 
 }  // namespace
