@@ -6,6 +6,7 @@
 // every cache row < n, its ancestors and itself:
 //   out_t = sum_j softmax_j(q_t k_j / sqrt(dh)) v_j.
 // A row whose chain does not end in -1 is absent.
+#include "tc_dev.cuh"
 #include "tree.cuh"
 
 namespace ssd {
@@ -108,6 +109,19 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
     if (h >= a.H + a.Hkv) a.vbad[(size_t)(h - a.H - a.Hkv) * tree_vbad_stride(a.T) + t] = (uint8_t)bad[h - h0];
 }
 
+// d2 matrices of d1 rows of dh bf16, `stride` bytes apart, in 128-row boxes.
+bool tree_map(CUtensorMap* m, const void* base, int dh, int d1, int d2, size_t stride) {
+  EncodeTiled enc = tma_encoder();
+  const cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)d1, (cuuint64_t)d2};
+  const cuuint64_t strides[2] = {dh * sizeof(bf16), stride};
+  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 size_t tree_workspace(TreeArgs& a, void* base) {
@@ -124,9 +138,11 @@ size_t tree_workspace(TreeArgs& a, void* base) {
   a.anc = (uint32_t*)take((size_t)a.T * a.anc_words * 4);
   a.depth = (int32_t*)take((size_t)a.T * 4);
   a.vbad = (uint8_t*)take((size_t)a.Hkv * tree_vbad_stride(a.T));
-  a.q = (bf16*)take(2 * a.Hkv * rows * a.dh * sizeof(bf16));
-  a.kt = (bf16*)take((size_t)a.Hkv * a.T * a.dh * sizeof(bf16));
-  a.vt = (bf16*)take((size_t)a.Hkv * a.T * a.dh * sizeof(bf16));
+  a.row_kt = (int)(2 * a.Hkv * rows);
+  a.row_vt = a.row_kt + a.Hkv * a.T;
+  a.q = (bf16*)take((size_t)(a.row_vt + a.Hkv * a.T) * a.dh * sizeof(bf16));
+  a.kt = a.q + (size_t)a.row_kt * a.dh;
+  a.vt = a.q + (size_t)a.row_vt * a.dh;
   a.lse = (float*)take(a.Hkv * rows * 4);
   a.part_o = (float*)take(slots * a.dh * 128 * 4);
   a.part_m = (float*)take(slots * 128 * 4);
@@ -140,8 +156,15 @@ cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
   tree_prep_kernel<<<dim3(a.T, (heads + kPrepHeads - 1) / kPrepHeads), kPrepThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = launch_tree_attn_tc(a, s)) != cudaSuccess || !a.w_out) return e;
-  return launch_tree_weight_tc(a, tree_sms(), s);
+  TreeMaps m;
+  const size_t cache_row = (size_t)a.dh * sizeof(bf16);
+  const int n = a.n ? a.n : 1;                   // no context: never read
+  if (!tree_map(&m.k, a.kc, a.dh, n, a.Hkv, a.max_seq * cache_row) ||
+      !tree_map(&m.v, a.vc, a.dh, n, a.Hkv, a.max_seq * cache_row) ||
+      !tree_map(&m.ws, a.q, a.dh, a.row_vt + a.Hkv * a.T, 1, cache_row))
+    return cudaErrorInvalidValue;
+  if ((e = launch_tree_attn_tc(a, m, s)) != cudaSuccess || !a.w_out) return e;
+  return launch_tree_weight_tc(a, m, s);
 }
 
 }  // namespace ssd

@@ -38,10 +38,11 @@ struct TreeArgs {
   float* part_l = nullptr;           // [slots][128] sum of 2^(score - maximum)
   int* err = nullptr;                // non-zero: a bounded wait gave up
   int anc_words = 0;
+  int row_kt = 0, row_vt = 0;        // first row of kt and vt in the workspace's matrix
   // the rows in tiles of 128, the keys in blocks of 128 (the context's, then
   // the tree's); a unit = (head, split, item): a run of key blocks for one tile
   // (two = 0: blocks in turn to two streams) or a pair of tiles (two = 1: one
-  // stream each)
+  // stream each); with one split a unit's result is final
   int tiles = 0, two = 0, items = 0, nb_ctx = 0, nb = 0, splits = 0, units = 0, ctas = 0;
   double inv_freq[kTreeMaxHalf];     // theta^(-2 i / dh) / pi
 };
@@ -57,11 +58,16 @@ cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 void tree_split(TreeArgs& a);        // tree_attn_tc.cu
 int tree_slots(const TreeArgs& a);
 int tree_sms();                      // SMs of the current device
-// Tensor map of 128-row boxes of [d2][stride rows][dh] bf16, d1 rows of each
-// seen (the others read as zero).
-bool tree_map(CUtensorMap* m, const void* base, int dh, int d1, int d2, int stride);
-cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s);
-cudaError_t launch_tree_weight_tc(const TreeArgs& a, int sms, cudaStream_t s);
+// Tensor maps of 128-row boxes: the caches ([Hkv][max_seq][dh], rows < n of
+// each head seen, the others read as zero), and the workspace's rows (the two
+// planes of q, kt and vt one behind the other, seen as one matrix: a box that
+// runs over the end of a head reads rows of what follows, all finite, whose
+// results nothing takes).
+struct TreeMaps {
+  CUtensorMap k, v, ws;
+};
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, const TreeMaps& m, cudaStream_t s);
+cudaError_t launch_tree_weight_tc(const TreeArgs& a, const TreeMaps& m, cudaStream_t s);
 
 // ---- device helpers of the two tensor-core kernels
 

@@ -102,13 +102,42 @@ SSD_DI Unit unit_of(const TreeArgs& a, int u) {
   return x;
 }
 
+// Whether any node's V row of this head holds inf or NaN (a warp asks).
+SSD_DI bool any_bad(const TreeArgs& a, int kvh, int lane) {
+  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
+  bool any = false;
+  for (int j = lane; j < a.T; j += 32) any |= flags[j] != 0;
+  return __any_sync(0xffffffffu, any);
+}
+
+// Adds to n columns from c0 on of row (node t) the inf and NaN of the V rows
+// that it sees, which the products left out: v += p_j V_j for those values.
+template <int DH>
+__device__ __noinline__ void add_bad(const TreeArgs& a, int kvh, int row, int t, float lse, int c0,
+                                     float* v, int n) {
+  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
+  const int rows = a.T * a.G;
+  const size_t plane = (size_t)a.Hkv * rows * DH;
+  const bf16* q = a.q + ((size_t)kvh * rows + row) * DH;
+  for (int j = 0; j <= t; ++j) {
+    if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+    const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
+    float acc = 0.f;
+    for (int i = 0; i < DH; ++i)
+      acc = fmaf(__bfloat162float(q[i]) + __bfloat162float(q[plane + i]), __bfloat162float(k[i]), acc);
+    const float p = exp2f(acc * a.scale_log2 - lse);
+    for (int e = 0; e < n; ++e) {
+      const float x = __bfloat162float(a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + c0 + e]);
+      if (!isfinite(x)) v[e] += p * x;
+    }
+  }
+}
+
 template <int DH, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ,
-                        const __grid_constant__ CUtensorMap mK,
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mK,
                         const __grid_constant__ CUtensorMap mV,
-                        const __grid_constant__ CUtensorMap mTK,
-                        const __grid_constant__ CUtensorMap mTV,
+                        const __grid_constant__ CUtensorMap mW,
                         const __grid_constant__ TreeArgs a) {
   constexpr int kRegs = DH / 64;                 // 64-column regions per row block
   constexpr int kItem = kRegs * kRegion;         // bytes of a K or V block, or a Q plane
@@ -118,18 +147,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kTileSmem);
+  float* xm = reinterpret_cast<float*>(sm + kTileSmem);  // stream 1's maxima and sums
+  float* xl = xm + 128;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(xl + 128);
   uint64_t* qfull = bars;
   uint64_t* qfree = bars + 1;
   uint64_t* sfull = bars + 2;                    // [2] S written
   uint64_t* pready = bars + 4;                   // [2] P written, O rescaled
   uint64_t* ofull = bars + 6;                    // [2] the unit's last product done
   uint64_t* mdone = bars + 8;
-  uint64_t* full = bars + 9;                     // [stages]
+  uint64_t* given = bars + 9;                    // stream 1's statistics written
+  uint64_t* taken = bars + 10;                   // and its output read by stream 0
+  uint64_t* full = bars + 11;                    // [stages]
   uint64_t* empty = full + kStages;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kStages);
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = a.T * a.G;
   unsigned char* ring = sm + kTiles * 2 * kItem;
 
   if (tid == 0) {
@@ -141,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ofull[s], 1);
     }
     mbar_init(mdone, 1);
+    mbar_init(given, 128);
+    mbar_init(taken, 128);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -158,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       // ---- copies, in the order in which the products use them: K of the
       // first `lag` blocks, then V of block i and K of block i + lag in turn
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&mQ) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mW) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&mK) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&mV) : "memory");
       Ring<kStages> at;
@@ -178,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < kTiles; ++t)
             for (int p = 0; p < 2; ++p)
               for (int r = 0; r < kRegs; ++r)
-                tma_load_3d(sm + (t * 2 + p) * kItem + r * kRegion, &mQ, r * 64,
-                            (x.item * kTiles + t) * 128, p * a.Hkv + x.kvh, qfull);
+                tma_load_3d(sm + (t * 2 + p) * kItem + r * kRegion, &mW, r * 64,
+                            (p * a.Hkv + x.kvh) * rows + (x.item * kTiles + t) * 128, 0, qfull);
           q_sent = true;
           return true;
         };
@@ -208,10 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[at.slot], (uint32_t)kItem);
-          const CUtensorMap* m = ctx ? (is_v ? &mV : &mK) : (is_v ? &mTV : &mTK);
-          const int row = (ctx ? b : b - a.nb_ctx) * kTreeKeys;
+          const CUtensorMap* m = !ctx ? &mW : is_v ? &mV : &mK;
+          const int row = ctx ? b * kTreeKeys
+                              : (is_v ? a.row_vt : a.row_kt) + x.kvh * a.T + (b - a.nb_ctx) * kTreeKeys;
           for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(ring + at.slot * kItem + r * kRegion, m, r * 64, row, x.kvh, &full[at.slot]);
+            tma_load_3d(ring + at.slot * kItem + r * kRegion, m, r * 64, row, ctx ? x.kvh : 0,
+                        &full[at.slot]);
           ++issued;
           at = at.next();
         }
@@ -318,8 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t col_s = (uint32_t)s * 128, col_o = kColO + (uint32_t)s * 128;
     const float scale = a.scale_log2;
-    const int rows = a.T * a.G;
-    int n_s = 0, n_o = 0;
+    int n_s = 0, n_own = 0, n_other = 0, units = 0;
     auto wait_w = [&](uint64_t* bar, uint32_t parity) -> bool {
       bool okw = !tree_flagged(fail) && mbar_wait_n(bar, parity, kPolls);
       okw = __all_sync(0xffffffffu, okw);
@@ -327,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return okw;
     };
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
       const Unit x = unit_of(a, u);
       const int tile = TWO ? x.item * 2 + s : x.item;
       const int cnt = TWO ? (tile < a.tiles ? x.nb : 0) : (x.nb + 1 - s) / 2;
@@ -432,45 +469,109 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += l0 + l1;
           tmem_wait_st();
         }
+        if (!TWO && s == 1 && j == 0 && units > 0) {
+          // the unit before has been read: its first product may start
+          ok = wait_w(taken, (uint32_t)((units - 1) & 1));
+          if (!ok) break;
+        }
         tc_fence_before();
         mbar_arrive_cta(&pready[s]);
       }
       if (!ok) break;
-      // ---- the unit's partial result
-      if (cnt > 0) {
-        ok = wait_w(&ofull[s], (uint32_t)(n_o++ & 1));
-        if (!ok) break;
-        tc_fence_after();
+      // ---- the unit's result: a tile's two streams are joined (the other
+      // stream's output lies in the same lanes), a pair's are two tiles
+      const int cnt1 = x.nb / 2;                 // of stream 1, one tile
+      if (cnt > 0) ok = wait_w(&ofull[s], (uint32_t)(n_own++ & 1));
+      if (!ok) break;
+      if (!TWO && s == 1) {
+        if (cnt == 0 && units > 0) {             // (no first product that waited)
+          ok = wait_w(taken, (uint32_t)((units - 1) & 1));
+          if (!ok) break;
+        }
+        xm[r] = m;
+        xl[r] = l;
+        mbar_arrive_cta(given);
+        continue;
       }
-      const int slot = TWO ? (x.kvh * a.splits + x.split) * (a.items * 2) + tile
-                             : (x.kvh * a.splits + x.split) * 2 + s;
+      float w0 = 1.f, w1 = 0.f;
+      if (!TWO) {
+        if (cnt1 > 0) ok = wait_w(&ofull[1], (uint32_t)(n_other++ & 1));
+        ok = ok && wait_w(given, (uint32_t)(units & 1));
+        if (!ok) break;
+        const float m1 = xm[r], mn = fmaxf(m, m1), base = mn == -INFINITY ? 0.f : mn;
+        w0 = tree_ex2(m - base);
+        w1 = tree_ex2(m1 - base);
+        l = l * w0 + xl[r] * w1;
+        m = mn;
+      }
+      tc_fence_after();
       if (warp_live) {
+        const bool both = !TWO && cnt1 > 0;
+        const bool last = a.splits == 1;         // the row's final result
+        const int slot = TWO ? (x.kvh * a.splits + x.split) * (a.items * 2) + tile
+                             : x.kvh * a.splits + x.split;
         float* po = a.part_o + (size_t)slot * DH * 128 + (size_t)r * 4;
-        if (cnt == 0) {
-          for (int e = 0; live && e < DH / 4; ++e)
-            *reinterpret_cast<uint4*>(po + (size_t)e * 512) = make_uint4(0u, 0u, 0u, 0u);
-        } else {
-#pragma unroll
-          for (int q = 0; q < DH / 32; ++q) {
-            uint32_t o[32];
+        float lse = INFINITY, inv = 0.f;
+        bool present = false, bad = false;
+        if (last) {
+          lse = l != 0.f ? m + log2f(l) : INFINITY;
+          inv = l != 0.f ? 1.f / l : 0.f;
+          present = live && a.depth[t] >= 0;
+          bad = any_bad(a, x.kvh, lane);
+        }
+        bf16* out = a.out + ((size_t)t * a.H + x.kvh * a.G + row % a.G) * DH;
+#pragma unroll 1
+        for (int q = 0; q < DH / 32; ++q) {
+          uint32_t o[32];
+          if (cnt > 0) {
             tmem_ld32_nw(trow + col_o + q * 32, o);
             tmem_wait_ld();
             tmem_pin32(o);
-            if (live) {
+          } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(po + (size_t)(q * 8 + e) * 512) =
-                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (both) {
+            uint32_t o1[32];
+            tmem_ld32_nw(trow + col_o + 128 + q * 32, o1);
+            tmem_wait_ld();
+            tmem_pin32(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(o1[e]) * w1);
+          }
+          if (!live) continue;
+          if (!last) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(po + (size_t)(q * 8 + e) * 512) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = present ? __uint_as_float(o[e + i]) * inv : 0.f;
+            if (bad && present) add_bad<DH>(a, x.kvh, row, t, lse, q * 32 + e, v, 8);
+            *reinterpret_cast<uint4*>(out + q * 32 + e) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
           }
         }
-        if (live) {
+        if (live && last) a.lse[(size_t)x.kvh * rows + row] = present ? lse : INFINITY;
+        if (live && !last) {
           a.part_m[(size_t)slot * 128 + r] = m;
           a.part_l[(size_t)slot * 128 + r] = l;
         }
       }
       tc_fence_before();
+      if (!TWO) mbar_arrive_cta(taken);
     }
+    // a wait gave up: one split's results are final, so they are made NaN here
+    if (!ok && a.splits == 1)
+      for (int i = blockIdx.x * 128 + (tid & 127); s == 0 && i < a.T * a.H * DH; i += gridDim.x * 128)
+        a.out[i] = __float2bfloat16(NAN);
   }
   pdl_trigger();
   tc_fence_before();
@@ -496,8 +597,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int row = min(blockIdx.x * 32 + lane, rows - 1);
   const int c0 = WAYS > 1 ? blockIdx.z : warp * kChunks;
   const int tile = row >> 7, r = row & 127, t = row / a.G;
-  const int per = a.two ? a.items * 2 : 2;       // slots per (head, split)
-  const int step = a.two ? per : 1, count = a.two ? a.splits : 2 * a.splits;
+  const int per = a.two ? a.items * 2 : 1;       // slots per (head, split)
+  const int step = per, count = a.splits;
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
   pdl_wait();
   pdl_trigger();
@@ -541,34 +642,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
   const float lse = l != 0.f ? m + log2f(l) : INFINITY;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
+  const bool marked = any_bad(a, kvh, lane);
 #pragma unroll
   for (int q = 0; q < kChunks; ++q) {
     float v[4] = {o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv};
-    if (present) {
-      // inf and NaN of the V rows that this row sees (left out of the products)
-      for (int j0 = 0; j0 <= t; j0 += 4) {
-        if (j0 + 3 < a.T && *reinterpret_cast<const uint32_t*>(flags + j0) == 0u) continue;
-        for (int j = j0; j <= t && j < j0 + 4; ++j) {
-          if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
-          const size_t plane = (size_t)a.Hkv * rows * DH;
-          const bf16* qr = a.q + ((size_t)kvh * rows + row) * DH;
-          const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
-          float acc = 0.f;
-          for (int i = 0; i < DH; ++i)
-            acc = fmaf(__bfloat162float(qr[i]) + __bfloat162float(qr[plane + i]),
-                       __bfloat162float(k[i]), acc);
-          const float p = exp2f(acc * a.scale_log2 - lse);
-          for (int e = 0; e < 4; ++e) {
-            const float x = __bfloat162float(
-                a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + (c0 + q) * 4 + e]);
-            if (!isfinite(x)) v[e] += p * x;
-          }
-        }
-      }
-    } else {
+    if (!present)
       v[0] = v[1] = v[2] = v[3] = 0.f;
-    }
+    else if (marked)
+      add_bad<DH>(a, kvh, row, t, lse, (c0 + q) * 4, v, 4);
     if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
     const uint2 packed = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     if (WAYS > 1) {
@@ -593,15 +674,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 template <int DH, bool TWO>
-cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
+cudaError_t launch(const TreeArgs& a, const TreeMaps& m, cudaStream_t st) {
   const int rows = a.T * a.G;
-  CUtensorMap mQ, mK, mV, mTK, mTV;
-  const int n = a.n ? a.n : 1;                   // no context: never read
-  if (!tree_map(&mQ, a.q, DH, rows, 2 * a.Hkv, rows) || !tree_map(&mK, a.kc, DH, n, a.Hkv, a.max_seq) ||
-      !tree_map(&mV, a.vc, DH, n, a.Hkv, a.max_seq) || !tree_map(&mTK, a.kt, DH, a.T, a.Hkv, a.T) ||
-      !tree_map(&mTV, a.vt, DH, a.T, a.Hkv, a.T))
-    return cudaErrorInvalidValue;
-  const size_t smem = (size_t)kTileSmem + 1024 + 512;
+  const size_t smem = (size_t)kTileSmem + 1024 + 1024 + 512;
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
@@ -620,9 +695,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t st) {
   lc.stream = st;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH, TWO>, mQ, mK, mV, mTK, mTV, a);
-  if (e != cudaSuccess) return e;
-  const bool many = (a.two ? a.splits : 2 * a.splits) >= 16;
+  cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH, TWO>, m.k, m.v, m.ws, a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const bool many = a.splits >= 16;
   lc.gridDim = dim3((rows + 31) / 32, a.Hkv, many ? DH / 4 : 1);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
@@ -645,22 +720,10 @@ int tree_sms() {
   return sms;
 }
 
-bool tree_map(CUtensorMap* m, const void* base, int dh, int d1, int d2, int stride) {
-  EncodeTiled enc = tma_encoder();
-  const cuuint64_t row = dh * sizeof(bf16);
-  const cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)d1, (cuuint64_t)d2};
-  const cuuint64_t strides[2] = {row, row * (cuuint64_t)stride};
-  const cuuint32_t box[3] = {64, 128, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Splits the key blocks so that the units of all heads and row tiles fill the
 // SMs in as few block steps as possible: a wave of units takes as long as its
-// longest run of blocks plus about three for the start and the hand-over.
+// longest run of blocks plus about three for the start and the hand-over, and
+// more than one split costs the second kernel, about three more.
 void tree_split(TreeArgs& a) {
   const int rows = a.T * a.G, sms = tree_sms();
   a.tiles = (rows + 127) / 128;
@@ -670,14 +733,15 @@ void tree_split(TreeArgs& a) {
   a.nb = a.nb_ctx + (a.T + kTreeKeys - 1) / kTreeKeys;
   const long long lanes = (long long)a.Hkv * a.items;
   long long best = -1;
-  // of the splits that take the same number of waves the most is the best
-  for (long long waves = 1; waves <= 8; ++waves) {
-    long long n = waves * sms / lanes;
-    if (n < 1 && (waves < 8 || best >= 0)) continue;
-    n = n < 1 ? 1 : n > a.nb ? a.nb : n > 160 ? 160 : n;
+  // of the splits that take the same number of waves the most is the best;
+  // and one split, whatever it takes
+  for (long long waves = 0; waves <= 8; ++waves) {
+    long long n = waves ? waves * sms / lanes : 1;
+    if (n < 1) continue;
+    n = n > a.nb ? a.nb : n > 160 ? 160 : n;
     // a stream takes every other block of a single tile's run
     const long long len = (a.nb + n - 1) / n, steps = a.two ? len : (len + 1) / 2;
-    const long long cost = ((lanes * n + sms - 1) / sms) * (steps + 3);
+    const long long cost = ((lanes * n + sms - 1) / sms) * (steps + 3) + (n > 1 ? 3 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       a.splits = (int)n;
@@ -687,11 +751,11 @@ void tree_split(TreeArgs& a) {
   a.ctas = a.units < sms ? a.units : sms;
 }
 
-int tree_slots(const TreeArgs& a) { return a.Hkv * a.splits * (a.two ? a.items * 2 : 2); }
+int tree_slots(const TreeArgs& a) { return a.Hkv * a.splits * (a.two ? a.items * 2 : 1); }
 
-cudaError_t launch_tree_attn_tc(const TreeArgs& a, cudaStream_t s) {
-  if (a.dh == 128) return a.two ? launch<128, true>(a, s) : launch<128, false>(a, s);
-  return a.two ? launch<64, true>(a, s) : launch<64, false>(a, s);
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, const TreeMaps& m, cudaStream_t s) {
+  if (a.dh == 128) return a.two ? launch<128, true>(a, m, s) : launch<128, false>(a, m, s);
+  return a.two ? launch<64, true>(a, m, s) : launch<64, false>(a, m, s);
 }
 
 }  // namespace ssd

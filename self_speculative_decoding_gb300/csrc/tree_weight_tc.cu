@@ -54,9 +54,8 @@ SSD_DI Range my_units(const TreeArgs& a) {
 
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_weight_tc_kernel(const __grid_constant__ CUtensorMap mQ,
-                          const __grid_constant__ CUtensorMap mK,
-                          const __grid_constant__ CUtensorMap mTK,
+    tree_weight_tc_kernel(const __grid_constant__ CUtensorMap mK,
+                          const __grid_constant__ CUtensorMap mW,
                           const __grid_constant__ TreeArgs a) {
   constexpr int kRegs = DH / 64;
   constexpr int kItem = kRegs * kRegion;
@@ -116,8 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (use > 0 && !mbar_wait_n(&qempty[sl], (uint32_t)((use - 1) & 1), kPolls)) return false;
           mbar_arrive_expect_tx(&qfull[sl], (uint32_t)kItem);
           for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(sm + sl * kItem + r * kRegion, &mQ, r * 64, tile * 128, p * a.Hkv + kvh,
-                        &qfull[sl]);
+            tma_load_3d(sm + sl * kItem + r * kRegion, &mW, r * 64,
+                        (p * a.Hkv + kvh) * rows + tile * 128, 0, &qfull[sl]);
           ++qissued;
         }
         return true;
@@ -138,9 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const bool ctx = b < a.nb_ctx;
           mbar_arrive_expect_tx(&full[st], (uint32_t)kItem);
+          const int row = ctx ? b * kTreeKeys : a.row_kt + kvh * a.T + (b - a.nb_ctx) * kTreeKeys;
           for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(ring + (size_t)st * kItem + r * kRegion, ctx ? &mK : &mTK, r * 64,
-                        (ctx ? b : b - a.nb_ctx) * kTreeKeys, kvh, &full[st]);
+            tma_load_3d(ring + (size_t)st * kItem + r * kRegion, ctx ? &mK : &mW, r * 64, row,
+                        ctx ? kvh : 0, &full[st]);
           ++issued;
         }
         if (!resident)
@@ -336,13 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DH>
-cudaError_t launch(const TreeArgs& a, int sms, cudaStream_t st) {
-  CUtensorMap mQ, mK, mTK;
-  const int rows = a.T * a.G;
-  if (!tree_map(&mQ, a.q, DH, rows, 2 * a.Hkv, rows) ||
-      !tree_map(&mK, a.kc, DH, a.n ? a.n : 1, a.Hkv, a.max_seq) ||
-      !tree_map(&mTK, a.kt, DH, a.T, a.Hkv, a.T))
-    return cudaErrorInvalidValue;
+cudaError_t launch(const TreeArgs& a, const TreeMaps& m, cudaStream_t st) {
+  const int sms = tree_sms();
   const size_t smem = (size_t)kTileSmem + 1024 + 1024 + 512;
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
@@ -363,13 +358,13 @@ cudaError_t launch(const TreeArgs& a, int sms, cudaStream_t st) {
   lc.stream = st;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, tree_weight_tc_kernel<DH>, mQ, mK, mTK, a);
+  return cudaLaunchKernelEx(&lc, tree_weight_tc_kernel<DH>, m.k, m.ws, a);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_weight_tc(const TreeArgs& a, int sms, cudaStream_t s) {
-  return a.dh == 128 ? launch<128>(a, sms, s) : launch<64>(a, sms, s);
+cudaError_t launch_tree_weight_tc(const TreeArgs& a, const TreeMaps& m, cudaStream_t s) {
+  return a.dh == 128 ? launch<128>(a, m, s) : launch<64>(a, m, s);
 }
 
 }  // namespace ssd
