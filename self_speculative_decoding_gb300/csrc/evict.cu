@@ -17,10 +17,11 @@ namespace cg = cooperative_groups;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCopies = 8;          // of the first histogram: lane l counts in copy l % 8
-constexpr int kSelKeys = 33792;     // weights of a CTA that fit its shared memory
+constexpr int kItems = 16;          // weights per thread that stay in registers
+constexpr int kChunk = kSelThreads * kItems;
 constexpr int kRankKeys = 512;      // at most so many middle rows are ranked by counting
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
+constexpr int kWords = 1024;        // of a histogram of 2048 bins
 constexpr int kFusedRows = 512;     // rows and 16-byte units that a selecting CTA copies itself
 constexpr int kFusedUnits = 4096;
 
@@ -101,11 +102,14 @@ __global__ void __launch_bounds__(kCopyThreads) evict_gather_kernel(const EvictA
   copy_rows<kCopyThreads>(a, blockIdx.y, j0, min(rows, a.keep - j0), src_row);
 }
 
-// Cluster = one K/V head, its middle rows divided among the CTAs.  Each keeps
-// its weights' keys in shared memory (re-reading them from L2 where a head
-// has more than a cluster holds); 11 + 11 + 10 bits of the cut are found from
-// histograms summed over the cluster.  Weights share few exponents, so the
-// first histogram has eight copies: lanes of a warp rarely meet in one.
+// Cluster = one K/V head, its middle rows divided among the CTAs, each
+// thread's weights in registers (a CTA with more than 16384 re-reads them from
+// L2).  11 + 11 + 10 bits of the cut are found from histograms summed over the
+// cluster; a pass whose bin stays as a whole is the last.  Counts are 16 bits,
+// two to a word, which halves what the CTAs read of each other (a word each,
+// `wide`, where a CTA has more rows than 16 bits count).  Weights share few
+// exponents, so the first histogram has eight copies: lanes of a warp rarely
+// meet in one.
 // With `fused` (one CTA per head, few rows) the CTA copies the rows too.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int fused) {
   extern __shared__ __align__(16) uint32_t smem[];
@@ -114,9 +118,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   __shared__ uint32_t s_bin;
   __shared__ int s_need;
   __shared__ int s_count[2];
+  __shared__ int s_all;
+  __shared__ uint32_t runs[kItems * kSelWarps];
   pdl_trigger();
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  if (tid < 2) s_count[tid] = 0;
   const float* w = a.weight + (size_t)blockIdx.y * a.max_seq;
   int32_t* kept = a.kept + (size_t)blockIdx.y * a.keep;
   const int lo = a.sinks, hi = a.n - a.recent, want = a.keep - a.sinks - a.recent;
@@ -141,38 +149,53 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int at = block_scan(before < want, wsum, total);
     if (before < want) kept[a.sinks + at] = c0 + tid;
   } else if (want > 0) {
-    int* hist = reinterpret_cast<int*>(smem);    // [bin][copy]
-    int* sums = hist + kCopies * kBins;          // [pass][bin]
-    uint32_t* keys = smem + (kCopies + 3) * kBins;
-    const bool held = share <= kSelKeys;
-    auto key = [&](int i) { return held ? keys[i] : weight_key(w[c0 + i]); };
-    for (int i = tid; i < (kCopies + 3) * kBins / 4; i += kSelThreads)
+    const bool wide = share > 65535;
+    const int words = wide ? 2 * kWords : kWords;
+    uint32_t* hist = smem;                       // [word][copy]
+    uint32_t* sums = hist + kCopies * words;     // [pass][word]
+    for (int i = tid; i < (kCopies + 3) * words / 4; i += kSelThreads)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (held)
-      for (int i = tid; i < len; i += kSelThreads) keys[i] = weight_key(w[c0 + i]);
+    // keys of a chunk, row base + 1024 q + thread; 0 beyond the share
+    uint32_t k[kItems];
+    auto load = [&](int base) {
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        const int i = base + q * kSelThreads + tid;
+        k[q] = i < len ? weight_key(w[c0 + i]) : 0u;
+      }
+    };
+    load(0);
     __syncthreads();
     // ---- the want-th largest key, and how many rows at it stay
     uint32_t cut = 0;
     int need = want;
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
+    bool exact = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && !exact; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
       const int above = shift + (pass == 2 ? 10 : 11);
-      int* sum = sums + pass * kBins;
-      if (pass == 0) {
-        for (int i = tid; i < len; i += kSelThreads)
-          atomicAdd(&hist[(key(i) >> 21) * kCopies + (tid & (kCopies - 1))], 1);
-        __syncthreads();
-        for (int i = tid; i < kBins; i += kSelThreads) {
-          const int4 x = reinterpret_cast<const int4*>(hist)[2 * i];
-          const int4 y = reinterpret_cast<const int4*>(hist)[2 * i + 1];
-          sum[i] = (x.x + x.y + x.z + x.w) + (y.x + y.y + y.z + y.w);
+      uint32_t* sum = sums + pass * words;
+      for (int base = 0; base < len; base += kChunk) {
+        if (len > kChunk) load(base);
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) {
+          if (base + q * kSelThreads >= len) break;
+          const uint32_t bin = (k[q] >> shift) & mask;
+          const uint32_t at = wide ? bin : bin >> 1, one = wide ? 1u : 1u << (16 * (bin & 1));
+          if (pass == 0) {
+            if (k[q]) atomicAdd(&hist[at * kCopies + (tid & (kCopies - 1))], one);
+          } else if ((k[q] >> above) == (cut >> above)) {
+            atomicAdd(&sum[at], one);
+          }
         }
-      } else {
-        for (int i = tid; i < len; i += kSelThreads) {
-          const uint32_t u = key(i);
-          if ((u >> above) == (cut >> above)) atomicAdd(&sum[(u >> shift) & mask], 1);
+      }
+      if (pass == 0) {
+        __syncthreads();
+        for (int i = tid; i < words; i += kSelThreads) {
+          const uint4 x = reinterpret_cast<const uint4*>(hist)[2 * i];
+          const uint4 y = reinterpret_cast<const uint4*>(hist)[2 * i + 1];
+          sum[i] = (x.x + x.y + x.z + x.w) + (y.x + y.y + y.z + y.w);
         }
       }
       if (nc > 1)
@@ -181,42 +204,64 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         __syncthreads();
       // thread t takes the bins 2047 - 2 t and 2046 - 2 t, so that lower
       // threads hold larger keys
-      const int b1 = kBins - 1 - 2 * tid;
-      int2 h = make_int2(0, 0);
+      const int pair = kWords - 1 - tid;
+      int hi_n = 0, lo_n = 0;
+      uint2 o[kMaxCluster];
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c)
-        if (c < nc) {
-          const int2 o = *reinterpret_cast<const int2*>(cluster.map_shared_rank(sum, c) + b1 - 1);
-          h.x += o.y;
-          h.y += o.x;
-        }
+      for (int c = 0; c < kMaxCluster; ++c) {
+        o[c] = make_uint2(0u, 0u);
+        if (c >= nc) continue;
+        const uint32_t* from = nc > 1 ? cluster.map_shared_rank(sum, c) : sum;
+        if (wide)
+          o[c] = reinterpret_cast<const uint2*>(from)[pair];
+        else
+          o[c].x = from[pair];
+      }
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        hi_n += wide ? o[c].y : o[c].x >> 16;
+        lo_n += wide ? o[c].x : o[c].x & 0xffffu;
+      }
       int total;
-      const int before = block_scan(h.x + h.y, wsum, total);
-      if (before < need && before + h.x + h.y >= need) {
-        const bool first = before + h.x >= need;
-        s_bin = (uint32_t)(first ? b1 : b1 - 1);
-        s_need = need - before - (first ? 0 : h.x);
+      const int before = block_scan(hi_n + lo_n, wsum, total);
+      if (before < need && before + hi_n + lo_n >= need) {
+        const bool first = before + hi_n >= need;
+        s_bin = (uint32_t)(2 * pair + first);
+        s_need = need - before - (first ? 0 : hi_n);
+        s_all = s_need == (first ? hi_n : lo_n);
       }
       __syncthreads();
       cut |= s_bin << shift;
       need = s_need;
-      __syncthreads();
+      exact = s_all;
     }
-    // ---- places: rows over the cut, and the lowest `need` rows at it
-    const int per = ((len + kSelThreads - 1) / kSelThreads) | 1;  // odd: no bank conflicts
-    const int i0 = min(tid * per, len), i1 = min(i0 + per, len);
-    int gt = 0, eq = 0;
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t u = key(i);
-      gt += u > cut;
-      eq += u == cut;
+    if (exact) {                                 // the last bin stays as a whole
+      cut -= 1;                                  // (bin 0 of every pass is no key)
+      need = 0;
     }
-    int tg, te;
-    int g = block_scan(gt, wsum, tg), e = block_scan(eq, wsum, te);
+    // ---- places: rows over the cut, and the lowest `need` rows at it, counted
+    // per warp and 1024 rows (over: low half, at: high half)
+    const uint32_t below = (1u << lane) - 1u;
+    int g = 0, e = 0;                            // before this chunk
     if (nc > 1) {
-      if (tid == 0) {
-        s_count[0] = tg;
-        s_count[1] = te;
+      // what the lower CTAs of the cluster have
+      int gt = 0, eq = 0;
+      for (int base = 0; base < len; base += kChunk) {
+        if (len > kChunk) load(base);
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) {
+          gt += k[q] > cut;
+          eq += k[q] == cut && k[q];
+        }
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        gt += __shfl_xor_sync(~0u, gt, d);
+        eq += __shfl_xor_sync(~0u, eq, d);
+      }
+      if (lane == 0) {
+        atomicAdd(&s_count[0], gt);
+        atomicAdd(&s_count[1], eq);
       }
       cluster.sync();
       for (int c = 0; c < rank; ++c) {
@@ -225,11 +270,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         e += other[1];
       }
     }
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t u = key(i);
-      if (u > cut || (u == cut && e < need)) kept[a.sinks + g + min(e, need)] = c0 + i;
-      g += u > cut;
-      e += u == cut;
+    for (int base = 0; base < len; base += kChunk) {
+      if (len > kChunk) load(base);
+      uint32_t mg[kItems], me[kItems];
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        mg[q] = __ballot_sync(~0u, k[q] > cut);
+        me[q] = __ballot_sync(~0u, k[q] == cut && k[q]);
+        if (lane == 0) runs[q * kSelWarps + warp] = __popc(mg[q]) | (__popc(me[q]) << 16);
+      }
+      __syncthreads();
+      // exclusive sums over the 512 runs (each half below 2^15)
+      const uint32_t mine = tid < kItems * kSelWarps ? runs[tid] : 0u;
+      int total;
+      const int at = block_scan((int)mine, wsum, total);
+      if (tid < kItems * kSelWarps) runs[tid] = (uint32_t)at;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        const uint32_t o = runs[q * kSelWarps + warp];
+        const int gq = g + (int)(o & 0xffffu) + __popc(mg[q] & below);
+        const int eq = e + (int)(o >> 16) + __popc(me[q] & below);
+        if (k[q] > cut || (k[q] == cut && k[q] && eq < need))
+          kept[a.sinks + gq + min(eq, need)] = c0 + base + q * kSelThreads + tid;
+      }
+      g += total & 0xffff;
+      e += (int)((uint32_t)total >> 16);
+      if (len > kChunk) __syncthreads();         // runs are read
     }
     if (nc > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
   }
@@ -253,14 +320,13 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const bool fused = few && nc == 1;
   const int share = (middle + nc - 1) / nc;
   const bool ranked = want == 0 || (nc == 1 && share <= kRankKeys);
-  const size_t smem = ranked ? kRankKeys * 4
-                             : ((size_t)(kCopies + 3) * kBins + (share <= kSelKeys ? share : 0)) * 4;
+  const size_t hist = (size_t)(kCopies + 3) * kWords * 4;
+  const size_t smem = ranked ? kRankKeys * 4 : share > 65535 ? 2 * hist : hist;
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ((kCopies + 3) * kBins + kSelKeys) * 4);
+    const cudaError_t e = cudaFuncSetAttribute(
+        evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * hist));
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
