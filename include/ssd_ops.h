@@ -148,7 +148,8 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * and the reordering of the beams' caches.  These calls allocate nothing:
  * where a call needs scratch memory, the caller gives a workspace of device
  * memory (256-byte aligned, at least what the call's _workspace function
- * returns for the current device; fewer bytes are SSD_ERR_CAPACITY).  Its
+ * returns for the current device; fewer bytes are SSD_ERR_CAPACITY; 0 for
+ * sizes that need none, or that the call refuses).  Its
  * contents need no initialisation and mean nothing afterwards; calls that may
  * overlap on the GPU need one each.  Each call can be captured into a CUDA
  * graph.  Inputs that these calls read from device memory (parents, done)

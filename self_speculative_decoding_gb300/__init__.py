@@ -530,17 +530,18 @@ class _Ops:
                 self._arg(scores, "scores", torch.float32, (B,), dev),
                 None if done is None else self._arg(done, "done", torch.int32, (B,), dev), end_id,
                 width)
-        lib = _lib()
+        lib, at = _lib(), logits.device
         need = lib.ssd_op_beam_select_workspace(B, V, width)
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=logits.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=at) if need else None
         # (rows of one tensor would cost more than four small tensors)
-        n, at = max(width, 0), logits.device
+        n = max(width, 0)
         tokens = torch.empty(n, dtype=torch.int32, device=at)
         parents = torch.empty(n, dtype=torch.int32, device=at)
         best = torch.empty(n, dtype=torch.float32, device=at)
         ended = torch.empty(n, dtype=torch.int32, device=at)
         self._check(lib.ssd_op_beam_select(*args, tokens.data_ptr(), parents.data_ptr(),
-                                           best.data_ptr(), ended.data_ptr(), ws.data_ptr(), need,
+                                           best.data_ptr(), ended.data_ptr(),
+                                           None if ws is None else ws.data_ptr(), need,
                                            _raw_stream(dev)))
         return tokens, parents, best, ended
 

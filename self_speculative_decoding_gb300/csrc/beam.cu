@@ -93,14 +93,13 @@ __device__ __noinline__ int piece_bisect(const float* row, int v0, int n, int W,
 // logits stay in registers; what lies at or over the W-th largest
 // of G group maxima is listed and ranked.
 template <int G>
-SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int pieces, int b) {
+SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out) {
   __shared__ uint64_t list[kList];
   __shared__ __align__(16) float gm[G];
   __shared__ float s_cut;
   __shared__ int s_n;
   const int tid = threadIdx.x;
   if (a.done && a.done[b]) return;               // the merge does not read its lists
-  uint64_t* out = a.lists + ((size_t)b * pieces + piece) * a.W;
   const int v0 = piece * len, n = min(len, a.V - v0);
   const float* row = a.logits + (size_t)b * a.V + v0;
   float z[kPieceItems];
@@ -139,7 +138,8 @@ SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int pieces, int b)
 template <int G>
 __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
   pdl_trigger();
-  piece_body<G>(a, len, blockIdx.x, gridDim.x, blockIdx.y);
+  piece_body<G>(a, len, blockIdx.x, blockIdx.y,
+                a.lists + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * a.W);
 }
 
 // A candidate in the whole order: the 64-bit score as an ordered integer
@@ -310,28 +310,63 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   merge_body<kMergeThreads>(a, pieces);
 }
 
-// Few pieces: one cluster holds them all, and its first CTA merges (one launch
-// instead of two).
+// Few pieces: one cluster holds them all, and its first CTA merges the lists
+// out of the others' shared memory (one launch instead of two, no workspace).
 template <int G>
 __global__ void __launch_bounds__(kPieceThreads, 1) beam_cluster_kernel(const BeamArgs a, int len) {
-  piece_body<G>(a, len, blockIdx.x, gridDim.x, blockIdx.y);
-  cooperative_groups::this_cluster().sync();
-  if (blockIdx.x == 0 && blockIdx.y == 0) merge_body<kPieceThreads>(a, gridDim.x);
+  constexpr int kMost = G == 128 ? 64 : 256;     // W at most
+  __shared__ uint64_t mine[kMost];
+  __shared__ uint64_t all[kMaxCluster * kMost];
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  piece_body<G>(a, len, blockIdx.x, blockIdx.y, mine);
+  cluster.sync();
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < (int)cluster.num_blocks() * a.W; i += kPieceThreads)
+      all[i] = cluster.map_shared_rank(mine, i / a.W)[i % a.W];
+  cluster.sync();                                // no list is gone while it is read
+  if (blockIdx.x || blockIdx.y) return;
+  BeamArgs b = a;
+  b.lists = all;
+  merge_body<kPieceThreads>(b, gridDim.x);
 }
 
-// Units of 16 bytes of the rows start .. stop-1 of every group of every state.
-__global__ void __launch_bounds__(256) beam_reorder_kernel(const ReorderArgs a) {
+// Reordering by source: a tile of 1024 16-byte units of one group's rows is
+// read once and written to every state that takes it (read once per taker, 8
+// beams of 32 layers at 1025 rows took 319 us; the copies of a source lie too
+// far apart for L2).
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnits = 4;       // per thread, of K and of V
+__global__ void __launch_bounds__(kCopyThreads) beam_reorder_kernel(const ReorderArgs a) {
   const size_t span = (size_t)(a.stop - a.start) * a.units;  // units per group
-  const size_t n = (size_t)a.W * a.groups * span;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (size_t)gridDim.x * blockDim.x) {
-    const size_t grp = i / span, u = i - grp * span;
-    const int w = (int)(grp / a.groups), p = a.parents[w];
-    if (p < 0 || p >= a.B) continue;
-    const size_t at = (size_t)a.start * a.units + u, len = (size_t)a.max_seq * a.units;
-    const size_t src = ((size_t)p * a.groups + grp % a.groups) * len + at, dst = grp * len + at;
-    a.k_out[dst] = a.k[src];
-    if (a.v) a.v_out[dst] = a.v[src];
+  const size_t per = (span + kCopyThreads * kCopyUnits - 1) / (kCopyThreads * kCopyUnits);
+  const size_t tiles = (size_t)a.B * a.groups * per, len = (size_t)a.max_seq * a.units;
+  for (size_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const size_t grp = i / per;                  // (source state, group)
+    const int p = (int)(grp / a.groups);
+    const size_t u0 = (i - grp * per) * (kCopyThreads * kCopyUnits) + threadIdx.x;
+    const size_t src = grp * len + (size_t)a.start * a.units + u0;
+    uint4 x[kCopyUnits], y[kCopyUnits];
+    bool read = false;
+    for (int w = 0; w < a.W; ++w) {
+      if (__ldg(a.parents + w) != p) continue;
+      if (!read) {
+        read = true;
+#pragma unroll
+        for (int q = 0; q < kCopyUnits; ++q) {
+          if (u0 + q * kCopyThreads >= span) continue;
+          x[q] = __ldcs(a.k + src + q * kCopyThreads);
+          if (a.v) y[q] = __ldcs(a.v + src + q * kCopyThreads);
+        }
+      }
+      const size_t dst = src + ((size_t)w - (size_t)p) * a.groups * len;
+#pragma unroll
+      for (int q = 0; q < kCopyUnits; ++q) {
+        if (u0 + q * kCopyThreads >= span) continue;
+        __stcs(a.k_out + dst + q * kCopyThreads, x[q]);
+        if (a.v) __stcs(a.v_out + dst + q * kCopyThreads, y[q]);
+      }
+    }
   }
 }
 
@@ -348,7 +383,8 @@ static int beam_pieces(int B, int V, int& len) {
 
 size_t beam_select_workspace(int B, int V, int W) {
   int len;
-  return (size_t)B * beam_pieces(B, V, len) * W * sizeof(uint64_t);
+  const size_t lists = (size_t)B * beam_pieces(B, V, len);
+  return lists <= kMaxCluster ? 0 : lists * W * sizeof(uint64_t);
 }
 
 cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s) {
@@ -381,7 +417,10 @@ cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_beam_reorder(const ReorderArgs& a, cudaStream_t s) {
-  beam_reorder_kernel<<<1216, 256, 0, s>>>(a);
+  const size_t span = (size_t)(a.stop - a.start) * a.units;
+  const size_t tiles = (size_t)a.B * a.groups * ((span + kCopyThreads * kCopyUnits - 1) /
+                                                 (kCopyThreads * kCopyUnits));
+  beam_reorder_kernel<<<(unsigned)(tiles < (1u << 20) ? tiles : 1u << 20), kCopyThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

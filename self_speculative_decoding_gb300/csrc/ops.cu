@@ -530,9 +530,11 @@ ssd_status ssd_op_beam_select(const float* logits, int32_t B, int32_t V, const f
     return op_fail(SSD_ERR_INVALID_ARG, "beam_select sizes");
   if (!al4(logits) || !al4(scores) || (lse && !al4(lse)) || (done && !al4(done)) ||
       !al4(tokens) || !al4(parents) || !al4(scores_out) || (done_out && !al4(done_out)) ||
-      !workspace || ((uintptr_t)workspace & 255u))
+      ((uintptr_t)workspace & 255u))
     return op_fail(SSD_ERR_INVALID_ARG, "beam_select pointers");
-  if (workspace_bytes < beam_select_workspace(B, V, W))
+  const size_t need = beam_select_workspace(B, V, W);
+  if (need && !workspace) return op_fail(SSD_ERR_INVALID_ARG, "beam_select pointers");
+  if (workspace_bytes < need)
     return op_fail(SSD_ERR_CAPACITY, "beam_select: workspace too small");
   BeamArgs a;
   a.logits = logits;

@@ -38,7 +38,8 @@ def test_small_workspaces(lib):
     assert lib.ssd_op_tree_attention(*{**TREE, "ws_bytes": need - 1}.values()) == CAPACITY
     assert lib.ssd_op_tree_attention_workspace(0, 10, 4, 2, 64) == 0
     assert lib.ssd_op_tree_attention_workspace(4, 10, 4, 3, 64) == 0
-    need = lib.ssd_op_beam_select_workspace(4, 1000, 4)
+    assert lib.ssd_op_beam_select_workspace(4, 1000, 4) == 0      # needs none
+    need = lib.ssd_op_beam_select_workspace(40, 100000, 4)
     assert need > 0
     assert lib.ssd_op_beam_select(*{**SELECT, "ws_bytes": need - 1}.values()) == CAPACITY
     assert lib.ssd_op_beam_select_workspace(4, 0, 4) == 0
@@ -60,13 +61,13 @@ def test_cache_evict(lib, change):
     assert b"cache_evict" in lib.ssd_ops_last_error()
 
 
-SELECT = dict(logits=P, B=4, V=1000, lse=P, stride=1, scores=P, done=P, end_id=2, W=4, tokens=P,
+SELECT = dict(logits=P, B=40, V=100000, lse=P, stride=1, scores=P, done=P, end_id=2, W=4, tokens=P,
               parents=P, scores_out=P, done_out=P, ws=P, ws_bytes=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("change", [
     dict(B=0), dict(B=257), dict(V=0), dict(W=0), dict(W=257), dict(stride=0), dict(end_id=-2),
-    dict(end_id=1000), dict(end_id=-1), dict(logits=None), dict(logits=P + 2), dict(scores=None),
+    dict(end_id=100000), dict(end_id=-1), dict(logits=None), dict(logits=P + 2), dict(scores=None),
     dict(lse=P + 1), dict(done=P + 1), dict(tokens=None), dict(parents=None),
     dict(scores_out=None), dict(done_out=P + 1), dict(ws=None), dict(ws=P + 8)])
 def test_beam_select(lib, change):
