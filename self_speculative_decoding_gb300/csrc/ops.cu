@@ -461,6 +461,7 @@ ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32
     return op_fail(SSD_ERR_INVALID_ARG, "tree_attention: weight_in needs weight_out");
   TreeArgs a;
   tree_sizes(a, T, n_ctx, H, Hkv, dh);
+  a.w_out = weight_out;
   if (tree_workspace(a, workspace) > workspace_bytes)
     return op_fail(SSD_ERR_CAPACITY, "tree_attention: workspace too small");
   a.qkv = qkv;
@@ -470,7 +471,6 @@ ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32
   a.kc = (bf16*)k_cache;
   a.vc = (bf16*)v_cache;
   a.w_in = weight_in;
-  a.w_out = weight_out;
   a.out = (bf16*)out;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)dh));
   tree_frequencies(theta, dh, a.inv_freq);

@@ -147,6 +147,10 @@ size_t tree_workspace(TreeArgs& a, void* base) {
   a.part_o = (float*)take(slots * a.dh * 128 * 4);
   a.part_m = (float*)take(slots * 128 * 4);
   a.part_l = (float*)take(slots * 128 * 4);
+  if (rows <= (size_t)kTreeScoreRows) {
+    a.part_s = (float*)take((size_t)a.Hkv * a.nb * rows * kTreeKeys * 4);
+    if (!a.w_out) a.part_s = nullptr;
+  }
   a.err = (int*)take(4);
   return off;
 }
@@ -163,7 +167,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
       !tree_map(&m.v, a.vc, a.dh, n, a.Hkv, a.max_seq * cache_row) ||
       !tree_map(&m.ws, a.q, a.dh, a.row_vt + a.Hkv * a.T, 1, cache_row))
     return cudaErrorInvalidValue;
-  if ((e = launch_tree_attn_tc(a, m, s)) != cudaSuccess || !a.w_out) return e;
+  if ((e = launch_tree_attn_tc(a, m, s)) != cudaSuccess || !a.w_out || a.part_s) return e;
   return launch_tree_weight_tc(a, m, s);
 }
 

@@ -14,6 +14,10 @@ namespace ssd {
 constexpr int kTreeMaxNodes = 1024;  // nodes (rows) of one tree
 constexpr int kTreeKeys = 128;       // keys per block
 constexpr int kTreeMaxHalf = 64;     // dh / 2 at most
+// Up to so many rows per K/V head, the weights are summed from scores that the
+// attention stores (4 bytes per row and key, against a second read of K and a
+// second pass of products): see tree_attn_tc.cu.
+constexpr int kTreeScoreRows = 32;
 
 struct TreeArgs {
   const float* qkv = nullptr;        // [T][(H + 2 Hkv) dh] raw projections
@@ -36,6 +40,7 @@ struct TreeArgs {
   float* part_o = nullptr;           // [slots][dh / 4][128 rows][4] unnormalised outputs
   float* part_m = nullptr;           // [slots][128] base-2 maximum of the row's scores
   float* part_l = nullptr;           // [slots][128] sum of 2^(score - maximum)
+  float* part_s = nullptr;           // [Hkv][nb][rows][128] masked scores (few rows with weights)
   int* err = nullptr;                // non-zero: a bounded wait gave up
   int anc_words = 0;
   int row_kt = 0, row_vt = 0;        // first row of kt and vt in the workspace's matrix

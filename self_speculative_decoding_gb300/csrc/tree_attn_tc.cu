@@ -427,6 +427,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[q][e]),
                                         __uint_as_float(sr[q][e + 1]));
           }
+          if (!TWO && a.part_s && live) {
+            float4* ps = reinterpret_cast<float4*>(
+                a.part_s + (((size_t)x.kvh * a.nb + b) * rows + row) * kTreeKeys);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              ps[e] = make_float4(__uint_as_float(sr[e >> 3][(4 * e) & 31]),
+                                  __uint_as_float(sr[e >> 3][(4 * e + 1) & 31]),
+                                  __uint_as_float(sr[e >> 3][(4 * e + 2) & 31]),
+                                  __uint_as_float(sr[e >> 3][(4 * e + 3) & 31]));
+          }
           const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
           const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
@@ -580,28 +590,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the units' partial results: CTA = 32 rows of one K/V head, lane = row;
-// the slots are added in order.  With WAYS = 1 each warp has an eighth of the
-// columns; with WAYS = 8 (many slots, few rows) a CTA has one 16-byte column
-// and each warp every eighth slot.  Rows leave through shared memory, so that
-// stores are whole rows.
+// After the units: CTAs 0 .. joins - 1 join their partial results, the rest
+// sum the weights from stored scores (where there are any).  Both read the
+// units' statistics, so that neither waits for the other.
+//
+// Joining: CTA = 32 rows of one K/V head, lane = row; the slots are added in
+// order.  With WAYS = 1 each warp has an eighth of the columns; with WAYS = 8
+// (many slots, few rows) a CTA has one 16-byte column and each warp every
+// eighth slot.  Rows leave through shared memory, so that stores are whole
+// rows.
 constexpr int kJoinWarps = 8;
 template <int DH, int WAYS>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    tree_join_kernel(const __grid_constant__ TreeArgs a) {
+SSD_DI void join_rows(const TreeArgs& a, int index) {
   constexpr int kChunks = WAYS > 1 ? 1 : DH / 4 / kJoinWarps;  // 16-byte columns per warp
+  constexpr int kParts = WAYS > 1 ? DH / 4 : 1;  // CTAs per 32 rows
   __shared__ float4 s_o[kJoinWarps * kChunks][33];
   __shared__ float s_l[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = WAYS > 1 ? warp : 0;
-  const int rows = a.T * a.G, kvh = blockIdx.y;
-  const int row = min(blockIdx.x * 32 + lane, rows - 1);
-  const int c0 = WAYS > 1 ? blockIdx.z : warp * kChunks;
+  const int rows = a.T * a.G, blocks = (rows + 31) / 32;
+  const int part = index % kParts, row0 = (index / kParts) % blocks * 32, kvh = index / kParts / blocks;
+  const int row = min(row0 + lane, rows - 1);
+  const int c0 = WAYS > 1 ? part : warp * kChunks;
   const int tile = row >> 7, r = row & 127, t = row / a.G;
   const int per = a.two ? a.items * 2 : 1;       // slots per (head, split)
   const int step = per, count = a.splits;
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
-  pdl_wait();
-  pdl_trigger();
   const bool present = a.depth[t] >= 0, bad = *a.err != 0;
   float m = -INFINITY;
 #pragma unroll 8
@@ -653,24 +666,77 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
     const uint2 packed = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     if (WAYS > 1) {
-      if (blockIdx.x * 32 + lane < rows)
+      if (row0 + lane < rows)
         *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.H + kvh * a.G + row % a.G) * DH + c0 * 4) =
             packed;
     } else {
       reinterpret_cast<uint2*>(&s_o[warp * kChunks + q][lane])[0] = packed;
     }
   }
-  if (c0 == 0 && blockIdx.x * 32 + lane < rows)
+  if (c0 == 0 && row0 + lane < rows)
     a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
   if (WAYS > 1) return;
   __syncthreads();
   // DH / 4 consecutive lanes write a row
   for (int e = threadIdx.x; e < 32 * (DH / 4); e += kJoinWarps * 32) {
-    const int i = e / (DH / 4), c = e % (DH / 4), rw = blockIdx.x * 32 + i;
+    const int i = e / (DH / 4), c = e % (DH / 4), rw = row0 + i;
     if (rw < rows)
       *reinterpret_cast<uint2*>(a.out + ((size_t)(rw / a.G) * a.H + kvh * a.G + rw % a.G) * DH +
                                 c * 4) = *reinterpret_cast<const uint2*>(&s_o[c][i]);
   }
+}
+
+// Weights from scores: thread = key, two blocks of 128 keys per CTA; the
+// rows' log-sum-exp from the units' statistics, one row per warp in turn.
+SSD_DI void score_weights(const TreeArgs& a, int index) {
+  __shared__ float s_lse[kTreeScoreRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = a.T * a.G;
+  const int pairs = (a.nb + 1) / 2, kvh = index / pairs;
+  const int b = (index - kvh * pairs) * 2 + (threadIdx.x >> 7), k = threadIdx.x & 127;
+  const bool bad = *a.err != 0;
+  for (int row = warp; row < rows; row += kJoinWarps) {
+    float lse;
+    if (a.splits == 1) {
+      lse = a.lse[(size_t)kvh * rows + row];
+    } else {
+      const size_t s0 = (size_t)kvh * a.splits * 128 + row;
+      float m = -INFINITY, l = 0.f;
+      for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, a.part_m[s0 + (size_t)i * 128]);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float base = m == -INFINITY ? 0.f : m;
+      for (int i = lane; i < a.splits; i += 32)
+        l = fmaf(a.part_l[s0 + (size_t)i * 128], exp2f(a.part_m[s0 + (size_t)i * 128] - base), l);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      lse = l != 0.f && a.depth[row / a.G] >= 0 ? m + log2f(l) : INFINITY;
+    }
+    if (lane == 0) s_lse[row] = bad ? NAN : lse;
+  }
+  __syncthreads();
+  const bool ctx = b < a.nb_ctx;
+  const int key = ctx ? b * kTreeKeys + k : a.n + (b - a.nb_ctx) * kTreeKeys + k;
+  if (b >= a.nb || key >= (ctx ? a.n : a.n + a.T)) return;
+  const float* ps = a.part_s + ((size_t)kvh * a.nb + b) * rows * kTreeKeys + k;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int row = 0; row < rows; ++row) {
+    const float lse = s_lse[row], p = tree_ex2(fmaf(ps[(size_t)row * kTreeKeys], a.scale_log2, -lse));
+    if (lse != INFINITY) sum += p;               // absent rows take no part
+  }
+  const size_t o = (size_t)kvh * a.max_seq + key;
+  a.w_out[o] = ctx && a.w_in ? a.w_in[o] + sum : sum;
+}
+
+template <int DH, int WAYS>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    tree_finish_kernel(const __grid_constant__ TreeArgs a, int joins) {
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < joins)
+    join_rows<DH, WAYS>(a, blockIdx.x);
+  else
+    score_weights(a, blockIdx.x - joins);
 }
 
 template <int DH, bool TWO>
@@ -696,13 +762,15 @@ cudaError_t launch(const TreeArgs& a, const TreeMaps& m, cudaStream_t st) {
   lc.attrs = attr;
   lc.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH, TWO>, m.k, m.v, m.ws, a);
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || (a.splits == 1 && !a.part_s)) return e;
   const bool many = a.splits >= 16;
-  lc.gridDim = dim3((rows + 31) / 32, a.Hkv, many ? DH / 4 : 1);
+  const int joins = a.splits == 1 ? 0 : (rows + 31) / 32 * a.Hkv * (many ? DH / 4 : 1);
+  const int sums = a.part_s ? (a.nb + 1) / 2 * a.Hkv : 0;
+  lc.gridDim = dim3(joins + sums);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
-  return many ? cudaLaunchKernelEx(&lc, tree_join_kernel<DH, kJoinWarps>, a)
-              : cudaLaunchKernelEx(&lc, tree_join_kernel<DH, 1>, a);
+  return many ? cudaLaunchKernelEx(&lc, tree_finish_kernel<DH, kJoinWarps>, a, joins)
+              : cudaLaunchKernelEx(&lc, tree_finish_kernel<DH, 1>, a, joins);
 }
 
 }  // namespace
