@@ -30,6 +30,21 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
   __shared__ float2 turn[kTreeMaxHalf];  // (cos, sin) of the node's position
   pdl_trigger();
   const int t = blockIdx.x, tid = threadIdx.x;
+  const int half = a.dh >> 1, heads = a.H + 2 * a.Hkv;
+  const int h0 = blockIdx.y * kPrepHeads, h1 = min(h0 + kPrepHeads, heads);
+  const float* row = a.qkv + (size_t)t * heads * a.dh;
+  // the projections load while the ancestors are found
+  constexpr int kPairs = kPrepHeads * kTreeMaxHalf / kPrepThreads;
+  float px[kPairs], py[kPairs];
+#pragma unroll
+  for (int q = 0; q < kPairs; ++q) {
+    const int e = tid + q * kPrepThreads, h = h0 + e / half, i = e % half;
+    px[q] = py[q] = 0.f;
+    if (h < h1) {
+      px[q] = row[(size_t)h * a.dh + i];
+      py[q] = row[(size_t)h * a.dh + half + i];
+    }
+  }
   if (t == 0 && blockIdx.y == 0 && tid == 0) *a.err = 0;
   for (int i = tid; i <= t; i += kPrepThreads) par[i] = a.parents[i];
   for (int i = tid; i < kTreeMaxNodes / 32; i += kPrepThreads) bits[i] = 0u;
@@ -63,14 +78,12 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
     sincospif((float)x, &turn[tid].y, &turn[tid].x);
   }
   __syncthreads();
-  const int half = a.dh >> 1, heads = a.H + 2 * a.Hkv;
-  const int h0 = blockIdx.y * kPrepHeads, h1 = min(h0 + kPrepHeads, heads);
-  const float* row = a.qkv + (size_t)t * heads * a.dh;
   const size_t qplane = (size_t)a.Hkv * a.T * a.G * a.dh;
-  for (int e = tid; e < (h1 - h0) * half; e += kPrepThreads) {
-    const int h = h0 + e / half, i = e % half;
-    float x = row[(size_t)h * a.dh + i], y = row[(size_t)h * a.dh + half + i];
-    if (d < 0) x = y = 0.f;
+#pragma unroll
+  for (int q = 0; q < kPairs; ++q) {
+    const int e = tid + q * kPrepThreads, h = h0 + e / half, i = e % half;
+    if (h >= h1) continue;
+    float x = d < 0 ? 0.f : px[q], y = d < 0 ? 0.f : py[q];
     if (h < a.H + a.Hkv) {
       const float cs = turn[i].x, sn = turn[i].y;
       const float rx = x * cs - y * sn, ry = y * cs + x * sn;

@@ -93,12 +93,14 @@ struct Unit {
 SSD_DI Unit unit_of(const TreeArgs& a, int u) {
   Unit x;
   // items fastest, then splits: CTAs that run together read the same keys
-  x.item = u % a.items;
   const int r = u / a.items;
-  x.split = r % a.splits;
+  x.item = u - r * a.items;
   x.kvh = r / a.splits;
-  x.b0 = (int)((long long)x.split * a.nb / a.splits);
-  x.nb = (int)((long long)(x.split + 1) * a.nb / a.splits) - x.b0;
+  x.split = r - x.kvh * a.splits;
+  // nb / splits blocks each, one more for the first nb % splits
+  const int len = a.nb / a.splits, more = a.nb - len * a.splits;
+  x.b0 = x.split * len + min(x.split, more);
+  x.nb = len + (x.split < more);
   return x;
 }
 
@@ -166,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rows = a.T * a.G;
   unsigned char* ring = sm + kTiles * 2 * kItem;
 
-  if (tid == 0) {
+  // (the copying thread itself: its first copies need not wait for the others)
+  if (tid == 256) {
     mbar_init(qfull, 1);
     mbar_init(qfree, 1);
     for (int s = 0; s < 2; ++s) {
@@ -185,30 +188,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(tslot, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
+  auto set_up = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return *reinterpret_cast<volatile uint32_t*>(tslot);
+  };
 
   if (warp == 8) {
+    // ---- copies, in the order in which the products use them: K of the first
+    // kLag blocks, then V of block i and K of block i + kLag in turn
+    Ring<kStages> at;
+    int issued = 0, units = 0;                   // copies / units so far
+    auto is_ctx = [&](const Unit& x, int i, int& b, bool& is_v) {
+      const int pro = min(kLag, x.nb), mid = 2 * (x.nb - pro);
+      if (i < pro) {
+        b = i;
+        is_v = false;
+      } else if (i - pro < mid) {
+        is_v = ((i - pro) & 1) == 0;
+        b = (i - pro) / 2 + (is_v ? 0 : kLag);
+      } else {
+        is_v = true;
+        b = mid / 2 + (i - pro - mid);
+      }
+      b += x.b0;
+      return b < a.nb_ctx;
+    };
+    auto copy = [&](const Unit& x, int b, bool is_v, bool ctx) {
+      mbar_arrive_expect_tx(&full[at.slot], (uint32_t)kItem);
+      const CUtensorMap* m = !ctx ? &mW : is_v ? &mV : &mK;
+      const int row = ctx ? b * kTreeKeys
+                          : (is_v ? a.row_vt : a.row_kt) + x.kvh * a.T + (b - a.nb_ctx) * kTreeKeys;
+      for (int r = 0; r < kRegs; ++r)
+        tma_load_3d(ring + at.slot * kItem + r * kRegion, m, r * 64, row, ctx ? x.kvh : 0,
+                    &full[at.slot]);
+      ++issued;
+      at = at.next();
+    };
+    // the first copies of context blocks need neither the others' set-up nor
+    // the preparation
+    int b;
+    bool is_v;
     if (lane == 0) {
-      // ---- copies, in the order in which the products use them: K of the
-      // first `lag` blocks, then V of block i and K of block i + lag in turn
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&mW) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&mK) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&mV) : "memory");
-      Ring<kStages> at;
-      int issued = 0, units = 0;                 // copies / units so far
-      bool ok = true, waited = false;
+      const Unit x = unit_of(a, blockIdx.x);
+      while (issued < min(kStages, 2 * x.nb) && is_ctx(x, issued, b, is_v)) copy(x, b, is_v, true);
+    }
+    __syncwarp();
+    set_up();
+    if (lane == 0) {
+      pdl_wait();                                // the queries come from the preparation
+      bool ok = true;
       for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++units) {
         const Unit x = unit_of(a, u);
-        const int pro = min(kLag, x.nb), mid = 2 * (x.nb - pro), total = 2 * x.nb;
         bool q_sent = false;
         auto send_q = [&]() {
-          if (!waited) {
-            pdl_wait();                          // the rows come from the preparation
-            waited = true;
-          }
           if (units > 0 && !mbar_wait_n(qfree, (uint32_t)((units - 1) & 1), kPolls)) return false;
           mbar_arrive_expect_tx(qfull, (uint32_t)(kTiles * 2 * kItem));
           for (int t = 0; t < kTiles; ++t)
@@ -219,39 +253,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           q_sent = true;
           return true;
         };
-        for (int i = 0; ok && i < total; ++i) {
-          int b;
-          bool is_v;
-          if (i < pro) {
-            b = i;
-            is_v = false;
-          } else if (i - pro < mid) {
-            is_v = ((i - pro) & 1) == 0;
-            b = (i - pro) / 2 + (is_v ? 0 : kLag);
-          } else {
-            is_v = true;
-            b = mid / 2 + (i - pro - mid);
-          }
-          b += x.b0;
-          const bool ctx = b < a.nb_ctx;
-          // the CTA's first copies of context blocks go out before the rows are
-          // ready; a later unit's first blocks before its rows are free (the
-          // slots they wait for need no query of this unit)
-          if (!q_sent && (units > 0 ? i >= kLag : !ctx || issued >= kStages)) ok = send_q();
+        for (int i = units > 0 ? 0 : issued; ok && i < 2 * x.nb; ++i) {
+          const bool ctx = is_ctx(x, i, b, is_v);
+          // a later unit's first blocks go out before its queries' place is
+          // free (the slots they wait for need no query of this unit)
+          if (!q_sent && (units == 0 || i >= kLag)) ok = send_q();
           if (ok && issued >= kStages) ok = mbar_wait_n(&empty[at.slot], at.phase ^ 1u, kPolls);
           if (!ok || tree_flagged(fail)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[at.slot], (uint32_t)kItem);
-          const CUtensorMap* m = !ctx ? &mW : is_v ? &mV : &mK;
-          const int row = ctx ? b * kTreeKeys
-                              : (is_v ? a.row_vt : a.row_kt) + x.kvh * a.T + (b - a.nb_ctx) * kTreeKeys;
-          for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(ring + at.slot * kItem + r * kRegion, m, r * 64, row, ctx ? x.kvh : 0,
-                        &full[at.slot]);
-          ++issued;
-          at = at.next();
+          copy(x, b, is_v, ctx);
         }
         if (ok && !q_sent) ok = send_q();
         if (!q_sent) break;
@@ -264,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ---- products: the warp runs together, one lane issues
+    const uint32_t tmem = set_up();
     const uint32_t lead = tree_elect();
     constexpr uint32_t ids = idesc_bf16(128, 128), idp = idesc_pv(DH);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -351,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_n(mdone, 0u, kPolls);
   } else {
     // ---- softmax: stream s, one thread per row of its tile
+    const uint32_t tmem = set_up();
     pdl_wait();
     const int s = warp >> 2, r = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -379,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (warp_live) {
+          const int b = x.b0 + (TWO ? j : 2 * j + s);
           uint32_t sr[4][32];
 #pragma unroll
           for (int q = 0; q < 2; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
-          const int b = x.b0 + (TWO ? j : 2 * j + s);
           const int left = a.n - b * kTreeKeys;  // context keys from this block on
           const bool whole = b < a.nb_ctx && left >= kTreeKeys;
           uint4 mask = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -427,16 +441,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[q][e]),
                                         __uint_as_float(sr[q][e + 1]));
           }
-          if (!TWO && a.part_s && live) {
-            float4* ps = reinterpret_cast<float4*>(
-                a.part_s + (((size_t)x.kvh * a.nb + b) * rows + row) * kTreeKeys);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              ps[e] = make_float4(__uint_as_float(sr[e >> 3][(4 * e) & 31]),
-                                  __uint_as_float(sr[e >> 3][(4 * e + 1) & 31]),
-                                  __uint_as_float(sr[e >> 3][(4 * e + 2) & 31]),
-                                  __uint_as_float(sr[e >> 3][(4 * e + 3) & 31]));
-          }
           const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
           const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
@@ -463,6 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
+            if (!TWO && a.part_s && live) {      // between the exponentials
+              float4* ps = reinterpret_cast<float4*>(
+                  a.part_s + (((size_t)x.kvh * a.nb + b) * rows + row) * kTreeKeys + q * 32);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                ps[e >> 2] = make_float4(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]),
+                                         __uint_as_float(sr[q][e + 2]), __uint_as_float(sr[q][e + 3]));
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float p0, p1;
@@ -587,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && tree_flagged(fail)) atomicExch(a.err, 1);
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(*tslot, 512);
 }
 
 // After the units: CTAs 0 .. joins - 1 join their partial results, the rest
