@@ -20,6 +20,7 @@
 // runs out, and the results become NaN.
 #include "tc_dev.cuh"
 #include "tree.cuh"
+#include "tree_join.cuh"
 
 namespace ssd {
 namespace {
@@ -102,37 +103,6 @@ SSD_DI Unit unit_of(const TreeArgs& a, int u) {
   x.b0 = x.split * len + min(x.split, more);
   x.nb = len + (x.split < more);
   return x;
-}
-
-// Whether any node's V row of this head holds inf or NaN (a warp asks).
-SSD_DI bool any_bad(const TreeArgs& a, int kvh, int lane) {
-  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
-  bool any = false;
-  for (int j = lane; j < a.T; j += 32) any |= flags[j] != 0;
-  return __any_sync(0xffffffffu, any);
-}
-
-// Adds to n columns from c0 on of row (node t) the inf and NaN of the V rows
-// that it sees, which the products left out: v += p_j V_j for those values.
-template <int DH>
-__device__ __noinline__ void add_bad(const TreeArgs& a, int kvh, int row, int t, float lse, int c0,
-                                     float* v, int n) {
-  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
-  const int rows = a.T * a.G;
-  const size_t plane = (size_t)a.Hkv * rows * DH;
-  const bf16* q = a.q + ((size_t)kvh * rows + row) * DH;
-  for (int j = 0; j <= t; ++j) {
-    if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
-    const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
-    float acc = 0.f;
-    for (int i = 0; i < DH; ++i)
-      acc = fmaf(__bfloat162float(q[i]) + __bfloat162float(q[plane + i]), __bfloat162float(k[i]), acc);
-    const float p = exp2f(acc * a.scale_log2 - lse);
-    for (int e = 0; e < n; ++e) {
-      const float x = __bfloat162float(a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + c0 + e]);
-      if (!isfinite(x)) v[e] += p * x;
-    }
-  }
 }
 
 template <int DH, bool TWO>
@@ -602,102 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(*tslot, 512);
 }
 
-// After the units: CTAs 0 .. joins - 1 join their partial results, the rest
-// sum the weights from stored scores (where there are any).  Both read the
-// units' statistics, so that neither waits for the other.
-//
-// Joining: CTA = 32 rows of one K/V head, lane = row; the slots are added in
-// order.  With WAYS = 1 each warp has an eighth of the columns; with WAYS = 8
-// (many slots, few rows) a CTA has one 16-byte column and each warp every
-// eighth slot.  Rows leave through shared memory, so that stores are whole
-// rows.
-constexpr int kJoinWarps = 8;
-template <int DH, int WAYS>
-SSD_DI void join_rows(const TreeArgs& a, int index) {
-  constexpr int kChunks = WAYS > 1 ? 1 : DH / 4 / kJoinWarps;  // 16-byte columns per warp
-  constexpr int kParts = WAYS > 1 ? DH / 4 : 1;  // CTAs per 32 rows
-  __shared__ float4 s_o[kJoinWarps * kChunks][33];
-  __shared__ float s_l[kJoinWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = WAYS > 1 ? warp : 0;
-  const int rows = a.T * a.G, blocks = (rows + 31) / 32;
-  const int part = index % kParts, row0 = (index / kParts) % blocks * 32, kvh = index / kParts / blocks;
-  const int row = min(row0 + lane, rows - 1);
-  const int c0 = WAYS > 1 ? part : warp * kChunks;
-  const int tile = row >> 7, r = row & 127, t = row / a.G;
-  const int per = a.two ? a.items * 2 : 1;       // slots per (head, split)
-  const int step = per, count = a.splits;
-  const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
-  const bool present = a.depth[t] >= 0, bad = *a.err != 0;
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < count; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * step) * 128 + r]);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float4 o[kChunks];
-#pragma unroll
-  for (int q = 0; q < kChunks; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = way; i < count; i += WAYS) {
-    const size_t sl = s0 + (size_t)i * step;
-    const float w = exp2f(a.part_m[sl * 128 + r] - base);
-    l = fmaf(a.part_l[sl * 128 + r], w, l);
-#pragma unroll
-    for (int q = 0; q < kChunks; ++q) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 +
-                                                        (size_t)(c0 + q) * 512 + r * 4);
-      o[q].x = fmaf(v.x, w, o[q].x);
-      o[q].y = fmaf(v.y, w, o[q].y);
-      o[q].z = fmaf(v.z, w, o[q].z);
-      o[q].w = fmaf(v.w, w, o[q].w);
-    }
-  }
-  if (WAYS > 1) {
-    s_o[warp][lane] = o[0];
-    s_l[warp][lane] = l;
-    __syncthreads();
-    if (way) return;
-    for (int i = 1; i < WAYS; ++i) {
-      const float4 v = s_o[i][lane];
-      l += s_l[i][lane];
-      o[0].x += v.x;
-      o[0].y += v.y;
-      o[0].z += v.z;
-      o[0].w += v.w;
-    }
-  }
-  const float lse = l != 0.f ? m + log2f(l) : INFINITY;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const bool marked = any_bad(a, kvh, lane);
-#pragma unroll
-  for (int q = 0; q < kChunks; ++q) {
-    float v[4] = {o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv};
-    if (!present)
-      v[0] = v[1] = v[2] = v[3] = 0.f;
-    else if (marked)
-      add_bad<DH>(a, kvh, row, t, lse, (c0 + q) * 4, v, 4);
-    if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
-    const uint2 packed = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    if (WAYS > 1) {
-      if (row0 + lane < rows)
-        *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.H + kvh * a.G + row % a.G) * DH + c0 * 4) =
-            packed;
-    } else {
-      reinterpret_cast<uint2*>(&s_o[warp * kChunks + q][lane])[0] = packed;
-    }
-  }
-  if (c0 == 0 && row0 + lane < rows)
-    a.lse[(size_t)kvh * rows + row] = bad ? NAN : present ? lse : INFINITY;
-  if (WAYS > 1) return;
-  __syncthreads();
-  // DH / 4 consecutive lanes write a row
-  for (int e = threadIdx.x; e < 32 * (DH / 4); e += kJoinWarps * 32) {
-    const int i = e / (DH / 4), c = e % (DH / 4), rw = row0 + i;
-    if (rw < rows)
-      *reinterpret_cast<uint2*>(a.out + ((size_t)(rw / a.G) * a.H + kvh * a.G + rw % a.G) * DH +
-                                c * 4) = *reinterpret_cast<const uint2*>(&s_o[c][i]);
-  }
-}
-
 // Weights from scores: thread = key, two blocks of 128 keys per CTA; the
 // rows' log-sum-exp from the units' statistics, one row per warp in turn.
 SSD_DI void score_weights(const TreeArgs& a, int index) {
@@ -740,15 +614,74 @@ SSD_DI void score_weights(const TreeArgs& a, int index) {
   a.w_out[o] = ctx && a.w_in ? a.w_in[o] + sum : sum;
 }
 
-template <int DH, int WAYS>
+// Many slots and few rows: CTA = one 16-byte column of 32 rows, each warp
+// adds every eighth slot, then the warps' sums are added in order.
+template <int DH>
+SSD_DI void join_column(const TreeArgs& a, int index) {
+  __shared__ float4 s_o[kJoinWarps][32];
+  __shared__ float s_l[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = a.T * a.G, blocks = (rows + 31) / 32;
+  const int c = index % (DH / 4), row0 = (index / (DH / 4)) % blocks * 32;
+  const int kvh = index / (DH / 4) / blocks, row = min(row0 + lane, rows - 1);
+  const int tile = row >> 7, r = row & 127, t = row / a.G, per = a.two ? a.items * 2 : 1;
+  const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
+  const bool present = a.depth[t] >= 0, bad = *a.err != 0;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * per) * 128 + r]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = warp; i < a.splits; i += kJoinWarps) {
+    const size_t sl = s0 + (size_t)i * per;
+    const float w = exp2f(a.part_m[sl * 128 + r] - base);
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 + (size_t)c * 512 + r * 4);
+    l = fmaf(a.part_l[sl * 128 + r], w, l);
+    o.x = fmaf(v.x, w, o.x);
+    o.y = fmaf(v.y, w, o.y);
+    o.z = fmaf(v.z, w, o.z);
+    o.w = fmaf(v.w, w, o.w);
+  }
+  s_o[warp][lane] = o;
+  s_l[warp][lane] = l;
+  __syncthreads();
+  if (warp) return;
+  for (int i = 1; i < kJoinWarps; ++i) {
+    const float4 v = s_o[i][lane];
+    l += s_l[i][lane];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+  }
+  const float lse = l != 0.f ? m + log2f(l) : INFINITY, inv = l != 0.f ? 1.f / l : 0.f;
+  float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  const bool marked = any_bad(a, kvh, lane);
+  if (!present)
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+  else if (marked)
+    add_bad<DH>(a, kvh, row, t, lse, c * 4, v, 4);
+  if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
+  if (row0 + lane < rows)
+    *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.H + kvh * a.G + row % a.G) * DH + c * 4) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// After the units: CTAs 0 .. joins - 1 join their partial results, the rest
+// sum the weights from stored scores (where there are any).  Both read the
+// units' statistics, so that neither waits for the other.
+template <int DH, bool COLUMNS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     tree_finish_kernel(const __grid_constant__ TreeArgs a, int joins) {
   pdl_wait();
-  pdl_trigger();
-  if ((int)blockIdx.x < joins)
-    join_rows<DH, WAYS>(a, blockIdx.x);
-  else
+  if ((int)blockIdx.x >= joins)
     score_weights(a, blockIdx.x - joins);
+  else if (COLUMNS)
+    join_column<DH>(a, blockIdx.x);
+  else
+    tree_join_rows<DH>(a, blockIdx.x);
 }
 
 template <int DH, bool TWO>
@@ -775,14 +708,15 @@ cudaError_t launch(const TreeArgs& a, const TreeMaps& m, cudaStream_t st) {
   lc.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&lc, tree_attn_tc_kernel<DH, TWO>, m.k, m.v, m.ws, a);
   if (e != cudaSuccess || (a.splits == 1 && !a.part_s)) return e;
-  const bool many = a.splits >= 16;
-  const int joins = a.splits == 1 ? 0 : (rows + 31) / 32 * a.Hkv * (many ? DH / 4 : 1);
+  if (a.w_out && !a.part_s) return e;            // the weights' kernel joins
+  const bool columns = a.splits >= 16 && rows <= 128;
+  const int joins = a.splits == 1 ? 0 : (rows + 31) / 32 * a.Hkv * (columns ? DH / 4 : 1);
   const int sums = a.part_s ? (a.nb + 1) / 2 * a.Hkv : 0;
   lc.gridDim = dim3(joins + sums);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
-  return many ? cudaLaunchKernelEx(&lc, tree_finish_kernel<DH, kJoinWarps>, a, joins)
-              : cudaLaunchKernelEx(&lc, tree_finish_kernel<DH, 1>, a, joins);
+  return columns ? cudaLaunchKernelEx(&lc, tree_finish_kernel<DH, true>, a, joins)
+                 : cudaLaunchKernelEx(&lc, tree_finish_kernel<DH, false>, a, joins);
 }
 
 }  // namespace

@@ -1,0 +1,118 @@
+// Joining the partial results of a tree attention's units (shared by the
+// kernel after the units and the one that sums the weights).
+#pragma once
+
+#include "tree.cuh"
+
+namespace ssd {
+
+// Whether any node's V row of this head holds inf or NaN (a warp asks).
+SSD_DI bool any_bad(const TreeArgs& a, int kvh, int lane) {
+  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
+  bool any = false;
+  for (int j = lane; j < a.T; j += 32) any |= flags[j] != 0;
+  return __any_sync(0xffffffffu, any);
+}
+
+// Adds to n columns from c0 on of row (node t) the inf and NaN of the V rows
+// that it sees, which the products left out: v += p_j V_j for those values.
+template <int DH>
+static __device__ __noinline__ void add_bad(const TreeArgs& a, int kvh, int row, int t, float lse, int c0,
+                                     float* v, int n) {
+  const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
+  const int rows = a.T * a.G;
+  const size_t plane = (size_t)a.Hkv * rows * DH;
+  const bf16* q = a.q + ((size_t)kvh * rows + row) * DH;
+  for (int j = 0; j <= t; ++j) {
+    if (!flags[j] || !((a.anc[(size_t)t * a.anc_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+    const bf16* k = a.kt + ((size_t)kvh * a.T + j) * DH;
+    float acc = 0.f;
+    for (int i = 0; i < DH; ++i)
+      acc = fmaf(__bfloat162float(q[i]) + __bfloat162float(q[plane + i]), __bfloat162float(k[i]), acc);
+    const float p = exp2f(acc * a.scale_log2 - lse);
+    for (int e = 0; e < n; ++e) {
+      const float x = __bfloat162float(a.vc[((size_t)kvh * a.max_seq + a.n + j) * DH + c0 + e]);
+      if (!isfinite(x)) v[e] += p * x;
+    }
+  }
+}
+
+// Base-2 log-sum-exp of a row from the units' statistics (one split: as the
+// attention wrote it); infinity for an absent row.
+SSD_DI float tree_row_lse(const TreeArgs& a, int kvh, int row) {
+  if (a.splits == 1) return a.lse[(size_t)kvh * a.T * a.G + row];
+  const int per = a.two ? a.items * 2 : 1;
+  const size_t s0 = ((size_t)kvh * a.splits * per + (a.two ? row >> 7 : 0)) * 128 + (row & 127);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[s0 + (size_t)i * per * 128]);
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i)
+    l = fmaf(a.part_l[s0 + (size_t)i * per * 128], exp2f(a.part_m[s0 + (size_t)i * per * 128] - base), l);
+  return l != 0.f && a.depth[row / a.G] >= 0 ? m + log2f(l) : INFINITY;
+}
+
+// Joins of 32 rows each, eight warps: lane = row, each warp an eighth of the
+// columns (whole 16- or 32-byte sectors per row); the slots are added in order.
+constexpr int kJoinWarps = 8;
+SSD_DI int tree_joins(const TreeArgs& a) { return (a.T * a.G + 31) / 32 * a.Hkv; }
+
+template <int DH>
+SSD_DI void tree_join_rows(const TreeArgs& a, int index) {
+  constexpr int kChunks = DH / 4 / kJoinWarps;   // 16-byte columns per warp
+  const int warp = (threadIdx.x >> 5) & (kJoinWarps - 1), lane = threadIdx.x & 31;
+  const int rows = a.T * a.G, blocks = (rows + 31) / 32;
+  const int kvh = index / blocks, row0 = (index - kvh * blocks) * 32;
+  const int row = min(row0 + lane, rows - 1), c0 = warp * kChunks;
+  const int tile = row >> 7, r = row & 127, t = row / a.G;
+  const int per = a.two ? a.items * 2 : 1;       // slots per (head, split)
+  const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
+  const bool present = a.depth[t] >= 0, bad = *a.err != 0;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * per) * 128 + r]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o[kChunks];
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) {
+    const size_t sl = s0 + (size_t)i * per;
+    const float w = exp2f(a.part_m[sl * 128 + r] - base);
+    l = fmaf(a.part_l[sl * 128 + r], w, l);
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 +
+                                                        (size_t)(c0 + q) * 512 + r * 4);
+      o[q].x = fmaf(v.x, w, o[q].x);
+      o[q].y = fmaf(v.y, w, o[q].y);
+      o[q].z = fmaf(v.z, w, o[q].z);
+      o[q].w = fmaf(v.w, w, o[q].w);
+    }
+  }
+  const float lse = l != 0.f ? m + log2f(l) : INFINITY;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const bool marked = any_bad(a, kvh, lane);
+  uint32_t packed[2 * kChunks];
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) {
+    float v[4] = {o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv};
+    if (!present)
+      v[0] = v[1] = v[2] = v[3] = 0.f;
+    else if (marked)
+      add_bad<DH>(a, kvh, row, t, lse, (c0 + q) * 4, v, 4);
+    if (bad) v[0] = v[1] = v[2] = v[3] = NAN;
+    packed[2 * q] = pack_bf16x2(v[0], v[1]);
+    packed[2 * q + 1] = pack_bf16x2(v[2], v[3]);
+  }
+  if (row0 + lane >= rows) return;
+  bf16* out = a.out + ((size_t)t * a.H + kvh * a.G + row % a.G) * DH + c0 * 4;
+#pragma unroll
+  for (int q = 0; q < kChunks; q += 2)
+    *reinterpret_cast<uint4*>(out + q * 4) =
+        make_uint4(packed[2 * q], packed[2 * q + 1], packed[2 * q + 2], packed[2 * q + 3]);
+}
+
+}  // namespace ssd

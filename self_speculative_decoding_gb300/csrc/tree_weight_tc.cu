@@ -5,14 +5,20 @@
 // memory lane, one row per column), so that a key's sum is one thread's sum
 // over its columns: no exchange between threads and a fixed order.
 //
-// Unit = two blocks of 128 keys of one K/V head; warps 0-3 and 4-7 take a
-// block each, every tile of 128 rows passes both (a Q tile read from L2
-// serves 256 keys), plane by plane (low part, high part).  Up to two Q tiles
-// stay in shared memory for all of a CTA's units of a head; more stream
-// through three slots of a plane each.  Warp 8: TMA copies, warp 9: MMA.  Waits are bounded;
-// one that gives up makes the CTA's weights NaN.
+// A CTA has a run of key blocks, taken in segments of up to 16.  A pass goes
+// over a segment with one tile of 128 rows: the tile's two planes (q's low and
+// high part) stay in shared memory while the K blocks stream, in turn to two
+// streams of four warps; the sums of a segment's keys stay with their threads
+// until every tile has passed.  The next pass's planes load meanwhile; up to
+// two tiles stay for all of a head's segments.  (Held the other way round, two
+// K blocks with the Q planes streaming, 64 nodes of 64 / 8 heads over 32768
+// rows took 61 us.)  The softmax warps first join the attention's partial
+// results, so that no kernel runs between.
+// Warp 8: TMA copies, warp 9: MMA.  Waits are bounded; one that gives up makes
+// the CTA's weights NaN.
 #include "tc_dev.cuh"
 #include "tree.cuh"
+#include "tree_join.cuh"
 
 namespace ssd {
 namespace {
@@ -25,6 +31,7 @@ constexpr int kRegion = 128 * 128;
 constexpr int kTileSmem = 224 * 1024;            // Q tiles (hi, lo), then the ring of K blocks
 constexpr int kMaxStages = 12;
 constexpr int kMaxPlanes = 4;
+constexpr int kSegment = 16;                     // key blocks of a segment
 
 // Barrier of one stream's 128 threads; true if any of them passed true.
 SSD_DI bool stream_any(int s, bool x) {
@@ -44,12 +51,33 @@ SSD_DI void stream_sync(int s) {
   asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(s + 1), "r"(128) : "memory");
 }
 
-struct Range {
-  int u0, u1;
+// A CTA's passes in order: every tile over each segment of its run.
+struct Pass {
+  int pos, end, kvh, b0, cnt, t;
+  SSD_DI void segment(const TreeArgs& a) {
+    kvh = pos / a.nb;
+    b0 = pos - kvh * a.nb;
+    cnt = min(kSegment, min(a.nb - b0, end - pos));
+    t = 0;
+  }
+  SSD_DI bool done() const { return pos >= end; }
+  SSD_DI bool last_of_head(const TreeArgs& a) const {
+    return t + 1 == a.tiles && (b0 + cnt == a.nb || pos + cnt == end);
+  }
+  SSD_DI bool first_of_head(int begin) const { return t == 0 && (b0 == 0 || pos == begin); }
+  SSD_DI void next(const TreeArgs& a) {
+    if (++t < a.tiles) return;
+    pos += cnt;
+    if (pos < end) segment(a);
+  }
 };
-SSD_DI Range my_units(const TreeArgs& a) {
-  const long long total = (long long)a.Hkv * ((a.nb + 1) / 2);
-  return {(int)(blockIdx.x * total / gridDim.x), (int)((blockIdx.x + 1) * total / gridDim.x)};
+SSD_DI Pass first_pass(const TreeArgs& a) {
+  const long long total = (long long)a.Hkv * a.nb;
+  Pass p;
+  p.pos = (int)(blockIdx.x * total / gridDim.x);
+  p.end = (int)((blockIdx.x + 1) * total / gridDim.x);
+  if (p.pos < p.end) p.segment(a);
+  return p;
 }
 
 template <int DH>
@@ -75,12 +103,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G;
-  const bool resident = a.tiles <= 2;            // Q stays for all units of a head
-  const int qslots = resident ? 2 * a.tiles : 3;
+  const bool resident = a.tiles <= 2;            // Q stays for all segments of a head
+  const int qslots = resident ? 2 * a.tiles : kMaxPlanes;
   const int stages = min(kMaxStages, kTileSmem / kItem - qslots);
   unsigned char* ring = sm + qslots * kItem;
-  const int pairs = (a.nb + 1) / 2;
-  const Range rg = my_units(a);
 
   if (tid == 0) {
     for (int s = 0; s < kMaxPlanes; ++s) {
@@ -107,124 +133,130 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 8) {
     if (lane == 0) {
-      int issued = 0, qissued = 0;
+      const Pass begin = first_pass(a);
+      int issued = 0, slot = 0, qsent = 0, heads = 0;  // copies, their slot, passes' and heads' planes
+      uint32_t phase = 0;
       bool ok = true;
-      auto send_q = [&](int kvh, int tile) {
-        for (int p = 1; p >= 0; --p) {
-          const int sl = qissued % qslots, use = qissued / qslots;
-          if (use > 0 && !mbar_wait_n(&qempty[sl], (uint32_t)((use - 1) & 1), kPolls)) return false;
-          mbar_arrive_expect_tx(&qfull[sl], (uint32_t)kItem);
-          for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(sm + sl * kItem + r * kRegion, &mW, r * 64,
-                        (p * a.Hkv + kvh) * rows + tile * 128, 0, &qfull[sl]);
-          ++qissued;
-        }
+      auto plane = [&](int sl, bool again, uint32_t ph, int kvh, int tile, int p) {
+        if (again && !mbar_wait_n(&qempty[sl], ph, kPolls)) return false;
+        mbar_arrive_expect_tx(&qfull[sl], (uint32_t)kItem);
+        for (int r = 0; r < kRegs; ++r)
+          tma_load_3d(sm + sl * kItem + r * kRegion, &mW, r * 64,
+                      (p * a.Hkv + kvh) * rows + tile * 128, 0, &qfull[sl]);
         return true;
       };
-      for (int u = rg.u0; ok && u < rg.u1; ++u) {
-        const int kvh = u / pairs, b0 = (u - kvh * pairs) * 2, nblk = min(2, a.nb - b0);
-        if (u == rg.u0) pdl_wait();              // Q and the tree's K rows
-        // Q of a new head before its keys: its slots wait for the old head's
-        // products only, and these for nothing of this unit
-        if (resident && (u == rg.u0 || u % pairs == 0))
-          for (int t = 0; ok && t < a.tiles; ++t) ok = send_q(kvh, t);
-        for (int s = 0; ok && s < nblk; ++s) {
-          const int b = b0 + s, st = issued % stages, use = issued / stages;
-          if (use > 0) ok = mbar_wait_n(&empty[st], (uint32_t)((use - 1) & 1), kPolls);
+      // the planes of a pass (streaming): two slots in turn
+      auto send_pass = [&](const Pass& x) {
+        const int sl = (qsent & 1) * 2;
+        const uint32_t ph = (uint32_t)(((qsent >> 1) - 1) & 1);
+        const bool again = qsent >= 2;
+        ++qsent;
+        return plane(sl, again, ph, x.kvh, x.t, 1) && plane(sl + 1, again, ph, x.kvh, x.t, 0);
+      };
+      pdl_wait();                                // Q and the tree's K rows
+      if (!resident && !begin.done()) ok = send_pass(begin);
+      for (Pass x = begin; ok && !x.done(); x.next(a)) {
+        if (resident && x.first_of_head(begin.pos)) {
+          for (int t = 0; ok && t < a.tiles; ++t)
+            for (int p = 1; ok && p >= 0; --p)
+              ok = plane(2 * t + 1 - p, heads > 0, (uint32_t)((heads - 1) & 1), x.kvh, t, p);
+          ++heads;
+        }
+        for (int j = 0; ok && j < x.cnt; ++j) {
+          if (!resident && j == min(2, x.cnt - 1)) {
+            // the next pass's planes: their slots are the pass before's
+            Pass y = x;
+            y.next(a);
+            if (!y.done()) ok = send_pass(y);
+          }
+          if (ok && issued >= stages) ok = mbar_wait_n(&empty[slot], phase ^ 1u, kPolls);
           if (!ok || tree_flagged(fail)) {
             ok = false;
             break;
           }
+          const int b = x.b0 + j;
           const bool ctx = b < a.nb_ctx;
-          mbar_arrive_expect_tx(&full[st], (uint32_t)kItem);
-          const int row = ctx ? b * kTreeKeys : a.row_kt + kvh * a.T + (b - a.nb_ctx) * kTreeKeys;
+          const int row = ctx ? b * kTreeKeys : a.row_kt + x.kvh * a.T + (b - a.nb_ctx) * kTreeKeys;
+          mbar_arrive_expect_tx(&full[slot], (uint32_t)kItem);
           for (int r = 0; r < kRegs; ++r)
-            tma_load_3d(ring + (size_t)st * kItem + r * kRegion, ctx ? &mK : &mW, r * 64, row,
-                        ctx ? kvh : 0, &full[st]);
+            tma_load_3d(ring + (size_t)slot * kItem + r * kRegion, ctx ? &mK : &mW, r * 64, row,
+                        ctx ? x.kvh : 0, &full[slot]);
           ++issued;
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
-        if (!resident)
-          for (int t = 0; ok && t < a.tiles; ++t) ok = !tree_flagged(fail) && send_q(kvh, t);
       }
       if (!ok) atomicExch(fail, 1);
       for (int i = max(0, issued - stages); i < issued; ++i)
         mbar_wait_n(&full[i % stages], (uint32_t)((i / stages) & 1), kPolls);
-      for (int i = max(0, qissued - qslots); i < qissued; ++i)
-        mbar_wait_n(&qfull[i % qslots], (uint32_t)((i / qslots) & 1), kPolls);
+      // the planes sent last (a slot's last use)
+      if (resident) {
+        for (int i = 0; heads > 0 && i < qslots; ++i)
+          mbar_wait_n(&qfull[i], (uint32_t)((heads - 1) & 1), ok ? kPolls : 1 << 16);
+      } else {
+        for (int q = max(0, qsent - 2); q < qsent; ++q)
+          for (int p = 0; p < 2; ++p)
+            mbar_wait_n(&qfull[(q & 1) * 2 + p], (uint32_t)((q >> 1) & 1), ok ? kPolls : 1 << 16);
+      }
     }
   } else if (warp == 9) {
     // the warp runs together, one lane issues
     const uint32_t lead = tree_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
-    int k0 = 0, kslot[2];                        // K slots of the unit
-    uint32_t kphase = 0;
-    int qslot = 0;
-    uint32_t qphase = 0;
+    const Pass begin = first_pass(a);
+    int slot = 0, passes = 0, heads = 0;
+    uint32_t phase = 0;
     int cs[2] = {0, 0};                          // score tiles per stream
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, phase, kPolls));
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, ph, kPolls));
       tc_fence_after();
     };
-    for (int u = rg.u0; ok && u < rg.u1; ++u) {
-      const int kvh = u / pairs, b0 = (u - kvh * pairs) * 2, nblk = min(2, a.nb - b0);
+    for (Pass x = begin; ok && !x.done(); x.next(a), ++passes) {
+      if (resident && x.first_of_head(begin.pos)) ++heads;
+      const int q0 = resident ? 2 * x.t : (passes & 1) * 2;
+      const uint32_t qph = (uint32_t)((resident ? heads - 1 : passes >> 1) & 1);
+      wait(&qfull[q0], qph);
+      wait(&qfull[q0 + 1], qph);
+      const int cols = min(128, (rows - x.t * 128 + 15) / 16 * 16);
+      const uint32_t id = idesc_bf16(128, cols);
+      const uint32_t qb = qa + (uint32_t)q0 * kItem;
+      for (int j = 0; ok && j < x.cnt; j += 2) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s < nblk) {
-          wait(&full[k0], kphase);
-          kslot[s] = k0;
-          if (++k0 == stages) {
-            k0 = 0;
-            kphase ^= 1u;
-          }
-        }
-      const int q0 = qslot;
-      const uint32_t qp0 = qphase;
-      for (int t = 0; ok && t < a.tiles; ++t) {
-        const int cols = min(128, (rows - t * 128 + 15) / 16 * 16);
-        const uint32_t id = idesc_bf16(128, cols);
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || j + s >= x.cnt) continue;
+          const int buf = cs[s] & 1;
+          wait(&full[slot], phase);
+          if (cs[s] >= 2) wait(&sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok && !tree_flagged(fail));
+          if (!ok) continue;
+          const uint32_t kb = ra + (uint32_t)slot * kItem;
+          const uint32_t acc = tm + (uint32_t)(s * 256 + buf * 128);
 #pragma unroll
-        for (int p = 1; p >= 0; --p) {           // the low part first
-          wait(&qfull[qslot], qphase);
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (!ok || s >= nblk) continue;
-            const int buf = cs[s] & 1;
-            if (p && cs[s] >= 2) wait(&sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1));
-            ok = __all_sync(0xffffffffu, ok && !tree_flagged(fail));
-            if (!ok) continue;
-            const uint32_t kb = ra + (uint32_t)kslot[s] * kItem;
-            const uint32_t qb = qa + (uint32_t)qslot * kItem;
-            const uint32_t acc = tm + (uint32_t)(s * 256 + buf * 128);
+          for (int p = 0; p < 2; ++p)            // the low part first
 #pragma unroll
             for (int ks = 0; ks < DH / 16; ++ks) {
               const uint32_t o = (uint32_t)(ks >> 2) * kRegion;
               tree_mma_ss(lead, acc, sw128_desc(kb + o) + 2 * (ks & 3),
-                          sw128_desc(qb + o) + 2 * (ks & 3), id, (p == 0 || ks > 0) ? 1u : 0u);
+                          sw128_desc(qb + p * kItem + o) + 2 * (ks & 3), id, (p || ks > 0) ? 1u : 0u);
             }
-            if (p == 0) {
-              tree_commit(lead, &sfull[s * 2 + buf]);
-              ++cs[s];
-            }
-          }
-          if (!resident) tree_commit(lead, &qempty[qslot]);
-          if (++qslot == qslots) {
-            qslot = 0;
-            qphase ^= 1u;
+          tree_commit(lead, &sfull[s * 2 + buf]);
+          tree_commit(lead, &empty[slot]);
+          ++cs[s];
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s < nblk) tree_commit(lead, &empty[kslot[s]]);
-      if (resident) {
-        if ((u + 1) % pairs == 0) {              // the head's last unit
-          for (int i = 0; i < 2 * a.tiles; ++i) tree_commit(lead, &qempty[i]);
-        } else {                                 // the same planes again
-          qslot = q0;
-          qphase = qp0;
-        }
+      if (!resident) {
+        tree_commit(lead, &qempty[q0]);
+        tree_commit(lead, &qempty[q0 + 1]);
+      } else if (x.last_of_head(a)) {
+        for (int i = 0; i < qslots; ++i) tree_commit(lead, &qempty[i]);
       }
     }
     if (!ok && lane == 0) atomicExch(fail, 1);
@@ -234,44 +266,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one key per thread.  Every thread passes every barrier: a wait that
     // gives up only turns the sums into NaN.
     pdl_wait();
+    if (a.splits > 1)
+      for (int i = blockIdx.x; i < tree_joins(a); i += gridDim.x) tree_join_rows<DH>(a, i);
     const int s = warp >> 2, r = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)s * 256;
     const float scale = a.scale_log2;
+    const bool bad = *a.err != 0;
+    float* nl = nlse + s * 128;
     int c = 0;
-    bool ok = true;
-    // -lse of row r of a tile; rows that are absent, or beyond the last, take
-    // no part
-    auto row_lse = [&](int kvh, int t) {
-      return t * 128 + r < rows ? -a.lse[(size_t)kvh * rows + t * 128 + r] : -INFINITY;
+    bool ok = !bad;
+    const Pass begin = first_pass(a);
+    // -log-sum-exp of row r of a pass's tile; rows that are absent, or beyond
+    // the last, take no part
+    auto row_lse = [&](const Pass& x) {
+      const int row = x.t * 128 + r;
+      return row < rows ? -tree_row_lse(a, x.kvh, row) : -INFINITY;
     };
-    float next = rg.u0 < rg.u1 ? row_lse(rg.u0 / pairs, 0) : 0.f;
-    for (int u = rg.u0; u < rg.u1; ++u) {
-      const int kvh = u / pairs, b = (u - kvh * pairs) * 2 + s;
-      if (b >= a.nb) {                           // an odd last block: no second one
-        if (u + 1 < rg.u1) next = row_lse((u + 1) / pairs, 0);
-        continue;
-      }
-      const bool ctx = b < a.nb_ctx;
-      const int key = ctx ? b * kTreeKeys + r : a.n + (b - a.nb_ctx) * kTreeKeys + r;
-      const bool live = key < (ctx ? a.n : a.n + a.T);
-      const size_t o = (size_t)kvh * a.max_seq + key;
-      const float before = live && ctx && a.w_in ? a.w_in[o] : 0.f;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int t = 0; t < a.tiles; ++t, ++c) {
-        const int buf = c & 1, cols = min(128, rows - t * 128);
-        float* nl = nlse + s * 128;
-        const float x = next;
-        stream_sync(s);                          // the tile before has been read
-        nl[r] = x;
-        const bool some = stream_any(s, x == -INFINITY);
-        // the next tile's, or the next unit's first, ahead of its use
-        if (t + 1 < a.tiles)
-          next = row_lse(kvh, t + 1);
-        else if (u + 1 < rg.u1)
-          next = row_lse((u + 1) / pairs, 0);
-        ok = ok && !tree_flagged(fail) && mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
-        const bool all_ok = __all_sync(0xffffffffu, ok);
-        if (!all_ok) {
+    float next = begin.done() ? 0.f : row_lse(begin);
+    float sums[kSegment / 2];                    // of this stream's blocks of the segment
+    for (Pass x = begin; !x.done(); x.next(a)) {
+      const float mine = next;
+      stream_sync(s);                            // the pass before has been read
+      nl[r] = mine;
+      const bool some = stream_any(s, mine == -INFINITY);
+      Pass y = x;
+      y.next(a);
+      if (!y.done()) next = row_lse(y);
+      const int cols = min(128, rows - x.t * 128);
+      for (int j = s; j < x.cnt; j += 2, ++c) {
+        const int buf = c & 1, b = x.b0 + j;
+        const bool ctx = b < a.nb_ctx;
+        ok = ok && !tree_flagged(fail) &&
+             mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
+        float sum[4] = {x.t ? sums[j >> 1] : 0.f, 0.f, 0.f, 0.f};
+        if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) atomicExch(fail, 1);
           ok = false;
         } else {
@@ -311,12 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               } else {
                 // a tree block: lane e holds the ancestor word of row q0 + e
-                const int row = min(t * 128 + q0 + lane, rows - 1);
-                const uint32_t mine =
+                const int row = min(x.t * 128 + q0 + lane, rows - 1);
+                const uint32_t word =
                     a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                  const uint32_t w = __shfl_sync(0xffffffffu, mine, e);
+                  const uint32_t w = __shfl_sync(0xffffffffu, word, e);
                   const float p = tree_ex2(fmaf(__uint_as_float(v[hlf][e]), scale, nl[q0 + e]));
                   if ((w >> lane) & 1u) sum[e & 3] += p;
                 }
@@ -326,8 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive_cta(&sfree[s * 2 + buf]);
+        const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sums[j >> 1] = total;
+        if (x.t + 1 == a.tiles) {
+          const int key = ctx ? b * kTreeKeys + r : a.n + (b - a.nb_ctx) * kTreeKeys + r;
+          const size_t o = (size_t)x.kvh * a.max_seq + key;
+          if (key < (ctx ? a.n : a.n + a.T))
+            a.w_out[o] = !ok ? NAN : ctx && a.w_in ? a.w_in[o] + total : total;
+        }
       }
-      if (live) a.w_out[o] = ok ? before + ((sum[0] + sum[1]) + (sum[2] + sum[3])) : NAN;
     }
   }
   tc_fence_before();
@@ -351,8 +386,8 @@ cudaError_t launch(const TreeArgs& a, const TreeMaps& m, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
-  const long long units = (long long)a.Hkv * ((a.nb + 1) / 2);
-  lc.gridDim = dim3((unsigned)(units < sms ? units : sms));
+  const long long blocks = (long long)a.Hkv * a.nb;
+  lc.gridDim = dim3((unsigned)(blocks < sms ? blocks : sms));
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = smem;
   lc.stream = st;
