@@ -91,7 +91,36 @@ struct Ring {
   }
 };
 
+// The warp's number as a value that the compiler knows to be the same in all
+// lanes: branches on it keep the warp together.
+SSD_DI int tree_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 SSD_DI bool tree_flagged(const int* f) { return *reinterpret_cast<const volatile int*>(f) != 0; }
+
+SSD_DI bool tree_try(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// Bounded wait for one or two barriers at once (b NULL: one); false if it ran
+// out or the CTA is flagged.
+SSD_DI bool tree_wait(const int* fail, uint64_t* a, uint32_t pa, uint64_t* b = nullptr,
+                      uint32_t pb = 0) {
+  bool da = false, db = b == nullptr;
+  for (int i = 0; i < 1 << 22; ++i) {
+    if (!da) da = tree_try(a, pa);
+    if (!db) db = tree_try(b, pb);
+    if (da && db) return true;
+    if ((i & 63) == 63 && tree_flagged(fail)) return false;
+  }
+  return false;
+}
 
 // 2^x on the special-function unit (relative error about 2^-22).
 SSD_DI float tree_ex2(float x) {
@@ -100,10 +129,40 @@ SSD_DI float tree_ex2(float x) {
   return y;
 }
 
+// Pairs of fp32 values in one instruction, and the maximum of three.
+SSD_DI uint64_t tree_pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+SSD_DI void tree_unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+SSD_DI uint64_t tree_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+SSD_DI uint64_t tree_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SSD_DI float tree_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The matrix instructions are issued by one elected lane of a warp that runs
-// its loop together: the operands are then uniform values, which one lane's
-// own branch would have to move into uniform registers for every instruction
-// (measured: 95 cycles per instruction instead of 64).
+// its loop together (in one lane's own branch an instruction took 95 cycles to
+// issue, of the 64 that it runs).  The matrix pipe holds hardly more than the
+// instruction that runs, so what the warp does between two groups is time
+// lost: about 95 cycles a wait, 42 a commit, 90 a look at the failure flag.
+// Hence waits are joint or early (tree_try), and the flag is looked at only
+// while a wait lasts.  A warp for each stream was no way out (256 nodes over
+// 131000 rows 1145 against 885 us): the streams' products then interleave, and
+// both wait for their softmax at the same time.
 SSD_DI uint32_t tree_elect() {
   uint32_t r;
   asm volatile(

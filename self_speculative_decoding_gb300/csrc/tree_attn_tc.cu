@@ -62,31 +62,6 @@ SSD_DI uint64_t mn_desc(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t idesc_pv(int N) {
   return idesc_bf16(128, N) | (1u << 16);        // B is MN-major
 }
-// Pairs of fp32 values in one instruction, and the maximum of three.
-SSD_DI uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-SSD_DI void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-SSD_DI uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-SSD_DI uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-SSD_DI float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Block range of a unit and its place.
 struct Unit {
   int kvh, item, split, b0, nb;
@@ -408,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 2 * hlf; q < 2 * hlf + 2; ++q)
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
-                mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[q][e]),
+                mx[(e >> 1) & 3] = tree_max3(mx[(e >> 1) & 3], __uint_as_float(sr[q][e]),
                                         __uint_as_float(sr[q][e + 1]));
           }
-          const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+          const float bm = fmaxf(tree_max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
           const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
           if (__any_sync(0xffffffffu, raise)) {
             const float corr = raise ? tree_ex2(m - bm) : 1.f;
@@ -431,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float nm = m == -INFINITY ? 0.f : -m;
-          const uint64_t sc2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
-          const uint64_t nm2 = pack2(__float_as_uint(nm), __float_as_uint(nm));
+          const uint64_t sc2 = tree_pack2(__float_as_uint(scale), __float_as_uint(scale));
+          const uint64_t nm2 = tree_pack2(__float_as_uint(nm), __float_as_uint(nm));
           uint64_t ls2[2] = {0, 0};              // pairs of partial sums
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -448,16 +423,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float p0, p1;
-              unpack2(fma2(pack2(sr[q][2 * e], sr[q][2 * e + 1]), sc2, nm2), p0, p1);
+              tree_unpack2(tree_fma2(tree_pack2(sr[q][2 * e], sr[q][2 * e + 1]), sc2, nm2), p0, p1);
               p0 = tree_ex2(p0);
               p1 = tree_ex2(p1);
-              ls2[e & 1] = add2(ls2[e & 1], pack2(__float_as_uint(p0), __float_as_uint(p1)));
+              ls2[e & 1] = tree_add2(ls2[e & 1], tree_pack2(__float_as_uint(p0), __float_as_uint(p1)));
               pk[e] = pack_bf16x2(p0, p1);
             }
             tmem_st16(trow + col_s + q * 16, pk);
           }
           float l0, l1;
-          unpack2(add2(ls2[0], ls2[1]), l0, l1);
+          tree_unpack2(tree_add2(ls2[0], ls2[1]), l0, l1);
           l += l0 + l1;
           tmem_wait_st();
         }
@@ -681,7 +656,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   else if (COLUMNS)
     join_column<DH>(a, blockIdx.x);
   else
-    tree_join_rows<DH>(a, blockIdx.x);
+    tree_join_rows<DH>(a, blockIdx.x, threadIdx.x >> 5);
 }
 
 template <int DH, bool TWO>

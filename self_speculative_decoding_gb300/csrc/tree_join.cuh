@@ -44,27 +44,28 @@ SSD_DI float tree_row_lse(const TreeArgs& a, int kvh, int row) {
   const int per = a.two ? a.items * 2 : 1;
   const size_t s0 = ((size_t)kvh * a.splits * per + (a.two ? row >> 7 : 0)) * 128 + (row & 127);
   float m = -INFINITY, l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[s0 + (size_t)i * per * 128]);
   const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < a.splits; ++i)
     l = fmaf(a.part_l[s0 + (size_t)i * per * 128], exp2f(a.part_m[s0 + (size_t)i * per * 128] - base), l);
   return l != 0.f && a.depth[row / a.G] >= 0 ? m + log2f(l) : INFINITY;
 }
 
-// Joins of 32 rows each, eight warps: lane = row, each warp an eighth of the
-// columns (whole 16- or 32-byte sectors per row); the slots are added in order.
+// Joins of 32 rows each by eight parts of a warp: lane = row, each part an
+// eighth of the columns (whole 16- or 32-byte sectors per row); the slots are
+// added in order.
 constexpr int kJoinWarps = 8;
 SSD_DI int tree_joins(const TreeArgs& a) { return (a.T * a.G + 31) / 32 * a.Hkv; }
 
 template <int DH>
-SSD_DI void tree_join_rows(const TreeArgs& a, int index) {
-  constexpr int kChunks = DH / 4 / kJoinWarps;   // 16-byte columns per warp
-  const int warp = (threadIdx.x >> 5) & (kJoinWarps - 1), lane = threadIdx.x & 31;
+SSD_DI void tree_join_rows(const TreeArgs& a, int index, int part) {
+  constexpr int kChunks = DH / 4 / kJoinWarps;   // 16-byte columns per part
+  const int lane = threadIdx.x & 31;
   const int rows = a.T * a.G, blocks = (rows + 31) / 32;
   const int kvh = index / blocks, row0 = (index - kvh * blocks) * 32;
-  const int row = min(row0 + lane, rows - 1), c0 = warp * kChunks;
+  const int row = min(row0 + lane, rows - 1), c0 = part * kChunks;
   const int tile = row >> 7, r = row & 127, t = row / a.G;
   const int per = a.two ? a.items * 2 : 1;       // slots per (head, split)
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);

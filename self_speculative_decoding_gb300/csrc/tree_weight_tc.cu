@@ -13,9 +13,9 @@
 // zigzag over the pairs, so that a new segment starts with the planes that are
 // there.  (With one tile per pass, 64 nodes of 64 / 8 heads over 32768 rows
 // took 62 us, waiting for K: 3 blocks in flight arrive at 19 bytes per cycle
-// and SM.)  The softmax warps first join the attention's partial results, so
+// and SM.)  Four more warps join the attention's partial results meanwhile, so
 // that no kernel runs between.
-// Warp 8: TMA copies, warp 9: MMA.  Waits are bounded; one that gives up makes
+// Warp 8: TMA copies, warp 9: the products.  Waits are bounded; one that gives up makes
 // the CTA's weights NaN.
 #include "tc_dev.cuh"
 #include "tree.cuh"
@@ -26,7 +26,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
 constexpr int kPolls = 1 << 22;
 constexpr int kRegion = 128 * 128;
 constexpr int kTileSmem = 224 * 1024;            // Q tiles (hi, lo), then the ring of K blocks
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + kMaxStages;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + kMaxStages);
   int* fail = reinterpret_cast<int*>(tslot + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tree_warp(), lane = tid & 31;
   const int rows = a.T * a.G;
   const int planes = a.tiles > 1 ? 4 : 2;        // of the pass's tiles: low, high, low, high
   const int stages = min(kMaxStages, kTileSmem / kItem - planes);
@@ -189,8 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cs[2] = {0, 0};                          // score tiles per stream
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t ph) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, ph, kPolls));
-      tc_fence_after();
+      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, bar, ph));
     };
     Pass before = first_pass(a);
     for (Pass x = before; ok && !x.over();) {
@@ -204,13 +203,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (!ok || j + s >= x.cnt) continue;
-          wait(&full[slot], phase);
           const uint32_t kb = ra + (uint32_t)slot * kItem;
-          for (int t = 0; ok && t < tiles; ++t) {
+          for (int t = 0; t < tiles; ++t) {
             const int buf = cs[s] & 1;
-            if (cs[s] >= 2) wait(&sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1));
-            ok = __all_sync(0xffffffffu, ok && !tree_flagged(fail));
-            if (!ok) continue;
+            // the score tile has been read (and, first, the block has landed)
+            uint64_t* there = t == 0 ? &full[slot] : nullptr;
+            if (cs[s] >= 2)
+              ok = __all_sync(0xffffffffu,
+                              tree_wait(fail, &sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1),
+                                        there, phase));
+            else if (there)
+              wait(there, phase);
+            tc_fence_after();
+            if (!ok) break;
             const int cols = min(128, (rows - (x.pair() * 2 + t) * 128 + 15) / 16 * 16);
             const uint32_t id = idesc_bf16(128, cols);
             const uint32_t acc = tm + (uint32_t)(s * 256 + buf * 128);
@@ -239,15 +244,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) atomicExch(fail, 1);
     tree_commit(lead, mdone);
     mbar_wait_n(mdone, 0u, kPolls);
+  } else if (warp > 9) {
+    pdl_wait();
+    if (a.splits > 1)
+      for (int i = blockIdx.x; i < tree_joins(a); i += gridDim.x)
+        for (int part = warp - 10; part < kJoinWarps; part += 4) tree_join_rows<DH>(a, i, part);
   } else {
     // one key per thread.  Every thread passes every barrier: a wait that
     // gives up only turns the sums into NaN.
     pdl_wait();
-    if (a.splits > 1)
-      for (int i = blockIdx.x; i < tree_joins(a); i += gridDim.x) tree_join_rows<DH>(a, i);
     const int s = warp >> 2, r = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)s * 256;
     const float scale = a.scale_log2;
+    const uint64_t sc2 = tree_pack2(__float_as_uint(scale), __float_as_uint(scale));
     const bool bad = *a.err != 0;
     int c = 0;
     bool ok = !bad;
@@ -270,9 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = s; j < x.cnt; j += 2) {
         const int b = x.b0 + j;
         const bool ctx = b < a.nb_ctx;
-        float sum[4] = {x.first() ? 0.f : sums[j >> 1], 0.f, 0.f, 0.f};
+        // pairs of partial sums
+        uint64_t sum[2] = {x.first() ? 0 : (uint64_t)__float_as_uint(sums[j >> 1]), 0};
         for (int t = 0; t < tiles; ++t, ++c) {
-          const int buf = c & 1, cols = min(128, rows - (x.pair() * 2 + t) * 128);
+          const int buf = c & 1, row0 = (x.pair() * 2 + t) * 128, cols = min(128, rows - row0);
           const float* nl = nlse + t * 128;
           ok = ok && !tree_flagged(fail) &&
                mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
@@ -281,58 +291,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
           } else {
             tc_fence_after();
-#pragma unroll 1
-            for (int q = 0; q < cols; q += 64) {
-              uint32_t v[2][32];
-              tmem_ld32_nw(trow + (uint32_t)(buf * 128 + q), v[0]);
-              if (q + 32 < cols) tmem_ld32_nw(trow + (uint32_t)(buf * 128 + q + 32), v[1]);
-              tmem_wait_ld();
-              tmem_pin32(v[0]);
-              tmem_pin32(v[1]);
+            // 32 columns are summed while the next 32 load
+            const uint32_t col = trow + (uint32_t)(buf * 128);
+            uint32_t v[2][32];
+            tmem_ld32_nw(col, v[0]);
+            tmem_wait_ld();
+            tmem_pin32(v[0]);
 #pragma unroll
-              for (int hlf = 0; hlf < 2; ++hlf) {
-                if (q + hlf * 32 >= cols) break;
-                const int q0 = q + hlf * 32;
-                if (some) {
-                  // a row without part may meet inf or NaN among the keys: its
-                  // score is made 0, and its 2^(0 - inf) is 0
+            for (int q = 0; q < 4; ++q) {
+              if (q * 32 >= cols) break;
+              uint32_t(&w)[32] = v[q & 1];
+              const bool more = q < 3 && q * 32 + 32 < cols;
+              if (more) tmem_ld32_nw(col + (uint32_t)(q * 32 + 32), v[(q + 1) & 1]);
+              if (some) {
+                // a row without part may meet inf or NaN among the keys: its
+                // score is made 0, and its 2^(0 - inf) is 0
 #pragma unroll
-                  for (int e = 0; e < 32; e += 4) {
-                    const float4 n4 = *reinterpret_cast<const float4*>(nl + q0 + e);
-                    if (n4.x == -INFINITY) v[hlf][e] = 0u;
-                    if (n4.y == -INFINITY) v[hlf][e + 1] = 0u;
-                    if (n4.z == -INFINITY) v[hlf][e + 2] = 0u;
-                    if (n4.w == -INFINITY) v[hlf][e + 3] = 0u;
-                  }
+                for (int e = 0; e < 32; ++e)
+                  if (nl[q * 32 + e] == -INFINITY) w[e] = 0u;
+              }
+              if (ctx) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const ulonglong2 n4 = *reinterpret_cast<const ulonglong2*>(nl + q * 32 + e);
+                  float p0, p1, p2, p3;
+                  tree_unpack2(tree_fma2(tree_pack2(w[e], w[e + 1]), sc2, n4.x), p0, p1);
+                  tree_unpack2(tree_fma2(tree_pack2(w[e + 2], w[e + 3]), sc2, n4.y), p2, p3);
+                  sum[0] = tree_add2(sum[0], tree_pack2(__float_as_uint(tree_ex2(p0)),
+                                                        __float_as_uint(tree_ex2(p1))));
+                  sum[1] = tree_add2(sum[1], tree_pack2(__float_as_uint(tree_ex2(p2)),
+                                                        __float_as_uint(tree_ex2(p3))));
                 }
-                if (ctx) {
+              } else {
+                // a tree block: lane e holds the ancestor word of row e
+                const int row = min(row0 + q * 32 + lane, rows - 1);
+                const uint32_t word =
+                    a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
+                float part = 0.f;
 #pragma unroll
-                  for (int e = 0; e < 32; e += 4) {
-                    const float4 n4 = *reinterpret_cast<const float4*>(nl + q0 + e);
-                    sum[0] += tree_ex2(fmaf(__uint_as_float(v[hlf][e]), scale, n4.x));
-                    sum[1] += tree_ex2(fmaf(__uint_as_float(v[hlf][e + 1]), scale, n4.y));
-                    sum[2] += tree_ex2(fmaf(__uint_as_float(v[hlf][e + 2]), scale, n4.z));
-                    sum[3] += tree_ex2(fmaf(__uint_as_float(v[hlf][e + 3]), scale, n4.w));
-                  }
-                } else {
-                  // a tree block: lane e holds the ancestor word of row q0 + e
-                  const int row = min((x.pair() * 2 + t) * 128 + q0 + lane, rows - 1);
-                  const uint32_t word =
-                      a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    const uint32_t w = __shfl_sync(0xffffffffu, word, e);
-                    const float p = tree_ex2(fmaf(__uint_as_float(v[hlf][e]), scale, nl[q0 + e]));
-                    if ((w >> lane) & 1u) sum[e & 3] += p;
-                  }
+                for (int e = 0; e < 32; ++e) {
+                  const uint32_t bits = __shfl_sync(0xffffffffu, word, e);
+                  const float p = tree_ex2(fmaf(__uint_as_float(w[e]), scale, nl[q * 32 + e]));
+                  if ((bits >> lane) & 1u) part += p;
                 }
+                sum[0] = tree_add2(sum[0], (uint64_t)__float_as_uint(part));
+              }
+              if (more) {
+                tmem_wait_ld();
+                tmem_pin32(v[(q + 1) & 1]);
               }
             }
           }
           tc_fence_before();
           mbar_arrive_cta(&sfree[s * 2 + buf]);
         }
-        const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        tree_unpack2(tree_add2(sum[0], sum[1]), s0, s1);
+        const float total = s0 + s1;
         sums[j >> 1] = total;
         if (x.last()) {
           const int key = ctx ? b * kTreeKeys + r : a.n + (b - a.nb_ctx) * kTreeKeys + r;
