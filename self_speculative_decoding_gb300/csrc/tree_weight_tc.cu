@@ -8,8 +8,10 @@
 // A CTA has a run of key blocks, taken in segments of up to 32.  A pass goes
 // over a segment with a pair of row tiles (or the only one): their planes (q's
 // low and high part) stay in shared memory while the K blocks stream, in turn
-// to two streams of four warps, each block against both tiles; the sums of a
-// segment's keys stay with their threads until every pair has passed.  Passes
+// to two streams of four warps, each block against both tiles at once (256
+// columns to an instruction: twice the time of 128, which covers what the
+// issuing warp does between two groups); the sums of a segment's keys stay
+// with their threads until every pair has passed.  Passes
 // zigzag over the pairs, so that a new segment starts with the planes that are
 // there.  (With one tile per pass, 64 nodes of 64 / 8 heads over 32768 rows
 // took 62 us, waiting for K: 3 blocks in flight arrive at 19 bytes per cycle
@@ -26,7 +28,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 384;
 constexpr int kPolls = 1 << 22;
 constexpr int kRegion = 128 * 128;
 constexpr int kTileSmem = 224 * 1024;            // Q tiles (hi, lo), then the ring of K blocks
@@ -86,6 +88,34 @@ SSD_DI Pass first_pass(const TreeArgs& a) {
   return p;
 }
 
+// Sum over `cols` score columns (rows row0 ..) of a key's 2^(s c - lse), of the
+// rows that take part (another one may meet inf or NaN) and, in a tree block
+// (word >= 0), that see the key.  Apart from the plain sum: conditions within
+// its loop became selections on every column, and 256 columns took 4200 cycles.
+__device__ __noinline__ float masked_columns(const TreeArgs& a, uint32_t col, const float* nlse,
+                                             int row0, int cols, int word) {
+  const int lane = threadIdx.x & 31, rows = a.T * a.G;
+  float part = 0.f;
+  for (int q = 0; q < cols; q += 32) {
+    uint32_t w[32];
+    tmem_ld32_nw(col + (uint32_t)q, w);
+    // lane e: the ancestor word of row e (a context key is seen by all)
+    const int row = row0 + q + lane;
+    uint32_t mine = ~0u;
+    if (word >= 0)
+      mine = row < rows ? a.anc[(size_t)(row / a.G) * a.anc_words + word] : 0u;
+    tmem_wait_ld();
+    tmem_pin32(w);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const uint32_t bits = __shfl_sync(0xffffffffu, mine, e);
+      const float n = nlse[q + e], p = tree_ex2(fmaf(__uint_as_float(w[e]), a.scale_log2, n));
+      if (((bits >> lane) & 1u) && n != -INFINITY) part += p;
+    }
+  }
+  return part;
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_weight_tc_kernel(const __grid_constant__ CUtensorMap mK,
@@ -109,8 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tree_warp(), lane = tid & 31;
   const int rows = a.T * a.G;
-  const int planes = a.tiles > 1 ? 4 : 2;        // of the pass's tiles: low, high, low, high
+  const int planes = a.tiles > 1 ? 4 : 2;        // of the pass's one or two tiles
   const int stages = min(kMaxStages, kTileSmem / kItem - planes);
+  const int bufs = a.tiles > 1 ? 1 : 2;          // of a stream's 256 score columns
   unsigned char* ring = sm + planes * kItem;
 
   if (tid == 0) {
@@ -147,11 +178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++sent;
           mbar_arrive_expect_tx(qfull, (uint32_t)(planes * kItem));
-          for (int i = 0; i < planes; ++i)       // (a tile beyond the last: rows of no use)
+          // [plane][64 columns][row of the pair] (beyond the last: of no use)
+          for (int p = 0; p < 2; ++p)
             for (int r = 0; r < kRegs; ++r)
-              tma_load_3d(sm + i * kItem + r * kRegion, &mW, r * 64,
-                          ((1 - (i & 1)) * a.Hkv + x.kvh) * rows + (x.pair() * 2 + (i >> 1)) * 128, 0,
-                          qfull);
+              for (int t = 0; t < planes / 2; ++t)
+                tma_load_3d(sm + ((p * kRegs + r) * (planes / 2) + t) * kRegion, &mW, r * 64,
+                            ((1 - p) * a.Hkv + x.kvh) * rows + (x.pair() * 2 + t) * 128, 0, qfull);
         }
         before = x;
         for (int j = 0; ok && j < x.cnt; ++j) {
@@ -184,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lead = tree_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);
+    const uint32_t qregion = (uint32_t)(planes / 2) * kRegion;
     int slot = 0, loads = 0;
     uint32_t phase = 0;
     int cs[2] = {0, 0};                          // score tiles per stream
@@ -198,40 +231,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++loads;
       }
       before = x;
-      const int tiles = min(2, a.tiles - x.pair() * 2);
+      const int cols = min(256, rows - x.pair() * 256);
+      const uint32_t id = idesc_bf16(128, (cols + 15) / 16 * 16);
       for (int j = 0; ok && j < x.cnt; j += 2) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (!ok || j + s >= x.cnt) continue;
+          // the block has landed and the stream's score columns have been read
+          const int buf = cs[s] % bufs, use = cs[s] / bufs;
+          if (use > 0)
+            ok = __all_sync(0xffffffffu, tree_wait(fail, &sfree[s * 2 + buf], (uint32_t)((use - 1) & 1),
+                                                   &full[slot], phase));
+          else
+            wait(&full[slot], phase);
+          tc_fence_after();
+          if (!ok) continue;
           const uint32_t kb = ra + (uint32_t)slot * kItem;
-          for (int t = 0; t < tiles; ++t) {
-            const int buf = cs[s] & 1;
-            // the score tile has been read (and, first, the block has landed)
-            uint64_t* there = t == 0 ? &full[slot] : nullptr;
-            if (cs[s] >= 2)
-              ok = __all_sync(0xffffffffu,
-                              tree_wait(fail, &sfree[s * 2 + buf], (uint32_t)((cs[s] / 2 - 1) & 1),
-                                        there, phase));
-            else if (there)
-              wait(there, phase);
-            tc_fence_after();
-            if (!ok) break;
-            const int cols = min(128, (rows - (x.pair() * 2 + t) * 128 + 15) / 16 * 16);
-            const uint32_t id = idesc_bf16(128, cols);
-            const uint32_t acc = tm + (uint32_t)(s * 256 + buf * 128);
-            const uint32_t qb = qa + (uint32_t)(2 * t) * kItem;
+          const uint32_t acc = tm + (uint32_t)(s * 256 + buf * 128);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)          // the low part first
+          for (int p = 0; p < 2; ++p)            // the low part first
 #pragma unroll
-              for (int ks = 0; ks < DH / 16; ++ks) {
-                const uint32_t o = (uint32_t)(ks >> 2) * kRegion;
-                tree_mma_ss(lead, acc, sw128_desc(kb + o) + 2 * (ks & 3),
-                            sw128_desc(qb + p * kItem + o) + 2 * (ks & 3), id, (p || ks > 0) ? 1u : 0u);
-              }
-            tree_commit(lead, &sfull[s * 2 + buf]);
-            ++cs[s];
-          }
+            for (int ks = 0; ks < DH / 16; ++ks) {
+              const uint32_t rg = (uint32_t)(ks >> 2);
+              tree_mma_ss(lead, acc, sw128_desc(kb + rg * kRegion) + 2 * (ks & 3),
+                          sw128_desc(qa + (p * kRegs + rg) * qregion) + 2 * (ks & 3), id,
+                          (p || ks > 0) ? 1u : 0u);
+            }
+          tree_commit(lead, &sfull[s * 2 + buf]);
           tree_commit(lead, &empty[slot]);
+          ++cs[s];
           if (++slot == stages) {
             slot = 0;
             phase ^= 1u;
@@ -247,16 +275,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp > 9) {
     pdl_wait();
     if (a.splits > 1)
-      for (int i = blockIdx.x; i < tree_joins(a); i += gridDim.x)
-        for (int part = warp - 10; part < kJoinWarps; part += 4) tree_join_rows<DH>(a, i, part);
+      for (int i = blockIdx.x + gridDim.x * (warp - 10); i < tree_joins(a) * kJoinWarps;
+           i += gridDim.x * (kThreads / 32 - 10))
+        tree_join_rows<DH>(a, i / kJoinWarps, i % kJoinWarps);
   } else {
     // one key per thread.  Every thread passes every barrier: a wait that
     // gives up only turns the sums into NaN.
     pdl_wait();
     const int s = warp >> 2, r = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)s * 256;
-    const float scale = a.scale_log2;
-    const uint64_t sc2 = tree_pack2(__float_as_uint(scale), __float_as_uint(scale));
+    const uint64_t sc2 = tree_pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
     const bool bad = *a.err != 0;
     int c = 0;
     bool ok = !bad;
@@ -272,79 +300,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (!x.over()) {
       streams_sync();                            // the pass before has been read
       nlse[tid] = next;
-      const int tiles = min(2, a.tiles - x.pair() * 2);
-      const bool some = streams_any(next == -INFINITY && tid < tiles * 128);
+      const int cols = min(256, rows - x.pair() * 256);
+      // (one tile has 128 columns, all of which count when the last 32 are read)
+      const bool some = streams_any(next == -INFINITY && tid < (cols + 31) / 32 * 32);
       const Pass y = x.next(a);
       if (!y.over()) next = row_lse(y);
-      for (int j = s; j < x.cnt; j += 2) {
-        const int b = x.b0 + j;
+      for (int j = s; j < x.cnt; j += 2, ++c) {
+        const int b = x.b0 + j, buf = c % bufs, use = c / bufs;
         const bool ctx = b < a.nb_ctx;
         // pairs of partial sums
         uint64_t sum[2] = {x.first() ? 0 : (uint64_t)__float_as_uint(sums[j >> 1]), 0};
-        for (int t = 0; t < tiles; ++t, ++c) {
-          const int buf = c & 1, row0 = (x.pair() * 2 + t) * 128, cols = min(128, rows - row0);
-          const float* nl = nlse + t * 128;
-          ok = ok && !tree_flagged(fail) &&
-               mbar_wait_n(&sfull[s * 2 + buf], (uint32_t)((c >> 1) & 1), kPolls);
-          if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) atomicExch(fail, 1);
-            ok = false;
-          } else {
-            tc_fence_after();
-            // 32 columns are summed while the next 32 load
-            const uint32_t col = trow + (uint32_t)(buf * 128);
-            uint32_t v[2][32];
-            tmem_ld32_nw(col, v[0]);
-            tmem_wait_ld();
-            tmem_pin32(v[0]);
+        ok = ok && tree_wait(fail, &sfull[s * 2 + buf], (uint32_t)(use & 1));
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) atomicExch(fail, 1);
+          ok = false;
+        } else {
+          tc_fence_after();
+          const uint32_t col = trow + (uint32_t)(buf * 128);
+          if (ctx && !some) {
+            // (a short loop: unrolled over 64 or 128 columns, with the next ones
+            // loading meanwhile, it was slower by 2 to 25 us on 64 nodes over
+            // 32768 rows)
+            auto add = [&](uint32_t(&w)[32], int q) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (q * 32 >= cols) break;
-              uint32_t(&w)[32] = v[q & 1];
-              const bool more = q < 3 && q * 32 + 32 < cols;
-              if (more) tmem_ld32_nw(col + (uint32_t)(q * 32 + 32), v[(q + 1) & 1]);
-              if (some) {
-                // a row without part may meet inf or NaN among the keys: its
-                // score is made 0, and its 2^(0 - inf) is 0
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (nl[q * 32 + e] == -INFINITY) w[e] = 0u;
+              for (int e = 0; e < 32; e += 4) {
+                const ulonglong2 n4 = *reinterpret_cast<const ulonglong2*>(nlse + q + e);
+                float p0, p1, p2, p3;
+                tree_unpack2(tree_fma2(tree_pack2(w[e], w[e + 1]), sc2, n4.x), p0, p1);
+                tree_unpack2(tree_fma2(tree_pack2(w[e + 2], w[e + 3]), sc2, n4.y), p2, p3);
+                sum[0] = tree_add2(sum[0], tree_pack2(__float_as_uint(tree_ex2(p0)),
+                                                      __float_as_uint(tree_ex2(p1))));
+                sum[1] = tree_add2(sum[1], tree_pack2(__float_as_uint(tree_ex2(p2)),
+                                                      __float_as_uint(tree_ex2(p3))));
               }
-              if (ctx) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const ulonglong2 n4 = *reinterpret_cast<const ulonglong2*>(nl + q * 32 + e);
-                  float p0, p1, p2, p3;
-                  tree_unpack2(tree_fma2(tree_pack2(w[e], w[e + 1]), sc2, n4.x), p0, p1);
-                  tree_unpack2(tree_fma2(tree_pack2(w[e + 2], w[e + 3]), sc2, n4.y), p2, p3);
-                  sum[0] = tree_add2(sum[0], tree_pack2(__float_as_uint(tree_ex2(p0)),
-                                                        __float_as_uint(tree_ex2(p1))));
-                  sum[1] = tree_add2(sum[1], tree_pack2(__float_as_uint(tree_ex2(p2)),
-                                                        __float_as_uint(tree_ex2(p3))));
-                }
-              } else {
-                // a tree block: lane e holds the ancestor word of row e
-                const int row = min(row0 + q * 32 + lane, rows - 1);
-                const uint32_t word =
-                    a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (warp & 3)];
-                float part = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const uint32_t bits = __shfl_sync(0xffffffffu, word, e);
-                  const float p = tree_ex2(fmaf(__uint_as_float(w[e]), scale, nl[q * 32 + e]));
-                  if ((bits >> lane) & 1u) part += p;
-                }
-                sum[0] = tree_add2(sum[0], (uint64_t)__float_as_uint(part));
-              }
-              if (more) {
-                tmem_wait_ld();
-                tmem_pin32(v[(q + 1) & 1]);
-              }
+            };
+#pragma unroll 1
+            for (int q = 0; q < cols; q += 32) {
+              uint32_t v0[32];
+              tmem_ld32_nw(col + (uint32_t)q, v0);
+              tmem_wait_ld();
+              tmem_pin32(v0);
+              add(v0, q);
             }
+          } else {
+            const float part = masked_columns(a, col, nlse, x.pair() * 256, cols,
+                                              ctx ? -1 : (b - a.nb_ctx) * 4 + (warp & 3));
+            sum[0] = tree_add2(sum[0], (uint64_t)__float_as_uint(part));
           }
-          tc_fence_before();
-          mbar_arrive_cta(&sfree[s * 2 + buf]);
         }
+        tc_fence_before();
+        mbar_arrive_cta(&sfree[s * 2 + buf]);
         float s0, s1;
         tree_unpack2(tree_add2(sum[0], sum[1]), s0, s1);
         const float total = s0 + s1;
