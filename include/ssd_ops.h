@@ -175,8 +175,8 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * weight_out (fp32 [Hkv][max_seq], nullable): the attention weight that each
  * key received, summed over the present rows and the query heads of its
  * group: rows j < n_ctx get weight_in[j] (fp32 [Hkv][max_seq]; NULL: zeros;
- * may be weight_out itself) plus this call's sum, rows n_ctx..n_ctx+T-1 this
- * call's sum alone; other rows stay as they are.
+ * may be weight_out itself, no other overlap) plus this call's sum, rows
+ * n_ctx..n_ctx+T-1 this call's sum alone; other rows stay as they are.
  * Scores keep fp32 accuracy (q is split into two bf16 parts); probabilities
  * are rounded to bf16 for the product with V.  The result of a call does not
  * depend on timing (no floating-point atomics). */

@@ -456,6 +456,8 @@ class _Ops:
             with torch.cuda.device(dev):
                 return self.tree_attention(qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv, dh,
                                            theta, weights, weights_out, out)
+        if qkv.dim() != 2 or k_cache.dim() != 3:
+            raise ValueError("expected qkv [T, (H + 2 Hkv) dh] and k_cache [Hkv, max_seq, dh]")
         T, max_seq = qkv.shape[0], k_cache.shape[1]
         cache, per_key = (Hkv, max_seq, dh), (Hkv, max_seq)
         args = (self._arg(qkv, "qkv", torch.float32, (T, (H + 2 * Hkv) * dh), dev),
@@ -486,8 +488,8 @@ class _Ops:
         weights fp32 [Hkv, max_seq].  Returns the kept rows, int32
         [Hkv, keep]."""
         dt = k.dtype
-        if dt not in self.CACHE_DTYPES or k.dim() != 3:
-            raise ValueError("k: expected a bf16 or fp32 tensor [Hkv, max_seq, dh]")
+        if dt not in self.CACHE_DTYPES or k.dim() != 3 or k_out.dim() != 3:
+            raise ValueError("k, k_out: expected bf16 or fp32 tensors [Hkv, rows, dh]")
         dev = k.get_device()
         if dev >= 0 and dev != _current_device():
             with torch.cuda.device(dev):

@@ -459,6 +459,10 @@ ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32
     return op_fail(SSD_ERR_INVALID_ARG, "tree_attention pointers");
   if ((weight_in && (!weight_out || !al4(weight_in))) || (weight_out && !al4(weight_out)))
     return op_fail(SSD_ERR_INVALID_ARG, "tree_attention: weight_in needs weight_out");
+  const size_t per_key = (size_t)4 * Hkv * max_seq, cache = per_key / 2 * dh;
+  if (overlap(k_cache, cache, v_cache, cache) ||
+      (weight_in && weight_in != weight_out && overlap(weight_in, per_key, weight_out, per_key)))
+    return op_fail(SSD_ERR_INVALID_ARG, "tree_attention: buffers overlap");
   TreeArgs a;
   tree_sizes(a, T, n_ctx, H, Hkv, dh);
   a.w_out = weight_out;

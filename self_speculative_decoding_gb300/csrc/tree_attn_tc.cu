@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ---- products: the warp runs together, one lane issues
     const uint32_t tmem = set_up();
+    pdl_wait();                                  // bounded waits begin after it
     const uint32_t lead = tree_elect();
     constexpr uint32_t ids = idesc_bf16(128, 128), idp = idesc_pv(DH);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);

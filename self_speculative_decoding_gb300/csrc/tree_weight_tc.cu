@@ -212,7 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sent) mbar_wait_n(qfull, (uint32_t)((sent - 1) & 1), kPolls);
     }
   } else if (warp == 9) {
-    // the warp runs together, one lane issues
+    // the warp runs together, one lane issues.  (A CTA may start while the
+    // attention still runs, for as long as that takes: bounded waits begin after
+    // the wait for it.)
+    pdl_wait();
     const uint32_t lead = tree_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t qa = smem_addr(sm), ra = smem_addr(ring);

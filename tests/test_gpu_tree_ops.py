@@ -243,6 +243,42 @@ def test_offsets_beyond_32_bits(ops):
     assert (out.float() - 1).abs().max().item() < 0.02
 
 
+@pytest.mark.parametrize("H,Hkv,dh,n,T", [(8, 1, 64, 700_001, 70), (16, 2, 128, 300_000, 40),
+                                          (4, 4, 128, 60_000, 7)])
+def test_long_contexts(ops, H, Hkv, dh, n, T):
+    # long enough that a CTA has several runs of keys and passes over them;
+    # the reference is the same formula as torch operations in 64 bits
+    g = torch.Generator(device="cuda").manual_seed(n)
+    G, S = H // Hkv, n + T
+    parents = [-1] + [i - 1 - (5 * i) % min(i, 4) for i in range(1, T)]
+    qkv = torch.randn(T, (H + 2 * Hkv) * dh, generator=g, device="cuda")
+    k = torch.randn(Hkv, S, dh, generator=g, device="cuda").bfloat16()
+    v = torch.randn(Hkv, S, dh, generator=g, device="cuda").bfloat16()
+    w = torch.zeros(Hkv, S, device="cuda")
+    out = ops.tree_attention(qkv, torch.tensor(parents, dtype=torch.int32).cuda(), k, v, n, n, H,
+                             Hkv, dh, 1e4, weights_out=w).double().view(T, H, dh)
+    q, _, _ = O.tree_rows(qkv.double().cpu().numpy(), parents, n, H, Hkv, dh, 1e4)
+    q = torch.from_numpy(q).cuda()
+    seen = torch.ones(T, S, dtype=torch.bool, device="cuda")
+    for t, path in enumerate(O.tree_paths(parents)):
+        seen[t, n:] = False
+        seen[t, [n + i for i in path]] = True
+    for kvh in range(Hkv):
+        rows = q[:, kvh * G:(kvh + 1) * G].reshape(T * G, dh)
+        K, V = k[kvh].double(), v[kvh].double()
+        size = (rows.abs() @ K.abs().T).amax().item()
+        d = (2.0 ** -16 + 2 * dh * 2.0 ** -24) * size / np.sqrt(dh) + 1e-6
+        s = (rows @ K.T / np.sqrt(dh)).masked_fill_(~seen.repeat_interleave(G, 0), float("-inf"))
+        p = torch.softmax(s, dim=1)
+        ref = (p @ V).view(T, G, dh)
+        spread = (p @ V.abs()).view(T, G, dh)
+        err = (out[:, kvh * G:(kvh + 1) * G] - ref).abs()
+        assert (err <= U * ref.abs() + (U + 2 * d) * spread).all()
+        mass = p.sum(0)
+        err = (w[kvh].double() - mass).abs()
+        assert (err <= 2 * d * mass + (T * G + 2) * 2.0 ** -24 * mass + 1e-12).all()
+
+
 def test_graphs_and_streams(ops):
     c, d = Case(8, 2, 128, 500, 30), Case(8, 2, 128, 900, 12, seed=3)
     want_c, want_d = c.call(ops), d.call(ops)
@@ -378,6 +414,11 @@ def test_select_ties_specials_and_sorted_rows(ops):
     check_select(ops, z, zero, W, np.array([0, np.inf, -np.inf, np.nan, 3, 4], np.float32))
     check_select(ops, z, np.full(B, -np.inf, np.float32), W, None, np.ones(B, np.int32), 3)
     check_select(ops, z, np.array([-1, -1, -5, 0, 2, 2], np.float32), W, None, np.ones(B, np.int32), 3)
+    # thousands of equal scores: ties go to the lower beam, then the lower token
+    flat = np.zeros((40, 9001), np.float32)
+    check_select(ops, flat, np.zeros(40, np.float32), 40)
+    check_select(ops, flat, (np.arange(40) // 2).astype(np.float32), 256)
+    check_select(ops, flat[:, :3], np.zeros(40, np.float32), 200)
 
 
 def test_select_reads_odd_rows_and_strided_lse(ops):
@@ -446,6 +487,38 @@ def test_reorder_beyond_32_bits(ops):
     ko[:, :, S - 4:] = 50
     ops.beam_reorder(k, None, torch.tensor([3, 1], dtype=torch.int32).cuda(), S - 3, S, ko, None)
     assert (ko[0, :, S - 3:] == 3).all() and (ko[1, :, S - 3:] == 1).all() and (ko[:, :, S - 4] == 50).all()
+
+
+def test_eviction_selection_and_reordering_in_a_graph(ops):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(4, 9000, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = torch.rand(4, 9000, generator=g, device="cuda")
+    ko, vo, wo = torch.zeros(4, 700, 64, device="cuda").bfloat16(), torch.zeros(4, 700, 64, device="cuda").bfloat16(), torch.zeros(4, 700, device="cuda")
+    z, sc = torch.randn(12, 40000, generator=g, device="cuda"), torch.zeros(12, device="cuda")
+    bk = torch.randn(12, 3, 50, 64, generator=g, device="cuda")
+    bo = torch.zeros(5, 3, 50, 64, device="cuda")
+
+    def step():
+        kept = ops.cache_evict(k, v, w, 8999, 700, ko, vo, wo, sinks=3, recent=50)
+        tok, par, best, _ = ops.beam_select(z, sc, 5)
+        ops.beam_reorder(bk, None, par, 7, 43, bo, None)
+        return kept, tok, par, best
+
+    want = [t.clone() for t in step()] + [t.clone() for t in (ko, vo, wo, bo)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in (*got, ko, vo, wo, bo):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*got, ko, vo, wo, bo), want))
+    w.mul_(-1)                                     # other inputs of the same graph
+    graph.replay()
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(got[0].cpu().numpy(), O.cache_evict(w.cpu().numpy(), 8999, 700, 3, 50))
 
 
 # --------------------------------------------------------------------------

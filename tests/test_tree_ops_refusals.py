@@ -15,7 +15,7 @@ def lib():
     return _abi.load()
 
 
-TREE = dict(qkv=P, parents=P, T=4, n=10, pos0=10, k=P, v=P, max_seq=64, H=4, Hkv=2, dh=64,
+TREE = dict(qkv=P, parents=P, T=4, n=10, pos0=10, k=1 << 24, v=1 << 25, max_seq=64, H=4, Hkv=2, dh=64,
             theta=1e4, w_in=None, w_out=None, out=P, ws=P, ws_bytes=1 << 30, stream=None)
 
 
@@ -23,9 +23,10 @@ TREE = dict(qkv=P, parents=P, T=4, n=10, pos0=10, k=P, v=P, max_seq=64, H=4, Hkv
     dict(T=0), dict(T=1025), dict(n=-1), dict(n=61), dict(n=2**31 - 1), dict(pos0=-1),
     dict(pos0=2**31 - 2), dict(max_seq=0), dict(H=0), dict(Hkv=0), dict(H=3), dict(dh=96),
     dict(theta=0.0), dict(theta=float("nan")), dict(theta=float("inf")), dict(qkv=None),
-    dict(qkv=P + 4), dict(parents=None), dict(parents=P + 2), dict(k=None), dict(v=P + 8),
+    dict(qkv=P + 4), dict(parents=None), dict(parents=P + 2), dict(k=None), dict(v=(1 << 25) + 8),
     dict(out=None), dict(ws=None), dict(ws=P + 16), dict(w_in=P), dict(w_out=P + 2),
-    dict(w_in=P + 1, w_out=P)])
+    dict(w_in=P + 1, w_out=P), dict(v=1 << 24), dict(v=(1 << 24) + 8192), dict(k=(1 << 25) - 256),
+    dict(w_in=P, w_out=P + 256), dict(w_in=P + 508, w_out=P)])
 def test_tree_attention(lib, change):
     a = {**TREE, **change}
     assert lib.ssd_op_tree_attention(*a.values()) == INVALID
