@@ -124,7 +124,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
-  if (tid < 2) s_count[tid] = 0;
   const float* w = a.weight + (size_t)blockIdx.y * a.max_seq;
   int32_t* kept = a.kept + (size_t)blockIdx.y * a.keep;
   const int lo = a.sinks, hi = a.n - a.recent, want = a.keep - a.sinks - a.recent;
@@ -242,26 +241,39 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     // ---- places: rows over the cut, and the lowest `need` rows at it, counted
     // per warp and 1024 rows (over: low half, at: high half)
     const uint32_t below = (1u << lane) - 1u;
+    uint32_t mg[kItems], me[kItems];
+    int total = 0;
+    // a chunk's rows by warp, and the exclusive sums over its 512 runs (each
+    // half below 2^15)
+    auto count = [&](int base) {
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        mg[q] = me[q] = 0u;
+        if (base + q * kSelThreads < len) {
+          mg[q] = __ballot_sync(~0u, k[q] > cut);
+          if (need) me[q] = __ballot_sync(~0u, k[q] == cut && k[q]);
+        }
+        if (lane == 0) runs[q * kSelWarps + warp] = __popc(mg[q]) | (__popc(me[q]) << 16);
+      }
+      __syncthreads();
+      const uint32_t mine = tid < kItems * kSelWarps ? runs[tid] : 0u;
+      const int at = block_scan((int)mine, wsum, total);
+      if (tid < kItems * kSelWarps) runs[tid] = (uint32_t)at;
+      __syncthreads();
+    };
     int g = 0, e = 0;                            // before this chunk
     if (nc > 1) {
       // what the lower CTAs of the cluster have
       int gt = 0, eq = 0;
       for (int base = 0; base < len; base += kChunk) {
         if (len > kChunk) load(base);
-#pragma unroll
-        for (int q = 0; q < kItems; ++q) {
-          gt += k[q] > cut;
-          eq += k[q] == cut && k[q];
-        }
+        count(base);
+        gt += total & 0xffff;
+        eq += (int)((uint32_t)total >> 16);
       }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) {
-        gt += __shfl_xor_sync(~0u, gt, d);
-        eq += __shfl_xor_sync(~0u, eq, d);
-      }
-      if (lane == 0) {
-        atomicAdd(&s_count[0], gt);
-        atomicAdd(&s_count[1], eq);
+      if (tid == 0) {
+        s_count[0] = gt;
+        s_count[1] = eq;
       }
       cluster.sync();
       for (int c = 0; c < rank; ++c) {
@@ -272,26 +284,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
     for (int base = 0; base < len; base += kChunk) {
       if (len > kChunk) load(base);
-      uint32_t mg[kItems], me[kItems];
+      if (nc == 1 || len > kChunk) count(base);
 #pragma unroll
       for (int q = 0; q < kItems; ++q) {
-        mg[q] = __ballot_sync(~0u, k[q] > cut);
-        me[q] = __ballot_sync(~0u, k[q] == cut && k[q]);
-        if (lane == 0) runs[q * kSelWarps + warp] = __popc(mg[q]) | (__popc(me[q]) << 16);
-      }
-      __syncthreads();
-      // exclusive sums over the 512 runs (each half below 2^15)
-      const uint32_t mine = tid < kItems * kSelWarps ? runs[tid] : 0u;
-      int total;
-      const int at = block_scan((int)mine, wsum, total);
-      if (tid < kItems * kSelWarps) runs[tid] = (uint32_t)at;
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kItems; ++q) {
+        if (base + q * kSelThreads >= len) break;
         const uint32_t o = runs[q * kSelWarps + warp];
         const int gq = g + (int)(o & 0xffffu) + __popc(mg[q] & below);
         const int eq = e + (int)(o >> 16) + __popc(me[q] & below);
-        if (k[q] > cut || (k[q] == cut && k[q] && eq < need))
+        if ((mg[q] >> lane) & 1u || (((me[q] >> lane) & 1u) && eq < need))
           kept[a.sinks + gq + min(eq, need)] = c0 + base + q * kSelThreads + tid;
       }
       g += total & 0xffff;
