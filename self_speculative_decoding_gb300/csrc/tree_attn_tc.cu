@@ -80,6 +80,24 @@ SSD_DI Unit unit_of(const TreeArgs& a, int u) {
   return x;
 }
 
+// Scores of keys that the row does not see become -infinity, in tensor memory:
+// a condition within the softmax became selections on every block.
+__device__ __noinline__ void mask_scores(uint32_t col, uint4 mask) {
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t w = q == 0 ? mask.x : q == 1 ? mask.y : q == 2 ? mask.z : mask.w;
+    uint32_t v[32];
+    tmem_ld32_nw(col + (uint32_t)q * 32, v);
+    tmem_wait_ld();
+    tmem_pin32(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((w >> e) & 1u)) v[e] = 0xff800000u;
+    tmem_st32(col + (uint32_t)q * 32, v);
+  }
+  tmem_wait_st();
+}
+
 template <int DH, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mK,
@@ -340,13 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (warp_live) {
           const int b = x.b0 + (TWO ? j : 2 * j + s);
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
           const int left = a.n - b * kTreeKeys;  // context keys from this block on
-          const bool whole = b < a.nb_ctx && left >= kTreeKeys;
-          uint4 mask = make_uint4(~0u, ~0u, ~0u, ~0u);
-          if (!whole) {
+          if (b >= a.nb_ctx || left < kTreeKeys) {
+            uint4 mask;
             if (b >= a.nb_ctx) {
               mask = live ? *reinterpret_cast<const uint4*>(anc + 4 * (b - a.nb_ctx))
                           : make_uint4(0u, 0u, 0u, 0u);
@@ -357,14 +371,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               };
               mask = make_uint4(low(0), low(1), low(2), low(3));
             }
+            mask_scores(trow + col_s, mask);
           }
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
           // the second half loads while the first half's maximum is taken
           tmem_wait_ld();
           tmem_pin32(sr[0]);
           tmem_pin32(sr[1]);
 #pragma unroll
           for (int q = 2; q < 4; ++q) tmem_ld32_nw(trow + col_s + q * 32, sr[q]);
-          const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int hlf = 0; hlf < 2; ++hlf) {
@@ -372,13 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld();
               tmem_pin32(sr[2]);
               tmem_pin32(sr[3]);
-            }
-            if (!whole) {
-#pragma unroll
-              for (int q = 2 * hlf; q < 2 * hlf + 2; ++q)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((mw[q] >> e) & 1u)) sr[q][e] = 0xff800000u;  // -infinity
             }
 #pragma unroll
             for (int q = 2 * hlf; q < 2 * hlf + 2; ++q)
