@@ -11,7 +11,6 @@ PyTorch fallback.
 from __future__ import annotations
 
 import ctypes as C
-import math
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -63,16 +62,28 @@ def _lib():
     return _abi.lib()
 
 
+_native = None
+
+
+def _tree_calls():
+    """The native binding of the tree-decoding calls (csrc/binding.cpp), bound
+    to the loaded library's functions."""
+    global _native
+    if _native is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the native binding is not built here: build it with "
+                               "`python -m self_speculative_decoding_gb300.build`") from e
+        lib = _lib()
+        _binding.bind({n: C.cast(getattr(lib, n), C.c_void_p).value for n in _abi.TREE_CALLS}, SSDError)
+        _native = _binding
+    return _native
+
+
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
-
-
-# The current device's index, and a device's current stream as the C calls take
-# it, without building Python stream objects (several microseconds a call).
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda dev: int(torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -428,20 +439,6 @@ class _Ops:
                                                   stream_handle()))
         return out
 
-    @staticmethod
-    def _arg(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
-        """The address of one tensor of a tree-decoding call (the library sees
-        bare pointers), its type, shape, device and layout checked."""
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0
-                and t.is_contiguous()):
-            return t.data_ptr()
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
-                             f"shape {tuple(t.shape)}")
-        if not t.is_cuda or t.get_device() != device:
-            raise ValueError(f"{name}: expected a tensor on CUDA device {device}, got {t.device}")
-        raise ValueError(f"{name}: expected a contiguous tensor")
-
     def tree_attention(self, qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv, dh, theta,
                        weights=None, weights_out=None, out=None) -> torch.Tensor:
         """Attention of a tree of drafted nodes over a cache of n_ctx rows
@@ -451,33 +448,8 @@ class _Ops:
         Returns bf16 [T, H dh].  weights_out fp32 [Hkv, max_seq] receives
         weights plus the attention weight of each key in this call; pass the
         same tensor twice to accumulate in place."""
-        dev = qkv.get_device()
-        if dev >= 0 and dev != _current_device():
-            with torch.cuda.device(dev):
-                return self.tree_attention(qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv, dh,
-                                           theta, weights, weights_out, out)
-        if qkv.dim() != 2 or k_cache.dim() != 3:
-            raise ValueError("expected qkv [T, (H + 2 Hkv) dh] and k_cache [Hkv, max_seq, dh]")
-        T, max_seq = qkv.shape[0], k_cache.shape[1]
-        cache, per_key = (Hkv, max_seq, dh), (Hkv, max_seq)
-        args = (self._arg(qkv, "qkv", torch.float32, (T, (H + 2 * Hkv) * dh), dev),
-                self._arg(parents, "parents", torch.int32, (T,), dev), T, n_ctx, pos0,
-                self._arg(k_cache, "k_cache", torch.bfloat16, cache, dev),
-                self._arg(v_cache, "v_cache", torch.bfloat16, cache, dev), max_seq, H, Hkv, dh, theta,
-                None if weights is None else self._arg(weights, "weights", torch.float32, per_key, dev),
-                None if weights_out is None else
-                self._arg(weights_out, "weights_out", torch.float32, per_key, dev))
-        if out is None:
-            out = torch.empty((T, H * dh), dtype=torch.bfloat16, device=qkv.device)
-        lib = _lib()
-        need = lib.ssd_op_tree_attention_workspace(T, n_ctx, H, Hkv, dh)
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=qkv.device)
-        self._check(lib.ssd_op_tree_attention(
-            *args, self._arg(out, "out", torch.bfloat16, (T, H * dh), dev), ws.data_ptr(), need,
-            _raw_stream(dev)))
-        return out
-
-    CACHE_DTYPES = {torch.bfloat16: _abi.SSD_DTYPE_BF16, torch.float32: _abi.SSD_DTYPE_FP32}
+        return _tree_calls().tree_attention(qkv, parents, k_cache, v_cache, n_ctx, pos0, H, Hkv,
+                                            dh, theta, weights, weights_out, out)
 
     def cache_evict(self, k, v, weights, n, keep, k_out, v_out, weights_out=None, sinks=0,
                     recent=0) -> torch.Tensor:
@@ -487,26 +459,8 @@ class _Ops:
         their order, ``keep`` in all.  k, v [Hkv, max_seq, dh] bf16 or fp32,
         weights fp32 [Hkv, max_seq].  Returns the kept rows, int32
         [Hkv, keep]."""
-        dt = k.dtype
-        if dt not in self.CACHE_DTYPES or k.dim() != 3 or k_out.dim() != 3:
-            raise ValueError("k, k_out: expected bf16 or fp32 tensors [Hkv, rows, dh]")
-        dev = k.get_device()
-        if dev >= 0 and dev != _current_device():
-            with torch.cuda.device(dev):
-                return self.cache_evict(k, v, weights, n, keep, k_out, v_out, weights_out, sinks,
-                                        recent)
-        Hkv, max_seq, dh = k.shape
-        max_out = k_out.shape[1]
-        shape, kept_rows = (Hkv, max_out, dh), (Hkv, max_out)
-        args = (self._arg(k, "k", dt, k.shape, dev), self._arg(v, "v", dt, k.shape, dev),
-                self._arg(weights, "weights", torch.float32, (Hkv, max_seq), dev), n, keep, sinks,
-                recent, max_seq, Hkv, dh, self.CACHE_DTYPES[dt],
-                self._arg(k_out, "k_out", dt, shape, dev), self._arg(v_out, "v_out", dt, shape, dev),
-                None if weights_out is None else
-                self._arg(weights_out, "weights_out", torch.float32, kept_rows, dev), max_out)
-        kept = torch.empty((Hkv, max(keep, 0)), dtype=torch.int32, device=k.device)
-        self._check(_lib().ssd_op_cache_evict(*args, kept.data_ptr(), _raw_stream(dev)))
-        return kept
+        return _tree_calls().cache_evict(k, v, weights, n, keep, k_out, v_out, weights_out, sinks,
+                                         recent)
 
     def beam_select(self, logits, scores, width, lse=None, done=None, end_id=-1):
         """Beam selection (ssd_op_beam_select): the ``width`` best (beam,
@@ -515,58 +469,14 @@ class _Ops:
         lm_head, or None for log-probabilities; done int32 [B] marks ended
         beams.  Returns (tokens, parents, scores, done) of the selected, best
         first."""
-        dev = logits.get_device()
-        if dev >= 0 and dev != _current_device():
-            with torch.cuda.device(dev):
-                return self.beam_select(logits, scores, width, lse, done, end_id)
-        B, V = logits.shape
-        step, lse_at = 1, None
-        if lse is not None and lse.dtype == torch.int32:
-            # ssd_row_stats records: lse is their seventh word
-            step, lse_at = 12, self._arg(lse, "lse", torch.int32, (B, 12), dev) + 24
-        elif lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != (B,) or lse.get_device() != dev:
-                raise ValueError(f"lse: expected fp32 [{B}] on CUDA device {dev}")
-            step, lse_at = lse.stride(0) if B > 1 else 1, lse.data_ptr()
-        args = (self._arg(logits, "logits", torch.float32, (B, V), dev), B, V, lse_at, step,
-                self._arg(scores, "scores", torch.float32, (B,), dev),
-                None if done is None else self._arg(done, "done", torch.int32, (B,), dev), end_id,
-                width)
-        lib, at = _lib(), logits.device
-        need = lib.ssd_op_beam_select_workspace(B, V, width)
-        ws = torch.empty(need, dtype=torch.uint8, device=at) if need else None
-        # (rows of one tensor would cost more than four small tensors)
-        n = max(width, 0)
-        tokens = torch.empty(n, dtype=torch.int32, device=at)
-        parents = torch.empty(n, dtype=torch.int32, device=at)
-        best = torch.empty(n, dtype=torch.float32, device=at)
-        ended = torch.empty(n, dtype=torch.int32, device=at)
-        self._check(lib.ssd_op_beam_select(*args, tokens.data_ptr(), parents.data_ptr(),
-                                           best.data_ptr(), ended.data_ptr(),
-                                           None if ws is None else ws.data_ptr(), need,
-                                           _raw_stream(dev)))
-        return tokens, parents, best, ended
+        return _tree_calls().beam_select(logits, scores, width, lse, done, end_id)
 
     def beam_reorder(self, k, v, parents, start, stop, k_out, v_out):
         """Reordering of the beams' caches (ssd_op_beam_reorder): state w of
         k_out / v_out takes rows start .. stop-1 of state parents[w].  k, v
         [B, ..., max_seq, dh] (any dims between: layers, heads), k_out, v_out
         [W, ..., max_seq, dh]; v and v_out may be None."""
-        shape, dt, dev, W = k.shape, k.dtype, k.get_device(), k_out.shape[0]
-        if len(shape) < 3:
-            raise ValueError("k: expected [B, ..., max_seq, dh]")
-        if (v is None) != (v_out is None):
-            raise ValueError("v and v_out go together")
-        if dev >= 0 and dev != _current_device():
-            with torch.cuda.device(dev):
-                return self.beam_reorder(k, v, parents, start, stop, k_out, v_out)
-        to = (W, *shape[1:])
-        self._check(_lib().ssd_op_beam_reorder(
-            self._arg(k, "k", dt, shape, dev), None if v is None else self._arg(v, "v", dt, shape, dev),
-            self._arg(parents, "parents", torch.int32, (W,), dev), shape[0], W,
-            math.prod(shape[1:-2]), shape[-2], start, stop, shape[-1] * k.element_size(),
-            self._arg(k_out, "k_out", dt, to, dev),
-            None if v_out is None else self._arg(v_out, "v_out", dt, to, dev), _raw_stream(dev)))
+        _tree_calls().beam_reorder(k, v, parents, start, stop, k_out, v_out)
         return k_out, v_out
 
     def wait_selftest(self, polls: int = 4096) -> int:

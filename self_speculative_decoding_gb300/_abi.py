@@ -145,6 +145,11 @@ _SIGS = {
 
 EXPORTED = tuple(_SIGS)
 
+# What the native binding calls (csrc/binding.cpp).
+TREE_CALLS = ("ssd_op_tree_attention_workspace", "ssd_op_tree_attention", "ssd_op_cache_evict",
+              "ssd_op_beam_select_workspace", "ssd_op_beam_select", "ssd_op_beam_reorder",
+              "ssd_ops_last_error")
+
 
 def load(path: Optional[str] = None) -> C.CDLL:
     """The library at ``path``; default: $SSD_LIBSSD if set (another build of

@@ -113,3 +113,29 @@ def test_binding_refuses_tensors_it_cannot_take():
         ops.beam_select(f, torch.zeros(3), 4)
     with pytest.raises(ValueError):
         ops.beam_reorder(c, None, i, 0, 4, c, c)
+
+
+def test_binding_refuses_arguments_of_other_types():
+    import torch
+    from self_speculative_decoding_gb300 import ops
+    f, i = torch.zeros(4, 8 * 64), torch.zeros(4, dtype=torch.int32)
+    c = torch.zeros(2, 64, 64, dtype=torch.bfloat16)
+    for bad in (2 ** 31, -2 ** 31 - 1, 2 ** 70):      # would not reach the kernels whole
+        with pytest.raises(ValueError, match="32 bits"):
+            ops.tree_attention(f, i, c, c, bad, 10, 4, 2, 64, 1e4)
+        with pytest.raises(ValueError, match="32 bits"):
+            ops.cache_evict(c, c, torch.zeros(2, 64), bad, 5, c, c)
+        with pytest.raises(ValueError, match="32 bits"):
+            ops.beam_select(f, torch.zeros(4), bad)
+        with pytest.raises(ValueError, match="32 bits"):
+            ops.beam_reorder(c, None, i, 0, bad, c, None)
+    with pytest.raises(TypeError):
+        ops.beam_select(f, torch.zeros(4), 2.5)
+    with pytest.raises(TypeError):
+        ops.tree_attention(f, i, c, c, 10, 10, 4, 2, 64, "theta")
+    with pytest.raises(ValueError, match="expected a tensor"):
+        ops.cache_evict(None, c, torch.zeros(2, 64), 10, 5, c, c)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        ops.beam_select(f.numpy(), torch.zeros(4), 2)
+    with pytest.raises(ValueError, match="go together"):
+        ops.beam_reorder(c, c, i, 0, 4, c, None)
