@@ -93,6 +93,9 @@ SSD_DI void copy_rows(const EvictArgs& a, int h, int j0, int cnt, int32_t* src_r
   }
 }
 
+// The kept rows of a head in turn to CTAs of 1024 units of K and of V, read once
+// (past the caches) and written once: bound by memory, 8 heads of 16384 rows
+// 20.4 us (134 MB, 6.6 TB/s), 40 heads of 2048 rows 14.7 (84 MB, 5.7 TB/s).
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = kCopyThreads * kCopyUnits;
 __global__ void __launch_bounds__(kCopyThreads) evict_gather_kernel(const EvictArgs a, int rows) {
@@ -109,7 +112,8 @@ __global__ void __launch_bounds__(kCopyThreads) evict_gather_kernel(const EvictA
 // two to a word, which halves what the CTAs read of each other (a word each,
 // `wide`, where a CTA has more rows than 16 bits count).  Weights share few
 // exponents, so the first histogram has eight copies: lanes of a warp rarely
-// meet in one.
+// meet in one.  Bound by latency (the passes' barriers and scans): 40 heads of
+// 4095 rows 9.5 us, 8 heads of 131072 rows 24 us, for 0.7 and 4 MB of weights.
 // With `fused` (one CTA per head, few rows) the CTA copies the rows too.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int fused) {
   extern __shared__ __align__(16) uint32_t smem[];

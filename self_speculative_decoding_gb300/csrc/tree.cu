@@ -22,6 +22,9 @@ constexpr int kPrepThreads = 256;
 // own copy (a matrix product must not meet 0 x inf at masked keys).
 // Angles: position * frequency in 64 bits, reduced to one turn, so that far
 // positions keep their angle.
+// Bound by latency: 4 us for one node, 7 for 61 nodes of 40 heads (4.7 MB
+// moved, under 1 us at the memory's rate): launch, parents, ancestor walk,
+// angle and stores one behind the other.  The projections load before the walk.
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ int par[kTreeMaxNodes];
   __shared__ uint32_t bits[kTreeMaxNodes / 32];

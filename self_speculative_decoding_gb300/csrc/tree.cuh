@@ -159,10 +159,11 @@ SSD_DI float tree_max3(float a, float b, float c) {
 // issue, of the 64 that it runs).  The matrix pipe holds hardly more than the
 // instruction that runs, so what the warp does between two groups is time
 // lost: about 95 cycles a wait, 42 a commit, 90 a look at the failure flag.
-// Hence waits are joint or early (tree_try), and the flag is looked at only
-// while a wait lasts.  A warp for each stream was no way out (256 nodes over
-// 131000 rows 1145 against 885 us): the streams' products then interleave, and
-// both wait for their softmax at the same time.
+// Hence the flag is looked at only while a wait lasts, and the weights' kernel
+// waits for two barriers at once (in the attention, whose streams take turns,
+// that was slower: 954 against 850 us for 256 nodes over 131000 rows).  A warp
+// for each stream was no way out (1145 against 885 us): the streams' products
+// then interleave, and both wait for their softmax at the same time.
 SSD_DI uint32_t tree_elect() {
   uint32_t r;
   asm volatile(

@@ -15,6 +15,14 @@
 // split into units over the SMs; a second kernel joins the units' partial
 // results in a fixed order.
 //
+// With many rows the matrix pipe bounds it: 256 nodes of 64 / 8 heads over
+// 131000 rows are 1.65 TFLOP in three products of one size (Q_hi K, Q_lo K,
+// P V), 854 us at the 1931 TFLOP/s that a library product reaches in a burst;
+// it takes 855 us, and up to 930 where the power limit lowers the clock.  With
+// few rows it is a stream's chain (copy, product, softmax, product) and the
+// first copy's latency: 61 nodes of 40 heads over 2047 rows take 15 us for
+// 7 us of bytes.
+//
 // Warps 0-3 and 4-7: the streams' softmax; warp 8: TMA copies; warp 9: MMA.
 // Every wait is bounded: one that gives up sets the CTA's flag, every role
 // runs out, and the results become NaN.

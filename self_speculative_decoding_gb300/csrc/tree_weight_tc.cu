@@ -11,14 +11,16 @@
 // to two streams of four warps, each block against both tiles at once (256
 // columns to an instruction: twice the time of 128, which covers what the
 // issuing warp does between two groups); the sums of a segment's keys stay
-// with their threads until every pair has passed.  Passes
-// zigzag over the pairs, so that a new segment starts with the planes that are
-// there.  (With one tile per pass, 64 nodes of 64 / 8 heads over 32768 rows
-// took 62 us, waiting for K: 3 blocks in flight arrive at 19 bytes per cycle
-// and SM.)  Four more warps join the attention's partial results meanwhile, so
-// that no kernel runs between.
-// Warp 8: TMA copies, warp 9: the products.  Waits are bounded; one that gives up makes
-// the CTA's weights NaN.
+// with their threads until every pair has passed.  Passes zigzag over the
+// pairs, so that a new segment starts with the planes that are there.
+// Warp 8: TMA copies, warp 9: the products, warps 10 and 11: the join of the
+// attention's partial results meanwhile, so that no kernel runs between.
+// Waits are bounded; one that gives up makes the CTA's weights NaN.
+//
+// 64 nodes of 64 / 8 heads over 32768 rows: 52 us (62 with one tile to a
+// pass), of which the products of both planes are 36 at the matrix peak; a
+// stream's chain of products (2400 cycles for 256 columns) and sums (3100)
+// bounds it, with the two streams' products in turn.
 #include "tc_dev.cuh"
 #include "tree.cuh"
 #include "tree_join.cuh"
