@@ -62,7 +62,9 @@ template <int kThreads>
 SSD_DI void copy_rows(const EvictArgs& a, int h, int j0, int cnt, int32_t* src_row) {
   const int tid = threadIdx.x;
   for (int j = tid; j < cnt; j += kThreads) {
-    const int i = a.kept[(size_t)h * a.keep + j0 + j];
+    // the first and the last rows are known without the selection
+    const int o = j0 + j, last = o - (a.keep - a.recent);
+    const int i = o < a.sinks ? o : last >= 0 ? a.n - a.recent + last : a.kept[(size_t)h * a.keep + o];
     src_row[j] = i;
     if (a.weight_out)
       a.weight_out[(size_t)h * a.max_out + j0 + j] = a.weight[(size_t)h * a.max_seq + i];
@@ -100,9 +102,12 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = kCopyThreads * kCopyUnits;
 __global__ void __launch_bounds__(kCopyThreads) evict_gather_kernel(const EvictArgs a, int rows) {
   __shared__ int32_t src_row[kCopyRows];
-  pdl_wait();
-  const int j0 = blockIdx.x * rows;
-  copy_rows<kCopyThreads>(a, blockIdx.y, j0, min(rows, a.keep - j0), src_row);
+  // (rows that are known are copied while the selection runs)
+  const int j0 = blockIdx.x * rows, cnt = min(rows, a.keep - j0);
+  const bool known = j0 + cnt <= a.sinks || j0 >= a.keep - a.recent;
+  if (!known) pdl_wait();
+  copy_rows<kCopyThreads>(a, blockIdx.y, j0, cnt, src_row);
+  if (known) pdl_wait();
 }
 
 // Cluster = one K/V head, its middle rows divided among the CTAs, each

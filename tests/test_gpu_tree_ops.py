@@ -353,6 +353,18 @@ def test_evict_ties_and_specials(ops):
         np.testing.assert_array_equal(got, O.cache_evict(w, n, keep, 0, min(keep, 7)))
 
 
+# weights a few steps of fp32 apart: few, some or many rows share all but their
+# last ten bits
+@pytest.mark.parametrize("n", [700, 6000, 8999, 20000, 150001])
+@pytest.mark.parametrize("steps", [2 ** 21, 2 ** 18, 2 ** 15, 2 ** 11])
+def test_evict_weights_that_differ_late(ops, n, steps):
+    rng = np.random.default_rng(n)
+    w = (1 + rng.integers(0, steps, (3, n)) * 2.0 ** -23).astype(np.float32)
+    for keep in (n // 3, n - 40):
+        got = run_evict(ops, torch.from_numpy(w).cuda(), n, keep, 3, 20, 8)
+        np.testing.assert_array_equal(got, O.cache_evict(w, n, keep, 3, 20))
+
+
 def test_evict_long_row(ops):
     rng = np.random.default_rng(5)
     n, keep = 1_000_003, 100_000
