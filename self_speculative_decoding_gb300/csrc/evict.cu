@@ -17,9 +17,10 @@ namespace cg = cooperative_groups;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCopies = 8;          // of the first histogram: lane l counts in copy l % 8
-constexpr int kItems = 16;          // weights per thread that stay in registers
+constexpr int kItems = 16;          // keys per thread that stay in shared memory
 constexpr int kChunk = kSelThreads * kItems;
 constexpr int kRankKeys = 512;      // at most so many middle rows are ranked by counting
+static_assert(kChunk < 1 << 15, "two counts of a chunk's rows share a word");
 constexpr int kMaxCluster = 8;
 constexpr int kWords = 1024;        // of a histogram of 2048 bins
 constexpr int kFusedRows = 512;     // rows and 16-byte units that a selecting CTA copies itself
@@ -55,6 +56,11 @@ SSD_DI int block_scan(int x, int* wsum, int& total) {
   return (warp ? below : 0) + v - x;
 }
 
+// log2 of the rows per thread of a chunk: 4, 8 or 16.
+SSD_HD int key_log(int share) {
+  return share <= 4 * kSelThreads ? 2 : share <= 8 * kSelThreads ? 3 : 4;
+}
+
 // Rows j0 .. j0 + cnt - 1 of a head's output: all of a thread's 16-byte units
 // in flight at once.
 constexpr int kCopyUnits = 4;       // units per thread and turn, of K and of V
@@ -66,6 +72,7 @@ SSD_DI void copy_rows(const EvictArgs& a, int h, int j0, int cnt, int32_t* src_r
     const int o = j0 + j, last = o - (a.keep - a.recent);
     const int i = o < a.sinks ? o : last >= 0 ? a.n - a.recent + last : a.kept[(size_t)h * a.keep + o];
     src_row[j] = i;
+    if (o < a.sinks || last >= 0) a.kept[(size_t)h * a.keep + o] = i;
     if (a.weight_out)
       a.weight_out[(size_t)h * a.max_out + j0 + j] = a.weight[(size_t)h * a.max_seq + i];
   }
@@ -110,25 +117,31 @@ __global__ void __launch_bounds__(kCopyThreads) evict_gather_kernel(const EvictA
   if (known) pdl_wait();
 }
 
-// Cluster = one K/V head, its middle rows divided among the CTAs, each
-// thread's weights in registers (a CTA with more than 16384 re-reads them from
-// L2).  11 + 11 + 10 bits of the cut are found from histograms summed over the
-// cluster; a pass whose bin stays as a whole is the last.  Counts are 16 bits,
-// two to a word, which halves what the CTAs read of each other (a word each,
-// `wide`, where a CTA has more rows than 16 bits count).  Weights share few
-// exponents, so the first histogram has eight copies: lanes of a warp rarely
-// meet in one.  Bound by latency (the passes' barriers and scans): 40 heads of
-// 4095 rows 9.5 us, 8 heads of 131072 rows 24 us, for 0.7 and 4 MB of weights.
+// Cluster = one K/V head, its middle rows divided among the CTAs (`share`
+// each), the weights' keys in shared memory (a CTA with more than 16384 reads
+// them again from L2).  11 + 11 + 10 bits of the cut are found from histograms
+// summed over the cluster; a pass whose bin stays as a whole is the last.
+// Counts are 16 bits, two to a word, which halves what the CTAs read of each
+// other (a word each, `wide`, where a CTA has more rows than 16 bits count).
+// Weights share few exponents, so the first histogram has eight copies: lanes
+// of a warp rarely meet in one.  What the lower CTAs have over the cut comes
+// out of the same sums, so that the places need no further exchange.
 // With `fused` (one CTA per head, few rows) the CTA copies the rows too.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int fused) {
+// Bound by latency: barriers, reads of the others' sums, and code that runs
+// only once.  Hence short loops over keys in shared memory and places counted
+// per thread over rows that lie together: 8 heads of 131072 rows take 36.9 us
+// with the copy (20.4), 40.8 with the keys in registers, unrolled loops and
+// places from ballots; 40 heads of 4095 rows 16.9 and 17.9 us.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int share,
+                                                                  int fused) {
   extern __shared__ __align__(16) uint32_t smem[];
   __shared__ int32_t src_row[kFusedRows];
   __shared__ int wsum[kSelWarps];
   __shared__ uint32_t s_bin;
   __shared__ int s_need;
-  __shared__ int s_count[2];
   __shared__ int s_all;
-  __shared__ uint32_t runs[kItems * kSelWarps];
+  __shared__ int s_over;         // rows of the lower CTAs over the cut's bin,
+  __shared__ int s_with;         // and in it
   pdl_trigger();
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
@@ -136,12 +149,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const float* w = a.weight + (size_t)blockIdx.y * a.max_seq;
   int32_t* kept = a.kept + (size_t)blockIdx.y * a.keep;
   const int lo = a.sinks, hi = a.n - a.recent, want = a.keep - a.sinks - a.recent;
-  const int share = (hi - lo + nc - 1) / nc;
   const int c0 = min(lo + rank * share, hi), len = min(share, hi - c0);
-  if (rank == 0) {
-    for (int i = tid; i < a.sinks; i += kSelThreads) kept[i] = i;
-    for (int i = tid; i < a.recent; i += kSelThreads) kept[a.keep - a.recent + i] = hi + i;
-  }
   if (nc == 1 && len <= kRankKeys) {
     // few rows: each counts the rows before it in the order
     if (tid < kRankKeys) smem[tid] = tid < len ? weight_key(w[c0 + tid]) : 0u;  // 0: under every key
@@ -161,18 +169,44 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int words = wide ? 2 * kWords : kWords;
     uint32_t* hist = smem;                       // [word][copy]
     uint32_t* sums = hist + kCopies * words;     // [pass][word]
-    for (int i = tid; i < (kCopies + 3) * words / 4; i += kSelThreads)
-      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-    // keys of a chunk, row base + 1024 q + thread; 0 beyond the share
-    uint32_t k[kItems];
-    auto load = [&](int base) {
+    // a chunk's keys: thread t has rows t << lg .. ((t + 1) << lg) - 1, four
+    // words more behind every thread's eight or sixteen (no bank conflicts)
+    uint32_t* keys = sums + 3 * words;
+    const int lg = key_log(share), pad = lg > 2 ? 4 : 0, stride = (1 << lg) + pad;
+    const bool again = len > kChunk;             // the chunks take turns in it
+    auto fetch = [&](int base) {
+      const int cnt = min(kChunk, len - base);
+      for (int i0 = tid; i0 < cnt; i0 += 8 * kSelThreads) {
+        float x[8];
 #pragma unroll
-      for (int q = 0; q < kItems; ++q) {
-        const int i = base + q * kSelThreads + tid;
-        k[q] = i < len ? weight_key(w[c0 + i]) : 0u;
+        for (int q = 0; q < 8; ++q) {
+          const int i = i0 + q * kSelThreads;
+          x[q] = i < cnt ? w[c0 + base + i] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int i = i0 + q * kSelThreads;
+          if (i < cnt) keys[i + (i >> lg) * pad] = __float_as_uint(x[q]);
+        }
       }
     };
-    load(0);
+    // four keys from the thread's row j on, 0 beyond the chunk's cnt rows
+    auto raw = [&](int j, int cnt) {
+      uint4 x = *reinterpret_cast<const uint4*>(keys + tid * stride + j);
+      const int left = cnt - (tid << lg) - j;
+      x.x = left > 0 ? weight_key(__uint_as_float(x.x)) : 0u;
+      x.y = left > 1 ? weight_key(__uint_as_float(x.y)) : 0u;
+      x.z = left > 2 ? weight_key(__uint_as_float(x.z)) : 0u;
+      x.w = left > 3 ? weight_key(__uint_as_float(x.w)) : 0u;
+      return x;
+    };
+    auto four = [&](int j, int cnt) {
+      return again ? raw(j, cnt) : *reinterpret_cast<const uint4*>(keys + tid * stride + j);
+    };
+    if (tid == 0) s_over = 0;
+    for (int i = tid; i < (kCopies + 3) * words / 4; i += kSelThreads)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (!again) fetch(0);
     __syncthreads();
     // ---- the want-th largest key, and how many rows at it stay
     uint32_t cut = 0;
@@ -185,16 +219,30 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       const int above = shift + (pass == 2 ? 10 : 11);
       uint32_t* sum = sums + pass * words;
       for (int base = 0; base < len; base += kChunk) {
-        if (len > kChunk) load(base);
+        const int cnt = min(kChunk, len - base);
+        if (again) {
+          __syncthreads();                       // the chunk before is read
+          fetch(base);
+          __syncthreads();
+        }
+        for (int j = 0; j < 1 << lg; j += 4) {
+          uint4 x;
+          if (pass == 0) {                       // keys take the place of the weights
+            x = raw(j, cnt);
+            *reinterpret_cast<uint4*>(keys + tid * stride + j) = x;
+          } else {
+            x = four(j, cnt);
+          }
 #pragma unroll
-        for (int q = 0; q < kItems; ++q) {
-          if (base + q * kSelThreads >= len) break;
-          const uint32_t bin = (k[q] >> shift) & mask;
-          const uint32_t at = wide ? bin : bin >> 1, one = wide ? 1u : 1u << (16 * (bin & 1));
-          if (pass == 0) {
-            if (k[q]) atomicAdd(&hist[at * kCopies + (tid & (kCopies - 1))], one);
-          } else if ((k[q] >> above) == (cut >> above)) {
-            atomicAdd(&sum[at], one);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t k = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+            const uint32_t bin = (k >> shift) & mask;
+            const uint32_t at = wide ? bin : bin >> 1, one = wide ? 1u : 1u << (16 * (bin & 1));
+            if (pass == 0) {
+              if (k) atomicAdd(&hist[at * kCopies + (tid & (kCopies - 1))], one);
+            } else if ((k >> above) == (cut >> above)) {
+              atomicAdd(&sum[at], one);
+            }
           }
         }
       }
@@ -225,10 +273,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         else
           o[c].x = from[pair];
       }
+      int hi_low = 0, lo_low = 0;                // of the lower CTAs
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
-        hi_n += wide ? o[c].y : o[c].x >> 16;
-        lo_n += wide ? o[c].x : o[c].x & 0xffffu;
+        const int h = (int)(wide ? o[c].y : o[c].x >> 16);
+        const int l = (int)(wide ? o[c].x : o[c].x & 0xffffu);
+        hi_n += h;
+        lo_n += l;
+        if (c < rank) {
+          hi_low += h;
+          lo_low += l;
+        }
       }
       int total;
       const int before = block_scan(hi_n + lo_n, wsum, total);
@@ -237,77 +292,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         s_bin = (uint32_t)(2 * pair + first);
         s_need = need - before - (first ? 0 : hi_n);
         s_all = s_need == (first ? hi_n : lo_n);
+        s_with = first ? hi_low : lo_low;
       }
       __syncthreads();
+      if (rank) {
+        const uint32_t b = s_bin;
+        const int over = __reduce_add_sync(~0u, ((uint32_t)(2 * pair + 1) > b ? hi_low : 0) +
+                                                    ((uint32_t)(2 * pair) > b ? lo_low : 0));
+        if (lane == 0 && over) atomicAdd(&s_over, over);
+      }
       cut |= s_bin << shift;
       need = s_need;
       exact = s_all;
     }
+    if (nc > 1) cluster.barrier_arrive();        // the others' sums are read
+    __syncthreads();
+    // rows over and at the cut before this CTA's
+    int g = s_over + (exact ? s_with : 0), e = s_with;
     if (exact) {                                 // the last bin stays as a whole
       cut -= 1;                                  // (bin 0 of every pass is no key)
       need = 0;
     }
-    // ---- places: rows over the cut, and the lowest `need` rows at it, counted
-    // per warp and 1024 rows (over: low half, at: high half)
-    const uint32_t below = (1u << lane) - 1u;
-    uint32_t mg[kItems], me[kItems];
-    int total = 0;
-    // a chunk's rows by warp, and the exclusive sums over its 512 runs (each
-    // half below 2^15)
-    auto count = [&](int base) {
-#pragma unroll
-      for (int q = 0; q < kItems; ++q) {
-        mg[q] = me[q] = 0u;
-        if (base + q * kSelThreads < len) {
-          mg[q] = __ballot_sync(~0u, k[q] > cut);
-          if (need) me[q] = __ballot_sync(~0u, k[q] == cut && k[q]);
-        }
-        if (lane == 0) runs[q * kSelWarps + warp] = __popc(mg[q]) | (__popc(me[q]) << 16);
-      }
-      __syncthreads();
-      const uint32_t mine = tid < kItems * kSelWarps ? runs[tid] : 0u;
-      const int at = block_scan((int)mine, wsum, total);
-      if (tid < kItems * kSelWarps) runs[tid] = (uint32_t)at;
-      __syncthreads();
-    };
-    int g = 0, e = 0;                            // before this chunk
-    if (nc > 1) {
-      // what the lower CTAs of the cluster have
-      int gt = 0, eq = 0;
-      for (int base = 0; base < len; base += kChunk) {
-        if (len > kChunk) load(base);
-        count(base);
-        gt += total & 0xffff;
-        eq += (int)((uint32_t)total >> 16);
-      }
-      if (tid == 0) {
-        s_count[0] = gt;
-        s_count[1] = eq;
-      }
-      cluster.sync();
-      for (int c = 0; c < rank; ++c) {
-        const int* other = cluster.map_shared_rank(&s_count[0], c);
-        g += other[0];
-        e += other[1];
-      }
-    }
+    // ---- places: rows over the cut, and the lowest `need` rows at it; each
+    // thread's counted (over: low half, at: high half; each below 2^15), then
+    // placed from where the threads before it end
     for (int base = 0; base < len; base += kChunk) {
-      if (len > kChunk) load(base);
-      if (nc == 1 || len > kChunk) count(base);
+      const int cnt = min(kChunk, len - base);
+      if (again) {
+        __syncthreads();
+        fetch(base);
+        __syncthreads();
+      }
+      int mine = 0;
+      for (int j = 0; j < 1 << lg; j += 4) {
+        const uint4 x = four(j, cnt);
+        mine += (x.x > cut) + (x.y > cut) + (x.z > cut) + (x.w > cut);
+        mine += ((x.x == cut) + (x.y == cut) + (x.z == cut) + (x.w == cut)) << 16;
+      }
+      int total;
+      const uint32_t at = (uint32_t)block_scan(mine, wsum, total);
+      int over = g + (int)(at & 0xffffu), with = e + (int)(at >> 16);
+      for (int j = 0; j < 1 << lg; j += 4) {
+        const uint4 x = four(j, cnt);
+        const int i0 = c0 + base + (tid << lg) + j;
 #pragma unroll
-      for (int q = 0; q < kItems; ++q) {
-        if (base + q * kSelThreads >= len) break;
-        const uint32_t o = runs[q * kSelWarps + warp];
-        const int gq = g + (int)(o & 0xffffu) + __popc(mg[q] & below);
-        const int eq = e + (int)(o >> 16) + __popc(me[q] & below);
-        if ((mg[q] >> lane) & 1u || (((me[q] >> lane) & 1u) && eq < need))
-          kept[a.sinks + gq + min(eq, need)] = c0 + base + q * kSelThreads + tid;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t k = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+          if (k > cut || (k == cut && with < need)) kept[a.sinks + over + min(with, need)] = i0 + i;
+          over += k > cut;
+          with += k == cut;
+        }
       }
       g += total & 0xffff;
       e += (int)((uint32_t)total >> 16);
-      if (len > kChunk) __syncthreads();         // runs are read
     }
-    if (nc > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
+    if (nc > 1) cluster.barrier_wait();          // no CTA leaves while another reads its sums
   }
   if (fused) {
     __syncthreads();             // the CTA's own entries of kept
@@ -330,12 +369,14 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const int share = (middle + nc - 1) / nc;
   const bool ranked = want == 0 || (nc == 1 && share <= kRankKeys);
   const size_t hist = (size_t)(kCopies + 3) * kWords * 4;
-  const size_t smem = ranked ? kRankKeys * 4 : share > 65535 ? 2 * hist : hist;
+  const int lg = key_log(share);
+  const size_t held = (size_t)kSelThreads * ((1 << lg) + (lg > 2 ? 4 : 0)) * 4;
+  const size_t smem = ranked ? kRankKeys * 4 : (share > 65535 ? 2 * hist : hist) + held;
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * hist));
+        evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * hist) + kSelThreads * (kItems + 4) * 4);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
@@ -351,7 +392,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   lc.stream = s;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&lc, evict_select_kernel, a, (int)fused);
+  cudaError_t e = cudaLaunchKernelEx(&lc, evict_select_kernel, a, share, (int)fused);
   if (e != cudaSuccess || fused) return e;
   int rows = kCopyRows / a.units;
   if (rows < 1) rows = 1;
