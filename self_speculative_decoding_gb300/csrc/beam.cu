@@ -92,31 +92,28 @@ __device__ __noinline__ int piece_bisect(const float* row, int v0, int n, int W,
 // Piece `piece` of row b: its W largest keys to its list, largest first.  The
 // logits stay in registers; what lies at or over the W-th largest
 // of G group maxima is listed and ranked.
-template <int G>
-SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out) {
-  __shared__ uint64_t list[kList];
-  __shared__ __align__(16) float gm[G];
-  __shared__ float s_cut;
-  __shared__ int s_n;
+template <int G, int kItems>
+SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* out,
+                        uint64_t* list, float* gm, float& s_cut, int& s_n) {
   const int tid = threadIdx.x;
   if (a.done && a.done[b]) return;               // the merge does not read its lists
   const int v0 = piece * len, n = min(len, a.V - v0);
   const float* row = a.logits + (size_t)b * a.V + v0;
-  float z[kPieceItems];
+  float z[kItems];
   float mx = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kPieceItems; ++i) {
+  for (int i = 0; i < kItems; ++i) {
     const int v = i * kPieceThreads + tid;
     z[i] = v < n ? __ldcs(row + v) : -INFINITY;
   }
 #pragma unroll
-  for (int i = 0; i < kPieceItems; ++i) mx = fmaxf(mx, z[i]);  // ignores NaN
+  for (int i = 0; i < kItems; ++i) mx = fmaxf(mx, z[i]);  // ignores NaN
 #pragma unroll
   for (int d = 1; d < kPieceThreads / G; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
   if (tid == 0) s_n = 0;
   const float cut = group_cut<G, kPieceThreads>(mx, a.W, gm, &s_cut);
 #pragma unroll
-  for (int i = 0; i < kPieceItems; ++i)
+  for (int i = 0; i < kItems; ++i)
     if (z[i] >= cut && z[i] > -INFINITY) {
       const int at = atomicAdd(&s_n, 1);
       if (at < kList) list[at] = logit_key(z[i], v0 + i * kPieceThreads + tid);
@@ -125,16 +122,36 @@ SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* o
   int cnt = s_n;
   if (cnt > kList) cnt = piece_bisect(row, v0, n, a.W, list, &s_n);
   // keys differ, so each key's rank is its place
-  for (int i = tid; i < cnt; i += kPieceThreads) {
-    const uint64_t k = list[i];
+  // (counted by four threads together)
+  for (int i = tid >> 2; i < ((cnt + 7) & ~7); i += kPieceThreads / 4) {
+    const uint64_t k = i < cnt ? list[i] : 0;
     int rank = 0;
-    for (int j = 0; j < cnt; ++j) rank += list[j] > k;
-    if (rank < a.W) out[rank] = k;
+    for (int j = tid & 3; j < cnt; j += 4) rank += list[j] > k;
+    rank += __shfl_xor_sync(~0u, rank, 1);
+    rank += __shfl_xor_sync(~0u, rank, 2);
+    if ((tid & 3) == 0 && i < cnt && rank < a.W) out[rank] = k;
   }
   for (int i = cnt + tid; i < a.W; i += kPieceThreads) out[i] = 0;
 }
 
-// CTA = (piece of a row, beam).
+// A short piece has code of its own: what runs once is bound by its fetching
+// (4 beams of 1024 logits 9.6 us with the long one, 8.1).
+constexpr int kFewItems = 4;
+template <int G>
+SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out) {
+  __shared__ uint64_t list[kList];
+  __shared__ __align__(16) float gm[G];
+  __shared__ float s_cut;
+  __shared__ int s_n;
+  if (len <= kFewItems * kPieceThreads)
+    piece_items<G, kFewItems>(a, len, piece, b, out, list, gm, s_cut, s_n);
+  else
+    piece_items<G, kPieceItems>(a, len, piece, b, out, list, gm, s_cut, s_n);
+}
+
+// CTA = (piece of a row, beam).  48 rows of 128003 logits (24.6 MB) take 11 us:
+// the loads 6 of them (4 bytes each, since rows begin anywhere; all of a
+// thread's in flight at once), then the threshold, the list and its ranks.
 template <int G>
 __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
   pdl_trigger();
@@ -211,8 +228,12 @@ SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool
 // candidates at least, so the W-th largest of their lower bounds, or of the
 // bounds' maxima over 256 groups, is a threshold that W candidates reach; the
 // entries of each list whose upper bound reaches it are collected and ranked
-// by the whole order.
-template <int kThreads>
+// by the whole order, eight threads to a candidate (48 beams of 128003 logits
+// 18.3 us in all, 21.2 with one thread to each).  Bound by latency, about 6 us
+// for 288 lists: two rounds of reads of L2, threshold and ranks between them;
+// holding the lists' first entries in shared memory was slower (22.1 against
+// 21.2).  WAIT: the lists come from the kernel before.
+template <int kThreads, bool WAIT>
 SSD_DI void merge_body(const BeamArgs& a, int pieces) {
   constexpr int kGroups = 256, kPer = kThreads / kGroups;
   __shared__ Cand list[kList];
@@ -227,6 +248,7 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
     beams[tid].ended = a.done && a.done[tid];
   }
   if (tid == 0) s_n = 0;
+  if (WAIT) pdl_wait();                          // (the beams are not the pieces' work)
   __syncthreads();
   // sample j: entry j / lists of list j % lists; 256 in a row go to 256 groups
   const int deep = min(a.W, (a.W + lists - 1) / lists), samples = lists * deep;
@@ -265,11 +287,13 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
   __syncthreads();
   const int cnt = s_n;
   if (cnt <= kList) {
-    for (int i = tid; i < cnt; i += kThreads) {
-      const Cand c = list[i];
+    for (int i = tid >> 3; i < ((cnt + 3) & ~3); i += kThreads / 8) {
+      const Cand c = list[min(i, cnt - 1)];
       int rank = 0;
-      for (int j = 0; j < cnt; ++j) rank += before(list[j], c);
-      if (rank < a.W) put(a, beams, rank, c, true);
+      for (int j = tid & 7; j < cnt; j += 8) rank += before(list[j], c);
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
+      if ((tid & 7) == 0 && i < cnt && rank < a.W) put(a, beams, rank, c, true);
     }
     for (int w = cnt + tid; w < a.W; w += kThreads) put(a, beams, w, Cand{}, false);
     return;
@@ -306,8 +330,7 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
 }
 
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArgs a, int pieces) {
-  pdl_wait();
-  merge_body<kMergeThreads>(a, pieces);
+  merge_body<kMergeThreads, true>(a, pieces);
 }
 
 // Few pieces: one cluster holds them all, and its first CTA merges the lists
@@ -328,7 +351,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) beam_cluster_kernel(const Be
   if (blockIdx.x || blockIdx.y) return;
   BeamArgs b = a;
   b.lists = all;
-  merge_body<kPieceThreads>(b, gridDim.x);
+  merge_body<kPieceThreads, false>(b, gridDim.x);
 }
 
 // Reordering by source: a tile of 1024 16-byte units of one group's rows is
