@@ -467,6 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the unit's result: a tile's two streams are joined (the other
       // stream's output lies in the same lanes), a pair's are two tiles
       const int cnt1 = x.nb / 2;                 // of stream 1, one tile
+      const bool last = a.splits == 1;           // the row's final result
+      const bool present = last && live && a.depth[t] >= 0;
+      const bool bad = last && any_bad(a, x.kvh, lane);
       if (cnt > 0) ok = wait_w(&ofull[s], (uint32_t)(n_own++ & 1));
       if (!ok) break;
       if (!TWO && s == 1) {
@@ -493,17 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (warp_live) {
         const bool both = !TWO && cnt1 > 0;
-        const bool last = a.splits == 1;         // the row's final result
         const int slot = TWO ? (x.kvh * a.splits + x.split) * (a.items * 2) + tile
                              : x.kvh * a.splits + x.split;
         float* po = a.part_o + (size_t)slot * DH * 128 + (size_t)r * 4;
         float lse = INFINITY, inv = 0.f;
-        bool present = false, bad = false;
         if (last) {
           lse = l != 0.f ? m + log2f(l) : INFINITY;
           inv = l != 0.f ? 1.f / l : 0.f;
-          present = live && a.depth[t] >= 0;
-          bad = any_bad(a, x.kvh, lane);
         }
         bf16* out = a.out + ((size_t)t * a.H + x.kvh * a.G + row % a.G) * DH;
 #pragma unroll 1
