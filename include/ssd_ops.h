@@ -152,7 +152,7 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * sizes that need none, or that the call refuses).  Its
  * contents need no initialisation and mean nothing afterwards; calls that may
  * overlap on the GPU need one each.  Each call can be captured into a CUDA
- * graph.  Inputs that these calls read from device memory (parents, done)
+ * graph.  Buffers overlap only where a call says so.  Inputs that these calls read from device memory (parents, done)
  * may hold any values, with the meanings below. */
 
 /* Attention of T drafted nodes over a cache of n_ctx rows.  1 <= T <= 1024,

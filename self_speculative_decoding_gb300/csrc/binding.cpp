@@ -31,6 +31,8 @@ struct Library {
   PyObject* error = nullptr;  // SSDError
 } lib;
 
+constexpr int kMostWidth = 256;  // of a selection (ssd_ops.h)
+
 // Thrown with a Python exception set.
 struct Refused {};
 
@@ -162,8 +164,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   {
     const Unlocked unlocked;
     const size_t need = lib.tree_workspace((int32_t)T, n_ctx, H, Hkv, dh);
-    if (!given) {
-      out = make(qkv, {T, res[1] > 0 ? res[1] : 0}, at::kBFloat16);
+    if (!given && need) {                        // (0: refused sizes)
+      out = make(qkv, res, at::kBFloat16);
       po = out.data_ptr();
     }
     const at::Tensor ws = make(qkv, {(int64_t)(need ? need : 256)}, at::kByte);
@@ -203,7 +205,7 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   ssd_status st;
   {
     const Unlocked unlocked;
-    kept = make(k, {k.size(0), keep > 0 ? keep : 0}, at::kInt);
+    kept = make(k, {k.size(0), keep > 0 && keep <= n ? keep : 0}, at::kInt);  // (else refused)
     st = lib.cache_evict(pk, pv, (const float*)pw, n, keep, sinks, recent, (int32_t)k.size(1),
                          (int32_t)k.size(0), (int32_t)k.size(2),
                          type == at::kBFloat16 ? SSD_DTYPE_BF16 : SSD_DTYPE_FP32, pko, pvo,
@@ -254,7 +256,7 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   {
     const Unlocked unlocked;
     const size_t need = lib.select_workspace((int32_t)B, (int32_t)V, W);
-    const int64_t w = W > 0 ? W : 0;
+    const int64_t w = W > 0 && W <= kMostWidth ? W : 0;  // (else refused)
     const at::Tensor ws = need ? make(z, {(int64_t)need}, at::kByte) : at::Tensor();
     tok = make(z, {w}, at::kInt);
     par = make(z, {w}, at::kInt);

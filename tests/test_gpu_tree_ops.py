@@ -591,3 +591,65 @@ def test_a_round_of_tree_decoding(ops):
         kept = ops.cache_evict(k, v, w, n, keep, ko, vo, wo, sinks=4, recent=len(path))
         np.testing.assert_array_equal(kept.cpu().numpy(), O.cache_evict(w.cpu().numpy(), n, keep, 4, len(path)))
         k, v, w, n = ko, vo, wo, keep
+
+
+# --------------------------------------------------------------------------
+# the binding
+
+
+def test_refused_sizes_allocate_nothing(ops):
+    from self_speculative_decoding_gb300 import SSDError
+    z, sc = torch.zeros(4, 100, device="cuda"), torch.zeros(4, device="cuda")
+    k = torch.zeros(2, 64, 64, device="cuda").bfloat16()
+    w = torch.zeros(2, 64, device="cuda")
+    par = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    now = torch.cuda.max_memory_allocated()
+    for width in (0, -1, 257, 2 ** 31 - 1):
+        with pytest.raises(SSDError):
+            ops.beam_select(z, sc, width)
+    for keep in (0, -5, 64, 2 ** 31 - 1):
+        with pytest.raises(SSDError):
+            ops.cache_evict(k, k, w, 63, keep, k.clone(), k.clone())
+    none = torch.zeros(0, 64, 64, device="cuda").bfloat16()
+    with pytest.raises(SSDError):
+        ops.tree_attention(torch.zeros(3, 384, device="cuda"), par, none, none, 10, 10, 6, 0, 64, 1e4)
+    assert torch.cuda.max_memory_allocated() - now < 1 << 20
+
+
+def test_two_threads_at_once(ops):
+    """Calls from two threads, each on its stream with tensors of its own."""
+    import threading
+    H, Hkv, dh, n, T = 8, 2, 64, 700, 9
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        qkv = torch.randn(T, (H + 2 * Hkv) * dh, generator=g, device="cuda")
+        k, v = (torch.randn(Hkv, n + T, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+        return qkv, torch.tensor([-1, 0, 0, 1, 1, 2, -1, 6, 7], dtype=torch.int32, device="cuda"), k, v
+    def step(x):
+        w = torch.zeros(Hkv, n + T, device="cuda")
+        out = ops.tree_attention(*x, n, n, H, Hkv, dh, 1e4, weights=w, weights_out=w)
+        ko, vo = torch.zeros_like(x[2]), torch.zeros_like(x[3])
+        kept = ops.cache_evict(x[2], x[3], w, n + T, 300, ko, vo, sinks=2, recent=9)
+        return out, w, kept, ko[:, :300], vo[:, :300]
+    data = [inputs(s) for s in (1, 2)]
+    want = [step(x) for x in data]
+    torch.cuda.synchronize()
+    bad, streams = [], [torch.cuda.Stream() for _ in data]
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(50):
+                    got = step(data[i])
+                    streams[i].synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        bad.append(i)
+        except Exception as e:
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
