@@ -43,14 +43,27 @@ SSD_DI float tree_row_lse(const TreeArgs& a, int kvh, int row) {
   if (a.splits == 1) return a.lse[(size_t)kvh * a.T * a.G + row];
   const int per = a.two ? a.items * 2 : 1;
   const size_t s0 = ((size_t)kvh * a.splits * per + (a.two ? row >> 7 : 0)) * 128 + (row & 127);
+  const bool present = a.depth[row / a.G] >= 0;
   float m = -INFINITY, l = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[s0 + (size_t)i * per * 128]);
-  const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-  for (int i = 0; i < a.splits; ++i)
-    l = fmaf(a.part_l[s0 + (size_t)i * per * 128], exp2f(a.part_m[s0 + (size_t)i * per * 128] - base), l);
-  return l != 0.f && a.depth[row / a.G] >= 0 ? m + log2f(l) : INFINITY;
+  // eight units' statistics in flight at once, the last ones' among them
+  for (int i0 = 0; i0 < a.splits; i0 += 8) {
+    float pm[8], pl[8], mn = m;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool got = i0 + u < a.splits;
+      const size_t at = s0 + (size_t)(i0 + u) * per * 128;
+      pm[u] = got ? a.part_m[at] : -INFINITY;
+      pl[u] = got ? a.part_l[at] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mn = fmaxf(mn, pm[u]);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    l *= exp2f(m - base);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) l = fmaf(pl[u], exp2f(pm[u] - base), l);
+    m = mn;
+  }
+  return l != 0.f && present ? m + log2f(l) : INFINITY;
 }
 
 // Joins of 32 rows each by eight parts of a warp: lane = row, each part an
@@ -70,6 +83,7 @@ SSD_DI void tree_join_rows(const TreeArgs& a, int index, int part) {
   const int per = a.two ? a.items * 2 : 1;       // slots per (head, split)
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
   const bool present = a.depth[t] >= 0, bad = *a.err != 0;
+  const bool marked = any_bad(a, kvh, lane);
   float m = -INFINITY;
 #pragma unroll 8
   for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * per) * 128 + r]);
@@ -78,24 +92,37 @@ SSD_DI void tree_join_rows(const TreeArgs& a, int index, int part) {
   float4 o[kChunks];
 #pragma unroll
   for (int q = 0; q < kChunks; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < a.splits; ++i) {
-    const size_t sl = s0 + (size_t)i * per;
-    const float w = exp2f(a.part_m[sl * 128 + r] - base);
-    l = fmaf(a.part_l[sl * 128 + r], w, l);
+  // four slots' values in flight at once, the last ones' among them
+  for (int i0 = 0; i0 < a.splits; i0 += 4) {
+    float4 v[4][kChunks];
+    float pm[4], pl[4];
 #pragma unroll
-    for (int q = 0; q < kChunks; ++q) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 +
-                                                        (size_t)(c0 + q) * 512 + r * 4);
-      o[q].x = fmaf(v.x, w, o[q].x);
-      o[q].y = fmaf(v.y, w, o[q].y);
-      o[q].z = fmaf(v.z, w, o[q].z);
-      o[q].w = fmaf(v.w, w, o[q].w);
+    for (int u = 0; u < 4; ++u) {
+      const bool got = i0 + u < a.splits;
+      const size_t sl = s0 + (size_t)(i0 + u) * per;
+      pm[u] = got ? a.part_m[sl * 128 + r] : -INFINITY;
+      pl[u] = got ? a.part_l[sl * 128 + r] : 0.f;
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q)
+        v[u][q] = got ? *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 +
+                                                         (size_t)(c0 + q) * 512 + r * 4)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = exp2f(pm[u] - base);
+      l = fmaf(pl[u], w, l);
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) {
+        o[q].x = fmaf(v[u][q].x, w, o[q].x);
+        o[q].y = fmaf(v[u][q].y, w, o[q].y);
+        o[q].z = fmaf(v[u][q].z, w, o[q].z);
+        o[q].w = fmaf(v[u][q].w, w, o[q].w);
+      }
     }
   }
   const float lse = l != 0.f ? m + log2f(l) : INFINITY;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  const bool marked = any_bad(a, kvh, lane);
   uint32_t packed[2 * kChunks];
 #pragma unroll
   for (int q = 0; q < kChunks; ++q) {

@@ -306,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       streams_sync();                            // the pass before has been read
       nlse[tid] = next;
       const int cols = min(256, rows - x.pair() * 256);
-      // (one tile has 128 columns, all of which count when the last 32 are read)
-      const bool some = streams_any(next == -INFINITY && tid < (cols + 31) / 32 * 32);
+      const bool some = streams_any(next == -INFINITY && tid < cols);
       const Pass y = x.next(a);
       if (!y.over()) next = row_lse(y);
       for (int j = s; j < x.cnt; j += 2, ++c) {
@@ -322,7 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           tc_fence_after();
           const uint32_t col = trow + (uint32_t)(buf * 128);
-          if (ctx && !some) {
+          // columns that all take part, 32 at a time; the others by selection
+          const int plain = ctx && !some ? cols & ~31 : 0;
+          if (plain) {
             // (a short loop: unrolled over 64 or 128 columns, with the next ones
             // loading meanwhile, it was slower by 2 to 25 us on 64 nodes over
             // 32768 rows)
@@ -340,16 +341,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             };
 #pragma unroll 1
-            for (int q = 0; q < cols; q += 32) {
+            for (int q = 0; q < plain; q += 32) {
               uint32_t v0[32];
               tmem_ld32_nw(col + (uint32_t)q, v0);
               tmem_wait_ld();
               tmem_pin32(v0);
               add(v0, q);
             }
-          } else {
-            const float part = masked_columns(a, col, nlse, x.pair() * 256, cols,
-                                              ctx ? -1 : (b - a.nb_ctx) * 4 + (warp & 3));
+          }
+          if (plain < cols) {
+            const float part =
+                masked_columns(a, col + (uint32_t)plain, nlse + plain, x.pair() * 256 + plain,
+                               cols - plain, ctx ? -1 : (b - a.nb_ctx) * 4 + (warp & 3));
             sum[0] = tree_add2(sum[0], (uint64_t)__float_as_uint(part));
           }
         }
