@@ -572,47 +572,64 @@ SSD_DI void score_weights(const TreeArgs& a, int index) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = a.T * a.G;
   const int pairs = (a.nb + 1) / 2, kvh = index / pairs;
   const int b = (index - kvh * pairs) * 2 + (threadIdx.x >> 7), k = threadIdx.x & 127;
-  const bool bad = *a.err != 0;
+  const bool bad = *a.err != 0, ctx = b < a.nb_ctx;
+  const int key = ctx ? b * kTreeKeys + k : a.n + (b - a.nb_ctx) * kTreeKeys + k;
+  const bool live = b < a.nb && key < (ctx ? a.n : a.n + a.T);
+  const float* ps = a.part_s + ((size_t)kvh * a.nb + b) * rows * kTreeKeys + k;
+  const size_t o = (size_t)kvh * a.max_seq + key;
+  // the first rows' scores are on their way meanwhile
+  constexpr int kFirst = 8;
+  float first[kFirst];
+#pragma unroll
+  for (int row = 0; row < kFirst; ++row)
+    first[row] = live && row < rows ? ps[(size_t)row * kTreeKeys] : 0.f;
+  const float before = live && ctx && a.w_in ? a.w_in[o] : 0.f;
   for (int row = warp; row < rows; row += kJoinWarps) {
+    const bool present = a.depth[row / a.G] >= 0;
     float lse;
     if (a.splits == 1) {
       lse = a.lse[(size_t)kvh * rows + row];
     } else {
       const size_t s0 = (size_t)kvh * a.splits * 128 + row;
-      float m = -INFINITY, l = 0.f;
-      for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, a.part_m[s0 + (size_t)i * 128]);
+      float m = -INFINITY, l = 0.f;              // of the lane's units, then of all
+      for (int i = lane; i < a.splits; i += 32) {
+        const float pm = a.part_m[s0 + (size_t)i * 128], pl = a.part_l[s0 + (size_t)i * 128];
+        const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.f : mn;
+        l = l * exp2f(m - base) + pl * exp2f(pm - base);
+        m = mn;
+      }
+      float all = m;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float base = m == -INFINITY ? 0.f : m;
-      for (int i = lane; i < a.splits; i += 32)
-        l = fmaf(a.part_l[s0 + (size_t)i * 128], exp2f(a.part_m[s0 + (size_t)i * 128] - base), l);
+      for (int d = 16; d; d >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
+      l *= exp2f(m - (all == -INFINITY ? 0.f : all));
 #pragma unroll
       for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      lse = l != 0.f && a.depth[row / a.G] >= 0 ? m + log2f(l) : INFINITY;
+      lse = l != 0.f && present ? all + log2f(l) : INFINITY;
     }
     if (lane == 0) s_lse[row] = bad ? NAN : lse;
   }
   __syncthreads();
-  const bool ctx = b < a.nb_ctx;
-  const int key = ctx ? b * kTreeKeys + k : a.n + (b - a.nb_ctx) * kTreeKeys + k;
-  if (b >= a.nb || key >= (ctx ? a.n : a.n + a.T)) return;
-  const float* ps = a.part_s + ((size_t)kvh * a.nb + b) * rows * kTreeKeys + k;
+  if (!live) return;
   float sum = 0.f;
-#pragma unroll 8
-  for (int row = 0; row < rows; ++row) {
-    const float lse = s_lse[row], p = tree_ex2(fmaf(ps[(size_t)row * kTreeKeys], a.scale_log2, -lse));
+  auto add = [&](int row, float score) {
+    const float lse = s_lse[row], p = tree_ex2(fmaf(score, a.scale_log2, -lse));
     if (lse != INFINITY) sum += p;               // absent rows take no part
-  }
-  const size_t o = (size_t)kvh * a.max_seq + key;
-  a.w_out[o] = ctx && a.w_in ? a.w_in[o] + sum : sum;
+  };
+#pragma unroll
+  for (int row = 0; row < kFirst; ++row)
+    if (row < rows) add(row, first[row]);
+#pragma unroll 8
+  for (int row = kFirst; row < rows; ++row) add(row, ps[(size_t)row * kTreeKeys]);
+  a.w_out[o] = before + sum;
 }
 
-// Many slots and few rows: CTA = one 16-byte column of 32 rows, each warp
-// adds every eighth slot, then the warps' sums are added in order.
+// Many slots and few rows: CTA = one 16-byte column of 32 rows; each warp adds
+// every eighth slot under the maximum of its own, then the warps' sums are
+// added in order.
 template <int DH>
 SSD_DI void join_column(const TreeArgs& a, int index) {
   __shared__ float4 s_o[kJoinWarps][32];
-  __shared__ float s_l[kJoinWarps][32];
+  __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = a.T * a.G, blocks = (rows + 31) / 32;
   const int c = index % (DH / 4), row0 = (index / (DH / 4)) % blocks * 32;
@@ -620,38 +637,63 @@ SSD_DI void join_column(const TreeArgs& a, int index) {
   const int tile = row >> 7, r = row & 127, t = row / a.G, per = a.two ? a.items * 2 : 1;
   const size_t s0 = (size_t)kvh * a.splits * per + (a.two ? tile : 0);
   const bool present = a.depth[t] >= 0, bad = *a.err != 0;
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_m[(s0 + (size_t)i * per) * 128 + r]);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  const bool marked = any_bad(a, kvh, lane);
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = warp; i < a.splits; i += kJoinWarps) {
-    const size_t sl = s0 + (size_t)i * per;
-    const float w = exp2f(a.part_m[sl * 128 + r] - base);
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 + (size_t)c * 512 + r * 4);
-    l = fmaf(a.part_l[sl * 128 + r], w, l);
+  // four slots in flight at once, the last ones among them
+  constexpr int kBatch = 4;
+  for (int i0 = warp; i0 < a.splits; i0 += kBatch * kJoinWarps) {
+    float pm[kBatch], pl[kBatch], mn = m;
+    float4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kJoinWarps;
+      const bool got = i < a.splits;
+      const size_t sl = s0 + (size_t)i * per;
+      pm[u] = got ? a.part_m[sl * 128 + r] : -INFINITY;
+      pl[u] = got ? a.part_l[sl * 128 + r] : 0.f;
+      v[u] = got ? *reinterpret_cast<const float4*>(a.part_o + sl * DH * 128 + (size_t)c * 512 + r * 4)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, pm[u]);
+    const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
+    l *= old;
+    o.x *= old;
+    o.y *= old;
+    o.z *= old;
+    o.w *= old;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float w = exp2f(pm[u] - base);
+      l = fmaf(pl[u], w, l);
+      o.x = fmaf(v[u].x, w, o.x);
+      o.y = fmaf(v[u].y, w, o.y);
+      o.z = fmaf(v[u].z, w, o.z);
+      o.w = fmaf(v[u].w, w, o.w);
+    }
+    m = mn;
+  }
+  s_o[warp][lane] = o;
+  s_l[warp][lane] = l;
+  s_m[warp][lane] = m;
+  __syncthreads();
+  if (warp) return;
+  for (int i = 1; i < kJoinWarps; ++i) m = fmaxf(m, s_m[i][lane]);
+  const float base = m == -INFINITY ? 0.f : m;
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kJoinWarps; ++i) {
+    const float4 v = s_o[i][lane];
+    const float w = exp2f(s_m[i][lane] - base);
+    l = fmaf(s_l[i][lane], w, l);
     o.x = fmaf(v.x, w, o.x);
     o.y = fmaf(v.y, w, o.y);
     o.z = fmaf(v.z, w, o.z);
     o.w = fmaf(v.w, w, o.w);
   }
-  s_o[warp][lane] = o;
-  s_l[warp][lane] = l;
-  __syncthreads();
-  if (warp) return;
-  for (int i = 1; i < kJoinWarps; ++i) {
-    const float4 v = s_o[i][lane];
-    l += s_l[i][lane];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
-  }
   const float lse = l != 0.f ? m + log2f(l) : INFINITY, inv = l != 0.f ? 1.f / l : 0.f;
   float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  const bool marked = any_bad(a, kvh, lane);
   if (!present)
     v[0] = v[1] = v[2] = v[3] = 0.f;
   else if (marked)
