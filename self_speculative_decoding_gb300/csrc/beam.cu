@@ -20,43 +20,37 @@ constexpr int kMergeThreads = 1024;
 constexpr int kMaxCluster = 8;      // portable cluster size
 constexpr int kList = 1024;         // candidates over the threshold that are ranked at once
 
+// Floats as unsigned integers in the same order (-0 as +0; no NaN).
+SSD_DI uint32_t float_order(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+SSD_DI float order_float(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+
 // (logit, token) as one key: larger logit first, then lower token; 0 stands
 // for no candidate (NaN and -infinity are none).
 SSD_DI uint64_t logit_key(float z, int token) {
   if (!(z > -INFINITY)) return 0;
-  const uint32_t u = __float_as_uint(z + 0.f);
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return ((uint64_t)o << 32) | (uint32_t)~token;
+  return ((uint64_t)float_order(z) << 32) | (uint32_t)~token;
 }
-SSD_DI float key_logit(uint64_t k) {
-  const uint32_t o = (uint32_t)(k >> 32);
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
-}
+SSD_DI float key_logit(uint64_t k) { return order_float((uint32_t)(k >> 32)); }
 SSD_DI int key_token(uint64_t k) { return (int)~(uint32_t)k; }
 
-// The W-th largest of G group maxima (W <= G; equal ones ordered by group):
-// at least W values are at or over it, and few more.  All threads of the
-// block call it with their group's maximum (threads of a group are adjacent)
-// and get it; each group's rank is counted by its threads together.
-template <int G, int kThreads>
-SSD_DI float group_cut(float gmax, int W, float* gm, float* cut) {
-  constexpr int kPer = kThreads / G;             // threads of a group
-  static_assert(kPer >= 1 && kPer <= 32 && (G / kPer) % 4 == 0, "group shape");
-  const int g = threadIdx.x / kPer, q = threadIdx.x % kPer;
-  if (q == 0) gm[g] = gmax;
-  __syncthreads();
-  int rank = 0;
-#pragma unroll 4
-  for (int i = q * (G / kPer); i < (q + 1) * (G / kPer); i += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(gm + i);
-    rank += (o.x > gmax || (o.x == gmax && i < g)) + (o.y > gmax || (o.y == gmax && i + 1 < g)) +
-            (o.z > gmax || (o.z == gmax && i + 2 < g)) + (o.w > gmax || (o.w == gmax && i + 3 < g));
+// A value that W of the block's threads reach (each with the maximum of its
+// own, not NaN) and that few others do: the W-th largest to its first kBits
+// bits, one vote of the block for each; -infinity where fewer than W have any.
+template <int kBits>
+SSD_DI float block_cut(float mine, int W) {
+  const uint32_t o = float_order(mine);
+  uint32_t t = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 32 - kBits; --bit) {
+    const uint32_t c = t | (1u << bit);
+    if (__syncthreads_count(o >= c) >= W) t = c;
   }
-#pragma unroll
-  for (int d = 1; d < kPer; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
-  if (q == 0 && rank == W - 1) *cut = gmax;
-  __syncthreads();
-  return *cut;
+  return t > float_order(-INFINITY) ? order_float(t) : -INFINITY;
 }
 
 // The W largest of n logits by bisection of the W-th largest key, bit by bit
@@ -90,11 +84,11 @@ __device__ __noinline__ int piece_bisect(const float* row, int v0, int n, int W,
 }
 
 // Piece `piece` of row b: its W largest keys to its list, largest first.  The
-// logits stay in registers; what lies at or over the W-th largest
-// of G group maxima is listed and ranked.
-template <int G, int kItems>
+// logits stay in registers; what reaches the W-th largest of the threads'
+// maxima is listed and ranked.
+template <int kItems>
 SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* out,
-                        uint64_t* list, float* gm, float& s_cut, int& s_n) {
+                        uint64_t* list, int& s_n) {
   const int tid = threadIdx.x;
   if (a.done && a.done[b]) return;               // the merge does not read its lists
   const int v0 = piece * len, n = min(len, a.V - v0);
@@ -108,10 +102,8 @@ SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* 
   }
 #pragma unroll
   for (int i = 0; i < kItems; ++i) mx = fmaxf(mx, z[i]);  // ignores NaN
-#pragma unroll
-  for (int d = 1; d < kPieceThreads / G; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
   if (tid == 0) s_n = 0;
-  const float cut = group_cut<G, kPieceThreads>(mx, a.W, gm, &s_cut);
+  const float cut = block_cut<24>(mx, a.W);
 #pragma unroll
   for (int i = 0; i < kItems; ++i)
     if (z[i] >= cut && z[i] > -INFINITY) {
@@ -137,26 +129,23 @@ SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* 
 // A short piece has code of its own: what runs once is bound by its fetching
 // (4 beams of 1024 logits 9.6 us with the long one, 8.1).
 constexpr int kFewItems = 4;
-template <int G>
-SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out) {
-  __shared__ uint64_t list[kList];
-  __shared__ __align__(16) float gm[G];
-  __shared__ float s_cut;
+SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out,
+                       uint64_t* list) {
   __shared__ int s_n;
   if (len <= kFewItems * kPieceThreads)
-    piece_items<G, kFewItems>(a, len, piece, b, out, list, gm, s_cut, s_n);
+    piece_items<kFewItems>(a, len, piece, b, out, list, s_n);
   else
-    piece_items<G, kPieceItems>(a, len, piece, b, out, list, gm, s_cut, s_n);
+    piece_items<kPieceItems>(a, len, piece, b, out, list, s_n);
 }
 
 // CTA = (piece of a row, beam).  48 rows of 128003 logits (24.6 MB) take 11 us:
 // the loads 6 of them (4 bytes each, since rows begin anywhere; all of a
 // thread's in flight at once), then the threshold, the list and its ranks.
-template <int G>
 __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
+  __shared__ uint64_t list[kList];
   pdl_trigger();
-  piece_body<G>(a, len, blockIdx.x, blockIdx.y,
-                a.lists + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * a.W);
+  piece_body(a, len, blockIdx.x, blockIdx.y,
+             a.lists + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * a.W, list);
 }
 
 // A candidate in the whole order: the 64-bit score as an ordered integer
@@ -223,23 +212,22 @@ SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool
   if (a.done_out) a.done_out[w] = !got || token == a.end_id;
 }
 
-// One CTA: the W best of all lists, which are sorted.  The lists' first
-// entries (their first few, where there are fewer lists than W) are W
-// candidates at least, so the W-th largest of their lower bounds, or of the
-// bounds' maxima over 256 groups, is a threshold that W candidates reach; the
-// entries of each list whose upper bound reaches it are collected and ranked
-// by the whole order, eight threads to a candidate (48 beams of 128003 logits
-// 18.3 us in all, 21.2 with one thread to each).  Bound by latency, about 6 us
-// for 288 lists: two rounds of reads of L2, threshold and ranks between them;
-// holding the lists' first entries in shared memory was slower (22.1 against
-// 21.2).  WAIT: the lists come from the kernel before.
+// One CTA: the W best of all lists, which are sorted.  The W-th largest of the
+// threads' maxima over the lists' first eight entries (of lower bounds of their
+// scores) is a threshold that W candidates reach; the entries of each list
+// whose upper bound reaches it are collected and ranked by the whole order,
+// eight threads to a candidate (48 beams of 128003 logits 18.3 us in all, 21.2
+// with one thread to each).  Where a few lists hold most of the best, too many
+// reach it: then every entry that does counts towards a second threshold (128
+// of 128 uneven beams of 32000 logits 21 us; one maximum after the other, what
+// is left for more than 1024 equal scores, took 715).
+// Bound by latency, about 6 us for 288 lists: two rounds of reads of L2, the
+// threshold and the ranks; holding the lists' first entries in shared memory
+// was slower (22.1 against 21.2).  WAIT: the lists come from the kernel before.
 template <int kThreads, bool WAIT>
-SSD_DI void merge_body(const BeamArgs& a, int pieces) {
-  constexpr int kGroups = 256, kPer = kThreads / kGroups;
-  __shared__ Cand list[kList];
+SSD_DI void merge_body(const BeamArgs& a, int pieces, Cand* list) {
   __shared__ Beam beams[256];
-  __shared__ __align__(16) float gm[kGroups];
-  __shared__ float s_cut;
+  __shared__ uint32_t gm[kThreads];
   __shared__ int s_n;
   const int tid = threadIdx.x, lists = a.B * pieces;
   if (tid < a.B) {
@@ -247,45 +235,57 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
     beams[tid].lse = a.lse ? a.lse[(size_t)tid * a.lse_stride] : 0.f;
     beams[tid].ended = a.done && a.done[tid];
   }
-  if (tid == 0) s_n = 0;
+  gm[tid] = 0u;
   if (WAIT) pdl_wait();                          // (the beams are not the pieces' work)
   __syncthreads();
-  // sample j: entry j / lists of list j % lists; 256 in a row go to 256 groups
-  const int deep = min(a.W, (a.W + lists - 1) / lists), samples = lists * deep;
+  // eight lanes go through a list together
   float mx = -INFINITY;
 #pragma unroll 2
-  for (int j = tid / kPer + kGroups * (tid % kPer); j < samples; j += kThreads) {
-    const int d = j / lists, i = j - d * lists;
-    const uint64_t k = entry(a, beams, pieces, i, d);
+  for (int i = tid >> 3; i < lists; i += kThreads / 8) {
+    const int d = tid & 7;
+    const uint64_t k = d < a.W ? entry(a, beams, pieces, i, d) : 0;
     float lo, up;
     score_bounds(beams[i / pieces], k, lo, up);
     if (k) mx = fmaxf(mx, lo);
   }
-#pragma unroll
-  for (int d = 1; d < kThreads / kGroups; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-  const float cut = group_cut<kGroups, kThreads>(mx, a.W, gm, &s_cut);
-  // eight lanes walk a list together
-  for (int i = tid >> 3; i < lists; i += kThreads / 8) {
-    for (int d0 = 0; d0 < a.W; d0 += 8) {
-      const int d = d0 + (tid & 7);
-      bool in = false;
-      const uint64_t k = d < a.W ? entry(a, beams, pieces, i, d) : 0;
-      if (k) {
-        float lo, up;
-        score_bounds(beams[i / pieces], k, lo, up);
-        Cand c;
-        in = up >= cut;
-        if (in && score(beams[i / pieces], k, i / pieces, c)) {
-          const int at = atomicAdd(&s_n, 1);
-          if (at < kList) list[at] = c;
+  float cut = block_cut<32>(mx, a.W);
+  int cnt = 0;
+#pragma unroll 1
+  for (int turn = 0; turn < 3; ++turn) {
+    // 0 and 2: collect; 1: the second threshold
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+    for (int i = tid >> 3; i < lists; i += kThreads / 8) {
+      for (int d0 = 0; d0 < a.W; d0 += 8) {
+        const int d = d0 + (tid & 7);
+        bool in = false;
+        const uint64_t k = d < a.W ? entry(a, beams, pieces, i, d) : 0;
+        if (k) {
+          float lo, up;
+          score_bounds(beams[i / pieces], k, lo, up);
+          in = up >= cut;
+          Cand c;
+          if (in && turn == 1) {
+            atomicMax(&gm[((size_t)i * a.W + d) % kThreads], float_order(lo));
+          } else if (in && score(beams[i / pieces], k, i / pieces, c)) {
+            const int at = atomicAdd(&s_n, 1);
+            if (at < kList) list[at] = c;
+          }
         }
+        const unsigned group = 0xffu << (tid & 24);
+        if (__ballot_sync(group, in) != group) break;
       }
-      const unsigned group = 0xffu << (tid & 24);
-      if (__ballot_sync(group, in) != group) break;
     }
+    __syncthreads();
+    if (turn == 1) {
+      const uint32_t o = gm[tid];
+      cut = fmaxf(cut, block_cut<32>(o ? order_float(o) : -INFINITY, a.W));
+      continue;
+    }
+    cnt = s_n;
+    if (cnt <= kList) break;
+    __syncthreads();                             // s_n is read
   }
-  __syncthreads();
-  const int cnt = s_n;
   if (cnt <= kList) {
     for (int i = tid >> 3; i < ((cnt + 3) & ~3); i += kThreads / 8) {
       const Cand c = list[min(i, cnt - 1)];
@@ -330,19 +330,20 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces) {
 }
 
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArgs a, int pieces) {
-  merge_body<kMergeThreads, true>(a, pieces);
+  __shared__ Cand list[kList];
+  merge_body<kMergeThreads, true>(a, pieces, list);
 }
 
 // Few pieces: one cluster holds them all, and its first CTA merges the lists
 // out of the others' shared memory (one launch instead of two, no workspace).
-template <int G>
 __global__ void __launch_bounds__(kPieceThreads, 1) beam_cluster_kernel(const BeamArgs a, int len) {
-  constexpr int kMost = G == 128 ? 64 : 256;     // W at most
+  constexpr int kMost = 256;                     // W at most
   __shared__ uint64_t mine[kMost];
   __shared__ uint64_t all[kMaxCluster * kMost];
+  __shared__ Cand list[kList];                   // and the piece's keys before
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  piece_body<G>(a, len, blockIdx.x, blockIdx.y, mine);
+  piece_body(a, len, blockIdx.x, blockIdx.y, mine, reinterpret_cast<uint64_t*>(list));
   cluster.sync();
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < (int)cluster.num_blocks() * a.W; i += kPieceThreads)
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) beam_cluster_kernel(const Be
   if (blockIdx.x || blockIdx.y) return;
   BeamArgs b = a;
   b.lists = all;
-  merge_body<kPieceThreads, false>(b, gridDim.x);
+  merge_body<kPieceThreads, false>(b, gridDim.x, list);
 }
 
 // Reordering by source: a tile of 1024 16-byte units of one group's rows is
@@ -425,11 +426,9 @@ cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s) {
     attr[0].val.clusterDim.y = a.B;
     attr[0].val.clusterDim.z = 1;
     lc.numAttrs = 1;
-    return a.W <= 64 ? cudaLaunchKernelEx(&lc, beam_cluster_kernel<128>, a, len)
-                     : cudaLaunchKernelEx(&lc, beam_cluster_kernel<256>, a, len);
+    return cudaLaunchKernelEx(&lc, beam_cluster_kernel, a, len);
   }
-  cudaError_t e = a.W <= 64 ? cudaLaunchKernelEx(&lc, beam_piece_kernel<128>, a, len)
-                            : cudaLaunchKernelEx(&lc, beam_piece_kernel<256>, a, len);
+  cudaError_t e = cudaLaunchKernelEx(&lc, beam_piece_kernel, a, len);
   if (e != cudaSuccess) return e;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -407,6 +407,19 @@ def test_select(ops, B, V, W, ended):
     check_select(ops, z, (-rng.exponential(size=B)).astype(np.float32), W, lse, done, V - 1 if ended else -1)
 
 
+@pytest.mark.parametrize("B,V,W", [(128, 5000, 128), (200, 1500, 256), (64, 9000, 64), (3, 30000, 200),
+                                   (16, 2500, 256), (2, 900, 256)])
+@pytest.mark.parametrize("kind", ["spread", "first", "offset", "one"])
+def test_select_uneven_beams(ops, B, V, W, kind):
+    """A few beams hold most of the best: spread scores, a first step (one beam
+    far above the others, or alone), scores far from zero."""
+    rng = np.random.default_rng(B + W)
+    z = rng.standard_normal((B, V)).astype(np.float32) * 2
+    scores = {"spread": -3 * rng.random(B), "first": np.where(np.arange(B) == B // 2, 0, -1e9),
+              "offset": -1000 - rng.random(B) * 1e-3, "one": np.where(np.arange(B) == 0, 0, -np.inf)}[kind]
+    check_select(ops, z, scores.astype(np.float32), W)
+
+
 def test_select_ties_specials_and_sorted_rows(ops):
     rng = np.random.default_rng(8)
     B, V, W = 6, 9001, 40
