@@ -53,34 +53,17 @@ SSD_DI float block_cut(float mine, int W) {
   return t > float_order(-INFINITY) ? order_float(t) : -INFINITY;
 }
 
-// The W largest of n logits by bisection of the W-th largest key, bit by bit
-// (many equal logits, or few finite ones); keys differ, so there are exactly W.
-__device__ __noinline__ int piece_bisect(const float* row, int v0, int n, int W, uint64_t* list,
-                                         int* s_n) {
-  const int tid = threadIdx.x;
-  uint64_t t = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const uint64_t c = t | (1ull << bit);
-    int k = 0;
-    for (int v = tid; v < n; v += kPieceThreads) k += logit_key(row[v], v0 + v) >= c;
+// Sum of the block's values; `turn` (0, 1, 0, ...) differs from the last call's.
+SSD_DI int block_sum(int x, int turn) {
+  constexpr int kWarps = kPieceThreads / 32;
+  __shared__ int part[2][kWarps];
+  const int all = __reduce_add_sync(~0u, x);
+  if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = all;
+  __syncthreads();
+  int sum = 0;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) k += __shfl_xor_sync(~0u, k, d);
-    __syncthreads();
-    if (tid == 0) *s_n = 0;
-    __syncthreads();
-    if ((tid & 31) == 0) atomicAdd(s_n, k);
-    __syncthreads();
-    if (*s_n >= W) t = c;
-  }
-  __syncthreads();
-  if (tid == 0) *s_n = 0;
-  __syncthreads();
-  for (int v = tid; v < n; v += kPieceThreads) {
-    const uint64_t k = logit_key(row[v], v0 + v);
-    if (k >= t && k) list[atomicAdd(s_n, 1)] = k;
-  }
-  __syncthreads();
-  return *s_n;
+  for (int i = 0; i < kWarps; ++i) sum += part[turn][i];
+  return sum;
 }
 
 // Piece `piece` of row b: its W largest keys to its list, largest first.  The
@@ -112,7 +95,42 @@ SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* 
     }
   __syncthreads();
   int cnt = s_n;
-  if (cnt > kList) cnt = piece_bisect(row, v0, n, a.W, list, &s_n);
+  if (cnt > kList) {
+    // many equal logits (a vocabulary masked by the type's lowest value): the
+    // W-th largest exactly, by its bits, then of its equals the lowest tokens
+    uint32_t t = 0;
+    int turn = 0, over = 0, m = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit, turn ^= 1) {
+      const float c = order_float(t | (1u << bit));
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) k += z[i] >= c;
+      if (block_sum(k, turn) >= a.W) t |= 1u << bit;
+    }
+    const float last = order_float(t);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) over += z[i] > last;
+    const int need = a.W - block_sum(over, turn);
+    turn ^= 1;
+#pragma unroll 1
+    for (int bit = 14; bit >= 0; --bit, turn ^= 1) {  // (a piece has under 2^15 logits)
+      const int c = m | (1 << bit);
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) k += z[i] == last && i * kPieceThreads + tid < c;
+      if (block_sum(k, turn) < need) m = c;
+    }
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int v = i * kPieceThreads + tid;
+      if (z[i] > last || (z[i] == last && v <= m)) list[atomicAdd(&s_n, 1)] = logit_key(z[i], v0 + v);
+    }
+    __syncthreads();
+    cnt = s_n;
+  }
   // keys differ, so each key's rank is its place
   // (counted by four threads together)
   for (int i = tid >> 2; i < ((cnt + 7) & ~7); i += kPieceThreads / 4) {
@@ -266,7 +284,9 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces, Cand* list) {
           in = up >= cut;
           Cand c;
           if (in && turn == 1) {
-            atomicMax(&gm[((size_t)i * a.W + d) % kThreads], float_order(lo));
+            // (a multiple of W by itself would meet few places where W is even)
+            const uint32_t place = ((uint32_t)i * (uint32_t)a.W + (uint32_t)d) * 2654435769u;
+            atomicMax(&gm[place / (0x80000000u / (kThreads / 2))], float_order(lo));
           } else if (in && score(beams[i / pieces], k, i / pieces, c)) {
             const int at = atomicAdd(&s_n, 1);
             if (at < kList) list[at] = c;
@@ -298,20 +318,37 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces, Cand* list) {
     for (int w = cnt + tid; w < a.W; w += kThreads) put(a, beams, w, Cand{}, false);
     return;
   }
-  // many equal scores: W maxima in turn, each below the one before
+  // many equal scores: W maxima in turn; each thread has the first candidate of
+  // its lists that is left (a list of its own: entry `next`)
   const Cand none = {0, 0, 1 << 30};
-  Cand last = {~0ull, ~0ull, -1};
-  for (int w = 0; w < a.W; ++w) {
-    Cand c = none;
-    for (int i = tid; i < lists; i += kThreads)
-      for (int d = 0; d < a.W; ++d) {
-        const uint64_t k = entry(a, beams, pieces, i, d);
-        Cand x;
-        if (!k || !score(beams[i / pieces], k, i / pieces, x)) break;  // the list's end
-        if (!before(last, x)) continue;
-        if (before(x, c)) c = x;
-        break;                                   // the rest of the list comes after
+  Cand own = none, last = {~0ull, ~0ull, -1};
+  int next = 0;
+  auto find = [&]() {
+    own = none;
+    for (int i = tid; i < lists; i += kThreads) {
+      const int b = i / pieces;
+      Cand x;
+      int d = next;
+      if (lists > kThreads) {                    // the first entry after the last candidate
+        int top = a.W;
+        d = 0;
+        while (d < top) {
+          const int mid = (d + top) >> 1;
+          const uint64_t k = entry(a, beams, pieces, i, mid);
+          if (k && score(beams[b], k, b, x) && !before(last, x))
+            d = mid + 1;
+          else
+            top = mid;
+        }
       }
+      const uint64_t k = d < a.W ? entry(a, beams, pieces, i, d) : 0;
+      if (k && score(beams[b], k, b, x) && before(x, own)) own = x;
+    }
+  };
+  find();
+#pragma unroll 1
+  for (int w = 0; w < a.W; ++w) {
+    Cand c = own;
     for (int d = 16; d; d >>= 1) {
       Cand x;
       x.s = __shfl_xor_sync(~0u, c.s, d);
@@ -326,6 +363,10 @@ SSD_DI void merge_body(const BeamArgs& a, int pieces, Cand* list) {
       if (before(list[i], c)) c = list[i];
     if (tid == 0) put(a, beams, w, c, c.k != 0);
     last = c;
+    if (c.k && own.k == c.k && own.b == c.b) {
+      ++next;
+      find();
+    }
   }
 }
 

@@ -420,6 +420,34 @@ def test_select_uneven_beams(ops, B, V, W, kind):
     check_select(ops, z, scores.astype(np.float32), W)
 
 
+@pytest.mark.parametrize("B,V,W", [(2, 1500, 7), (5, 30000, 48), (60, 5000, 60), (150, 4500, 256), (3, 25000, 130)])
+@pytest.mark.parametrize("kind", ["lowest", "equal", "coarse", "zeros", "infinite"])
+def test_select_with_few_different_logits(ops, B, V, W, kind):
+    """A vocabulary masked by the type's lowest value, equal logits: more
+    candidates share a score than are ranked at once."""
+    rng = np.random.default_rng(V + W)
+    z = {"lowest": np.full((B, V), np.finfo(np.float32).min), "equal": np.full((B, V), -2.5),
+         "coarse": rng.integers(0, 3, (B, V)) * 0.5, "zeros": np.where(rng.random((B, V)) < 0.5, 0.0, -0.0),
+         "infinite": np.where(rng.random((B, V)) < 0.001, 1.0, -np.inf)}[kind].astype(np.float32)
+    if kind == "lowest":
+        z[:, rng.integers(0, V, 3)] = 1.5
+        z[0, V - 1] = 2.0
+    check_select(ops, z, np.where(np.arange(B) % 3 == 1, -1.0, 0.0).astype(np.float32), W)
+
+
+def test_select_equal_logits_of_many_beams(ops):
+    B, V, W = 256, 100000, 200                     # more lists than a block has threads
+    z = torch.zeros(B, V, device="cuda")
+    z[200, 5] = 1.0
+    sc = -(torch.arange(B, device="cuda") % 7).float()
+    tok, par, best, _ = ops.beam_select(z, sc - torch.where(torch.arange(B, device="cuda") == 0, 0.5, 0.0), W)
+    # beam 7 is the first of those at 0; beam 200 is at -4, its token 5 at -3
+    assert tok.tolist() == list(range(W)) and par.tolist() == [7] * W and (best == 0).all()
+    z[7, 100:] = -9.0                              # a hundred of beam 7, then of beam 14
+    tok, par, best, _ = ops.beam_select(z, sc - torch.where(torch.arange(B, device="cuda") == 0, 0.5, 0.0), W)
+    assert tok.tolist() == list(range(100)) * 2 and par.tolist() == [7] * 100 + [14] * 100 and (best == 0).all()
+
+
 def test_select_ties_specials_and_sorted_rows(ops):
     rng = np.random.default_rng(8)
     B, V, W = 6, 9001, 40
