@@ -40,6 +40,10 @@ def make_tree(kind, T, rng):
         return [-1] * T
     if kind == "none":
         return [-2] * T
+    if kind == "broken":  # a chain with an end that is none
+        return [i - 1 if i != T // 3 else T for i in range(T)]
+    if kind == "comb":  # a long spine, each node with a leaf
+        return [i - 1 if i % 2 else max(i - 2, -1) for i in range(T)]
     if kind == "bad":  # values out of range, self-loops, forward edges
         p = [-1] + [int(rng.integers(0, i)) for i in range(1, T)]
         for i, bad in ((1, 1), (2, 5000), (T // 2, T // 2 + 1), (T - 1, -7), (T // 3, 2 ** 31 - 1)):
@@ -126,7 +130,8 @@ def test_tree_attention(ops, H, Hkv, dh, n, T, kind):
     (2, 2, 128, 200, 127, "tree"), (2, 2, 128, 200, 128, "tree"), (2, 2, 64, 200, 129, "bushy"),
     (4, 2, 128, 70, 255, "tree-padded"), (2, 1, 64, 0, 513, "tree"), (2, 1, 128, 300, 1024, "chain"),
     (16, 1, 128, 1500, 40, "tree"), (1, 1, 64, 4100, 9, "tree"), (40, 40, 128, 700, 3, "tree"),
-    (64, 8, 128, 2500, 1, "tree"), (33, 11, 64, 129, 2, "chain")])
+    (64, 8, 128, 2500, 1, "tree"), (33, 11, 64, 129, 2, "chain"), (2, 1, 64, 90, 34, "chain"),
+    (2, 1, 64, 90, 300, "broken"), (2, 2, 64, 140, 701, "comb"), (1, 1, 128, 3, 1024, "broken")])
 def test_tree_attention_sizes(ops, H, Hkv, dh, n, T, kind):
     c = Case(H, Hkv, dh, n, T, kind, spare=0)
     c.check(c.call(ops))
