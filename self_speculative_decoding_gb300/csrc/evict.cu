@@ -8,6 +8,7 @@
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
+#include "tree.cuh"
 
 namespace ssd {
 namespace {
@@ -360,11 +361,16 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const int middle = a.n - a.sinks - a.recent, want = a.keep - a.sinks - a.recent;
   // Few rows that stay: the selecting CTA copies them (one launch).
   const bool few = (long long)a.keep * a.units <= kFusedUnits && a.keep <= kFusedRows;
-  // A CTA per 8192 middle rows up to the portable cluster size: the exchange
-  // of histograms costs a cluster more than a CTA's longer runs (40 heads of
-  // 4095 rows: 12 us with one CTA per head, 25 us with four).
+  // A CTA per 4096 middle rows up to the portable cluster size (8 heads of 16000
+  // rows 18.9 us so, 20.9 with one per 8192; 40 heads of 4095 rows 16.4, 18 with
+  // two CTAs a head), while no SM gets a second one (32 heads of 32768 rows 31.7
+  // us with four CTAs a head, 49.5 with eight; 40 heads of 20000 rows 25.1 with
+  // two, 29 with four) or a CTA has more rows than it holds (80 heads of 65536
+  // rows 72 us with four, 95 with one, 104 with eight).
   int nc = 1;
-  while (nc < kMaxCluster && (long long)nc * 8192 < middle) nc *= 2;
+  while (nc < kMaxCluster && (long long)nc * 4096 < middle &&
+         (2LL * nc * a.Hkv <= tree_sms() || (long long)nc * kChunk < middle))
+    nc *= 2;
   const bool fused = few && nc == 1;
   const int share = (middle + nc - 1) / nc;
   const bool ranked = want == 0 || (nc == 1 && share <= kRankKeys);
