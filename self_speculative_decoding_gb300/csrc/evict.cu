@@ -20,8 +20,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCopies = 8;          // of the first histogram: lane l counts in copy l % 8
 constexpr int kItems = 16;          // keys per thread that stay in shared memory
 constexpr int kChunk = kSelThreads * kItems;
-constexpr int kRankKeys = 512;      // at most so many middle rows are ranked by counting
 static_assert(kChunk < 1 << 15, "two counts of a chunk's rows share a word");
+constexpr int kRankKeys = 512;      // at most so many middle rows are ranked by counting
 constexpr int kMaxCluster = 8;
 constexpr int kWords = 1024;        // of a histogram of 2048 bins
 constexpr int kFusedRows = 512;     // rows and 16-byte units that a selecting CTA copies itself
@@ -382,7 +382,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * hist) + kSelThreads * (kItems + 4) * 4);
+        evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)(2 * hist) + kSelThreads * (kItems + 4) * 4);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }

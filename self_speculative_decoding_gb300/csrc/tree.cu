@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
   }
   __syncthreads();
   for (int h = h0 + tid; h < h1; h += kPrepThreads)
-    if (h >= a.H + a.Hkv) a.vbad[(size_t)(h - a.H - a.Hkv) * tree_vbad_stride(a.T) + t] = (uint8_t)bad[h - h0];
+    if (h >= a.H + a.Hkv)
+      a.vbad[(size_t)(h - a.H - a.Hkv) * tree_vbad_stride(a.T) + t] = (uint8_t)bad[h - h0];
 }
 
 // d2 matrices of d1 rows of dh bf16, `stride` bytes apart, in 128-row boxes.

@@ -17,8 +17,8 @@ SSD_DI bool any_bad(const TreeArgs& a, int kvh, int lane) {
 // Adds to n columns from c0 on of row (node t) the inf and NaN of the V rows
 // that it sees, which the products left out: v += p_j V_j for those values.
 template <int DH>
-static __device__ __noinline__ void add_bad(const TreeArgs& a, int kvh, int row, int t, float lse, int c0,
-                                     float* v, int n) {
+static __device__ __noinline__ void add_bad(const TreeArgs& a, int kvh, int row, int t, float lse,
+                                            int c0, float* v, int n) {
   const uint8_t* flags = a.vbad + kvh * tree_vbad_stride(a.T);
   const int rows = a.T * a.G;
   const size_t plane = (size_t)a.Hkv * rows * DH;

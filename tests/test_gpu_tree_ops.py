@@ -370,6 +370,17 @@ def test_evict_weights_that_differ_late(ops, n, steps):
         np.testing.assert_array_equal(got, O.cache_evict(w, n, keep, 3, 20))
 
 
+# as many clusters of one to eight CTAs as these heads get
+@pytest.mark.parametrize("Hkv,n,keep", [(160, 20000, 3000), (80, 5000, 700), (100, 17000, 16000), (30, 4200, 4000)])
+def test_evict_many_heads(ops, Hkv, n, keep):
+    w = torch.rand(Hkv, n, generator=torch.Generator(device="cuda").manual_seed(n), device="cuda") ** 4
+    got = run_evict(ops, w, n, keep, 2, 30, 8)
+    middle = torch.sort(w[:, 2:n - 30], dim=1, descending=True, stable=True).indices[:, :keep - 32] + 2
+    first, last = torch.arange(2).expand(Hkv, 2), torch.arange(n - 30, n).expand(Hkv, 30)
+    want = torch.cat([first, torch.sort(middle, dim=1).values.cpu(), last], 1)
+    np.testing.assert_array_equal(got, want.numpy())
+
+
 def test_evict_long_row(ops):
     rng = np.random.default_rng(5)
     n, keep = 1_000_003, 100_000
