@@ -200,10 +200,15 @@ SSD_DI uint64_t entry(const BeamArgs& a, const Beam* beams, int pieces, int i, i
   return a.lists[(size_t)i * a.W + d];
 }
 
+// The score of an entry in 64 bits; NaN and -infinity are no candidate's.
+SSD_DI double whole_score(const Beam& m, uint64_t k) {
+  const double sc = (double)m.score;
+  return m.ended ? sc : sc + ((double)key_logit(k) - (double)m.lse);
+}
+
 // The candidate of an entry; false where its score is NaN or -infinity.
 SSD_DI bool score(const Beam& m, uint64_t k, int b, Cand& c) {
-  const double sc = (double)m.score;
-  const double s = m.ended ? sc : sc + ((double)key_logit(k) - (double)m.lse);
+  const double s = whole_score(m, k);
   c.s = ordered(s);
   c.k = k;
   c.b = b;
@@ -211,14 +216,19 @@ SSD_DI bool score(const Beam& m, uint64_t k, int b, Cand& c) {
 }
 
 // Bounds of that score in 32-bit arithmetic: the two sums are off by half a
-// step each, 2^-24 of |z| + |lse| and of the whole.  Overflow to an infinity
-// bounds from one side only; NaN (inf - inf) gives no bound.
+// step each, 2^-24 of |z| + |lse| and of the whole.  Where one of these leaves
+// the 32-bit range (a beam masked as a whole has z = lse = the lowest value) or
+// meets inf or NaN, the 64-bit score itself is rounded down and up.
 SSD_DI void score_bounds(const Beam& m, uint64_t k, float& lower, float& upper) {
   const float z = key_logit(k);
   const float f = m.ended ? m.score : m.score + (z - m.lse);
   const float e = m.ended ? 0.f : (fabsf(z) + fabsf(m.lse) + fabsf(m.score)) * 2.4e-7f;
-  lower = fabsf(f) < INFINITY && e < INFINITY ? f - e : f > 0.f ? 3e38f : -INFINITY;
-  upper = fabsf(f) < INFINITY && e < INFINITY ? f + e : f == -INFINITY ? -3e38f : INFINITY;
+  lower = f - e;
+  upper = f + e;
+  if (fabsf(f) < INFINITY && e < INFINITY) return;
+  const double s = whole_score(m, k);
+  lower = s > -INFINITY ? __double2float_rd(s) : -INFINITY;
+  upper = s > -INFINITY ? __double2float_ru(s) : -INFINITY;
 }
 
 SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool got) {
