@@ -111,6 +111,9 @@ void tree_sizes(TreeArgs& a, int T, int n_ctx, int H, int Hkv, int dh) {
   a.dh = dh;
 }
 
+// What ssd_debug_tree_give_up asked for.
+thread_local int t_give_up[2] = {-1, -1};
+
 // theta^(-2 i / dh) / pi.  The table of the thread's last (theta, dh) is kept:
 // 64 powers cost a small call several microseconds.
 void tree_frequencies(float theta, int dh, double* out) {
@@ -478,7 +481,16 @@ ssd_status ssd_op_tree_attention(const float* qkv, const int32_t* parents, int32
   a.out = (bf16*)out;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)dh));
   tree_frequencies(theta, dh, a.inv_freq);
+  a.give_up = t_give_up[0];
+  a.give_up_weights = t_give_up[1];
   return cu(launch_tree_attention(a, (cudaStream_t)stream), "tree_attention");
+}
+
+ssd_status ssd_debug_tree_give_up(int32_t attention, int32_t weights) {
+  if (attention < -1 || weights < -1) return op_fail(SSD_ERR_INVALID_ARG, "tree_give_up: a CTA, or -1");
+  t_give_up[0] = attention;
+  t_give_up[1] = weights;
+  return SSD_OK;
 }
 
 ssd_status ssd_op_cache_evict(const void* k, const void* v, const float* weight, int32_t n,

@@ -50,6 +50,9 @@ struct TreeArgs {
   // stream each); with one split a unit's result is final
   int tiles = 0, two = 0, items = 0, nb_ctx = 0, nb = 0, splits = 0, units = 0, ctas = 0;
   double inv_freq[kTreeMaxHalf];     // theta^(-2 i / dh) / pi
+  // self-test: the waits of this CTA of the attention, of the weights' kernel,
+  // give up at once (-1: of none)
+  int give_up = -1, give_up_weights = -1;
 };
 
 SSD_HD int tree_anc_words(int T) { return 4 * ((T + kTreeKeys - 1) / kTreeKeys); }
@@ -110,10 +113,10 @@ SSD_DI bool tree_try(uint64_t* bar, uint32_t parity) {
 }
 // Bounded wait for one or two barriers at once (b NULL: one); false if it ran
 // out or the CTA is flagged.
-SSD_DI bool tree_wait(const int* fail, uint64_t* a, uint32_t pa, uint64_t* b = nullptr,
+SSD_DI bool tree_wait(const int* fail, int polls, uint64_t* a, uint32_t pa, uint64_t* b = nullptr,
                       uint32_t pb = 0) {
   bool da = false, db = b == nullptr;
-  for (int i = 0; i < 1 << 22; ++i) {
+  for (int i = 0; i < polls; ++i) {
     if (!da) da = tree_try(a, pa);
     if (!db) db = tree_try(b, pb);
     if (da && db) return true;

@@ -24,8 +24,9 @@
 // 7 us of bytes.
 //
 // Warps 0-3 and 4-7: the streams' softmax; warp 8: TMA copies; warp 9: MMA.
-// Every wait is bounded: one that gives up sets the CTA's flag, every role
-// runs out, and the results become NaN.
+// Every wait is bounded: one that gives up sets the CTA's flag and every role
+// runs out; then the CTA's own rows become NaN, or, with several splits, all
+// rows that are joined after it, and so do the weights.
 #include "tc_dev.cuh"
 #include "tree.cuh"
 #include "tree_join.cuh"
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G;
+  const int polls = (int)blockIdx.x == a.give_up ? 0 : kPolls;
   unsigned char* ring = sm + kTiles * 2 * kItem;
 
   // (the copying thread itself: its first copies need not wait for the others)
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit x = unit_of(a, u);
         bool q_sent = false;
         auto send_q = [&]() {
-          if (units > 0 && !mbar_wait_n(qfree, (uint32_t)((units - 1) & 1), kPolls)) return false;
+          if (units > 0 && !mbar_wait_n(qfree, (uint32_t)((units - 1) & 1), polls)) return false;
           mbar_arrive_expect_tx(qfull, (uint32_t)(kTiles * 2 * kItem));
           for (int t = 0; t < kTiles; ++t)
             for (int p = 0; p < 2; ++p)
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a later unit's first blocks go out before its queries' place is
           // free (the slots they wait for need no query of this unit)
           if (!q_sent && (units == 0 || i >= kLag)) ok = send_q();
-          if (ok && issued >= kStages) ok = mbar_wait_n(&empty[at.slot], at.phase ^ 1u, kPolls);
+          if (ok && issued >= kStages) ok = mbar_wait_n(&empty[at.slot], at.phase ^ 1u, polls);
           if (!ok || tree_flagged(fail)) {
             ok = false;
             break;
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what is still in flight lands before the memory is released
       for (int i = max(0, issued - kStages); i < issued; ++i)
         mbar_wait_n(&full[i % kStages], (uint32_t)((i / kStages) & 1), kPolls);
-      if (units > 0) mbar_wait_n(qfull, (uint32_t)((units - 1) & 1), ok ? kPolls : 1 << 16);
+      if (units > 0) mbar_wait_n(qfull, (uint32_t)((units - 1) & 1), kPolls);
     }
   } else if (warp == 9) {
     // ---- products: the warp runs together, one lane issues
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t pphase[2] = {0, 0};                 // of the streams' P tiles
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, phase, kPolls));
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, phase, polls));
       tc_fence_after();
     };
     auto landed = [&](const Ring<kStages>& r) {
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = a.scale_log2;
     int n_s = 0, n_own = 0, n_other = 0, units = 0;
     auto wait_w = [&](uint64_t* bar, uint32_t parity) -> bool {
-      bool okw = !tree_flagged(fail) && mbar_wait_n(bar, parity, kPolls);
+      bool okw = !tree_flagged(fail) && mbar_wait_n(bar, parity, polls);
       okw = __all_sync(0xffffffffu, okw);
       if (!okw && lane == 0) atomicExch(fail, 1);
       return okw;
@@ -553,15 +555,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       if (!TWO) mbar_arrive_cta(taken);
     }
-    // a wait gave up: one split's results are final, so they are made NaN here
-    if (!ok && a.splits == 1)
-      for (int i = blockIdx.x * 128 + (tid & 127); s == 0 && i < a.T * a.H * DH; i += gridDim.x * 128)
-        a.out[i] = __float2bfloat16(NAN);
   }
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && tree_flagged(fail)) atomicExch(a.err, 1);
+  // a wait gave up: one split's rows are final, and none of the CTA's is sure
+  if (a.splits == 1 && tree_flagged(fail))
+    for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+      const Unit x = unit_of(a, u);
+      for (int i = tid; i < kTiles * 128 * DH; i += kThreads) {
+        const int row = x.item * kTiles * 128 + i / DH;
+        if (row < rows)
+          a.out[((size_t)(row / a.G) * a.H + x.kvh * a.G + row % a.G) * DH + i % DH] = __float2bfloat16(NAN);
+      }
+    }
   if (warp == 0) tmem_dealloc(*tslot, 512);
 }
 

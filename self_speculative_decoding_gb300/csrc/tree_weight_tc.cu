@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tree_warp(), lane = tid & 31;
   const int rows = a.T * a.G;
+  const int polls = (int)blockIdx.x == a.give_up_weights ? 0 : kPolls;
   const int planes = a.tiles > 1 ? 4 : 2;        // of the pass's one or two tiles
   const int stages = min(kMaxStages, kTileSmem / kItem - planes);
   const int bufs = a.tiles > 1 ? 1 : 2;          // of a stream's 256 score columns
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Pass before = first_pass(a);
       for (Pass x = before; ok && !x.over(); x = x.next(a)) {
         if (!sent || x.other(before)) {
-          if (sent) ok = mbar_wait_n(qempty, (uint32_t)((sent - 1) & 1), kPolls);
+          if (sent) ok = mbar_wait_n(qempty, (uint32_t)((sent - 1) & 1), polls);
           if (!ok) break;
           ++sent;
           mbar_arrive_expect_tx(qfull, (uint32_t)(planes * kItem));
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         before = x;
         for (int j = 0; ok && j < x.cnt; ++j) {
-          if (issued >= stages) ok = mbar_wait_n(&empty[slot], phase ^ 1u, kPolls);
+          if (issued >= stages) ok = mbar_wait_n(&empty[slot], phase ^ 1u, polls);
           if (!ok || tree_flagged(fail)) {
             ok = false;
             break;
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cs[2] = {0, 0};                          // score tiles per stream
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t ph) {
-      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, bar, ph));
+      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, polls, bar, ph));
     };
     Pass before = first_pass(a);
     for (Pass x = before; ok && !x.over();) {
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the block has landed and the stream's score columns have been read
           const int buf = cs[s] % bufs, use = cs[s] / bufs;
           if (use > 0)
-            ok = __all_sync(0xffffffffu, tree_wait(fail, &sfree[s * 2 + buf], (uint32_t)((use - 1) & 1),
+            ok = __all_sync(0xffffffffu, tree_wait(fail, polls, &sfree[s * 2 + buf], (uint32_t)((use - 1) & 1),
                                                    &full[slot], phase));
           else
             wait(&full[slot], phase);
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ctx = b < a.nb_ctx;
         // pairs of partial sums
         uint64_t sum[2] = {x.first() ? 0 : (uint64_t)__float_as_uint(sums[j >> 1]), 0};
-        ok = ok && tree_wait(fail, &sfull[s * 2 + buf], (uint32_t)(use & 1));
+        ok = ok && tree_wait(fail, polls, &sfull[s * 2 + buf], (uint32_t)(use & 1));
         if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) atomicExch(fail, 1);
           ok = false;

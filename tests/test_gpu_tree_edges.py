@@ -79,3 +79,80 @@ def test_select_where_the_score_brings_the_sum_back(ops, B, V, W):
     z[0], lse[0], scores[0] = 3e38, -3e38, LOWEST     # 6e38 - 3.4e38 = 2.6e38
     check_select(ops, z, scores, lse, W)
     check_select(ops, -z, -scores, -lse, W)
+
+
+# --------------------------------------------------------------------------
+# waits that run out
+
+
+@pytest.fixture
+def give_up(ops):
+    """Makes the waits of one CTA give up at once, in this thread's calls."""
+    from self_speculative_decoding_gb300 import _abi
+    call = _abi.lib().ssd_debug_tree_give_up
+    assert call(-2, -1) == 1 and call(-1, -2) == 1
+    yield lambda attention=-1, weights=-1: call(attention, weights)
+    call(-1, -1)
+
+
+def tree_inputs(H, Hkv, dh, n, T, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * n + T)
+    qkv = torch.randn(T, (H + 2 * Hkv) * dh, generator=g, device="cuda")
+    parents = torch.tensor([-1] + [i - 1 - (5 * i) % min(i, 4) for i in range(1, T)], dtype=torch.int32).cuda()
+    k, v = (torch.randn(Hkv, n + T + 3, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    return qkv, parents, k, v
+
+
+def tree_call(ops, x, H, Hkv, dh, n, weights=True):
+    w = torch.zeros(Hkv, x[2].shape[1], device="cuda") if weights else None
+    return ops.tree_attention(*x, n, n, H, Hkv, dh, 1e4, weights_out=w), w
+
+
+@pytest.mark.parametrize("H,Hkv,dh,n,T,cta,lost", [
+    # (K/V head, its first lost row, the one behind its last) of one split:
+    (40, 40, 128, 100, 9, 5, [(5, 0, 9)]),                  # a CTA for each head
+    (200, 200, 64, 10, 2, 7, [(7, 0, 2), (159, 0, 2)]),     # 152 CTAs for 200
+    (8, 4, 64, 60, 200, 3, [(1, 256, 400)]),                # two pairs of 128-row tiles a head
+    (8, 4, 128, 60, 200, 2, [(1, 0, 256)])])
+@pytest.mark.parametrize("weights", [False, True])
+def test_a_wait_that_runs_out_marks_its_rows(ops, give_up, H, Hkv, dh, n, T, cta, lost, weights):
+    x = tree_inputs(H, Hkv, dh, n, T)
+    want, want_w = tree_call(ops, x, H, Hkv, dh, n, weights)
+    assert torch.isfinite(want).all()
+    give_up(attention=cta)
+    out, w = tree_call(ops, x, H, Hkv, dh, n, weights)
+    give_up()
+    bad = torch.zeros(Hkv, T * (H // Hkv), dtype=torch.bool, device="cuda")
+    for kvh, a, b in lost:
+        bad[kvh, a:b] = True
+    rows = out.view(T, Hkv, H // Hkv, dh).permute(1, 0, 2, 3).reshape(Hkv, -1, dh)
+    want_rows = want.view(T, Hkv, H // Hkv, dh).permute(1, 0, 2, 3).reshape(Hkv, -1, dh)
+    assert torch.isnan(rows[bad]).all() and torch.equal(rows[~bad], want_rows[~bad])
+    if weights:
+        assert torch.isnan(w[:, :n + T]).all() and not w[:, n + T:].any()
+    out, w = tree_call(ops, x, H, Hkv, dh, n, weights)
+    assert torch.equal(out, want) and (not weights or torch.equal(w, want_w))
+
+
+@pytest.mark.parametrize("H,Hkv,dh,n,T", [(4, 1, 128, 9000, 5), (16, 2, 64, 5000, 30)])
+def test_a_wait_that_runs_out_marks_what_is_joined(ops, give_up, H, Hkv, dh, n, T):
+    x = tree_inputs(H, Hkv, dh, n, T)
+    want, want_w = tree_call(ops, x, H, Hkv, dh, n)
+    give_up(attention=4)
+    out, w = tree_call(ops, x, H, Hkv, dh, n)
+    give_up()
+    assert torch.isnan(out).all() and torch.isnan(w[:, :n + T]).all()
+    out, w = tree_call(ops, x, H, Hkv, dh, n)
+    assert torch.equal(out, want) and torch.equal(w, want_w)
+
+
+def test_a_wait_for_the_weights_that_runs_out_marks_its_keys(ops, give_up):
+    H, Hkv, dh, n, T = 16, 2, 128, 1500, 40                 # 13 blocks of 128 keys a head, a CTA each
+    x = tree_inputs(H, Hkv, dh, n, T)
+    want, want_w = tree_call(ops, x, H, Hkv, dh, n)
+    give_up(weights=16)
+    out, w = tree_call(ops, x, H, Hkv, dh, n)
+    bad = torch.zeros_like(w, dtype=torch.bool)
+    bad[1, 3 * 128:4 * 128] = True
+    assert torch.equal(out, want)
+    assert torch.isnan(w[bad]).all() and torch.equal(w[~bad], want_w[~bad])
