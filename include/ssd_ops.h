@@ -173,8 +173,8 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * differ when rows have been evicted.  Cache rows >= n_ctx + T are neither
  * read nor written.
  * weight_out (fp32 [Hkv][max_seq], nullable): the attention weight that each
- * key received, summed over the present rows and the query heads of its
- * group: rows j < n_ctx get weight_in[j] (fp32 [Hkv][max_seq]; NULL: zeros;
+ * key received, summed over the present rows that see it and the query heads
+ * of its group: rows j < n_ctx get weight_in[j] (fp32 [Hkv][max_seq]; NULL: zeros;
  * may be weight_out itself, no other overlap) plus this call's sum, rows
  * n_ctx..n_ctx+T-1 this call's sum alone; other rows stay as they are.
  * Scores keep fp32 accuracy (q is split into two bf16 parts); probabilities

@@ -621,7 +621,12 @@ SSD_DI void score_weights(const TreeArgs& a, int index) {
   float sum = 0.f;
   auto add = [&](int row, float score) {
     const float lse = s_lse[row], p = tree_ex2(fmaf(score, a.scale_log2, -lse));
-    if (lse != INFINITY) sum += p;               // absent rows take no part
+    if (lse == INFINITY) return;                 // absent rows take no part
+    // a row of NaN has none at the tree's keys that it does not see
+    if (isnan(lse) && !ctx && !bad &&
+        !((a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (k >> 5)] >> (k & 31)) & 1u))
+      return;
+    sum += p;
   };
 #pragma unroll
   for (int row = 0; row < kFirst; ++row)

@@ -156,3 +156,25 @@ def test_a_wait_for_the_weights_that_runs_out_marks_its_keys(ops, give_up):
     bad[1, 3 * 128:4 * 128] = True
     assert torch.equal(out, want)
     assert torch.isnan(w[bad]).all() and torch.equal(w[~bad], want_w[~bad])
+
+
+# --------------------------------------------------------------------------
+# NaN and infinities
+
+
+@pytest.mark.parametrize("T", [6, 10, 16, 40, 150])     # stored scores up to 16 nodes, a second pass from there
+@pytest.mark.parametrize("where", ["q", "k"])
+def test_weights_of_keys_that_a_row_of_nan_does_not_see(ops, T, where):
+    H, Hkv, dh, n = 4, 2, 64, 150
+    x = tree_inputs(H, Hkv, dh, n, T)
+    parents = [-1, 0, 0] + [i - 2 for i in range(3, T)]     # the odd nodes, and the even ones
+    x[1].copy_(torch.tensor(parents, dtype=torch.int32))
+    _, clean = tree_call(ops, x, H, Hkv, dh, n)
+    row = x[0].view(T, H + 2 * Hkv, dh)[T - 1 - T % 2]      # the last odd node: no node follows it
+    row[slice(H) if where == "q" else slice(H, H + Hkv), 3] = float("nan")
+    _, w = tree_call(ops, x, H, Hkv, dh, n)
+    even = [n + t for t in range(2, T, 2)]
+    odd = [n + t for t in range(T) if t == 0 or t % 2]
+    assert torch.isfinite(clean[:, :n + T]).all()
+    assert torch.isnan(w[:, :n]).all() and torch.isnan(w[:, odd]).all()
+    assert torch.equal(w[:, even], clean[:, even])
