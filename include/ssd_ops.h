@@ -177,8 +177,10 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * of its group: rows j < n_ctx get weight_in[j] (fp32 [Hkv][max_seq]; NULL: zeros;
  * may be weight_out itself, no other overlap) plus this call's sum, rows
  * n_ctx..n_ctx+T-1 this call's sum alone; other rows stay as they are.
- * Scores keep fp32 accuracy (q is split into two bf16 parts); probabilities
- * are rounded to bf16 for the product with V.  The result of a call does not
+ * q enters the scores as two bf16 parts, which leaves a score
+ *   (2^-16 + 2 dh 2^-24) sum |q_i k_i| / sqrt(dh)
+ * off at most; an infinite element of K gives the infinity that it gives q.
+ * Probabilities are rounded to bf16 for the product with V.  The result of a call does not
  * depend on timing (no floating-point atomics). */
 size_t ssd_op_tree_attention_workspace(int32_t T, int32_t n_ctx, int32_t H, int32_t Hkv,
                                        int32_t dh);

@@ -57,9 +57,21 @@ __device__ __noinline__ void far_ancestors(int t, int* par, uint32_t* bits, int&
   __syncthreads();
 }
 
+// q = hi + lo to 2^-16 of q (hi alone: 2^-7), so that bf16 matrix instructions
+// give scores to 2^-16 of sum |q_i k_i|.  hi is cut towards zero and lo is never
+// zero beside a hi that is not (hi 2^-24 for it, an fp32 rounding): both have
+// q's sign, so that an infinite element of K makes the score the infinity that
+// it is with q, not inf - inf or 0 x inf.  (hi rounded would give 2^-17; a pass
+// over scores that are NaN would cost one token over 16385 rows 3 %.)
+SSD_DI void two_parts(float q, bf16& hi, bf16& lo) {
+  hi = __float2bfloat16_rz(q);
+  const float h = __bfloat162float(hi), rest = q - h;  // exact
+  lo = __float2bfloat16(rest);
+  if (!(rest != 0.f && isfinite(rest))) lo = __float2bfloat16(h * 0x1p-24f);
+}
+
 // One CTA per (node, group of heads): the node's ancestor bits and depth,
-// the rotated query in two bf16 parts (q = hi + lo to 2^-17: the scores keep
-// 32-bit accuracy on bf16 matrix instructions), the K/V rows rounded to bf16
+// the rotated query in two bf16 parts, the K/V rows rounded to bf16
 // into the cache and, with inf and NaN of V replaced by 0, into the tree's
 // own copy (a matrix product must not meet 0 x inf at masked keys).
 // Angles: position * frequency in 64 bits, reduced to one turn, so that far
@@ -144,12 +156,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
     if (h < a.H) {
       const int kvh = h / a.G, g = h - kvh * a.G;
       const size_t o = ((size_t)kvh * a.T * a.G + (size_t)t * a.G + g) * a.dh + i;
-      const bf16 xh = __float2bfloat16(x), yh = __float2bfloat16(y);
-      a.q[o] = xh;
-      a.q[o + half] = yh;
-      const float xl = x - __bfloat162float(xh), yl = y - __bfloat162float(yh);
-      a.q[qplane + o] = __float2bfloat16(isfinite(xl) ? xl : 0.f);
-      a.q[qplane + o + half] = __float2bfloat16(isfinite(yl) ? yl : 0.f);
+      two_parts(x, a.q[o], a.q[qplane + o]);
+      two_parts(y, a.q[o + half], a.q[qplane + o + half]);
     } else {
       const bool is_k = h < a.H + a.Hkv;
       const int kvh = is_k ? h - a.H : h - a.H - a.Hkv;

@@ -178,3 +178,96 @@ def test_weights_of_keys_that_a_row_of_nan_does_not_see(ops, T, where):
     assert torch.isfinite(clean[:, :n + T]).all()
     assert torch.isnan(w[:, :n]).all() and torch.isnan(w[:, odd]).all()
     assert torch.equal(w[:, even], clean[:, even])
+
+
+U = 2.0 ** -8      # half a bf16 step, relative
+
+
+def seen_softmax(q, parents, n, K, V):
+    """out [T, H, dh], the weights of each key, the sum of p |v| and the largest
+    sum of |q k|, in 64 bits; K may hold infinities (q k summed term by term)."""
+    (T, H, dh), (Hkv, S, _) = q.shape, K.shape
+    G = H // Hkv
+    seen = np.zeros((T, S), bool)
+    seen[:, :n] = True
+    for t, path in enumerate(O.tree_paths(parents)):
+        seen[t, [n + i for i in path]] = True
+    out, spread, size = np.zeros((T, H, dh)), np.zeros((T, H, dh)), np.zeros((T, H))
+    mass = np.zeros((Hkv, S))
+    with np.errstate(invalid="ignore"):
+        for t in range(T):
+            for h in range(H):
+                terms = q[t, h] * K[h // G, seen[t]]
+                s = terms.sum(1) / np.sqrt(dh)
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                out[t, h], spread[t, h] = p @ V[h // G, seen[t]], p @ np.abs(V[h // G, seen[t]])
+                size[t, h] = np.where(np.isfinite(terms), np.abs(terms), 0).sum(1).max()
+                mass[h // G, seen[t]] += p
+    return out, mass, spread, size
+
+
+# tolerances as in test_gpu_tree_ops.py: the output's rounding and the
+# probabilities' u each, and 2 d for a score that is off by d
+def check_seen(out, w, x, parents, pos0, n, H, Hkv, dh):
+    T = len(parents)
+    q, _, _ = O.tree_rows(x[0].double().cpu().numpy(), parents, pos0, H, Hkv, dh, 1e4)
+    K, V = (t[:, :n + T].double().cpu().numpy() for t in x[2:])
+    ref, mass, spread, size = seen_softmax(q, parents, n, K, V)
+    d = (2.0 ** -16 + 2 * dh * 2.0 ** -24) * size / np.sqrt(dh) + 1e-6
+    got = out.double().cpu().numpy().reshape(T, H, dh)
+    nan = np.isnan(ref)
+    np.testing.assert_array_equal(np.isnan(got), nan)
+    err, tol = np.abs(got - ref), U * np.abs(ref) + (U + 2 * d[..., None]) * spread
+    assert np.all(err[~nan] <= tol[~nan])
+    got = w[:, :n + T].double().cpu().numpy()
+    nan_w = np.isnan(mass)
+    np.testing.assert_array_equal(np.isnan(got), nan_w)
+    err, tol = np.abs(got - mass), (2 * d.max() + (T * (H // Hkv) + 2) * 2.0 ** -24) * mass + 1e-12
+    assert np.all(err[~nan_w] <= tol[~nan_w])
+    return nan
+
+
+# stored scores and a second pass of products, one tile and two, one split and several
+SHAPES = [(4, 2, 64, 150, 6), (4, 4, 128, 700, 30), (2, 1, 128, 300, 40), (4, 2, 64, 60, 150), (8, 2, 128, 5000, 12)]
+
+
+@pytest.mark.parametrize("H,Hkv,dh,n,T", SHAPES)
+@pytest.mark.parametrize("what", [float("inf"), float("-inf")])
+def test_infinite_elements_of_k_that_are_seen(ops, H, Hkv, dh, n, T, what):
+    """A score of -infinity is no weight, +infinity makes its row NaN."""
+    x = tree_inputs(H, Hkv, dh, n, T)
+    x[2][:, [3, n // 2, n - 1], dh // 3] = what
+    out, w = tree_call(ops, x, H, Hkv, dh, n)
+    nan = check_seen(out, w, x, x[1].tolist(), n, n, H, Hkv, dh)
+    assert nan.any() and not nan.all()
+
+
+@pytest.mark.parametrize("H,Hkv,dh,n,T", SHAPES)
+def test_scores_of_minus_infinity_leave_the_rest_finite(ops, H, Hkv, dh, n, T):
+    """Roots at position 0 (their projections are not turned), q positive in the
+    column where some keys are -infinity, its low part zero in half of the rows."""
+    x = tree_inputs(H, Hkv, dh, n, T)
+    parents = [-1] * T
+    x[1].fill_(-1)
+    rows = x[0].view(T, H + 2 * Hkv, dh)
+    rows[:, :H, 5] = rows[:, :H, 5].abs() + 0.1
+    rows[::2, :H] = rows[::2, :H].bfloat16().float()
+    x[2][:, 1:n:7, 5] = float("-inf")
+    rows[1, H:H + Hkv, 5] = -3.4e38                   # rounded to -inf in the cache
+    w = torch.zeros(Hkv, x[2].shape[1], device="cuda")
+    out = ops.tree_attention(*x, n, 0, H, Hkv, dh, 1e4, weights_out=w)
+    assert torch.isinf(x[2][:, n + 1, 5]).all()
+    nan = check_seen(out, w, x, parents, 0, n, H, Hkv, dh)
+    assert not nan.any() and not w[:, 1:n:7].any() and not w[:, n + 1].any()
+
+
+def test_nan_in_k_stays(ops):
+    H, Hkv, dh, n, T = 4, 2, 128, 900, 40
+    x = tree_inputs(H, Hkv, dh, n, T)
+    x[2][0, 500, 7] = float("nan")
+    x[2][0, 600, 9] = float("-inf")
+    out, w = tree_call(ops, x, H, Hkv, dh, n)
+    out = out.view(T, H, dh)
+    assert torch.isnan(out[:, :2]).all() and torch.isfinite(out[:, 2:]).all()
+    assert torch.isnan(w[0, :n + T]).all() and torch.isfinite(w[1]).all()
