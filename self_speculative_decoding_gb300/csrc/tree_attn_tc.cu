@@ -138,7 +138,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* fail = reinterpret_cast<int*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G;
-  const int polls = (int)blockIdx.x == a.give_up ? 0 : kPolls;
   unsigned char* ring = sm + kTiles * 2 * kItem;
 
   // (the copying thread itself: its first copies need not wait for the others)
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    *fail = 0;
+    *fail = (int)blockIdx.x == a.give_up;        // (self-test: the softmax's waits)
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(tslot, 512);
@@ -173,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // kLag blocks, then V of block i and K of block i + kLag in turn
     Ring<kStages> at;
     int issued = 0, units = 0;                   // copies / units so far
+    const int polls = (int)blockIdx.x == a.give_up ? 0 : kPolls;
     auto is_ctx = [&](const Unit& x, int i, int& b, bool& is_v) {
       const int pro = min(kLag, x.nb), mid = 2 * (x.nb - pro);
       if (i < pro) {
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kStages> at;                            // the next K or V block
     int units = 0;
     uint32_t pphase[2] = {0, 0};                 // of the streams' P tiles
+    const int polls = (int)blockIdx.x == a.give_up ? 0 : kPolls;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait_n(bar, phase, polls));
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = a.scale_log2;
     int n_s = 0, n_own = 0, n_other = 0, units = 0;
     auto wait_w = [&](uint64_t* bar, uint32_t parity) -> bool {
-      bool okw = !tree_flagged(fail) && mbar_wait_n(bar, parity, polls);
+      bool okw = !tree_flagged(fail) && mbar_wait_n(bar, parity, kPolls);
       okw = __all_sync(0xffffffffu, okw);
       if (!okw && lane == 0) atomicExch(fail, 1);
       return okw;
@@ -621,18 +622,20 @@ SSD_DI void score_weights(const TreeArgs& a, int index) {
   float sum = 0.f;
   auto add = [&](int row, float score) {
     const float lse = s_lse[row], p = tree_ex2(fmaf(score, a.scale_log2, -lse));
-    if (lse == INFINITY) return;                 // absent rows take no part
-    // a row of NaN has none at the tree's keys that it does not see
-    if (isnan(lse) && !ctx && !bad &&
-        !((a.anc[(size_t)(row / a.G) * a.anc_words + (b - a.nb_ctx) * 4 + (k >> 5)] >> (k & 31)) & 1u))
-      return;
-    sum += p;
+    if (lse != INFINITY) sum += p;               // absent rows take no part
   };
 #pragma unroll
   for (int row = 0; row < kFirst; ++row)
     if (row < rows) add(row, first[row]);
 #pragma unroll 8
   for (int row = kFirst; row < rows; ++row) add(row, ps[(size_t)row * kTreeKeys]);
+  if (isnan(sum) && !ctx && !bad) {
+    // a row of NaN has none at the tree's keys that it does not see
+    const uint32_t* anc = a.anc + (b - a.nb_ctx) * 4 + (k >> 5);
+    sum = 0.f;
+    for (int row = 0; row < rows; ++row)
+      if ((anc[(size_t)(row / a.G) * a.anc_words] >> (k & 31)) & 1u) add(row, ps[(size_t)row * kTreeKeys]);
+  }
   a.w_out[o] = before + sum;
 }
 
