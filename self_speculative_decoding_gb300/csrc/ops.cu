@@ -96,7 +96,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 ssd_status check_tree_sizes(int T, int n_ctx, int H, int Hkv, int dh) {
-  if (T < 1 || T > kTreeMaxNodes || n_ctx < 0 || H < 1 || Hkv < 1 || H % Hkv || H > 4096 ||
+  if (T < 1 || T > kTreeMaxNodes || n_ctx < 0 || n_ctx > INT32_MAX - T || H < 1 || Hkv < 1 || H % Hkv || H > 4096 ||
       (dh != 64 && dh != 128))
     return op_fail(SSD_ERR_INVALID_ARG, "tree_attention sizes");
   return SSD_OK;

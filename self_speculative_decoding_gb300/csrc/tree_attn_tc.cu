@@ -794,7 +794,7 @@ void tree_split(TreeArgs& a) {
   a.tiles = (rows + 127) / 128;
   a.two = a.tiles > 1;
   a.items = a.two ? (a.tiles + 1) / 2 : 1;
-  a.nb_ctx = (a.n + kTreeKeys - 1) / kTreeKeys;
+  a.nb_ctx = a.n / kTreeKeys + (a.n % kTreeKeys != 0);
   a.nb = a.nb_ctx + (a.T + kTreeKeys - 1) / kTreeKeys;
   const long long lanes = (long long)a.Hkv * a.items;
   long long best = -1;

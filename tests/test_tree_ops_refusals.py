@@ -94,6 +94,16 @@ def test_an_empty_range_is_no_call(lib):
     assert lib.ssd_op_beam_reorder(*{**REORDER, "start": 9}.values()) == 0
 
 
+def test_workspaces_of_the_largest_sizes(lib):
+    """n_ctx + T and V up to 2^31 - 1: sizes that are whole, or 0 where the call
+    refuses them."""
+    tree = lib.ssd_op_tree_attention_workspace
+    sizes = [tree(1, n, 4, 2, 64) for n in (10, 2**30, 2**31 - 200, 2**31 - 100, 2**31 - 2)]
+    assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] < 2**37
+    assert tree(1, 2**31 - 1, 4, 2, 64) == 0
+    assert tree(1024, 2**31 - 1024, 4, 2, 64) == 0 and tree(1024, 2**31 - 1025, 4, 2, 64) > 0
+
+
 def test_binding_refuses_tensors_it_cannot_take():
     import torch
     from self_speculative_decoding_gb300 import ops
