@@ -163,7 +163,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   ssd_status st;
   {
     const Unlocked unlocked;
-    const size_t need = lib.tree_workspace((int32_t)T, n_ctx, H, Hkv, dh);
+    // (rows that the cache does not have are refused)
+    const size_t need = n_ctx <= S - T ? lib.tree_workspace((int32_t)T, n_ctx, H, Hkv, dh) : 0;
     if (!given && need) {                        // (0: refused sizes)
       out = make(qkv, res, at::kBFloat16);
       po = out.data_ptr();
@@ -205,7 +206,8 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   ssd_status st;
   {
     const Unlocked unlocked;
-    kept = make(k, {k.size(0), keep > 0 && keep <= n ? keep : 0}, at::kInt);  // (else refused)
+    const bool fits = keep > 0 && keep <= n && n <= k.size(1) && keep <= ko.size(1);  // (else refused)
+    kept = make(k, {k.size(0), fits ? keep : 0}, at::kInt);
     st = lib.cache_evict(pk, pv, (const float*)pw, n, keep, sinks, recent, (int32_t)k.size(1),
                          (int32_t)k.size(0), (int32_t)k.size(2),
                          type == at::kBFloat16 ? SSD_DTYPE_BF16 : SSD_DTYPE_FP32, pko, pvo,

@@ -271,3 +271,26 @@ def test_nan_in_k_stays(ops):
     out = out.view(T, H, dh)
     assert torch.isnan(out[:, :2]).all() and torch.isfinite(out[:, 2:]).all()
     assert torch.isnan(w[0, :n + T]).all() and torch.isfinite(w[1]).all()
+
+
+# --------------------------------------------------------------------------
+# refusals
+
+
+def test_rows_that_a_cache_does_not_have_allocate_nothing(ops):
+    from self_speculative_decoding_gb300 import SSDError
+    H, Hkv, dh = 64, 8, 128
+    x = tree_inputs(H, Hkv, dh, 60, 1)
+    S = x[2].shape[1]
+    w = torch.zeros(Hkv, S, device="cuda")
+    k2, v2 = x[2][:, :20].clone(), x[3][:, :20].clone()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    now = torch.cuda.max_memory_allocated()
+    for n in (S, 10 ** 7, 2 ** 31 - 1, -1):
+        with pytest.raises(SSDError):
+            ops.tree_attention(*x, n, 60, H, Hkv, dh, 1e4)
+    for n, keep in ((10 ** 8, 10 ** 8), (10 ** 8, 20), (S, 21), (2 ** 31 - 1, 2 ** 31 - 1)):
+        with pytest.raises(SSDError):
+            ops.cache_evict(x[2], x[3], w, n, keep, k2, v2)
+    assert torch.cuda.max_memory_allocated() - now < 1 << 16
