@@ -450,9 +450,9 @@ __global__ void __launch_bounds__(kCopyThreads) beam_reorder_kernel(const Reorde
 // Pieces per row, and their length: as few as hold a row in registers, and
 // more while they leave SMs idle and a piece is over 2048 logits.
 static int beam_pieces(int B, int V, int& len) {
-  int p = (V + kPieceMax - 1) / kPieceMax;
+  int p = V / kPieceMax + (V % kPieceMax != 0);
   while ((long long)B * p < 152 && V / (2 * p) >= 2048) p *= 2;
-  len = (V + p - 1) / p;
+  len = V / p + (V % p != 0);
   return p;
 }
 

@@ -294,3 +294,18 @@ def test_rows_that_a_cache_does_not_have_allocate_nothing(ops):
         with pytest.raises(SSDError):
             ops.cache_evict(x[2], x[3], w, n, keep, k2, v2)
     assert torch.cuda.max_memory_allocated() - now < 1 << 16
+
+
+# --------------------------------------------------------------------------
+# the largest sizes
+
+
+def test_select_over_the_largest_vocabulary(ops):
+    V = 2 ** 31 - 1
+    z = torch.full((1, V), -3.0, device="cuda")
+    at = [V - 1, 5, V // 2, 22528, V - 22528]
+    for i, v in enumerate(at):
+        z[0, v] = 10.0 - i
+    tok, par, best, done = ops.beam_select(z, torch.tensor([-1.0], device="cuda"), 8, end_id=V - 1)
+    assert tok.tolist() == at + [0, 1, 2] and par.tolist() == [0] * 8
+    assert best.tolist() == [9.0, 8.0, 7.0, 6.0, 5.0, -4.0, -4.0, -4.0] and done.tolist() == [1] + [0] * 7

@@ -104,6 +104,12 @@ def test_workspaces_of_the_largest_sizes(lib):
     assert tree(1024, 2**31 - 1024, 4, 2, 64) == 0 and tree(1024, 2**31 - 1025, 4, 2, 64) > 0
 
 
+def test_workspaces_of_the_largest_vocabularies(lib):
+    # a list of W keys of 8 bytes for each piece of at most 22528 logits
+    for V in (2**30, 2**31 - 22528, 2**31 - 10000, 2**31 - 1):
+        assert lib.ssd_op_beam_select_workspace(256, V, 7) == 256 * -(-V // 22528) * 7 * 8
+
+
 def test_binding_refuses_tensors_it_cannot_take():
     import torch
     from self_speculative_decoding_gb300 import ops
