@@ -70,11 +70,12 @@ def _tree_calls():
     to the loaded library's functions."""
     global _native
     if _native is None:
-        try:
-            from . import _binding
-        except ImportError as e:
-            raise RuntimeError("the native binding is not built here: build it with "
-                               "`python -m self_speculative_decoding_gb300.build`") from e
+        from . import build
+        why = build.binding_failure()
+        if why:
+            raise RuntimeError("no native binding of the tree-decoding calls (build it with `python -m "
+                               f"self_speculative_decoding_gb300.build`): {why}")
+        from . import _binding
         lib = _lib()
         _binding.bind({n: C.cast(getattr(lib, n), C.c_void_p).value for n in _abi.TREE_CALLS}, SSDError)
         _native = _binding

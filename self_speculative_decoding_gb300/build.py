@@ -4,7 +4,8 @@ Each translation unit is compiled in parallel to an object file under
 ``_build/`` and linked into ``libssd.so`` next to this file.  The CUDA
 runtime is linked statically.  ``csrc/binding.cpp``, the tree-decoding calls'
 Python module, is compiled against the installed PyTorch's headers into
-``_binding.so``.
+``_binding.so``; where that fails the library is built all the same, and those
+calls raise the reason.
 """
 
 from __future__ import annotations
@@ -13,6 +14,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libssd.so")
 BINDING = os.path.join(HERE, "_binding.so")
+STAMP = os.path.join(HERE, "_binding.txt")  # what it was built against; the reason if that failed
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]
@@ -36,17 +40,64 @@ def sources():
     return sorted(f for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _newest_input() -> float:
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+def _newest_input(files) -> float:
+    paths = [os.path.join(CSRC, f) for f in files]
     paths.append(os.path.join(os.path.dirname(HERE), "include", "ssd.h"))
     paths.append(os.path.join(os.path.dirname(HERE), "include", "ssd_ops.h"))
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths if os.path.exists(p))
 
 
-def _build_binding() -> None:
-    import sysconfig
+def _current(path: str, files) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= _newest_input(files)
 
+
+def binding_key() -> str:
+    """What _binding.so is built against (its C++ interfaces change with both)."""
+    import torch
+    return f"PyTorch {torch.__version__} in {os.path.dirname(torch.__file__)}, Python {sys.version.split()[0]}"
+
+
+def _stamp():
+    """(what _binding.so, or the attempt at it, was built against, why it failed)."""
+    if not os.path.exists(STAMP):
+        return "", ""
+    with open(STAMP) as f:
+        key, _, reason = f.read().partition("\n")
+    return key, reason
+
+
+def binding_failure() -> str:
+    """Why there is no _binding.so for this PyTorch; empty if there is one."""
+    key, reason = _stamp()
+    if key and key != binding_key():
+        return f"it was built against {key}, and this is {binding_key()}"
+    return reason or ("" if os.path.exists(BINDING) else "it has not been built")
+
+
+def _binding_current() -> bool:
+    """Whether it, or an attempt that failed, is of this PyTorch and these sources."""
+    key, reason = _stamp()
+    return (key == binding_key() and (bool(reason) or os.path.exists(BINDING)) and
+            _current(STAMP, ["binding.cpp"]))
+
+
+def _build_binding() -> None:
+    """_binding.so, or the reason why not, in STAMP."""
+    key = binding_key()
+    try:
+        _compile_binding()
+        reason = ""
+    except Exception as e:
+        reason = str(e)
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # of other sources, or another PyTorch
+        warnings.warn(f"no tree-decoding calls, the rest of the library is built: {reason}")
+    with open(STAMP, "w") as f:
+        f.write(key + "\n" + reason)
+
+
+def _compile_binding() -> None:
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -66,10 +117,19 @@ def _build_binding() -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input()
-                         for p in (LIB, BINDING)):
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        os.makedirs(BUILD, exist_ok=True)
+        binding = None
+        if force or not _binding_current():
+            binding = ex.submit(_build_binding)
+        if force or not _current(LIB, [f for f in os.listdir(CSRC) if f != "binding.cpp"]):
+            _build_library(verbose, extra_flags)
+        if binding:
+            binding.result()
+    return LIB
+
+
+def _build_library(verbose: bool, extra_flags) -> None:
     cc = nvcc()
 
     def compile_one(src):
@@ -85,16 +145,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, sources()))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 def build_variant(tag: str, flags) -> str:
