@@ -217,9 +217,11 @@ size_t tree_workspace(TreeArgs& a, void* base) {
   a.kt = a.q + (size_t)a.row_kt * a.dh;
   a.vt = a.q + (size_t)a.row_vt * a.dh;
   a.lse = (float*)take(a.Hkv * rows * 4);
-  a.part_o = (float*)take(slots * a.dh * 128 * 4);
-  a.part_m = (float*)take(slots * 128 * 4);
-  a.part_l = (float*)take(slots * 128 * 4);
+  if (a.splits > 1) {                            // (one split's results are final)
+    a.part_o = (float*)take(slots * a.dh * 128 * 4);
+    a.part_m = (float*)take(slots * 128 * 4);
+    a.part_l = (float*)take(slots * 128 * 4);
+  }
   if (rows <= (size_t)kTreeScoreRows) {
     a.part_s = (float*)take((size_t)a.Hkv * a.nb * rows * kTreeKeys * 4);
     if (!a.w_out) a.part_s = nullptr;

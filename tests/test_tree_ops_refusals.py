@@ -104,6 +104,15 @@ def test_workspaces_of_the_largest_sizes(lib):
     assert tree(1024, 2**31 - 1024, 4, 2, 64) == 0 and tree(1024, 2**31 - 1025, 4, 2, 64) > 0
 
 
+@pytest.mark.parametrize("T,n,H,Hkv,dh", [(1024, 0, 64, 8, 128), (5, 83, 40, 40, 64), (300, 100, 32, 32, 128)])
+def test_workspace_of_one_split_holds_no_partial_outputs(lib, T, n, H, Hkv, dh):
+    q = (2 * T * H + 2 * T * Hkv) * dh * 2               # two planes of q, the tree's K and V rows
+    rows, blocks = T * H // Hkv, -(-n // 128) + -(-T // 128)
+    scores = Hkv * blocks * rows * 512 if rows <= 32 else 0
+    small = T * (4 * -(-T // 128) + 2) * 4 + Hkv * (T + 3) + 4 * T * H
+    assert lib.ssd_op_tree_attention_workspace(T, n, H, Hkv, dh) <= q + scores + small + 10 * 256
+
+
 def test_workspaces_of_the_largest_vocabularies(lib):
     # a list of W keys of 8 bytes for each piece of at most 22528 logits
     for V in (2**30, 2**31 - 22528, 2**31 - 10000, 2**31 - 1):
