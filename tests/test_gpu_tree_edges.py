@@ -309,3 +309,42 @@ def test_select_over_the_largest_vocabulary(ops):
     tok, par, best, done = ops.beam_select(z, torch.tensor([-1.0], device="cuda"), 8, end_id=V - 1)
     assert tok.tolist() == at + [0, 1, 2] and par.tolist() == [0] * 8
     assert best.tolist() == [9.0, 8.0, 7.0, 6.0, 5.0, -4.0, -4.0, -4.0] and done.tolist() == [1] + [0] * 7
+
+
+@pytest.mark.parametrize("T", [1, 40])              # stored scores, and a second pass of products
+def test_rows_far_along_a_cache_are_the_right_ones(ops, T):
+    """1.2 million rows of 8 heads, the last head's beyond 2^31 elements: in each
+    head one key outweighs the rest, and every key's weight is checked."""
+    H = Hkv = 8
+    dh, n, S = 128, 1_200_000, 2_400_000
+    g = torch.Generator(device="cuda").manual_seed(T)
+    qkv = torch.randn(1, 3 * H * dh, generator=g, device="cuda").repeat(T, 1)
+    parents = torch.full((T,), -1, dtype=torch.int32, device="cuda")   # roots at 0: nothing is turned
+    k = torch.zeros(Hkv, S, dh, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty(Hkv, S, dh, dtype=torch.bfloat16, device="cuda")
+    v.copy_(torch.arange(1, Hkv + 1, device="cuda")[:, None, None].expand(v.shape))
+    q, own_k, own_v = (x.double() for x in qkv[0].view(3, H, dh))
+    own = (q * own_k.bfloat16().double()).sum(1) / dh ** 0.5
+    heads = torch.arange(H, device="cuda")
+    for rows in (None, [n - 1] * H, [0, 1, 127, 2 ** 20, 2 ** 20 + 1, n - 2, n - 128, 777_777]):
+        k[:, :n] = 0
+        score = torch.zeros(H, n, dtype=torch.float64, device="cuda")
+        if rows is not None:
+            at = torch.tensor(rows, device="cuda")
+            k[heads, at] = (3 * q).bfloat16()
+            v[heads, at] = (100.0 + heads)[:, None].bfloat16()
+            score[heads, at] = (q * k[heads, at].double()).sum(1) / dh ** 0.5
+        w = torch.zeros(Hkv, S, device="cuda")
+        out = ops.tree_attention(qkv, parents, k, v, n, 0, H, Hkv, dh, 1e4, weights_out=w).double().view(T, H, dh)
+        p = torch.softmax(torch.cat((score, own[:, None]), 1), 1)
+        ref = torch.einsum("hn,hnd->hd", p[:, :n], v[:, :n, :1].double()) + p[:, n:] * own_v.bfloat16().double()
+        spread = torch.einsum("hn,hnd->hd", p[:, :n], v[:, :n, :1].double()) + p[:, n:] * own_v.abs()
+        # scores up to 3 |q|^2 / sqrt(dh), off by 2^-16 of that and the fp32 sums
+        d = (2.0 ** -16 + 2 * dh * 2.0 ** -24) * 3.1 * (q * q).sum(1).max().item() / dh ** 0.5 + 1e-6
+        assert ((out - ref).abs() <= U * ref.abs() + (U + 2 * d) * spread).all()
+        mass = T * p[:, :n]
+        assert ((w[:, :n].double() - mass).abs() <= (2 * d + (T + 2) * 2.0 ** -24) * mass + 1e-30).all()
+        assert ((w[:, n:n + T].double() - p[:, n:]).abs() <= 3 * d * p[:, n:] + 1e-30).all() and not w[:, n + T:].any()
+        if rows is not None:
+            assert (out[0] - (100.0 + heads)[:, None]).abs().max().item() < 0.5 and (w[heads, at] > 0.99 * T).all()
+            v[heads, at] = (1.0 + heads)[:, None].bfloat16()
