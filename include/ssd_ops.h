@@ -182,7 +182,7 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * off at most; an infinite element of K gives the infinity that it gives q.
  * Probabilities are rounded to bf16 for the product with V.  The result of a call does not
  * depend on timing (no floating-point atomics). */
-/* (Of calls with and without weights: with up to 32 rows per K/V head, 4 bytes
+/* (Of calls with and without weights: with up to 16 rows per K/V head, 4 bytes
  * for each row and key are those of the weights.) */
 size_t ssd_op_tree_attention_workspace(int32_t T, int32_t n_ctx, int32_t H, int32_t Hkv,
                                        int32_t dh);

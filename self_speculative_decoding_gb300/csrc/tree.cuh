@@ -16,8 +16,14 @@ constexpr int kTreeKeys = 128;       // keys per block
 constexpr int kTreeMaxHalf = 64;     // dh / 2 at most
 // Up to so many rows per K/V head, the weights are summed from scores that the
 // attention stores (4 bytes per row and key, against a second read of K and a
-// second pass of products): see tree_attn_tc.cu.
-constexpr int kTreeScoreRows = 32;
+// second pass of products).  Both grow with the context and the heads, so that
+// the rows alone decide: us of a call so | by a second pass, for 8, 16, 32 and
+// 64 rows per head, 128 elements each,
+//    8 heads,   4000 keys   14 | 18,   16 | 18,   20 | 18,   28 | 19
+//    8 heads, 131072 keys  115 | 138, 132 | 138, 168 | 131, 257 | 135
+//   40 heads,  32768 keys  141 | 168, 162 | 168, 210 | 165, 307 | 171
+// and of 64 elements 4 heads, 131072 keys 53 | 59, 65 | 59, 89 | 54, 140 | 57.
+constexpr int kTreeScoreRows = 16;
 
 struct TreeArgs {
   const float* qkv = nullptr;        // [T][(H + 2 Hkv) dh] raw projections

@@ -162,7 +162,7 @@ def test_a_wait_for_the_weights_that_runs_out_marks_its_keys(ops, give_up):
 # NaN and infinities
 
 
-@pytest.mark.parametrize("T", [6, 10, 16, 40, 150])     # stored scores up to 16 nodes, a second pass from there
+@pytest.mark.parametrize("T", [6, 10, 16, 40, 150])     # stored scores for few nodes, a second pass of products for more
 @pytest.mark.parametrize("where", ["q", "k"])
 def test_weights_of_keys_that_a_row_of_nan_does_not_see(ops, T, where):
     H, Hkv, dh, n = 4, 2, 64, 150
@@ -229,7 +229,7 @@ def check_seen(out, w, x, parents, pos0, n, H, Hkv, dh):
 
 
 # stored scores and a second pass of products, one tile and two, one split and several
-SHAPES = [(4, 2, 64, 150, 6), (4, 4, 128, 700, 30), (2, 1, 128, 300, 40), (4, 2, 64, 60, 150), (8, 2, 128, 5000, 12)]
+SHAPES = [(4, 2, 64, 150, 6), (4, 4, 128, 700, 30), (2, 1, 128, 300, 40), (4, 2, 64, 60, 150), (8, 2, 128, 5000, 12), (8, 2, 128, 5000, 4)]
 
 
 @pytest.mark.parametrize("H,Hkv,dh,n,T", SHAPES)
