@@ -9,6 +9,7 @@
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
+#include "tree.cuh"
 
 namespace ssd {
 namespace {
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kCopyThreads) beam_reorder_kernel(const Reorde
 // more while they leave SMs idle and a piece is over 2048 logits.
 static int beam_pieces(int B, int V, int& len) {
   int p = V / kPieceMax + (V % kPieceMax != 0);
-  while ((long long)B * p < 152 && V / (2 * p) >= 2048) p *= 2;
+  while ((long long)B * p < tree_sms() && V / (2 * p) >= 2048) p *= 2;
   len = V / p + (V % p != 0);
   return p;
 }
