@@ -255,9 +255,9 @@ const char* ssd_ops_last_error(void);
 ssd_status ssd_op_wait_selftest(int32_t polls, int32_t* code_out, void* stream);
 
 /* The same of the tree attention, for the later calls of this host thread:
- * the device waits of CTA `attention` of its attention kernel, and of CTA
- * `weights` of the kernel that sums the weights of many rows, give up at once
- * (-1: of none, as at the start).  A call whose waits give up ends, still
+ * CTA `attention` of its attention kernel acts as after a wait that gave up,
+ * and the waits of CTA `weights` of the kernel that sums the weights of many
+ * rows give up at once (-1: none, as at the start).  Such a call ends, still
  * returns SSD_OK, and has NaN in every row of out (in every key's weight) that
  * may be incomplete.  Errors: INVALID_ARG (below -1). */
 ssd_status ssd_debug_tree_give_up(int32_t attention, int32_t weights);

@@ -56,8 +56,8 @@ struct TreeArgs {
   // stream each); with one split a unit's result is final
   int tiles = 0, two = 0, items = 0, nb_ctx = 0, nb = 0, splits = 0, units = 0, ctas = 0;
   double inv_freq[kTreeMaxHalf];     // theta^(-2 i / dh) / pi
-  // self-test: the waits of this CTA of the attention, of the weights' kernel,
-  // give up at once (-1: of none)
+  // self-test: this CTA of the attention acts as after a wait that gave up, this
+  // CTA's waits of the weights' kernel give up at once (-1: none)
   int give_up = -1, give_up_weights = -1;
 };
 
