@@ -18,7 +18,8 @@
  *
  * Every kernel's reduction order is fixed by the element's own position and
  * never depends on M or on the other rows: row m of a call with M rows is
- * bit-identical to the same row computed alone.
+ * bit-identical to the same row computed alone.  ssd_op_tree_attention is the
+ * exception (see there).
  */
 #ifndef SSD_OPS_H_
 #define SSD_OPS_H_
@@ -149,11 +150,11 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * where a call needs scratch memory, the caller gives a workspace of device
  * memory (256-byte aligned, at least what the call's _workspace function
  * returns for the current device; fewer bytes are SSD_ERR_CAPACITY; 0 for
- * sizes that need none, or that the call refuses).  Its
- * contents need no initialisation and mean nothing afterwards; calls that may
- * overlap on the GPU need one each.  Each call can be captured into a CUDA
- * graph.  Buffers overlap only where a call says so.  Inputs that these calls read from device memory (parents, done)
- * may hold any values, with the meanings below. */
+ * sizes that need none, or that the call refuses).  Its contents need no
+ * initialisation and mean nothing afterwards; calls that may overlap on the GPU
+ * need one each.  Each call can be captured into a CUDA graph.  Buffers overlap
+ * only where a call says so.  Inputs that these calls read from device memory
+ * (parents, done) may hold any values, with the meanings below. */
 
 /* Attention of T drafted nodes over a cache of n_ctx rows.  1 <= T <= 1024,
  * n_ctx >= 0, n_ctx + T <= max_seq, pos0 >= 0; dh 64 or 128.
@@ -180,8 +181,14 @@ ssd_status ssd_op_score_attention(const void* q, const int32_t* cand, int32_t n_
  * q enters the scores as two bf16 parts, which leaves a score
  *   (2^-16 + 2 dh 2^-24) sum |q_i k_i| / sqrt(dh)
  * off at most; an infinite element of K gives the infinity that it gives q.
- * Probabilities are rounded to bf16 for the product with V.  The result of a call does not
- * depend on timing (no floating-point atomics). */
+ * Probabilities are rounded to bf16 for the product with V.  A row whose every
+ * score is -infinity gives no key weight.  The result of a call does not depend
+ * on timing (no floating-point atomics): equal calls give equal bits.  But keys
+ * are summed in blocks from row 0 and from row n_ctx on, split and interleaved
+ * as T, n_ctx, the heads and the device's SMs suggest, so that a node's row may
+ * differ in its last bits from the same node's in another tree or alone, and
+ * from ssd_op_attention's: the greedy choice between near ties is not held to
+ * that of one token at a time. */
 /* (Of calls with and without weights: with up to 16 rows per K/V head, 4 bytes
  * for each row and key are those of the weights.) */
 size_t ssd_op_tree_attention_workspace(int32_t T, int32_t n_ctx, int32_t H, int32_t Hkv,

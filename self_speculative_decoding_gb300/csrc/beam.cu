@@ -146,7 +146,8 @@ SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* 
 }
 
 // A short piece has code of its own: what runs once is bound by its fetching
-// (4 beams of 1024 logits 9.6 us with the long one, 8.1).
+// (4 beams of 1024 logits 9.6 us with the long one and 8.1 when that changed,
+// 8.6 in the present build).
 constexpr int kFewItems = 4;
 SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out,
                        uint64_t* list) {
@@ -157,7 +158,8 @@ SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* o
     piece_items<kPieceItems>(a, len, piece, b, out, list, s_n);
 }
 
-// CTA = (piece of a row, beam).  48 rows of 128003 logits (24.6 MB) take 11 us:
+// CTA = (piece of a row, beam).  48 rows of 128003 logits (24.6 MB) take 11 us
+// (12 alone and cold):
 // the loads 6 of them (4 bytes each, since rows begin anywhere; all of a
 // thread's in flight at once), then the threshold, the list and its ranks.
 __global__ void __launch_bounds__(kPieceThreads, 2) beam_piece_kernel(const BeamArgs a, int len) {
@@ -245,14 +247,14 @@ SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool
 // threads' maxima over the lists' first eight entries (of lower bounds of their
 // scores) is a threshold that W candidates reach; the entries of each list
 // whose upper bound reaches it are collected and ranked by the whole order,
-// eight threads to a candidate (48 beams of 128003 logits 18.3 us in all, 21.2
-// with one thread to each).  Where a few lists hold most of the best, too many
+// eight threads to a candidate (48 beams of 128003 logits 16.9 us in all; when
+// that changed, 18.3 after 21.2 with one thread to each).  Where a few lists hold most of the best, too many
 // reach it: then every entry that does counts towards a second threshold (128
 // of 128 uneven beams of 32000 logits 21 us; one maximum after the other, what
 // is left for more than 1024 equal scores, took 715).
 // Bound by latency, about 6 us for 288 lists: two rounds of reads of L2, the
 // threshold and the ranks; holding the lists' first entries in shared memory
-// was slower (22.1 against 21.2).  WAIT: the lists come from the kernel before.
+// was slower (22.1 against 21.2 at the time).  WAIT: the lists come from the kernel before.
 template <int kThreads, bool WAIT>
 SSD_DI void merge_body(const BeamArgs& a, int pieces, Cand* list) {
   __shared__ Beam beams[256];

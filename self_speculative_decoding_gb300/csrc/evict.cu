@@ -130,9 +130,10 @@ __global__ void __launch_bounds__(kCopyThreads) evict_gather_kernel(const EvictA
 // With `fused` (one CTA per head, few rows) the CTA copies the rows too.
 // Bound by latency: barriers, reads of the others' sums, and code that runs
 // only once.  Hence short loops over keys in shared memory and places counted
-// per thread over rows that lie together: 8 heads of 131072 rows take 36.9 us
-// with the copy (20.4), 40.8 with the keys in registers, unrolled loops and
-// places from ballots; 40 heads of 4095 rows 16.9 and 17.9 us.
+// per thread over rows that lie together: 8 heads of 131072 rows took 36.9 us
+// with the copy (20.4) against 40.8 with the keys in registers, unrolled loops
+// and places from ballots, 40 heads of 4095 rows 16.9 against 17.9, in turns in
+// one process (processes differ: 36.5 to 41.4 and 17.2 to 20.0 us).
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int share,
                                                                   int fused) {
   extern __shared__ __align__(16) uint32_t smem[];
@@ -362,8 +363,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   // Few rows that stay: the selecting CTA copies them (one launch).
   const bool few = (long long)a.keep * a.units <= kFusedUnits && a.keep <= kFusedRows;
   // A CTA per 4096 middle rows up to the portable cluster size (8 heads of 16000
-  // rows 18.9 us so, 20.9 with one per 8192; 40 heads of 4095 rows 16.4, 18 with
-  // two CTAs a head), while no SM gets a second one (32 heads of 32768 rows 31.7
+  // rows 18.9 us so, 20.9 with one per 8192; 40 heads of 4095 rows 16.4 with one,
+  // 18 with two CTAs a head, in turns in one process), while no SM gets a second one (32 heads of 32768 rows 31.7
   // us with four CTAs a head, 49.5 with eight; 40 heads of 20000 rows 25.1 with
   // two, 29 with four) or a CTA has more rows than it holds (80 heads of 65536
   // rows 72 us with four, 95 with one, 104 with eight).

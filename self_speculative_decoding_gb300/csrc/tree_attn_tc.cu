@@ -11,17 +11,20 @@
 // take the key blocks in turn (both of the one tile); with more, each takes a
 // tile of its own and the pair reads every key block once.  m is raised, and
 // O rescaled, only when a block's maximum passes it by 8 (a factor of 256,
-// which fp32 sums and bf16 probabilities carry without loss).  The keys are
-// split into units over the SMs; a second kernel joins the units' partial
-// results in a fixed order.
+// which fp32 sums and bf16 probabilities carry without loss).  P is rounded to
+// bf16, half a step of 2^-8 each like the output's own, because a second part of
+// it would cost another product as large as the three; its sum is of the
+// unrounded values in fp32.  The keys are split into units over the SMs; a
+// second kernel joins the units' partial results in a fixed order.
 //
 // With many rows the matrix pipe bounds it: 256 nodes of 64 / 8 heads over
 // 131000 rows are 1.65 TFLOP in three products of one size (Q_hi K, Q_lo K,
 // P V), 854 us at the 1931 TFLOP/s that a library product reaches in a burst;
-// it takes 855 us, and up to 930 where the power limit lowers the clock.  With
-// few rows it is a stream's chain (copy, product, softmax, product) and the
-// first copy's latency: 61 nodes of 40 heads over 2047 rows take 15 us for
-// 7 us of bytes.
+// from a graph it takes 846 to 880 us, as a pass among others 931 to 959, where
+// the power limit lowers the clock.  With few rows it is a stream's chain (copy,
+// product, softmax, product) and the first copy's latency: 61 nodes of 40 heads
+// over 2047 rows take 15 us for 7 us of bytes.  A thread's 128 scores at the 168
+// registers that ten warps leave spill 24 to 64 bytes.
 //
 // Warps 0-3 and 4-7: the streams' softmax; warp 8: TMA copies; warp 9: MMA.
 // Every wait is bounded: one that gives up sets the CTA's flag and every role
