@@ -72,10 +72,14 @@ def _tree_calls():
     if _native is None:
         from . import build
         why = build.binding_failure()
+        if not why:
+            try:
+                from . import _binding
+            except ImportError as e:
+                why = str(e)
         if why:
             raise RuntimeError("no native binding of the tree-decoding calls (build it with `python -m "
                                f"self_speculative_decoding_gb300.build`): {why}")
-        from . import _binding
         lib = _lib()
         _binding.bind({n: C.cast(getattr(lib, n), C.c_void_p).value for n in _abi.TREE_CALLS}, SSDError)
         _native = _binding

@@ -66,3 +66,14 @@ def test_a_binding_that_fails_takes_an_old_one_along(build, monkeypatch):
     with pytest.warns(UserWarning, match="no compiler"):
         build.build()
     assert not os.path.exists(build.BINDING) and build.binding_failure() == "no compiler"
+
+
+def test_a_binding_that_does_not_load_is_named(monkeypatch):
+    import sys
+
+    import self_speculative_decoding_gb300 as ssd
+    monkeypatch.setattr(ssd, "_native", None)
+    monkeypatch.delattr(ssd, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, ssd.__name__ + "._binding", None)
+    with pytest.raises(RuntimeError, match="native binding"):
+        ssd.ops.beam_select(None, None, 1)
