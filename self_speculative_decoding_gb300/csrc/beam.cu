@@ -147,7 +147,7 @@ SSD_DI void piece_items(const BeamArgs& a, int len, int piece, int b, uint64_t* 
 
 // A short piece has code of its own: what runs once is bound by its fetching
 // (4 beams of 1024 logits 9.6 us with the long one and 8.1 when that changed,
-// 8.6 in the present build).
+// 8.2 in the present build).
 constexpr int kFewItems = 4;
 SSD_DI void piece_body(const BeamArgs& a, int len, int piece, int b, uint64_t* out,
                        uint64_t* list) {
@@ -203,35 +203,29 @@ SSD_DI uint64_t entry(const BeamArgs& a, const Beam* beams, int pieces, int i, i
   return a.lists[(size_t)i * a.W + d];
 }
 
-// The score of an entry in 64 bits; NaN and -infinity are no candidate's.
-SSD_DI double whole_score(const Beam& m, uint64_t k) {
-  const double sc = (double)m.score;
-  return m.ended ? sc : sc + ((double)key_logit(k) - (double)m.lse);
-}
-
 // The candidate of an entry; false where its score is NaN or -infinity.
 SSD_DI bool score(const Beam& m, uint64_t k, int b, Cand& c) {
-  const double s = whole_score(m, k);
+  const double sc = (double)m.score;
+  const double s = m.ended ? sc : sc + ((double)key_logit(k) - (double)m.lse);
   c.s = ordered(s);
   c.k = k;
   c.b = b;
   return s > -INFINITY;
 }
 
-// Bounds of that score in 32-bit arithmetic: the two sums are off by half a
-// step each, 2^-24 of |z| + |lse| and of the whole.  Where one of these leaves
-// the 32-bit range (a beam masked as a whole has z = lse = the lowest value) or
-// meets inf or NaN, the 64-bit score itself is rounded down and up.
+// Bounds of that score in 32-bit arithmetic: either sum is off by half a step of
+// its result, 2^-24 (twice that is taken; the bounds are rounded too).  All is
+// taken by a quarter, so that no sum leaves the 32-bit range (z - lse may); what
+// the last product makes an infinity lies beyond every 32-bit value.  A quarter
+// is exact but for the last steps above zero (1e-44).  A sum that is infinite has
+// an infinite term, and NaN is no candidate.
 SSD_DI void score_bounds(const Beam& m, uint64_t k, float& lower, float& upper) {
-  const float z = key_logit(k);
-  const float f = m.ended ? m.score : m.score + (z - m.lse);
-  const float e = m.ended ? 0.f : (fabsf(z) + fabsf(m.lse) + fabsf(m.score)) * 2.4e-7f;
-  lower = f - e;
-  upper = f + e;
-  if (fabsf(f) < INFINITY && e < INFINITY) return;
-  const double s = whole_score(m, k);
-  lower = s > -INFINITY ? __double2float_rd(s) : -INFINITY;
-  upper = s > -INFINITY ? __double2float_ru(s) : -INFINITY;
+  const float d = m.ended ? 0.f : 0.25f * key_logit(k) - 0.25f * m.lse;
+  const float f = 0.25f * m.score + d;
+  const float e = fmaf(fabsf(d), 1.2e-7f, fmaf(fabsf(f), 1.2e-7f, 1e-44f));
+  const bool finite = fabsf(f) < INFINITY;
+  lower = finite ? 4.f * (f - e) : f > 0.f ? INFINITY : -INFINITY;
+  upper = finite ? 4.f * (f + e) : lower;
 }
 
 SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool got) {
@@ -247,7 +241,7 @@ SSD_DI void put(const BeamArgs& a, const Beam* beams, int w, const Cand& c, bool
 // threads' maxima over the lists' first eight entries (of lower bounds of their
 // scores) is a threshold that W candidates reach; the entries of each list
 // whose upper bound reaches it are collected and ranked by the whole order,
-// eight threads to a candidate (48 beams of 128003 logits 16.9 us in all; when
+// eight threads to a candidate (48 beams of 128003 logits 16.5 us in all; when
 // that changed, 18.3 after 21.2 with one thread to each).  Where a few lists hold most of the best, too many
 // reach it: then every entry that does counts towards a second threshold (128
 // of 128 uneven beams of 32000 logits 21 us; one maximum after the other, what
