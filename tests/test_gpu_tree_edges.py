@@ -348,3 +348,49 @@ def test_rows_far_along_a_cache_are_the_right_ones(ops, T):
         if rows is not None:
             assert (out[0] - (100.0 + heads)[:, None]).abs().max().item() < 0.5 and (w[heads, at] > 0.99 * T).all()
             v[heads, at] = (1.0 + heads)[:, None].bfloat16()
+
+
+# --------------------------------------------------------------------------
+# calls in other forms
+
+
+def test_a_given_output_is_written_and_returned(ops):
+    from self_speculative_decoding_gb300 import SSDError
+    H, Hkv, dh, n, T = 8, 2, 64, 400, 9
+    x = tree_inputs(H, Hkv, dh, n, T)
+    want, _ = tree_call(ops, x, H, Hkv, dh, n, False)
+    out = torch.full((T, H * dh), 7.0, device="cuda").bfloat16()
+    assert ops.tree_attention(*x, n, n, H, Hkv, dh, 1e4, out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, want)
+    with pytest.raises(SSDError):
+        ops.tree_attention(*x, n + 4, n, H, Hkv, dh, 1e4, out=out.fill_(7.0))
+    for bad in (out.float(), out[:, :-8].contiguous(), out.t(), out.cpu()):
+        with pytest.raises(ValueError, match="out"):
+            ops.tree_attention(*x, n, n, H, Hkv, dh, 1e4, out=bad)
+    w = torch.zeros(Hkv, x[2].shape[1], device="cuda")
+    with pytest.raises(SSDError):
+        ops.tree_attention(*x, n, n, H, Hkv, dh, 1e4, weights=w, out=out)
+    assert (out == 7).all()
+
+
+@pytest.mark.parametrize("H,Hkv,dh,n,T", [(8, 2, 64, 700, 4), (8, 2, 128, 700, 20), (16, 2, 128, 3000, 40)])
+def test_a_replayed_graph_takes_new_trees(ops, H, Hkv, dh, n, T):
+    """Other nodes, parents (absent ones among them) and weights of one captured call."""
+    x, y = (tree_inputs(H, Hkv, dh, n, T, seed) for seed in (0, 1))
+    y[1].copy_(torch.tensor([-1] + [(3 * i) % i if i % 5 else -2 for i in range(1, T)], dtype=torch.int32))
+    w = torch.rand(Hkv, n + T + 3, device="cuda")
+    held, held_w = [t.clone() for t in x], w.clone()
+    ops.tree_attention(*held, n, n, H, Hkv, dh, 1e4, weights=held_w, weights_out=held_w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ops.tree_attention(*held, n, n, H, Hkv, dh, 1e4, weights=held_w, weights_out=held_w)
+    for inputs in (x, y, x):
+        for a, b in zip(held, inputs):
+            a.copy_(b)
+        held_w.copy_(w)
+        graph.replay()
+        mine, mine_w = [t.clone() for t in inputs], w.clone()
+        want = ops.tree_attention(*mine, n, n, H, Hkv, dh, 1e4, weights=mine_w, weights_out=mine_w)
+        assert torch.equal(out, want) and torch.equal(held_w, mine_w)
+        assert all(torch.equal(a, b) for a, b in zip(held, mine))
