@@ -18,8 +18,8 @@
  *
  * Every kernel's reduction order is fixed by the element's own position and
  * never depends on M or on the other rows: row m of a call with M rows is
- * bit-identical to the same row computed alone.  ssd_op_tree_attention is the
- * exception (see there).
+ * bit-identical to the same row computed alone.  ssd_op_tree_attention and
+ * ssd_op_cache_attention are the exceptions (see there).
  */
 #ifndef SSD_OPS_H_
 #define SSD_OPS_H_
@@ -249,6 +249,114 @@ ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* pare
                                int32_t W, int32_t groups, int32_t max_seq, int32_t start,
                                int32_t stop, int32_t row_bytes, void* k_out, void* v_out,
                                void* stream);
+
+/* ---- Rounds of several sequences over caches of one layer, whose old rows are
+ * held in 8 bits: norms, rotation and append; the move of committed rows to 8
+ * bits; attention over the rows that result, whole or through a window; the
+ * verification of the drafts.  As above these calls allocate nothing and can be
+ * captured into graphs; what differs between sequences or rounds (lengths,
+ * counts, held, ...: device int32 [B]) is read from device memory when the call
+ * runs, so that a captured graph serves every round.  1 <= B <= 1024.
+ *
+ * Caches: row p of sequence b and K/V head h is the dh elements at
+ *   k + b seq_stride + (h rows + p % rows) dh     (bf16; v the same)
+ * so that `rows` is the longest sequence, or less where the caches are rings of
+ * the newest rows; and once it has been moved to 8 bits
+ *   k8 + b seq8_stride + (h max_seq + p) dh       (e4m3; v8 the same)
+ * with the scale k_scale[b scale_stride + h (max_seq / block) + p / block]
+ * (fp32; v_scale the same): the row's values are its elements times its scale.
+ * Strides are in elements and at least what one sequence takes (so that a layer
+ * of [B][layers][Hkv][rows][dh] can be given); seq_stride a multiple of 8,
+ * seq8_stride of 16.  dh is 64 or 128, block 32, 64 or 128, max_seq a
+ * multiple of block.  k and v of different sequences may alternate in memory, and
+ * a call that only reads a pair of caches may be given one for both; buffers
+ * overlap in no other way. */
+
+/* Norms of the query and key heads, rotation and append: token t < counts[b]
+ * (counts NULL: T for all; clamped to 0..T) of sequence b goes to row
+ * lengths[b] + t, at position positions[b] + t (positions NULL: lengths).
+ * qkv fp32 [B][T][(H + 2 Hkv) dh] holds the raw projections (q, k, v).  Heads of
+ * q become x / sqrt(mean(x^2) + eps) * q_gain (fp32 [dh]; NULL: stay as they
+ * are), heads of k the same with k_gain; both are then turned by rotate-half RoPE
+ * (base theta), the angle exact for every position; bf16(q) goes to q_out
+ * (bf16 [B][T][H][dh]), bf16(k) and bf16(v) to their rows.  A token that a
+ * sequence does not have (t >= counts[b], or lengths[b] below 0 or beyond
+ * 2^31 - 1 - T) has zeros in q_out and no row.  Other rows stay as they are.
+ * 1 <= T <= rows.  A token's results do not depend on the other tokens. */
+ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int32_t* lengths,
+                              const int32_t* counts, const int32_t* positions,
+                              const float* q_gain, const float* k_gain, float eps, float theta,
+                              void* k, void* v, int32_t rows, size_t seq_stride, int32_t H,
+                              int32_t Hkv, int32_t dh, void* q_out, void* stream);
+
+/* The move of rows to 8 bits: every whole block of rows held[b] .. lengths[b] - 1
+ * is read from k, v and written to k8, v8 with its scale, the smallest power of two
+ * (2^-64 at least; 1 for zeros) that brings the block's largest magnitude to at
+ * most 448; elements are rounded to nearest, ties to even.  Infinities and NaN
+ * become NaN and do not enter the scale.  held_out[b] = held[b] + the rows moved
+ * (held_out may not be held).  lengths is what is to stay: rows of drafts that
+ * may yet be rejected are not in it.  A sequence whose numbers make no sense
+ * (held[b] negative, no multiple of block or beyond max_seq, lengths[b] beyond
+ * max_seq), or of whose rows the ring has lost one (lengths[b] - held[b] > rows),
+ * stays as it is. */
+ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, size_t seq_stride,
+                                 const int32_t* held, const int32_t* lengths, int32_t B,
+                                 int32_t Hkv, int32_t dh, int32_t block, void* k8, void* v8,
+                                 float* k_scale, float* v_scale, int32_t max_seq,
+                                 size_t seq8_stride, size_t scale_stride, int32_t* held_out,
+                                 void* stream);
+
+/* Attention of T tokens per sequence, already rotated and appended:
+ *   out[b][t][h] = softmax_j(scale q[b][t][h] k_j) v_j    (bf16 [B][T][H][dh])
+ * over rows j <= lengths[b] + t and, with window > 0, of those the first `sinks`
+ * and the last `window` (the token's own row among them; window 0: all rows).
+ * Rows j < held[b] are read from k8, v8, the others from k, v (held, k8, v8,
+ * k_scale and v_scale NULL together: all from k, v; max_seq, block and the strides
+ * then mean nothing).  q bf16 [B][T][H][dh]; query head h reads K/V head
+ * h / (H / Hkv); 1 <= T, T H / Hkv <= 128.  counts as for ssd_op_rope_append but
+ * not clamped; rows of out behind a sequence's tokens are zeros.  A row that
+ * sees keys of score -infinity alone is zeros.  Rows that a token does not see
+ * take no part in it, whatever they hold; of the rings only rows that some token
+ * of the sequence sees are needed.  A sequence whose numbers make no sense
+ * (lengths[b] negative or beyond 2^31 - 257 - T, counts[b] outside 0..T, held[b]
+ * outside 0..max_seq or beyond lengths[b] + counts[b]), or of whose rows the
+ * ring no longer holds one that is needed, gives NaN in all of its rows of out.
+ * Scores are exact products of the bf16 query and the stored keys, summed in
+ * fp32 (elements of q below 2^-9 of their row's largest are good to 2^-17 of
+ * that; a query row with infinity or NaN gives NaN); probabilities, times the value's scale, are
+ * rounded to bf16 for the product with V.  Equal calls give equal bits, but a
+ * row's last bits depend on how the rows of all sequences of the call are divided
+ * among the SMs. */
+size_t ssd_op_cache_attention_workspace(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh);
+ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int32_t* lengths,
+                                  const int32_t* counts, const void* k, const void* v,
+                                  int32_t rows, size_t seq_stride, const void* k8, const void* v8,
+                                  const float* k_scale, const float* v_scale, const int32_t* held,
+                                  int32_t max_seq, int32_t block, size_t seq8_stride,
+                                  size_t scale_stride, int32_t window, int32_t sinks, int32_t H,
+                                  int32_t Hkv, int32_t dh, float scale, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Verification of drafts from given random numbers.  p fp32 [B][d + 1][V]: the
+ * target's probabilities at each draft and after the last; q fp32 [B][d][V]:
+ * the probabilities that the drafts were drawn from (NULL: each was certain, as
+ * a greedy draft is); drafts int32 [B][d], counts int32 [B] (NULL: d for all;
+ * clamped to 0..d); accept_u fp32 [B][d], sample_u fp32 [B], in [0, 1).
+ * Draft j, token y, is accepted while accept_u[j] q_j(y) < p_j(y), compared
+ * without rounding (a token outside 0..V-1 is rejected).  At the first that
+ * is not, one token is drawn from max(p_j - q_j, 0) (q NULL: p_j without y), or
+ * from p_j where nothing is left; after the last, from p_counts: the lowest v with
+ *   sum_{w <= v} r_w > sample_u sum r     (r: the entries drawn from)
+ * the sums good to 2^-40; where rounding or a sample_u of 1 or more leaves none,
+ * the last v with r_v > 0.  Entries that are negative or NaN count as 0.
+ * tokens int32 [B][d + 1] = the accepted drafts, the drawn token, then -1;
+ * n int32 [B] = the number of them (no drawn token where p_j has no entry over 0,
+ * or an infinite one).  d >= 0 (0: one draw from p; q, drafts and accept_u are not
+ * read), d <= 1024, V >= 1; 4-byte alignment. */
+ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* drafts,
+                                const int32_t* counts, const float* accept_u,
+                                const float* sample_u, int32_t B, int32_t d, int32_t V,
+                                int32_t* tokens, int32_t* n, void* stream);
 
 /* Description of the most recent failed op call on this host thread. */
 const char* ssd_ops_last_error(void);

@@ -484,6 +484,46 @@ class _Ops:
         _tree_calls().beam_reorder(k, v, parents, start, stop, k_out, v_out)
         return k_out, v_out
 
+    def rope_append(self, qkv, lengths, k, v, H, Hkv, dh, theta, q_gain=None, k_gain=None, eps=1e-5,
+                    counts=None, positions=None, out=None) -> torch.Tensor:
+        """Norms of the query and key heads (where gains, fp32 [dh], are given),
+        rotation and append (ssd_op_rope_append): qkv fp32
+        [B, T, (H + 2 Hkv) dh] raw projections, lengths int32 [B] the rows before
+        the call, counts int32 [B] its tokens (None: T), positions int32 [B] the
+        first token's (None: lengths), all on the device.  Token t's K/V rows go
+        to row (lengths[b] + t) % rows of k, v bf16 [B, Hkv, rows, dh] (any
+        stride between sequences).  Returns q bf16 [B, T, H, dh]."""
+        return _tree_calls().rope_append(qkv, lengths, k, v, H, Hkv, dh, theta, q_gain, k_gain, eps,
+                                         counts, positions, out)
+
+    def cache_quantize(self, k, v, held, lengths, k8, v8, k_scale, v_scale,
+                       held_out=None) -> torch.Tensor:
+        """The move of cache rows to 8 bits (ssd_op_cache_quantize): every whole
+        block of rows held[b] .. lengths[b] - 1 of k, v bf16 [B, Hkv, rows, dh]
+        goes to k8, v8 float8_e4m3fn [B, Hkv, max_seq, dh] and its scale to
+        k_scale, v_scale fp32 [B, Hkv, max_seq / block]; held, lengths int32 [B]
+        on the device.  Returns the new held."""
+        return _tree_calls().cache_quantize(k, v, held, lengths, k8, v8, k_scale, v_scale, held_out)
+
+    def cache_attention(self, q, k, v, lengths, k8=None, v8=None, k_scale=None, v_scale=None, held=None,
+                        counts=None, window=0, sinks=0, scale=None, out=None) -> torch.Tensor:
+        """Attention of q bf16 [B, T, H, dh], tokens that rope_append has
+        appended behind lengths[b] rows, over rows held in 8 bits (j < held[b])
+        and in bf16 (ssd_op_cache_attention); with a window, over the first
+        ``sinks`` rows and the last ``window``.  Without 8-bit caches all rows are
+        those of k, v.  scale: None for 1 / sqrt(dh).  Returns bf16
+        [B, T, H, dh]."""
+        return _tree_calls().cache_attention(q, k, v, lengths, k8, v8, k_scale, v_scale, held, counts,
+                                             window, sinks, scale, out)
+
+    def verify_drafts(self, p, drafts, accept_u, sample_u, q=None, counts=None):
+        """Verification of drafts int32 [B, d] from given random numbers
+        accept_u fp32 [B, d] and sample_u fp32 [B] (ssd_op_verify_drafts): p fp32
+        [B, d + 1, V] the target's probabilities, q fp32 [B, d, V] the drafts'
+        (None: certain drafts).  Returns (tokens int32 [B, d + 1]: the accepted,
+        one drawn, then -1; n int32 [B]: how many)."""
+        return _tree_calls().verify_drafts(p, drafts, accept_u, sample_u, q, counts)
+
     def wait_selftest(self, polls: int = 4096) -> int:
         """Device bounded waits made to run out (ssd_op_wait_selftest);
         returns the code (3 = both waits gave up and reported)."""

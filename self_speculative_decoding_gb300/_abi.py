@@ -142,6 +142,15 @@ _SIGS = {
     "ssd_op_beam_select_workspace": [_I, _I, _I],
     "ssd_op_beam_select": [_P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, C.c_size_t, _P],
     "ssd_op_beam_reorder": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P],
+    "ssd_op_rope_append": [_P, _I, _I, _P, _P, _P, _P, _P, C.c_float, C.c_float, _P, _P, _I, C.c_size_t,
+                           _I, _I, _I, _P, _P],
+    "ssd_op_cache_quantize": [_P, _P, _I, C.c_size_t, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I,
+                              C.c_size_t, C.c_size_t, _P, _P],
+    "ssd_op_cache_attention_workspace": [_I, _I, _I, _I, _I],
+    "ssd_op_cache_attention": [_P, _I, _I, _P, _P, _P, _P, _I, C.c_size_t, _P, _P, _P, _P, _P, _I, _I,
+                               C.c_size_t, C.c_size_t, _I, _I, _I, _I, _I, C.c_float, _P, _P,
+                               C.c_size_t, _P],
+    "ssd_op_verify_drafts": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P],
 }
 
 EXPORTED = tuple(_SIGS)
@@ -149,7 +158,8 @@ EXPORTED = tuple(_SIGS)
 # What the native binding calls (csrc/binding.cpp).
 TREE_CALLS = ("ssd_op_tree_attention_workspace", "ssd_op_tree_attention", "ssd_op_cache_evict",
               "ssd_op_beam_select_workspace", "ssd_op_beam_select", "ssd_op_beam_reorder",
-              "ssd_ops_last_error")
+              "ssd_op_rope_append", "ssd_op_cache_quantize", "ssd_op_cache_attention_workspace",
+              "ssd_op_cache_attention", "ssd_op_verify_drafts", "ssd_ops_last_error")
 
 
 def load(path: Optional[str] = None) -> C.CDLL:

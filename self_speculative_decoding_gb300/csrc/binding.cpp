@@ -1,4 +1,5 @@
-// Python binding of the tree-decoding calls (ssd_ops.h): checks the tensors
+// Python binding of the tree-decoding calls and of those of several sequences
+// (ssd_ops.h): checks the tensors
 // (the library sees bare pointers), allocates results and workspaces, and
 // calls the library.  Marshalling only, as _abi.py is for the other calls;
 // these run several times per layer or token, and through ctypes the checks
@@ -12,6 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <limits>
 #include <string>
 
@@ -27,6 +29,11 @@ struct Library {
   decltype(&ssd_op_beam_select_workspace) select_workspace = nullptr;
   decltype(&ssd_op_beam_select) beam_select = nullptr;
   decltype(&ssd_op_beam_reorder) beam_reorder = nullptr;
+  decltype(&ssd_op_rope_append) rope_append = nullptr;
+  decltype(&ssd_op_cache_quantize) cache_quantize = nullptr;
+  decltype(&ssd_op_cache_attention_workspace) cache_workspace = nullptr;
+  decltype(&ssd_op_cache_attention) cache_attention = nullptr;
+  decltype(&ssd_op_verify_drafts) verify_drafts = nullptr;
   decltype(&ssd_ops_last_error) last_error = nullptr;
   PyObject* error = nullptr;  // SSDError
 } lib;
@@ -315,6 +322,248 @@ PyObject* beam_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
   SSD_END
 }
 
+// Caches of several sequences, [B, Hkv, rows, dh] with any stride between two:
+// the address, and the stride (that of both caches of a pair).
+void* seq_arg(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape,
+              int device, size_t& stride, bool first) {
+  if (t.scalar_type() != type || t.sizes() != shape)
+    refuse(std::string(name) + ": expected " + c10::toString(type) + " of shape " +
+           shape_text(shape) + ", got " + c10::toString(t.scalar_type()) + " of shape " +
+           shape_text(t.sizes()));
+  if (!t.is_cuda() || t.get_device() != device)
+    refuse(std::string(name) + ": expected a tensor on CUDA device " + std::to_string(device) +
+           ", got " + t.device().str());
+  int64_t one = 1;
+  for (int64_t i = t.dim() - 1; i > 0; --i) {
+    if (t.size(i) > 1 && t.stride(i) != one) refuse(std::string(name) + ": expected contiguous sequences");
+    one *= t.size(i);
+  }
+  const int64_t s = t.size(0) > 1 ? t.stride(0) : one;
+  if (s < one) refuse(std::string(name) + ": sequences overlap");
+  // (a lone sequence has any stride)
+  if (first)
+    stride = (size_t)s;
+  else if (t.size(0) > 1 && stride != (size_t)s)
+    refuse(std::string(name) + ": expected the stride of its pair");
+  return t.data_ptr();
+}
+
+void few(at::IntArrayRef sizes) {
+  for (int64_t x : sizes)
+    if (x > std::numeric_limits<int32_t>::max()) refuse("too many rows");
+}
+
+// The rows of a scale: max_seq / block, where that is whole.
+int64_t block_of(const at::Tensor& k8, const at::Tensor& scale) {
+  if (k8.dim() != 4 || scale.dim() != 3 || scale.size(2) < 1 || k8.size(2) % scale.size(2))
+    refuse("expected k8 [B, Hkv, max_seq, dh] and k_scale [B, Hkv, max_seq / block]");
+  return k8.size(2) / scale.size(2);
+}
+
+const int32_t* per_seq(const at::Tensor* t, const char* name, int64_t B, int device) {
+  return t ? (const int32_t*)arg(*t, name, at::kInt, at::IntArrayRef(&B, 1), device) : nullptr;
+}
+
+// (qkv, lengths, k, v, H, Hkv, dh, theta, q_gain, k_gain, eps, counts,
+//  positions, out) -> q
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  SSD_BEGIN
+  want(14, n);
+  const at::Tensor &qkv = tensor(a[0], "qkv"), &lengths = tensor(a[1], "lengths");
+  const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  const int32_t H = whole(a[4], "H"), Hkv = whole(a[5], "Hkv"), dh = whole(a[6], "dh");
+  const double theta = PyFloat_AsDouble(a[7]);
+  if (theta == -1.0 && PyErr_Occurred()) throw Refused();
+  const at::Tensor *qg = optional(a[8], "q_gain"), *kg = optional(a[9], "k_gain");
+  const double eps = PyFloat_AsDouble(a[10]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Refused();
+  const at::Tensor *counts = optional(a[11], "counts"), *positions = optional(a[12], "positions");
+  const at::Tensor* given = optional(a[13], "out");
+  if (qkv.dim() != 3 || k.dim() != 4)
+    refuse("expected qkv [B, T, (H + 2 Hkv) dh] and k [B, Hkv, rows, dh]");
+  const int dev = device_of(qkv, "qkv");
+  const int64_t B = qkv.size(0), T = qkv.size(1), R = k.size(2);
+  few(qkv.sizes());
+  few(k.sizes());
+  if (H < 1 || Hkv < 1 || dh < 1 || H > 65536 || Hkv > 65536 || dh > 65536) refuse("H, Hkv, dh");
+  const int64_t row[3] = {B, T, ((int64_t)H + 2 * (int64_t)Hkv) * dh}, cache[4] = {B, Hkv, R, dh};
+  const int64_t res[4] = {B, T, H, dh}, gain[1] = {dh};
+  size_t stride = 0;
+  void* pq = arg(qkv, "qkv", at::kFloat, row, dev);
+  const int32_t* pl = per_seq(&lengths, "lengths", B, dev);
+  void* pk = seq_arg(k, "k", at::kBFloat16, cache, dev, stride, true);
+  void* pv = seq_arg(v, "v", at::kBFloat16, cache, dev, stride, false);
+  void* pqg = qg ? arg(*qg, "q_gain", at::kFloat, gain, dev) : nullptr;
+  void* pkg = kg ? arg(*kg, "k_gain", at::kFloat, gain, dev) : nullptr;
+  const int32_t* pc = per_seq(counts, "counts", B, dev);
+  const int32_t* pp = per_seq(positions, "positions", B, dev);
+  const Place place(qkv);
+  void* po = given ? arg(*given, "out", at::kBFloat16, res, dev) : nullptr;
+  at::Tensor out;
+  ssd_status st;
+  {
+    const Unlocked unlocked;
+    if (!given) {
+      out = make(qkv, res, at::kBFloat16);
+      po = out.data_ptr();
+    }
+    st = lib.rope_append((const float*)pq, (int32_t)B, (int32_t)T, pl, pc, pp, (const float*)pqg,
+                         (const float*)pkg, (float)eps, (float)theta, pk, pv, (int32_t)R, stride, H,
+                         Hkv, dh, po, place.stream);
+  }
+  check(st);
+  return THPVariable_Wrap(given ? *given : out);
+  SSD_END
+}
+
+// (k, v, held, lengths, k8, v8, k_scale, v_scale, held_out) -> held_out
+PyObject* cache_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  SSD_BEGIN
+  want(9, n);
+  const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+  const at::Tensor &held = tensor(a[2], "held"), &lengths = tensor(a[3], "lengths");
+  const at::Tensor &k8 = tensor(a[4], "k8"), &v8 = tensor(a[5], "v8");
+  const at::Tensor &ks = tensor(a[6], "k_scale"), &vs = tensor(a[7], "v_scale");
+  const at::Tensor* given = optional(a[8], "held_out");
+  if (k.dim() != 4) refuse("k: expected [B, Hkv, rows, dh]");
+  const int64_t block = block_of(k8, ks), B = k.size(0);
+  const int dev = device_of(k, "k");
+  few(k.sizes());
+  few(k8.sizes());
+  const int64_t eight[4] = {B, k.size(1), k8.size(2), k.size(3)};
+  const int64_t scales[3] = {B, k.size(1), ks.size(2)};
+  size_t stride = 0, stride8 = 0, scale_stride = 0;
+  void* pk = seq_arg(k, "k", at::kBFloat16, k.sizes(), dev, stride, true);
+  void* pv = seq_arg(v, "v", at::kBFloat16, k.sizes(), dev, stride, false);
+  const int32_t* ph = per_seq(&held, "held", B, dev);
+  const int32_t* pl = per_seq(&lengths, "lengths", B, dev);
+  void* pk8 = seq_arg(k8, "k8", at::kFloat8_e4m3fn, eight, dev, stride8, true);
+  void* pv8 = seq_arg(v8, "v8", at::kFloat8_e4m3fn, eight, dev, stride8, false);
+  void* pks = seq_arg(ks, "k_scale", at::kFloat, scales, dev, scale_stride, true);
+  void* pvs = seq_arg(vs, "v_scale", at::kFloat, scales, dev, scale_stride, false);
+  const Place place(k);
+  void* po = given ? arg(*given, "held_out", at::kInt, at::IntArrayRef(&B, 1), dev) : nullptr;
+  at::Tensor out;
+  ssd_status st;
+  {
+    const Unlocked unlocked;
+    if (!given) {
+      out = make(k, {B}, at::kInt);
+      po = out.data_ptr();
+    }
+    st = lib.cache_quantize(pk, pv, (int32_t)k.size(2), stride, ph, pl, (int32_t)B, (int32_t)k.size(1),
+                            (int32_t)k.size(3), (int32_t)block, pk8, pv8, (float*)pks, (float*)pvs,
+                            (int32_t)k8.size(2), stride8, scale_stride, (int32_t*)po, place.stream);
+  }
+  check(st);
+  return THPVariable_Wrap(given ? *given : out);
+  SSD_END
+}
+
+// (q, k, v, lengths, k8, v8, k_scale, v_scale, held, counts, window, sinks,
+//  scale, out) -> out
+PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  SSD_BEGIN
+  want(14, n);
+  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+  const at::Tensor& lengths = tensor(a[3], "lengths");
+  const at::Tensor *k8 = optional(a[4], "k8"), *v8 = optional(a[5], "v8");
+  const at::Tensor *ks = optional(a[6], "k_scale"), *vs = optional(a[7], "v_scale");
+  const at::Tensor *held = optional(a[8], "held"), *counts = optional(a[9], "counts");
+  const int32_t window = whole(a[10], "window"), sinks = whole(a[11], "sinks");
+  const at::Tensor* given = optional(a[13], "out");
+  if (q.dim() != 4 || k.dim() != 4) refuse("expected q [B, T, H, dh] and k [B, Hkv, rows, dh]");
+  const bool eight = k8 || v8 || ks || vs || held;
+  if (eight && !(k8 && v8 && ks && vs && held)) refuse("k8, v8, k_scale, v_scale and held go together");
+  const int dev = device_of(q, "q");
+  few(q.sizes());
+  few(k.sizes());
+  const int64_t B = q.size(0), T = q.size(1), H = q.size(2), dh = q.size(3), Hkv = k.size(1);
+  double scale = dh ? 1.0 / std::sqrt((double)dh) : 0.0;
+  if (a[12] != Py_None) {
+    scale = PyFloat_AsDouble(a[12]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Refused();
+  }
+  const int64_t cache[4] = {B, Hkv, k.size(2), dh};
+  size_t stride = 0, stride8 = 0, scale_stride = 0;
+  int64_t block = 0, max_seq = 0;
+  void* pq = arg(q, "q", at::kBFloat16, q.sizes(), dev);
+  void* pk = seq_arg(k, "k", at::kBFloat16, cache, dev, stride, true);
+  void* pv = seq_arg(v, "v", at::kBFloat16, cache, dev, stride, false);
+  const int32_t* pl = per_seq(&lengths, "lengths", B, dev);
+  const int32_t* pc = per_seq(counts, "counts", B, dev);
+  const int32_t* ph = per_seq(held, "held", B, dev);
+  void *pk8 = nullptr, *pv8 = nullptr, *pks = nullptr, *pvs = nullptr;
+  if (eight) {
+    block = block_of(*k8, *ks);
+    max_seq = k8->size(2);
+    few(k8->sizes());
+    const int64_t rows8[4] = {B, Hkv, max_seq, dh}, scales[3] = {B, Hkv, ks->size(2)};
+    pk8 = seq_arg(*k8, "k8", at::kFloat8_e4m3fn, rows8, dev, stride8, true);
+    pv8 = seq_arg(*v8, "v8", at::kFloat8_e4m3fn, rows8, dev, stride8, false);
+    pks = seq_arg(*ks, "k_scale", at::kFloat, scales, dev, scale_stride, true);
+    pvs = seq_arg(*vs, "v_scale", at::kFloat, scales, dev, scale_stride, false);
+  }
+  const Place place(q);
+  void* po = given ? arg(*given, "out", at::kBFloat16, q.sizes(), dev) : nullptr;
+  at::Tensor out;
+  ssd_status st;
+  {
+    const Unlocked unlocked;
+    const size_t need = lib.cache_workspace((int32_t)B, (int32_t)T, (int32_t)H, (int32_t)Hkv, (int32_t)dh);
+    if (!given && need) {                        // (0: refused sizes)
+      out = make(q, q.sizes(), at::kBFloat16);
+      po = out.data_ptr();
+    }
+    const at::Tensor ws = make(q, {(int64_t)(need ? need : 256)}, at::kByte);
+    st = lib.cache_attention(pq, (int32_t)B, (int32_t)T, pl, pc, pk, pv, (int32_t)k.size(2), stride, pk8,
+                             pv8, (const float*)pks, (const float*)pvs, ph, (int32_t)max_seq,
+                             (int32_t)block, stride8, scale_stride, window, sinks, (int32_t)H, (int32_t)Hkv,
+                             (int32_t)dh, (float)scale, po, ws.data_ptr(), need, place.stream);
+  }
+  check(st);
+  return THPVariable_Wrap(given ? *given : out);
+  SSD_END
+}
+
+// (p, drafts, accept_u, sample_u, q, counts) -> (tokens, n)
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  SSD_BEGIN
+  want(6, n);
+  const at::Tensor &p = tensor(a[0], "p"), &drafts = tensor(a[1], "drafts");
+  const at::Tensor &au = tensor(a[2], "accept_u"), &su = tensor(a[3], "sample_u");
+  const at::Tensor *q = optional(a[4], "q"), *counts = optional(a[5], "counts");
+  if (p.dim() != 3 || p.size(1) < 1) refuse("p: expected [B, d + 1, V]");
+  const int dev = device_of(p, "p");
+  few(p.sizes());
+  const int64_t B = p.size(0), d = p.size(1) - 1, V = p.size(2);
+  const int64_t each[2] = {B, d}, other[3] = {B, d, V};
+  void* pp = arg(p, "p", at::kFloat, p.sizes(), dev);
+  void* pd = arg(drafts, "drafts", at::kInt, each, dev);
+  void* pa = arg(au, "accept_u", at::kFloat, each, dev);
+  void* ps = arg(su, "sample_u", at::kFloat, at::IntArrayRef(&B, 1), dev);
+  void* pq = q ? arg(*q, "q", at::kFloat, other, dev) : nullptr;
+  const int32_t* pc = per_seq(counts, "counts", B, dev);
+  const Place place(p);
+  at::Tensor tokens, many;
+  ssd_status st;
+  {
+    const Unlocked unlocked;
+    tokens = make(p, {B, d + 1}, at::kInt);
+    many = make(p, {B}, at::kInt);
+    st = lib.verify_drafts((const float*)pp, (const float*)pq, (const int32_t*)pd, pc, (const float*)pa,
+                           (const float*)ps, (int32_t)B, (int32_t)d, (int32_t)V,
+                           (int32_t*)tokens.data_ptr(), (int32_t*)many.data_ptr(), place.stream);
+  }
+  check(st);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(tokens));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(many));
+  return r;
+  SSD_END
+}
+
 // ({name: address}, SSDError)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   SSD_BEGIN
@@ -330,6 +579,11 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   lib.select_workspace = (decltype(lib.select_workspace))at("ssd_op_beam_select_workspace");
   lib.beam_select = (decltype(lib.beam_select))at("ssd_op_beam_select");
   lib.beam_reorder = (decltype(lib.beam_reorder))at("ssd_op_beam_reorder");
+  lib.rope_append = (decltype(lib.rope_append))at("ssd_op_rope_append");
+  lib.cache_quantize = (decltype(lib.cache_quantize))at("ssd_op_cache_quantize");
+  lib.cache_workspace = (decltype(lib.cache_workspace))at("ssd_op_cache_attention_workspace");
+  lib.cache_attention = (decltype(lib.cache_attention))at("ssd_op_cache_attention");
+  lib.verify_drafts = (decltype(lib.verify_drafts))at("ssd_op_verify_drafts");
   lib.last_error = (decltype(lib.last_error))at("ssd_ops_last_error");
   if (PyErr_Occurred()) throw Refused();
   Py_INCREF(a[1]);
@@ -343,7 +597,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   { #f, (PyCFunction)(void*)f, METH_FASTCALL, "" }
 PyMethodDef methods[] = {SSD_METHOD(bind),        SSD_METHOD(tree_attention),
                          SSD_METHOD(cache_evict), SSD_METHOD(beam_select),
-                         SSD_METHOD(beam_reorder), {nullptr, nullptr, 0, nullptr}};
+                         SSD_METHOD(beam_reorder), SSD_METHOD(rope_append),
+                         SSD_METHOD(cache_quantize), SSD_METHOD(cache_attention),
+                         SSD_METHOD(verify_drafts), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr,               nullptr,    nullptr, nullptr};
 

@@ -1,0 +1,140 @@
+// Cache rows to 8 bits (sm_103a).
+//
+// A block of `block` rows of one head becomes e4m3 values and one scale,
+//   scale = 2^e, the smallest with max |x| <= 448 2^e   (e >= -64; 1 for zeros)
+//   x8    = e4m3(x / scale), to nearest, ties to even.
+// The scale is a power of two: a division by it is exact, so that each value is
+// rounded once, and e4m3, being a floating format, has the same relative steps
+// wherever the largest value lies in its last binade.  Infinities and NaN become
+// NaN and do not enter the scale.
+#include <cuda_fp8.h>
+
+#include "batch.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sequence b's whole blocks that are to be moved: [from, to).
+SSD_DI void blocks_of(const QuantizeArgs& a, int b, int& from, int& to) {
+  const int held = a.held[b], n = a.lengths[b];
+  from = to = 0;
+  if (held < 0 || held % a.block || held > a.max_seq || n > a.max_seq || n <= held) return;
+  if (n - held > a.rows) return;                 // the ring has lost a row
+  from = held / a.block;
+  to = n / a.block;
+}
+
+SSD_DI uint32_t abs_finite(uint32_t x) {         // of two bf16: |x|'s bits, 0 if not finite
+  x &= 0x7fff7fffu;
+  if ((x & 0xffffu) >= 0x7f80u) x &= 0xffff0000u;
+  if (x >= 0x7f800000u) x &= 0xffffu;
+  return x;
+}
+
+SSD_DI uint32_t eight_of(float x, float inv) {
+  return isfinite(x) ? __nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3) : 0x7fu;
+}
+
+// Items = (sequence, block, K or V, head), dealt to the CTAs in turn; a CTA has
+// a block in registers: one read, one write.
+__global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_constant__ QuantizeArgs a) {
+  __shared__ int first[kBatchMaxSeqs + 1];       // blocks of all sequences before b
+  __shared__ uint32_t warp_max[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int b = tid; b < a.B; b += kThreads) {
+    int from, to;
+    blocks_of(a, b, from, to);
+    first[b + 1] = to - from;
+    if (blockIdx.x == 0) a.held_out[b] = to > from ? to * a.block : a.held[b];
+  }
+  if (tid == 0) first[0] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    int sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int x = b0 + lane < a.B ? first[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += y;
+      }
+      if (b0 + lane < a.B) first[b0 + lane + 1] = sum + x;
+      sum += __shfl_sync(~0u, x, 31);
+    }
+  }
+  __syncthreads();
+  const int total = first[a.B], per = 2 * a.Hkv;
+  const int units = a.block * a.dh / 8;          // of 16 bytes
+  for (long long item = blockIdx.x; item < (long long)total * per; item += gridDim.x) {
+    const int j = (int)(item / per), rest = (int)(item - (long long)j * per);
+    const bool is_v = rest >= a.Hkv;
+    const int h = rest - (is_v ? a.Hkv : 0);
+    int lo = 0, hi = a.B - 1;                    // the last b with first[b] <= j
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (first[mid] <= j) lo = mid;
+      else hi = mid - 1;
+    }
+    int from, to;
+    blocks_of(a, lo, from, to);
+    const int block = from + j - first[lo];
+    const size_t row0 = (size_t)block * a.block;
+    const bf16* src = (is_v ? a.v : a.k) + (size_t)lo * a.seq_stride + (size_t)h * a.rows * a.dh;
+    uint4 x[8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int u = tid + q * kThreads;
+      x[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (u < units) {
+        const size_t e = (size_t)u * 8, row = (row0 + e / a.dh) % a.rows;
+        x[q] = *reinterpret_cast<const uint4*>(src + row * a.dh + e % a.dh);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      most = __vmaxu2(__vmaxu2(most, __vmaxu2(abs_finite(x[q].x), abs_finite(x[q].y))),
+                      __vmaxu2(abs_finite(x[q].z), abs_finite(x[q].w)));
+    most = max(most & 0xffffu, most >> 16);
+    most = __reduce_max_sync(~0u, most);
+    __syncthreads();                             // (the item before has read)
+    if (lane == 0) warp_max[warp] = most;
+    __syncthreads();
+    most = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[lane] : 0u);
+    float scale = 1.f;
+    int e = 0;
+    if (most) {
+      const float part = frexpf(__uint_as_float(most << 16), &e);
+      e = max(e - (part > 0.875f ? 8 : 9), -64);
+      scale = ldexpf(1.f, e);
+    }
+    const float inv = ldexpf(1.f, -e);
+    uint8_t* dst = (is_v ? a.v8 : a.k8) + (size_t)lo * a.seq8_stride + ((size_t)h * a.max_seq + row0) * a.dh;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int u = tid + q * kThreads;
+      if (u >= units) continue;
+      auto four = [&](uint32_t s, uint32_t t) {
+        return eight_of(bf16_lo(s), inv) | eight_of(bf16_hi(s), inv) << 8 | eight_of(bf16_lo(t), inv) << 16 |
+               eight_of(bf16_hi(t), inv) << 24;
+      };
+      *reinterpret_cast<uint2*>(dst + (size_t)u * 8) = make_uint2(four(x[q].x, x[q].y), four(x[q].z, x[q].w));
+    }
+    if (tid == 0)
+      (is_v ? a.v_scale : a.k_scale)[(size_t)lo * a.scale_stride + (size_t)h * (a.max_seq / a.block) + block] = scale;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_quantize(const QuantizeArgs& a, cudaStream_t s) {
+  // at most so many items, and eight CTAs for each SM
+  const long long most = (long long)a.B * 2 * a.Hkv * ((a.rows < a.max_seq ? a.rows : a.max_seq) / a.block + 1);
+  const long long ctas = most < 8 * 152 ? most : 8 * 152;
+  cache_quantize_kernel<<<dim3((unsigned)ctas), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace ssd

@@ -7,6 +7,7 @@
 #include <string>
 
 #include "../../include/ssd_ops.h"
+#include "batch.cuh"
 #include "kernels.cuh"
 #include "tree.cuh"
 
@@ -127,6 +128,54 @@ void tree_frequencies(float theta, int dh, double* out) {
     last_dh = dh;
   }
   std::memcpy(out, table, sizeof(double) * (dh / 2));
+}
+
+// Whether two sets of n runs of `span` bytes, `stride` bytes apart, meet.
+bool runs_overlap(const void* a, const void* b, size_t n, size_t stride, size_t span) {
+  const size_t all = (n - 1) * stride + span;
+  if (!overlap(a, all, b, all)) return false;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  const size_t d = (x < y ? y - x : x - y) % stride;
+  return d < span || stride - d < span;
+}
+
+// The caches of a call of many sequences: sizes, strides, pointers.
+ssd_status check_caches(const char* call, const void* k, const void* v, int32_t rows, size_t stride, int32_t B,
+                        int32_t Hkv, int32_t dh) {
+  const std::string at(call);
+  if (B < 1 || B > kBatchMaxSeqs || Hkv < 1 || Hkv > 4096 || (dh != 64 && dh != 128) || rows < 1)
+    return op_fail(SSD_ERR_INVALID_ARG, at + ": B / Hkv / dh / rows");
+  const size_t one = (size_t)Hkv * rows * dh;
+  if (stride < one || stride % 8 || stride > ((size_t)1 << 46))
+    return op_fail(SSD_ERR_INVALID_ARG, at + ": seq_stride");
+  if (!al16(k) || !al16(v)) return op_fail(SSD_ERR_INVALID_ARG, at + ": k / v pointers");
+  return SSD_OK;
+}
+ssd_status check_eight(const char* call, const void* k8, const void* v8, const float* ks, const float* vs,
+                       int32_t max_seq, int32_t block, size_t stride8, size_t scale_stride, int32_t B, int32_t Hkv,
+                       int32_t dh) {
+  const std::string at(call);
+  if ((block != 32 && block != 64 && block != 128) || max_seq < block || max_seq % block)
+    return op_fail(SSD_ERR_INVALID_ARG, at + ": block / max_seq");
+  const size_t one = (size_t)Hkv * max_seq * dh, scales = (size_t)Hkv * (max_seq / block);
+  if (stride8 < one || stride8 % 16 || stride8 > ((size_t)1 << 46) || scale_stride < scales ||
+      scale_stride > ((size_t)1 << 46))
+    return op_fail(SSD_ERR_INVALID_ARG, at + ": seq8_stride / scale_stride");
+  if (!al16(k8) || !al16(v8) || !al4(ks) || !al4(vs))
+    return op_fail(SSD_ERR_INVALID_ARG, at + ": k8 / v8 / scale pointers");
+  return SSD_OK;
+}
+
+// Bytes from a cache's first element to the end of its last.
+size_t cache_span(int32_t B, size_t stride, size_t one, size_t element) {
+  return ((size_t)(B - 1) * stride + one) * element;
+}
+
+ssd_status check_cache_attention(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh) {
+  if (B < 1 || B > kBatchMaxSeqs || T < 1 || Hkv < 1 || Hkv > 4096 || H < 1 || H % Hkv || H / Hkv > 128 ||
+      T > 128 / (H / Hkv) || (dh != 64 && dh != 128))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_attention sizes");
+  return SSD_OK;
 }
 
 }  // namespace
@@ -599,6 +648,189 @@ ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* pare
   a.stop = stop;
   a.units = row_bytes / 16;
   return cu(launch_beam_reorder(a, (cudaStream_t)stream), "beam_reorder");
+}
+
+ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int32_t* lengths,
+                              const int32_t* counts, const int32_t* positions,
+                              const float* q_gain, const float* k_gain, float eps, float theta,
+                              void* k, void* v, int32_t rows, size_t seq_stride, int32_t H,
+                              int32_t Hkv, int32_t dh, void* q_out, void* stream) {
+  ssd_status r = check_caches("rope_append", k, v, rows, seq_stride, B, Hkv, dh);
+  if (r != SSD_OK) return r;
+  if (T < 1 || T > rows || H < 1 || H > 65536 || !(theta > 0.f) || !std::isfinite(theta) || !(eps >= 0.f) ||
+      !std::isfinite(eps))
+    return op_fail(SSD_ERR_INVALID_ARG, "rope_append: T / H / theta / eps");
+  if (!al16(qkv) || !al16(q_out) || !al4(lengths) || (counts && !al4(counts)) || (positions && !al4(positions)) ||
+      (q_gain && !al16(q_gain)) || (k_gain && !al16(k_gain)))
+    return op_fail(SSD_ERR_INVALID_ARG, "rope_append pointers");
+  const size_t tokens = (size_t)B * T, in = tokens * ((size_t)H + 2 * Hkv) * dh * 4, o = tokens * H * dh * 2;
+  const size_t one = (size_t)Hkv * rows * dh, cache = cache_span(B, seq_stride, one, 2);
+  if (runs_overlap(k, v, B, seq_stride * 2, one * 2) || overlap(qkv, in, q_out, o) || overlap(qkv, in, k, cache) || overlap(qkv, in, v, cache) ||
+      overlap(q_out, o, k, cache) || overlap(q_out, o, v, cache))
+    return op_fail(SSD_ERR_INVALID_ARG, "rope_append: buffers overlap");
+  RopeAppendArgs a;
+  a.qkv = qkv;
+  a.lengths = lengths;
+  a.counts = counts;
+  a.positions = positions;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.eps = eps;
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.dh = dh;
+  a.rows = rows;
+  a.seq_stride = seq_stride;
+  a.k = (bf16*)k;
+  a.v = (bf16*)v;
+  a.q = (bf16*)q_out;
+  double half_turns[kTreeMaxHalf];
+  tree_frequencies(theta, dh, half_turns);
+  for (int i = 0; i < dh / 2; ++i) {
+    const double x = 0.5 * half_turns[i];
+    a.turns[i] = (uint64_t)((x - std::floor(x)) * 0x1p64);
+  }
+  return cu(launch_rope_append(a, (cudaStream_t)stream), "rope_append");
+}
+
+ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, size_t seq_stride,
+                                 const int32_t* held, const int32_t* lengths, int32_t B,
+                                 int32_t Hkv, int32_t dh, int32_t block, void* k8, void* v8,
+                                 float* k_scale, float* v_scale, int32_t max_seq,
+                                 size_t seq8_stride, size_t scale_stride, int32_t* held_out,
+                                 void* stream) {
+  ssd_status r = check_caches("cache_quantize", k, v, rows, seq_stride, B, Hkv, dh);
+  if (r != SSD_OK) return r;
+  r = check_eight("cache_quantize", k8, v8, k_scale, v_scale, max_seq, block, seq8_stride, scale_stride, B, Hkv, dh);
+  if (r != SSD_OK) return r;
+  if (!al4(held) || !al4(lengths) || !al4(held_out))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_quantize pointers");
+  const size_t in = cache_span(B, seq_stride, (size_t)Hkv * rows * dh, 2);
+  const size_t one = (size_t)Hkv * max_seq * dh, scales = (size_t)4 * Hkv * (max_seq / block);
+  const size_t o = cache_span(B, seq8_stride, one, 1), n = (size_t)4 * B;
+  if (runs_overlap(k8, v8, B, seq8_stride, one) || runs_overlap(k_scale, v_scale, B, scale_stride * 4, scales) ||
+      overlap(k, in, k8, o) || overlap(k, in, v8, o) || overlap(v, in, k8, o) || overlap(v, in, v8, o) ||
+      overlap(held, n, held_out, n) || overlap(lengths, n, held_out, n))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_quantize: buffers overlap");
+  QuantizeArgs a;
+  a.k = (const bf16*)k;
+  a.v = (const bf16*)v;
+  a.held = held;
+  a.lengths = lengths;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.dh = dh;
+  a.rows = rows;
+  a.block = block;
+  a.max_seq = max_seq;
+  a.seq_stride = seq_stride;
+  a.seq8_stride = seq8_stride;
+  a.scale_stride = scale_stride;
+  a.k8 = (uint8_t*)k8;
+  a.v8 = (uint8_t*)v8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.held_out = held_out;
+  return cu(launch_cache_quantize(a, (cudaStream_t)stream), "cache_quantize");
+}
+
+size_t ssd_op_cache_attention_workspace(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh) {
+  if (check_cache_attention(B, T, H, Hkv, dh) != SSD_OK) return 0;
+  CacheAttnArgs a;
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.dh = dh;
+  return cache_attn_workspace(a, nullptr);
+}
+
+ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int32_t* lengths,
+                                  const int32_t* counts, const void* k, const void* v,
+                                  int32_t rows, size_t seq_stride, const void* k8, const void* v8,
+                                  const float* k_scale, const float* v_scale, const int32_t* held,
+                                  int32_t max_seq, int32_t block, size_t seq8_stride,
+                                  size_t scale_stride, int32_t window, int32_t sinks, int32_t H,
+                                  int32_t Hkv, int32_t dh, float scale, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  ssd_status r = check_cache_attention(B, T, H, Hkv, dh);
+  if (r != SSD_OK) return r;
+  r = check_caches("cache_attention", k, v, rows, seq_stride, B, Hkv, dh);
+  if (r != SSD_OK) return r;
+  const bool eight = held != nullptr;
+  if (eight) {
+    r = check_eight("cache_attention", k8, v8, k_scale, v_scale, max_seq, block, seq8_stride, scale_stride, B, Hkv,
+                    dh);
+    if (r != SSD_OK) return r;
+  } else if (k8 || v8 || k_scale || v_scale) {
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_attention: 8-bit caches need held");
+  }
+  if (window < 0 || sinks < 0 || !std::isfinite(scale))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_attention: window / sinks / scale");
+  if (!al16(q) || !al16(out) || !al4(lengths) || (counts && !al4(counts)) || (held && !al4(held)) || !workspace ||
+      ((uintptr_t)workspace & 255u))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_attention pointers");
+  CacheAttnArgs a;
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.dh = dh;
+  if (cache_attn_workspace(a, workspace) > workspace_bytes)
+    return op_fail(SSD_ERR_CAPACITY, "cache_attention: workspace too small");
+  a.q = (const bf16*)q;
+  a.lengths = lengths;
+  a.counts = counts;
+  a.held = held;
+  a.k = (const bf16*)k;
+  a.v = (const bf16*)v;
+  a.rows = rows;
+  a.seq_stride = seq_stride;
+  if (eight) {
+    a.k8 = (const uint8_t*)k8;
+    a.v8 = (const uint8_t*)v8;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.max_seq = max_seq;
+    a.block = block;
+    a.seq8_stride = seq8_stride;
+    a.scale_stride = scale_stride;
+  }
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  a.out = (bf16*)out;
+  return cu(launch_cache_attn(a, (cudaStream_t)stream), "cache_attention");
+}
+
+ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* drafts,
+                                const int32_t* counts, const float* accept_u,
+                                const float* sample_u, int32_t B, int32_t d, int32_t V,
+                                int32_t* tokens, int32_t* n, void* stream) {
+  if (B < 1 || B > kBatchMaxSeqs || d < 0 || d > 1024 || V < 1)
+    return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts sizes");
+  if (!al4(p) || (q && !al4(q)) || (d && (!al4(drafts) || !al4(accept_u))) || (counts && !al4(counts)) ||
+      !al4(sample_u) || !al4(tokens) || !al4(n))
+    return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts pointers");
+  if (d && overlap(drafts, (size_t)4 * B * d, tokens, (size_t)4 * B * (d + 1)))
+    return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts: drafts and tokens overlap");
+  VerifyArgs a;
+  a.p = p;
+  a.q = d ? q : nullptr;
+  a.drafts = drafts;
+  a.counts = counts;
+  a.accept_u = accept_u;
+  a.sample_u = sample_u;
+  a.B = B;
+  a.d = d;
+  a.V = V;
+  a.tokens = tokens;
+  a.n = n;
+  return cu(launch_verify_drafts(a, (cudaStream_t)stream), "verify_drafts");
 }
 
 }  // extern "C"
