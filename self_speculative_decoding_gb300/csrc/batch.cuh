@@ -65,8 +65,18 @@ struct CacheAttnArgs {
   int B = 0, T = 0, H = 0, Hkv = 0, G = 0, dh = 0, rows = 0, max_seq = 0, block = 32;
   int window = 0, sinks = 0;           // window 0: all rows
   size_t seq_stride = 0, seq8_stride = 0, scale_stride = 0;
-  float scale_log2 = 0.f;              // scale of the scores times log2(e)
+  float scale_log2 = 0.f;              // |scale| of the scores times log2(e)
+  bool negate = false;                 // the scale is below 0: q with the other sign
   bf16* out = nullptr;                 // [B][T][H][dh]
+  // workspace: partial results of the pairs (sequence, K/V head) that several
+  // CTAs share, two places for each CTA
+  int ctas = 0;
+  float* part_o = nullptr;             // [2 ctas][T G][dh] unnormalised outputs
+  float* part_m = nullptr;             // [2 ctas][T G] base-2 maximum of the row's scores
+  float* part_l = nullptr;             // [2 ctas][T G] sum of 2^(score - maximum)
+  int4* shared = nullptr;              // [ctas] (sequence, head, last CTA, -) of the pair that goes on
+                                       // behind the CTA's last tile; sequence -1: none
+  int give_up = -1;                    // self-test: this CTA acts as after a wait that gave up
 };
 size_t cache_attn_workspace(CacheAttnArgs& a, void* base);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);
@@ -91,32 +101,31 @@ SSD_DI int batch_count(const int32_t* counts, const int32_t* lengths, int b, int
   return n < 0 || n > INT32_MAX - T ? 0 : c;
 }
 
-// What an attention call reads of sequence b: rows [0, sinks) and [low, end),
+// What an attention call reads of a sequence: rows [0, sinks) and [low, end),
 // of which those below `held` are in 8 bits.  count < 0: the numbers make no
 // sense, or the ring no longer holds a row that is needed.
 struct SeqRange {
   int length, count, held, low, sinks, end;
 };
-SSD_DI SeqRange seq_range(const CacheAttnArgs& a, int b) {
-  SeqRange r;
-  r.length = a.lengths[b];
-  r.count = a.counts ? a.counts[b] : a.T;
-  r.held = a.held ? a.held[b] : 0;
-  if (r.length < 0 || r.length > INT32_MAX - a.T - 256 || r.count < 0 || r.count > a.T || r.held < 0 ||
-      r.held > a.max_seq || r.held > r.length + r.count) {
-    r = SeqRange{0, -1, 0, 0, 0, 0};
+SSD_DI SeqRange seq_range(const CacheAttnArgs& a, int length, int count, int held) {
+  SeqRange r = {0, 0, 0, 0, 0, 0};
+  if (length < 0 || length > INT32_MAX - a.T - 256 || count < 0 || count > a.T || held < 0 ||
+      held > a.max_seq || held > length + count) {
+    r.count = -1;
     return r;
   }
-  r.end = r.length + r.count;
-  r.low = a.window ? max(0, r.length + 1 - a.window) : 0;
+  if (count == 0) return r;
+  r.length = length;
+  r.count = count;
+  r.held = held;
+  r.end = length + count;
+  r.low = a.window ? max(0, length + 1 - a.window) : 0;
   r.sinks = min(a.sinks, r.low);
   if (r.sinks == r.low) r.sinks = r.low = 0;     // one run of rows
-  if (r.count == 0) r.end = r.low = r.sinks = 0;
-  // rows below `held` come from 8 bits; the ring has the others' newest only
-  const int first = r.sinks > r.held ? r.held : max(r.low, r.held);
+  // rows from `held` on come from the ring, which has the newest only
+  const int first = r.sinks > held ? held : max(r.low, held);
   if (r.end - first > a.rows || (a.rows % 128 && r.end > a.rows && r.end > first)) {
-    r.count = -1;
-    r.end = r.low = r.sinks = 0;
+    r = SeqRange{0, -1, 0, 0, 0, 0};
   }
   return r;
 }

@@ -802,7 +802,8 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
   }
   a.window = window;
   a.sinks = sinks;
-  a.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  a.scale_log2 = (float)(1.4426950408889634 * std::fabs((double)scale));
+  a.negate = scale < 0.f;
   a.out = (bf16*)out;
   return cu(launch_cache_attn(a, (cudaStream_t)stream), "cache_attention");
 }

@@ -368,6 +368,50 @@ def test_many_short_sequences(ops):
     a.check(a.call(ops))
 
 
+def plain_attention(a_q, K, V, length, scale, window=0, sinks=0):
+    """One sequence in 64 bits as torch operations: q [T, H, dh], K, V [Hkv, n,
+    dh] -> the result, sum p |v|, and a bound of the scores' error."""
+    T, H, dh = a_q.shape
+    Hkv, n = K.shape[:2]
+    q = a_q.double().view(T, Hkv, H // Hkv, dh).permute(1, 2, 0, 3)
+    s = scale * (q @ K[:, None].transpose(2, 3))
+    j, pos = torch.arange(n, device=q.device), length + torch.arange(T, device=q.device)[:, None]
+    hidden = j > pos
+    if window:
+        hidden |= (j >= sinks) & (j <= pos - window)
+    p = torch.softmax(s.masked_fill(hidden, -float("inf")), -1)
+    d = scale * (2.0 ** -17 * q.abs().amax() * K.abs().sum(-1).amax() +
+                 2 * dh * 2.0 ** -24 * (q.abs() @ K[:, None].abs().transpose(2, 3)).amax()) + 1e-6
+    back = lambda x: x.permute(2, 0, 1, 3).reshape(T, H, dh)  # noqa: E731
+    return back(p @ V[:, None]), back(p @ V[:, None].abs()), d.item()
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,window,std", [
+    ([131000], 1, 64, 8, 128, 0, 1.5), ([60000, 3, 9000], 3, 8, 2, 64, 0, 3.0), ([9000] * 9, 9, 16, 2, 128, 0, 1.5),
+    ([20000, 30001], 5, 6, 6, 128, 0, 4.0), ([40000, 17000], 16, 8, 1, 128, 0, 1.0), ([30000], 2, 40, 40, 128, 9000, 2.0),
+    ([50001], 40, 3, 1, 64, 20011, 2.0), ([700] * 300, 1, 8, 2, 64, 0, 2.0)])
+def test_long_contexts(ops, lengths, T, H, Hkv, dh, window, std):
+    # a CTA has many tiles, and runs of several sequences and heads
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    B, block, rows, sinks = len(lengths), 64, 256, 7 if window else 0
+    S = -(-max(lengths) // block) * block
+    held = [max(0, n - 31) // block * block for n in lengths]
+    q = (torch.randn(B, T, H, dh, generator=g, device="cuda") * std).bfloat16()
+    k, v = (torch.randn(B, Hkv, rows, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k8, v8 = ((torch.randn(B, Hkv, S, dh, generator=g, device="cuda") * 90).clamp_(-448, 448).to(torch.float8_e4m3fn)
+              for _ in range(2))
+    ks, vs = (torch.rand(B, Hkv, S // block, generator=g, device="cuda") / 90 + 0.004 for _ in range(2))
+    out = ops.cache_attention(q, k, v, whole(lengths), k8=k8, v8=v8, k_scale=ks, v_scale=vs, held=whole(held),
+                              window=window, sinks=sinks).double()
+    for b in range(0, B, max(1, B // 9)):
+        at = torch.arange(held[b], lengths[b] + T, device="cuda") % rows
+        K, V = (torch.cat((e[b, :, :held[b]].double() * s[b, :, :held[b] // block].double().repeat_interleave(block, 1)[..., None],
+                           x[b, :, at].double()), 1) for e, s, x in ((k8, ks, k), (v8, vs, v)))
+        ref, spread, d = plain_attention(q[b], K, V, lengths[b], dh ** -0.5, window, sinks)
+        off = (out[b] - ref).abs() / (U * ref.abs() + (U + 2 * d) * spread)
+        assert off.max().item() <= 1, (b, off.max().item())
+
+
 def test_scores_far_apart(ops):
     # one key takes nearly all, then a larger one comes; and 16 units of scale
     a = Attn([700], 2, 4, 2, 128, 128, [640], std=8.0)
@@ -729,7 +773,7 @@ def test_rounds_of_drafting_as_a_graph(ops):
         tokens, n = ops.verify_drafts(p.contiguous(), drafts, u[:, :d].contiguous(), u[:, 2 * d].contiguous(),
                                       q=torch.stack(probs, 1).contiguous())
         lengths.add_(n)
-        last.copy_(tokens.gather(1, (n - 1).long()[:, None])[:, 0])
+        last.copy_(tokens.gather(1, (n - 1).clamp(min=0).long()[:, None])[:, 0].clamp(0, V - 1))
         held.copy_(ops.cache_quantize(k, v, held, lengths, k8, v8, ks, vs))
         return tokens, n
 
