@@ -7,13 +7,17 @@
 //   S = q K^T               8-bit rows: q = (q0 + q1) 2^-a with two e4m3 parts, which
 //                           hold every bit of a bf16 number, so that the products
 //                           with the stored bytes are exact; bf16 rows: q itself
-//   P = 2^(S c - m) v_scale one thread per row, bf16 over S's columns
-//   O += P V                V as bf16 (e4m3 is a part of it) in shared memory
+//   P = 2^(S c - m) v_scale one thread per row, 16 bits over S's columns
+//   O += P V                8-bit rows: V widened to fp16, P in fp16; bf16 rows: both bf16
 //
 // K and q enter the matrix instructions as they are: a tile of K costs no thread
 // anything.  V cannot: P needs more than e4m3's range and bits (a first row that
 // takes most of the weight leaves the others small), and both operands of a
-// 16-bit product are 16 bits wide, so four warps widen V on its way.
+// 16-bit product are 16 bits wide, so four warps widen V on its way: to fp16,
+// which one instruction does for two values (bf16 takes four).  fp16 has less
+// range than P: P is held in units of 2^-7 vref 2^m, vref a power of two not
+// below any value scale so far, which keeps 11 bits down to 2^-18 of a row's
+// largest weight and steps of 2^-28 below; two binades of room make it grow seldom.
 //
 // Rows of the tile: with up to 32 query rows the tile holds four copies of them,
 // each of which keeps the keys of one quarter of the tile alone (64 rows: two
@@ -31,6 +35,8 @@
 // CTA's flag, every role runs out, and the CTA's rows become NaN.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "batch.cuh"
 #include "tc_dev.cuh"
@@ -188,24 +194,48 @@ SSD_DI Segment segment_at(const CacheAttnArgs& a, const Plan& p, long long at) {
 
 // ---- values
 
-// Four e4m3 to four bf16 (exact).
-SSD_DI uint2 widen(uint32_t x) {
-  const __half2 a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-  const __half2 b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3);
-  const float2 f = __half22float2(a), g = __half22float2(b);
-  return make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(g.x, g.y));
+// Two e4m3 (bytes lo and lo + 1 of x) to two fp16 of 2^-8 their value: the same
+// sign, exponent and fraction at fp16's places (exact, fp16's range holds what
+// e4m3's does; the code of NaN becomes 480 / 2^8).  Four integer instructions:
+// the conversion instruction runs on the unit of the exponentials, far more
+// slowly (a tile of 128 x 128 took 3000 cycles, against CYCLES so).
+template <int LO>
+SSD_DI uint32_t widen(uint32_t x) {
+  const uint32_t h = __byte_perm(x, 0u, LO == 0 ? 0x1404 : 0x3424);
+  return (h & 0x80008000u) | ((h >> 1) & 0x3fff3fffu);
 }
-// Two bf16 with what is not finite as 0; `bad` if there was any.
-SSD_DI uint32_t finite_only(uint32_t x, bool& bad) {
-  if ((x & 0x7f80u) == 0x7f80u) {
+constexpr uint32_t kWideNan = 0x3f80;            // what the code of NaN becomes, over all others
+SSD_DI uint32_t larger(uint32_t most, uint32_t x) {
+  const __half2 a = *reinterpret_cast<const __half2*>(&most), b = *reinterpret_cast<const __half2*>(&x);
+  const __half2 m = __hmax2(a, __habs2(b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+// The NaN of two widened values as such.
+SSD_DI uint32_t with_nan(uint32_t x) {
+  if ((x & 0x7fffu) == kWideNan) x |= 0x7fffu;
+  if ((x & 0x7fff0000u) == kWideNan << 16) x |= 0x7fff0000u;
+  return x;
+}
+// Two 16-bit numbers with what is not finite (all of the exponent's bits `e`
+// set) as 0; `bad` if there was any.
+SSD_DI uint32_t finite_only(uint32_t x, uint32_t e, bool& bad) {
+  if ((x & e & 0xffffu) == (e & 0xffffu)) {
     x &= 0xffff0000u;
     bad = true;
   }
-  if ((x & 0x7f800000u) == 0x7f800000u) {
+  if ((x & e & 0xffff0000u) == (e & 0xffff0000u)) {
     x &= 0xffffu;
     bad = true;
   }
   return x;
+}
+SSD_DI uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The smallest power of two that is not below |x| (x finite and not 0), 2^-126 at least.
+SSD_DI float power_above(float x) {
+  return __uint_as_float((__float_as_uint(fabsf(x)) + 0x7fffffu) & 0x7f800000u);
 }
 
 // How a row of V goes into the products: 0 as zeros (it is outside the tile's
@@ -379,13 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t kr = smem_addr(kring), wr = smem_addr(wide);
     constexpr uint32_t id8 = idesc_e4m3(128, kKeys), id16 = idesc_bf16(128, kKeys);
-    constexpr uint32_t idp = idesc_bf16(128, DH) | (1u << 16);  // B is MN-major
+    // (B is MN-major; fp16 in place of bf16 without bits 7 and 10)
+    constexpr uint32_t idp16 = idesc_bf16(128, DH) | (1u << 16), idp8 = idp16 & ~(1u << 7 | 1u << 10);
     Ring<KU> at;
     int segments = 0;
     uint32_t n_s = 0, n_p = 0;                   // tiles whose scores / values were issued
     bool ok = !tree_flagged(fail);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, kPolls, bar, parity));
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint64_t* other = nullptr, uint32_t other_parity = 0) {
+      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, kPolls, bar, parity, other, other_parity));
       tc_fence_after();
     };
     auto scores = [&](const Tile& t) {
@@ -427,13 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i + 1 < s.n) scores(tile_at(s.r, s.i0 + i + 1));
         if (!ok) break;
         const uint32_t buf = n_p & 1u, ph = (n_p >> 1) & 1u;
-        wait(&wfull[buf], ph);
-        wait(&pready[buf], ph);
+        wait(&wfull[buf], ph, &pready[buf], ph);
         if (!ok) break;
         const uint32_t vb = wr + buf * (uint32_t)X::kWide;
+        const bool eight = tile_at(s.r, s.i0 + i).eight;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tree_mma_ts(lead, tm + kColO, tm + buf * 128 + 8 * ks, mn_desc(vb + ks * 2048), idp,
+          tree_mma_ts(lead, tm + kColO, tm + buf * 128 + 8 * ks, mn_desc(vb + ks * 2048), eight ? idp8 : idp16,
                       (i > 0 || ks > 0) ? 1u : 0u);
         tree_commit(lead, &wempty[buf]);
         ++n_p;
@@ -471,13 +502,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && n >= 2) wait_w(&wempty[buf], ((n >> 1) & 1u) ^ 1u);
         if (!ok) break;
         bool bad = false;
+        const uint32_t exponent = t.eight ? 0x7c007c00u : 0x7f807f80u;
         auto fix = [&](uint4& x, int kd) {
           if (kd == 0) x = make_uint4(0u, 0u, 0u, 0u);
           if (kd == 1) {
-            x.x = finite_only(x.x, bad);
-            x.y = finite_only(x.y, bad);
-            x.z = finite_only(x.z, bad);
-            x.w = finite_only(x.w, bad);
+            x.x = finite_only(x.x, exponent, bad);
+            x.y = finite_only(x.y, exponent, bad);
+            x.z = finite_only(x.z, exponent, bad);
+            x.w = finite_only(x.w, exponent, bad);
           }
         };
         if (t.eight) {
@@ -485,23 +517,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           // first half of theirs while the others write the second: all banks
           const unsigned char* from = vring + at.slot * kUnit;
           const int c = lane & 3, half = (lane >> 2) & 1, kq = lane >> 3;
+          uint32_t most = 0;
+          uint4 xs[4 * P];
 #pragma unroll
           for (int it = 0; it < 4 * P; ++it) {
             const int panel = P == 2 ? it & 1 : 0, key = cw * 32 + (P == 2 ? it >> 1 : it) * 8 + kq + 4 * half;
             const int off = DH == 128 ? key * 128 + (((panel * 4 + c) ^ (key & 7)) << 4)
                                       : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-            const uint4 x = *reinterpret_cast<const uint4*>(from + off);
-            const uint2 w0 = widen(x.x), w1 = widen(x.y), w2 = widen(x.z), w3 = widen(x.w);
-            uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-            if (edge) {
-              const int kd = row_kind(a, s.r, t, t.p0 + key);
-              fix(lo, kd);
-              fix(hi, kd);
-            }
+            xs[it] = *reinterpret_cast<const uint4*>(from + off);
+          }
+          auto store = [&](int it, const uint4& lo, const uint4& hi) {
+            const int panel = P == 2 ? it & 1 : 0, key = cw * 32 + (P == 2 ? it >> 1 : it) * 8 + kq + 4 * half;
             unsigned char* row = to + panel * kUnit + key * 128;
             const int a0 = ((2 * c) ^ (key & 7)) << 4, a1 = ((2 * c + 1) ^ (key & 7)) << 4;
             *reinterpret_cast<uint4*>(row + (half ? a1 : a0)) = half ? hi : lo;
             *reinterpret_cast<uint4*>(row + (half ? a0 : a1)) = half ? lo : hi;
+          };
+#pragma unroll
+          for (int it = 0; it < 4 * P; ++it) {
+            const uint4 x = xs[it];
+            const uint4 lo = make_uint4(widen<0>(x.x), widen<2>(x.x), widen<0>(x.y), widen<2>(x.y));
+            const uint4 hi = make_uint4(widen<0>(x.z), widen<2>(x.z), widen<0>(x.w), widen<2>(x.w));
+            most = larger(larger(larger(larger(most, lo.x), lo.y), lo.z), lo.w);
+            most = larger(larger(larger(larger(most, hi.x), hi.y), hi.z), hi.w);
+            store(it, lo, hi);
+          }
+          if (edge || (most & 0xffffu) >= kWideNan || most >> 16 >= kWideNan) {
+#pragma unroll 1
+            for (int it = 0; it < 4 * P; ++it) {
+              const int panel = P == 2 ? it & 1 : 0, key = cw * 32 + (P == 2 ? it >> 1 : it) * 8 + kq + 4 * half;
+              const int off = DH == 128 ? key * 128 + (((panel * 4 + c) ^ (key & 7)) << 4)
+                                        : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+              const uint4 x = *reinterpret_cast<const uint4*>(from + off);
+              uint4 lo = make_uint4(with_nan(widen<0>(x.x)), with_nan(widen<2>(x.x)), with_nan(widen<0>(x.y)),
+                                    with_nan(widen<2>(x.y)));
+              uint4 hi = make_uint4(with_nan(widen<0>(x.z)), with_nan(widen<2>(x.z)), with_nan(widen<0>(x.w)),
+                                    with_nan(widen<2>(x.w)));
+              const int kd = row_kind(a, s.r, t, t.p0 + key);
+              fix(lo, kd);
+              fix(hi, kd);
+              store(it, lo, hi);
+            }
           }
           mbar_arrive_cta(&vempty[at.slot]);
           at = at.next();
@@ -615,7 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_cta(qready);
       }
       // ---- tiles
-      float m = -INFINITY, l = 0.f;
+      // O holds sums of 2^(score - m) v 2^-1 / vref: P has 2^7 of it and fp16 V 2^-8,
+      // bf16 P 2^-1 by itself
+      float m = -INFINITY, l = 0.f, vref = 0.f;
       const float* kscale = a.k_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
       const float* vscale = a.v_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
       float ks[NCH], vs[NCH];                    // of the tile to come
@@ -681,10 +739,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (NCH > 2 && edge) tmem_wait_st();
           const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float corr = raise ? tree_ex2(m - bm) : 1.f;
+          float over = 0.f;                      // the largest scale over vref
+#pragma unroll
+          for (int q = 0; q < NCH; ++q)
+            if (now.eight && fabsf(v[q]) > fmaxf(vref, over) && fabsf(v[q]) < 0x1p100f) over = fabsf(v[q]);
+          if (__any_sync(0xffffffffu, raise || over > 0.f || vref == 0.f)) {
+            float corr = raise ? tree_ex2(m - bm) : 1.f;
             if (raise) m = bm;
             l *= corr;
+            if (over > 0.f || vref == 0.f) {
+              const float next = over > 0.f ? power_above(over) * 4.f : 1.f;
+              corr *= vref / next;               // (both are powers of two, or 0 at the start)
+              vref = next;
+            }
             if (i > 0) {
               wait_values(n);                    // O as the tile before left it
               if (!ok) break;
@@ -700,30 +767,35 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float nm = m == -INFINITY ? 0.f : -m;
+          const float nm = m == -INFINITY ? 0.f : -m, unit = (now.eight ? 0x1p7f : 0x1p-1f) / vref;
           const uint64_t nm2 = tree_pack2(__float_as_uint(nm), __float_as_uint(nm));
           uint64_t ls2[2] = {0, 0};
+          auto weights = [&](auto eight) {
 #pragma unroll
-          for (int q = 0; q < NCH; ++q) {
-            uint32_t(&x)[32] = sr[q % kKept];
-            if (NCH > 2) {
-              tmem_ld32_nw(scol + key0 + 32 * q, x);
-              tmem_wait_ld();
-              tmem_pin32(x);
-            }
-            const uint64_t c2 = tree_pack2(__float_as_uint(c[q]), __float_as_uint(c[q]));
-            uint32_t pk[16];
+            for (int q = 0; q < NCH; ++q) {
+              uint32_t(&x)[32] = sr[q % kKept];
+              if (NCH > 2) {
+                tmem_ld32_nw(scol + key0 + 32 * q, x);
+                tmem_wait_ld();
+                tmem_pin32(x);
+              }
+              const uint64_t c2 = tree_pack2(__float_as_uint(c[q]), __float_as_uint(c[q]));
+              const float pv = v[q] * unit;
+              uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float p0, p1;
-              tree_unpack2(tree_fma2(tree_pack2(x[2 * e], x[2 * e + 1]), c2, nm2), p0, p1);
-              p0 = tree_ex2(p0);
-              p1 = tree_ex2(p1);
-              ls2[e & 1] = tree_add2(ls2[e & 1], tree_pack2(__float_as_uint(p0), __float_as_uint(p1)));
-              pk[e] = pack_bf16x2(p0 * v[q], p1 * v[q]);
+              for (int e = 0; e < 16; ++e) {
+                float p0, p1;
+                tree_unpack2(tree_fma2(tree_pack2(x[2 * e], x[2 * e + 1]), c2, nm2), p0, p1);
+                p0 = tree_ex2(p0);
+                p1 = tree_ex2(p1);
+                ls2[e & 1] = tree_add2(ls2[e & 1], tree_pack2(__float_as_uint(p0), __float_as_uint(p1)));
+                pk[e] = decltype(eight)::value ? pack_f16x2(p0 * pv, p1 * pv) : pack_bf16x2(p0 * pv, p1 * pv);
+              }
+              tmem_st16(scol + (key0 + 32 * q) / 2, pk);
             }
-            tmem_st16(scol + (key0 + 32 * q) / 2, pk);
-          }
+          };
+          if (now.eight) weights(std::true_type());
+          else weights(std::false_type());
           // the other copies' keys
           if (kCopies > 1) {
             const uint32_t zero[16] = {};
@@ -756,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* pl = a.part_l + (size_t)slot * rows;
       if (kCopies == 1) {
         if (warp_live) {
-          const float inv = s.whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+          const float inv = vref * 2.f * (s.whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f);
           if (live && !s.whole) {
             pm[row] = m;
             pl[row] = l;
@@ -798,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float base = all == -INFINITY ? 0.f : all;
 #pragma unroll
         for (int k = 0; k < kCopies; ++k) sum += xl[k * kRows + row] * tree_ex2(xm[k * kRows + row] - base);
-        const float w0 = tree_ex2(m - base);
+        const float w0 = tree_ex2(m - base) * (vref * 2.f);
         if (copy == 0) {
           row_m[row] = all;
           row_l[row] = sum;
