@@ -1,36 +1,35 @@
 // Attention of a few tokens per sequence over rows held in 8 bits and in bf16,
 // on the 5th-generation tensor cores (sm_103a).
 //
-// The T G query rows of a sequence and K/V head (G query heads share it), 128 at
-// most, are one tile, against tiles of 128 cache rows:
+// The R = T G query rows of a sequence and K/V head (G query heads share it), 128
+// at most, are the narrow side of every product, tiles of 128 cache rows the wide
+// one (tensor memory lanes), so that the matrix pipe's work goes by R:
 //
-//   S = q K^T               8-bit rows: q = (q0 + q1) 2^-a with two e4m3 parts, which
+//   S = K q^T               8-bit rows: q = (q0 + q1) 2^-a with two e4m3 parts, which
 //                           hold every bit of a bf16 number, so that the products
 //                           with the stored bytes are exact; bf16 rows: q itself
-//   P = 2^(S c - m) v_scale one thread per row, 16 bits over S's columns
-//   O += P V                8-bit rows: V widened to fp16, P in fp16; bf16 rows: both bf16
+//   P = 2^(S c - m) v_scale one thread per key, 16 bits, to shared memory
+//   O += V^T P              8-bit rows: V widened to fp16, P in fp16; bf16 rows: both bf16
+//
+// A thread has one key and all rows: what lies below the rows' maxima so far by
+// less than nothing (m + 8: a factor of 256, which the sums and P carry) needs no
+// look at other threads but one vote of the four warps for 16 rows; where a score
+// passes it, m is raised and O rescaled.
 //
 // K and q enter the matrix instructions as they are: a tile of K costs no thread
 // anything.  V cannot: P needs more than e4m3's range and bits (a first row that
 // takes most of the weight leaves the others small), and both operands of a
-// 16-bit product are 16 bits wide, so four warps widen V on its way: to fp16,
-// which one instruction does for two values (bf16 takes four).  fp16 has less
-// range than P: P is held in units of 2^-7 vref 2^m, vref a power of two not
+// 16-bit product are 16 bits wide, so four warps widen V on its way.  fp16 has
+// less range than P: P is held in units of 2^-7 vref 2^m, vref a power of two not
 // below any value scale so far, which keeps 11 bits down to 2^-18 of a row's
 // largest weight and steps of 2^-28 below; two binades of room make it grow seldom.
-//
-// Rows of the tile: with up to 32 query rows the tile holds four copies of them,
-// each of which keeps the keys of one quarter of the tile alone (64 rows: two
-// copies, two halves): the softmax's work is divided among all four warps without
-// an exchange, at the price of joining the copies at the end; the matrix pipe
-// computes 128 rows in any case.
 //
 // Work: the tiles of all sequences and heads in one line, divided evenly among
 // the CTAs (one per SM); a pair of sequence and head that several CTAs share is
 // joined by a second kernel in a fixed order.  The division is computed from the
 // lengths on the device, so that a graph follows them.
 //
-// Warps 0-3: softmax and results; 4-7: V to bf16; 8: copies of K; 9: copies of V;
+// Warps 0-3: softmax and results; 4-7: V to 16 bits; 8: copies of K; 9: copies of V;
 // 10: matrix instructions.  Every wait is bounded: one that gives up sets the
 // CTA's flag, every role runs out, and the CTA's rows become NaN.
 #include <cuda_fp16.h>
@@ -49,19 +48,47 @@ using namespace tc;
 
 constexpr int kKeys = 128;
 constexpr int kThreads = 352;
+constexpr int kWiden = 128;                      // threads that widen V
 constexpr int kPolls = 1 << 22;
 constexpr int kUnit = 16 * 1024;                 // 128 rows of up to 128 bytes, swizzled
 constexpr float kRaise = 8.f;
-constexpr uint32_t kColO = 256, kColQ8 = 384, kColQ16 = 448;  // TMEM: S0, S1 (P over each), O, q
+constexpr float kNone = -1e30f;                  // the maximum of a row that has seen no key
 
-template <int DH>
-struct Shape {
-  static constexpr int kKUnits = DH == 128 ? 4 : 5;
-  static constexpr int kVUnits = DH == 128 ? 3 : 4;
-  static constexpr int kPanels = DH / 64;        // 16-bit panels of 64 columns
-  static constexpr int kWide = kPanels * kUnit;  // a V tile in bf16
-  static constexpr size_t kSmem = (size_t)(kKUnits + kVUnits) * kUnit + 2 * kWide + 4 * 32 * 33 * 4 + 6 * 128 * 4 + 512;
+// Shared memory: q in e4m3 parts and in bf16, P, V in 16 bits, rings of K and V.
+struct Layout {
+  int rows;                                      // padded to 16
+  int q16, p, wide, kring, vring, rest, bytes;   // offsets
+  int p_bufs, k_units, v_units;
 };
+constexpr int kSmemMost = 227 * 1024 - 1024;     // (from a 1024-byte boundary)
+constexpr int kSmall = 5 * 128 * 4 + 512;        // per-row values, barriers
+__host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
+  Layout l;
+  l.rows = (rows + 15) / 16 * 16;
+  const int q8 = 2 * l.rows * dh, q16 = 2 * l.rows * dh, p = l.rows * 256, wide = dh / 64 * kUnit;
+  const int plan = (14 * B + 4 + 127) / 128 * 128;
+  const int fixed = (q8 + q16 + 2 * wide + kSmall + plan + 1023) / 1024 * 1024;
+  l.k_units = dh / 64;                           // (a tile of bf16 rows)
+  l.v_units = 1;
+  l.p_bufs = 1;
+  int left = kSmemMost - fixed - p - (l.k_units + l.v_units) * kUnit;
+  if (left >= p + kUnit) {
+    l.p_bufs = 2;
+    left -= p;
+  }
+  for (; left >= kUnit && l.v_units < 6; left -= kUnit) {
+    if (l.k_units <= l.v_units) ++l.k_units;
+    else ++l.v_units;
+  }
+  l.q16 = q8;
+  l.p = l.q16 + q16;
+  l.wide = (l.p + l.p_bufs * p + 1023) / 1024 * 1024;
+  l.kring = l.wide + 2 * wide;
+  l.vring = l.kring + l.k_units * kUnit;
+  l.rest = l.vring + l.v_units * kUnit;
+  l.bytes = l.rest + kSmall + plan + 1024;
+  return l;
+}
 
 SSD_DI void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -72,6 +99,15 @@ SSD_DI void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[15])
       : "memory");
 }
+// Four columns of the thread's lane, waited for.
+SSD_DI void tmem_ld4(uint32_t taddr, float (&r)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+      : "r"(taddr)
+      : "memory");
+}
 SSD_DI void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -79,8 +115,9 @@ SSD_DI void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
       : "memory");
 }
-// V tile in panels of 64 columns as the MN-major B operand.
-SSD_DI uint64_t mn_desc(uint32_t saddr) {
+// V tile in panels of 64 columns as the MN-major A operand (with 64 columns the
+// second panel is whatever follows: lanes that nobody reads).
+SSD_DI uint64_t v_desc(uint32_t saddr) {
   uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
   d |= (uint64_t)(kUnit >> 4) << 16;             // leading offset: next 64 columns
   d |= (uint64_t)(1024 >> 4) << 32;              // stride offset: next 8 keys
@@ -88,100 +125,180 @@ SSD_DI uint64_t mn_desc(uint32_t saddr) {
   d |= (uint64_t)2 << 61;                        // 128-byte swizzle
   return d;
 }
-// e4m3 A and B, fp32 D, both K-major; A in tensor memory.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// P in panels of 16 rows as the MN-major B operand: 32 bytes per key, swizzled.
+constexpr int kPanel = kKeys * 32;
+SSD_DI uint64_t p_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kPanel >> 4) << 16;            // leading offset: next 16 rows
+  d |= (uint64_t)(256 >> 4) << 32;               // stride offset: next 8 keys
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)6 << 61;                        // 32-byte swizzle
+  return d;
 }
-SSD_DI void mma_ts_e4m3(uint32_t lead, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// fp32 D; e4m3 (or, with bits 7 and 10, as bf16 of the 16-bit kind) A and B, K-major.
+SSD_DI uint32_t idesc_e4m3(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24); }
+SSD_DI void mma_ss_e4m3(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
+// tree_wait, in a loop that stays one.
+SSD_DI bool wait_for(const int* fail, uint64_t* a, uint32_t pa) {
+  if (tree_try(a, pa)) return true;
+#pragma unroll 1
+  for (int i = 0; i < kPolls; ++i) {
+    if (tree_try(a, pa)) return true;
+    if ((i & 63) == 63 && tree_flagged(fail)) return false;
+  }
+  return false;
+}
 SSD_DI void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// 16 values of each lane joined over the warp by halving: lane l ends with value
+// l / 2 in v[0].
+template <class F>
+SSD_DI void over_lanes(float (&v)[16], F join) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = 16; w > 1; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int e = 0; e < w / 2; ++e) {
+      const float got = __shfl_xor_sync(~0u, up ? v[e] : v[e + w / 2], w);
+      v[e] = join(up ? v[e + w / 2] : v[e], got);
+    }
+  }
+  v[0] = join(v[0], __shfl_xor_sync(~0u, v[0], 1));
+}
+// Whether any of the softmax threads says so.
+SSD_DI bool any_softmax(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
 
 // ---- division of the work
 
-// A tile: rows p0 .. p0 + 127, of which [rs, re) count.
-struct Tile {
-  int p0, rs, re;
-  bool eight;
-};
+// (What runs once per sequence or run of tiles is kept out of line: the roles'
+// loops have to lie in the instruction cache beside one another.  With all of it
+// inlined the kernel was 160 KB, and one token over 131000 rows took 108 us, not
+// 75.)
 SSD_DI int cdiv_keys(int x) { return (x + kKeys - 1) / kKeys; }
+static __device__ __noinline__ SeqRange seq_range_of(const CacheAttnArgs& a, int length, int count, int held) {
+  return seq_range(a, length, count, held);
+}
+// Tiles in 8 bits: the first rows, then the run; and in bf16 the same.
+SSD_DI int tiles_eight(const SeqRange& r) {
+  return cdiv_keys(min(r.sinks, r.held)) + (r.low < r.held ? cdiv_keys(r.held) - r.low / kKeys : 0);
+}
 SSD_DI int tiles_of(const SeqRange& r) {
   const int first = max(r.low, r.held);
-  return cdiv_keys(min(r.sinks, r.held)) + (r.low < r.held ? cdiv_keys(r.held) - r.low / kKeys : 0) +
-         (r.sinks > r.held ? cdiv_keys(r.sinks) - r.held / kKeys : 0) +
+  return tiles_eight(r) + (r.sinks > r.held ? cdiv_keys(r.sinks) - r.held / kKeys : 0) +
          (r.end > first ? cdiv_keys(r.end) - first / kKeys : 0);
 }
-// The i-th tile: first rows and the run in 8 bits, then the same in bf16.
-SSD_DI Tile tile_at(const SeqRange& r, int i) {
+// A place in a pair's tiles: rows p0 .. p0 + 127, of which [rs, re) count; all
+// tokens see all of them where f0 <= p0 and p0 + 128 <= f1.
+struct Walk {
+  int p0, rs, re, f0, f1;
+  int i, left;                                   // the tile's number, tiles to the end of its run
+  bool eight;
+  SSD_DI bool edge() const { return p0 < f0 || p0 + kKeys > f1; }
+};
+static __device__ __noinline__ Walk walk_from(SeqRange r, int window, int tile) {
+  Walk w;
   const int first = max(r.low, r.held);
-  int n = cdiv_keys(min(r.sinks, r.held));
-  if (i < n) return Tile{i * kKeys, 0, min(r.sinks, r.held), true};
-  i -= n;
-  n = r.low < r.held ? cdiv_keys(r.held) - r.low / kKeys : 0;
-  if (i < n) return Tile{(r.low / kKeys + i) * kKeys, r.low, r.held, true};
-  i -= n;
-  n = r.sinks > r.held ? cdiv_keys(r.sinks) - r.held / kKeys : 0;
-  if (i < n) return Tile{(r.held / kKeys + i) * kKeys, r.held, r.sinks, false};
-  i -= n;
-  return Tile{(first / kKeys + i) * kKeys, first, r.end, false};
+  int i = tile, start = 0, n;
+  bool whole = true;                             // (first rows: all tokens see them)
+  w.i = tile;
+  w.eight = true;
+  w.rs = 0;
+  w.re = min(r.sinks, r.held);
+  n = cdiv_keys(w.re);
+  if (i >= n) {
+    i -= n;
+    whole = false;
+    w.rs = r.low;
+    w.re = r.held;
+    start = r.low / kKeys;
+    n = r.low < r.held ? cdiv_keys(r.held) - start : 0;
+    if (i >= n) {
+      i -= n;
+      whole = true;
+      w.eight = false;
+      w.rs = r.held;
+      w.re = r.sinks;
+      start = r.held / kKeys;
+      n = r.sinks > r.held ? cdiv_keys(r.sinks) - start : 0;
+      if (i >= n) {
+        i -= n;
+        whole = false;
+        w.rs = first;
+        w.re = r.end;
+        start = first / kKeys;
+        n = cdiv_keys(r.end) - start;
+      }
+    }
+  }
+  w.p0 = (start + i) * kKeys;
+  w.left = n - i;
+  w.f0 = window && !whole ? max(w.rs, r.end - window) : w.rs;
+  w.f1 = min(w.re, r.length + 1);
+  return w;
 }
-// Whether some key of the tile is not seen by every token.
-SSD_DI bool has_edge(const CacheAttnArgs& a, const SeqRange& r, const Tile& t) {
-  return t.p0 < t.rs || t.p0 + kKeys > t.re || t.p0 + kKeys - 1 > r.length ||
-         (a.window && t.p0 <= r.end - 1 - a.window && t.p0 + kKeys > a.sinks);
-}
-// Bits lo .. hi - 1 of a word, clipped.
-SSD_DI uint32_t bits_between(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 32);
-  if (hi <= lo) return 0u;
-  return (0xffffffffu >> (32 - (hi - lo))) << lo;
-}
-// Which of the 32 keys from j on a token in row pos sees.
-SSD_DI uint32_t seen_bits(const CacheAttnArgs& a, const Tile& t, int pos, int j) {
-  uint32_t m = bits_between(t.rs - j, min(t.re, pos + 1) - j);
-  if (a.window) m &= bits_between(0, a.sinks - j) | bits_between(pos - a.window + 1 - j, 32);
-  return m;
+SSD_DI void step(Walk& w, const SeqRange& r, int window) {
+  ++w.i;
+  w.p0 += kKeys;
+  if (--w.left == 0) w = walk_from(r, window, w.i);
 }
 
 // What the CTA's threads know of the sequences, in shared memory.
 struct Plan {
-  long long* first;                              // [B + 1] tiles (of one head) before sequence b
-  int *length, *count, *held;                    // [B]
+  int* first;                                    // [B + 1] tiles (of one head) before sequence b: all lie
+                                                 // in the caches, so that 31 bits count them
+  int *length, *held;                            // [B]
+  short* count;
   long long begin, end;                          // the CTA's tiles
   long long total;
   int ctas;                                      // that have any
-  SSD_DI long long start(int cta) const { return cta < ctas ? total * cta / ctas : total; }
-  // The CTA that has a tile.
-  SSD_DI int owner(long long tile) const {
-    int cta = (int)(tile * ctas / total);
-    while (start(cta + 1) <= tile) ++cta;
-    return cta;
-  }
 };
+static __device__ __noinline__ long long cta_start(long long total, int ctas, int cta) {
+  return cta < ctas ? total * cta / ctas : total;
+}
+// The CTA that has the last tile of a pair.
+static __device__ __noinline__ int last_cta(const CacheAttnArgs& a, const Plan& p, int b, int h) {
+  const long long n = p.first[b + 1] - p.first[b], tile = (long long)p.first[b] * a.Hkv + (h + 1) * n - 1;
+  int cta = (int)(tile * p.ctas / p.total);
+  while (cta_start(p.total, p.ctas, cta + 1) <= tile) ++cta;
+  return cta;
+}
 // A run of a pair's tiles within the CTA's.
 struct Segment {
   int b, h, i0, n;                               // tiles i0 .. i0 + n - 1 of the pair
+  int eight;                                     // of which so many are in 8 bits (the first ones)
   bool whole, head;                              // all of them; the pair began in an earlier CTA
   SeqRange r;
 };
-SSD_DI Segment segment_at(const CacheAttnArgs& a, const Plan& p, long long at) {
+static __device__ __noinline__ Segment segment_at(const CacheAttnArgs& a, const Plan& p, long long at) {
   Segment s;
   int lo = 0, hi = a.B - 1;                      // the last b with first[b] Hkv <= at
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (p.first[mid] * a.Hkv <= at) lo = mid;
+    if ((long long)p.first[mid] * a.Hkv <= at) lo = mid;
     else hi = mid - 1;
   }
   s.b = lo;
-  const int n = (int)(p.first[lo + 1] - p.first[lo]);
-  const long long local = at - p.first[lo] * a.Hkv;
+  const int n = p.first[lo + 1] - p.first[lo];
+  const long long local = at - (long long)p.first[lo] * a.Hkv;
   s.h = (int)(local / n);
   s.i0 = (int)(local - (long long)s.h * n);
   const long long left = p.end - at;
@@ -189,33 +306,19 @@ SSD_DI Segment segment_at(const CacheAttnArgs& a, const Plan& p, long long at) {
   s.whole = s.n == n;
   s.head = s.i0 > 0;
   s.r = seq_range(a, p.length[lo], p.count[lo], p.held[lo]);
+  s.eight = max(0, min(s.n, tiles_eight(s.r) - s.i0));
   return s;
 }
 
 // ---- values
 
-// Two e4m3 (bytes lo and lo + 1 of x) to two fp16 of 2^-8 their value: the same
-// sign, exponent and fraction at fp16's places (exact, fp16's range holds what
-// e4m3's does; the code of NaN becomes 480 / 2^8).  Four integer instructions:
-// the conversion instruction runs on the unit of the exponentials, far more
-// slowly (a tile of 128 x 128 took 3000 cycles, against CYCLES so).
-template <int LO>
+// The two e4m3 in the low half of x as two fp16 (exact).
 SSD_DI uint32_t widen(uint32_t x) {
-  const uint32_t h = __byte_perm(x, 0u, LO == 0 ? 0x1404 : 0x3424);
-  return (h & 0x80008000u) | ((h >> 1) & 0x3fff3fffu);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
+  return r;
 }
-constexpr uint32_t kWideNan = 0x3f80;            // what the code of NaN becomes, over all others
-SSD_DI uint32_t larger(uint32_t most, uint32_t x) {
-  const __half2 a = *reinterpret_cast<const __half2*>(&most), b = *reinterpret_cast<const __half2*>(&x);
-  const __half2 m = __hmax2(a, __habs2(b));
-  return *reinterpret_cast<const uint32_t*>(&m);
-}
-// The NaN of two widened values as such.
-SSD_DI uint32_t with_nan(uint32_t x) {
-  if ((x & 0x7fffu) == kWideNan) x |= 0x7fffu;
-  if ((x & 0x7fff0000u) == kWideNan << 16) x |= 0x7fff0000u;
-  return x;
-}
+SSD_DI uint4 widen(uint32_t x, uint32_t y) { return make_uint4(widen(x), widen(x >> 16), widen(y), widen(y >> 16)); }
 // Two 16-bit numbers with what is not finite (all of the exponent's bits `e`
 // set) as 0; `bad` if there was any.
 SSD_DI uint32_t finite_only(uint32_t x, uint32_t e, bool& bad) {
@@ -239,62 +342,85 @@ SSD_DI float power_above(float x) {
 }
 
 // How a row of V goes into the products: 0 as zeros (it is outside the tile's
-// run), 1 without what is not finite (0 x infinity is NaN, and some row of the
-// products has a 0 there: a token that does not see it, or another copy), 2 as
-// it is.
-SSD_DI int row_kind(const CacheAttnArgs& a, const SeqRange& r, const Tile& t, int j) {
+// run), 1 without what is not finite (0 x infinity is NaN, and some token of the
+// sequence does not see it), 2 as it is.
+SSD_DI int row_kind(const CacheAttnArgs& a, const SeqRange& r, const Walk& t, int j) {
   if (j < t.rs || j >= t.re) return 0;
-  if (!t.eight || j > r.length) return 1;
+  if (j > r.length) return 1;
   return a.window && j >= a.sinks && j <= r.end - 1 - a.window ? 1 : 2;
 }
-// Adds to a row's n values from column c0 on what the products left out of the
-// segment's V rows that the row's token, in row pos, sees.
-static __device__ __noinline__ void add_not_finite(const CacheAttnArgs& a, const Segment& s, int pos, int c0, int n,
-                                                   float* v) {
-  for (int i = s.i0; i < s.i0 + s.n; ++i) {
-    const Tile t = tile_at(s.r, i);
+// What the products left out in column c of the segment's V rows that the token
+// in row pos sees.
+static __device__ __noinline__ float not_finite(const CacheAttnArgs& a, const Segment& s, int pos, int c) {
+  float sum = 0.f;
+  Walk t = walk_from(s.r, a.window, s.i0);
+  for (int i = 0; i < s.n; ++i) {
     for (int j = max(t.p0, t.rs); j < min(t.p0 + kKeys, t.re); ++j) {
       if (row_kind(a, s.r, t, j) != 1 || j > pos || (a.window && j >= a.sinks && j <= pos - a.window)) continue;
-      for (int e = 0; e < n; ++e) {
-        float x;
-        if (t.eight) {
-          const uint8_t code = a.v8[(size_t)s.b * a.seq8_stride + ((size_t)s.h * a.max_seq + j) * a.dh + c0 + e];
-          x = (code & 0x7f) == 0x7f ? NAN : 0.f;
-        } else {
-          x = __bfloat162float(a.v[(size_t)s.b * a.seq_stride + ((size_t)s.h * a.rows + j % a.rows) * a.dh + c0 + e]);
-        }
-        if (!isfinite(x)) v[e] += x;
+      float x;
+      if (t.eight) {
+        const uint8_t code = a.v8[(size_t)s.b * a.seq8_stride + ((size_t)s.h * a.max_seq + j) * a.dh + c];
+        x = (code & 0x7f) == 0x7f ? NAN : 0.f;
+      } else {
+        x = __bfloat162float(a.v[(size_t)s.b * a.seq_stride + ((size_t)s.h * a.rows + j % a.rows) * a.dh + c]);
+      }
+      if (!isfinite(x)) sum += x;
+    }
+    if (i + 1 < s.n) step(t, s.r, a.window);
+  }
+  return sum;
+}
+// The CTA's rows as NaN: a wait gave up, and none is sure.
+static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan& plan) {
+  const int rows = a.T * a.G;
+  for (long long at = plan.begin; at < plan.end;) {
+    const Segment s = segment_at(a, plan, at);
+    const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
+    if (!s.whole && !s.head && threadIdx.x == 0)
+      a.shared[blockIdx.x] = make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0);
+    for (int i = threadIdx.x; i < rows * a.dh; i += kThreads) {
+      const int r = i / a.dh, tk = r / a.G;
+      if (s.whole) {
+        if (tk < s.r.count)
+          a.out[(((size_t)s.b * a.T + tk) * a.H + s.h * a.G + r % a.G) * a.dh + i % a.dh] = __float2bfloat16(NAN);
+      } else if (i % a.dh == 0) {
+        a.part_m[slot * rows + r] = 0.f;
+        a.part_l[slot * rows + r] = tk < s.r.count ? NAN : 0.f;
       }
     }
+    at += s.n;
   }
 }
 
-template <int DH, int NCH>                       // NCH: chunks of 32 keys of a tile that a thread's row has
+// SMALL: up to 16 rows, whose parts of q make one product (twice as wide) and
+// whose sums a thread keeps in registers (else in tensor memory).
+template <int DH, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_tc_kernel(const __grid_constant__ CUtensorMap mK8, const __grid_constant__ CUtensorMap mV8,
                          const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                         const __grid_constant__ CacheAttnArgs a) {
-  using X = Shape<DH>;
-  constexpr int kCopies = 4 / NCH;
-  constexpr int KU = X::kKUnits, VU = X::kVUnits, P = X::kPanels;
+                         const __grid_constant__ CacheAttnArgs a, const Layout lay) {
+  constexpr int P = DH / 64;                     // 16-bit panels of 64 columns
+  constexpr int kWide = P * kUnit;               // a V tile in 16 bits
+  const int NP = SMALL ? 16 : lay.rows;
+  const uint32_t scols = SMALL ? 32 : NP;        // TMEM: S0, S1, O, sums
+  const uint32_t col_o = 2 * scols, col_l = col_o + NP;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* kring = sm;
-  unsigned char* vring = kring + KU * kUnit;
-  unsigned char* wide = vring + VU * kUnit;      // [2]
-  float* merge = reinterpret_cast<float*>(wide + 2 * X::kWide);  // [4][32][33]
-  float* xm = merge + 4 * 32 * 33;               // [128] per thread: maximum, sum
-  float* xl = xm + 128;
-  float* row_m = xl + 128;                       // [128] per row, of all copies
-  float* row_l = row_m + 128;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(row_l + 128);
-  uint64_t* kfull = bars;
-  uint64_t* kempty = kfull + KU;
-  uint64_t* vfull = kempty + KU;
-  uint64_t* vempty = vfull + VU;
-  uint64_t* wfull = vempty + VU;                 // [2] V in bf16
-  uint64_t* wempty = wfull + 2;                  // [2] the tile's products P V done
+  unsigned char *q8 = sm, *q16 = sm + lay.q16, *psm = sm + lay.p, *wide = sm + lay.wide;
+  unsigned char *kring = sm + lay.kring, *vring = sm + lay.vring;
+  float* row_c = reinterpret_cast<float*>(sm + lay.rest);  // [128] what a row's 8-bit scores are multiplied by
+  float* row_nm = row_c + 128;                   // [128] minus its maximum
+  float* row_f = row_nm + 128;                   // [128] what O is multiplied by in the end
+  float* part = row_f + 128;                     // [4][32] of the warps
+  int* row_at = reinterpret_cast<int*>(part + 128);  // [128] a row's place among the sequence's heads
+  uint64_t* bars = reinterpret_cast<uint64_t*>(row_c + 5 * 128);
+  uint64_t* kfull = bars;                        // [8] each
+  uint64_t* kempty = kfull + 8;
+  uint64_t* vfull = kempty + 8;
+  uint64_t* vempty = vfull + 8;
+  uint64_t* wfull = vempty + 8;                  // [2] V in 16 bits
+  uint64_t* wempty = wfull + 2;                  // [2] the tile's products V^T P done
   uint64_t* sfull = wempty + 2;                  // [2]
   uint64_t* pready = sfull + 2;                  // [2]
   uint64_t* qready = pready + 2;
@@ -303,52 +429,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* fail = reinterpret_cast<int*>(tslot + 1);
   int* odd = fail + 1;                           // a V element that is not finite was left out
   Plan plan;
-  plan.first = reinterpret_cast<long long*>(reinterpret_cast<unsigned char*>(bars) + 512);
-  plan.length = reinterpret_cast<int*>(plan.first + a.B + 1);
-  plan.count = plan.length + a.B;
-  plan.held = plan.count + a.B;
+  plan.first = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(row_c) + kSmall);
+  plan.length = plan.first + a.B + 1;
+  plan.held = plan.length + a.B;
+  plan.count = reinterpret_cast<short*>(plan.held + a.B);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G;
 
   // ---- set-up
   if (tid == 320) {
-    for (int i = 0; i < KU; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&kfull[i], 1);
       mbar_init(&kempty[i], 1);
-    }
-    for (int i = 0; i < VU; ++i) {
       mbar_init(&vfull[i], 1);
-      mbar_init(&vempty[i], 128);
+      mbar_init(&vempty[i], kWiden / 32);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&wfull[i], 128);
+      mbar_init(&wfull[i], kWiden / 32);
       mbar_init(&wempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], 128);
+      mbar_init(&pready[i], 4);
     }
-    mbar_init(qready, 128);
+    mbar_init(qready, 4);
     mbar_init(mdone, 1);
     *fail = (int)blockIdx.x == a.give_up;
     *odd = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(tslot, 512);
+#pragma unroll 1
   for (int b = tid; b < a.B; b += kThreads) {
-    const int n = a.lengths[b], c = a.counts ? a.counts[b] : a.T, h = a.held ? a.held[b] : 0;
+    const int n = a.lengths[b], h = a.held ? a.held[b] : 0;
+    const int c = a.counts ? min(max(a.counts[b], -1), 129) : a.T;  // (129: too many, like all above)
     plan.length[b] = n;
-    plan.count[b] = c;
     plan.held[b] = h;
-    plan.first[b + 1] = tiles_of(seq_range(a, n, c, h));
+    plan.count[b] = (short)c;
+    plan.first[b + 1] = tiles_of(seq_range_of(a, n, c, h));
   }
+  if (tid < rows) row_at[tid] = tid / a.G * a.H + tid % a.G;
+  // q's rows that there are none of
+#pragma unroll 1
+  for (int i = tid; i < lay.p / 16; i += kThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   if (warp == 4) {
-    long long sum = 0;
+    int sum = 0;
     if (lane == 0) plan.first[0] = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      long long x = b0 + lane < a.B ? plan.first[b0 + lane + 1] : 0;
+      int x = b0 + lane < a.B ? plan.first[b0 + lane + 1] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(~0u, x, d);
+        const int y = __shfl_up_sync(~0u, x, d);
         if (lane >= d) x += y;
       }
       if (b0 + lane < a.B) plan.first[b0 + lane + 1] = sum + x;
@@ -359,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
-  plan.total = plan.first[a.B] * a.Hkv;
+  plan.total = (long long)plan.first[a.B] * a.Hkv;
   plan.ctas = (int)min((long long)gridDim.x, plan.total);  // each with a tile at least
-  plan.begin = plan.start(blockIdx.x);
-  plan.end = plan.start(blockIdx.x + 1);
+  plan.begin = cta_start(plan.total, plan.ctas, blockIdx.x);
+  plan.end = cta_start(plan.total, plan.ctas, blockIdx.x + 1);
   auto give_up = [&](bool ok) {
     if (!ok) atomicExch(fail, 1);
   };
@@ -372,19 +505,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 128 bytes: one for a tile of 8-bit rows, a panel of 64 columns each for bf16
     if (lane == 0) {
       const bool is_v = warp == 9;
-      const int units = is_v ? VU : KU;
+      const int units = is_v ? lay.v_units : lay.k_units;
       unsigned char* ring = is_v ? vring : kring;
       uint64_t *full = is_v ? vfull : kfull, *empty = is_v ? vempty : kempty;
       const CUtensorMap *m8 = is_v ? &mV8 : &mK8, *m16 = is_v ? &mV : &mK;
       int issued = 0, slot = 0;
       uint32_t phase = 0;
       bool ok = !tree_flagged(fail);
+#pragma unroll 1
       for (long long at = plan.begin; ok && at < plan.end;) {
         const Segment s = segment_at(a, plan, at);
+        Walk t = walk_from(s.r, a.window, s.i0);
+#pragma unroll 1
         for (int i = 0; ok && i < s.n; ++i) {
-          const Tile t = tile_at(s.r, s.i0 + i);
+#pragma unroll 1
           for (int u = 0; ok && u < (t.eight ? 1 : P); ++u) {
-            if (issued >= units) ok = tree_wait(fail, kPolls, &empty[slot], phase ^ 1u);
+            if (issued >= units) ok = wait_for(fail, &empty[slot], phase ^ 1u);
             if (!ok) break;
             mbar_arrive_expect_tx(&full[slot], t.eight ? 128u * DH : (uint32_t)kUnit);
             if (t.eight) tma_load_4d(ring + slot * kUnit, m8, 0, t.p0, s.h, s.b, &full[slot]);
@@ -395,11 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               phase ^= 1u;
             }
           }
+          if (i + 1 < s.n) step(t, s.r, a.window);
         }
         at += s.n;
       }
       give_up(ok);
       // what is still in flight lands before the memory is released
+#pragma unroll 1
       for (int i = max(0, issued - units); i < issued; ++i)
         mbar_wait_n(&full[i % units], (uint32_t)((i / units) & 1), kPolls);
     }
@@ -407,65 +545,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- products: the warp runs together, one lane issues
     const uint32_t lead = tree_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t kr = smem_addr(kring), wr = smem_addr(wide);
-    constexpr uint32_t id8 = idesc_e4m3(128, kKeys), id16 = idesc_bf16(128, kKeys);
-    // (B is MN-major; fp16 in place of bf16 without bits 7 and 10)
-    constexpr uint32_t idp16 = idesc_bf16(128, DH) | (1u << 16), idp8 = idp16 & ~(1u << 7 | 1u << 10);
-    Ring<KU> at;
+    const uint32_t kr = smem_addr(kring), wr = smem_addr(wide), pr = smem_addr(psm);
+    const uint32_t qa8 = smem_addr(q8), qa16 = smem_addr(q16);
+    const uint32_t id8 = idesc_e4m3((int)scols), id16 = idesc_e4m3(NP) | 1u << 7 | 1u << 10;
+    // (both operands MN-major; fp16, bf16)
+    const uint32_t idp8 = idesc_e4m3(NP) | 3u << 15, idp16 = idp8 | 1u << 7 | 1u << 10;
+    int kslot = 0;
+    uint32_t kphase = 0;
+    auto next_k = [&]() {
+      if (++kslot == lay.k_units) {
+        kslot = 0;
+        kphase ^= 1u;
+      }
+    };
     int segments = 0;
     uint32_t n_s = 0, n_p = 0;                   // tiles whose scores / values were issued
     bool ok = !tree_flagged(fail);
     auto wait = [&](uint64_t* bar, uint32_t parity, uint64_t* other = nullptr, uint32_t other_parity = 0) {
-      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, kPolls, bar, parity, other, other_parity));
+      ok = __all_sync(0xffffffffu, ok && wait_for(fail, bar, parity) && (!other || wait_for(fail, other, other_parity)));
       tc_fence_after();
     };
-    auto scores = [&](const Tile& t) {
-      const uint32_t d = tm + (n_s & 1u) * 128;
-      const Ring<KU> k0 = at, k1 = at.next();
-      wait(&kfull[k0.slot], k0.phase);
-      if (!t.eight && P == 2) wait(&kfull[k1.slot], k1.phase);
+    auto scores = [&](bool eight) {
+      const uint32_t d = tm + (n_s & 1u) * scols;
+      const int k0 = kslot;
+      wait(&kfull[k0], kphase);
       if (!ok) return;
-      const uint32_t kb = kr + (uint32_t)k0.slot * kUnit;
-      if (t.eight) {
-        const uint64_t desc = DH == 128 ? sw128_desc(kb) : sw64_desc(kb);
-#pragma unroll
-        for (int p = 1; p >= 0; --p)             // the low part first
+      const uint32_t kb = kr + (uint32_t)k0 * kUnit;
+      next_k();
+      if (eight) {
+        const uint64_t kd = DH == 128 ? sw128_desc(kb) : sw64_desc(kb);
+        uint64_t qd = DH == 128 ? sw128_desc(qa8) : sw64_desc(qa8);
+        // (the low part first)
+        if (!SMALL) qd += (uint64_t)((uint32_t)(NP * DH) >> 4);
+#pragma unroll 1
+        for (int part = SMALL ? 1 : 0; part < 2; ++part) {
 #pragma unroll
           for (int ks = 0; ks < DH / 32; ++ks)
-            mma_ts_e4m3(lead, d, tm + kColQ8 + (uint32_t)(p * (DH / 4) + ks * 8), desc + 2 * ks, id8,
-                        (p == 0 || ks > 0) ? 1u : 0u);
+            mma_ss_e4m3(lead, d, kd + 2 * ks, qd + 2 * ks, id8, (!SMALL && part) || ks > 0 ? 1u : 0u);
+          qd -= (uint64_t)((uint32_t)(NP * DH) >> 4);
+        }
       } else {
-        const uint32_t kb1 = kr + (uint32_t)k1.slot * kUnit;
+#pragma unroll 1
+        for (int u = 0; u < P; ++u) {
+          if (u) wait(&kfull[kslot], kphase);
+          if (!ok) return;
+          const uint64_t kd = sw128_desc(kr + (uint32_t)(u ? kslot : k0) * kUnit);
+          const uint64_t qd = sw128_desc(qa16 + (uint32_t)(u * NP) * 128);
 #pragma unroll
-        for (int ks = 0; ks < DH / 16; ++ks)
-          tree_mma_ts(lead, d, tm + kColQ16 + (uint32_t)ks * 8, sw128_desc(ks < 4 ? kb : kb1) + 2 * (ks & 3), id16,
-                      ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks) tree_mma_ss(lead, d, kd + 2 * ks, qd + 2 * ks, id16, u || ks > 0 ? 1u : 0u);
+        }
       }
       tree_commit(lead, &sfull[n_s & 1u]);
-      tree_commit(lead, &kempty[k0.slot]);
-      at = at.next();
-      if (!t.eight && P == 2) {
-        tree_commit(lead, &kempty[k1.slot]);
-        at = at.next();
+      tree_commit(lead, &kempty[k0]);
+      if (!eight && P == 2) {
+        tree_commit(lead, &kempty[kslot]);
+        next_k();
       }
       ++n_s;
     };
+#pragma unroll 1
     for (long long pos = plan.begin; ok && pos < plan.end; ++segments) {
       const Segment s = segment_at(a, plan, pos);
       wait(qready, (uint32_t)(segments & 1));
-      if (ok) scores(tile_at(s.r, s.i0));
-      for (int i = 0; ok && i < s.n; ++i) {
-        if (i + 1 < s.n) scores(tile_at(s.r, s.i0 + i + 1));
+      // (one place in the code for the scores: the first tile's before the others')
+#pragma unroll 1
+      for (int i = -1; ok && i < s.n; ++i) {
+        if (i + 1 < s.n) scores(i + 1 < s.eight);
         if (!ok) break;
+        if (i < 0) continue;
         const uint32_t buf = n_p & 1u, ph = (n_p >> 1) & 1u;
         wait(&wfull[buf], ph, &pready[buf], ph);
         if (!ok) break;
-        const uint32_t vb = wr + buf * (uint32_t)X::kWide;
-        const bool eight = tile_at(s.r, s.i0 + i).eight;
+        const uint64_t vd = v_desc(wr + buf * (uint32_t)kWide);
+        const uint64_t pd = p_desc(pr + (lay.p_bufs == 2 ? buf * (uint32_t)NP * 256u : 0u));
+        const uint32_t idp = i < s.eight ? idp8 : idp16;
+#pragma unroll 1
+        for (int k4 = 0; k4 < 8; k4 += 4)
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tree_mma_ts(lead, tm + kColO, tm + buf * 128 + 8 * ks, mn_desc(vb + ks * 2048), eight ? idp8 : idp16,
-                      (i > 0 || ks > 0) ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks)
+            tree_mma_ss(lead, tm + col_o, vd + 128 * (k4 + ks), pd + 32 * (k4 + ks), idp,
+                        (i > 0 || k4 > 0 || ks > 0) ? 1u : 0u);
         tree_commit(lead, &wempty[buf]);
         ++n_p;
       }
@@ -475,448 +634,424 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_commit(lead, mdone);
     mbar_wait_n(mdone, 0u, kPolls);
   } else if (warp >= 4) {
-    // ---- V to bf16 in the products' layout
+    // ---- V to 16 bits in the products' layout
     const int cw = warp - 4, ct = tid - 128;
+#pragma unroll 1
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       if (plan.first[b + 1] != plan.first[b]) continue;
       // a sequence without tokens, or without sense
-      const float x = seq_range(a, plan.length[b], plan.count[b], plan.held[b]).count < 0 ? NAN : 0.f;
+      const float x = seq_range_of(a, plan.length[b], plan.count[b], plan.held[b]).count < 0 ? NAN : 0.f;
       const uint32_t w = pack_bf16x2(x, x);
       uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * a.T * a.H * DH);
-      for (size_t i = ct; i < (size_t)a.T * a.H * DH / 8; i += 128) o[i] = make_uint4(w, w, w, w);
+#pragma unroll 1
+      for (size_t i = ct; i < (size_t)a.T * a.H * DH / 8; i += kWiden) o[i] = make_uint4(w, w, w, w);
     }
-    Ring<VU> at;
-    uint32_t n = 0;
+    int slot = 0;
+    uint32_t phase = 0, n = 0;
     bool ok = !tree_flagged(fail);
     auto wait_w = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, kPolls, bar, parity));
+      ok = __all_sync(0xffffffffu, ok && wait_for(fail, bar, parity));
     };
+    auto freed = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&vempty[slot]);
+      if (++slot == lay.v_units) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    };
+#pragma unroll 1
     for (long long pos = plan.begin; ok && pos < plan.end;) {
       const Segment s = segment_at(a, plan, pos);
+      Walk t = walk_from(s.r, a.window, s.i0);
+#pragma unroll 1
       for (int i = 0; ok && i < s.n; ++i, ++n) {
-        const Tile t = tile_at(s.r, s.i0 + i);
-        const bool edge = has_edge(a, s.r, t);
+        if (i) step(t, s.r, a.window);
+        const bool edge = t.edge();
         const uint32_t buf = n & 1u;
-        unsigned char* to = wide + buf * X::kWide;
-        wait_w(&vfull[at.slot], at.phase);
+        unsigned char* to = wide + buf * kWide;
+        wait_w(&vfull[slot], phase);
         if (ok && n >= 2) wait_w(&wempty[buf], ((n >> 1) & 1u) ^ 1u);
         if (!ok) break;
-        bool bad = false;
-        const uint32_t exponent = t.eight ? 0x7c007c00u : 0x7f807f80u;
-        auto fix = [&](uint4& x, int kd) {
-          if (kd == 0) x = make_uint4(0u, 0u, 0u, 0u);
-          if (kd == 1) {
-            x.x = finite_only(x.x, exponent, bad);
-            x.y = finite_only(x.y, exponent, bad);
-            x.z = finite_only(x.z, exponent, bad);
-            x.w = finite_only(x.w, exponent, bad);
-          }
-        };
+        // (a warp has rows 32 cw .. + 31 of the tile)
         if (t.eight) {
           // eight lanes read 16 bytes each of two rows four apart, and write the
           // first half of theirs while the others write the second: all banks
-          const unsigned char* from = vring + at.slot * kUnit;
-          const int c = lane & 3, half = (lane >> 2) & 1, kq = lane >> 3;
-          uint32_t most = 0;
-          uint4 xs[4 * P];
-#pragma unroll
-          for (int it = 0; it < 4 * P; ++it) {
-            const int panel = P == 2 ? it & 1 : 0, key = cw * 32 + (P == 2 ? it >> 1 : it) * 8 + kq + 4 * half;
-            const int off = DH == 128 ? key * 128 + (((panel * 4 + c) ^ (key & 7)) << 4)
-                                      : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-            xs[it] = *reinterpret_cast<const uint4*>(from + off);
-          }
-          auto store = [&](int it, const uint4& lo, const uint4& hi) {
-            const int panel = P == 2 ? it & 1 : 0, key = cw * 32 + (P == 2 ? it >> 1 : it) * 8 + kq + 4 * half;
-            unsigned char* row = to + panel * kUnit + key * 128;
-            const int a0 = ((2 * c) ^ (key & 7)) << 4, a1 = ((2 * c + 1) ^ (key & 7)) << 4;
-            *reinterpret_cast<uint4*>(row + (half ? a1 : a0)) = half ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (half ? a0 : a1)) = half ? lo : hi;
-          };
-#pragma unroll
-          for (int it = 0; it < 4 * P; ++it) {
-            const uint4 x = xs[it];
-            const uint4 lo = make_uint4(widen<0>(x.x), widen<2>(x.x), widen<0>(x.y), widen<2>(x.y));
-            const uint4 hi = make_uint4(widen<0>(x.z), widen<2>(x.z), widen<0>(x.w), widen<2>(x.w));
-            most = larger(larger(larger(larger(most, lo.x), lo.y), lo.z), lo.w);
-            most = larger(larger(larger(larger(most, hi.x), hi.y), hi.z), hi.w);
-            store(it, lo, hi);
-          }
-          if (edge || (most & 0xffffu) >= kWideNan || most >> 16 >= kWideNan) {
+          const unsigned char* from = vring + slot * kUnit + (cw * 32) * DH;
+          unsigned char* rows_to = to + cw * 32 * 128;
+          const int c = lane & 3, half = (lane >> 2) & 1, k7 = (lane >> 3) + 4 * half;
+          const int a0 = ((2 * c + half) ^ k7) << 4, a1 = ((2 * c + 1 - half) ^ k7) << 4;
 #pragma unroll 1
-            for (int it = 0; it < 4 * P; ++it) {
-              const int panel = P == 2 ? it & 1 : 0, key = cw * 32 + (P == 2 ? it >> 1 : it) * 8 + kq + 4 * half;
-              const int off = DH == 128 ? key * 128 + (((panel * 4 + c) ^ (key & 7)) << 4)
-                                        : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-              const uint4 x = *reinterpret_cast<const uint4*>(from + off);
-              uint4 lo = make_uint4(with_nan(widen<0>(x.x)), with_nan(widen<2>(x.x)), with_nan(widen<0>(x.y)),
-                                    with_nan(widen<2>(x.y)));
-              uint4 hi = make_uint4(with_nan(widen<0>(x.z)), with_nan(widen<2>(x.z)), with_nan(widen<0>(x.w)),
-                                    with_nan(widen<2>(x.w)));
-              const int kd = row_kind(a, s.r, t, t.p0 + key);
-              fix(lo, kd);
-              fix(hi, kd);
-              store(it, lo, hi);
+          for (int r0 = 0; r0 < 32; r0 += 16) {
+            uint4 xs[2 * P];
+#pragma unroll
+            for (int it = 0; it < 2 * P; ++it) {
+              const int key = r0 + (P == 2 ? it >> 1 : it) * 8 + k7, panel = P == 2 ? it & 1 : 0;
+              xs[it] = *reinterpret_cast<const uint4*>(
+                  from + (DH == 128 ? key * 128 + (((panel * 4 + c) ^ k7) << 4)
+                                    : key * 64 + ((c ^ ((key >> 1) & 3)) << 4)));
+            }
+#pragma unroll
+            for (int it = 0; it < 2 * P; ++it) {
+              const int key = r0 + (P == 2 ? it >> 1 : it) * 8 + k7, panel = P == 2 ? it & 1 : 0;
+              const uint4 x = xs[it];
+              const uint32_t u0 = half ? x.z : x.x, u1 = half ? x.w : x.y, v0 = half ? x.x : x.z, v1 = half ? x.y : x.w;
+              unsigned char* row = rows_to + panel * kUnit + key * 128;
+              *reinterpret_cast<uint4*>(row + a0) = widen(u0, u1);
+              *reinterpret_cast<uint4*>(row + a1) = widen(v0, v1);
             }
           }
-          mbar_arrive_cta(&vempty[at.slot]);
-          at = at.next();
+          freed();
         } else {
 #pragma unroll 1
           for (int u = 0; ok && u < P; ++u) {
-            if (u) wait_w(&vfull[at.slot], at.phase);
+            if (u) wait_w(&vfull[slot], phase);
             if (!ok) break;
-            const unsigned char* from = vring + at.slot * kUnit;
+            const uint4* from = reinterpret_cast<const uint4*>(vring + slot * kUnit) + cw * 256 + lane;
+            uint4* rows_to = reinterpret_cast<uint4*>(to + u * kUnit) + cw * 256 + lane;
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
-              const int off = (it * 128 + ct) * 16;
-              uint4 x = *reinterpret_cast<const uint4*>(from + off);
-              fix(x, row_kind(a, s.r, t, t.p0 + (off >> 7)));
-              *reinterpret_cast<uint4*>(to + u * kUnit + off) = x;
-            }
-            mbar_arrive_cta(&vempty[at.slot]);
-            at = at.next();
+            for (int it = 0; it < 8; ++it) rows_to[it * 32] = from[it * 32];
+            freed();
           }
           if (!ok) break;
         }
-        if (bad) atomicExch(odd, 1);
+        if (edge) {
+          // rows that not all tokens see, two at a time
+          __syncwarp();
+#pragma unroll 1
+          for (int k = lane >> 4; k < 32; k += 2) {
+            const int key = cw * 32 + k, kd = row_kind(a, s.r, t, t.p0 + key);
+            uint4* x = reinterpret_cast<uint4*>(to + ((lane >> 3) & 1) * kUnit + key * 128) + (lane & 7);
+            if ((P == 1 && (lane & 8)) || kd == 2) continue;
+            uint4 v = kd == 0 ? make_uint4(0u, 0u, 0u, 0u) : *x;
+            bool bad = false;
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              // (the four words in turn)
+              v = make_uint4(v.y, v.z, v.w, finite_only(v.x, t.eight ? 0x7c007c00u : 0x7f807f80u, bad));
+            }
+            *x = v;
+            if (bad) atomicExch(odd, 1);
+          }
+        }
         fence_proxy_async_smem();
-        mbar_arrive_cta(&wfull[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&wfull[buf]);
       }
       pos += s.n;
     }
     if (!ok && lane == 0) atomicExch(fail, 1);
   } else {
-    // ---- softmax and results: one thread per row of a copy
+    // ---- softmax and results: one thread per key of a tile, then per column of V
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-    const int copy = kCopies == 4 ? warp : kCopies == 2 ? warp >> 1 : 0;
-    const int row = kCopies == 4 ? lane : kCopies == 2 ? (warp & 1) * 32 + lane : tid;
-    const int key0 = copy * NCH * 32;            // the thread's first key of a tile
-    const bool live = row < rows;
-    const bool warp_live = row - lane < rows;
-    const int tok = live ? row / a.G : 0, g = live ? row - tok * a.G : 0;
     const int nblk = a.max_seq / a.block, shift = 31 - __clz(a.block);
+    const int chunks = SMALL ? 1 : NP / 16;
     uint32_t n = 0;                              // tiles so far
     int4 go_on = make_int4(-1, 0, 0, 0);
+    // A wait that gives up is the last that this warp makes; it goes on without
+    // (its results are marked in the end), as the others count on it at their
+    // common barriers.
     bool ok = !tree_flagged(fail);
     auto wait_w = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && tree_wait(fail, kPolls, bar, parity));
-      if (!ok && lane == 0) atomicExch(fail, 1);
+      if (ok) {
+        ok = __all_sync(0xffffffffu, wait_for(fail, bar, parity));
+        if (!ok && lane == 0) atomicExch(fail, 1);
+      }
       tc_fence_after();
     };
-    // The products P V of the first `done` tiles: those of the last but two are
+    // The products V^T P of the first `done` tiles: those of the last but two are
     // done (the scores that followed them are here), so that the last one's barrier
     // has one phase at most to go and its parity tells.
     auto wait_values = [&](uint32_t done) { wait_w(&wempty[(done - 1) & 1u], ((done - 1) >> 1) & 1u); };
-    for (long long at = plan.begin; ok && at < plan.end;) {
+    // Columns `col` .. + 15 of the thread's lane times f.
+    auto rescale = [&](uint32_t col, const float* f, float all) {
+      uint32_t o[16];
+      tmem_ld16_nw(trow + col, o);
+      tmem_wait_ld();
+      tmem_pin16(o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (f ? f[e] : all));
+      tmem_st16(trow + col, o);
+      tmem_wait_st();
+    };
+#pragma unroll 1
+    for (long long at = plan.begin; at < plan.end;) {
       const Segment s = segment_at(a, plan, at);
-      const int pos = s.r.length + tok;          // the row's own place
-      const size_t out_row = ((size_t)(s.b * (long long)a.T + tok) * a.H + s.h * a.G + g) * DH;
-      const bool present = live && tok < s.r.count;
+      const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
+      auto out_row = [&](int row) { return out0 + (size_t)row_at[row] * DH; };
+      const int live = s.r.count * a.G;          // rows with a token
       // ---- the query's parts: bf16, and e4m3 twice under a power of two
-      float c16, c8;
       {
-        uint32_t q[DH / 2];
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row);
-        uint32_t most = 0;
+        constexpr int kEach = DH / 8;            // threads per row, 8 elements each
+        const int c = tid % kEach;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 128 / kEach) {
+          const int row = r0 + tid / kEach;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < live) x = *reinterpret_cast<const uint4*>(a.q + out_row(row) + c * 8);
+          uint32_t w[4] = {x.x, x.y, x.z, x.w}, most = 0, hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < DH / 8; ++i) {
-          const uint4 x = present ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-          q[4 * i] = x.x;
-          q[4 * i + 1] = x.y;
-          q[4 * i + 2] = x.z;
-          q[4 * i + 3] = x.w;
-        }
+          for (int k = 0; k < 4; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
+          most = max(most & 0xffffu, most >> 16);
 #pragma unroll
-        for (int i = 0; i < DH / 2; ++i) most = __vmaxu2(most, q[i] & 0x7fff7fffu);
-        most = max(most & 0xffffu, most >> 16);
-        const int e = min(134 - (int)(most >> 7), 120);  // |q| 2^e below 256
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        const bool sane = most < 0x7f80u;
-        c16 = sane ? a.scale_log2 : NAN;
-        c8 = sane ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+          for (int d = kEach / 2; d; d >>= 1) most = max(most, __shfl_xor_sync(~0u, most, d));
+          const int e = min(134 - (int)(most >> 7), 120);  // |q| 2^e below 256
+          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-        for (int i = 0; i < DH / 2; i += 32) {
-          uint32_t x[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = a.negate ? q[i + k] ^ 0x80008000u : q[i + k];
-          tmem_st32(trow + kColQ16 + i, x);
-        }
-#pragma unroll
-        for (int i = 0; i < DH / 4; i += 16) {
-          uint32_t p0[16], p1[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t w = a.negate ? q[2 * (i + k) + z] ^ 0x80008000u : q[2 * (i + k) + z];
-              const float2 f = make_float2(bf16_lo(w) * up, bf16_hi(w) * up);
-              const uint32_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-              const __half2 b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
-              const float2 d = __half22float2(b);
-              const uint32_t l =
-                  __nv_cvt_float2_to_fp8x2(make_float2(f.x - d.x, f.y - d.y), __NV_SATFINITE, __NV_E4M3);
-              w0 |= h << (16 * z);
-              w1 |= l << (16 * z);
-            }
-            p0[k] = w0;
-            p1[k] = w1;
+          for (int k = 0; k < 4; ++k) {
+            if (a.negate) w[k] ^= 0x80008000u;
+            const float2 f = make_float2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+            const uint32_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+            const __half2 b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
+            const float2 d = __half22float2(b);
+            const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(f.x - d.x, f.y - d.y), __NV_SATFINITE, __NV_E4M3);
+            hi[k >> 1] |= h << (16 * (k & 1));
+            lo[k >> 1] |= l << (16 * (k & 1));
           }
-          tmem_st16(trow + kColQ8 + i, p0);
-          tmem_st16(trow + kColQ8 + DH / 4 + i, p1);
+          if (row >= rows) continue;
+          auto place = [&](int r) {
+            return DH == 128 ? r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8
+                             : r * 64 + (((c >> 1) ^ ((r >> 1) & 3)) << 4) + (c & 1) * 8;
+          };
+          *reinterpret_cast<uint2*>(q8 + place(row)) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(q8 + place(NP + row)) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint4*>(q16 + (c >> 3) * NP * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+          if (c == 0)
+            row_c[row] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive_cta(qready);
+        if (tid < NP) row_nm[tid] = -kNone;
+        if (tid >= rows && tid < NP) row_c[tid] = 0.f;
+        fence_proxy_async_smem();
+        bar_softmax();
+        if (lane == 0) mbar_arrive_cta(qready);
       }
       // ---- tiles
-      // O holds sums of 2^(score - m) v 2^-1 / vref: P has 2^7 of it and fp16 V 2^-8,
-      // bf16 P 2^-1 by itself
-      float m = -INFINITY, l = 0.f, vref = 0.f;
+      // O holds sums of 2^(score - m) v 2^7 / vref
+      float vref = 0.f, ls[16] = {};
+      if (!SMALL) {
+        uint32_t zero[16] = {};
+#pragma unroll 1
+        for (int q = 0; q < chunks; ++q) tmem_st16(trow + col_l + q * 16, zero);
+        tmem_wait_st();
+      }
       const float* kscale = a.k_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
       const float* vscale = a.v_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
-      float ks[NCH], vs[NCH];                    // of the tile to come
-      auto fetch = [&](const Tile& t) {
-#pragma unroll
-        for (int q = 0; q < NCH; ++q) {
-          ks[q] = vs[q] = 1.f;
-          if (t.eight) {
-            const int blk = min((t.p0 + key0 + 32 * q) >> shift, nblk - 1);
-            ks[q] = kscale[blk];
-            vs[q] = vscale[blk];
-          }
+      float ks = 1.f, vs = 1.f;                  // of the tile to come, the warp's 32 keys
+      auto fetch = [&](const Walk& t) {
+        const int blk = min((t.p0 + warp * 32) >> shift, nblk - 1);
+        if (t.eight) {
+          ks = kscale[blk];
+          vs = vscale[blk];
         }
       };
-      Tile t = tile_at(s.r, s.i0);
+      Walk t = walk_from(s.r, a.window, s.i0);
       fetch(t);
+      float unit = 0.f;                          // 2^7 / vref
+#pragma unroll 1
       for (int i = 0; i < s.n; ++i, ++n) {
         const uint32_t buf = n & 1u;
-        const uint32_t scol = trow + buf * 128;
-        float c[NCH], v[NCH];
-#pragma unroll
-        for (int q = 0; q < NCH; ++q) {
-          // (a scale of 0 must not meet the minus infinity of a key that is not
-          // seen; scales below 0 are none)
-          c[q] = t.eight ? (ks[q] >= 0.f ? fmaxf(c8 * ks[q], 1.2e-38f) : NAN) : c16;
-          if (!(c8 == c8)) c[q] = NAN;
-          v[q] = vs[q];
-        }
-        const Tile now = t;
-        const bool edge = has_edge(a, s.r, now);
+        const Walk now = t;
+        const bool edge = now.edge();
+        const float kc = ks, vc = now.eight ? vs : 1.f;
         if (i + 1 < s.n) {
-          t = tile_at(s.r, s.i0 + i + 1);
+          step(t, s.r, a.window);
           fetch(t);
         }
-        wait_w(&sfull[buf], (n >> 1) & 1u);
-        if (!ok) break;
-        if (warp_live) {
-          constexpr int kKept = NCH <= 2 ? NCH : 1;
-          uint32_t sr[kKept][32];
-          float bm = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < NCH; ++q) {
-            uint32_t(&x)[32] = sr[q % kKept];
-            tmem_ld32_nw(scol + key0 + 32 * q, x);
-            tmem_wait_ld();
-            tmem_pin32(x);
-            if (edge) {
-              const uint32_t seen = present ? seen_bits(a, now, pos, now.p0 + key0 + 32 * q) : 0u;
-              if (seen == 0u) {
-                c[q] = 1.2e-38f;
-                v[q] = 0.f;
-              }
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((seen >> e) & 1u)) x[e] = 0xff800000u;
-              if (NCH > 2) tmem_st32(scol + key0 + 32 * q, x);
-            }
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx[(e >> 1) & 1] = tree_max3(mx[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            bm = fmaxf(bm, fmaxf(mx[0], mx[1]) * c[q]);
+        // the rows that see the thread's key: [r0, r1)
+        int r0 = 0, r1 = NP;
+        if (edge) {
+          const int j = now.p0 + tid;
+          r0 = max(j - s.r.length, 0) * a.G;
+          r1 = live;
+          if (a.window && j >= a.sinks) {
+            const long long last = (long long)j + a.window - s.r.length;
+            if (last < s.r.count) r1 = last < 0 ? 0 : (int)last * a.G;
           }
-          if (NCH > 2 && edge) tmem_wait_st();
-          const bool raise = bm > m + kRaise || (m == -INFINITY && bm > -INFINITY);
-          float over = 0.f;                      // the largest scale over vref
+          if (j < now.rs || j >= now.re) r1 = 0;
+        }
+        wait_w(&sfull[buf], (n >> 1) & 1u);
+        if (lay.p_bufs == 1 && n > 0) wait_values(n);  // P's only place is free
+        // the warp's scale passes vref (if any of its keys counts)
+        const bool over = now.eight && fabsf(vc) > vref && fabsf(vc) < 0x1p100f && now.p0 + warp * 32 < now.re &&
+                          now.p0 + warp * 32 + 32 > now.rs;
+        float pv = vc * unit;
+        unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + tid * 32;
+#pragma unroll 1
+        for (int q = 0; q < chunks; ++q) {
+          uint32_t x[16], y[16];
+          const uint32_t scol = trow + buf * scols + q * 16;
+          tmem_ld16_nw(scol, x);
+          tmem_ld16_nw(SMALL ? scol + 16 : trow + col_l + q * 16, y);
+          float c[16], nm[16];
 #pragma unroll
-          for (int q = 0; q < NCH; ++q)
-            if (now.eight && fabsf(v[q]) > fmaxf(vref, over) && fabsf(v[q]) < 0x1p100f) over = fabsf(v[q]);
-          if (__any_sync(0xffffffffu, raise || over > 0.f || vref == 0.f)) {
-            float corr = raise ? tree_ex2(m - bm) : 1.f;
-            if (raise) m = bm;
-            l *= corr;
-            if (over > 0.f || vref == 0.f) {
-              const float next = over > 0.f ? power_above(over) * 4.f : 1.f;
-              corr *= vref / next;               // (both are powers of two, or 0 at the start)
-              vref = next;
+          for (int e = 0; e < 16; e += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(row_c + q * 16 + e);
+            const float4 w = *reinterpret_cast<const float4*>(row_nm + q * 16 + e);
+            c[e] = u.x, c[e + 1] = u.y, c[e + 2] = u.z, c[e + 3] = u.w;
+            nm[e] = w.x, nm[e + 1] = w.y, nm[e + 2] = w.z, nm[e + 3] = w.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) c[e] = now.eight ? c[e] * kc : a.scale_log2;
+          tmem_wait_ld();
+          tmem_pin16(x);
+          tmem_pin16(y);
+          const int m0 = max(r0 - q * 16, 0), m1 = min(r1 - q * 16, 16);
+          const uint32_t seen = m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
+          float d[16];
+          auto below = [&]() {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              d[e] = fmaf(__uint_as_float(x[e]), c[e], nm[e]);
+              if (edge && !((seen >> e) & 1u)) d[e] = -INFINITY;
+            }
+          };
+          if (SMALL && now.eight)                // the low part's product
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
+          below();
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) top[(e >> 1) & 1] = tree_max3(top[(e >> 1) & 1], d[e], d[e + 1]);
+          if (any_softmax(fmaxf(top[0], top[1]) > kRaise || (over && q == 0) || vref == 0.f)) {
+            if (q == 0) {
+              // the largest of the four warps' scales
+              bar_softmax();
+              if (lane == 0) part[warp] = over ? fabsf(vc) : 0.f;
+              bar_softmax();
+              const float most = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+              if (most > vref || vref == 0.f) {
+                const float next = most > 0.f ? power_above(most) * 4.f : 1.f;
+                if (i > 0) {
+                  wait_values(n);
+#pragma unroll 1
+                  for (int z = 0; z < chunks; ++z) rescale(col_o + z * 16, nullptr, vref / next);
+                }
+                vref = next;
+                unit = 0x1p7f / next;
+                pv = vc * unit;
+              }
+              bar_softmax();
+            }
+            // the rows' largest scores of all keys; those that pass m + 8 become m
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              d[e] = edge && !((seen >> e) & 1u) ? -INFINITY : __uint_as_float(x[e]) * c[e];
+            over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
+            if (!(lane & 1)) part[warp * 32 + (lane >> 1)] = d[0];
+            bar_softmax();
+            if (tid < 16) {
+              const float old = -row_nm[q * 16 + tid];
+              const float z = fmaxf(fmaxf(part[tid], part[32 + tid]), fmaxf(part[64 + tid], part[96 + tid]));
+              const float m = z > old + kRaise ? z : old;
+              row_f[q * 16 + tid] = tree_ex2(old - m);
+              row_nm[q * 16 + tid] = -m;
+            }
+            bar_softmax();
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              f[e] = row_f[q * 16 + e];
+              nm[e] = row_nm[q * 16 + e];
+              if (SMALL) ls[e] *= f[e];
+              else y[e] = __float_as_uint(__uint_as_float(y[e]) * f[e]);
             }
             if (i > 0) {
               wait_values(n);                    // O as the tile before left it
-              if (!ok) break;
-#pragma unroll 1
-              for (int q = 0; q < DH / 16; ++q) {
-                uint32_t o[16];
-                tmem_ld16_nw(trow + kColO + q * 16, o);
-                tmem_wait_ld();
-                tmem_pin16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                tmem_st16(trow + kColO + q * 16, o);
-              }
+              rescale(col_o + q * 16, f, 1.f);
             }
+            below();
           }
-          const float nm = m == -INFINITY ? 0.f : -m, unit = (now.eight ? 0x1p7f : 0x1p-1f) / vref;
-          const uint64_t nm2 = tree_pack2(__float_as_uint(nm), __float_as_uint(nm));
-          uint64_t ls2[2] = {0, 0};
+          uint32_t pk[8];
           auto weights = [&](auto eight) {
 #pragma unroll
-            for (int q = 0; q < NCH; ++q) {
-              uint32_t(&x)[32] = sr[q % kKept];
-              if (NCH > 2) {
-                tmem_ld32_nw(scol + key0 + 32 * q, x);
-                tmem_wait_ld();
-                tmem_pin32(x);
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = tree_ex2(d[e]), p1 = tree_ex2(d[e + 1]);
+              if (SMALL) {
+                ls[e] += p0;
+                ls[e + 1] += p1;
+              } else {
+                y[e] = __float_as_uint(__uint_as_float(y[e]) + p0);
+                y[e + 1] = __float_as_uint(__uint_as_float(y[e + 1]) + p1);
               }
-              const uint64_t c2 = tree_pack2(__float_as_uint(c[q]), __float_as_uint(c[q]));
-              const float pv = v[q] * unit;
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float p0, p1;
-                tree_unpack2(tree_fma2(tree_pack2(x[2 * e], x[2 * e + 1]), c2, nm2), p0, p1);
-                p0 = tree_ex2(p0);
-                p1 = tree_ex2(p1);
-                ls2[e & 1] = tree_add2(ls2[e & 1], tree_pack2(__float_as_uint(p0), __float_as_uint(p1)));
-                pk[e] = decltype(eight)::value ? pack_f16x2(p0 * pv, p1 * pv) : pack_bf16x2(p0 * pv, p1 * pv);
-              }
-              tmem_st16(scol + (key0 + 32 * q) / 2, pk);
+              pk[e / 2] = decltype(eight)::value ? pack_f16x2(p0 * pv, p1 * pv) : pack_bf16x2(p0 * pv, p1 * pv);
             }
           };
           if (now.eight) weights(std::true_type());
           else weights(std::false_type());
-          // the other copies' keys
-          if (kCopies > 1) {
-            const uint32_t zero[16] = {};
+          if (edge)                              // (a scale that is none of the row's)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (q * 32 < key0 || q * 32 >= key0 + NCH * 32) tmem_st16(scol + q * 16, zero);
-          }
-          float l0, l1;
-          tree_unpack2(tree_add2(ls2[0], ls2[1]), l0, l1);
-          l += l0 + l1;
-          tmem_wait_st();
+            for (int e = 0; e < 16; e += 2)
+              pk[e / 2] &= ((seen >> e) & 1u ? 0x0000ffffu : 0u) | ((seen >> e) & 2u ? 0xffff0000u : 0u);
+          const int flip = ((tid >> 2) & 1) << 4;
+          *reinterpret_cast<uint4*>(pto + q * kPanel + flip) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(pto + q * kPanel + (16 ^ flip)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          if (!SMALL) tmem_st16(trow + col_l + q * 16, y);
         }
+        if (!SMALL) tmem_wait_st();
+        fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive_cta(&pready[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&pready[buf]);
       }
-      if (!ok) break;
       // ---- the run's result: final, or a part of the pair's
       wait_values(n);
-      if (!ok) break;
       const bool bad = tree_flagged(odd);
-      const long long slot = (long long)blockIdx.x * 2 + (s.head ? 0 : 1);
-      if (!s.whole && at + s.n == plan.end && s.i0 + s.n < (int)(plan.first[s.b + 1] - plan.first[s.b]) && !s.head) {
-        // the pair's last tile: which CTA has it
-        const long long last = plan.first[s.b] * a.Hkv +
-                               (long long)(s.h + 1) * (plan.first[s.b + 1] - plan.first[s.b]) - 1;
-        go_on = make_int4(s.b, s.h, plan.owner(last), 0);
-      }
-      float* po = a.part_o + (size_t)slot * rows * DH;
-      float* pm = a.part_m + (size_t)slot * rows;
-      float* pl = a.part_l + (size_t)slot * rows;
-      if (kCopies == 1) {
-        if (warp_live) {
-          const float inv = vref * 2.f * (s.whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f);
-          if (live && !s.whole) {
-            pm[row] = m;
-            pl[row] = l;
-          }
+      const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
+      if (!s.whole && !s.head)                   // which CTA has the pair's last tile
+        go_on = make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0);
+      // the sums over the keys: a warp's, then the four warps'
 #pragma unroll 1
-          for (int q = 0; q < DH / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32_nw(trow + kColO + q * 32, o);
-            tmem_wait_ld();
-            tmem_pin32(o);
-            if (!live) continue;
+      for (int q = 0; q < chunks; ++q) {
+        float v[16];
+        if (SMALL) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = present ? __uint_as_float(o[e + k]) * inv : 0.f;
-              if (bad && present) add_not_finite(a, s, pos, q * 32 + e, 8, w);
-              if (s.whole) {
-                *reinterpret_cast<uint4*>(a.out + out_row + q * 32 + e) =
-                    make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
-                               pack_bf16x2(w[6], w[7]));
-              } else {
-                float4* d = reinterpret_cast<float4*>(po + (size_t)row * DH + q * 32 + e);
-                d[0] = make_float4(w[0], w[1], w[2], w[3]);
-                d[1] = make_float4(w[4], w[5], w[6], w[7]);
-              }
-            }
-          }
-        }
-      } else {
-        // the copies of a row, under the largest of their maxima
-        constexpr int kRows = 128 / kCopies;
-        xm[tid] = m;
-        xl[tid] = l;
-        bar_softmax();
-        float all = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kCopies; ++k) all = fmaxf(all, xm[k * kRows + row]);
-        const float base = all == -INFINITY ? 0.f : all;
-#pragma unroll
-        for (int k = 0; k < kCopies; ++k) sum += xl[k * kRows + row] * tree_ex2(xm[k * kRows + row] - base);
-        const float w0 = tree_ex2(m - base) * (vref * 2.f);
-        if (copy == 0) {
-          row_m[row] = all;
-          row_l[row] = sum;
-          if (live && !s.whole) {
-            pm[row] = all;
-            pl[row] = sum;
-          }
-        }
-#pragma unroll 1
-        for (int q = 0; q < DH / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32_nw(trow + kColO + q * 32, o);
+          for (int e = 0; e < 16; ++e) v[e] = ls[e];
+        } else {
+          uint32_t y[16];
+          tmem_ld16_nw(trow + col_l + q * 16, y);
           tmem_wait_ld();
-          tmem_pin32(o);
-          float* mine = merge + warp * 32 * 33 + lane * 33;
+          tmem_pin16(y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mine[e] = m == -INFINITY ? 0.f : __uint_as_float(o[e]) * w0;
-          bar_softmax();
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(y[e]);
+        }
+        over_lanes(v, [](float u, float w) { return u + w; });
+        if (!(lane & 1)) part[warp * 32 + (lane >> 1)] = v[0];
+        bar_softmax();
+        if (tid < 16) {
+          const int row = q * 16 + tid;
+          const float l = (part[tid] + part[32 + tid]) + (part[64 + tid] + part[96 + tid]);
+          row_f[row] = row < live ? 0x1p-7f * vref * (!s.whole ? 1.f : l != 0.f ? 1.f / l : 0.f) : 0.f;
+          if (!s.whole && row < rows) {
+            a.part_m[slot * rows + row] = -row_nm[row];
+            a.part_l[slot * rows + row] = row < live ? l : 0.f;
+          }
+        }
+        bar_softmax();
+        if (DH == 128 || warp < 2) {
+          const int most = min(16, rows - q * 16);
+          bf16* out = a.out + out0 + tid;
+          float* po = a.part_o + (slot * rows + q * 16) * DH + tid;
+#pragma unroll 1
+          for (int e0 = 0; e0 < most; e0 += 4) {
+            float o[4];
+            tmem_ld4(trow + col_o + q * 16 + e0, o);
 #pragma unroll
-          for (int z = 0; z < kRows / 32; ++z) {
-            const int rr = z * 32 + tid / 4, e0 = (tid & 3) * 8;
-            if (rr < rows) {
-              const int tk = rr / a.G, gg = rr - tk * a.G;
-              const float lt = row_l[rr], inv = s.whole ? (lt != 0.f ? 1.f / lt : 0.f) : 1.f;
-              const bool here = tk < s.r.count;
-              float w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float x = 0.f;
-#pragma unroll
-                for (int k = 0; k < kCopies; ++k) x += merge[(k * kRows + rr) * 33 + e0 + e];
-                w[e] = here ? x * inv : 0.f;
-              }
-              if (bad && here) add_not_finite(a, s, s.r.length + tk, q * 32 + e0, 8, w);
-              if (s.whole) {
-                bf16* o8 = a.out + ((size_t)(s.b * (long long)a.T + tk) * a.H + s.h * a.G + gg) * DH + q * 32 + e0;
-                *reinterpret_cast<uint4*>(o8) = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
-                                                           pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
-              } else {
-                float4* d = reinterpret_cast<float4*>(po + (size_t)rr * DH + q * 32 + e0);
-                d[0] = make_float4(w[0], w[1], w[2], w[3]);
-                d[1] = make_float4(w[4], w[5], w[6], w[7]);
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int row = q * 16 + e0 + e;
+              const float w = row < live ? o[e] * row_f[row] : 0.f;
+              if (row < rows && s.whole) out[row_at[row] * DH] = __float2bfloat16(w);
+              if (row < rows && !s.whole) po[(e0 + e) * DH] = w;
             }
           }
-          bar_softmax();
+          if (bad)                               // what the products left out
+#pragma unroll 1
+            for (int e = 0; e < min(most, live - q * 16); ++e) {
+              const int row = q * 16 + e;
+              const float w = not_finite(a, s, s.r.length + row / a.G, tid);
+              if (s.whole) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
+              else po[e * DH] += w;
+            }
         }
       }
       at += s.n;
@@ -926,28 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  // a wait gave up: none of the CTA's rows is sure
-  if (tree_flagged(fail))
-    for (long long at = plan.begin; at < plan.end;) {
-      const Segment s = segment_at(a, plan, at);
-      const long long slot = (long long)blockIdx.x * 2 + (s.head ? 0 : 1);
-      if (!s.whole && !s.head && tid == 0) {
-        const long long n = plan.first[s.b + 1] - plan.first[s.b];
-        const long long last = plan.first[s.b] * a.Hkv + (long long)(s.h + 1) * n - 1;
-        a.shared[blockIdx.x] = make_int4(s.b, s.h, plan.owner(last), 0);
-      }
-      for (int i = tid; i < rows * DH; i += kThreads) {
-        const int r = i / DH, tk = r / a.G;
-        if (s.whole) {
-          if (tk < s.r.count)
-            a.out[((size_t)(s.b * (long long)a.T + tk) * a.H + s.h * a.G + r % a.G) * DH + i % DH] = __float2bfloat16(NAN);
-        } else if (i % DH == 0) {
-          a.part_m[slot * rows + r] = 0.f;
-          a.part_l[slot * rows + r] = NAN;
-        }
-      }
-      at += s.n;
-    }
+  if (tree_flagged(fail)) mark_rows(a, plan);
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -1004,20 +1118,18 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
   *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int DH, int NCH>
+template <int DH, bool SMALL>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream_t st) {
-  const size_t most = Shape<DH>::kSmem + 1024 + 8 * (kBatchMaxSeqs + 1) + 12 * kBatchMaxSeqs;
-  const size_t smem = Shape<DH>::kSmem + 1024 + 8 * ((size_t)a.B + 1) + 12 * (size_t)a.B;
-  static_assert(Shape<DH>::kSmem + 1024 + 20 * kBatchMaxSeqs + 8 <= 227 * 1024, "shared memory");
+  const Layout lay = layout_of(a.T * a.G, DH, a.B);
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, NCH>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, SMALL>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  cache_attn_tc_kernel<DH, NCH><<<a.ctas, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], a);
+  cache_attn_tc_kernel<DH, SMALL><<<a.ctas, kThreads, lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1072,10 +1184,9 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   m[1] = m[3];
   if (a.k8 && (!map(&m[0], true, a.k8, a.max_seq, a.seq8_stride) || !map(&m[1], true, a.v8, a.max_seq, a.seq8_stride)))
     return cudaErrorInvalidValue;
-  const int rows = a.T * a.G;
-  if (a.dh == 128)
-    return rows <= 32 ? launch<128, 1>(a, m, s) : rows <= 64 ? launch<128, 2>(a, m, s) : launch<128, 4>(a, m, s);
-  return rows <= 32 ? launch<64, 1>(a, m, s) : rows <= 64 ? launch<64, 2>(a, m, s) : launch<64, 4>(a, m, s);
+  const bool few = a.T * a.G <= 16;
+  if (a.dh == 128) return few ? launch<128, true>(a, m, s) : launch<128, false>(a, m, s);
+  return few ? launch<64, true>(a, m, s) : launch<64, false>(a, m, s);
 }
 
 }  // namespace ssd
