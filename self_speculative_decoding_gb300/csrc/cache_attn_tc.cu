@@ -11,10 +11,10 @@
 //   P = 2^(S c - m) v_scale one thread per key, 16 bits, to shared memory
 //   O += V^T P              8-bit rows: V widened to fp16, P in fp16; bf16 rows: both bf16
 //
-// A thread has one key and all rows: what lies below the rows' maxima so far by
-// less than nothing (m + 8: a factor of 256, which the sums and P carry) needs no
-// look at other threads but one vote of the four warps for 16 rows; where a score
-// passes it, m is raised and O rescaled.
+// A thread has one key and all rows: scores up to m + 8 (a factor of 256, which the
+// sums and P carry) over the rows' maxima so far need no look at other threads but
+// one vote of four warps for 8 rows; where a score passes that, m is raised and O
+// rescaled.
 //
 // K and q enter the matrix instructions as they are: a tile of K costs no thread
 // anything.  V cannot: P needs more than e4m3's range and bits (a first row that
@@ -29,9 +29,14 @@
 // joined by a second kernel in a fixed order.  The division is computed from the
 // lengths on the device, so that a graph follows them.
 //
-// Warps 0-3: softmax and results; 4-7: V to 16 bits; 8: copies of K; 9: copies of V;
-// 10: matrix instructions.  Every wait is bounded: one that gives up sets the
-// CTA's flag, every role runs out, and the CTA's rows become NaN.
+// The softmax is a chain of latencies (scores out of tensor memory, a vote, the
+// exponentials) and no unit's full load, so that several groups of four warps
+// take 8 rows of a tile each, in turn.
+//
+// Warps 0 .. 4 groups - 1: softmax and results; then four warps that widen V, one
+// that copies K, one that copies V, one for the matrix instructions.  Every wait is
+// bounded: one that gives up sets the CTA's flag, every role runs out, and the
+// CTA's rows become NaN.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -47,12 +52,14 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = 128;
-constexpr int kThreads = 352;
 constexpr int kWiden = 128;                      // threads that widen V
 constexpr int kPolls = 1 << 22;
 constexpr int kUnit = 16 * 1024;                 // 128 rows of up to 128 bytes, swizzled
 constexpr float kRaise = 8.f;
 constexpr float kNone = -1e30f;                  // the maximum of a row that has seen no key
+
+// A condition that seldom holds: its code lies apart from the loop's.
+SSD_DI bool seldom(bool x) { return __builtin_expect(x, false); }
 
 // Shared memory: q in e4m3 parts and in bf16, P, V in 16 bits, rings of K and V.
 struct Layout {
@@ -90,15 +97,6 @@ __host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
   return l;
 }
 
-SSD_DI void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
 // Four columns of the thread's lane, waited for.
 SSD_DI void tmem_ld4(uint32_t taddr, float (&r)[4]) {
   asm volatile(
@@ -148,41 +146,60 @@ SSD_DI void mma_ss_e4m3(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdes
 }
 // tree_wait, in a loop that stays one.
 SSD_DI bool wait_for(const int* fail, uint64_t* a, uint32_t pa) {
-  if (tree_try(a, pa)) return true;
+  if (!seldom(!tree_try(a, pa))) return true;
 #pragma unroll 1
   for (int i = 0; i < kPolls; ++i) {
     if (tree_try(a, pa)) return true;
-    if ((i & 63) == 63 && tree_flagged(fail)) return false;
+    if (seldom((i & 63) == 63) && tree_flagged(fail)) return false;
   }
   return false;
 }
-SSD_DI void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// 16 values of each lane joined over the warp by halving: lane l ends with value
-// l / 2 in v[0].
+// The barrier of a group of four softmax warps.
+SSD_DI void bar_group(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+// 8 columns of the thread's tensor memory lane.
+SSD_DI void tmem_ld8_nw(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+SSD_DI void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+SSD_DI void tmem_pin8(uint32_t (&r)[8]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+// 8 values of each lane joined over the warp by halving: lane l ends with value
+// l / 4 in v[0].
 template <class F>
-SSD_DI void over_lanes(float (&v)[16], F join) {
+SSD_DI void over_lanes(float (&v)[8], F join) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int w = 16; w > 1; w >>= 1) {
+  for (int w = 16; w > 2; w >>= 1) {
     const bool up = lane & w;
 #pragma unroll
-    for (int e = 0; e < w / 2; ++e) {
-      const float got = __shfl_xor_sync(~0u, up ? v[e] : v[e + w / 2], w);
-      v[e] = join(up ? v[e + w / 2] : v[e], got);
+    for (int e = 0; e < w / 4; ++e) {
+      const float got = __shfl_xor_sync(~0u, up ? v[e] : v[e + w / 4], w);
+      v[e] = join(up ? v[e + w / 4] : v[e], got);
     }
   }
+  v[0] = join(v[0], __shfl_xor_sync(~0u, v[0], 2));
   v[0] = join(v[0], __shfl_xor_sync(~0u, v[0], 1));
 }
-// Whether any of the softmax threads says so.
-SSD_DI bool any_softmax(bool x) {
+// Whether any thread of the group says so.
+SSD_DI bool any_group(int group, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(group + 1)
       : "memory");
   return r != 0;
 }
@@ -258,7 +275,7 @@ static __device__ __noinline__ Walk walk_from(SeqRange r, int window, int tile) 
 SSD_DI void step(Walk& w, const SeqRange& r, int window) {
   ++w.i;
   w.p0 += kKeys;
-  if (--w.left == 0) w = walk_from(r, window, w.i);
+  if (seldom(--w.left == 0)) w = walk_from(r, window, w.i);
 }
 
 // What the CTA's threads know of the sequences, in shared memory.
@@ -378,7 +395,7 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
     const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
     if (!s.whole && !s.head && threadIdx.x == 0)
       a.shared[blockIdx.x] = make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0);
-    for (int i = threadIdx.x; i < rows * a.dh; i += kThreads) {
+    for (int i = threadIdx.x; i < rows * a.dh; i += blockDim.x) {
       const int r = i / a.dh, tk = r / a.G;
       if (s.whole) {
         if (tk < s.r.count)
@@ -393,12 +410,16 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
 }
 
 // SMALL: up to 16 rows, whose parts of q make one product (twice as wide) and
-// whose sums a thread keeps in registers (else in tensor memory).
+// whose state two groups keep in registers.
+constexpr int groups_of(bool small) { return small ? 2 : 3; }
+constexpr int threads_of(bool small) { return (4 * groups_of(small) + 7) * 32; }
 template <int DH, bool SMALL>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(SMALL), 1)
     cache_attn_tc_kernel(const __grid_constant__ CUtensorMap mK8, const __grid_constant__ CUtensorMap mV8,
                          const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                          const __grid_constant__ CacheAttnArgs a, const Layout lay) {
+  constexpr int kGroups = groups_of(SMALL), kThreads = threads_of(SMALL);
+  constexpr int kWidenWarp = 4 * kGroups, kCopyWarp = kWidenWarp + 4, kMmaWarp = kCopyWarp + 2;
   constexpr int P = DH / 64;                     // 16-bit panels of 64 columns
   constexpr int kWide = P * kUnit;               // a V tile in 16 bits
   const int NP = SMALL ? 16 : lay.rows;
@@ -412,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* row_c = reinterpret_cast<float*>(sm + lay.rest);  // [128] what a row's 8-bit scores are multiplied by
   float* row_nm = row_c + 128;                   // [128] minus its maximum
   float* row_f = row_nm + 128;                   // [128] what O is multiplied by in the end
-  float* part = row_f + 128;                     // [4][32] of the warps
+  float* part = row_f + 128;                     // [groups][4][8] of the warps
   int* row_at = reinterpret_cast<int*>(part + 128);  // [128] a row's place among the sequence's heads
   uint64_t* bars = reinterpret_cast<uint64_t*>(row_c + 5 * 128);
   uint64_t* kfull = bars;                        // [8] each
@@ -434,10 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   plan.held = plan.length + a.B;
   plan.count = reinterpret_cast<short*>(plan.held + a.B);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rows = a.T * a.G;
+  const int rows = a.T * a.G, chunks = (rows + 7) / 8;
+  const int active = min(kGroups, chunks);       // groups with any rows
 
   // ---- set-up
-  if (tid == 320) {
+  if (tid == kMmaWarp * 32) {
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       mbar_init(&kfull[i], 1);
@@ -450,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&wfull[i], kWiden / 32);
       mbar_init(&wempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], 4);
+      mbar_init(&pready[i], 4 * active);
     }
-    mbar_init(qready, 4);
+    mbar_init(qready, 4 * active);
     mbar_init(mdone, 1);
     *fail = (int)blockIdx.x == a.give_up;
     *odd = 0;
@@ -469,11 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     plan.first[b + 1] = tiles_of(seq_range_of(a, n, c, h));
   }
   if (tid < rows) row_at[tid] = tid / a.G * a.H + tid % a.G;
-  // q's rows that there are none of
+  // the rows beyond
+  if (tid >= rows && tid < 128) row_c[tid] = 0.f;
 #pragma unroll 1
   for (int i = tid; i < lay.p / 16; i += kThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kWidenWarp) {
     int sum = 0;
     if (lane == 0) plan.first[0] = 0;
 #pragma unroll 1
@@ -500,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) atomicExch(fail, 1);
   };
 
-  if (warp == 8 || warp == 9) {
-    // ---- copies of K (warp 8) or V (warp 9) tiles, in units of 128 rows of up to
+  if (warp == kCopyWarp || warp == kCopyWarp + 1) {
+    // ---- copies of K (first warp) or V tiles, in units of 128 rows of up to
     // 128 bytes: one for a tile of 8-bit rows, a panel of 64 columns each for bf16
     if (lane == 0) {
-      const bool is_v = warp == 9;
+      const bool is_v = warp > kCopyWarp;
       const int units = is_v ? lay.v_units : lay.k_units;
       unsigned char* ring = is_v ? vring : kring;
       uint64_t *full = is_v ? vfull : kfull, *empty = is_v ? vempty : kempty;
@@ -541,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, issued - units); i < issued; ++i)
         mbar_wait_n(&full[i % units], (uint32_t)((i / units) & 1), kPolls);
     }
-  } else if (warp == 10) {
+  } else if (warp == kMmaWarp) {
     // ---- products: the warp runs together, one lane issues
     const uint32_t lead = tree_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -572,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) return;
       const uint32_t kb = kr + (uint32_t)k0 * kUnit;
       next_k();
-      if (eight) {
+      if (!seldom(!eight)) {
         const uint64_t kd = DH == 128 ? sw128_desc(kb) : sw64_desc(kb);
         uint64_t qd = DH == 128 ? sw128_desc(qa8) : sw64_desc(qa8);
         // (the low part first)
@@ -633,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) atomicExch(fail, 1);
     tree_commit(lead, mdone);
     mbar_wait_n(mdone, 0u, kPolls);
-  } else if (warp >= 4) {
+  } else if (warp >= kWidenWarp) {
     // ---- V to 16 bits in the products' layout
-    const int cw = warp - 4, ct = tid - 128;
+    const int cw = warp - kWidenWarp, ct = tid - kWidenWarp * 32;
 #pragma unroll 1
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       if (plan.first[b + 1] != plan.first[b]) continue;
@@ -674,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && n >= 2) wait_w(&wempty[buf], ((n >> 1) & 1u) ^ 1u);
         if (!ok) break;
         // (a warp has rows 32 cw .. + 31 of the tile)
-        if (t.eight) {
+        if (!seldom(!t.eight)) {
           // eight lanes read 16 bytes each of two rows four apart, and write the
           // first half of theirs while the others write the second: all banks
           const unsigned char* from = vring + slot * kUnit + (cw * 32) * DH;
@@ -715,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        if (edge) {
+        if (seldom(edge)) {
           // rows that not all tokens see, two at a time
           __syncwarp();
 #pragma unroll 1
@@ -742,10 +766,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) atomicExch(fail, 1);
   } else {
-    // ---- softmax and results: one thread per key of a tile, then per column of V
-    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    // ---- softmax and results: one thread per key of a tile and group, then per
+    // column of V; group g has rows 8 q .. 8 q + 7 for q = g, g + groups, ...
+    const int group = warp >> 2, w4 = warp & 3, key = tid & 127;
+    const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
     const int nblk = a.max_seq / a.block, shift = 31 - __clz(a.block);
-    const int chunks = SMALL ? 1 : NP / 16;
+    float* gpart = part + group * 32;
     uint32_t n = 0;                              // tiles so far
     int4 go_on = make_int4(-1, 0, 0, 0);
     // A wait that gives up is the last that this warp makes; it goes on without
@@ -755,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_w = [&](uint64_t* bar, uint32_t parity) {
       if (ok) {
         ok = __all_sync(0xffffffffu, wait_for(fail, bar, parity));
-        if (!ok && lane == 0) atomicExch(fail, 1);
+        if (seldom(!ok) && lane == 0) atomicExch(fail, 1);
       }
       tc_fence_after();
     };
@@ -763,83 +789,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     // done (the scores that followed them are here), so that the last one's barrier
     // has one phase at most to go and its parity tells.
     auto wait_values = [&](uint32_t done) { wait_w(&wempty[(done - 1) & 1u], ((done - 1) >> 1) & 1u); };
-    // Columns `col` .. + 15 of the thread's lane times f.
-    auto rescale = [&](uint32_t col, const float* f, float all) {
-      uint32_t o[16];
-      tmem_ld16_nw(trow + col, o);
+    // Columns of O of 8 rows times f, or all.
+    auto rescale = [&](int q, const float* f, float all) {
+      uint32_t o[8];
+      tmem_ld8_nw(trow + col_o + q * 8, o);
       tmem_wait_ld();
-      tmem_pin16(o);
+      tmem_pin8(o);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (f ? f[e] : all));
-      tmem_st16(trow + col, o);
+      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (f ? f[e] : all));
+      tmem_st8(trow + col_o + q * 8, o);
       tmem_wait_st();
     };
 #pragma unroll 1
-    for (long long at = plan.begin; at < plan.end;) {
+    for (long long at = group < active ? plan.begin : plan.end; at < plan.end;) {
       const Segment s = segment_at(a, plan, at);
       const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
-      auto out_row = [&](int row) { return out0 + (size_t)row_at[row] * DH; };
       const int live = s.r.count * a.G;          // rows with a token
       // ---- the query's parts: bf16, and e4m3 twice under a power of two
       {
         constexpr int kEach = DH / 8;            // threads per row, 8 elements each
-        const int c = tid % kEach;
+        const int c = key % kEach;
 #pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 128 / kEach) {
-          const int row = r0 + tid / kEach;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < live) x = *reinterpret_cast<const uint4*>(a.q + out_row(row) + c * 8);
-          uint32_t w[4] = {x.x, x.y, x.z, x.w}, most = 0, hi[2] = {0, 0}, lo[2] = {0, 0};
+        for (int r0 = 0; r0 < chunks * 8; r0 += 8 * kGroups) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
-          most = max(most & 0xffffu, most >> 16);
+          for (int r1 = 0; r1 < 8; r1 += 128 / kEach) {
+            const int row = r0 + group * 8 + r1 + key / kEach;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (row < live && r1 + key / kEach < 8)
+              x = *reinterpret_cast<const uint4*>(a.q + out0 + (size_t)row_at[row] * DH + c * 8);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, most = 0, hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-          for (int d = kEach / 2; d; d >>= 1) most = max(most, __shfl_xor_sync(~0u, most, d));
-          const int e = min(134 - (int)(most >> 7), 120);  // |q| 2^e below 256
-          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            for (int k = 0; k < 4; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
+            most = max(most & 0xffffu, most >> 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (a.negate) w[k] ^= 0x80008000u;
-            const float2 f = make_float2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
-            const uint32_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-            const __half2 b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
-            const float2 d = __half22float2(b);
-            const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(f.x - d.x, f.y - d.y), __NV_SATFINITE, __NV_E4M3);
-            hi[k >> 1] |= h << (16 * (k & 1));
-            lo[k >> 1] |= l << (16 * (k & 1));
+            for (int d = kEach / 2; d; d >>= 1) most = max(most, __shfl_xor_sync(~0u, most, d));
+            const int e = min(134 - (int)(most >> 7), 120);  // |q| 2^e below 256
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (a.negate) w[k] ^= 0x80008000u;
+              const float2 f = make_float2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+              const uint32_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+              const __half2 b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
+              const float2 d = __half22float2(b);
+              const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(f.x - d.x, f.y - d.y), __NV_SATFINITE, __NV_E4M3);
+              hi[k >> 1] |= h << (16 * (k & 1));
+              lo[k >> 1] |= l << (16 * (k & 1));
+            }
+            if (row >= rows || r1 + key / kEach >= 8) continue;
+            auto place = [&](int r) {
+              return DH == 128 ? r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8
+                               : r * 64 + (((c >> 1) ^ ((r >> 1) & 3)) << 4) + (c & 1) * 8;
+            };
+            *reinterpret_cast<uint2*>(q8 + place(row)) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(q8 + place(NP + row)) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint4*>(q16 + (c >> 3) * NP * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            if (c == 0)
+              row_c[row] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
           }
-          if (row >= rows) continue;
-          auto place = [&](int r) {
-            return DH == 128 ? r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8
-                             : r * 64 + (((c >> 1) ^ ((r >> 1) & 3)) << 4) + (c & 1) * 8;
-          };
-          *reinterpret_cast<uint2*>(q8 + place(row)) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(q8 + place(NP + row)) = make_uint2(lo[0], lo[1]);
-          *reinterpret_cast<uint4*>(q16 + (c >> 3) * NP * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-          if (c == 0)
-            row_c[row] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+          if (key < 8 && r0 + group * 8 < chunks * 8) row_nm[r0 + group * 8 + key] = -kNone;
         }
-        if (tid < NP) row_nm[tid] = -kNone;
-        if (tid >= rows && tid < NP) row_c[tid] = 0.f;
         fence_proxy_async_smem();
-        bar_softmax();
+        bar_group(group);
         if (lane == 0) mbar_arrive_cta(qready);
       }
       // ---- tiles
       // O holds sums of 2^(score - m) v 2^7 / vref
-      float vref = 0.f, ls[16] = {};
-      if (!SMALL) {
-        uint32_t zero[16] = {};
+      float vref = 0.f, unit = 0.f;              // (unit = 2^7 / vref)
+      float c[8], nm[8], ls[8];                  // of the chunk; the sums of SMALL
+      auto state = [&](int q) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(row_c + q * 8 + e);
+          const float4 w = *reinterpret_cast<const float4*>(row_nm + q * 8 + e);
+          c[e] = u.x, c[e + 1] = u.y, c[e + 2] = u.z, c[e + 3] = u.w;
+          nm[e] = w.x, nm[e + 1] = w.y, nm[e + 2] = w.z, nm[e + 3] = w.w;
+        }
+      };
+      if (SMALL) {
+        state(group);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ls[e] = 0.f;
+      } else {
+        const uint32_t zero[8] = {};
 #pragma unroll 1
-        for (int q = 0; q < chunks; ++q) tmem_st16(trow + col_l + q * 16, zero);
+        for (int q = group; q < chunks; q += kGroups) tmem_st8(trow + col_l + q * 8, zero);
         tmem_wait_st();
       }
       const float* kscale = a.k_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
       const float* vscale = a.v_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
       float ks = 1.f, vs = 1.f;                  // of the tile to come, the warp's 32 keys
       auto fetch = [&](const Walk& t) {
-        const int blk = min((t.p0 + warp * 32) >> shift, nblk - 1);
+        const int blk = min((t.p0 + w4 * 32) >> shift, nblk - 1);
         if (t.eight) {
           ks = kscale[blk];
           vs = vscale[blk];
@@ -847,146 +889,133 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Walk t = walk_from(s.r, a.window, s.i0);
       fetch(t);
-      float unit = 0.f;                          // 2^7 / vref
 #pragma unroll 1
       for (int i = 0; i < s.n; ++i, ++n) {
         const uint32_t buf = n & 1u;
-        const Walk now = t;
-        const bool edge = now.edge();
-        const float kc = ks, vc = now.eight ? vs : 1.f;
-        if (i + 1 < s.n) {
-          step(t, s.r, a.window);
-          fetch(t);
-        }
-        // the rows that see the thread's key: [r0, r1)
+        const bool eight = t.eight, edge = t.edge();
+        const float kc = ks, vc = eight ? vs : 1.f;
+        // the rows that see the thread's key: [r0, r1); the warp's scale passes vref
+        // (if any of its keys counts)
         int r0 = 0, r1 = NP;
-        if (edge) {
-          const int j = now.p0 + tid;
+        bool over = eight && fabsf(vc) > vref && fabsf(vc) < 0x1p100f;
+        if (seldom(edge)) {
+          const int j = t.p0 + key;
           r0 = max(j - s.r.length, 0) * a.G;
           r1 = live;
           if (a.window && j >= a.sinks) {
             const long long last = (long long)j + a.window - s.r.length;
             if (last < s.r.count) r1 = last < 0 ? 0 : (int)last * a.G;
           }
-          if (j < now.rs || j >= now.re) r1 = 0;
+          if (j < t.rs || j >= t.re) r1 = 0;
+          over = over && t.p0 + w4 * 32 < t.re && t.p0 + w4 * 32 + 32 > t.rs;
+        }
+        if (i + 1 < s.n) {
+          step(t, s.r, a.window);
+          fetch(t);
         }
         wait_w(&sfull[buf], (n >> 1) & 1u);
         if (lay.p_bufs == 1 && n > 0) wait_values(n);  // P's only place is free
-        // the warp's scale passes vref (if any of its keys counts)
-        const bool over = now.eight && fabsf(vc) > vref && fabsf(vc) < 0x1p100f && now.p0 + warp * 32 < now.re &&
-                          now.p0 + warp * 32 + 32 > now.rs;
         float pv = vc * unit;
-        unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + tid * 32;
+        unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
 #pragma unroll 1
-        for (int q = 0; q < chunks; ++q) {
-          uint32_t x[16], y[16];
-          const uint32_t scol = trow + buf * scols + q * 16;
-          tmem_ld16_nw(scol, x);
-          tmem_ld16_nw(SMALL ? scol + 16 : trow + col_l + q * 16, y);
-          float c[16], nm[16];
+        for (int q = group; q < chunks; q += kGroups) {
+          uint32_t x[8], y[8];
+          const uint32_t scol = trow + buf * scols + q * 8;
+          tmem_ld8_nw(scol, x);
+          tmem_ld8_nw(SMALL ? scol + 16 : trow + col_l + q * 8, y);
+          if (!SMALL) state(q);
+          float f[8], d[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(row_c + q * 16 + e);
-            const float4 w = *reinterpret_cast<const float4*>(row_nm + q * 16 + e);
-            c[e] = u.x, c[e + 1] = u.y, c[e + 2] = u.z, c[e + 3] = u.w;
-            nm[e] = w.x, nm[e + 1] = w.y, nm[e + 2] = w.z, nm[e + 3] = w.w;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) c[e] = now.eight ? c[e] * kc : a.scale_log2;
-          tmem_wait_ld();
-          tmem_pin16(x);
-          tmem_pin16(y);
-          const int m0 = max(r0 - q * 16, 0), m1 = min(r1 - q * 16, 16);
+          for (int e = 0; e < 8; ++e) f[e] = eight ? c[e] * kc : a.scale_log2;
+          const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
           const uint32_t seen = m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
-          float d[16];
+          tmem_wait_ld();
+          tmem_pin8(x);
+          tmem_pin8(y);
+          if (SMALL && eight)                    // the low part's product
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
           auto below = [&]() {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              d[e] = fmaf(__uint_as_float(x[e]), c[e], nm[e]);
-              if (edge && !((seen >> e) & 1u)) d[e] = -INFINITY;
-            }
+            for (int e = 0; e < 8; ++e) d[e] = fmaf(__uint_as_float(x[e]), f[e], nm[e]);
+            if (seldom(edge))
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (!((seen >> e) & 1u)) d[e] = -INFINITY;
           };
-          if (SMALL && now.eight)                // the low part's product
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
           below();
-          float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) top[(e >> 1) & 1] = tree_max3(top[(e >> 1) & 1], d[e], d[e + 1]);
-          if (any_softmax(fmaxf(top[0], top[1]) > kRaise || (over && q == 0) || vref == 0.f)) {
-            if (q == 0) {
+          const float top = tree_max3(tree_max3(d[0], d[1], d[2]), tree_max3(d[3], d[4], d[5]), fmaxf(d[6], d[7]));
+          if (seldom(any_group(group, top > kRaise || over || vref == 0.f))) {
+            if (q == group) {
               // the largest of the four warps' scales
-              bar_softmax();
-              if (lane == 0) part[warp] = over ? fabsf(vc) : 0.f;
-              bar_softmax();
-              const float most = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+              if (lane == 0) gpart[w4] = over ? fabsf(vc) : 0.f;
+              bar_group(group);
+              const float most = fmaxf(fmaxf(gpart[0], gpart[1]), fmaxf(gpart[2], gpart[3]));
               if (most > vref || vref == 0.f) {
                 const float next = most > 0.f ? power_above(most) * 4.f : 1.f;
                 if (i > 0) {
                   wait_values(n);
 #pragma unroll 1
-                  for (int z = 0; z < chunks; ++z) rescale(col_o + z * 16, nullptr, vref / next);
+                  for (int z = group; z < chunks; z += kGroups) rescale(z, nullptr, vref / next);
                 }
                 vref = next;
                 unit = 0x1p7f / next;
                 pv = vc * unit;
               }
-              bar_softmax();
+              over = false;
+              bar_group(group);
             }
             // the rows' largest scores of all keys; those that pass m + 8 become m
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              d[e] = edge && !((seen >> e) & 1u) ? -INFINITY : __uint_as_float(x[e]) * c[e];
+            for (int e = 0; e < 8; ++e)
+              d[e] = edge && !((seen >> e) & 1u) ? -INFINITY : __uint_as_float(x[e]) * f[e];
             over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
-            if (!(lane & 1)) part[warp * 32 + (lane >> 1)] = d[0];
-            bar_softmax();
-            if (tid < 16) {
-              const float old = -row_nm[q * 16 + tid];
-              const float z = fmaxf(fmaxf(part[tid], part[32 + tid]), fmaxf(part[64 + tid], part[96 + tid]));
+            if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = d[0];
+            bar_group(group);
+            if (key < 8) {
+              const float old = -row_nm[q * 8 + key];
+              const float z = fmaxf(fmaxf(gpart[key], gpart[8 + key]), fmaxf(gpart[16 + key], gpart[24 + key]));
               const float m = z > old + kRaise ? z : old;
-              row_f[q * 16 + tid] = tree_ex2(old - m);
-              row_nm[q * 16 + tid] = -m;
+              row_f[q * 8 + key] = tree_ex2(old - m);
+              row_nm[q * 8 + key] = -m;
             }
-            bar_softmax();
-            float f[16];
+            bar_group(group);
+            float g[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              f[e] = row_f[q * 16 + e];
-              nm[e] = row_nm[q * 16 + e];
-              if (SMALL) ls[e] *= f[e];
-              else y[e] = __float_as_uint(__uint_as_float(y[e]) * f[e]);
+            for (int e = 0; e < 8; ++e) {
+              g[e] = row_f[q * 8 + e];
+              nm[e] = row_nm[q * 8 + e];
+              if (SMALL) ls[e] *= g[e];
+              else y[e] = __float_as_uint(__uint_as_float(y[e]) * g[e]);
             }
             if (i > 0) {
               wait_values(n);                    // O as the tile before left it
-              rescale(col_o + q * 16, f, 1.f);
+              rescale(q, g, 1.f);
             }
             below();
           }
-          uint32_t pk[8];
-          auto weights = [&](auto eight) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float p0 = tree_ex2(d[e]), p1 = tree_ex2(d[e + 1]);
-              if (SMALL) {
-                ls[e] += p0;
-                ls[e + 1] += p1;
-              } else {
-                y[e] = __float_as_uint(__uint_as_float(y[e]) + p0);
-                y[e + 1] = __float_as_uint(__uint_as_float(y[e + 1]) + p1);
-              }
-              pk[e / 2] = decltype(eight)::value ? pack_f16x2(p0 * pv, p1 * pv) : pack_bf16x2(p0 * pv, p1 * pv);
-            }
-          };
-          if (now.eight) weights(std::true_type());
-          else weights(std::false_type());
-          if (edge)                              // (a scale that is none of the row's)
+          for (int e = 0; e < 8; ++e) {
+            d[e] = tree_ex2(d[e]);
+            if (SMALL) ls[e] += d[e];
+            else y[e] = __float_as_uint(__uint_as_float(y[e]) + d[e]);
+            d[e] *= pv;
+          }
+          uint32_t pk[4];
+          if (!seldom(!eight)) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 2)
+            for (int e = 0; e < 4; ++e) pk[e] = pack_f16x2(d[2 * e], d[2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+          }
+          if (seldom(edge))                      // (a scale that is none of the row's)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
               pk[e / 2] &= ((seen >> e) & 1u ? 0x0000ffffu : 0u) | ((seen >> e) & 2u ? 0xffff0000u : 0u);
-          const int flip = ((tid >> 2) & 1) << 4;
-          *reinterpret_cast<uint4*>(pto + q * kPanel + flip) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(pto + q * kPanel + (16 ^ flip)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          if (!SMALL) tmem_st16(trow + col_l + q * 16, y);
+          *reinterpret_cast<uint4*>(pto + (q >> 1) * kPanel + (((q & 1) ^ ((key >> 2) & 1)) << 4)) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          if (!SMALL) tmem_st8(trow + col_l + q * 8, y);
         }
         if (!SMALL) tmem_wait_st();
         fence_proxy_async_smem();
@@ -1000,55 +1029,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
       if (!s.whole && !s.head)                   // which CTA has the pair's last tile
         go_on = make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0);
-      // the sums over the keys: a warp's, then the four warps'
 #pragma unroll 1
-      for (int q = 0; q < chunks; ++q) {
-        float v[16];
-        if (SMALL) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = ls[e];
-        } else {
-          uint32_t y[16];
-          tmem_ld16_nw(trow + col_l + q * 16, y);
+      for (int q = group; q < chunks; q += kGroups) {
+        // the sums over the keys: a warp's, then the four warps'
+        if (!SMALL) {
+          uint32_t y[8];
+          tmem_ld8_nw(trow + col_l + q * 8, y);
           tmem_wait_ld();
-          tmem_pin16(y);
+          tmem_pin8(y);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(y[e]);
+          for (int e = 0; e < 8; ++e) ls[e] = __uint_as_float(y[e]);
         }
-        over_lanes(v, [](float u, float w) { return u + w; });
-        if (!(lane & 1)) part[warp * 32 + (lane >> 1)] = v[0];
-        bar_softmax();
-        if (tid < 16) {
-          const int row = q * 16 + tid;
-          const float l = (part[tid] + part[32 + tid]) + (part[64 + tid] + part[96 + tid]);
+        over_lanes(ls, [](float u, float w) { return u + w; });
+        if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = ls[0];
+        bar_group(group);
+        if (key < 8) {
+          const int row = q * 8 + key;
+          const float l = (gpart[key] + gpart[8 + key]) + (gpart[16 + key] + gpart[24 + key]);
           row_f[row] = row < live ? 0x1p-7f * vref * (!s.whole ? 1.f : l != 0.f ? 1.f / l : 0.f) : 0.f;
           if (!s.whole && row < rows) {
             a.part_m[slot * rows + row] = -row_nm[row];
             a.part_l[slot * rows + row] = row < live ? l : 0.f;
           }
         }
-        bar_softmax();
-        if (DH == 128 || warp < 2) {
-          const int most = min(16, rows - q * 16);
-          bf16* out = a.out + out0 + tid;
-          float* po = a.part_o + (slot * rows + q * 16) * DH + tid;
-#pragma unroll 1
-          for (int e0 = 0; e0 < most; e0 += 4) {
-            float o[4];
-            tmem_ld4(trow + col_o + q * 16 + e0, o);
+        bar_group(group);
+        if (DH == 128 || w4 < 2) {
+          const int most = min(8, rows - q * 8);
+          bf16* out = a.out + out0 + key;
+          float* po = a.part_o + (slot * rows + q * 8) * DH + key;
+          uint32_t o[8];
+          tmem_ld8_nw(trow + col_o + q * 8, o);
+          tmem_wait_ld();
+          tmem_pin8(o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int row = q * 16 + e0 + e;
-              const float w = row < live ? o[e] * row_f[row] : 0.f;
-              if (row < rows && s.whole) out[row_at[row] * DH] = __float2bfloat16(w);
-              if (row < rows && !s.whole) po[(e0 + e) * DH] = w;
-            }
+          for (int e = 0; e < 8; ++e) {
+            const int row = q * 8 + e;
+            const float w = row < live ? __uint_as_float(o[e]) * row_f[row] : 0.f;
+            if (row < rows && s.whole) out[row_at[row] * DH] = __float2bfloat16(w);
+            if (row < rows && !s.whole) po[e * DH] = w;
           }
           if (bad)                               // what the products left out
 #pragma unroll 1
-            for (int e = 0; e < min(most, live - q * 16); ++e) {
-              const int row = q * 16 + e;
-              const float w = not_finite(a, s, s.r.length + row / a.G, tid);
+            for (int e = 0; e < min(most, live - q * 8); ++e) {
+              const int row = q * 8 + e;
+              const float w = not_finite(a, s, s.r.length + row / a.G, key);
               if (s.whole) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
               else po[e * DH] += w;
             }
@@ -1129,7 +1153,7 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  cache_attn_tc_kernel<DH, SMALL><<<a.ctas, kThreads, lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
+  cache_attn_tc_kernel<DH, SMALL><<<a.ctas, threads_of(SMALL), lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
