@@ -282,7 +282,7 @@ ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* pare
  * (bf16 [B][T][H][dh]), bf16(k) and bf16(v) to their rows.  A token that a
  * sequence does not have (t >= counts[b], or lengths[b] below 0 or beyond
  * 2^31 - 1 - T) has zeros in q_out and no row.  Other rows stay as they are.
- * 1 <= T <= rows.  A token's results do not depend on the other tokens. */
+ * 1 <= T <= rows; B T (H + 2 Hkv) dh <= 2^38.  A token's results do not depend on the other tokens. */
 ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int32_t* lengths,
                               const int32_t* counts, const int32_t* positions,
                               const float* q_gain, const float* k_gain, float eps, float theta,
@@ -352,7 +352,7 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
  * tokens int32 [B][d + 1] = the accepted drafts, the drawn token, then -1;
  * n int32 [B] = the number of them (no drawn token where p_j has no entry over 0,
  * or an infinite one).  d >= 0 (0: one draw from p; q, drafts and accept_u are not
- * read), d <= 1024, V >= 1; 4-byte alignment. */
+ * read), d <= 1024, 1 <= V <= 2^30; 4-byte alignment. */
 ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* drafts,
                                 const int32_t* counts, const float* accept_u,
                                 const float* sample_u, int32_t B, int32_t d, int32_t V,

@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "batch.cuh"
+#include "tree.cuh"
 
 namespace ssd {
 namespace {
@@ -32,13 +33,23 @@ SSD_DI uint32_t abs_finite(uint32_t x) {         // of two bf16: |x|'s bits, 0 i
   if (x >= 0x7f800000u) x &= 0xffffu;
   return x;
 }
-
-SSD_DI uint32_t eight_of(float x, float inv) {
-  return isfinite(x) ? __nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3) : 0x7fu;
+// Two bf16 times inv as two e4m3; what is not finite as NaN.
+SSD_DI uint32_t two_of(uint32_t x, float inv) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(x) * inv, bf16_hi(x) * inv), __NV_SATFINITE, __NV_E4M3);
+}
+SSD_DI uint32_t two_any(uint32_t x, float inv) {
+  uint32_t r = two_of(x, inv);
+  if ((x & 0x7f80u) == 0x7f80u) r |= 0x7fu;
+  if ((x & 0x7f800000u) == 0x7f800000u) r |= 0x7f00u;
+  return r;
+}
+SSD_DI uint32_t largest(uint32_t most) {         // over a warp, of packed pairs
+  return __reduce_max_sync(~0u, max(most & 0xffffu, most >> 16));
 }
 
 // Items = (sequence, block, K or V, head), dealt to the CTAs in turn; a CTA has
 // a block in registers: one read, one write.
+template <int DH, int UNITS>                     // 16-byte units of a block per thread
 __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_constant__ QuantizeArgs a) {
   __shared__ int first[kBatchMaxSeqs + 1];       // blocks of all sequences before b
   __shared__ uint32_t warp_max[kThreads / 32];
@@ -66,7 +77,6 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
   }
   __syncthreads();
   const int total = first[a.B], per = 2 * a.Hkv;
-  const int units = a.block * a.dh / 8;          // of 16 bytes
   for (long long item = blockIdx.x; item < (long long)total * per; item += gridDim.x) {
     const int j = (int)(item / per), rest = (int)(item - (long long)j * per);
     const bool is_v = rest >= a.Hkv;
@@ -81,28 +91,38 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
     blocks_of(a, lo, from, to);
     const int block = from + j - first[lo];
     const size_t row0 = (size_t)block * a.block;
-    const bf16* src = (is_v ? a.v : a.k) + (size_t)lo * a.seq_stride + (size_t)h * a.rows * a.dh;
-    uint4 x[8];
+    const bf16* src = (is_v ? a.v : a.k) + (size_t)lo * a.seq_stride + (size_t)h * a.rows * DH;
+    // (a block turns over at the ring's end once at most)
+    const int slot0 = (int)((unsigned)row0 % (unsigned)a.rows);
+    uint4 x[UNITS];
     uint32_t most = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int u = tid + q * kThreads;
-      x[q] = make_uint4(0u, 0u, 0u, 0u);
-      if (u < units) {
-        const size_t e = (size_t)u * 8, row = (row0 + e / a.dh) % a.rows;
-        x[q] = *reinterpret_cast<const uint4*>(src + row * a.dh + e % a.dh);
-      }
+    for (int q = 0; q < UNITS; ++q) {
+      const int e = (tid + q * kThreads) * 8, at = slot0 + e / DH;
+      x[q] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(at < a.rows ? at : at - a.rows) * DH + e % DH));
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      most = __vmaxu2(__vmaxu2(most, __vmaxu2(abs_finite(x[q].x), abs_finite(x[q].y))),
-                      __vmaxu2(abs_finite(x[q].z), abs_finite(x[q].w)));
-    most = max(most & 0xffffu, most >> 16);
-    most = __reduce_max_sync(~0u, most);
+    for (int q = 0; q < UNITS; ++q)
+      most = __vmaxu2(__vmaxu2(most, __vmaxu2(x[q].x & 0x7fff7fffu, x[q].y & 0x7fff7fffu)),
+                      __vmaxu2(x[q].z & 0x7fff7fffu, x[q].w & 0x7fff7fffu));
+    most = largest(most);
     __syncthreads();                             // (the item before has read)
     if (lane == 0) warp_max[warp] = most;
     __syncthreads();
     most = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[lane] : 0u);
+    const bool odd = most >= 0x7f80u;            // something is not finite: without it
+    if (odd) {
+      most = 0;
+#pragma unroll
+      for (int q = 0; q < UNITS; ++q)
+        most = __vmaxu2(__vmaxu2(most, __vmaxu2(abs_finite(x[q].x), abs_finite(x[q].y))),
+                        __vmaxu2(abs_finite(x[q].z), abs_finite(x[q].w)));
+      most = largest(most);
+      __syncthreads();
+      if (lane == 0) warp_max[warp] = most;
+      __syncthreads();
+      most = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[lane] : 0u);
+    }
     float scale = 1.f;
     int e = 0;
     if (most) {
@@ -111,20 +131,31 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
       scale = ldexpf(1.f, e);
     }
     const float inv = ldexpf(1.f, -e);
-    uint8_t* dst = (is_v ? a.v8 : a.k8) + (size_t)lo * a.seq8_stride + ((size_t)h * a.max_seq + row0) * a.dh;
+    uint8_t* dst = (is_v ? a.v8 : a.k8) + (size_t)lo * a.seq8_stride + ((size_t)h * a.max_seq + row0) * DH;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < UNITS; ++q) {
       const int u = tid + q * kThreads;
-      if (u >= units) continue;
-      auto four = [&](uint32_t s, uint32_t t) {
-        return eight_of(bf16_lo(s), inv) | eight_of(bf16_hi(s), inv) << 8 | eight_of(bf16_lo(t), inv) << 16 |
-               eight_of(bf16_hi(t), inv) << 24;
-      };
-      *reinterpret_cast<uint2*>(dst + (size_t)u * 8) = make_uint2(four(x[q].x, x[q].y), four(x[q].z, x[q].w));
+      uint2 y;
+      if (!odd)
+        y = make_uint2(two_of(x[q].x, inv) | two_of(x[q].y, inv) << 16, two_of(x[q].z, inv) | two_of(x[q].w, inv) << 16);
+      else
+        y = make_uint2(two_any(x[q].x, inv) | two_any(x[q].y, inv) << 16,
+                       two_any(x[q].z, inv) | two_any(x[q].w, inv) << 16);
+      *reinterpret_cast<uint2*>(dst + (size_t)u * 8) = y;
     }
     if (tid == 0)
       (is_v ? a.v_scale : a.k_scale)[(size_t)lo * a.scale_stride + (size_t)h * (a.max_seq / a.block) + block] = scale;
   }
+}
+
+template <int DH>
+cudaError_t launch(const QuantizeArgs& a, unsigned ctas, cudaStream_t s) {
+  switch (a.block) {
+    case 32: cache_quantize_kernel<DH, 32 * DH / 8 / kThreads><<<ctas, kThreads, 0, s>>>(a); break;
+    case 64: cache_quantize_kernel<DH, 64 * DH / 8 / kThreads><<<ctas, kThreads, 0, s>>>(a); break;
+    default: cache_quantize_kernel<DH, 128 * DH / 8 / kThreads><<<ctas, kThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -132,9 +163,8 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
 cudaError_t launch_cache_quantize(const QuantizeArgs& a, cudaStream_t s) {
   // at most so many items, and eight CTAs for each SM
   const long long most = (long long)a.B * 2 * a.Hkv * ((a.rows < a.max_seq ? a.rows : a.max_seq) / a.block + 1);
-  const long long ctas = most < 8 * 152 ? most : 8 * 152;
-  cache_quantize_kernel<<<dim3((unsigned)ctas), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const unsigned ctas = (unsigned)(most < 8 * tree_sms() ? most : 8 * tree_sms());
+  return a.dh == 128 ? launch<128>(a, ctas, s) : launch<64>(a, ctas, s);
 }
 
 }  // namespace ssd

@@ -660,6 +660,7 @@ ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int3
   if (T < 1 || T > rows || H < 1 || H > 65536 || !(theta > 0.f) || !std::isfinite(theta) || !(eps >= 0.f) ||
       !std::isfinite(eps))
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append: T / H / theta / eps");
+  if ((double)B * T * ((double)H + 2 * Hkv) * dh > 0x1p38) return op_fail(SSD_ERR_INVALID_ARG, "rope_append: too many tokens");
   if (!al16(qkv) || !al16(q_out) || !al4(lengths) || (counts && !al4(counts)) || (positions && !al4(positions)) ||
       (q_gain && !al16(q_gain)) || (k_gain && !al16(k_gain)))
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append pointers");
@@ -812,7 +813,7 @@ ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* d
                                 const int32_t* counts, const float* accept_u,
                                 const float* sample_u, int32_t B, int32_t d, int32_t V,
                                 int32_t* tokens, int32_t* n, void* stream) {
-  if (B < 1 || B > kBatchMaxSeqs || d < 0 || d > 1024 || V < 1)
+  if (B < 1 || B > kBatchMaxSeqs || d < 0 || d > 1024 || V < 1 || V > (1 << 30))
     return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts sizes");
   if (!al4(p) || (q && !al4(q)) || (d && (!al4(drafts) || !al4(accept_u))) || (counts && !al4(counts)) ||
       !al4(sample_u) || !al4(tokens) || !al4(n))

@@ -22,90 +22,97 @@ SSD_DI float2 turn_of(int64_t pos, uint64_t frequency) {
   return r;
 }
 
-SSD_DI void load_pair(const float* p, float (&x)[4], int half) {
-  const float2 a = *reinterpret_cast<const float2*>(p), b = *reinterpret_cast<const float2*>(p + half);
-  x[0] = a.x;
-  x[1] = a.y;
-  x[2] = b.x;
-  x[3] = b.y;
+SSD_DI void load_quads(const float* p, float (&x)[8], int half) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + half);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// A warp takes one token and `kHeads` groups of heads; a lane two pairs of
-// (i, i + dh/2) of a head, so that a warp holds 128 / dh heads at a time and
-// needs no barrier.  The loads of all its heads go out before the first use.
-template <int DH, int kHeads>
+// A warp takes one token and `kSteps` times as many heads as it holds at once (256
+// elements): a lane has four pairs (i, i + dh/2) of a head, and needs their four
+// angles once.  No barrier; the next step's loads go out before this one's work.
+template <int DH, int kSteps, bool NORMS>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
-  constexpr int kLanes = DH / 4, kAtOnce = 32 / kLanes, kHalf = DH / 2;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, i = 2 * (lane % kLanes);
-  const int heads = a.H + 2 * a.Hkv, groups = (heads + kAtOnce * kHeads - 1) / (kAtOnce * kHeads);
-  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long token = w / groups;
-  const int h0 = (int)(w - token * groups) * kAtOnce * kHeads + sub;
-  if (token >= (long long)a.B * a.T) return;
-  const int b = (int)(token / a.T), t = (int)(token - (long long)b * a.T);
-  float x[kHeads][4];
-#pragma unroll
-  for (int q = 0; q < kHeads; ++q) {
-    const int h = h0 + q * kAtOnce;
-    if (h < heads) load_pair(a.qkv + (size_t)token * heads * DH + (size_t)h * DH + i, x[q], kHalf);
-  }
+  constexpr int kLanes = DH / 8, kAtOnce = 32 / kLanes, kHalf = DH / 2;
+  const int lane = threadIdx.x & 31, i = 4 * (lane % kLanes);
+  const int heads = a.H + 2 * a.Hkv, groups = (heads + kAtOnce * kSteps - 1) / (kAtOnce * kSteps);
+  const unsigned w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const unsigned token = w / groups;
+  if (token >= (unsigned)(a.B * a.T)) return;
+  int h = (int)(w - token * groups) * kAtOnce * kSteps + lane / kLanes;
+  const int b = (int)(token / (unsigned)a.T), t = (int)(token - (unsigned)b * a.T);
+  const float* src = a.qkv + ((size_t)token * heads + h) * DH + i;
+  float x[8], next[8] = {};
+  if (h < heads) load_quads(src, next, kHalf);
   const int n = a.lengths[b];
   const bool here = t < batch_count(a.counts, a.lengths, b, a.T);
   const int64_t pos = (int64_t)(a.positions ? a.positions[b] : n) + t;
-  const float2 r0 = turn_of(pos, a.turns[i]), r1 = turn_of(pos, a.turns[i + 1]);
-  const size_t slot = here ? (size_t)((n + t) % a.rows) : 0;
+  float2 r[4];
 #pragma unroll
-  for (int q = 0; q < kHeads; ++q) {
-    const int h = h0 + q * kAtOnce;
-    float(&y)[4] = x[q];
-    const float* gain = h < a.H ? a.q_gain : h < a.H + a.Hkv ? a.k_gain : nullptr;
-    float ss = h < heads ? y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3] : 0.f;
-    if (a.q_gain || a.k_gain)
+  for (int e = 0; e < 4; ++e) r[e] = turn_of(pos, a.turns[i + e]);
+  const size_t row = (size_t)b * a.seq_stride + (size_t)(here ? (n + t) % a.rows : 0) * DH + i;
+#pragma unroll 1
+  for (int step = 0; step < kSteps; ++step, h += kAtOnce) {
+    if (NORMS ? h - lane / kLanes >= heads : h >= heads) break;
+    src += kAtOnce * DH;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = next[e];
+    if (step + 1 < kSteps && h + kAtOnce < heads) load_quads(src, next, kHalf);
+    if (NORMS) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
       for (int d = kLanes / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (h >= heads) continue;
-    if (gain) {
-      const float s = 1.f / sqrtf(ss * (1.f / DH) + a.eps);
-      float g[4];
-      load_pair(gain + i, g, kHalf);
+      const float* gain = h < a.H ? a.q_gain : h < a.H + a.Hkv ? a.k_gain : nullptr;
+      if (gain) {
+        const float scale = rsqrtf(fmaf(ss, 1.f / DH, a.eps));
+        float g[8];
+        load_quads(gain + i, g, kHalf);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= s * g[e];
+        for (int e = 0; e < 8; ++e) x[e] *= scale * g[e];
+      }
+      if (h >= heads) continue;
     }
-    if (h < a.H + a.Hkv) {
-      const float u0 = y[0] * r0.x - y[2] * r0.y, u1 = y[1] * r1.x - y[3] * r1.y;
-      y[2] = y[2] * r0.x + y[0] * r0.y;
-      y[3] = y[3] * r1.x + y[1] * r1.y;
-      y[0] = u0;
-      y[1] = u1;
-    }
+    if (h < a.H + a.Hkv)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[e] * r[e].x - x[e + 4] * r[e].y;
+        x[e + 4] = x[e + 4] * r[e].x + x[e] * r[e].y;
+        x[e] = u;
+      }
     bf16* to;
     if (h < a.H) {
-      to = a.q + ((size_t)token * a.H + h) * DH;
-      if (!here) y[0] = y[1] = y[2] = y[3] = 0.f;
+      to = a.q + ((size_t)token * a.H + h) * DH + i;
+      if (!here)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
     } else {
       if (!here) continue;
-      const bool is_k = h < a.H + a.Hkv;
-      const int kvh = h - a.H - (is_k ? 0 : a.Hkv);
-      to = (is_k ? a.k : a.v) + (size_t)b * a.seq_stride + ((size_t)kvh * a.rows + slot) * DH;
+      to = (h < a.H + a.Hkv ? a.k : a.v) + row + (size_t)(h - a.H - (h < a.H + a.Hkv ? 0 : a.Hkv)) * a.rows * DH;
     }
-    *reinterpret_cast<uint32_t*>(to + i) = pack_bf16x2(y[0], y[1]);
-    *reinterpret_cast<uint32_t*>(to + kHalf + i) = pack_bf16x2(y[2], y[3]);
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    *reinterpret_cast<uint2*>(to + kHalf) = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
 }
 
-template <int DH, int kHeads>
+template <int DH, int kSteps>
 cudaError_t launch(const RopeAppendArgs& a, cudaStream_t s) {
-  constexpr int kEach = 128 / DH * kHeads;
+  constexpr int kEach = 256 / DH * kSteps;
   const long long warps = (long long)a.B * a.T * ((a.H + 2 * a.Hkv + kEach - 1) / kEach);
-  const long long ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  rope_append_kernel<DH, kHeads><<<dim3((unsigned)ctas), kThreads, 0, s>>>(a);
+  const unsigned ctas = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+  if (a.q_gain || a.k_gain) rope_append_kernel<DH, kSteps, true><<<ctas, kThreads, 0, s>>>(a);
+  else rope_append_kernel<DH, kSteps, false><<<ctas, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s) {
-  return a.dh == 128 ? launch<128, 4>(a, s) : launch<64, 4>(a, s);
+  // few tokens: a warp for every 256 elements; many: the angles serve 8 times that
+  const bool many = (long long)a.B * a.T * (a.H + 2 * a.Hkv) * a.dh >= (long long)1 << 22;
+  if (a.dh == 128) return many ? launch<128, 8>(a, s) : launch<128, 1>(a, s);
+  return many ? launch<64, 8>(a, s) : launch<64, 1>(a, s);
 }
 
 }  // namespace ssd

@@ -11,6 +11,7 @@
 #include <cooperative_groups.h>
 
 #include "batch.cuh"
+#include "tree.cuh"
 
 namespace ssd {
 namespace {
@@ -19,7 +20,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 // s + e = a + b exactly.
 SSD_DI void two_sum(float a, float b, float& s, float& e) {
@@ -34,87 +35,123 @@ SSD_DI void rest_of(float p, float q, float& r, float& e) {
   if (!(r > 0.f)) r = e = 0.f;                   // (NaN too)
 }
 
+// Sum over the warp's lower lanes and itself, in 64 bits.
+SSD_DI double scan(double x, int lanes) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    if (d >= lanes) break;
+    const double y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// The row that a token is drawn from: max(p - q, 0), p, or p without one token.
+struct Rest {
+  const float *p, *q;
+  int out;
+  SSD_DI void entry(int v, float& r, float& e) const { rest_of(p[v], q ? q[v] : v == out ? p[v] : 0.f, r, e); }
+};
+
+constexpr int kBatch = 16;                       // entries of a lane in flight at once
+
+// A lane's sum over the entries v0 + k step < v1, k < kBatch.
+SSD_DI void add_batch(const Rest& rest, int v0, int step, int v1, float& s, float& c) {
+  float p[kBatch], q[kBatch];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int v = v0 + k * step;
+    p[k] = v < v1 ? rest.p[v] : 0.f;
+    q[k] = v < v1 && rest.q ? rest.q[v] : v == rest.out ? p[k] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    float r, e, t;
+    rest_of(p[k], q[k], r, e);
+    two_sum(s, r, s, t);
+    c += t + e;
+  }
+}
+
 // A cluster per sequence, a slice of the vocabulary per CTA and a run of it per
-// warp.  Each CTA tests the drafts by itself; the sums meet once.
+// warp.  Each CTA tests the drafts by itself; the sums meet once.  Then one warp
+// walks its run again, 16 entries in a row to a lane.
+// Bound by latency: the drafts, their probabilities, the row's entries, the
+// cluster's exchange and the walk one behind the other.
 __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ int s_taken;
-  __shared__ double s_warp[kWarps];
-  __shared__ double s_cta[2][kMaxCluster];       // each CTA's sum, from the CTAs themselves
   cluster.barrier_arrive();                      // (all CTAs run before one writes to another)
+  __shared__ int s_taken;
+  __shared__ double s_warp[kWarps];              // sums of the warps, then of those up to each
+  __shared__ double s_cta[2][kMaxCluster];       // each CTA's sum, from the CTAs themselves
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / size;
   const int count = a.counts ? min(max(a.counts[b], 0), a.d) : a.d;
   if (tid == 0) s_taken = count;
+  const float sample = a.sample_u[b];
   __syncthreads();
   for (int j = tid; j < count; j += kThreads) {
+    const float u = a.accept_u[(size_t)b * a.d + j];
     const int y = a.drafts[(size_t)b * a.d + j];
     bool good = y >= 0 && y < a.V;
     if (good) {
-      const double p = a.p[((size_t)b * (a.d + 1) + j) * a.V + y];
-      const double q = a.q ? a.q[((size_t)b * a.d + j) * a.V + y] : 1.f;
-      good = (double)a.accept_u[(size_t)b * a.d + j] * q < p;
+      const float p = a.p[((size_t)b * (a.d + 1) + j) * a.V + y];
+      const float q = a.q ? a.q[((size_t)b * a.d + j) * a.V + y] : 1.f;
+      good = (double)u * (double)q < (double)p;
     }
     if (!good) atomicMin(&s_taken, j);
   }
   __syncthreads();
   const int taken = s_taken;
-  const float* p = a.p + ((size_t)b * (a.d + 1) + taken) * a.V;
-  const float* q = a.q && taken < count ? a.q + ((size_t)b * a.d + taken) * a.V : nullptr;
-  // without probabilities of the drafts the rejected token alone is left out
-  const int out = !a.q && taken < count ? a.drafts[(size_t)b * a.d + taken] : -1;
   bool plain = taken == count;                   // r = p
-  const int slice = (a.V + size - 1) / size, lo = min(rank * slice, a.V), hi = min(lo + slice, a.V);
+  Rest rest;
+  rest.p = a.p + ((size_t)b * (a.d + 1) + taken) * a.V;
+  rest.q = a.q && !plain ? a.q + ((size_t)b * a.d + taken) * a.V : nullptr;
+  // without probabilities of the drafts the rejected token alone is left out
+  rest.out = !a.q && !plain ? a.drafts[(size_t)b * a.d + taken] : -1;
+  const int slice = (a.V + size - 1) / size, lo = (int)min((long long)rank * slice, (long long)a.V);
+  const int hi = min(lo, a.V - slice) + slice;
   const int run = (hi - lo + kWarps - 1) / kWarps, w0 = min(lo + warp * run, hi), w1 = min(w0 + run, hi);
-  auto entry = [&](int v, float& r, float& e) {
-    rest_of(p[v], plain ? 0.f : q ? q[v] : v == out ? p[v] : 0.f, r, e);
-  };
   double total = 0.0, before = 0.0, mine = 0.0;
-  int last = -1;                                 // the last CTA with anything
-  for (int turn = 0; turn < 2; ++turn) {
+  int owner = -1, turn = 0;
+  while (true) {
     float s = 0.f, c = 0.f;
-#pragma unroll 4
-    for (int v = w0 + lane; v < w1; v += 32) {
-      float r, e, t;
-      entry(v, r, e);
-      two_sum(s, r, s, t);
-      c += t + e;
-    }
+#pragma unroll 1
+    for (int v = w0 + lane; v - lane < w1; v += 32 * kBatch) add_batch(rest, v, 32, w1, s, c);
     double x = (double)s + (double)c;
 #pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
     if (lane == 0) s_warp[warp] = x;
     __syncthreads();
-    mine = 0.0;
-    for (int i = 0; i < kWarps; ++i) mine += s_warp[i];
-    if (turn == 0) cluster.barrier_wait();
-    if (tid < size) cluster.map_shared_rank(&s_cta[turn][rank], tid)[0] = mine;
-    cluster.sync();
-    total = 0.0;
-    last = -1;
-    for (int i = 0; i < size; ++i) {
-      if (i == rank) before = total;
-      total += s_cta[turn][i];
-      if (s_cta[turn][i] > 0.0) last = i;
+    if (warp == 0) {
+      const double up = scan(lane < kWarps ? s_warp[lane] : 0.0, kWarps);
+      mine = __shfl_sync(~0u, up, kWarps - 1);
+      if (turn == 0) cluster.barrier_wait();
+      if (lane < size) *cluster.map_shared_rank(&s_cta[turn][rank], lane) = mine;
+      __syncwarp();
+      if (lane < kWarps) s_warp[lane] = up;
+    } else if (turn == 0) {
+      cluster.barrier_wait();
     }
+    cluster.sync();
+    // the first CTA whose sums pass the target, or the last that has any
+    const double sums = scan(lane < size ? s_cta[turn][lane] : 0.0, kMaxCluster);
+    total = __shfl_sync(~0u, sums, size - 1);
+    const unsigned any = __ballot_sync(~0u, lane < size && s_cta[turn][lane < size ? lane : 0] > 0.0);
+    const unsigned past = __ballot_sync(~0u, lane < size && sums > (double)sample * total);
+    owner = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
+    before = __shfl_sync(~0u, sums, rank ? rank - 1 : 0);
+    if (rank == 0) before = 0.0;
     if (plain || total > 0.0) break;
     plain = true;                                // nothing is left: from p itself
+    rest.q = nullptr;
+    rest.out = -1;
+    turn = 1;
     __syncthreads();
   }
-  // the CTA, then the warp, then the entry in which the sum passes the target
-  const double target = (double)a.sample_u[b] * total;
-  int owner = total < INFINITY ? last : -1;
-  if (owner >= 0) {
-    double sum = 0.0;
-    for (int i = 0; i < size; ++i) {
-      sum += s_cta[plain && taken < count ? 1 : 0][i];
-      if (sum > target) {
-        owner = i;
-        break;
-      }
-    }
-  }
+  if (!(total < INFINITY)) owner = -1;
   int32_t* tokens = a.tokens + (size_t)b * (a.d + 1);
   if (rank == 0) {
     for (int j = tid; j <= a.d; j += kThreads)
@@ -125,39 +162,39 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
     }
   }
   if (rank != owner) return;
-  double sum = before;
-  int w = -1, lastw = -1;
-  for (int i = 0; i < kWarps; ++i) {
-    if (s_warp[i] > 0.0) lastw = i;
-    if (sum + s_warp[i] > target) {
-      w = i;
-      break;
+  // the warp, then the lane, then the entry in which the sum passes the target
+  const double target = (double)sample * total;
+  const double up = lane < kWarps ? s_warp[lane] : 0.0;
+  const unsigned past = __ballot_sync(~0u, lane < kWarps && before + up > target);
+  const double lower = __shfl_up_sync(~0u, up, 1);
+  const unsigned any = __ballot_sync(~0u, lane < kWarps && up > (lane ? lower : 0.0));
+  const bool found = past != 0;
+  if (warp != (found ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0)) return;
+  double sum = before + (warp ? s_warp[warp - 1] : 0.0);
+  int token = -1, last = -1;                     // last: the last entry over 0
+#pragma unroll 1
+  for (int base = w0; base < w1; base += 32 * kBatch) {
+    const int v0 = base + lane * kBatch;
+    float s = 0.f, c = 0.f;
+    add_batch(rest, v0, 1, w1, s, c);
+    const double x = (double)s + (double)c, to = scan(x, 32);
+    const unsigned here = __ballot_sync(~0u, found && x > 0.0 && sum + to > target);
+    const unsigned some = __ballot_sync(~0u, x > 0.0);
+    const int who = here ? __ffs(here) - 1 : some ? 31 - __clz(some) : -1;
+    if (lane == who) {
+      double at = sum + (to - x);
+#pragma unroll 1
+      for (int v = v0; v < min(v0 + kBatch, w1); ++v) {
+        float r, e;
+        rest.entry(v, r, e);
+        if (r > 0.f) last = v;
+        at += (double)r + (double)e;
+        if (here && r > 0.f && at > target) break;
+      }
     }
-    sum += s_warp[i];
-  }
-  const bool found = w >= 0;
-  if (warp != (found ? w : lastw)) return;
-  int token = -1;
-  for (int v0 = w0; v0 < w1 && token < 0; v0 += 32) {
-    float r = 0.f, e = 0.f;
-    if (v0 + lane < w1) entry(v0 + lane, r, e);
-    double x = (double)r + (double)e;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(~0u, x, d);
-      if (lane >= d) x += y;
-    }
-    const unsigned past = __ballot_sync(~0u, found && v0 + lane < w1 && r > 0.f && sum + x > target);
-    if (past) token = v0 + __ffs(past) - 1;
-    sum += __shfl_sync(~0u, x, 31);
-  }
-  if (token < 0) {                               // U at the sum's very end: the last entry with anything
-    for (int v0 = w0; v0 < w1; v0 += 32) {
-      float r = 0.f, e = 0.f;
-      if (v0 + lane < w1) entry(v0 + lane, r, e);
-      const unsigned any = __ballot_sync(~0u, r > 0.f);
-      if (any) token = v0 + 31 - __clz(any);
-    }
+    if (who >= 0) token = __shfl_sync(~0u, last, who);
+    if (here) break;
+    sum += __shfl_sync(~0u, to, 31);
   }
   if (lane == 0) tokens[taken] = token;
 }
@@ -165,8 +202,19 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
+  // as many CTAs to a sequence as have 2048 entries each and are resident together
+  // (four of an SM)
   int size = 1;
-  while (size < kMaxCluster && a.V > size * 4096) size *= 2;
+  while (size < kMaxCluster && a.V > size * 2048 && a.B * size * 2 <= 4 * tree_sms()) size *= 2;
+  if (size > 8) {
+    static bool ready[kDeviceSlots] = {};
+    const int dv = device_slot();
+    if (dv < 0 || !ready[dv]) {
+      const cudaError_t e = cudaFuncSetAttribute(verify_drafts_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (dv >= 0) ready[dv] = true;
+    }
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)size, 1, 1};
