@@ -47,12 +47,12 @@ SSD_DI uint32_t largest(uint32_t most) {         // over a warp, of packed pairs
   return __reduce_max_sync(~0u, max(most & 0xffffu, most >> 16));
 }
 
-// Items = (sequence, block, K or V, head), dealt to the CTAs in turn; a CTA has
-// a block in registers: one read, one write.
+// Items = (sequence, block, head), dealt to the CTAs in turn; a CTA has a block of K
+// and of V in registers: one read, one write.
 template <int DH, int UNITS>                     // 16-byte units of a block per thread
 __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_constant__ QuantizeArgs a) {
   __shared__ int first[kBatchMaxSeqs + 1];       // blocks of all sequences before b
-  __shared__ uint32_t warp_max[kThreads / 32];
+  __shared__ uint32_t warp_max[2][kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int b = tid; b < a.B; b += kThreads) {
     int from, to;
@@ -76,11 +76,9 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
     }
   }
   __syncthreads();
-  const int total = first[a.B], per = 2 * a.Hkv;
-  for (long long item = blockIdx.x; item < (long long)total * per; item += gridDim.x) {
-    const int j = (int)(item / per), rest = (int)(item - (long long)j * per);
-    const bool is_v = rest >= a.Hkv;
-    const int h = rest - (is_v ? a.Hkv : 0);
+  const int total = first[a.B];
+  for (long long item = blockIdx.x; item < (long long)total * a.Hkv; item += gridDim.x) {
+    const int j = (int)(item / a.Hkv), h = (int)(item - (long long)j * a.Hkv);
     int lo = 0, hi = a.B - 1;                    // the last b with first[b] <= j
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -91,60 +89,69 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
     blocks_of(a, lo, from, to);
     const int block = from + j - first[lo];
     const size_t row0 = (size_t)block * a.block;
-    const bf16* src = (is_v ? a.v : a.k) + (size_t)lo * a.seq_stride + (size_t)h * a.rows * DH;
+    const size_t from_head = (size_t)lo * a.seq_stride + (size_t)h * a.rows * DH;
+    const size_t to_head = (size_t)lo * a.seq8_stride + ((size_t)h * a.max_seq + row0) * DH;
     // (a block turns over at the ring's end once at most)
     const int slot0 = (int)((unsigned)row0 % (unsigned)a.rows);
-    uint4 x[UNITS];
-    uint32_t most = 0;
+    uint4 x[2][UNITS];                           // of K, of V
 #pragma unroll
     for (int q = 0; q < UNITS; ++q) {
       const int e = (tid + q * kThreads) * 8, at = slot0 + e / DH;
-      x[q] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(at < a.rows ? at : at - a.rows) * DH + e % DH));
+      const size_t o = from_head + (size_t)(at < a.rows ? at : at - a.rows) * DH + e % DH;
+      x[0][q] = __ldcs(reinterpret_cast<const uint4*>(a.k + o));
+      x[1][q] = __ldcs(reinterpret_cast<const uint4*>(a.v + o));
     }
+    uint32_t most[2];
 #pragma unroll
-    for (int q = 0; q < UNITS; ++q)
-      most = __vmaxu2(__vmaxu2(most, __vmaxu2(x[q].x & 0x7fff7fffu, x[q].y & 0x7fff7fffu)),
-                      __vmaxu2(x[q].z & 0x7fff7fffu, x[q].w & 0x7fff7fffu));
-    most = largest(most);
-    __syncthreads();                             // (the item before has read)
-    if (lane == 0) warp_max[warp] = most;
-    __syncthreads();
-    most = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[lane] : 0u);
-    const bool odd = most >= 0x7f80u;            // something is not finite: without it
-    if (odd) {
-      most = 0;
+    for (int z = 0; z < 2; ++z) {
+      uint32_t m = 0;
 #pragma unroll
       for (int q = 0; q < UNITS; ++q)
-        most = __vmaxu2(__vmaxu2(most, __vmaxu2(abs_finite(x[q].x), abs_finite(x[q].y))),
-                        __vmaxu2(abs_finite(x[q].z), abs_finite(x[q].w)));
-      most = largest(most);
-      __syncthreads();
-      if (lane == 0) warp_max[warp] = most;
-      __syncthreads();
-      most = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[lane] : 0u);
+        m = __vmaxu2(__vmaxu2(m, __vmaxu2(x[z][q].x & 0x7fff7fffu, x[z][q].y & 0x7fff7fffu)),
+                     __vmaxu2(x[z][q].z & 0x7fff7fffu, x[z][q].w & 0x7fff7fffu));
+      most[z] = largest(m);
     }
-    float scale = 1.f;
-    int e = 0;
-    if (most) {
-      const float part = frexpf(__uint_as_float(most << 16), &e);
-      e = max(e - (part > 0.875f ? 8 : 9), -64);
-      scale = ldexpf(1.f, e);
-    }
-    const float inv = ldexpf(1.f, -e);
-    uint8_t* dst = (is_v ? a.v8 : a.k8) + (size_t)lo * a.seq8_stride + ((size_t)h * a.max_seq + row0) * DH;
+    __syncthreads();                             // (the item before has read)
+    if (lane < 2) warp_max[lane][warp] = lane ? most[1] : most[0];
+    __syncthreads();
 #pragma unroll
-    for (int q = 0; q < UNITS; ++q) {
-      const int u = tid + q * kThreads;
-      uint2 y;
-      if (!odd)
-        y = make_uint2(two_of(x[q].x, inv) | two_of(x[q].y, inv) << 16, two_of(x[q].z, inv) | two_of(x[q].w, inv) << 16);
-      else
-        y = make_uint2(two_any(x[q].x, inv) | two_any(x[q].y, inv) << 16,
-                       two_any(x[q].z, inv) | two_any(x[q].w, inv) << 16);
-      *reinterpret_cast<uint2*>(dst + (size_t)u * 8) = y;
+    for (int z = 0; z < 2; ++z) {
+      uint32_t m = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[z][lane] : 0u);
+      const bool odd = m >= 0x7f80u;             // something is not finite: without it
+      if (odd) {
+        m = 0;
+#pragma unroll
+        for (int q = 0; q < UNITS; ++q)
+          m = __vmaxu2(__vmaxu2(m, __vmaxu2(abs_finite(x[z][q].x), abs_finite(x[z][q].y))),
+                       __vmaxu2(abs_finite(x[z][q].z), abs_finite(x[z][q].w)));
+        m = largest(m);
+        __syncthreads();
+        if (lane == 0) warp_max[z][warp] = m;
+        __syncthreads();
+        m = __reduce_max_sync(~0u, lane < kThreads / 32 ? warp_max[z][lane] : 0u);
+      }
+      float scale = 1.f;
+      int e = 0;
+      if (m) {
+        const float part = frexpf(__uint_as_float(m << 16), &e);
+        e = max(e - (part > 0.875f ? 8 : 9), -64);
+        scale = ldexpf(1.f, e);
+      }
+      const float inv = ldexpf(1.f, -e);
+      uint8_t* dst = (z ? a.v8 : a.k8) + to_head;
+#pragma unroll
+      for (int q = 0; q < UNITS; ++q) {
+        const uint4 w = x[z][q];
+        uint2 y;
+        if (!odd)
+          y = make_uint2(two_of(w.x, inv) | two_of(w.y, inv) << 16, two_of(w.z, inv) | two_of(w.w, inv) << 16);
+        else
+          y = make_uint2(two_any(w.x, inv) | two_any(w.y, inv) << 16, two_any(w.z, inv) | two_any(w.w, inv) << 16);
+        *reinterpret_cast<uint2*>(dst + (size_t)(tid + q * kThreads) * 8) = y;
+      }
+      if (tid == 0)
+        (z ? a.v_scale : a.k_scale)[(size_t)lo * a.scale_stride + (size_t)h * (a.max_seq / a.block) + block] = scale;
     }
-    if (tid == 0)
-      (is_v ? a.v_scale : a.k_scale)[(size_t)lo * a.scale_stride + (size_t)h * (a.max_seq / a.block) + block] = scale;
   }
 }
 
@@ -162,7 +169,7 @@ cudaError_t launch(const QuantizeArgs& a, unsigned ctas, cudaStream_t s) {
 
 cudaError_t launch_cache_quantize(const QuantizeArgs& a, cudaStream_t s) {
   // at most so many items, and eight CTAs for each SM
-  const long long most = (long long)a.B * 2 * a.Hkv * ((a.rows < a.max_seq ? a.rows : a.max_seq) / a.block + 1);
+  const long long most = (long long)a.B * a.Hkv * ((a.rows < a.max_seq ? a.rows : a.max_seq) / a.block + 1);
   const unsigned ctas = (unsigned)(most < 8 * tree_sms() ? most : 8 * tree_sms());
   return a.dh == 128 ? launch<128>(a, ctas, s) : launch<64>(a, ctas, s);
 }

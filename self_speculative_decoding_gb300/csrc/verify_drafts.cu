@@ -51,60 +51,59 @@ SSD_DI double scan(double x, int lanes) {
 struct Rest {
   const float *p, *q;
   int out;
-  SSD_DI void entry(int v, float& r, float& e) const { rest_of(p[v], q ? q[v] : v == out ? p[v] : 0.f, r, e); }
 };
 
-constexpr int kBatch = 16;                       // entries of a lane in flight at once
+constexpr int kBatch = 8;                        // entries of a lane in flight at once
 
-// A lane's sum over the entries v0 + k step < v1, k < kBatch.
-SSD_DI void add_batch(const Rest& rest, int v0, int step, int v1, float& s, float& c) {
-  float p[kBatch], q[kBatch];
+// A lane's entries v0 + k step < v1, k < kBatch, as values and rounding errors.
+SSD_DI void get_batch(const Rest& rest, int v0, int step, int v1, float (&r)[kBatch], float (&e)[kBatch]) {
 #pragma unroll
   for (int k = 0; k < kBatch; ++k) {
     const int v = v0 + k * step;
-    p[k] = v < v1 ? rest.p[v] : 0.f;
-    q[k] = v < v1 && rest.q ? rest.q[v] : v == rest.out ? p[k] : 0.f;
+    r[k] = v < v1 ? rest.p[v] : 0.f;
+    e[k] = v < v1 && rest.q ? rest.q[v] : v == rest.out ? r[k] : 0.f;
   }
 #pragma unroll
-  for (int k = 0; k < kBatch; ++k) {
-    float r, e, t;
-    rest_of(p[k], q[k], r, e);
-    two_sum(s, r, s, t);
-    c += t + e;
-  }
+  for (int k = 0; k < kBatch; ++k) rest_of(r[k], e[k], r[k], e[k]);
 }
 
 // A cluster per sequence, a slice of the vocabulary per CTA and a run of it per
 // warp.  Each CTA tests the drafts by itself; the sums meet once.  Then one warp
-// walks its run again, 16 entries in a row to a lane.
+// walks its run again, 8 entries in a row to a lane.
 // Bound by latency: the drafts, their probabilities, the row's entries, the
 // cluster's exchange and the walk one behind the other.
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   cluster.barrier_arrive();                      // (all CTAs run before one writes to another)
-  __shared__ int s_taken;
   __shared__ double s_warp[kWarps];              // sums of the warps, then of those up to each
   __shared__ double s_cta[2][kMaxCluster];       // each CTA's sum, from the CTAs themselves
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / size;
   const int count = a.counts ? min(max(a.counts[b], 0), a.d) : a.d;
-  if (tid == 0) s_taken = count;
   const float sample = a.sample_u[b];
-  __syncthreads();
-  for (int j = tid; j < count; j += kThreads) {
-    const float u = a.accept_u[(size_t)b * a.d + j];
-    const int y = a.drafts[(size_t)b * a.d + j];
-    bool good = y >= 0 && y < a.V;
-    if (good) {
-      const float p = a.p[((size_t)b * (a.d + 1) + j) * a.V + y];
-      const float q = a.q ? a.q[((size_t)b * a.d + j) * a.V + y] : 1.f;
-      good = (double)u * (double)q < (double)p;
+  // the drafts in order, 32 at a time (by each warp for itself)
+  int taken = count;
+#pragma unroll 1
+  for (int j0 = 0; j0 < count; j0 += 32) {
+    const int j = j0 + lane;
+    bool good = true;
+    if (j < count) {
+      const float u = a.accept_u[(size_t)b * a.d + j];
+      const int y = a.drafts[(size_t)b * a.d + j];
+      good = y >= 0 && y < a.V;
+      if (good) {
+        const float p = a.p[((size_t)b * (a.d + 1) + j) * a.V + y];
+        const float q = a.q ? a.q[((size_t)b * a.d + j) * a.V + y] : 1.f;
+        good = (double)u * (double)q < (double)p;
+      }
     }
-    if (!good) atomicMin(&s_taken, j);
+    const unsigned bad = __ballot_sync(~0u, !good);
+    if (bad) {
+      taken = j0 + __ffs(bad) - 1;
+      break;
+    }
   }
-  __syncthreads();
-  const int taken = s_taken;
   bool plain = taken == count;                   // r = p
   Rest rest;
   rest.p = a.p + ((size_t)b * (a.d + 1) + taken) * a.V;
@@ -119,7 +118,16 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
   while (true) {
     float s = 0.f, c = 0.f;
 #pragma unroll 1
-    for (int v = w0 + lane; v - lane < w1; v += 32 * kBatch) add_batch(rest, v, 32, w1, s, c);
+    for (int v = w0 + lane; v - lane < w1; v += 32 * kBatch) {
+      float r[kBatch], e[kBatch];
+      get_batch(rest, v, 32, w1, r, e);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        float t;
+        two_sum(s, r[k], s, t);
+        c += t + e[k];
+      }
+    }
     double x = (double)s + (double)c;
 #pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
@@ -171,28 +179,33 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
   const bool found = past != 0;
   if (warp != (found ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0)) return;
   double sum = before + (warp ? s_warp[warp - 1] : 0.0);
-  int token = -1, last = -1;                     // last: the last entry over 0
+  int token = -1;
 #pragma unroll 1
   for (int base = w0; base < w1; base += 32 * kBatch) {
     const int v0 = base + lane * kBatch;
-    float s = 0.f, c = 0.f;
-    add_batch(rest, v0, 1, w1, s, c);
+    float r[kBatch], e[kBatch], s = 0.f, c = 0.f;
+    get_batch(rest, v0, 1, w1, r, e);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      float t;
+      two_sum(s, r[k], s, t);
+      c += t + e[k];
+    }
     const double x = (double)s + (double)c, to = scan(x, 32);
     const unsigned here = __ballot_sync(~0u, found && x > 0.0 && sum + to > target);
     const unsigned some = __ballot_sync(~0u, x > 0.0);
-    const int who = here ? __ffs(here) - 1 : some ? 31 - __clz(some) : -1;
-    if (lane == who) {
-      double at = sum + (to - x);
-#pragma unroll 1
-      for (int v = v0; v < min(v0 + kBatch, w1); ++v) {
-        float r, e;
-        rest.entry(v, r, e);
-        if (r > 0.f) last = v;
-        at += (double)r + (double)e;
-        if (here && r > 0.f && at > target) break;
+    double at = sum + (to - x);
+    int first = -1, last = -1;                   // the lane's first past the target, its last over 0
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      at += (double)r[k] + (double)e[k];
+      if (r[k] > 0.f) {
+        last = v0 + k;
+        if (first < 0 && at > target) first = v0 + k;
       }
     }
-    if (who >= 0) token = __shfl_sync(~0u, last, who);
+    if (here && first >= 0) last = first;
+    if (some) token = __shfl_sync(~0u, last, here ? __ffs(here) - 1 : 31 - __clz(some));
     if (here) break;
     sum += __shfl_sync(~0u, to, 31);
   }
@@ -203,9 +216,9 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
   // as many CTAs to a sequence as have 2048 entries each and are resident together
-  // (four of an SM)
+  // (three of an SM)
   int size = 1;
-  while (size < kMaxCluster && a.V > size * 2048 && a.B * size * 2 <= 4 * tree_sms()) size *= 2;
+  while (size < kMaxCluster && a.V > size * 2048 && a.B * size * 2 <= 3 * tree_sms()) size *= 2;
   if (size > 8) {
     static bool ready[kDeviceSlots] = {};
     const int dv = device_slot();
