@@ -35,6 +35,15 @@ SSD_DI void rest_of(float p, float q, float& r, float& e) {
   if (!(r > 0.f)) r = e = 0.f;                   // (NaN too)
 }
 
+// u q < p without rounding: the product's rounding error decides where the rounded
+// product is p (scaled, so that the error of a small product is a normal number).
+SSD_DI bool less(float u, float q, float p) {
+  q *= 0x1p64f;
+  p *= 0x1p64f;
+  const float h = __fmul_rn(u, q), l = __fmaf_rn(u, q, -h);
+  return h < p || (h == p && l < 0.f);
+}
+
 // Sum over the warp's lower lanes and itself, in 64 bits.
 SSD_DI double scan(double x, int lanes) {
   const int lane = threadIdx.x & 31;
@@ -56,26 +65,64 @@ struct Rest {
 constexpr int kBatch = 8;                        // entries of a lane in flight at once
 
 // A lane's entries v0 + k step < v1, k < kBatch, as values and rounding errors.
-SSD_DI void get_batch(const Rest& rest, int v0, int step, int v1, float (&r)[kBatch], float (&e)[kBatch]) {
+// FULL: all are below v1.
+template <bool FULL>
+SSD_DI void get_entries(const Rest& rest, int v0, int step, int v1, float (&r)[kBatch], float (&e)[kBatch]) {
+  const float *p = rest.p + v0, *q = rest.q + v0;
 #pragma unroll
-  for (int k = 0; k < kBatch; ++k) {
-    const int v = v0 + k * step;
-    r[k] = v < v1 ? rest.p[v] : 0.f;
-    e[k] = v < v1 && rest.q ? rest.q[v] : v == rest.out ? r[k] : 0.f;
+  for (int k = 0; k < kBatch; ++k) r[k] = FULL || v0 + k * step < v1 ? p[k * step] : 0.f;
+  if (rest.q) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) e[k] = FULL || v0 + k * step < v1 ? q[k * step] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) rest_of(r[k], e[k], r[k], e[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      r[k] = r[k] > 0.f && v0 + k * step != rest.out ? r[k] : 0.f;  // (NaN too)
+      e[k] = 0.f;
+    }
+  }
+}
+SSD_DI void get_batch(const Rest& rest, int v0, int step, int end, int v1, float (&r)[kBatch], float (&e)[kBatch]) {
+  if (end <= v1) get_entries<true>(rest, v0, step, v1, r, e);
+  else get_entries<false>(rest, v0, step, v1, r, e);
+}
+
+// A warp's sum of the entries w0 .. w1 - 1.
+static __device__ __noinline__ float2 sum_run(const Rest& rest, int w0, int w1) {
+  const int lane = threadIdx.x & 31;
+  float s = 0.f, c = 0.f, t;
+#pragma unroll 1
+  for (int v = w0; v < w1; v += 32 * kBatch) {
+    float r[kBatch], e[kBatch];
+    get_batch(rest, v + lane, 32, v + 32 * kBatch, w1, r, e);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      two_sum(s, r[k], s, t);
+      c += t + e[k];
+    }
   }
 #pragma unroll
-  for (int k = 0; k < kBatch; ++k) rest_of(r[k], e[k], r[k], e[k]);
+  for (int d = 16; d; d >>= 1) {
+    two_sum(s, __shfl_xor_sync(~0u, s, d), s, t);
+    c += __shfl_xor_sync(~0u, c, d) + t;
+  }
+  return make_float2(s, c);
 }
 
 // A cluster per sequence, a slice of the vocabulary per CTA and a run of it per
-// warp.  Each CTA tests the drafts by itself; the sums meet once.  Then one warp
-// walks its run again, 8 entries in a row to a lane.
+// warp.  Each CTA tests the drafts by itself; the sums meet once.  Then the CTA in
+// whose slice the token lies searches it.
 // Bound by latency: the drafts, their probabilities, the row's entries, the
-// cluster's exchange and the walk one behind the other.
+// cluster's exchange and the search one behind the other.
 __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   cluster.barrier_arrive();                      // (all CTAs run before one writes to another)
-  __shared__ double s_warp[kWarps];              // sums of the warps, then of those up to each
+  __shared__ float2 s_part[kWarps];              // sums of the warps
+  __shared__ double s_warp[kWarps];              // of those up to each
+  __shared__ double s_before, s_total;           // of the CTAs below, of all
+  __shared__ int s_owner;
   __shared__ double s_cta[2][kMaxCluster];       // each CTA's sum, from the CTAs themselves
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -95,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
       if (good) {
         const float p = a.p[((size_t)b * (a.d + 1) + j) * a.V + y];
         const float q = a.q ? a.q[((size_t)b * a.d + j) * a.V + y] : 1.f;
-        good = (double)u * (double)q < (double)p;
+        good = less(u, q, p);
       }
     }
     const unsigned bad = __ballot_sync(~0u, !good);
@@ -113,45 +160,36 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
   const int slice = (a.V + size - 1) / size, lo = (int)min((long long)rank * slice, (long long)a.V);
   const int hi = min(lo, a.V - slice) + slice;
   const int run = (hi - lo + kWarps - 1) / kWarps, w0 = min(lo + warp * run, hi), w1 = min(w0 + run, hi);
-  double total = 0.0, before = 0.0, mine = 0.0;
-  int owner = -1, turn = 0;
+  double total;
+  int owner, turn = 0;
   while (true) {
-    float s = 0.f, c = 0.f;
-#pragma unroll 1
-    for (int v = w0 + lane; v - lane < w1; v += 32 * kBatch) {
-      float r[kBatch], e[kBatch];
-      get_batch(rest, v, 32, w1, r, e);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        float t;
-        two_sum(s, r[k], s, t);
-        c += t + e[k];
-      }
-    }
-    double x = (double)s + (double)c;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-    if (lane == 0) s_warp[warp] = x;
+    const float2 own = sum_run(rest, w0, w1);
+    if (lane == 0) s_part[warp] = own;
     __syncthreads();
+    if (turn == 0) cluster.barrier_wait();
     if (warp == 0) {
-      const double up = scan(lane < kWarps ? s_warp[lane] : 0.0, kWarps);
-      mine = __shfl_sync(~0u, up, kWarps - 1);
-      if (turn == 0) cluster.barrier_wait();
-      if (lane < size) *cluster.map_shared_rank(&s_cta[turn][rank], lane) = mine;
-      __syncwarp();
+      const float2 part = lane < kWarps ? s_part[lane] : make_float2(0.f, 0.f);
+      const double up = scan((double)part.x + (double)part.y, kWarps);
       if (lane < kWarps) s_warp[lane] = up;
-    } else if (turn == 0) {
-      cluster.barrier_wait();
+      const double mine = __shfl_sync(~0u, up, kWarps - 1);
+      if (lane < size) *cluster.map_shared_rank(&s_cta[turn][rank], lane) = mine;
     }
     cluster.sync();
-    // the first CTA whose sums pass the target, or the last that has any
-    const double sums = scan(lane < size ? s_cta[turn][lane] : 0.0, kMaxCluster);
-    total = __shfl_sync(~0u, sums, size - 1);
-    const unsigned any = __ballot_sync(~0u, lane < size && s_cta[turn][lane < size ? lane : 0] > 0.0);
-    const unsigned past = __ballot_sync(~0u, lane < size && sums > (double)sample * total);
-    owner = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
-    before = __shfl_sync(~0u, sums, rank ? rank - 1 : 0);
-    if (rank == 0) before = 0.0;
+    if (warp == 0) {
+      // the first CTA whose sums pass the target, or the last that has any
+      const double x = lane < size ? s_cta[turn][lane] : 0.0, sums = scan(x, kMaxCluster);
+      const double all = __shfl_sync(~0u, sums, size - 1);
+      const unsigned any = __ballot_sync(~0u, x > 0.0), past = __ballot_sync(~0u, lane < size && sums > (double)sample * all);
+      const double below = __shfl_sync(~0u, sums, rank ? rank - 1 : 0);
+      if (lane == 0) {
+        s_before = rank ? below : 0.0;
+        s_total = all;
+        s_owner = !(all < INFINITY) ? -1 : past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
+      }
+    }
+    __syncthreads();
+    total = s_total;
+    owner = s_owner;
     if (plain || total > 0.0) break;
     plain = true;                                // nothing is left: from p itself
     rest.q = nullptr;
@@ -159,56 +197,77 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
     turn = 1;
     __syncthreads();
   }
-  if (!(total < INFINITY)) owner = -1;
   int32_t* tokens = a.tokens + (size_t)b * (a.d + 1);
-  if (rank == 0) {
-    for (int j = tid; j <= a.d; j += kThreads)
+  if (rank == 0 && warp == 1) {
+    for (int j = lane; j <= a.d; j += 32)
       if (j != taken) tokens[j] = j < taken ? a.drafts[(size_t)b * a.d + j] : -1;
-    if (tid == 0) {
+    if (lane == 0) {
       a.n[b] = taken + (owner >= 0 ? 1 : 0);
       if (owner < 0) tokens[taken] = -1;         // no probability anywhere
     }
   }
   if (rank != owner) return;
-  // the warp, then the lane, then the entry in which the sum passes the target
+  // the warp's run in which the sum passes the target, a 16th of that, and so on,
+  // all warps together; the last 128 entries by one
   const double target = (double)sample * total;
-  const double up = lane < kWarps ? s_warp[lane] : 0.0;
-  const unsigned past = __ballot_sync(~0u, lane < kWarps && before + up > target);
-  const double lower = __shfl_up_sync(~0u, up, 1);
-  const unsigned any = __ballot_sync(~0u, lane < kWarps && up > (lane ? lower : 0.0));
-  const bool found = past != 0;
-  if (warp != (found ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0)) return;
-  double sum = before + (warp ? s_warp[warp - 1] : 0.0);
-  int token = -1;
+  int x0 = lo, x1 = hi;
+  double below = s_before;
 #pragma unroll 1
-  for (int base = w0; base < w1; base += 32 * kBatch) {
-    const int v0 = base + lane * kBatch;
-    float r[kBatch], e[kBatch], s = 0.f, c = 0.f;
-    get_batch(rest, v0, 1, w1, r, e);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      float t;
-      two_sum(s, r[k], s, t);
-      c += t + e[k];
-    }
-    const double x = (double)s + (double)c, to = scan(x, 32);
-    const unsigned here = __ballot_sync(~0u, found && x > 0.0 && sum + to > target);
-    const unsigned some = __ballot_sync(~0u, x > 0.0);
-    double at = sum + (to - x);
-    int first = -1, last = -1;                   // the lane's first past the target, its last over 0
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      at += (double)r[k] + (double)e[k];
-      if (r[k] > 0.f) {
-        last = v0 + k;
-        if (first < 0 && at > target) first = v0 + k;
+  while (true) {
+    const int part = (x1 - x0 + kWarps - 1) / kWarps;
+    if (warp == 0) {                             // (s_warp: the sums up to each warp's part)
+      const double up = lane < kWarps ? s_warp[lane] : 0.0, lower = __shfl_up_sync(~0u, up, 1);
+      const unsigned past = __ballot_sync(~0u, lane < kWarps && below + up > target);
+      const unsigned any = __ballot_sync(~0u, lane < kWarps && up > (lane ? lower : 0.0));
+      const int w = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0;
+      if (lane == w) {
+        s_owner = w;
+        s_before = below + (w ? lower : 0.0);
       }
     }
-    if (here && first >= 0) last = first;
-    if (some) token = __shfl_sync(~0u, last, here ? __ffs(here) - 1 : 31 - __clz(some));
-    if (here) break;
-    sum += __shfl_sync(~0u, to, 31);
+    __syncthreads();
+    const int w = s_owner;
+    below = s_before;
+    x0 = min(x0 + w * part, x1);
+    x1 = min(x0 + part, x1);
+    if (x1 - x0 <= 128) break;
+    const int next = (x1 - x0 + kWarps - 1) / kWarps, y0 = min(x0 + warp * next, x1);
+    const float2 own = sum_run(rest, y0, min(y0 + next, x1));
+    if (lane == 0) s_part[warp] = own;
+    __syncthreads();
+    if (warp == 0) {
+      const float2 y = lane < kWarps ? s_part[lane] : make_float2(0.f, 0.f);
+      const double up = scan((double)y.x + (double)y.y, kWarps);
+      if (lane < kWarps) s_warp[lane] = up;
+      __syncwarp();
+    }
   }
+  if (warp != 0) return;
+  const int v0 = x0 + lane * 4;
+  double at[4], sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float r = 0.f, e = 0.f;
+    if (v0 + k < x1) {
+      const float pk = rest.p[v0 + k];
+      rest_of(pk, rest.q ? rest.q[v0 + k] : v0 + k == rest.out ? pk : 0.f, r, e);
+    }
+    at[k] = (double)r + (double)e;
+    sum += at[k];
+  }
+  const double to = scan(sum, 32);
+  double up = below + (to - sum);
+  int first = -1, last = -1;                     // the lane's first past the target, its last over 0
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    up += at[k];
+    if (at[k] > 0.0) {
+      last = v0 + k;
+      if (first < 0 && up > target) first = v0 + k;
+    }
+  }
+  const unsigned here = __ballot_sync(~0u, first >= 0), some = __ballot_sync(~0u, last >= 0);
+  const int token = here ? __shfl_sync(~0u, first, __ffs(here) - 1) : some ? __shfl_sync(~0u, last, 31 - __clz(some)) : -1;
   if (lane == 0) tokens[taken] = token;
 }
 
