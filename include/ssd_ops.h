@@ -256,7 +256,7 @@ ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* pare
  * verification of the drafts.  As above these calls allocate nothing and can be
  * captured into graphs; what differs between sequences or rounds (lengths,
  * counts, held, ...: device int32 [B]) is read from device memory when the call
- * runs, so that a captured graph serves every round.  1 <= B <= 1024.
+ * runs, so that a captured graph serves every round.  1 <= B <= 512.
  *
  * Caches: row p of sequence b and K/V head h is the dh elements at
  *   k + b seq_stride + (h rows + p % rows) dh     (bf16; v the same)

@@ -16,7 +16,7 @@
 
 namespace ssd {
 
-constexpr int kBatchMaxSeqs = 1024;
+constexpr int kBatchMaxSeqs = 512;
 
 struct RopeAppendArgs {
   const float* qkv = nullptr;          // [B][T][(H + 2 Hkv) dh] raw projections

@@ -68,7 +68,7 @@ struct Layout {
   int p_bufs, k_units, v_units;
 };
 constexpr int kSmemMost = 227 * 1024 - 1024;     // (from a 1024-byte boundary)
-constexpr int kSmall = 5 * 128 * 4 + 512;        // per-row values, barriers
+constexpr int kSmall = 5 * 128 * 4 + 512 + 19 * 96;       // per-row values, barriers
 __host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
   Layout l;
   l.rows = (rows + 15) / 16 * 16;
@@ -206,14 +206,12 @@ SSD_DI bool any_group(int group, bool x) {
 
 // ---- division of the work
 
-// (What runs once per sequence or run of tiles is kept out of line: the roles'
-// loops have to lie in the instruction cache beside one another.  With all of it
-// inlined the kernel was 160 KB, and one token over 131000 rows took 108 us, not
-// 75.)
+// What runs once per sequence or run of tiles is kept out of line (code beyond 32
+// KB is fetched at 2.4 cycles an instruction, beyond 128 KB at 6), and what it
+// finds lies in shared memory, a place for each warp: with a block's shared memory
+// this large there is next to no L1 cache, and each value that the stack holds
+// costs a trip to L2.
 SSD_DI int cdiv_keys(int x) { return (x + kKeys - 1) / kKeys; }
-static __device__ __noinline__ SeqRange seq_range_of(const CacheAttnArgs& a, int length, int count, int held) {
-  return seq_range(a, length, count, held);
-}
 // Tiles in 8 bits: the first rows, then the run; and in bf16 the same.
 SSD_DI int tiles_eight(const SeqRange& r) {
   return cdiv_keys(min(r.sinks, r.held)) + (r.low < r.held ? cdiv_keys(r.held) - r.low / kKeys : 0);
@@ -231,8 +229,8 @@ struct Walk {
   bool eight;
   SSD_DI bool edge() const { return p0 < f0 || p0 + kKeys > f1; }
 };
-static __device__ __noinline__ Walk walk_from(SeqRange r, int window, int tile) {
-  Walk w;
+
+static __device__ __noinline__ void find_run(const SeqRange& r, int window, int tile, Walk& w) {
   const int first = max(r.low, r.held);
   int i = tile, start = 0, n;
   bool whole = true;                             // (first rows: all tokens see them)
@@ -270,12 +268,6 @@ static __device__ __noinline__ Walk walk_from(SeqRange r, int window, int tile) 
   w.left = n - i;
   w.f0 = window && !whole ? max(w.rs, r.end - window) : w.rs;
   w.f1 = min(w.re, r.length + 1);
-  return w;
-}
-SSD_DI void step(Walk& w, const SeqRange& r, int window) {
-  ++w.i;
-  w.p0 += kKeys;
-  if (seldom(--w.left == 0)) w = walk_from(r, window, w.i);
 }
 
 // What the CTA's threads know of the sequences, in shared memory.
@@ -305,7 +297,12 @@ struct Segment {
   bool whole, head;                              // all of them; the pair began in an earlier CTA
   SeqRange r;
 };
-static __device__ __noinline__ Segment segment_at(const CacheAttnArgs& a, const Plan& p, long long at) {
+// A warp's own copies of what it works on.
+struct Place {
+  Segment s;
+  Walk w;
+};
+static __device__ __noinline__ void segment_at(const CacheAttnArgs& a, const Plan& p, long long at, Place& to) {
   Segment s;
   int lo = 0, hi = a.B - 1;                      // the last b with first[b] Hkv <= at
   while (lo < hi) {
@@ -324,7 +321,21 @@ static __device__ __noinline__ Segment segment_at(const CacheAttnArgs& a, const 
   s.head = s.i0 > 0;
   s.r = seq_range(a, p.length[lo], p.count[lo], p.held[lo]);
   s.eight = max(0, min(s.n, tiles_eight(s.r) - s.i0));
-  return s;
+  __syncwarp();
+  to.s = s;
+  find_run(s.r, a.window, s.i0, to.w);
+  __syncwarp();
+}
+// One tile on.
+SSD_DI void step(Walk& w, Place& place, int window) {
+  ++w.i;
+  w.p0 += kKeys;
+  if (seldom(--w.left == 0)) {
+    __syncwarp();
+    find_run(place.s.r, window, w.i, place.w);
+    __syncwarp();
+    w = place.w;
+  }
 }
 
 // ---- values
@@ -370,8 +381,9 @@ SSD_DI int row_kind(const CacheAttnArgs& a, const SeqRange& r, const Walk& t, in
 // in row pos sees.
 static __device__ __noinline__ float not_finite(const CacheAttnArgs& a, const Segment& s, int pos, int c) {
   float sum = 0.f;
-  Walk t = walk_from(s.r, a.window, s.i0);
+  Walk t;
   for (int i = 0; i < s.n; ++i) {
+    find_run(s.r, a.window, s.i0 + i, t);
     for (int j = max(t.p0, t.rs); j < min(t.p0 + kKeys, t.re); ++j) {
       if (row_kind(a, s.r, t, j) != 1 || j > pos || (a.window && j >= a.sinks && j <= pos - a.window)) continue;
       float x;
@@ -383,15 +395,15 @@ static __device__ __noinline__ float not_finite(const CacheAttnArgs& a, const Se
       }
       if (!isfinite(x)) sum += x;
     }
-    if (i + 1 < s.n) step(t, s.r, a.window);
   }
   return sum;
 }
 // The CTA's rows as NaN: a wait gave up, and none is sure.
-static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan& plan) {
+static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan& plan, Place& place) {
   const int rows = a.T * a.G;
   for (long long at = plan.begin; at < plan.end;) {
-    const Segment s = segment_at(a, plan, at);
+    segment_at(a, plan, at, place);
+    const Segment& s = place.s;
     const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
     if (!s.whole && !s.head && threadIdx.x == 0)
       a.shared[blockIdx.x] = make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0);
@@ -410,15 +422,14 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
 }
 
 // SMALL: up to 16 rows, whose parts of q make one product (twice as wide) and
-// whose state two groups keep in registers.
-constexpr int groups_of(bool small) { return small ? 2 : 3; }
-constexpr int threads_of(bool small) { return (4 * groups_of(small) + 7) * 32; }
-template <int DH, bool SMALL>
-__global__ void __launch_bounds__(threads_of(SMALL), 1)
+// whose state the groups keep in registers.
+constexpr int threads_of(int groups) { return (4 * groups + 7) * 32; }
+template <int DH, bool SMALL, int kGroups>
+__global__ void __launch_bounds__(threads_of(kGroups), 1)
     cache_attn_tc_kernel(const __grid_constant__ CUtensorMap mK8, const __grid_constant__ CUtensorMap mV8,
                          const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                          const __grid_constant__ CacheAttnArgs a, const Layout lay) {
-  constexpr int kGroups = groups_of(SMALL), kThreads = threads_of(SMALL);
+  constexpr int kThreads = threads_of(kGroups);
   constexpr int kWidenWarp = 4 * kGroups, kCopyWarp = kWidenWarp + 4, kMmaWarp = kCopyWarp + 2;
   constexpr int P = DH / 64;                     // 16-bit panels of 64 columns
   constexpr int kWide = P * kUnit;               // a V tile in 16 bits
@@ -449,46 +460,44 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 1);
   int* fail = reinterpret_cast<int*>(tslot + 1);
   int* odd = fail + 1;                           // a V element that is not finite was left out
-  Plan plan;
-  plan.first = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(row_c) + kSmall);
-  plan.length = plan.first + a.B + 1;
-  plan.held = plan.length + a.B;
-  plan.count = reinterpret_cast<short*>(plan.held + a.B);
+  Plan& plan = *reinterpret_cast<Plan*>(bars + 44);
+  Place* places = reinterpret_cast<Place*>(bars + 64);  // of the warps
+  int* first = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(row_c) + kSmall);  // the plan's arrays
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G, chunks = (rows + 7) / 8;
   const int active = min(kGroups, chunks);       // groups with any rows
 
   // ---- set-up
-  if (tid == kMmaWarp * 32) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&kfull[i], 1);
-      mbar_init(&kempty[i], 1);
-      mbar_init(&vfull[i], 1);
-      mbar_init(&vempty[i], kWiden / 32);
+  if (warp == kMmaWarp) {
+    // (kfull, kempty, vfull, vempty: 8 each; wfull, wempty, sfull, pready: 2; qready, mdone)
+    if (lane < 24) mbar_init(bars + lane, 1);
+    else mbar_init(bars + lane, kWiden / 32);
+    if (lane < 10)
+      mbar_init(bars + 32 + lane,
+                lane < 2 ? kWiden / 32 : lane == 6 || lane == 7 || lane == 8 ? 4 * active : 1);
+    if (lane == 0) {
+      *fail = (int)blockIdx.x == a.give_up;
+      *odd = 0;
+      plan.first = first;
+      plan.length = first + a.B + 1;
+      plan.held = plan.length + a.B;
+      plan.count = reinterpret_cast<short*>(plan.held + a.B);
     }
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&wfull[i], kWiden / 32);
-      mbar_init(&wempty[i], 1);
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], 4 * active);
-    }
-    mbar_init(qready, 4 * active);
-    mbar_init(mdone, 1);
-    *fail = (int)blockIdx.x == a.give_up;
-    *odd = 0;
     fence_mbar_init();
+  }
+  if (warp == kCopyWarp && lane < 4) {
+    const CUtensorMap* m = lane == 0 ? &mK8 : lane == 1 ? &mV8 : lane == 2 ? &mK : &mV;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
   if (warp == 0) tmem_alloc(tslot, 512);
 #pragma unroll 1
   for (int b = tid; b < a.B; b += kThreads) {
     const int n = a.lengths[b], h = a.held ? a.held[b] : 0;
     const int c = a.counts ? min(max(a.counts[b], -1), 129) : a.T;  // (129: too many, like all above)
-    plan.length[b] = n;
-    plan.held[b] = h;
-    plan.count[b] = (short)c;
-    plan.first[b + 1] = tiles_of(seq_range_of(a, n, c, h));
+    first[a.B + 1 + b] = n;
+    first[2 * a.B + 1 + b] = h;
+    reinterpret_cast<short*>(first + 3 * a.B + 1)[b] = (short)c;
+    first[b + 1] = tiles_of(seq_range(a, n, c, h));
   }
   if (tid < rows) row_at[tid] = tid / a.G * a.H + tid % a.G;
   // the rows beyond
@@ -499,27 +508,32 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   __syncthreads();
   if (warp == kWidenWarp) {
     int sum = 0;
-    if (lane == 0) plan.first[0] = 0;
+    if (lane == 0) first[0] = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      int x = b0 + lane < a.B ? plan.first[b0 + lane + 1] : 0;
+      int x = b0 + lane < a.B ? first[b0 + lane + 1] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(~0u, x, d);
         if (lane >= d) x += y;
       }
-      if (b0 + lane < a.B) plan.first[b0 + lane + 1] = sum + x;
+      if (b0 + lane < a.B) first[b0 + lane + 1] = sum + x;
       sum += __shfl_sync(~0u, x, 31);
+    }
+    if (lane < 2) {
+      const long long total = (long long)sum * a.Hkv;
+      const int ctas = (int)min((long long)gridDim.x, total);  // each with a tile at least
+      (lane ? plan.end : plan.begin) = cta_start(total, ctas, blockIdx.x + lane);
+      plan.total = total;
+      plan.ctas = ctas;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
-  plan.total = (long long)plan.first[a.B] * a.Hkv;
-  plan.ctas = (int)min((long long)gridDim.x, plan.total);  // each with a tile at least
-  plan.begin = cta_start(plan.total, plan.ctas, blockIdx.x);
-  plan.end = cta_start(plan.total, plan.ctas, blockIdx.x + 1);
+  const long long begin = plan.begin, end = plan.end;
+  Place& place = places[warp];
   auto give_up = [&](bool ok) {
     if (!ok) atomicExch(fail, 1);
   };
@@ -527,7 +541,8 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   if (warp == kCopyWarp || warp == kCopyWarp + 1) {
     // ---- copies of K (first warp) or V tiles, in units of 128 rows of up to
     // 128 bytes: one for a tile of 8-bit rows, a panel of 64 columns each for bf16
-    if (lane == 0) {
+    // (the warp runs together up to the copies themselves)
+    {
       const bool is_v = warp > kCopyWarp;
       const int units = is_v ? lay.v_units : lay.k_units;
       unsigned char* ring = is_v ? vring : kring;
@@ -537,29 +552,38 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       uint32_t phase = 0;
       bool ok = !tree_flagged(fail);
 #pragma unroll 1
-      for (long long at = plan.begin; ok && at < plan.end;) {
-        const Segment s = segment_at(a, plan, at);
-        Walk t = walk_from(s.r, a.window, s.i0);
+      for (long long at = begin; ok && at < end;) {
+        segment_at(a, plan, at, place);
+        const int sn = place.s.n, sb = place.s.b, sh = place.s.h;
+        Walk t = place.w;
 #pragma unroll 1
-        for (int i = 0; ok && i < s.n; ++i) {
+        for (int i = 0; ok && i < sn; ++i) {
 #pragma unroll 1
           for (int u = 0; ok && u < (t.eight ? 1 : P); ++u) {
             if (issued >= units) ok = wait_for(fail, &empty[slot], phase ^ 1u);
+            ok = __all_sync(~0u, ok);
             if (!ok) break;
-            mbar_arrive_expect_tx(&full[slot], t.eight ? 128u * DH : (uint32_t)kUnit);
-            if (t.eight) tma_load_4d(ring + slot * kUnit, m8, 0, t.p0, s.h, s.b, &full[slot]);
-            else tma_load_4d(ring + slot * kUnit, m16, u * 64, t.p0 % a.rows, s.h, s.b, &full[slot]);
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], t.eight ? 128u * DH : (uint32_t)kUnit);
+            if (lane != 0) {
+            } else if (t.eight) tma_load_4d(ring + slot * kUnit, m8, 0, t.p0, sh, sb, &full[slot]);
+            else tma_load_4d(ring + slot * kUnit, m16, u * 64, t.p0 % a.rows, sh, sb, &full[slot]);
             ++issued;
             if (++slot == units) {
               slot = 0;
               phase ^= 1u;
             }
           }
-          if (i + 1 < s.n) step(t, s.r, a.window);
+          if (i + 1 < sn) step(t, place, a.window);
         }
-        at += s.n;
+        at += sn;
       }
       give_up(ok);
+      if (is_v && lane == 0) {
+        // the pair that goes on in the next CTA, and which one has its last tile
+        const Segment& s = place.s;
+        const bool goes_on = begin < end && !s.whole && !s.head;
+        a.shared[blockIdx.x] = goes_on ? make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0) : make_int4(-1, 0, 0, 0);
+      }
       // what is still in flight lands before the memory is released
 #pragma unroll 1
       for (int i = max(0, issued - units); i < issued; ++i)
@@ -628,13 +652,14 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       ++n_s;
     };
 #pragma unroll 1
-    for (long long pos = plan.begin; ok && pos < plan.end; ++segments) {
-      const Segment s = segment_at(a, plan, pos);
+    for (long long pos = begin; ok && pos < end; ++segments) {
+      segment_at(a, plan, pos, place);
+      const int sn = place.s.n, in_eight = place.s.eight;
       wait(qready, (uint32_t)(segments & 1));
       // (one place in the code for the scores: the first tile's before the others')
 #pragma unroll 1
-      for (int i = -1; ok && i < s.n; ++i) {
-        if (i + 1 < s.n) scores(i + 1 < s.eight);
+      for (int i = -1; ok && i < sn; ++i) {
+        if (i + 1 < sn) scores(i + 1 < in_eight);
         if (!ok) break;
         if (i < 0) continue;
         const uint32_t buf = n_p & 1u, ph = (n_p >> 1) & 1u;
@@ -642,7 +667,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         if (!ok) break;
         const uint64_t vd = v_desc(wr + buf * (uint32_t)kWide);
         const uint64_t pd = p_desc(pr + (lay.p_bufs == 2 ? buf * (uint32_t)NP * 256u : 0u));
-        const uint32_t idp = i < s.eight ? idp8 : idp16;
+        const uint32_t idp = i < in_eight ? idp8 : idp16;
 #pragma unroll 1
         for (int k4 = 0; k4 < 8; k4 += 4)
 #pragma unroll
@@ -652,7 +677,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         tree_commit(lead, &wempty[buf]);
         ++n_p;
       }
-      pos += s.n;
+      pos += sn;
     }
     if (!ok && lane == 0) atomicExch(fail, 1);
     tree_commit(lead, mdone);
@@ -662,9 +687,9 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
     const int cw = warp - kWidenWarp, ct = tid - kWidenWarp * 32;
 #pragma unroll 1
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      if (plan.first[b + 1] != plan.first[b]) continue;
+      if (first[b + 1] != first[b]) continue;
       // a sequence without tokens, or without sense
-      const float x = seq_range_of(a, plan.length[b], plan.count[b], plan.held[b]).count < 0 ? NAN : 0.f;
+      const float x = seq_range(a, plan.length[b], plan.count[b], plan.held[b]).count < 0 ? NAN : 0.f;
       const uint32_t w = pack_bf16x2(x, x);
       uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * a.T * a.H * DH);
 #pragma unroll 1
@@ -685,12 +710,13 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       }
     };
 #pragma unroll 1
-    for (long long pos = plan.begin; ok && pos < plan.end;) {
-      const Segment s = segment_at(a, plan, pos);
-      Walk t = walk_from(s.r, a.window, s.i0);
+    for (long long pos = begin; ok && pos < end;) {
+      segment_at(a, plan, pos, place);
+      const int sn = place.s.n;
+      Walk t = place.w;
 #pragma unroll 1
-      for (int i = 0; ok && i < s.n; ++i, ++n) {
-        if (i) step(t, s.r, a.window);
+      for (int i = 0; ok && i < sn; ++i, ++n) {
+        if (i) step(t, place, a.window);
         const bool edge = t.edge();
         const uint32_t buf = n & 1u;
         unsigned char* to = wide + buf * kWide;
@@ -741,28 +767,36 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         }
         if (seldom(edge)) {
           // rows that not all tokens see, two at a time
+          const int kd = row_kind(a, place.s.r, t, t.p0 + cw * 32 + lane);
           __syncwarp();
 #pragma unroll 1
-          for (int k = lane >> 4; k < 32; k += 2) {
-            const int key = cw * 32 + k, kd = row_kind(a, s.r, t, t.p0 + key);
-            uint4* x = reinterpret_cast<uint4*>(to + ((lane >> 3) & 1) * kUnit + key * 128) + (lane & 7);
-            if ((P == 1 && (lane & 8)) || kd == 2) continue;
-            uint4 v = kd == 0 ? make_uint4(0u, 0u, 0u, 0u) : *x;
-            bool bad = false;
+          for (int kind = 0; kind < 2; ++kind) {
+            uint32_t left = __ballot_sync(~0u, kd == kind);
 #pragma unroll 1
-            for (int e = 0; e < 4; ++e) {
-              // (the four words in turn)
-              v = make_uint4(v.y, v.z, v.w, finite_only(v.x, t.eight ? 0x7c007c00u : 0x7f807f80u, bad));
+            while (left) {
+              const uint32_t rest = left & (left - 1), one = lane < 16 || !rest ? left : rest;
+              left = rest & (rest - 1);
+              uint4* x = reinterpret_cast<uint4*>(to + ((lane >> 3) & 1) * kUnit + (cw * 32 + __ffs(one) - 1) * 128) +
+                         (lane & 7);
+              if (P == 1 && (lane & 8)) continue;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (kind) {
+                const uint32_t e = t.eight ? 0x7c007c00u : 0x7f807f80u;
+                bool bad = false;
+                v = *x;
+                v = make_uint4(finite_only(v.x, e, bad), finite_only(v.y, e, bad), finite_only(v.z, e, bad),
+                               finite_only(v.w, e, bad));
+                if (bad) atomicExch(odd, 1);
+              }
+              *x = v;
             }
-            *x = v;
-            if (bad) atomicExch(odd, 1);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&wfull[buf]);
       }
-      pos += s.n;
+      pos += sn;
     }
     if (!ok && lane == 0) atomicExch(fail, 1);
   } else {
@@ -773,7 +807,6 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
     const int nblk = a.max_seq / a.block, shift = 31 - __clz(a.block);
     float* gpart = part + group * 32;
     uint32_t n = 0;                              // tiles so far
-    int4 go_on = make_int4(-1, 0, 0, 0);
     // A wait that gives up is the last that this warp makes; it goes on without
     // (its results are marked in the end), as the others count on it at their
     // common barriers.
@@ -801,14 +834,15 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       tmem_wait_st();
     };
 #pragma unroll 1
-    for (long long at = group < active ? plan.begin : plan.end; at < plan.end;) {
-      const Segment s = segment_at(a, plan, at);
-      const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
-      const int live = s.r.count * a.G;          // rows with a token
+    for (long long at = group < active ? begin : end; at < end;) {
+      segment_at(a, plan, at, place);
+      const Segment& s = place.s;
+      const int sn = s.n;
       // ---- the query's parts: bf16, and e4m3 twice under a power of two
       {
         constexpr int kEach = DH / 8;            // threads per row, 8 elements each
-        const int c = key % kEach;
+        const int c = key % kEach, live = s.r.count * a.G;
+        const bf16* src = a.q + ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH + c * 8;
 #pragma unroll 1
         for (int r0 = 0; r0 < chunks * 8; r0 += 8 * kGroups) {
 #pragma unroll
@@ -816,7 +850,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
             const int row = r0 + group * 8 + r1 + key / kEach;
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (row < live && r1 + key / kEach < 8)
-              x = *reinterpret_cast<const uint4*>(a.q + out0 + (size_t)row_at[row] * DH + c * 8);
+              x = *reinterpret_cast<const uint4*>(src + (size_t)row_at[row] * DH);
             uint32_t w[4] = {x.x, x.y, x.z, x.w}, most = 0, hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < 4; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
@@ -887,10 +921,10 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
           vs = vscale[blk];
         }
       };
-      Walk t = walk_from(s.r, a.window, s.i0);
+      Walk t = place.w;
       fetch(t);
 #pragma unroll 1
-      for (int i = 0; i < s.n; ++i, ++n) {
+      for (int i = 0; i < sn; ++i, ++n) {
         const uint32_t buf = n & 1u;
         const bool eight = t.eight, edge = t.edge();
         const float kc = ks, vc = eight ? vs : 1.f;
@@ -901,7 +935,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         if (seldom(edge)) {
           const int j = t.p0 + key;
           r0 = max(j - s.r.length, 0) * a.G;
-          r1 = live;
+          r1 = s.r.count * a.G;
           if (a.window && j >= a.sinks) {
             const long long last = (long long)j + a.window - s.r.length;
             if (last < s.r.count) r1 = last < 0 ? 0 : (int)last * a.G;
@@ -909,8 +943,8 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
           if (j < t.rs || j >= t.re) r1 = 0;
           over = over && t.p0 + w4 * 32 < t.re && t.p0 + w4 * 32 + 32 > t.rs;
         }
-        if (i + 1 < s.n) {
-          step(t, s.r, a.window);
+        if (i + 1 < sn) {
+          step(t, place, a.window);
           fetch(t);
         }
         wait_w(&sfull[buf], (n >> 1) & 1u);
@@ -1027,8 +1061,8 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       wait_values(n);
       const bool bad = tree_flagged(odd);
       const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
-      if (!s.whole && !s.head)                   // which CTA has the pair's last tile
-        go_on = make_int4(s.b, s.h, last_cta(a, plan, s.b, s.h), 0);
+      const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
+      const int live = s.r.count * a.G;          // rows with a token
 #pragma unroll 1
       for (int q = group; q < chunks; q += kGroups) {
         // the sums over the keys: a warp's, then the four warps'
@@ -1078,19 +1112,18 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
             }
         }
       }
-      at += s.n;
+      at += sn;
     }
-    if (tid == 0) a.shared[blockIdx.x] = go_on;
   }
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  if (tree_flagged(fail)) mark_rows(a, plan);
+  if (tree_flagged(fail)) mark_rows(a, plan, place);
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // Joins a pair that several CTAs share: CTA x = the first of them, thread = 16
-// bytes of a row's output; the parts are added in order, four in flight.
+// bytes of a row's output; the parts are added in order, 16 in flight.
 constexpr int kJoinThreads = 256;
 template <int DH>
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
@@ -1104,7 +1137,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
   auto place = [&](int k) { return k == 0 ? (size_t)c0 * 2 + 1 : (size_t)(c0 + k) * 2; };
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 16;
   for (int k0 = 0; k0 < n; k0 += kBatch) {
     float pm[kBatch], pl[kBatch], mn = m;
     float4 v[kBatch];
@@ -1142,18 +1175,18 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
   *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int DH, bool SMALL>
+template <int DH, bool SMALL, int kGroups>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream_t st) {
   const Layout lay = layout_of(a.T * a.G, DH, a.B);
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, SMALL>,
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, SMALL, kGroups>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  cache_attn_tc_kernel<DH, SMALL><<<a.ctas, threads_of(SMALL), lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
+  cache_attn_tc_kernel<DH, SMALL, kGroups><<<a.ctas, threads_of(kGroups), lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1208,9 +1241,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   m[1] = m[3];
   if (a.k8 && (!map(&m[0], true, a.k8, a.max_seq, a.seq8_stride) || !map(&m[1], true, a.v8, a.max_seq, a.seq8_stride)))
     return cudaErrorInvalidValue;
-  const bool few = a.T * a.G <= 16;
-  if (a.dh == 128) return few ? launch<128, true>(a, m, s) : launch<128, false>(a, m, s);
-  return few ? launch<64, true>(a, m, s) : launch<64, false>(a, m, s);
+  const int rows = a.T * a.G;
+  if (a.dh == 128)
+    return rows <= 8    ? launch<128, true, 1>(a, m, s)
+           : rows <= 16 ? launch<128, true, 2>(a, m, s)
+                        : launch<128, false, 2>(a, m, s);
+  return rows <= 8 ? launch<64, true, 1>(a, m, s) : rows <= 16 ? launch<64, true, 2>(a, m, s) : launch<64, false, 2>(a, m, s);
 }
 
 }  // namespace ssd

@@ -22,7 +22,7 @@ ROPE = dict(qkv=MB, B=2, T=4, lengths=P, counts=P, positions=P, q_gain=P, k_gain
 
 
 @pytest.mark.parametrize("change", [
-    dict(qkv=None), dict(qkv=MB + 8), dict(B=0), dict(B=1025), dict(T=0), dict(T=257), dict(H=65536, T=256, B=1024, dh=128, rows=2**20, stride=2**40), dict(lengths=None),
+    dict(qkv=None), dict(qkv=MB + 8), dict(B=0), dict(B=513), dict(T=0), dict(T=257), dict(H=65536, T=256, B=512, dh=128, rows=2**20, stride=2**40), dict(lengths=None),
     dict(lengths=P + 2), dict(counts=P + 1), dict(positions=P + 1), dict(q_gain=P + 4), dict(k_gain=P + 8),
     dict(eps=-1.0), dict(eps=float("nan")), dict(theta=0.0), dict(theta=float("inf")), dict(k=None),
     dict(v=32 * MB + 8), dict(rows=0), dict(stride=ONE - 8), dict(stride=ONE + 4), dict(H=0), dict(Hkv=0),
@@ -56,7 +56,7 @@ ATTN = dict(q=MB, B=2, T=4, lengths=P, counts=P, k=16 * MB, v=32 * MB, rows=256,
 
 
 @pytest.mark.parametrize("change", [
-    dict(q=None), dict(q=MB + 8), dict(B=0), dict(B=1025), dict(T=0), dict(T=65), dict(H=3), dict(H=0),
+    dict(q=None), dict(q=MB + 8), dict(B=0), dict(B=513), dict(T=0), dict(T=65), dict(H=3), dict(H=0),
     dict(H=258), dict(Hkv=0), dict(dh=96), dict(lengths=None), dict(counts=P + 1), dict(k=None),
     dict(v=None), dict(rows=0), dict(stride=ONE - 8), dict(k8=None), dict(v8=None), dict(ks=None),
     dict(vs=None), dict(held=None), dict(held=P + 2), dict(max_seq=500), dict(block=96), dict(stride8=16),
@@ -81,7 +81,7 @@ VERIFY = dict(p=MB, q=2 * MB, drafts=P, counts=P, au=P, su=P, B=2, d=4, V=100, t
 
 @pytest.mark.parametrize("change", [
     dict(p=None), dict(p=MB + 2), dict(q=2 * MB + 1), dict(drafts=None), dict(counts=P + 1), dict(au=None),
-    dict(su=None), dict(B=0), dict(B=1025), dict(d=-1), dict(d=1025), dict(V=0), dict(V=2**30 + 1), dict(tokens=None),
+    dict(su=None), dict(B=0), dict(B=513), dict(d=-1), dict(d=1025), dict(V=0), dict(V=2**30 + 1), dict(tokens=None),
     dict(n=None), dict(n=P + 1), dict(tokens=P), dict(tokens=P + 28)])
 def test_verify_drafts(lib, change):
     assert lib.ssd_op_verify_drafts(*{**VERIFY, **change}.values()) == INVALID

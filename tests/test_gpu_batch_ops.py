@@ -206,8 +206,8 @@ def test_cache_quantize_refuses_senseless_sequences_alone(ops):
 
 def test_cache_quantize_many_sequences_and_layers(ops):
     rng = np.random.default_rng(5)
-    held = [int(x) * 32 for x in rng.integers(0, 4, 1024)]
-    run_quantize(ops, held, [h + int(x) for h, x in zip(held, rng.integers(0, 100, 1024))], 1, 64, 32, 128, 256)
+    held = [int(x) * 32 for x in rng.integers(0, 4, 512)]
+    run_quantize(ops, held, [h + int(x) for h, x in zip(held, rng.integers(0, 100, 512))], 1, 64, 32, 128, 256)
     run_quantize(ops, [0, 64], [200, 300], 3, 128, 64, 256, 320, layers=3)
 
 
@@ -363,7 +363,7 @@ def test_uneven_sequences(ops):
 
 def test_many_short_sequences(ops):
     rng = np.random.default_rng(4)
-    lengths = [int(x) for x in rng.integers(0, 9, 1024)]
+    lengths = [int(x) for x in rng.integers(0, 9, 512)]
     a = Attn(lengths, 1, 2, 1, 64, 10)
     a.check(a.call(ops))
 
@@ -697,8 +697,8 @@ def test_verify_many_drafts_and_sequences(ops):
     rng = np.random.default_rng(3)
     p = probabilities(rng, 3, 1025, 40)
     run_verify(ops, p, None, p[:, :1024].argmax(-1), rng.random((3, 1024)) * 1e-3, rng.random(3))
-    p = probabilities(rng, 1024, 3, 50)
-    run_verify(ops, p, probabilities(rng, 1024, 2, 50), rng.integers(0, 50, (1024, 2)), rng.random((1024, 2)), rng.random(1024))
+    p = probabilities(rng, 512, 3, 50)
+    run_verify(ops, p, probabilities(rng, 512, 2, 50), rng.integers(0, 50, (512, 2)), rng.random((512, 2)), rng.random(512))
 
 
 # --------------------------------------------------------------------------
