@@ -30,11 +30,13 @@
 // lengths on the device, so that a graph follows them.
 //
 // The softmax is a chain of latencies (scores out of tensor memory, a vote, the
-// exponentials) and no unit's full load, so that several groups of four warps
-// take 8 rows of a tile each, in turn.
+// exponentials) and no unit's full load, so that two or three groups of four warps
+// share it: 8 rows of a tile each, in turn, or with up to 8 rows every other tile (each
+// with maxima and outputs of its own, joined in the end).  The matrix
+// instructions' chain of waits and issues is shared by two warps likewise.
 //
-// Warps 0 .. 4 groups - 1: softmax and results; then four warps that widen V, one
-// that copies K, one that copies V, one for the matrix instructions.  Every wait is
+// The groups' warps come first, then four that widen V, one that copies K, one that
+// copies V, one for the products K q^T and one for V^T P.  Every wait is
 // bounded: one that gives up sets the CTA's flag, every role runs out, and the
 // CTA's rows become NaN.
 #include <cuda_fp16.h>
@@ -156,6 +158,8 @@ SSD_DI bool wait_for(const int* fail, uint64_t* a, uint32_t pa) {
 }
 // The barrier of a group of four softmax warps.
 SSD_DI void bar_group(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+// Of both groups.
+SSD_DI void bar_both() { asm volatile("bar.sync 4, 256;" ::: "memory"); }
 // 8 columns of the thread's tensor memory lane.
 SSD_DI void tmem_ld8_nw(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -423,13 +427,15 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
 
 // SMALL: up to 16 rows, whose parts of q make one product (twice as wide) and
 // whose state the groups keep in registers.
-constexpr int threads_of(int groups) { return (4 * groups + 7) * 32; }
-template <int DH, bool SMALL, int kGroups>
-__global__ void __launch_bounds__(threads_of(kGroups), 1)
+// TURNS: up to 8 rows, the groups take the tiles in turn.
+constexpr int groups_of(bool small) { return small ? 2 : 3; }
+constexpr int threads_of(bool small) { return (4 * groups_of(small) + 8) * 32; }
+template <int DH, bool SMALL, bool TURNS>
+__global__ void __launch_bounds__(threads_of(SMALL), 1)
     cache_attn_tc_kernel(const __grid_constant__ CUtensorMap mK8, const __grid_constant__ CUtensorMap mV8,
                          const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                          const __grid_constant__ CacheAttnArgs a, const Layout lay) {
-  constexpr int kThreads = threads_of(kGroups);
+  constexpr int kGroups = groups_of(SMALL), kThreads = threads_of(SMALL);
   constexpr int kWidenWarp = 4 * kGroups, kCopyWarp = kWidenWarp + 4, kMmaWarp = kCopyWarp + 2;
   constexpr int P = DH / 64;                     // 16-bit panels of 64 columns
   constexpr int kWide = P * kUnit;               // a V tile in 16 bits
@@ -456,25 +462,27 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
   uint64_t* sfull = wempty + 2;                  // [2]
   uint64_t* pready = sfull + 2;                  // [2]
   uint64_t* qready = pready + 2;
-  uint64_t* mdone = qready + 1;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 1);
+  uint64_t* mdone = qready + 1;                  // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 2);
   int* fail = reinterpret_cast<int*>(tslot + 1);
   int* odd = fail + 1;                           // a V element that is not finite was left out
-  Plan& plan = *reinterpret_cast<Plan*>(bars + 44);
+  Plan& plan = *reinterpret_cast<Plan*>(bars + 46);
   Place* places = reinterpret_cast<Place*>(bars + 64);  // of the warps
   int* first = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(row_c) + kSmall);  // the plan's arrays
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.T * a.G, chunks = (rows + 7) / 8;
-  const int active = min(kGroups, chunks);       // groups with any rows
+  const int active = TURNS ? kGroups : min(kGroups, chunks);  // groups with any rows
 
   // ---- set-up
   if (warp == kMmaWarp) {
-    // (kfull, kempty, vfull, vempty: 8 each; wfull, wempty, sfull, pready: 2; qready, mdone)
+    // (kfull, kempty, vfull, vempty: 8 each; wfull, wempty, sfull, pready: 2; qready; mdone: 2)
     if (lane < 24) mbar_init(bars + lane, 1);
     else mbar_init(bars + lane, kWiden / 32);
-    if (lane < 10)
-      mbar_init(bars + 32 + lane,
-                lane < 2 ? kWiden / 32 : lane == 6 || lane == 7 || lane == 8 ? 4 * active : 1);
+    if (lane < 11)
+      mbar_init(bars + 32 + lane, lane < 2                ? kWiden / 32
+                                  : lane == 6 || lane == 7 ? (TURNS ? 4 : 4 * active)
+                                  : lane == 8              ? (TURNS ? 4 : 4 * active)
+                                                           : 1);
     if (lane == 0) {
       *fail = (int)blockIdx.x == a.give_up;
       *odd = 0;
@@ -589,99 +597,102 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
       for (int i = max(0, issued - units); i < issued; ++i)
         mbar_wait_n(&full[i % units], (uint32_t)((i / units) & 1), kPolls);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ---- products: the warp runs together, one lane issues
     const uint32_t lead = tree_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t kr = smem_addr(kring), wr = smem_addr(wide), pr = smem_addr(psm);
-    const uint32_t qa8 = smem_addr(q8), qa16 = smem_addr(q16);
-    const uint32_t id8 = idesc_e4m3((int)scols), id16 = idesc_e4m3(NP) | 1u << 7 | 1u << 10;
-    // (both operands MN-major; fp16, bf16)
-    const uint32_t idp8 = idesc_e4m3(NP) | 3u << 15, idp16 = idp8 | 1u << 7 | 1u << 10;
-    int kslot = 0;
-    uint32_t kphase = 0;
-    auto next_k = [&]() {
-      if (++kslot == lay.k_units) {
-        kslot = 0;
-        kphase ^= 1u;
-      }
-    };
-    int segments = 0;
-    uint32_t n_s = 0, n_p = 0;                   // tiles whose scores / values were issued
     bool ok = !tree_flagged(fail);
-    auto wait = [&](uint64_t* bar, uint32_t parity, uint64_t* other = nullptr, uint32_t other_parity = 0) {
-      ok = __all_sync(0xffffffffu, ok && wait_for(fail, bar, parity) && (!other || wait_for(fail, other, other_parity)));
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && wait_for(fail, bar, parity));
       tc_fence_after();
     };
-    auto scores = [&](bool eight) {
-      const uint32_t d = tm + (n_s & 1u) * scols;
-      const int k0 = kslot;
-      wait(&kfull[k0], kphase);
-      if (!ok) return;
-      const uint32_t kb = kr + (uint32_t)k0 * kUnit;
-      next_k();
-      if (!seldom(!eight)) {
-        const uint64_t kd = DH == 128 ? sw128_desc(kb) : sw64_desc(kb);
-        uint64_t qd = DH == 128 ? sw128_desc(qa8) : sw64_desc(qa8);
-        // (the low part first)
-        if (!SMALL) qd += (uint64_t)((uint32_t)(NP * DH) >> 4);
-#pragma unroll 1
-        for (int part = SMALL ? 1 : 0; part < 2; ++part) {
-#pragma unroll
-          for (int ks = 0; ks < DH / 32; ++ks)
-            mma_ss_e4m3(lead, d, kd + 2 * ks, qd + 2 * ks, id8, (!SMALL && part) || ks > 0 ? 1u : 0u);
-          qd -= (uint64_t)((uint32_t)(NP * DH) >> 4);
+    uint32_t n = 0;                              // tiles so far
+    if (warp == kMmaWarp) {
+      // scores: K q^T
+      const uint32_t kr = smem_addr(kring), qa8 = smem_addr(q8), qa16 = smem_addr(q16);
+      const uint32_t id8 = idesc_e4m3((int)scols), id16 = idesc_e4m3(NP) | 1u << 7 | 1u << 10;
+      const uint64_t low = (uint64_t)((uint32_t)(NP * DH) >> 4);
+      uint32_t kphase = 0, segments = 0;
+      int kslot = 0;
+      auto next_k = [&]() {
+        if (++kslot == lay.k_units) {
+          kslot = 0;
+          kphase ^= 1u;
         }
-      } else {
+      };
 #pragma unroll 1
-        for (int u = 0; u < P; ++u) {
-          if (u) wait(&kfull[kslot], kphase);
-          if (!ok) return;
-          const uint64_t kd = sw128_desc(kr + (uint32_t)(u ? kslot : k0) * kUnit);
-          const uint64_t qd = sw128_desc(qa16 + (uint32_t)(u * NP) * 128);
+      for (long long pos = begin; ok && pos < end; ++segments) {
+        segment_at(a, plan, pos, place);
+        const int sn = place.s.n, in_eight = place.s.eight;
+        wait(qready, segments & 1u);
+#pragma unroll 1
+        for (int i = 0; ok && i < sn; ++i, ++n) {
+          const uint32_t buf = n & 1u, d = tm + buf * scols;
+          // the softmax has read what was in this place
+          if (n >= 2) wait(&pready[buf], ((n >> 1) & 1u) ^ 1u);
+          wait(&kfull[kslot], kphase);
+          if (!ok) break;
+          if (!seldom(i >= in_eight)) {
+            const uint32_t kb = kr + (uint32_t)kslot * kUnit;
+            const uint64_t kd = DH == 128 ? sw128_desc(kb) : sw64_desc(kb);
+            const uint64_t qd = DH == 128 ? sw128_desc(qa8) : sw64_desc(qa8);
+            // (the low part first)
+            if (!SMALL)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) tree_mma_ss(lead, d, kd + 2 * ks, qd + 2 * ks, id16, u || ks > 0 ? 1u : 0u);
+              for (int ks = 0; ks < DH / 32; ++ks)
+                mma_ss_e4m3(lead, d, kd + 2 * ks, qd + low + 2 * ks, id8, ks > 0 ? 1u : 0u);
+#pragma unroll
+            for (int ks = 0; ks < DH / 32; ++ks)
+              mma_ss_e4m3(lead, d, kd + 2 * ks, qd + 2 * ks, id8, !SMALL || ks > 0 ? 1u : 0u);
+            tree_commit(lead, &sfull[buf]);
+            tree_commit(lead, &kempty[kslot]);
+            next_k();
+          } else {
+#pragma unroll 1
+            for (int u = 0; ok && u < P; ++u) {
+              if (u) wait(&kfull[kslot], kphase);
+              if (!ok) break;
+              const uint64_t kd = sw128_desc(kr + (uint32_t)kslot * kUnit);
+              const uint64_t qd = sw128_desc(qa16 + (uint32_t)(u * NP) * 128);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) tree_mma_ss(lead, d, kd + 2 * ks, qd + 2 * ks, id16, u || ks > 0 ? 1u : 0u);
+              if (u + 1 == P) tree_commit(lead, &sfull[buf]);
+              tree_commit(lead, &kempty[kslot]);
+              next_k();
+            }
+          }
         }
+        pos += sn;
       }
-      tree_commit(lead, &sfull[n_s & 1u]);
-      tree_commit(lead, &kempty[k0]);
-      if (!eight && P == 2) {
-        tree_commit(lead, &kempty[kslot]);
-        next_k();
-      }
-      ++n_s;
-    };
+    } else {
+      // values: V^T P
+      const uint32_t wr = smem_addr(wide), pr = smem_addr(psm);
+      // (both operands MN-major; fp16, bf16)
+      const uint32_t idp8 = idesc_e4m3(NP) | 3u << 15, idp16 = idp8 | 1u << 7 | 1u << 10;
 #pragma unroll 1
-    for (long long pos = begin; ok && pos < end; ++segments) {
-      segment_at(a, plan, pos, place);
-      const int sn = place.s.n, in_eight = place.s.eight;
-      wait(qready, (uint32_t)(segments & 1));
-      // (one place in the code for the scores: the first tile's before the others')
+      for (long long pos = begin; ok && pos < end;) {
+        segment_at(a, plan, pos, place);
+        const int sn = place.s.n, in_eight = place.s.eight;
 #pragma unroll 1
-      for (int i = -1; ok && i < sn; ++i) {
-        if (i + 1 < sn) scores(i + 1 < in_eight);
-        if (!ok) break;
-        if (i < 0) continue;
-        const uint32_t buf = n_p & 1u, ph = (n_p >> 1) & 1u;
-        wait(&wfull[buf], ph, &pready[buf], ph);
-        if (!ok) break;
-        const uint64_t vd = v_desc(wr + buf * (uint32_t)kWide);
-        const uint64_t pd = p_desc(pr + (lay.p_bufs == 2 ? buf * (uint32_t)NP * 256u : 0u));
-        const uint32_t idp = i < in_eight ? idp8 : idp16;
-#pragma unroll 1
-        for (int k4 = 0; k4 < 8; k4 += 4)
+        for (int i = 0; ok && i < sn; ++i, ++n) {
+          const uint32_t buf = n & 1u, ph = (n >> 1) & 1u;
+          wait(&wfull[buf], ph);
+          wait(&pready[buf], ph);
+          if (!ok) break;
+          const uint64_t vd = v_desc(wr + buf * (uint32_t)kWide);
+          const uint64_t pd = p_desc(pr + (lay.p_bufs == 2 ? buf * (uint32_t)NP * 256u : 0u));
+          const uint32_t idp = i < in_eight ? idp8 : idp16, d = tm + col_o + (TURNS ? buf * 16u : 0u);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tree_mma_ss(lead, tm + col_o, vd + 128 * (k4 + ks), pd + 32 * (k4 + ks), idp,
-                        (i > 0 || k4 > 0 || ks > 0) ? 1u : 0u);
-        tree_commit(lead, &wempty[buf]);
-        ++n_p;
+          for (int ks = 0; ks < 8; ++ks)
+            tree_mma_ss(lead, d, vd + 128 * ks, pd + 32 * ks, idp, (i > (TURNS ? 1 : 0) || ks > 0) ? 1u : 0u);
+          tree_commit(lead, &wempty[buf]);
+        }
+        pos += sn;
       }
-      pos += sn;
     }
     if (!ok && lane == 0) atomicExch(fail, 1);
-    tree_commit(lead, mdone);
-    mbar_wait_n(mdone, 0u, kPolls);
+    tree_commit(lead, &mdone[warp - kMmaWarp]);
+    mbar_wait_n(&mdone[warp - kMmaWarp], 0u, kPolls);
   } else if (warp >= kWidenWarp) {
     // ---- V to 16 bits in the products' layout
     const int cw = warp - kWidenWarp, ct = tid - kWidenWarp * 32;
@@ -801,7 +812,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
     if (!ok && lane == 0) atomicExch(fail, 1);
   } else {
     // ---- softmax and results: one thread per key of a tile and group, then per
-    // column of V; group g has rows 8 q .. 8 q + 7 for q = g, g + groups, ...
+    // column of V; group g has rows 8 q .. 8 q + 7 for q = g, g + groups, ..., or all
+    // rows of tiles n = g, g + groups, ...
     const int group = warp >> 2, w4 = warp & 3, key = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
     const int nblk = a.max_seq / a.block, shift = 31 - __clz(a.block);
@@ -818,19 +830,21 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
       }
       tc_fence_after();
     };
-    // The products V^T P of the first `done` tiles: those of the last but two are
-    // done (the scores that followed them are here), so that the last one's barrier
-    // has one phase at most to go and its parity tells.
+    // The products V^T P of tile `done` - 1 (the barrier's phase before has been
+    // waited for, so that its parity tells).
     auto wait_values = [&](uint32_t done) { wait_w(&wempty[(done - 1) & 1u], ((done - 1) >> 1) & 1u); };
+    const int q0 = TURNS ? 0 : group, q_step = TURNS ? 1 : kGroups;
+    const int s0 = TURNS ? group : 0;            // where the rows' state lies: chunk s0 + q
+    const uint32_t col_mine = col_o + (TURNS ? group * 16u : 0u);
     // Columns of O of 8 rows times f, or all.
     auto rescale = [&](int q, const float* f, float all) {
       uint32_t o[8];
-      tmem_ld8_nw(trow + col_o + q * 8, o);
+      tmem_ld8_nw(trow + col_mine + q * 8, o);
       tmem_wait_ld();
       tmem_pin8(o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (f ? f[e] : all));
-      tmem_st8(trow + col_o + q * 8, o);
+      tmem_st8(trow + col_mine + q * 8, o);
       tmem_wait_st();
     };
 #pragma unroll 1
@@ -844,10 +858,10 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         const int c = key % kEach, live = s.r.count * a.G;
         const bf16* src = a.q + ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH + c * 8;
 #pragma unroll 1
-        for (int r0 = 0; r0 < chunks * 8; r0 += 8 * kGroups) {
+        for (int r0 = q0 * 8; r0 < (TURNS && group ? 0 : chunks * 8); r0 += q_step * 8) {
 #pragma unroll
           for (int r1 = 0; r1 < 8; r1 += 128 / kEach) {
-            const int row = r0 + group * 8 + r1 + key / kEach;
+            const int row = r0 + r1 + key / kEach;
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (row < live && r1 + key / kEach < 8)
               x = *reinterpret_cast<const uint4*>(src + (size_t)row_at[row] * DH);
@@ -882,11 +896,13 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
             if (c == 0)
               row_c[row] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
           }
-          if (key < 8 && r0 + group * 8 < chunks * 8) row_nm[r0 + group * 8 + key] = -kNone;
+          if (key < 8) row_nm[r0 + key] = -kNone;
         }
+        if (TURNS && group && key < 8) row_nm[8 + key] = -kNone;
         fence_proxy_async_smem();
-        bar_group(group);
-        if (lane == 0) mbar_arrive_cta(qready);
+        if (TURNS) bar_both();
+        else bar_group(group);
+        if (lane == 0 && (!TURNS || group == 0)) mbar_arrive_cta(qready);
       }
       // ---- tiles
       // O holds sums of 2^(score - m) v 2^7 / vref
@@ -896,19 +912,19 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
           const float4 u = *reinterpret_cast<const float4*>(row_c + q * 8 + e);
-          const float4 w = *reinterpret_cast<const float4*>(row_nm + q * 8 + e);
+          const float4 w = *reinterpret_cast<const float4*>(row_nm + (s0 + q) * 8 + e);
           c[e] = u.x, c[e + 1] = u.y, c[e + 2] = u.z, c[e + 3] = u.w;
           nm[e] = w.x, nm[e + 1] = w.y, nm[e + 2] = w.z, nm[e + 3] = w.w;
         }
       };
       if (SMALL) {
-        state(group);
+        state(q0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) ls[e] = 0.f;
       } else {
         const uint32_t zero[8] = {};
 #pragma unroll 1
-        for (int q = group; q < chunks; q += kGroups) tmem_st8(trow + col_l + q * 8, zero);
+        for (int q = q0; q < chunks; q += q_step) tmem_st8(trow + col_l + q * 8, zero);
         tmem_wait_st();
       }
       const float* kscale = a.k_scale + (size_t)s.b * a.scale_stride + (size_t)s.h * nblk;
@@ -922,9 +938,16 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         }
       };
       Walk t = place.w;
-      fetch(t);
+      // (TURNS: the tiles that the other group takes are passed by)
+      int i = TURNS ? (int)((n ^ (uint32_t)group) & 1u) : 0;
+      const int i_first = i;
+      if (TURNS) {
+        n += i;
+        if (i && i < sn) step(t, place, a.window);
+      }
+      if (i < sn) fetch(t);
 #pragma unroll 1
-      for (int i = 0; i < sn; ++i, ++n) {
+      for (; i < sn; i += TURNS ? 2 : 1, n += TURNS ? 2 : 1) {
         const uint32_t buf = n & 1u;
         const bool eight = t.eight, edge = t.edge();
         const float kc = ks, vc = eight ? vs : 1.f;
@@ -943,54 +966,58 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
           if (j < t.rs || j >= t.re) r1 = 0;
           over = over && t.p0 + w4 * 32 < t.re && t.p0 + w4 * 32 + 32 > t.rs;
         }
-        if (i + 1 < sn) {
+        if (i + (TURNS ? 2 : 1) < sn) {
+          if (TURNS) step(t, place, a.window);
           step(t, place, a.window);
           fetch(t);
         }
         wait_w(&sfull[buf], (n >> 1) & 1u);
-        if (lay.p_bufs == 1 && n > 0) wait_values(n);  // P's only place is free
+        if (n >= 2) wait_w(&wempty[buf], ((n >> 1) & 1u) ^ 1u);  // P's place is free
+        if (!SMALL && lay.p_bufs == 1 && n > 0) wait_values(n);  // (its only one)
         float pv = vc * unit;
         unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
 #pragma unroll 1
-        for (int q = group; q < chunks; q += kGroups) {
+        for (int q = q0; q < chunks; q += q_step) {
           uint32_t x[8], y[8];
           const uint32_t scol = trow + buf * scols + q * 8;
           tmem_ld8_nw(scol, x);
           tmem_ld8_nw(SMALL ? scol + 16 : trow + col_l + q * 8, y);
           if (!SMALL) state(q);
-          float f[8], d[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = eight ? c[e] * kc : a.scale_log2;
           const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
           const uint32_t seen = m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
           tmem_wait_ld();
           tmem_pin8(x);
           tmem_pin8(y);
-          if (SMALL && eight)                    // the low part's product
+          // scores (of the products' two parts), as multiples of what the exponential takes
+          float d[8];
+          auto scores = [&]() {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
-          auto below = [&]() {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = fmaf(__uint_as_float(x[e]), f[e], nm[e]);
+            for (int e = 0; e < 8; ++e) {
+              d[e] = __uint_as_float(x[e]);
+              if (SMALL && eight) d[e] += __uint_as_float(y[e]);
+              d[e] *= eight ? c[e] * kc : a.scale_log2;
+            }
             if (seldom(edge))
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (!((seen >> e) & 1u)) d[e] = -INFINITY;
           };
-          below();
+          scores();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] += nm[e];
           const float top = tree_max3(tree_max3(d[0], d[1], d[2]), tree_max3(d[3], d[4], d[5]), fmaxf(d[6], d[7]));
           if (seldom(any_group(group, top > kRaise || over || vref == 0.f))) {
-            if (q == group) {
+            if (q == q0) {
               // the largest of the four warps' scales
               if (lane == 0) gpart[w4] = over ? fabsf(vc) : 0.f;
               bar_group(group);
               const float most = fmaxf(fmaxf(gpart[0], gpart[1]), fmaxf(gpart[2], gpart[3]));
               if (most > vref || vref == 0.f) {
                 const float next = most > 0.f ? power_above(most) * 4.f : 1.f;
-                if (i > 0) {
-                  wait_values(n);
+                if (i > i_first) {
+                  if (!TURNS) wait_values(n);
 #pragma unroll 1
-                  for (int z = group; z < chunks; z += kGroups) rescale(z, nullptr, vref / next);
+                  for (int z = q0; z < chunks; z += q_step) rescale(z, nullptr, vref / next);
                 }
                 vref = next;
                 unit = 0x1p7f / next;
@@ -1000,33 +1027,44 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
               bar_group(group);
             }
             // the rows' largest scores of all keys; those that pass m + 8 become m
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              d[e] = edge && !((seen >> e) & 1u) ? -INFINITY : __uint_as_float(x[e]) * f[e];
+            tmem_ld8_nw(scol, x);
+            if (SMALL) tmem_ld8_nw(scol + 16, y);
+            tmem_wait_ld();
+            tmem_pin8(x);
+            tmem_pin8(y);
+            scores();
             over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
             if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = d[0];
             bar_group(group);
             if (key < 8) {
-              const float old = -row_nm[q * 8 + key];
+              const int at_row = (s0 + q) * 8 + key;
+              const float old = -row_nm[at_row];
               const float z = fmaxf(fmaxf(gpart[key], gpart[8 + key]), fmaxf(gpart[16 + key], gpart[24 + key]));
               const float m = z > old + kRaise ? z : old;
-              row_f[q * 8 + key] = tree_ex2(old - m);
-              row_nm[q * 8 + key] = -m;
+              row_f[at_row] = tree_ex2(old - m);
+              row_nm[at_row] = -m;
             }
             bar_group(group);
             float g[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              g[e] = row_f[q * 8 + e];
-              nm[e] = row_nm[q * 8 + e];
+              g[e] = row_f[(s0 + q) * 8 + e];
+              nm[e] = row_nm[(s0 + q) * 8 + e];
               if (SMALL) ls[e] *= g[e];
               else y[e] = __float_as_uint(__uint_as_float(y[e]) * g[e]);
             }
-            if (i > 0) {
-              wait_values(n);                    // O as the tile before left it
+            if (i > i_first) {                   // (O as the tile before left it)
+              if (!TURNS) wait_values(n);
               rescale(q, g, 1.f);
             }
-            below();
+            tmem_ld8_nw(scol, x);
+            if (SMALL) tmem_ld8_nw(scol + 16, y);
+            tmem_wait_ld();
+            tmem_pin8(x);
+            if (SMALL) tmem_pin8(y);
+            scores();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] += nm[e];
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -1058,13 +1096,19 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         if (lane == 0) mbar_arrive_cta(&pready[buf]);
       }
       // ---- the run's result: final, or a part of the pair's
-      wait_values(n);
+      const bool any = i_first < sn;             // (TURNS: the group had a tile)
+      if (TURNS) {
+        if (any) wait_values(n - 1);             // (n - 2 was the last)
+        n = n - i + sn;                          // tiles so far, of both groups
+      } else {
+        wait_values(n);
+      }
       const bool bad = tree_flagged(odd);
       const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
       const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
       const int live = s.r.count * a.G;          // rows with a token
 #pragma unroll 1
-      for (int q = group; q < chunks; q += kGroups) {
+      for (int q = q0; q < chunks; q += q_step) {
         // the sums over the keys: a warp's, then the four warps'
         if (!SMALL) {
           uint32_t y[8];
@@ -1077,40 +1121,78 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         over_lanes(ls, [](float u, float w) { return u + w; });
         if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = ls[0];
         bar_group(group);
+        float m = kNone, l = 0.f;
         if (key < 8) {
-          const int row = q * 8 + key;
-          const float l = (gpart[key] + gpart[8 + key]) + (gpart[16 + key] + gpart[24 + key]);
-          row_f[row] = row < live ? 0x1p-7f * vref * (!s.whole ? 1.f : l != 0.f ? 1.f / l : 0.f) : 0.f;
-          if (!s.whole && row < rows) {
-            a.part_m[slot * rows + row] = -row_nm[row];
-            a.part_l[slot * rows + row] = row < live ? l : 0.f;
-          }
+          m = -row_nm[(s0 + q) * 8 + key];
+          l = (gpart[key] + gpart[8 + key]) + (gpart[16 + key] + gpart[24 + key]);
         }
-        bar_group(group);
-        if (DH == 128 || w4 < 2) {
-          const int most = min(8, rows - q * 8);
-          bf16* out = a.out + out0 + key;
-          float* po = a.part_o + (slot * rows + q * 8) * DH + key;
-          uint32_t o[8];
-          tmem_ld8_nw(trow + col_o + q * 8, o);
+        uint32_t o[8];
+        if (any) {
+          tmem_ld8_nw(trow + col_mine + q * 8, o);
           tmem_wait_ld();
           tmem_pin8(o);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int row = q * 8 + e;
-            const float w = row < live ? __uint_as_float(o[e]) * row_f[row] : 0.f;
-            if (row < rows && s.whole) out[row_at[row] * DH] = __float2bfloat16(w);
-            if (row < rows && !s.whole) po[e * DH] = w;
-          }
-          if (bad)                               // what the products left out
-#pragma unroll 1
-            for (int e = 0; e < min(most, live - q * 8); ++e) {
-              const int row = q * 8 + e;
-              const float w = not_finite(a, s, s.r.length + row / a.G, key);
-              if (s.whole) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
-              else po[e * DH] += w;
-            }
+          for (int e = 0; e < 8; ++e) o[e] = 0u;
         }
+        if (TURNS) {
+          // the second group's: its sums, and its outputs in the place of its P
+          float* other = reinterpret_cast<float*>(psm + 4096);
+          if (group && key < 8) gpart[key] = l;
+          if (group)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) other[e * 128 + key] = __uint_as_float(o[e]) * (0x1p-7f * vref);
+          bar_both();
+          if (group == 0) {
+            float f[8];
+            if (key < 8) {
+              const float m1 = -row_nm[8 + key], top = fmaxf(m, m1);
+              const float w0 = tree_ex2(m - top), w1 = tree_ex2(m1 - top);
+              l = l * w0 + gpart[32 + key] * w1;
+              m = top;
+              row_f[key] = w0;
+              row_f[8 + key] = w1;
+            }
+            bar_group(group);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              f[e] = __uint_as_float(o[e]) * (0x1p-7f * vref * row_f[e]) + other[e * 128 + key] * row_f[8 + e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(f[e]);
+            bar_group(group);
+          }
+        }
+        if (!TURNS || group == 0) {
+          if (key < 8) {
+            const int row = q * 8 + key;
+            row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * (!s.whole ? 1.f : l != 0.f ? 1.f / l : 0.f) : 0.f;
+            if (!s.whole && row < rows) {
+              a.part_m[slot * rows + row] = m;
+              a.part_l[slot * rows + row] = row < live ? l : 0.f;
+            }
+          }
+          bar_group(group);
+          if (DH == 128 || w4 < 2) {
+            bf16* out = a.out + out0 + key;
+            float* po = a.part_o + (slot * rows + q * 8) * DH + key;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int row = q * 8 + e;
+              const float w = row < live ? __uint_as_float(o[e]) * row_f[row] : 0.f;
+              if (row < rows && s.whole) out[row_at[row] * DH] = __float2bfloat16(w);
+              if (row < rows && !s.whole) po[e * DH] = w;
+            }
+            if (bad)                             // what the products left out
+#pragma unroll 1
+              for (int e = 0; e < min(8, live - q * 8); ++e) {
+                const int row = q * 8 + e;
+                const float w = not_finite(a, s, s.r.length + row / a.G, key);
+                if (s.whole) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
+                else po[e * DH] += w;
+              }
+          }
+        }
+        if (TURNS) bar_both();                   // (its P's place is the second group's again)
       }
       at += sn;
     }
@@ -1123,34 +1205,45 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
 }
 
 // Joins a pair that several CTAs share: CTA x = the first of them, thread = 16
-// bytes of a row's output; the parts are added in order, 16 in flight.
+// bytes of a row's output; the parts are added in order.  Bound by latency: the
+// first parts are asked for together with the word that says how many there are.
+// (Few rows are split among many CTAs, many rows among few: kBatch parts at once.)
 constexpr int kJoinThreads = 256;
-template <int DH>
+template <int DH, int kBatch>
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
-  pdl_wait();
-  const int4 pair = a.shared[blockIdx.x];
-  const int rows = a.T * a.G, i = blockIdx.y * kJoinThreads + threadIdx.x;
-  const int row = i / (DH / 4), col = i % (DH / 4) * 4;
-  if (pair.x < 0 || row >= rows) return;
-  const int c0 = blockIdx.x, n = pair.z - c0 + 1;
+  const int rows = a.T * a.G, i = blockIdx.y * kJoinThreads + threadIdx.x, c0 = blockIdx.x;
+  const int row = i / (DH / 4), col = i % (DH / 4) * 4, tok = row / a.G;
+  if (row >= rows) return;
+  float pm[kBatch], pl[kBatch], m = -INFINITY, l = 0.f;
+  float4 v[kBatch], o = make_float4(0.f, 0.f, 0.f, 0.f);
   // the first CTA's second place, the others' first
-  auto place = [&](int k) { return k == 0 ? (size_t)c0 * 2 + 1 : (size_t)(c0 + k) * 2; };
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 16;
-  for (int k0 = 0; k0 < n; k0 += kBatch) {
-    float pm[kBatch], pl[kBatch], mn = m;
-    float4 v[kBatch];
+  auto load = [&](int k0, int n) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const bool got = k0 + u < n;
-      const size_t at = got ? place(k0 + u) * rows + row : 0;
-      pm[u] = got ? a.part_m[at] : -INFINITY;
-      pl[u] = got ? a.part_l[at] : 0.f;
-      v[u] = got ? *reinterpret_cast<const float4*>(a.part_o + at * DH + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int k = k0 + u;
+      pm[u] = -INFINITY;
+      pl[u] = 0.f;
+      v[u] = o;
+      if (k < n) {
+        const size_t at = (k == 0 ? (size_t)c0 * 2 + 1 : (size_t)(c0 + k) * 2) * rows + row;
+        pm[u] = a.part_m[at];
+        pl[u] = a.part_l[at];
+        v[u] = *reinterpret_cast<const float4*>(a.part_o + at * DH + col);
+      }
     }
+  };
+  pdl_wait();
+  const int4 pair = a.shared[c0];
+  const int guess = min((int)gridDim.x - c0, kBatch);
+  load(0, guess);                                // (what is there: some of it nobody wrote)
+  if (pair.x < 0) return;
+  const int n = pair.z - c0 + 1;
+  if (n > guess) load(0, n);
+  for (int k0 = 0;;) {
+    float mn = m;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, pm[u]);
+    for (int u = 0; u < kBatch; ++u)
+      if (k0 + u < n) mn = fmaxf(mn, pm[u]);
     const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
     l *= old;
     o.x *= old;
@@ -1158,35 +1251,36 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
     o.z *= old;
     o.w *= old;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (k0 + u >= n) break;
-      const float w = exp2f(pm[u] - base);
-      l = fmaf(pl[u], w, l);
-      o.x = fmaf(v[u].x, w, o.x);
-      o.y = fmaf(v[u].y, w, o.y);
-      o.z = fmaf(v[u].z, w, o.z);
-      o.w = fmaf(v[u].w, w, o.w);
-    }
+    for (int u = 0; u < kBatch; ++u)
+      if (k0 + u < n) {
+        const float w = exp2f(pm[u] - base);
+        l = fmaf(pl[u], w, l);
+        o.x = fmaf(v[u].x, w, o.x);
+        o.y = fmaf(v[u].y, w, o.y);
+        o.z = fmaf(v[u].z, w, o.z);
+        o.w = fmaf(v[u].w, w, o.w);
+      }
     m = mn;
+    if ((k0 += kBatch) >= n) break;
+    load(k0, n);
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;    // (NaN where a wait gave up)
-  const int tok = row / a.G;
-  const size_t to = ((size_t)(pair.x * (long long)a.T + tok) * a.H + pair.y * a.G + row % a.G) * DH + col;
+  const size_t to = (((size_t)pair.x * a.T + tok) * a.H + pair.y * a.G + row % a.G) * DH + col;
   *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int DH, bool SMALL, int kGroups>
+template <int DH, bool SMALL, bool TURNS>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream_t st) {
   const Layout lay = layout_of(a.T * a.G, DH, a.B);
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, SMALL, kGroups>,
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, SMALL, TURNS>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  cache_attn_tc_kernel<DH, SMALL, kGroups><<<a.ctas, threads_of(kGroups), lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
+  cache_attn_tc_kernel<DH, SMALL, TURNS><<<a.ctas, threads_of(SMALL), lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1198,7 +1292,7 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
   lc.stream = st;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH>, a);
+  return cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH, SMALL ? 20 : 2>, a);
 }
 
 }  // namespace
@@ -1243,10 +1337,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const int rows = a.T * a.G;
   if (a.dh == 128)
-    return rows <= 8    ? launch<128, true, 1>(a, m, s)
-           : rows <= 16 ? launch<128, true, 2>(a, m, s)
-                        : launch<128, false, 2>(a, m, s);
-  return rows <= 8 ? launch<64, true, 1>(a, m, s) : rows <= 16 ? launch<64, true, 2>(a, m, s) : launch<64, false, 2>(a, m, s);
+    return rows <= 8    ? launch<128, true, true>(a, m, s)
+           : rows <= 16 ? launch<128, true, false>(a, m, s)
+                        : launch<128, false, false>(a, m, s);
+  return rows <= 8    ? launch<64, true, true>(a, m, s)
+         : rows <= 16 ? launch<64, true, false>(a, m, s)
+                      : launch<64, false, false>(a, m, s);
 }
 
 }  // namespace ssd
