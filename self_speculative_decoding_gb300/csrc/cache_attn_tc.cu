@@ -75,7 +75,7 @@ __host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
   Layout l;
   l.rows = (rows + 15) / 16 * 16;
   const int q8 = 2 * l.rows * dh, q16 = 2 * l.rows * dh, p = l.rows * 256, wide = dh / 64 * kUnit;
-  const int plan = (14 * B + 4 + 127) / 128 * 128;
+  const int plan = (16 * B + 8 + 127) / 128 * 128;
   const int fixed = (q8 + q16 + 2 * wide + kSmall + plan + 1023) / 1024 * 1024;
   l.k_units = dh / 64;                           // (a tile of bf16 rows)
   l.v_units = 1;
@@ -279,20 +279,45 @@ struct Plan {
   int* first;                                    // [B + 1] tiles (of one head) before sequence b: all lie
                                                  // in the caches, so that 31 bits count them
   int *length, *held;                            // [B]
-  short* count;
+  short *some, *count;                           // [B + 1] sequences with any tiles before b; [B]
   long long begin, end;                          // the CTA's tiles
-  long long total;
-  int ctas;                                      // that have any
+  long long total;                               // units
+  int ctas;                                      // that share them
+  int start;                                     // units for the start of a pair
+
+  SSD_DI long long units(int b) const { return (long long)first[b] + start * some[b]; }  // before b, of one head
 };
-static __device__ __noinline__ long long cta_start(long long total, int ctas, int cta) {
-  return cta < ctas ? total * cta / ctas : total;
+// The work is divided in units of a tile.  A pair's start counts as several (q, the
+// first scores and the result's way out are no tile's work, and take as long as
+// kStart tiles), but at most as a quarter of a CTA's tiles: with less
+// to do than that the CTAs' tiles, and not their starts, differ.
+constexpr int kStart = 5;
+// (64-bit divisions cost a thousand cycles where they are cold)
+SSD_DI long long cta_start(long long total, int ctas, int cta) {
+  if (cta >= ctas) return total;
+  if (total < 1 << 20) return (unsigned)total * (unsigned)cta / (unsigned)ctas;  // (at most 1024 CTAs)
+  return total * cta / ctas;
 }
 // The CTA that has the last tile of a pair.
 static __device__ __noinline__ int last_cta(const CacheAttnArgs& a, const Plan& p, int b, int h) {
-  const long long n = p.first[b + 1] - p.first[b], tile = (long long)p.first[b] * a.Hkv + (h + 1) * n - 1;
-  int cta = (int)(tile * p.ctas / p.total);
-  while (cta_start(p.total, p.ctas, cta + 1) <= tile) ++cta;
+  const long long unit = p.units(b) * a.Hkv + (h + 1) * (p.units(b + 1) - p.units(b)) - 1;
+  int cta = (int)(unit * p.ctas / p.total);
+  while (cta_start(p.total, p.ctas, cta + 1) <= unit) ++cta;
   return cta;
+}
+// Tiles before unit `at`.
+static __device__ __noinline__ long long tiles_before(const CacheAttnArgs& a, const Plan& p, long long at) {
+  if (at >= p.total) return (long long)p.first[a.B] * a.Hkv;
+  int lo = 0, hi = a.B - 1;                      // the last b whose units begin at or before `at`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (p.units(mid) * a.Hkv <= at) lo = mid;
+    else hi = mid - 1;
+  }
+  const int n = p.first[lo + 1] - p.first[lo];
+  const long long local = at - p.units(lo) * a.Hkv;
+  const int w = n + p.start, h = local < 0x7fffffff ? (int)((unsigned)local / (unsigned)w) : (int)(local / w);
+  return (long long)p.first[lo] * a.Hkv + (long long)h * n + max((int)(local - (long long)h * w) - p.start, 0);
 }
 // A run of a pair's tiles within the CTA's.
 struct Segment {
@@ -306,30 +331,55 @@ struct Place {
   Segment s;
   Walk w;
 };
-static __device__ __noinline__ void segment_at(const CacheAttnArgs& a, const Plan& p, long long at, Place& to) {
-  Segment s;
+// The segment at tile `at`, the CTA's first.
+static __device__ __noinline__ void first_segment(const CacheAttnArgs& a, const Plan& p, long long at, Place& to) {
   int lo = 0, hi = a.B - 1;                      // the last b with first[b] Hkv <= at
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if ((long long)p.first[mid] * a.Hkv <= at) lo = mid;
     else hi = mid - 1;
   }
-  s.b = lo;
   const int n = p.first[lo + 1] - p.first[lo];
-  const long long local = at - (long long)p.first[lo] * a.Hkv;
-  s.h = (int)(local / n);
-  s.i0 = (int)(local - (long long)s.h * n);
-  const long long left = p.end - at;
-  s.n = n - s.i0 < left ? n - s.i0 : (int)left;
-  s.whole = s.n == n;
-  s.head = s.i0 > 0;
-  s.r = seq_range(a, p.length[lo], p.count[lo], p.held[lo]);
-  s.eight = max(0, min(s.n, tiles_eight(s.r) - s.i0));
+  const long long local = at - (long long)p.first[lo] * a.Hkv, left = p.end - at;
+  const int h = local < 0x7fffffff ? (int)((unsigned)local / (unsigned)n) : (int)(local / n);
+  const int i0 = (int)(local - (long long)h * n), m = n - i0 < left ? n - i0 : (int)left;
+  to.s.b = lo;
+  to.s.h = h;
+  to.s.i0 = i0;
+  to.s.n = m;
+  to.s.whole = m == n;
+  to.s.head = i0 > 0;
+  to.s.r = seq_range(a, p.length[lo], p.count[lo], p.held[lo]);
+  to.s.eight = max(0, min(m, tiles_eight(to.s.r) - i0));
+  find_run(to.s.r, a.window, i0, to.w);
+}
+// The segment behind the one that a warp has, at tile `at`: the next head or the
+// next sequence with any tiles.
+static __device__ __noinline__ void next_segment(const CacheAttnArgs& a, const Plan& p, long long at, Place& to) {
   __syncwarp();
-  to.s = s;
-  find_run(s.r, a.window, s.i0, to.w);
+  int b = to.s.b, h = to.s.h + 1;
+  __syncwarp();
+  if (h == a.Hkv) {
+    h = 0;
+    do ++b;
+    while (p.first[b + 1] == p.first[b]);
+    to.s.b = b;
+    to.s.r = seq_range(a, p.length[b], p.count[b], p.held[b]);
+  }
+  const int n = p.first[b + 1] - p.first[b];
+  const long long left = p.end - at;
+  const int m = n < left ? n : (int)left;
+  to.s.h = h;
+  to.s.i0 = 0;
+  to.s.n = m;
+  to.s.whole = m == n;
+  to.s.head = false;
+  __syncwarp();
+  to.s.eight = min(m, tiles_eight(to.s.r));
+  find_run(to.s.r, a.window, 0, to.w);
   __syncwarp();
 }
+
 // One tile on.
 SSD_DI void step(Walk& w, Place& place, int window) {
   ++w.i;
@@ -405,8 +455,10 @@ static __device__ __noinline__ float not_finite(const CacheAttnArgs& a, const Se
 // The CTA's rows as NaN: a wait gave up, and none is sure.
 static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan& plan, Place& place) {
   const int rows = a.T * a.G;
+  __syncthreads();
+  if (plan.begin < plan.end) first_segment(a, plan, plan.begin, place);
   for (long long at = plan.begin; at < plan.end;) {
-    segment_at(a, plan, at, place);
+    __syncwarp();
     const Segment& s = place.s;
     const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
     if (!s.whole && !s.head && threadIdx.x == 0)
@@ -422,6 +474,7 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
       }
     }
     at += s.n;
+    if (at < plan.end) next_segment(a, plan, at, place);
   }
 }
 
@@ -489,7 +542,8 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       plan.first = first;
       plan.length = first + a.B + 1;
       plan.held = plan.length + a.B;
-      plan.count = reinterpret_cast<short*>(plan.held + a.B);
+      plan.some = reinterpret_cast<short*>(plan.held + a.B);
+      plan.count = plan.some + a.B + 1;
     }
     fence_mbar_init();
   }
@@ -504,7 +558,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
     const int c = a.counts ? min(max(a.counts[b], -1), 129) : a.T;  // (129: too many, like all above)
     first[a.B + 1 + b] = n;
     first[2 * a.B + 1 + b] = h;
-    reinterpret_cast<short*>(first + 3 * a.B + 1)[b] = (short)c;
+    reinterpret_cast<short*>(first + 3 * a.B + 1)[a.B + 1 + b] = (short)c;
     first[b + 1] = tiles_of(seq_range(a, n, c, h));
   }
   if (tid < rows) row_at[tid] = tid / a.G * a.H + tid % a.G;
@@ -515,11 +569,14 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   fence_proxy_async_smem();
   __syncthreads();
   if (warp == kWidenWarp) {
-    int sum = 0;
-    if (lane == 0) first[0] = 0;
+    int sum = 0, some = 0;
+    if (lane == 0) first[0] = plan.some[0] = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       int x = b0 + lane < a.B ? first[b0 + lane + 1] : 0;
+      const uint32_t any = __ballot_sync(~0u, x > 0);
+      if (b0 + lane < a.B) plan.some[b0 + lane + 1] = (short)(some + __popc(any & (~0u >> (31 - lane))));
+      some += __popc(any);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(~0u, x, d);
@@ -528,13 +585,19 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       if (b0 + lane < a.B) first[b0 + lane + 1] = sum + x;
       sum += __shfl_sync(~0u, x, 31);
     }
-    if (lane < 2) {
-      const long long total = (long long)sum * a.Hkv;
-      const int ctas = (int)min((long long)gridDim.x, total);  // each with a tile at least
-      (lane ? plan.end : plan.begin) = cta_start(total, ctas, blockIdx.x + lane);
-      plan.total = total;
+    const long long tiles = (long long)sum * a.Hkv;
+    const int ctas = (int)min((long long)gridDim.x, tiles);
+    if (lane == 0) {
+      int start = kStart;                        // (as long as a CTA has four times as many tiles)
+      while (start && tiles < 4ll * start * ctas) --start;
+      plan.start = start;
+      plan.total = tiles + (long long)start * some * a.Hkv;
       plan.ctas = ctas;
     }
+    __syncwarp();
+    if (lane < 2) (lane ? plan.end : plan.begin) = tiles_before(a, plan, cta_start(plan.total, ctas, blockIdx.x + lane));
+    __syncwarp();
+    if (plan.begin < plan.end && lane == 0) first_segment(a, plan, plan.begin, places[0]);
   }
   tc_fence_before();
   __syncthreads();
@@ -542,6 +605,10 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
   const long long begin = plan.begin, end = plan.end;
   Place& place = places[warp];
+  static_assert(sizeof(Place) % 4 == 0 && sizeof(Place) <= 128, "a word per lane");
+  if (warp && lane < (int)sizeof(Place) / 4)
+    reinterpret_cast<int*>(&place)[lane] = reinterpret_cast<const int*>(places)[lane];
+  __syncthreads();                               // (the first warp's own may change from here on)
   auto give_up = [&](bool ok) {
     if (!ok) atomicExch(fail, 1);
   };
@@ -561,7 +628,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       bool ok = !tree_flagged(fail);
 #pragma unroll 1
       for (long long at = begin; ok && at < end;) {
-        segment_at(a, plan, at, place);
+        if (at != begin) next_segment(a, plan, at, place);
         const int sn = place.s.n, sb = place.s.b, sh = place.s.h;
         Walk t = place.w;
 #pragma unroll 1
@@ -622,7 +689,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       };
 #pragma unroll 1
       for (long long pos = begin; ok && pos < end; ++segments) {
-        segment_at(a, plan, pos, place);
+        if (pos != begin) next_segment(a, plan, pos, place);
         const int sn = place.s.n, in_eight = place.s.eight;
         wait(qready, segments & 1u);
 #pragma unroll 1
@@ -671,7 +738,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       const uint32_t idp8 = idesc_e4m3(NP) | 3u << 15, idp16 = idp8 | 1u << 7 | 1u << 10;
 #pragma unroll 1
       for (long long pos = begin; ok && pos < end;) {
-        segment_at(a, plan, pos, place);
+        if (pos != begin) next_segment(a, plan, pos, place);
         const int sn = place.s.n, in_eight = place.s.eight;
 #pragma unroll 1
         for (int i = 0; ok && i < sn; ++i, ++n) {
@@ -722,7 +789,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
     };
 #pragma unroll 1
     for (long long pos = begin; ok && pos < end;) {
-      segment_at(a, plan, pos, place);
+      if (pos != begin) next_segment(a, plan, pos, place);
       const int sn = place.s.n;
       Walk t = place.w;
 #pragma unroll 1
@@ -849,7 +916,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
     };
 #pragma unroll 1
     for (long long at = group < active ? begin : end; at < end;) {
-      segment_at(a, plan, at, place);
+      if (at != begin) next_segment(a, plan, at, place);
       const Segment& s = place.s;
       const int sn = s.n;
       // ---- the query's parts: bf16, and e4m3 twice under a power of two
@@ -1165,7 +1232,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         if (!TURNS || group == 0) {
           if (key < 8) {
             const int row = q * 8 + key;
-            row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * (!s.whole ? 1.f : l != 0.f ? 1.f / l : 0.f) : 0.f;
+            row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * (!s.whole ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f) : 0.f;
             if (!s.whole && row < rows) {
               a.part_m[slot * rows + row] = m;
               a.part_l[slot * rows + row] = row < live ? l : 0.f;
