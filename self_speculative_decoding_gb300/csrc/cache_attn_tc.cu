@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   const uint32_t scols = SMALL ? 32 : NP;        // TMEM: S0, S1, O, sums
   const uint32_t col_o = 2 * scols, col_l = col_o + NP;
   extern __shared__ unsigned char sm_raw[];
-  unsigned char* sm =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  // (an offset, and not a rounded address: the compiler keeps sight of shared memory)
+  unsigned char* sm = sm_raw + (-smem_addr(sm_raw) & 1023u);
   unsigned char *q8 = sm, *q16 = sm + lay.q16, *psm = sm + lay.p, *wide = sm + lay.wide;
   unsigned char *kring = sm + lay.kring, *vring = sm + lay.vring;
   float* row_c = reinterpret_cast<float*>(sm + lay.rest);  // [128] what a row's 8-bit scores are multiplied by
@@ -1043,37 +1043,53 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         if (!SMALL && lay.p_bufs == 1 && n > 0) wait_values(n);  // (its only one)
         float pv = vc * unit;
         unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
+        // the tokens that see the key, of chunk q's rows
+        auto seen_of = [&](int q) {
+          const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
+          return m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
+        };
+        bool force = over || vref == 0.f;
+        uint32_t x[8], y[8];                     // products; SMALL: their second parts, else the sums
+        tmem_ld8_nw(trow + buf * scols + q0 * 8, x);
+        if (SMALL) tmem_ld8_nw(trow + buf * scols + q0 * 8 + 16, y);
+        tmem_wait_ld();
+        tmem_pin8(x);
+        if (SMALL) tmem_pin8(y);
 #pragma unroll 1
         for (int q = q0; q < chunks; q += q_step) {
-          uint32_t x[8], y[8];
           const uint32_t scol = trow + buf * scols + q * 8;
-          tmem_ld8_nw(scol, x);
-          tmem_ld8_nw(SMALL ? scol + 16 : trow + col_l + q * 8, y);
-          if (!SMALL) state(q);
-          const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
-          const uint32_t seen = m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
-          tmem_wait_ld();
-          tmem_pin8(x);
-          tmem_pin8(y);
-          // scores (of the products' two parts), as multiples of what the exponential takes
+          if (!SMALL) {
+            tmem_ld8_nw(trow + col_l + q * 8, y);  // (needed in the end)
+            state(q);
+          }
+          // scores (of the products' two parts), as multiples of what the exponential
+          // takes, minus m
           float d[8];
-          auto scores = [&]() {
+          auto scores = [&](bool from_m) {
+            const float2 k2 = make_float2(kc, kc), s2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              d[e] = __uint_as_float(x[e]);
-              if (SMALL && eight) d[e] += __uint_as_float(y[e]);
-              d[e] *= eight ? c[e] * kc : a.scale_log2;
+            for (int e = 0; e < 8; e += 2) {
+              float2 v = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              const float2 at = from_m ? make_float2(nm[e], nm[e + 1]) : make_float2(0.f, 0.f);
+              if (eight) {
+                if (SMALL) v = __fadd2_rn(v, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
+                v = __ffma2_rn(v, __fmul2_rn(make_float2(c[e], c[e + 1]), k2), at);
+              } else {
+                v = __ffma2_rn(v, s2, at);
+              }
+              d[e] = v.x;
+              d[e + 1] = v.y;
             }
-            if (seldom(edge))
+            if (seldom(edge)) {
+              const uint32_t seen = seen_of(q);
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (!((seen >> e) & 1u)) d[e] = -INFINITY;
+            }
           };
-          scores();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] += nm[e];
+          scores(true);
           const float top = tree_max3(tree_max3(d[0], d[1], d[2]), tree_max3(d[3], d[4], d[5]), fmaxf(d[6], d[7]));
-          if (seldom(any_group(group, top > kRaise || over || vref == 0.f))) {
+          if (seldom(any_group(group, top > kRaise || force))) {
             if (q == q0) {
               // the largest of the four warps' scales
               if (lane == 0) gpart[w4] = over ? fabsf(vc) : 0.f;
@@ -1091,6 +1107,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
                 pv = vc * unit;
               }
               over = false;
+              force = vref == 0.f;
               bar_group(group);
             }
             // the rows' largest scores of all keys; those that pass m + 8 become m
@@ -1099,7 +1116,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
             tmem_wait_ld();
             tmem_pin8(x);
             tmem_pin8(y);
-            scores();
+            scores(false);
             over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
             if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = d[0];
             bar_group(group);
@@ -1129,32 +1146,47 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
             tmem_wait_ld();
             tmem_pin8(x);
             if (SMALL) tmem_pin8(y);
-            scores();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] += nm[e];
+            scores(true);
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            d[e] = tree_ex2(d[e]);
-            if (SMALL) ls[e] += d[e];
-            else y[e] = __float_as_uint(__uint_as_float(y[e]) + d[e]);
-            d[e] *= pv;
-          }
+          // (the next chunk's products come in behind the exponentials)
+          const bool more = !SMALL && q + q_step < chunks;
+          if (more) tmem_ld8_nw(scol + q_step * 8, x);
           uint32_t pk[4];
-          if (!seldom(!eight)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pk[e] = pack_f16x2(d[2 * e], d[2 * e + 1]);
-          } else {
+          for (int e = 0; e < 8; ++e) d[e] = tree_ex2(d[e]);
+          if (SMALL)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+            for (int e = 0; e < 8; e += 2) {
+              const float2 v = __fadd2_rn(make_float2(ls[e], ls[e + 1]), make_float2(d[e], d[e + 1]));
+              ls[e] = v.x;
+              ls[e + 1] = v.y;
+            }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = __fmul2_rn(make_float2(d[2 * e], d[2 * e + 1]), make_float2(pv, pv));
+            pk[e] = eight ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
           }
-          if (seldom(edge))                      // (a scale that is none of the row's)
+          if (seldom(edge)) {                    // (a scale that is none of the row's)
+            const uint32_t seen = seen_of(q);
 #pragma unroll
             for (int e = 0; e < 8; e += 2)
               pk[e / 2] &= ((seen >> e) & 1u ? 0x0000ffffu : 0u) | ((seen >> e) & 2u ? 0xffff0000u : 0u);
+          }
           *reinterpret_cast<uint4*>(pto + (q >> 1) * kPanel + (((q & 1) ^ ((key >> 2) & 1)) << 4)) =
               make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          if (!SMALL) tmem_st8(trow + col_l + q * 8, y);
+          if (!SMALL) {
+            tmem_wait_ld();
+            tmem_pin8(x);
+            tmem_pin8(y);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float2 v = __fadd2_rn(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
+                                          make_float2(d[e], d[e + 1]));
+              y[e] = __float_as_uint(v.x);
+              y[e + 1] = __float_as_uint(v.y);
+            }
+            tmem_st8(trow + col_l + q * 8, y);
+          }
         }
         if (!SMALL) tmem_wait_st();
         fence_proxy_async_smem();
