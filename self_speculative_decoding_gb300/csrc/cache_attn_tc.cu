@@ -70,7 +70,7 @@ struct Layout {
   int p_bufs, k_units, v_units;
 };
 constexpr int kSmemMost = 227 * 1024 - 1024;     // (from a 1024-byte boundary)
-constexpr int kSmall = 5 * 128 * 4 + 512 + 19 * 96;       // per-row values, barriers
+constexpr int kSmall = (4 * 128 + 4 * 128) * 4 + 512 + 19 * 96;       // per-row values, barriers
 __host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
   Layout l;
   l.rows = (rows + 15) / 16 * 16;
@@ -503,9 +503,9 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
   float* row_c = reinterpret_cast<float*>(sm + lay.rest);  // [128] what a row's 8-bit scores are multiplied by
   float* row_nm = row_c + 128;                   // [128] minus its maximum
   float* row_f = row_nm + 128;                   // [128] what O is multiplied by in the end
-  float* part = row_f + 128;                     // [groups][4][8] of the warps
-  int* row_at = reinterpret_cast<int*>(part + 128);  // [128] a row's place among the sequence's heads
-  uint64_t* bars = reinterpret_cast<uint64_t*>(row_c + 5 * 128);
+  float* part = row_f + 128;                     // [16][4][8] of chunks' warps; of groups' while tiles go on
+  int* row_at = reinterpret_cast<int*>(part + 4 * 128);  // [128] a row's place among the sequence's heads
+  uint64_t* bars = reinterpret_cast<uint64_t*>(row_c + 8 * 128);
   uint64_t* kfull = bars;                        // [8] each
   uint64_t* kempty = kfull + 8;
   uint64_t* vfull = kempty + 8;
@@ -631,6 +631,11 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         if (at != begin) next_segment(a, plan, at, place);
         const int sn = place.s.n, sb = place.s.b, sh = place.s.h;
         Walk t = place.w;
+        if (!is_v)                               // q on its way, while the pair before is at work
+#pragma unroll 1
+          for (int i = lane; i < rows * P; i += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + ((size_t)sb * a.T * a.H + (size_t)sh * a.G + row_at[i / P]) * DH +
+                                                         i % P * 64));
 #pragma unroll 1
         for (int i = 0; ok && i < sn; ++i) {
 #pragma unroll 1
@@ -924,14 +929,18 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         constexpr int kEach = DH / 8;            // threads per row, 8 elements each
         const int c = key % kEach, live = s.r.count * a.G;
         const bf16* src = a.q + ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH + c * 8;
+        auto fetch_q = [&](int row) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < live && key / kEach < 8 && !(TURNS && group)) x = *reinterpret_cast<const uint4*>(src + (size_t)row_at[row] * DH);
+          return x;
+        };
+        uint4 coming = fetch_q(q0 * 8 + key / kEach);
 #pragma unroll 1
         for (int r0 = q0 * 8; r0 < (TURNS && group ? 0 : chunks * 8); r0 += q_step * 8) {
-#pragma unroll
-          for (int r1 = 0; r1 < 8; r1 += 128 / kEach) {
-            const int row = r0 + r1 + key / kEach;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (row < live && r1 + key / kEach < 8)
-              x = *reinterpret_cast<const uint4*>(src + (size_t)row_at[row] * DH);
+          {
+            const int row = r0 + key / kEach;
+            const uint4 x = coming;
+            if (!SMALL) coming = fetch_q(row + q_step * 8);
             uint32_t w[4] = {x.x, x.y, x.z, x.w}, most = 0, hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < 4; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
@@ -951,17 +960,18 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
               hi[k >> 1] |= h << (16 * (k & 1));
               lo[k >> 1] |= l << (16 * (k & 1));
             }
-            if (row >= rows || r1 + key / kEach >= 8) continue;
             auto place = [&](int r) {
               return DH == 128 ? r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8
                                : r * 64 + (((c >> 1) ^ ((r >> 1) & 3)) << 4) + (c & 1) * 8;
             };
-            *reinterpret_cast<uint2*>(q8 + place(row)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(q8 + place(NP + row)) = make_uint2(lo[0], lo[1]);
-            *reinterpret_cast<uint4*>(q16 + (c >> 3) * NP * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-            if (c == 0)
-              row_c[row] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+            if (row < rows && key / kEach < 8) {
+              *reinterpret_cast<uint2*>(q8 + place(row)) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(q8 + place(NP + row)) = make_uint2(lo[0], lo[1]);
+              *reinterpret_cast<uint4*>(q16 + (c >> 3) * NP * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+              if (c == 0)
+                row_c[row] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+            }
           }
           if (key < 8) row_nm[r0 + key] = -kNone;
         }
@@ -1202,13 +1212,13 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       } else {
         wait_values(n);
       }
-      const bool bad = tree_flagged(odd);
+      const bool bad = tree_flagged(odd), final = s.whole;
       const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
       const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
       const int live = s.r.count * a.G;          // rows with a token
+      // the sums over the keys: a warp's, then (a thread per row) the four warps'
 #pragma unroll 1
       for (int q = q0; q < chunks; q += q_step) {
-        // the sums over the keys: a warp's, then the four warps'
         if (!SMALL) {
           uint32_t y[8];
           tmem_ld8_nw(trow + col_l + q * 8, y);
@@ -1218,81 +1228,89 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
           for (int e = 0; e < 8; ++e) ls[e] = __uint_as_float(y[e]);
         }
         over_lanes(ls, [](float u, float w) { return u + w; });
-        if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = ls[0];
-        bar_group(group);
-        float m = kNone, l = 0.f;
-        if (key < 8) {
-          m = -row_nm[(s0 + q) * 8 + key];
-          l = (gpart[key] + gpart[8 + key]) + (gpart[16 + key] + gpart[24 + key]);
-        }
-        uint32_t o[8];
+        if (!(lane & 3)) part[(s0 + q) * 32 + w4 * 8 + (lane >> 2)] = ls[0];
+      }
+      bar_group(group);
+      const int mine = q0 + (key >> 3) * q_step, row = mine * 8 + (key & 7);  // the thread's chunk and row
+      float m = kNone, l = 0.f;
+      if (mine < chunks) {
+        const float* p4 = part + (s0 + mine) * 32 + (key & 7);
+        m = -row_nm[s0 * 8 + row];
+        l = (p4[0] + p4[8]) + (p4[16] + p4[24]);
+      }
+      uint32_t o[8];
+      auto fetch_o = [&](int q) {
+        tmem_ld8_nw(trow + col_mine + q * 8, o);
+        tmem_wait_ld();
+        tmem_pin8(o);
+      };
+      if (TURNS) {
+        // the second group's: its sums, and its outputs in the place of its P
+        float* other = reinterpret_cast<float*>(psm + 4096);
         if (any) {
-          tmem_ld8_nw(trow + col_mine + q * 8, o);
-          tmem_wait_ld();
-          tmem_pin8(o);
+          fetch_o(0);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = 0u;
         }
-        if (TURNS) {
-          // the second group's: its sums, and its outputs in the place of its P
-          float* other = reinterpret_cast<float*>(psm + 4096);
-          if (group && key < 8) gpart[key] = l;
-          if (group)
+        if (group) {
+          if (key < 8) part[64 + key] = l;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) other[e * 128 + key] = __uint_as_float(o[e]) * (0x1p-7f * vref);
-          bar_both();
-          if (group == 0) {
-            float f[8];
-            if (key < 8) {
-              const float m1 = -row_nm[8 + key], top = fmaxf(m, m1);
-              const float w0 = tree_ex2(m - top), w1 = tree_ex2(m1 - top);
-              l = l * w0 + gpart[32 + key] * w1;
-              m = top;
-              row_f[key] = w0;
-              row_f[8 + key] = w1;
-            }
-            bar_group(group);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              f[e] = __uint_as_float(o[e]) * (0x1p-7f * vref * row_f[e]) + other[e * 128 + key] * row_f[8 + e];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(f[e]);
-            bar_group(group);
-          }
+          for (int e = 0; e < 8; ++e) other[e * 128 + key] = __uint_as_float(o[e]) * (0x1p-7f * vref);
         }
-        if (!TURNS || group == 0) {
+        bar_both();
+        if (group == 0) {
+          float f[8];
           if (key < 8) {
-            const int row = q * 8 + key;
-            row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * (!s.whole ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f) : 0.f;
-            if (!s.whole && row < rows) {
-              a.part_m[slot * rows + row] = m;
-              a.part_l[slot * rows + row] = row < live ? l : 0.f;
-            }
+            const float m1 = -row_nm[8 + key], top = fmaxf(m, m1);
+            const float w0 = tree_ex2(m - top), w1 = tree_ex2(m1 - top);
+            l = l * w0 + part[64 + key] * w1;
+            m = top;
+            row_f[key] = w0;
+            row_f[8 + key] = w1;
           }
           bar_group(group);
-          if (DH == 128 || w4 < 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            f[e] = __uint_as_float(o[e]) * (0x1p-7f * vref * row_f[e]) + other[e * 128 + key] * row_f[8 + e];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(f[e]);
+          bar_group(group);
+        }
+      }
+      if (!TURNS || group == 0) {
+        if (mine < chunks) {
+          row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * (!final ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f) : 0.f;
+          if (!final && row < rows) {
+            a.part_m[slot * rows + row] = m;
+            a.part_l[slot * rows + row] = row < live ? l : 0.f;
+          }
+        }
+        bar_group(group);
+        if (DH == 128 || w4 < 2)
+#pragma unroll 1
+          for (int q = q0; q < chunks; q += q_step) {
+            if (!TURNS) fetch_o(q);
             bf16* out = a.out + out0 + key;
             float* po = a.part_o + (slot * rows + q * 8) * DH + key;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int row = q * 8 + e;
               const float w = row < live ? __uint_as_float(o[e]) * row_f[row] : 0.f;
-              if (row < rows && s.whole) out[row_at[row] * DH] = __float2bfloat16(w);
-              if (row < rows && !s.whole) po[e * DH] = w;
+              if (row < rows && final) out[row_at[row] * DH] = __float2bfloat16(w);
+              if (row < rows && !final) po[e * DH] = w;
             }
             if (bad)                             // what the products left out
 #pragma unroll 1
               for (int e = 0; e < min(8, live - q * 8); ++e) {
                 const int row = q * 8 + e;
                 const float w = not_finite(a, s, s.r.length + row / a.G, key);
-                if (s.whole) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
+                if (final) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
                 else po[e * DH] += w;
               }
           }
-        }
-        if (TURNS) bar_both();                   // (its P's place is the second group's again)
       }
+      if (TURNS) bar_both();                     // (its P's place is the second group's again)
       at += sn;
     }
   }
