@@ -323,8 +323,10 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * ring no longer holds one that is needed, gives NaN in all of its rows of out.
  * Scores are exact products of the bf16 query and the stored keys, summed in
  * fp32 (elements of q below 2^-9 of their row's largest are good to 2^-17 of
- * that; a query row with infinity or NaN gives NaN); probabilities, times the value's scale, are
- * rounded to bf16 for the product with V.  Equal calls give equal bits, but a
+ * that; a query row with infinity or NaN gives NaN); probabilities are rounded to
+ * bf16 for the product with bf16 rows of V, and, times the value's scale, to fp16
+ * for the product with 8-bit rows (in units that keep 11 bits down to 2^-18 of
+ * a row's largest weight, and steps of 2^-28 below).  Equal calls give equal bits, but a
  * row's last bits depend on how the rows of all sequences of the call are divided
  * among the SMs. */
 size_t ssd_op_cache_attention_workspace(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh);
@@ -376,6 +378,11 @@ ssd_status ssd_op_wait_selftest(int32_t polls, int32_t* code_out, void* stream);
  * returns SSD_OK, and has NaN in every row of out (in every key's weight) that
  * may be incomplete.  Errors: INVALID_ARG (below -1). */
 ssd_status ssd_debug_tree_give_up(int32_t attention, int32_t weights);
+
+/* The same of ssd_op_cache_attention: CTA `cta` of its kernel acts as after a
+ * wait that gave up (-1: none).  Every row of out that the CTA has a part in is
+ * NaN then. */
+ssd_status ssd_debug_cache_give_up(int32_t cta);
 
 /* ssd_op_linear for callers that cannot allocate device memory (the pages
  * have no counterpart; this is a library convenience).  Same arguments,

@@ -138,6 +138,7 @@ _SIGS = {
     "ssd_op_tree_attention": [_P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, C.c_float, _P, _P, _P,
                               _P, C.c_size_t, _P],
     "ssd_debug_tree_give_up": [_I, _I],
+    "ssd_debug_cache_give_up": [_I],
     "ssd_op_cache_evict": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P],
     "ssd_op_beam_select_workspace": [_I, _I, _I],
     "ssd_op_beam_select": [_P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, C.c_size_t, _P],

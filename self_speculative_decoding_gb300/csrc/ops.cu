@@ -2,6 +2,7 @@
 // caller-provided device buffers, so that every kernel can be checked on
 // its own against the CPU oracle.
 #include <cmath>
+#include <initializer_list>
 #include <cstdio>
 #include <cstring>
 #include <string>
@@ -112,8 +113,8 @@ void tree_sizes(TreeArgs& a, int T, int n_ctx, int H, int Hkv, int dh) {
   a.dh = dh;
 }
 
-// What ssd_debug_tree_give_up asked for.
-thread_local int t_give_up[2] = {-1, -1};
+// What ssd_debug_tree_give_up and ssd_debug_cache_give_up asked for.
+thread_local int t_give_up[2] = {-1, -1}, t_cache_give_up = -1;
 
 // theta^(-2 i / dh) / pi.  The table of the thread's last (theta, dh) is kept:
 // 64 powers cost a small call several microseconds.
@@ -128,6 +129,18 @@ void tree_frequencies(float theta, int dh, double* out) {
     last_dh = dh;
   }
   std::memcpy(out, table, sizeof(double) * (dh / 2));
+}
+
+// Whether what a call writes meets what it reads (NULL: not given).
+struct Bytes {
+  const void* at;
+  size_t n;
+};
+bool meets(std::initializer_list<Bytes> written, std::initializer_list<Bytes> read) {
+  for (const Bytes& w : written)
+    for (const Bytes& r : read)
+      if (w.at && r.at && overlap(w.at, w.n, r.at, r.n)) return true;
+  return false;
 }
 
 // Whether two sets of n runs of `span` bytes, `stride` bytes apart, meet.
@@ -666,8 +679,10 @@ ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int3
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append pointers");
   const size_t tokens = (size_t)B * T, in = tokens * ((size_t)H + 2 * Hkv) * dh * 4, o = tokens * H * dh * 2;
   const size_t one = (size_t)Hkv * rows * dh, cache = cache_span(B, seq_stride, one, 2);
-  if (runs_overlap(k, v, B, seq_stride * 2, one * 2) || overlap(qkv, in, q_out, o) || overlap(qkv, in, k, cache) || overlap(qkv, in, v, cache) ||
-      overlap(q_out, o, k, cache) || overlap(q_out, o, v, cache))
+  const size_t n4 = (size_t)4 * B, gain = (size_t)4 * dh;
+  if (runs_overlap(k, v, B, seq_stride * 2, one * 2) || meets({{q_out, o}}, {{k, cache}, {v, cache}}) ||
+      meets({{q_out, o}, {k, cache}, {v, cache}}, {{qkv, in}, {lengths, n4}, {counts, n4}, {positions, tokens * 4},
+                                                   {q_gain, gain}, {k_gain, gain}}))
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append: buffers overlap");
   RopeAppendArgs a;
   a.qkv = qkv;
@@ -711,9 +726,12 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
   const size_t in = cache_span(B, seq_stride, (size_t)Hkv * rows * dh, 2);
   const size_t one = (size_t)Hkv * max_seq * dh, scales = (size_t)4 * Hkv * (max_seq / block);
   const size_t o = cache_span(B, seq8_stride, one, 1), n = (size_t)4 * B;
+  const size_t all_scales = cache_span(B, scale_stride, (size_t)Hkv * (max_seq / block), 4);
   if (runs_overlap(k8, v8, B, seq8_stride, one) || runs_overlap(k_scale, v_scale, B, scale_stride * 4, scales) ||
-      overlap(k, in, k8, o) || overlap(k, in, v8, o) || overlap(v, in, k8, o) || overlap(v, in, v8, o) ||
-      overlap(held, n, held_out, n) || overlap(lengths, n, held_out, n))
+      meets({{k8, o}, {v8, o}, {k_scale, all_scales}, {v_scale, all_scales}, {held_out, n}},
+            {{k, in}, {v, in}, {held, n}, {lengths, n}}) ||
+      meets({{k8, o}, {v8, o}}, {{k_scale, all_scales}, {v_scale, all_scales}, {held_out, n}}) ||
+      meets({{held_out, n}}, {{k_scale, all_scales}, {v_scale, all_scales}}))
     return op_fail(SSD_ERR_INVALID_ARG, "cache_quantize: buffers overlap");
   QuantizeArgs a;
   a.k = (const bf16*)k;
@@ -781,8 +799,16 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
   a.Hkv = Hkv;
   a.G = H / Hkv;
   a.dh = dh;
-  if (cache_attn_workspace(a, workspace) > workspace_bytes)
-    return op_fail(SSD_ERR_CAPACITY, "cache_attention: workspace too small");
+  const size_t need = cache_attn_workspace(a, workspace);
+  if (need > workspace_bytes) return op_fail(SSD_ERR_CAPACITY, "cache_attention: workspace too small");
+  const size_t o = (size_t)B * T * H * dh * 2, n4 = (size_t)4 * B;
+  const size_t in = cache_span(B, seq_stride, (size_t)Hkv * rows * dh, 2);
+  const size_t in8 = eight ? cache_span(B, seq8_stride, (size_t)Hkv * max_seq * dh, 1) : 0;
+  const size_t scales = eight ? cache_span(B, scale_stride, (size_t)Hkv * (max_seq / block), 4) : 0;
+  if (meets({{out, o}, {workspace, need}}, {{q, o}, {k, in}, {v, in}, {k8, in8}, {v8, in8}, {k_scale, scales},
+                                            {v_scale, scales}, {lengths, n4}, {counts, n4}, {held, n4}}) ||
+      meets({{out, o}}, {{workspace, need}}))
+    return op_fail(SSD_ERR_INVALID_ARG, "cache_attention: buffers overlap");
   a.q = (const bf16*)q;
   a.lengths = lengths;
   a.counts = counts;
@@ -806,7 +832,14 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
   a.scale_log2 = (float)(1.4426950408889634 * std::fabs((double)scale));
   a.negate = scale < 0.f;
   a.out = (bf16*)out;
+  a.give_up = t_cache_give_up;
   return cu(launch_cache_attn(a, (cudaStream_t)stream), "cache_attention");
+}
+
+ssd_status ssd_debug_cache_give_up(int32_t cta) {
+  if (cta < -1) return op_fail(SSD_ERR_INVALID_ARG, "cache_give_up: a CTA, or -1");
+  t_cache_give_up = cta;
+  return SSD_OK;
 }
 
 ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* drafts,
@@ -818,8 +851,11 @@ ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* d
   if (!al4(p) || (q && !al4(q)) || (d && (!al4(drafts) || !al4(accept_u))) || (counts && !al4(counts)) ||
       !al4(sample_u) || !al4(tokens) || !al4(n))
     return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts pointers");
-  if (d && overlap(drafts, (size_t)4 * B * d, tokens, (size_t)4 * B * (d + 1)))
-    return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts: drafts and tokens overlap");
+  const size_t n4 = (size_t)4 * B, said = n4 * (d + 1), each = n4 * d;
+  if (meets({{tokens, said}, {n, n4}}, {{p, said * V}, {d ? q : nullptr, each * V}, {d ? drafts : nullptr, each},
+                                        {d ? accept_u : nullptr, each}, {counts, n4}, {sample_u, n4}}) ||
+      meets({{tokens, said}}, {{n, n4}}))
+    return op_fail(SSD_ERR_INVALID_ARG, "verify_drafts: buffers overlap");
   VerifyArgs a;
   a.p = p;
   a.q = d ? q : nullptr;

@@ -565,6 +565,50 @@ def test_calls_repeat_their_bits_and_ignore_the_workspace(ops):
         assert bool((ws[need:] == fill).all())
 
 
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,counts", [
+    ([30000], 1, 16, 2, 128, None),                    # one pair over many CTAs
+    ([2000, 0, 700], 2, 24, 24, 64, [2, 0, 1]),        # many pairs, tokens left out
+    ([5000, 300], 3, 16, 4, 128, None),                # twelve rows
+    ([9000, 4000, 10], 9, 16, 2, 128, [9, 3, 9])])     # 72 rows
+def test_a_wait_that_runs_out_marks_its_rows(ops, lengths, T, H, Hkv, dh, counts):
+    from self_speculative_decoding_gb300 import _abi
+    call = _abi.lib().ssd_debug_cache_give_up
+    B, rows, block = len(lengths), 256, 64
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q = torch.randn(B, T, H, dh, generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn(B, Hkv, rows, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    S = -(-max(lengths) // block) * block
+    held = whole([max(0, n - 100) // block * block for n in lengths])
+    k8, v8 = (torch.randn(B, Hkv, S, dh, generator=g, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.ones(B, Hkv, S // block, device="cuda") for _ in range(2))
+    def run():  # noqa: E306
+        return ops.cache_attention(q, k, v, whole(lengths), k8=k8, v8=v8, k_scale=ks, v_scale=vs, held=held,
+                                   counts=None if counts is None else whole(counts))
+    want = run()
+    assert torch.isfinite(want).all()
+    live = torch.ones(B, T, dtype=torch.bool, device="cuda")
+    for b, c in enumerate(counts or ()):
+        live[b, c:] = False
+    pairs = 0
+    try:
+        for cta in (0, 1, 40, 140):
+            call(cta)
+            out = run()
+            call(-1)
+            lost = torch.isnan(out).permute(0, 2, 1, 3).reshape(B, Hkv, H // Hkv, T, dh)
+            for b in range(B):
+                for h in range(Hkv):
+                    x = lost[b, h][:, live[b]]
+                    assert x.all() or not x.any()
+                    pairs += bool(x.numel() and x.any())
+                    assert not lost[b, h][:, ~live[b]].any()
+            assert torch.equal(out[~torch.isnan(out)], want[~torch.isnan(out)])
+            assert torch.equal(run(), want)
+    finally:
+        call(-1)
+    assert pairs >= 4 and pairs <= 4 * max(2, 2 * B * Hkv // 100 + 3)
+
+
 def test_graphs_follow_the_lengths(ops):
     a = Attn([700, 340], 3, 8, 2, 128, 1024)
     a.k.nan_to_num_(0)
