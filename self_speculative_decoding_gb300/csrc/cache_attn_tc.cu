@@ -35,6 +35,17 @@
 // with maxima and outputs of its own, joined in the end).  The matrix
 // instructions' chain of waits and issues is shared by two warps likewise.
 //
+// Measured (graphs of calls over inputs larger than L2; bytes of the rows read at
+// 6.7 TB/s would be the floor):
+//   1 sequence x 1 token, 64 / 8 heads, 131000 rows       53 us   5.1 TB/s (floor 40)
+//   8 x 2 tokens, 40 / 40 heads, 4095 rows, window 2048   52 us   3.4 TB/s (floor 26)
+//   16 x 9 tokens, 64 / 8 heads, up to 16385 rows        143 us   2.2 TB/s (floor 48)
+// One token is bound by the copies and by the CTAs that end last, many heads by the
+// start and the end of each pair (a few thousand cycles in which nothing streams),
+// 72 rows by the softmax: 840 cycles for 8 rows of a tile in each of three warps of a
+// scheduler, which issues 2.2 instructions a cycle of the SM's four, and the matrix pipe
+// is busy for 15% of the time.
+//
 // The groups' warps come first, then four that widen V, one that copies K, one that
 // copies V, one for the products K q^T and one for V^T P.  Every wait is
 // bounded: one that gives up sets the CTA's flag, every role runs out, and the
@@ -146,7 +157,8 @@ SSD_DI void mma_ss_e4m3(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdes
       ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-// tree_wait, in a loop that stays one.
+// tree_wait, in a loop that stays one.  (A sleeping hint of 2 us costs 72 rows 6
+// us of 147, a loop that polls faster 10, naps in the warps that copy or widen none.)
 SSD_DI bool wait_for(const int* fail, uint64_t* a, uint32_t pa) {
   if (!seldom(!tree_try(a, pa))) return true;
 #pragma unroll 1
@@ -290,7 +302,8 @@ struct Plan {
 // The work is divided in units of a tile.  A pair's start counts as several (q, the
 // first scores and the result's way out are no tile's work, and take as long as
 // kStart tiles), but at most as a quarter of a CTA's tiles: with less
-// to do than that the CTAs' tiles, and not their starts, differ.
+// to do than that the CTAs' tiles, and not their starts, differ.  (0, 3, 5, 8: 8 x 2
+// tokens of 40 heads 70, 62, 59, 60 us; 16 x 9 tokens 162, 155, 154, 154)
 constexpr int kStart = 5;
 // (64-bit divisions cost a thousand cycles where they are cold)
 SSD_DI long long cta_start(long long total, int ctas, int cta) {
@@ -479,8 +492,13 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
 }
 
 // SMALL: up to 16 rows, whose parts of q make one product (twice as wide) and
-// whose state the groups keep in registers.
-// TURNS: up to 8 rows, the groups take the tiles in turn.
+// whose state the groups keep in registers.  (16 sequences of 8192 rows, 8 and 16
+// query rows a pair: 59.6 and 66.3 us, with the kernel for more rows 62.5 and 68.6)
+// TURNS: up to 8 rows, the groups take the tiles in turn.  (the same with 8 rows 56.5
+// us, one sequence of 131000 rows 56.0 -> 52.7; four of 300 rows 11.4 -> 12.0, which
+// the lengths on the device decide and the launch cannot know)
+// More rows: three groups.  (72 rows: 147 us, with four groups, of 80 registers a
+// thread, 168, with five 155)
 constexpr int groups_of(bool small) { return small ? 2 : 3; }
 constexpr int threads_of(bool small) { return (4 * groups_of(small) + 8) * 32; }
 template <int DH, bool SMALL, bool TURNS>
@@ -1324,7 +1342,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
 // Joins a pair that several CTAs share: CTA x = the first of them, thread = 16
 // bytes of a row's output; the parts are added in order.  Bound by latency: the
 // first parts are asked for together with the word that says how many there are.
-// (Few rows are split among many CTAs, many rows among few: kBatch parts at once.)
+// kBatch parts at once.
 constexpr int kJoinThreads = 256;
 template <int DH, int kBatch>
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
@@ -1409,7 +1427,15 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
   lc.stream = st;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH, SMALL ? 20 : 2>, a);
+  // A pair of few rows that 16 CTAs or more share (if the sequences are alike, and
+  // long enough): its parts are asked for at once, in a short join.  Others two at a time: the
+  // loads that go out unasked are traffic.  (20 at a time and 2, us: one sequence of
+  // 131000 rows and 8 heads, 8 query rows each 52.1 and 53.8, 72 rows 127 and 115;
+  // four of 20000 rows 39.9 and 38.5; 16 of 8192 rows 56.4 and 55.1)
+  const long long tiles = ((long long)(a.k8 ? a.max_seq : 0) + a.rows) / kKeys, pairs = (long long)a.B * a.Hkv;
+  const bool many = SMALL && a.ctas / pairs >= 16 && tiles >= 16;
+  return many ? cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH, 20>, a)
+              : cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH, 2>, a);
 }
 
 }  // namespace

@@ -8,6 +8,10 @@
 // Angles: a turn is 2^64, so that position * frequency wraps by itself and
 // keeps 2^-64 of a turn times the position, however far that is; the product's
 // upper half, exact to 2^-24 of a half turn as fp32, gives sine and cosine.
+//
+// Bound by the bytes: fp32 in, bf16 out, once each.  8064 tokens of 120 heads: 743 MB
+// in 115 us, 6.5 TB/s, 97% of a plain copy's; one token: 2.5 us, a launch.  Roundings: q,
+// k', v to bf16, which the caches and the products take; all else is fp32.
 #include "batch.cuh"
 
 namespace ssd {
@@ -109,8 +113,10 @@ cudaError_t launch(const RopeAppendArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s) {
-  // few tokens: a warp for every 256 elements; many: the angles serve 8 times that
-  const bool many = (long long)a.B * a.T * (a.H + 2 * a.Hkv) * a.dh >= (long long)1 << 22;
+  // Few tokens: a warp for every 256 elements; many: the angles serve 8 times that.
+  // (48 heads of 128, us: 64 tokens 3.3 and 4.0, 128 tokens 3.8 and 4.0, 192 tokens
+  // 4.5 and 4.1, 512 tokens 9.2 and 5.1, 4096 tokens 57 and 28)
+  const bool many = (long long)a.B * a.T * (a.H + 2 * a.Hkv) * a.dh >= (long long)1 << 20;
   if (a.dh == 128) return many ? launch<128, 8>(a, s) : launch<128, 1>(a, s);
   return many ? launch<64, 8>(a, s) : launch<64, 1>(a, s);
 }

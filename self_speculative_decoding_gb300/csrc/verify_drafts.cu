@@ -115,7 +115,9 @@ static __device__ __noinline__ float2 sum_run(const Rest& rest, int w0, int w1) 
 // warp.  Each CTA tests the drafts by itself; the sums meet once.  Then the CTA in
 // whose slice the token lies searches it.
 // Bound by latency: the drafts, their probabilities, the row's entries, the
-// cluster's exchange and the search one behind the other.
+// cluster's exchange and the search one behind the other.  48 sequences x 128003
+// entries: 49 MB in 20 us, 2.5 TB/s (7.3 us at a copy's rate); 16 x 32000 without q 9
+// us; one x 1024 6.9 us.
 __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   cluster.barrier_arrive();                      // (all CTAs run before one writes to another)
@@ -274,10 +276,15 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
-  // as many CTAs to a sequence as have 2048 entries each and are resident together
-  // (three of an SM)
+  // As many CTAs to a sequence as have 2048 entries each and an SM for each, and
+  // three of an SM where they have 16000 entries.  (us with 1, 2, 4, 8, 16 CTAs:
+  // one sequence of 32000 entries 12.9, 10.5, 9.1, 8.5, 7.1; 16 of them 13.4, 10.9,
+  // 9.6, 10.0, 10.1; 48 of them 13.6, 11.0, 11.9, 12.4, 18.2; 48 of 128003 39, 25,
+  // 20, 18.7, 27; 128 of 32000 15.2, 15.3, 20, 25, 42)
   int size = 1;
-  while (size < kMaxCluster && a.V > size * 2048 && a.B * size * 2 <= 3 * tree_sms()) size *= 2;
+  while (size < kMaxCluster && a.V > size * 2048 &&
+         (a.B * size * 2 <= tree_sms() || (a.V > size * 16000 && a.B * size * 2 <= 3 * tree_sms())))
+    size *= 2;
   if (size > 8) {
     static bool ready[kDeviceSlots] = {};
     const int dv = device_slot();
