@@ -66,7 +66,8 @@ _native = None
 
 
 def _tree_calls():
-    """The native binding of the tree-decoding calls (csrc/binding.cpp), bound
+    """The native binding of the tree-decoding calls and of those of several
+    sequences (csrc/binding.cpp), bound
     to the loaded library's functions."""
     global _native
     if _native is None:
@@ -78,7 +79,7 @@ def _tree_calls():
             except ImportError as e:
                 why = str(e)
         if why:
-            raise RuntimeError("no native binding of the tree-decoding calls (build it with `python -m "
+            raise RuntimeError("no native binding of the tree-decoding calls and those of several sequences (build it with `python -m "
                                f"self_speculative_decoding_gb300.build`): {why}")
         lib = _lib()
         _binding.bind({n: C.cast(getattr(lib, n), C.c_void_p).value for n in _abi.TREE_CALLS}, SSDError)

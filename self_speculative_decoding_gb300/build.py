@@ -2,7 +2,7 @@
 
 Each translation unit is compiled in parallel to an object file under
 ``_build/`` and linked into ``libssd.so`` next to this file.  The CUDA
-runtime is linked statically.  ``csrc/binding.cpp``, the tree-decoding calls'
+runtime is linked statically.  ``csrc/binding.cpp``, the tree-decoding and several sequences' calls'
 Python module, is compiled against the installed PyTorch's headers into
 ``_binding.so``; where that fails the library is built all the same, and those
 calls raise the reason.
@@ -92,7 +92,7 @@ def _build_binding() -> None:
         reason = str(e)
         if os.path.exists(BINDING):
             os.remove(BINDING)  # of other sources, or another PyTorch
-        warnings.warn(f"no tree-decoding calls, the rest of the library is built: {reason}")
+        warnings.warn(f"no tree-decoding calls and none of several sequences, the rest of the library is built: {reason}")
     with open(STAMP, "w") as f:
         f.write(key + "\n" + reason)
 
