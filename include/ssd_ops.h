@@ -320,7 +320,8 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * of the sequence sees are needed.  A sequence whose numbers make no sense
  * (lengths[b] negative or beyond 2^31 - 257 - T, counts[b] outside 0..T, held[b]
  * outside 0..max_seq or beyond lengths[b] + counts[b]), or of whose rows the
- * ring no longer holds one that is needed, gives NaN in all of its rows of out.
+ * ring no longer holds one that is needed, gives NaN in all of its rows of out;
+ * so does one that has gone round a ring whose rows are no multiple of 128.
  * Scores are exact products of the bf16 query and the stored keys, summed in
  * fp32 (elements of q below 2^-9 of their row's largest are good to 2^-17 of
  * that; a query row with infinity or NaN gives NaN); probabilities are rounded to

@@ -122,7 +122,8 @@ SSD_DI SeqRange seq_range(const CacheAttnArgs& a, int length, int count, int hel
   r.low = a.window ? max(0, length + 1 - a.window) : 0;
   r.sinks = min(a.sinks, r.low);
   if (r.sinks == r.low) r.sinks = r.low = 0;     // one run of rows
-  // rows from `held` on come from the ring, which has the newest only
+  // rows from `held` on come from the ring, which has the newest only (and whose end
+  // no tile of 128 may cross)
   const int first = r.sinks > held ? held : max(r.low, held);
   if (r.end - first > a.rows || (a.rows % 128 && r.end > a.rows && r.end > first)) {
     r = SeqRange{0, -1, 0, 0, 0, 0};

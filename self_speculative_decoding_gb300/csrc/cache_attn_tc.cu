@@ -69,7 +69,7 @@ constexpr int kWiden = 128;                      // threads that widen V
 constexpr int kPolls = 1 << 22;
 constexpr int kUnit = 16 * 1024;                 // 128 rows of up to 128 bytes, swizzled
 constexpr float kRaise = 8.f;
-constexpr float kNone = -1e30f;                  // the maximum of a row that has seen no key
+constexpr float kNone = -3.402823466e38f;        // the maximum of a row that has seen no key: no score is below
 
 // A condition that seldom holds: its code lies apart from the loop's.
 SSD_DI bool seldom(bool x) { return __builtin_expect(x, false); }
@@ -1098,13 +1098,14 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               float2 v = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              const float2 at = from_m ? make_float2(nm[e], nm[e + 1]) : make_float2(0.f, 0.f);
               if (eight) {
                 if (SMALL) v = __fadd2_rn(v, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
-                v = __ffma2_rn(v, __fmul2_rn(make_float2(c[e], c[e + 1]), k2), at);
+                v = __fmul2_rn(v, __fmul2_rn(make_float2(c[e], c[e + 1]), k2));
               } else {
-                v = __ffma2_rn(v, s2, at);
+                v = __fmul2_rn(v, s2);
               }
+              // (not fused: m is a rounded product, and so is at most 8 below any)
+              if (from_m) v = __fadd2_rn(v, make_float2(nm[e], nm[e + 1]));
               d[e] = v.x;
               d[e + 1] = v.y;
             }
@@ -1177,8 +1178,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
             scores(true);
           }
           // (the next chunk's products come in behind the exponentials)
-          const bool more = !SMALL && q + q_step < chunks;
-          if (more) tmem_ld8_nw(scol + q_step * 8, x);
+          if (!SMALL) tmem_ld8_nw(scol + (q + q_step < chunks ? q_step * 8 : 0), x);
           uint32_t pk[4];
 #pragma unroll
           for (int e = 0; e < 8; ++e) d[e] = tree_ex2(d[e]);

@@ -422,6 +422,32 @@ def test_scores_far_apart(ops):
     a.check(a.call(ops))
 
 
+@pytest.mark.parametrize("T,H,Hkv", [(1, 4, 1), (3, 4, 1), (9, 4, 1)])
+@pytest.mark.parametrize("far", [-1e30, -2e38, 2e38])
+def test_scores_near_the_ends_of_the_range(ops, T, H, Hkv, far):
+    # equal scores, however far from 0, weigh their rows alike: 2^k sums are exact
+    dh, n, held = 64, 300, 256
+    q = torch.zeros(1, T, H, dh, device="cuda").bfloat16()
+    q[..., 0] = 2.0 ** 60 if far > 0 else -2.0 ** 60
+    row = abs(far) / 2.0 ** 60
+    e = int(np.floor(np.log2(row)))
+    rng = np.random.default_rng(3)
+    k = torch.zeros(1, Hkv, 512, dh, device="cuda").bfloat16()
+    k[..., 0] = 2.0 ** e
+    v = normal(rng, 1, Hkv, 512, dh).bfloat16().cuda()
+    k8 = torch.zeros(1, Hkv, held, dh, device="cuda").to(torch.float8_e4m3fn)
+    k8[..., 0] = 1.0
+    v8 = normal(rng, 1, Hkv, held, dh).to(torch.float8_e4m3fn).cuda()
+    ks = torch.full((1, Hkv, held // 64), 2.0 ** e, device="cuda")
+    vs = torch.ones_like(ks)
+    out = ops.cache_attention(q, k, v, whole([n]), k8=k8, v8=v8, k_scale=ks, v_scale=vs, held=whole([held]), scale=1.0)
+    V = torch.cat((v8.double()[0, 0], v.double()[0, 0, held:n + T]))
+    for t in range(T):
+        want, spread = V[:n + 1 + t].mean(0), V[:n + 1 + t].abs().mean(0)
+        off = (out[0, t].double() - want).abs() / (U * want.abs() + U * spread + 1e-30)
+        assert off.max().item() <= 1, off.max().item()
+
+
 def test_a_mass_of_small_weights_beside_a_large_one(ops):
     # a first key 12 above 20000 others, whose sum is a tenth of it: none of
     # them may be lost
