@@ -168,6 +168,12 @@ SSD_DI bool wait_for(const int* fail, uint64_t* a, uint32_t pa) {
   }
   return false;
 }
+// The same for two barriers, or the first alone: one latency for both where they are over.
+SSD_DI bool wait_for_both(const int* fail, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, bool two) {
+  const bool da = tree_try(a, pa), db = tree_try(two ? b : a, two ? pb : pa);
+  if (!seldom(!(da && db))) return true;
+  return wait_for(fail, a, pa) && (!two || wait_for(fail, b, pb));
+}
 // The barrier of a group of four softmax warps.
 SSD_DI void bar_group(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
 // Of both groups.
@@ -696,6 +702,10 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
       ok = __all_sync(0xffffffffu, ok && wait_for(fail, bar, parity));
       tc_fence_after();
     };
+    auto wait_both = [&](uint64_t* a0, uint32_t p0, uint64_t* a1, uint32_t p1, bool two) {
+      ok = __all_sync(0xffffffffu, ok && wait_for_both(fail, a0, p0, a1, p1, two));
+      tc_fence_after();
+    };
     uint32_t n = 0;                              // tiles so far
     if (warp == kMmaWarp) {
       // scores: K q^T
@@ -719,8 +729,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         for (int i = 0; ok && i < sn; ++i, ++n) {
           const uint32_t buf = n & 1u, d = tm + buf * scols;
           // the softmax has read what was in this place
-          if (n >= 2) wait(&pready[buf], ((n >> 1) & 1u) ^ 1u);
-          wait(&kfull[kslot], kphase);
+          wait_both(&kfull[kslot], kphase, &pready[buf], ((n >> 1) & 1u) ^ 1u, n >= 2);
           if (!ok) break;
           if (!seldom(i >= in_eight)) {
             const uint32_t kb = kr + (uint32_t)kslot * kUnit;
@@ -766,8 +775,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
 #pragma unroll 1
         for (int i = 0; ok && i < sn; ++i, ++n) {
           const uint32_t buf = n & 1u, ph = (n >> 1) & 1u;
-          wait(&wfull[buf], ph);
-          wait(&pready[buf], ph);
+          wait_both(&pready[buf], ph, &wfull[buf], ph, true);
           if (!ok) break;
           const uint64_t vd = v_desc(wr + buf * (uint32_t)kWide);
           const uint64_t pd = p_desc(pr + (lay.p_bufs == 2 ? buf * (uint32_t)NP * 256u : 0u));
@@ -821,8 +829,8 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
         const bool edge = t.edge();
         const uint32_t buf = n & 1u;
         unsigned char* to = wide + buf * kWide;
-        wait_w(&vfull[slot], phase);
-        if (ok && n >= 2) wait_w(&wempty[buf], ((n >> 1) & 1u) ^ 1u);
+        ok = __all_sync(0xffffffffu, ok && wait_for_both(fail, &vfull[slot], phase, &wempty[buf],
+                                                         ((n >> 1) & 1u) ^ 1u, n >= 2));
         if (!ok) break;
         // (a warp has rows 32 cw .. + 31 of the tile)
         if (!seldom(!t.eight)) {
@@ -1066,8 +1074,13 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
           step(t, place, a.window);
           fetch(t);
         }
-        wait_w(&sfull[buf], (n >> 1) & 1u);
-        if (n >= 2) wait_w(&wempty[buf], ((n >> 1) & 1u) ^ 1u);  // P's place is free
+        // the scores are there, P's place is free
+        if (ok) {
+          ok = __all_sync(0xffffffffu, wait_for_both(fail, &sfull[buf], (n >> 1) & 1u, &wempty[buf],
+                                                     ((n >> 1) & 1u) ^ 1u, n >= 2));
+          if (seldom(!ok) && lane == 0) atomicExch(fail, 1);
+        }
+        tc_fence_after();
         if (!SMALL && lay.p_bufs == 1 && n > 0) wait_values(n);  // (its only one)
         float pv = vc * unit;
         unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
