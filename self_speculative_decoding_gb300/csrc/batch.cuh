@@ -94,6 +94,26 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s);
 
+// A launch whose CTAs may start while the kernel before ends; the kernel waits for
+// that one (pdl_wait) before it touches memory, and lets the next start likewise.
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,
+                                A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&lc, kernel, static_cast<A&&>(args)...);
+}
+
 // Tokens of sequence b in a call (none where its numbers make no sense).
 SSD_DI int batch_count(const int32_t* counts, const int32_t* lengths, int b, int T) {
   const int n = lengths[b];

@@ -575,6 +575,7 @@ __global__ void __launch_bounds__(threads_of(SMALL), 1)
     const CUtensorMap* m = lane == 0 ? &mK8 : lane == 1 ? &mV8 : lane == 2 ? &mK : &mV;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
+  pdl_wait();                                    // (up to here beside the kernel before; nothing is held)
   if (warp == 0) tmem_alloc(tslot, 512);
 #pragma unroll 1
   for (int b = tid; b < a.B; b += kThreads) {
@@ -1381,6 +1382,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
     }
   };
   pdl_wait();
+  pdl_trigger();
   const int4 pair = a.shared[c0];
   const int guess = min((int)gridDim.x - c0, kBatch);
   load(0, guess);                                // (what is there: some of it nobody wrote)
@@ -1428,18 +1430,10 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  cache_attn_tc_kernel<DH, SMALL, TURNS><<<a.ctas, threads_of(SMALL), lay.bytes, st>>>(m[0], m[1], m[2], m[3], a, lay);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(cache_attn_tc_kernel<DH, SMALL, TURNS>, a.ctas, threads_of(SMALL), lay.bytes, st, 0,
+                                     m[0], m[1], m[2], m[3], a, lay);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(a.ctas, (a.T * a.G * (DH / 4) + kJoinThreads - 1) / kJoinThreads);
-  lc.blockDim = dim3(kJoinThreads);
-  lc.stream = st;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
+  const dim3 grid(a.ctas, (a.T * a.G * (DH / 4) + kJoinThreads - 1) / kJoinThreads);
   // A pair of few rows that 16 CTAs or more share (if the sequences are alike, and
   // long enough): its parts are asked for at once, in a short join.  Others two at a time: the
   // loads that go out unasked are traffic.  (20 at a time and 2, us: one sequence of
@@ -1447,8 +1441,8 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
   // four of 20000 rows 39.9 and 38.5; 16 of 8192 rows 56.4 and 55.1)
   const long long tiles = ((long long)(a.k8 ? a.max_seq : 0) + a.rows) / kKeys, pairs = (long long)a.B * a.Hkv;
   const bool many = SMALL && a.ctas / pairs >= 16 && tiles >= 16;
-  return many ? cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH, 20>, a)
-              : cudaLaunchKernelEx(&lc, cache_attn_join_kernel<DH, 2>, a);
+  return many ? launch_early(cache_attn_join_kernel<DH, 20>, grid, kJoinThreads, 0, st, 0, a)
+              : launch_early(cache_attn_join_kernel<DH, 2>, grid, kJoinThreads, 0, st, 0, a);
 }
 
 }  // namespace

@@ -60,6 +60,8 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
   __shared__ int first[kBatchMaxSeqs + 1];       // blocks of all sequences before b
   __shared__ uint32_t warp_max[2][kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
   for (int b = tid; b < a.B; b += kThreads) {
     int from, to;
     blocks_of(a, b, from, to);
@@ -164,11 +166,10 @@ __global__ void __launch_bounds__(kThreads) cache_quantize_kernel(const __grid_c
 template <int DH>
 cudaError_t launch(const QuantizeArgs& a, unsigned ctas, cudaStream_t s) {
   switch (a.block) {
-    case 32: cache_quantize_kernel<DH, 32 * DH / 8 / kThreads><<<ctas, kThreads, 0, s>>>(a); break;
-    case 64: cache_quantize_kernel<DH, 64 * DH / 8 / kThreads><<<ctas, kThreads, 0, s>>>(a); break;
-    default: cache_quantize_kernel<DH, 128 * DH / 8 / kThreads><<<ctas, kThreads, 0, s>>>(a);
+    case 32: return launch_early(cache_quantize_kernel<DH, 32 * DH / 8 / kThreads>, ctas, kThreads, 0, s, 0, a);
+    case 64: return launch_early(cache_quantize_kernel<DH, 64 * DH / 8 / kThreads>, ctas, kThreads, 0, s, 0, a);
+    default: return launch_early(cache_quantize_kernel<DH, 128 * DH / 8 / kThreads>, ctas, kThreads, 0, s, 0, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

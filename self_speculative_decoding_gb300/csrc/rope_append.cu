@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
   const int b = (int)(token / (unsigned)a.T), t = (int)(token - (unsigned)b * a.T);
   const float* src = a.qkv + ((size_t)token * heads + h) * DH + i;
   float x[8], next[8] = {};
+  pdl_wait();
+  pdl_trigger();
   if (h < heads) load_quads(src, next, kHalf);
   const int n = a.lengths[b];
   const bool here = t < batch_count(a.counts, a.lengths, b, a.T);
@@ -105,9 +107,8 @@ cudaError_t launch(const RopeAppendArgs& a, cudaStream_t s) {
   constexpr int kEach = 256 / DH * kSteps;
   const long long warps = (long long)a.B * a.T * ((a.H + 2 * a.Hkv + kEach - 1) / kEach);
   const unsigned ctas = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-  if (a.q_gain || a.k_gain) rope_append_kernel<DH, kSteps, true><<<ctas, kThreads, 0, s>>>(a);
-  else rope_append_kernel<DH, kSteps, false><<<ctas, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.q_gain || a.k_gain ? launch_early(rope_append_kernel<DH, kSteps, true>, ctas, kThreads, 0, s, 0, a)
+                              : launch_early(rope_append_kernel<DH, kSteps, false>, ctas, kThreads, 0, s, 0, a);
 }
 
 }  // namespace

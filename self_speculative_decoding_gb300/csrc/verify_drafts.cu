@@ -129,6 +129,8 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / size;
+  pdl_wait();
+  pdl_trigger();
   const int count = a.counts ? min(max(a.counts[b], 0), a.d) : a.d;
   const float sample = a.sample_u[b];
   // the drafts in order, 32 at a time (by each warp for itself)
@@ -294,16 +296,7 @@ cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
       if (dv >= 0) ready[dv] = true;
     }
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)size, 1, 1};
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(a.B * size));
-  lc.blockDim = dim3(kThreads);
-  lc.stream = s;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, verify_drafts_kernel, a);
+  return launch_early(verify_drafts_kernel, (unsigned)(a.B * size), kThreads, 0, s, size, a);
 }
 
 }  // namespace ssd
