@@ -37,14 +37,14 @@
 //
 // Measured (graphs of calls over inputs larger than L2; bytes of the rows read at
 // 6.7 TB/s would be the floor):
-//   1 sequence x 1 token, 64 / 8 heads, 131000 rows       53 us   5.1 TB/s (floor 40)
-//   8 x 2 tokens, 40 / 40 heads, 4095 rows, window 2048   52 us   3.4 TB/s (floor 26)
-//   16 x 9 tokens, 64 / 8 heads, up to 16385 rows        143 us   2.2 TB/s (floor 48)
+//   1 sequence x 1 token, 64 / 8 heads, 131000 rows       51 us   5.2 TB/s (floor 40)
+//   8 x 2 tokens, 40 / 40 heads, 4095 rows, window 2048   48 us   3.6 TB/s (floor 26)
+//   16 x 9 tokens, 64 / 8 heads, up to 16385 rows        134 us   2.4 TB/s (floor 48)
 // One token is bound by the copies and by the CTAs that end last, many heads by the
 // start and the end of each pair (a few thousand cycles in which nothing streams),
-// 72 rows by the softmax: 840 cycles for 8 rows of a tile in each of three warps of a
-// scheduler, which issues 2.2 instructions a cycle of the SM's four, and the matrix pipe
-// is busy for 15% of the time.
+// 72 rows by the softmax: some 800 cycles for 8 rows of a tile in each of three warps of
+// a scheduler; the SM issues 2.1 instructions a cycle of four, and the matrix pipe
+// is busy for 16% of the time.
 //
 // The groups' warps come first, then four that widen V, one that copies K, one that
 // copies V, one for the products K q^T and one for V^T P.  Every wait is
@@ -499,20 +499,21 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
 
 // SMALL: up to 16 rows, whose parts of q make one product (twice as wide) and
 // whose state the groups keep in registers.  (16 sequences of 8192 rows, 8 and 16
-// query rows a pair: 59.6 and 66.3 us, with the kernel for more rows 62.5 and 68.6)
-// TURNS: up to 8 rows, the groups take the tiles in turn.  (the same with 8 rows 56.5
-// us, one sequence of 131000 rows 56.0 -> 52.7; four of 300 rows 11.4 -> 12.0, which
+// query rows a pair: 54.8 and 59.2 us, with the kernel for more rows 58.8 and 63.9)
+// TURNS: up to 8 rows, the groups take the tiles in turn.  (the same with 8 rows 52.7
+// us, one sequence of 131000 rows 52.3 -> 51.2; four of 300 rows 10.3 -> 10.7, which
 // the lengths on the device decide and the launch cannot know)
-// More rows: three groups.  (72 rows: 147 us, with four groups, of 80 registers a
-// thread, 168, with five 155)
-constexpr int groups_of(bool small) { return small ? 2 : 3; }
-constexpr int threads_of(bool small) { return (4 * groups_of(small) + 8) * 32; }
-template <int DH, bool SMALL, bool TURNS>
-__global__ void __launch_bounds__(threads_of(SMALL), 1)
+// More rows: three groups, or two where that leaves none with more than two chunks
+// (25 to 32 rows).  (16 sequences of 8192 rows, 24, 32 and 40 query rows: three groups
+// 68.7, 81.3 and 85.0 us, two 73.7, 77.9 and 89.2; 72 rows: three 134, two 149, four, of 80
+// registers a thread, 155)
+constexpr int threads_of(int groups) { return (4 * groups + 8) * 32; }
+template <int DH, int kGroups, bool SMALL, bool TURNS>
+__global__ void __launch_bounds__(threads_of(kGroups), 1)
     cache_attn_tc_kernel(const __grid_constant__ CUtensorMap mK8, const __grid_constant__ CUtensorMap mV8,
                          const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                          const __grid_constant__ CacheAttnArgs a, const Layout lay) {
-  constexpr int kGroups = groups_of(SMALL), kThreads = threads_of(SMALL);
+  constexpr int kThreads = threads_of(kGroups);
   constexpr int kWidenWarp = 4 * kGroups, kCopyWarp = kWidenWarp + 4, kMmaWarp = kCopyWarp + 2;
   constexpr int P = DH / 64;                     // 16-bit panels of 64 columns
   constexpr int kWide = P * kUnit;               // a V tile in 16 bits
@@ -1419,18 +1420,18 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
   *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int DH, bool SMALL, bool TURNS>
+template <int DH, int GROUPS, bool SMALL, bool TURNS>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream_t st) {
   const Layout lay = layout_of(a.T * a.G, DH, a.B);
   static bool ready[kDeviceSlots] = {};
   const int dv = device_slot();
   if (dv < 0 || !ready[dv]) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, SMALL, TURNS>,
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<DH, GROUPS, SMALL, TURNS>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  const cudaError_t e = launch_early(cache_attn_tc_kernel<DH, SMALL, TURNS>, a.ctas, threads_of(SMALL), lay.bytes, st, 0,
+  const cudaError_t e = launch_early(cache_attn_tc_kernel<DH, GROUPS, SMALL, TURNS>, a.ctas, threads_of(GROUPS), lay.bytes, st, 0,
                                      m[0], m[1], m[2], m[3], a, lay);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.ctas, (a.T * a.G * (DH / 4) + kJoinThreads - 1) / kJoinThreads);
@@ -1443,6 +1444,14 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
   const bool many = SMALL && a.ctas / pairs >= 16 && tiles >= 16;
   return many ? launch_early(cache_attn_join_kernel<DH, 20>, grid, kJoinThreads, 0, st, 0, a)
               : launch_early(cache_attn_join_kernel<DH, 2>, grid, kJoinThreads, 0, st, 0, a);
+}
+
+template <int DH>
+cudaError_t launch_rows(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream_t st) {
+  const int rows = a.T * a.G;
+  if (rows <= 8) return launch<DH, 2, true, true>(a, m, st);
+  if (rows <= 16) return launch<DH, 2, true, false>(a, m, st);
+  return rows > 24 && rows <= 32 ? launch<DH, 2, false, false>(a, m, st) : launch<DH, 3, false, false>(a, m, st);
 }
 
 }  // namespace
@@ -1485,14 +1494,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   m[1] = m[3];
   if (a.k8 && (!map(&m[0], true, a.k8, a.max_seq, a.seq8_stride) || !map(&m[1], true, a.v8, a.max_seq, a.seq8_stride)))
     return cudaErrorInvalidValue;
-  const int rows = a.T * a.G;
-  if (a.dh == 128)
-    return rows <= 8    ? launch<128, true, true>(a, m, s)
-           : rows <= 16 ? launch<128, true, false>(a, m, s)
-                        : launch<128, false, false>(a, m, s);
-  return rows <= 8    ? launch<64, true, true>(a, m, s)
-         : rows <= 16 ? launch<64, true, false>(a, m, s)
-                      : launch<64, false, false>(a, m, s);
+  return a.dh == 128 ? launch_rows<128>(a, m, s) : launch_rows<64>(a, m, s);
 }
 
 }  // namespace ssd

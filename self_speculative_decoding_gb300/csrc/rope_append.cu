@@ -10,7 +10,7 @@
 // upper half, exact to 2^-24 of a half turn as fp32, gives sine and cosine.
 //
 // Bound by the bytes: fp32 in, bf16 out, once each.  8064 tokens of 120 heads: 743 MB
-// in 115 us, 6.5 TB/s, 97% of a plain copy's; one token: 2.5 us, a launch.  Roundings: q,
+// in 114 us, 6.5 TB/s, 97% of a plain copy's; one token: 2.3 us, a launch.  Roundings: q,
 // k', v to bf16, which the caches and the products take; all else is fp32.
 #include "batch.cuh"
 

@@ -116,8 +116,8 @@ static __device__ __noinline__ float2 sum_run(const Rest& rest, int w0, int w1) 
 // whose slice the token lies searches it.
 // Bound by latency: the drafts, their probabilities, the row's entries, the
 // cluster's exchange and the search one behind the other.  48 sequences x 128003
-// entries: 49 MB in 20 us, 2.5 TB/s (7.3 us at a copy's rate); 16 x 32000 without q 9
-// us; one x 1024 6.9 us.
+// entries: 49 MB in 20 us, 2.5 TB/s (7.3 us at a copy's rate); 16 x 32000 without q
+// 8.7 us; one x 1024 6.2 us.
 __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   cluster.barrier_arrive();                      // (all CTAs run before one writes to another)
