@@ -81,7 +81,8 @@ struct Layout {
   int p_bufs, k_units, v_units;
 };
 constexpr int kSmemMost = 227 * 1024 - 1024;     // (from a 1024-byte boundary)
-constexpr int kSmall = (4 * 128 + 4 * 128) * 4 + 512 + 19 * 96;       // per-row values, barriers
+constexpr int kPlaces = 20 * 80;                 // of up to 20 warps
+constexpr int kSmall = (4 * 128 + 4 * 128) * 4 + 512 + kPlaces + 96;  // per-row values, barriers, places
 __host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
   Layout l;
   l.rows = (rows + 15) / 16 * 16;
@@ -632,6 +633,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
   const long long begin = plan.begin, end = plan.end;
   Place& place = places[warp];
   static_assert(sizeof(Place) % 4 == 0 && sizeof(Place) <= 128, "a word per lane");
+  static_assert(sizeof(Place) * (kThreads / 32) <= kPlaces, "a place per warp");
   if (warp && lane < (int)sizeof(Place) / 4)
     reinterpret_cast<int*>(&place)[lane] = reinterpret_cast<const int*>(places)[lane];
   __syncthreads();                               // (the first warp's own may change from here on)

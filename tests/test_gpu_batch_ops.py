@@ -787,6 +787,55 @@ def test_another_stream_and_a_given_output(ops):
     assert torch.equal(out, want)
 
 
+def test_two_threads_and_streams_at_once(ops):
+    # calls that start beside one another's ends, from two threads, say what they say alone
+    import threading
+    def work(seed):  # noqa: E306
+        rng = np.random.default_rng(seed)
+        H, Hkv, dh, V, T = (16, 2, 128, 5000, 3) if seed else (8, 8, 64, 32000, 1)
+        k, v = (torch.zeros(3, Hkv, 1024, dh, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        k8, v8 = (torch.zeros(3, Hkv, 1024, dh, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.ones(3, Hkv, 1024 // 64, device="cuda") for _ in range(2))
+        lengths, held = whole([0, 0, 0]), whole([0, 0, 0])
+        p = torch.from_numpy(probabilities(rng, 3, T + 1, V).astype(np.float32)).cuda()
+        au, su = (torch.from_numpy(rng.random(n).astype(np.float32)).cuda() for n in ((3, T), 3))
+        drafts = torch.from_numpy(rng.integers(0, V, (3, T)).astype(np.int32)).cuda()
+        qkv = [normal(rng, 3, 200, (H + 2 * Hkv) * dh).cuda()] + [normal(rng, 3, T, (H + 2 * Hkv) * dh).cuda()
+                                                                  for _ in range(30)]
+        said = []
+        for x in qkv:
+            q = ops.rope_append(x, lengths, k, v, H, Hkv, dh, 1e4)
+            if x.shape[1] == T:
+                said.append(ops.cache_attention(q, k, v, lengths, k8, v8, ks, vs, held, window=150, sinks=3))
+                said += ops.verify_drafts(p, drafts, au, su)
+            lengths = lengths + x.shape[1]
+            held = ops.cache_quantize(k, v, held, lengths, k8, v8, ks, vs)
+        return said + [k, v, bits(k8), bits(v8), ks, vs, held]
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                got[i] = work(i)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for w, g in zip(want, got):
+        assert all(torch.isfinite(x.float()).all() for x in w[:1])
+        assert len(w) == len(g) and all(torch.equal(x, y) for x, y in zip(w, g))
+
+
 def test_arguments_of_the_python_calls(ops):
     a = Attn([300, 40], 2, 4, 2, 64, 256, [256, 0])
     q, k, v, n = a.q.cuda(), a.k, a.v, whole(a.lengths)
