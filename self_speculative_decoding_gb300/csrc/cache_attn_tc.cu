@@ -1088,151 +1088,158 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         if (!SMALL && lay.p_bufs == 1 && n > 0) wait_values(n);  // (its only one)
         float pv = vc * unit;
         unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
-        // the tokens that see the key, of chunk q's rows
-        auto seen_of = [&](int q) {
-          const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
-          return m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
-        };
-        bool force = over || vref == 0.f;
-        uint32_t x[8], y[8];                     // products; SMALL: their second parts, else the sums
-        tmem_ld8_nw(trow + buf * scols + q0 * 8, x);
-        if (SMALL) tmem_ld8_nw(trow + buf * scols + q0 * 8 + 16, y);
-        tmem_wait_ld();
-        tmem_pin8(x);
-        if (SMALL) tmem_pin8(y);
+        // (more than 16 rows: the loop once for each kind of tile, 72 rows 134.2 -> 130.9
+        // us; for few rows the longer code costs one token 0.6 us of 51.5)
+        auto tile = [&](auto kind) {
+          const bool in_eight = SMALL ? eight : decltype(kind)::value;
+          // the tokens that see the key, of chunk q's rows
+          auto seen_of = [&](int q) {
+            const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
+            return m1 > m0 ? ((1u << m1) - 1u) & ~((1u << m0) - 1u) : 0u;
+          };
+          bool force = over || vref == 0.f;
+          uint32_t x[8], y[8];                     // products; SMALL: their second parts, else the sums
+          tmem_ld8_nw(trow + buf * scols + q0 * 8, x);
+          if (SMALL) tmem_ld8_nw(trow + buf * scols + q0 * 8 + 16, y);
+          tmem_wait_ld();
+          tmem_pin8(x);
+          if (SMALL) tmem_pin8(y);
 #pragma unroll 1
-        for (int q = q0; q < chunks; q += q_step) {
-          const uint32_t scol = trow + buf * scols + q * 8;
-          if (!SMALL) {
-            tmem_ld8_nw(trow + col_l + q * 8, y);  // (needed in the end)
-            state(q);
-          }
-          // scores (of the products' two parts), as multiples of what the exponential
-          // takes, minus m
-          float d[8];
-          auto scores = [&](bool from_m) {
-            const float2 k2 = make_float2(kc, kc), s2 = make_float2(a.scale_log2, a.scale_log2);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              float2 v = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              if (eight) {
-                if (SMALL) v = __fadd2_rn(v, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
-                v = __fmul2_rn(v, __fmul2_rn(make_float2(c[e], c[e + 1]), k2));
-              } else {
-                v = __fmul2_rn(v, s2);
-              }
-              // (not fused: m is a rounded product, and so is at most 8 below any)
-              if (from_m) v = __fadd2_rn(v, make_float2(nm[e], nm[e + 1]));
-              d[e] = v.x;
-              d[e + 1] = v.y;
+          for (int q = q0; q < chunks; q += q_step) {
+            const uint32_t scol = trow + buf * scols + q * 8;
+            if (!SMALL) {
+              tmem_ld8_nw(trow + col_l + q * 8, y);  // (needed in the end)
+              state(q);
             }
-            if (seldom(edge)) {
+            // scores (of the products' two parts), as multiples of what the exponential
+            // takes, minus m
+            float d[8];
+            auto scores = [&](bool from_m) {
+              const float2 k2 = make_float2(kc, kc), s2 = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                float2 v = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                if (in_eight) {
+                  if (SMALL) v = __fadd2_rn(v, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
+                  v = __fmul2_rn(v, __fmul2_rn(make_float2(c[e], c[e + 1]), k2));
+                } else {
+                  v = __fmul2_rn(v, s2);
+                }
+                // (not fused: m is a rounded product, and so is at most 8 below any)
+                if (from_m) v = __fadd2_rn(v, make_float2(nm[e], nm[e + 1]));
+                d[e] = v.x;
+                d[e + 1] = v.y;
+              }
+              if (seldom(edge)) {
+                const uint32_t seen = seen_of(q);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (!((seen >> e) & 1u)) d[e] = -INFINITY;
+              }
+            };
+            scores(true);
+            const float top = tree_max3(tree_max3(d[0], d[1], d[2]), tree_max3(d[3], d[4], d[5]), fmaxf(d[6], d[7]));
+            if (seldom(any_group(group, top > kRaise || force))) {
+              if (q == q0) {
+                // the largest of the four warps' scales
+                if (lane == 0) gpart[w4] = over ? fabsf(vc) : 0.f;
+                bar_group(group);
+                const float most = fmaxf(fmaxf(gpart[0], gpart[1]), fmaxf(gpart[2], gpart[3]));
+                if (most > vref || vref == 0.f) {
+                  const float next = most > 0.f ? power_above(most) * 4.f : 1.f;
+                  if (i > i_first) {
+                    if (!TURNS) wait_values(n);
+#pragma unroll 1
+                    for (int z = q0; z < chunks; z += q_step) rescale(z, nullptr, vref / next);
+                  }
+                  vref = next;
+                  unit = 0x1p7f / next;
+                  pv = vc * unit;
+                }
+                over = false;
+                force = vref == 0.f;
+                bar_group(group);
+              }
+              // the rows' largest scores of all keys; those that pass m + 8 become m
+              tmem_ld8_nw(scol, x);
+              if (SMALL) tmem_ld8_nw(scol + 16, y);
+              tmem_wait_ld();
+              tmem_pin8(x);
+              tmem_pin8(y);
+              scores(false);
+              over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
+              if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = d[0];
+              bar_group(group);
+              if (key < 8) {
+                const int at_row = (s0 + q) * 8 + key;
+                const float old = -row_nm[at_row];
+                const float z = fmaxf(fmaxf(gpart[key], gpart[8 + key]), fmaxf(gpart[16 + key], gpart[24 + key]));
+                const float m = z > old + kRaise ? z : old;
+                row_f[at_row] = tree_ex2(old - m);
+                row_nm[at_row] = -m;
+              }
+              bar_group(group);
+              float g[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                g[e] = row_f[(s0 + q) * 8 + e];
+                nm[e] = row_nm[(s0 + q) * 8 + e];
+                if (SMALL) ls[e] *= g[e];
+                else y[e] = __float_as_uint(__uint_as_float(y[e]) * g[e]);
+              }
+              if (i > i_first) {                   // (O as the tile before left it)
+                if (!TURNS) wait_values(n);
+                rescale(q, g, 1.f);
+              }
+              tmem_ld8_nw(scol, x);
+              if (SMALL) tmem_ld8_nw(scol + 16, y);
+              tmem_wait_ld();
+              tmem_pin8(x);
+              if (SMALL) tmem_pin8(y);
+              scores(true);
+            }
+            // (the next chunk's products come in behind the exponentials)
+            if (!SMALL) tmem_ld8_nw(scol + (q + q_step < chunks ? q_step * 8 : 0), x);
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = tree_ex2(d[e]);
+            if (SMALL)
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float2 v = __fadd2_rn(make_float2(ls[e], ls[e + 1]), make_float2(d[e], d[e + 1]));
+                ls[e] = v.x;
+                ls[e + 1] = v.y;
+              }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = __fmul2_rn(make_float2(d[2 * e], d[2 * e + 1]), make_float2(pv, pv));
+              pk[e] = in_eight ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
+            }
+            if (seldom(edge)) {                    // (a scale that is none of the row's)
               const uint32_t seen = seen_of(q);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (!((seen >> e) & 1u)) d[e] = -INFINITY;
+              for (int e = 0; e < 8; e += 2)
+                pk[e / 2] &= ((seen >> e) & 1u ? 0x0000ffffu : 0u) | ((seen >> e) & 2u ? 0xffff0000u : 0u);
             }
-          };
-          scores(true);
-          const float top = tree_max3(tree_max3(d[0], d[1], d[2]), tree_max3(d[3], d[4], d[5]), fmaxf(d[6], d[7]));
-          if (seldom(any_group(group, top > kRaise || force))) {
-            if (q == q0) {
-              // the largest of the four warps' scales
-              if (lane == 0) gpart[w4] = over ? fabsf(vc) : 0.f;
-              bar_group(group);
-              const float most = fmaxf(fmaxf(gpart[0], gpart[1]), fmaxf(gpart[2], gpart[3]));
-              if (most > vref || vref == 0.f) {
-                const float next = most > 0.f ? power_above(most) * 4.f : 1.f;
-                if (i > i_first) {
-                  if (!TURNS) wait_values(n);
-#pragma unroll 1
-                  for (int z = q0; z < chunks; z += q_step) rescale(z, nullptr, vref / next);
-                }
-                vref = next;
-                unit = 0x1p7f / next;
-                pv = vc * unit;
+            *reinterpret_cast<uint4*>(pto + (q >> 1) * kPanel + (((q & 1) ^ ((key >> 2) & 1)) << 4)) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            if (!SMALL) {
+              tmem_wait_ld();
+              tmem_pin8(x);
+              tmem_pin8(y);
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float2 v = __fadd2_rn(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
+                                            make_float2(d[e], d[e + 1]));
+                y[e] = __float_as_uint(v.x);
+                y[e + 1] = __float_as_uint(v.y);
               }
-              over = false;
-              force = vref == 0.f;
-              bar_group(group);
+              tmem_st8(trow + col_l + q * 8, y);
             }
-            // the rows' largest scores of all keys; those that pass m + 8 become m
-            tmem_ld8_nw(scol, x);
-            if (SMALL) tmem_ld8_nw(scol + 16, y);
-            tmem_wait_ld();
-            tmem_pin8(x);
-            tmem_pin8(y);
-            scores(false);
-            over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
-            if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = d[0];
-            bar_group(group);
-            if (key < 8) {
-              const int at_row = (s0 + q) * 8 + key;
-              const float old = -row_nm[at_row];
-              const float z = fmaxf(fmaxf(gpart[key], gpart[8 + key]), fmaxf(gpart[16 + key], gpart[24 + key]));
-              const float m = z > old + kRaise ? z : old;
-              row_f[at_row] = tree_ex2(old - m);
-              row_nm[at_row] = -m;
-            }
-            bar_group(group);
-            float g[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              g[e] = row_f[(s0 + q) * 8 + e];
-              nm[e] = row_nm[(s0 + q) * 8 + e];
-              if (SMALL) ls[e] *= g[e];
-              else y[e] = __float_as_uint(__uint_as_float(y[e]) * g[e]);
-            }
-            if (i > i_first) {                   // (O as the tile before left it)
-              if (!TURNS) wait_values(n);
-              rescale(q, g, 1.f);
-            }
-            tmem_ld8_nw(scol, x);
-            if (SMALL) tmem_ld8_nw(scol + 16, y);
-            tmem_wait_ld();
-            tmem_pin8(x);
-            if (SMALL) tmem_pin8(y);
-            scores(true);
           }
-          // (the next chunk's products come in behind the exponentials)
-          if (!SMALL) tmem_ld8_nw(scol + (q + q_step < chunks ? q_step * 8 : 0), x);
-          uint32_t pk[4];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = tree_ex2(d[e]);
-          if (SMALL)
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 v = __fadd2_rn(make_float2(ls[e], ls[e + 1]), make_float2(d[e], d[e + 1]));
-              ls[e] = v.x;
-              ls[e + 1] = v.y;
-            }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = __fmul2_rn(make_float2(d[2 * e], d[2 * e + 1]), make_float2(pv, pv));
-            pk[e] = eight ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
-          }
-          if (seldom(edge)) {                    // (a scale that is none of the row's)
-            const uint32_t seen = seen_of(q);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-              pk[e / 2] &= ((seen >> e) & 1u ? 0x0000ffffu : 0u) | ((seen >> e) & 2u ? 0xffff0000u : 0u);
-          }
-          *reinterpret_cast<uint4*>(pto + (q >> 1) * kPanel + (((q & 1) ^ ((key >> 2) & 1)) << 4)) =
-              make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          if (!SMALL) {
-            tmem_wait_ld();
-            tmem_pin8(x);
-            tmem_pin8(y);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 v = __fadd2_rn(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
-                                          make_float2(d[e], d[e + 1]));
-              y[e] = __float_as_uint(v.x);
-              y[e + 1] = __float_as_uint(v.y);
-            }
-            tmem_st8(trow + col_l + q * 8, y);
-          }
-        }
+        };
+        if (SMALL || !seldom(!eight)) tile(std::true_type{});
+        else tile(std::false_type{});
         if (!SMALL) tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();
