@@ -39,12 +39,12 @@
 // 6.7 TB/s would be the floor):
 //   1 sequence x 1 token, 64 / 8 heads, 131000 rows       51 us   5.2 TB/s (floor 40)
 //   8 x 2 tokens, 40 / 40 heads, 4095 rows, window 2048   48 us   3.6 TB/s (floor 26)
-//   16 x 9 tokens, 64 / 8 heads, up to 16385 rows        134 us   2.4 TB/s (floor 48)
+//   16 x 9 tokens, 64 / 8 heads, up to 16385 rows        123 us   2.6 TB/s (floor 48)
 // One token is bound by the copies and by the CTAs that end last, many heads by the
 // start and the end of each pair (a few thousand cycles in which nothing streams),
-// 72 rows by the softmax: some 800 cycles for 8 rows of a tile in each of three warps of
-// a scheduler; the SM issues 2.1 instructions a cycle of four, and the matrix pipe
-// is busy for 16% of the time.
+// 72 rows by the softmax: some 700 cycles for 8 rows of a tile in each of three warps of
+// a scheduler, whose issue slots are half taken, and the matrix pipe is busy for
+// 18% of the time.
 //
 // The groups' warps come first, then four that widen V, one that copies K, one that
 // copies V, one for the products K q^T and one for V^T P.  Every wait is
@@ -507,7 +507,7 @@ static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan
 // More rows: three groups, or two where that leaves none with more than two chunks
 // (25 to 32 rows).  (16 sequences of 8192 rows, 24, 32 and 40 query rows: three groups
 // 68.7, 81.3 and 85.0 us, two 73.7, 77.9 and 89.2; 72 rows: three 134, two 149, four, of 80
-// registers a thread, 155)
+// registers a thread, 155; all before the loop for plain 8-bit tiles, below)
 constexpr int threads_of(int groups) { return (4 * groups + 8) * 32; }
 template <int DH, int kGroups, bool SMALL, bool TURNS>
 __global__ void __launch_bounds__(threads_of(kGroups), 1)
@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
       plan.ctas = ctas;
     }
     __syncwarp();
-    if (lane < 2) (lane ? plan.end : plan.begin) = tiles_before(a, plan, cta_start(plan.total, ctas, blockIdx.x + lane));
+    if (lane < 2)
+      (lane ? plan.end : plan.begin) = tiles_before(a, plan, cta_start(plan.total, ctas, blockIdx.x + lane));
     __syncwarp();
     if (plan.begin < plan.end && lane == 0) first_segment(a, plan, plan.begin, places[0]);
   }
@@ -661,9 +662,10 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         Walk t = place.w;
         if (!is_v)                               // q on its way, while the pair before is at work
 #pragma unroll 1
-          for (int i = lane; i < rows * P; i += 32)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + ((size_t)sb * a.T * a.H + (size_t)sh * a.G + row_at[i / P]) * DH +
-                                                         i % P * 64));
+          for (int i = lane; i < rows * P; i += 32) {
+            const bf16* at_q = a.q + ((size_t)sb * a.T * a.H + (size_t)sh * a.G + row_at[i / P]) * DH + i % P * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at_q));
+          }
 #pragma unroll 1
         for (int i = 0; ok && i < sn; ++i) {
 #pragma unroll 1
@@ -961,7 +963,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         const bf16* src = a.q + ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH + c * 8;
         auto fetch_q = [&](int row) {
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < live && key / kEach < 8 && !(TURNS && group)) x = *reinterpret_cast<const uint4*>(src + (size_t)row_at[row] * DH);
+          if (row < live && key / kEach < 8 && !(TURNS && group))
+            x = *reinterpret_cast<const uint4*>(src + (size_t)row_at[row] * DH);
           return x;
         };
         uint4 coming = fetch_q(q0 * 8 + key / kEach);
@@ -1088,10 +1091,13 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         if (!SMALL && lay.p_bufs == 1 && n > 0) wait_values(n);  // (its only one)
         float pv = vc * unit;
         unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
-        // (more than 16 rows: the loop once for each kind of tile, 72 rows 134.2 -> 130.9
-        // us; for few rows the longer code costs one token 0.6 us of 51.5)
-        auto tile = [&](auto kind) {
-          const bool in_eight = SMALL ? eight : decltype(kind)::value;
+        // More than 16 rows: the loop a second time for what nearly all tiles are, 8-bit rows
+        // that all tokens see, without the questions after the others.  (72 rows 134.2 ->
+        // 122.6 us; for few rows the longer code costs a window 12.1 -> 12.7 us and takes
+        // two tokens of 40 heads from 48.3 to 47.6)
+        auto tile = [&](auto plain) {
+          const bool in_eight = SMALL ? eight : decltype(plain)::value || eight;
+          const bool at_edge = SMALL ? edge : !decltype(plain)::value && edge;
           // the tokens that see the key, of chunk q's rows
           auto seen_of = [&](int q) {
             const int m0 = max(r0 - q * 8, 0), m1 = min(r1 - q * 8, 8);
@@ -1130,7 +1136,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
                 d[e] = v.x;
                 d[e + 1] = v.y;
               }
-              if (seldom(edge)) {
+              if (seldom(at_edge)) {
                 const uint32_t seen = seen_of(q);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -1215,7 +1221,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
               const float2 v = __fmul2_rn(make_float2(d[2 * e], d[2 * e + 1]), make_float2(pv, pv));
               pk[e] = in_eight ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
             }
-            if (seldom(edge)) {                    // (a scale that is none of the row's)
+            if (seldom(at_edge)) {                    // (a scale that is none of the row's)
               const uint32_t seen = seen_of(q);
 #pragma unroll
               for (int e = 0; e < 8; e += 2)
@@ -1238,7 +1244,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
             }
           }
         };
-        if (SMALL || !seldom(!eight)) tile(std::true_type{});
+        if (SMALL || !seldom(!eight || edge)) tile(std::true_type{});
         else tile(std::false_type{});
         if (!SMALL) tmem_wait_st();
         fence_proxy_async_smem();
@@ -1322,7 +1328,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
       }
       if (!TURNS || group == 0) {
         if (mine < chunks) {
-          row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * (!final ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f) : 0.f;
+          const float over_l = !final ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f;
+          row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * over_l : 0.f;
           if (!final && row < rows) {
             a.part_m[slot * rows + row] = m;
             a.part_l[slot * rows + row] = row < live ? l : 0.f;
@@ -1440,8 +1447,8 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap (&m)[4], cudaStream
     if (e != cudaSuccess) return e;
     if (dv >= 0) ready[dv] = true;
   }
-  const cudaError_t e = launch_early(cache_attn_tc_kernel<DH, GROUPS, SMALL, TURNS>, a.ctas, threads_of(GROUPS), lay.bytes, st, 0,
-                                     m[0], m[1], m[2], m[3], a, lay);
+  const cudaError_t e = launch_early(cache_attn_tc_kernel<DH, GROUPS, SMALL, TURNS>, a.ctas, threads_of(GROUPS),
+                                     lay.bytes, st, 0, m[0], m[1], m[2], m[3], a, lay);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.ctas, (a.T * a.G * (DH / 4) + kJoinThreads - 1) / kJoinThreads);
   // A pair of few rows that 16 CTAs or more share (if the sequences are alike, and
