@@ -43,8 +43,8 @@
 // One token is bound by the copies and by the CTAs that end last, many heads by the
 // start and the end of each pair (a few thousand cycles in which nothing streams),
 // 72 rows by the softmax: some 700 cycles for 8 rows of a tile in each of three warps of
-// a scheduler, whose issue slots are half taken, and the matrix pipe is busy for
-// 18% of the time.
+// a scheduler, whose issue slots are taken for 57% of the time, and the matrix pipe is
+// busy for 19%.
 //
 // The groups' warps come first, then four that widen V, one that copies K, one that
 // copies V, one for the products K q^T and one for V^T P.  Every wait is
