@@ -1064,7 +1064,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         // the rows that see the thread's key: [r0, r1); the warp's scale passes vref
         // (if any of its keys counts)
         int r0 = 0, r1 = NP;
-        bool over = eight && fabsf(vc) > vref && fabsf(vc) < 0x1p100f;
+        bool over = eight && fabsf(vc) > vref && fabsf(vc) < 0x1p124f;
         if (seldom(edge)) {
           const int j = t.p0 + key;
           r0 = max(j - s.r.length, 0) * a.G;
@@ -1152,7 +1152,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
                 bar_group(group);
                 const float most = fmaxf(fmaxf(gpart[0], gpart[1]), fmaxf(gpart[2], gpart[3]));
                 if (most > vref || vref == 0.f) {
-                  const float next = most > 0.f ? power_above(most) * 4.f : 1.f;
+                  // (2^7 / next: finite)
+                  const float next = most > 0.f ? fmaxf(power_above(most) * 4.f, 0x1p-119f) : 1.f;
                   if (i > i_first) {
                     if (!TURNS) wait_values(n);
 #pragma unroll 1

@@ -544,6 +544,26 @@ def test_scales_far_apart(ops):
     a.check(a.call(ops))
 
 
+@pytest.mark.parametrize("T,H", [(1, 2), (3, 4), (5, 8)])
+@pytest.mark.parametrize("e", [-115, -64, 64, 115, 119])
+def test_scales_near_the_ends_of_the_range(ops, T, H, e):
+    rng = np.random.default_rng(400 + e)
+    n, dh = 512 - T, 64
+    q = normal(rng, 1, T, H, dh).bfloat16().cuda()
+    k8, v8 = (normal(rng, 1, 1, 512, dh).cuda().to(torch.float8_e4m3fn) for _ in range(2))
+    ks = torch.ones(1, 1, 512 // 32, device="cuda")
+    vs = torch.from_numpy(2.0 ** rng.integers(e - 5, e + 1, (1, 1, 512 // 32))).float().cuda()
+    ring = torch.full((1, 1, 128, dh), NAN, device="cuda").bfloat16()
+    out = ops.cache_attention(q, ring, ring, whole([n]), k8=k8, v8=v8, k_scale=ks, v_scale=vs, held=whole([512]))
+    V = v8.double()[0, 0] * vs.double()[0, 0].repeat_interleave(32)[:, None]
+    for t in range(T):
+        p = torch.softmax(q[0, t].double() @ k8.double()[0, 0, :n + 1 + t].T / 8.0, -1)
+        want, spread = p @ V[:n + 1 + t], p @ V[:n + 1 + t].abs()
+        # the result's rounding, and the weights' to fp16 (2^-11; the sums' are far below)
+        off = (out[0, t].double() - want).abs() / (U * want.abs() + 2.0 ** -10 * spread)
+        assert off.max().item() <= 1, off.max().item()
+
+
 def test_senseless_sequences_are_nan_and_alone(ops):
     good = Attn([200, 150, 90], 2, 4, 2, 64, 128, [128, 96, 64])
     want = good.call(ops)
