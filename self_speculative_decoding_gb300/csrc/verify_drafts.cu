@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
   __shared__ double s_warp[kWarps];              // of those up to each
   __shared__ double s_before, s_total;           // of the CTAs below, of all
   __shared__ int s_owner;
+  __shared__ int s_pick;                         // of the search (late warps may still read the owner)
+  __shared__ double s_low;
   __shared__ double s_cta[2][kMaxCluster];       // each CTA's sum, from the CTAs themselves
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -225,13 +227,13 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
       const unsigned any = __ballot_sync(~0u, lane < kWarps && up > (lane ? lower : 0.0));
       const int w = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0;
       if (lane == w) {
-        s_owner = w;
-        s_before = below + (w ? lower : 0.0);
+        s_pick = w;
+        s_low = below + (w ? lower : 0.0);
       }
     }
     __syncthreads();
-    const int w = s_owner;
-    below = s_before;
+    const int w = s_pick;
+    below = s_low;
     x0 = min(x0 + w * part, x1);
     x1 = min(x0 + part, x1);
     if (x1 - x0 <= 128) break;
