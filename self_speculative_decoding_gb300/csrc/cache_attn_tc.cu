@@ -1261,7 +1261,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
       } else {
         wait_values(n);
       }
-      const bool bad = tree_flagged(odd), final = s.whole;
+      const bool final = s.whole;
       const size_t slot = (size_t)blockIdx.x * 2 + (s.head ? 0 : 1);
       const size_t out0 = ((size_t)s.b * a.T * a.H + (size_t)s.h * a.G) * DH;
       const int live = s.r.count * a.G;          // rows with a token
@@ -1328,6 +1328,9 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         }
       }
       if (!TURNS || group == 0) {
+        // (the segment's tiles are all behind: with TURNS the other group's since
+        // bar_both, as it waited for its own before that)
+        const bool bad = tree_flagged(odd);
         if (mine < chunks) {
           const float over_l = !final ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f;
           row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * over_l : 0.f;

@@ -52,3 +52,59 @@ def test_verify_drafts_says_the_same_every_time(ops, B, d, V, given):
         for a, b in zip(ops.verify_drafts(p, drafts, au, su, q=q), first):
             same &= (a == b).all()
     assert same.item()
+
+
+# --------------------------------------------------------------------------
+# attention: values that are not finite, which some tokens see
+
+
+def caches(g, B, Hkv, dh, rows, max_seq, block):
+    """Seeded bf16 rings and 8-bit caches with scales."""
+    k, v = (torch.randn(B, Hkv, rows, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k8, v8 = ((torch.randn(B, Hkv, max_seq, dh, generator=g, device="cuda") * 90).clamp_(-448, 448).to(torch.float8_e4m3fn)
+              for _ in range(2))
+    ks, vs = (torch.rand(B, Hkv, max_seq // block, generator=g, device="cuda") / 90 + 0.004 for _ in range(2))
+    return k, v, dict(k8=k8, v8=v8, k_scale=ks, v_scale=vs)
+
+
+@pytest.mark.parametrize("what", [NAN, float("inf"), float("-inf")])
+@pytest.mark.parametrize("T,G", [(2, 1), (3, 1), (4, 1), (2, 2), (4, 2), (3, 5)])
+@pytest.mark.parametrize("B,Hkv,n,held,window", [
+    (64, 8, 20, 0, 0),             # pairs of one tile, several of a CTA: either group's
+    (1, 2, 250, 0, 0),             # the drafted rows in the second tile of two
+    (2, 3, 509, 480, 0),           # in the fourth and fifth
+    (40, 5, 300, 288, 280),        # rows that leave the window as well
+])
+def test_values_that_some_tokens_see_reach_them(ops, B, Hkv, n, held, window, T, G, what):
+    dh, block = 64, 32
+    g = torch.Generator(device="cuda").manual_seed(T * 10 + G)
+    k, v, kw = caches(g, B, Hkv, dh, 512, 512, block)
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").bfloat16()
+    kw["held"] = whole([held] * B)
+
+    def run():
+        return ops.cache_attention(q, k, v, whole([n] * B), window=window, **kw)
+
+    clean = run()
+    assert torch.isfinite(clean).all()
+    rng = np.random.default_rng(T)
+    v_was, e, e_was = v.clone(), kw["v8"].view(torch.uint8), kw["v8"].view(torch.uint8).clone()
+    low = max(0, n + 1 - window) if window else 0
+    for share in (0.02, 0.3, 1.0):               # of the pairs
+        for row in [n + T - 1, n + 1] + ([low, low + T - 2] if window else []):
+            hit = torch.from_numpy(rng.random((B, Hkv)) < share).cuda()
+            v.copy_(v_was)
+            e.copy_(e_was)
+            if row >= held:
+                at = row % 512
+                v[:, :, at, 7] = torch.where(hit, torch.full_like(v[:, :, at, 7], what), v[:, :, at, 7])
+            else:
+                e[:, :, row, 7] = torch.where(hit, torch.full_like(e[:, :, row, 7], 0x7F), e[:, :, row, 7])
+            out = run()
+            pos = n + torch.arange(T, device="cuda")
+            sees = (row <= pos) & ((row > pos - window) if window else True)
+            lost = hit.repeat_interleave(G, 1)[:, None] & sees[None, :, None]        # [B, T, H]
+            assert not torch.isfinite(out[..., 7][lost]).any(), (share, row)
+            assert torch.equal(out[..., 7][~lost], clean[..., 7][~lost])
+            cols = [i for i in range(dh) if i != 7]
+            assert torch.equal(out[..., cols], clean[..., cols])
