@@ -681,7 +681,7 @@ ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int3
   const size_t one = (size_t)Hkv * rows * dh, cache = cache_span(B, seq_stride, one, 2);
   const size_t n4 = (size_t)4 * B, gain = (size_t)4 * dh;
   if (runs_overlap(k, v, B, seq_stride * 2, one * 2) || meets({{q_out, o}}, {{k, cache}, {v, cache}}) ||
-      meets({{q_out, o}, {k, cache}, {v, cache}}, {{qkv, in}, {lengths, n4}, {counts, n4}, {positions, tokens * 4},
+      meets({{q_out, o}, {k, cache}, {v, cache}}, {{qkv, in}, {lengths, n4}, {counts, n4}, {positions, n4},
                                                    {q_gain, gain}, {k_gain, gain}}))
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append: buffers overlap");
   RopeAppendArgs a;

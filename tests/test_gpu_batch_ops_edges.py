@@ -24,6 +24,43 @@ def whole(x):
 
 
 # --------------------------------------------------------------------------
+# buffers side by side
+
+
+@pytest.mark.parametrize("name", ["lengths", "counts", "positions", "q_gain", "k_gain", "qkv"])
+@pytest.mark.parametrize("next_to", ["out", "k", "v"])
+def test_rope_append_inputs_that_end_where_outputs_begin(ops, name, next_to):
+    B, T, H, Hkv, dh, rows = 4, 160, 2, 1, 64, 160
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def inputs():
+        g.manual_seed(3)
+        return dict(qkv=torch.randn(B, T, (H + 2 * Hkv) * dh, generator=g, device="cuda"), lengths=whole([3, 0, 200, 7]),
+                    k=torch.zeros(B, Hkv, rows, dh, device="cuda").bfloat16(),
+                    v=torch.zeros(B, Hkv, rows, dh, device="cuda").bfloat16(), counts=whole([160, 0, 5, 31]),
+                    positions=whole([9, 8, 7, 6]), q_gain=torch.rand(dh, generator=g, device="cuda") + 0.5,
+                    k_gain=torch.rand(dh, generator=g, device="cuda") + 0.5,
+                    out=torch.zeros(B, T, H, dh, device="cuda").bfloat16())
+
+    def call(a):
+        return ops.rope_append(a["qkv"], a["lengths"], a["k"], a["v"], H, Hkv, dh, 1e4, a["q_gain"], a["k_gain"],
+                               counts=a["counts"], positions=a["positions"], out=a["out"])
+
+    want, a = inputs(), inputs()
+    call(want)
+    # the two in one buffer, the output right behind the input
+    x, y = a[name], a[next_to]
+    nx, ny = x.numel() * x.element_size(), y.numel() * y.element_size()
+    assert nx % 16 == 0
+    buf = torch.zeros(nx + ny, dtype=torch.uint8, device="cuda")
+    a[name] = buf[:nx].view(x.dtype).view(x.shape).copy_(x)
+    a[next_to] = buf[nx:].view(y.dtype).view(y.shape).copy_(y)
+    call(a)
+    for k in want:
+        assert torch.equal(a[k], want[k]), k
+
+
+# --------------------------------------------------------------------------
 # verification
 
 
