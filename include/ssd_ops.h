@@ -327,10 +327,13 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * that; a query row with infinity or NaN gives NaN); probabilities are rounded to
  * bf16 for the product with bf16 rows of V, and, times the value's scale, to fp16
  * for the product with 8-bit rows (in units that keep 11 bits down to 2^-18 of
- * a row's largest weight, and steps of 2^-28 below).  Sums of values are divided in the
- * end: where 2^8 times the sum of a row's values leaves fp32's range, so may the
- * result.  Equal calls give equal bits, but a row's last bits depend on how the rows
- * of all sequences of the call are divided among the SMs. */
+ * a row's largest such weight, and steps of 2^-28 below; where the value scales that a
+ * sequence's tokens see lie further than 2^40 apart, or scores beyond 2^21, the steps are
+ * 2^-28 of the largest scale times the row's largest probability.  Value scales are below
+ * 2^124).  Sums of values are divided in the end: where 2^9 times the sum of a row's
+ * values leaves fp32's range, so may the result.  Equal calls give equal bits, but a
+ * row's last bits depend on how the rows of all sequences of the call are divided among
+ * the SMs. */
 size_t ssd_op_cache_attention_workspace(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh);
 ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int32_t* lengths,
                                   const int32_t* counts, const void* k, const void* v,

@@ -12,17 +12,20 @@
 //   O += V^T P              8-bit rows: V widened to fp16, P in fp16; bf16 rows: both bf16
 //
 // A thread has one key and all rows: scores up to m + 8 (a factor of 256, which the
-// sums and P carry) over the rows' maxima so far need no look at other threads but
-// one vote of four warps for 8 rows; where a score passes that, m is raised and O
-// rescaled.
+// sums and P carry; with a small scale so much more, which the sums do) need no look at
+// other threads but one vote of four warps for 8 rows; where a score passes that, m is
+// raised and O rescaled.
 //
 // K and q enter the matrix instructions as they are: a tile of K costs no thread
 // anything.  V cannot: P needs more than e4m3's range and bits (a first row that
 // takes most of the weight leaves the others small), and both operands of a
 // 16-bit product are 16 bits wide, so four warps widen V on its way.  fp16 has
 // less range than P: P is held in units of 2^-7 vref 2^m, vref a power of two not
-// below any value scale so far, which keeps 11 bits down to 2^-18 of a row's
-// largest weight and steps of 2^-28 below; two binades of room make it grow seldom.
+// below any value scale so far (two binades of room make it grow seldom), and m
+// follows the largest of score + log2(4 scale / vref) over the row's keys: 11 bits down to
+// 2^-18 of the row's largest weight (probability times scale) and steps of 2^-28 below,
+// while a sequence's scales lie within 2^40 of each other and scores below 2^21; beyond
+// that the steps are 2^-28 of the largest scale times the largest probability.
 //
 // Work: the tiles of all sequences and heads in one line, divided evenly among
 // the CTAs (one per SM); a pair of sequence and head that several CTAs share is
@@ -68,7 +71,7 @@ constexpr int kKeys = 128;
 constexpr int kWiden = 128;                      // threads that widen V
 constexpr int kPolls = 1 << 22;
 constexpr int kUnit = 16 * 1024;                 // 128 rows of up to 128 bytes, swizzled
-constexpr float kRaise = 8.f;
+constexpr int kRaise = 8;
 constexpr float kNone = -3.402823466e38f;        // the maximum of a row that has seen no key: no score is below
 
 // A condition that seldom holds: its code lies apart from the loop's.
@@ -438,10 +441,23 @@ SSD_DI uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// The smallest power of two that is not below |x| (x finite and not 0), 2^-126 at least.
+// The smallest power of two that is not below |x| (x finite and not 0), 2^-126 at least;
+// and its exponent, from 1 on (0 for 0).
 SSD_DI float power_above(float x) {
   return __uint_as_float((__float_as_uint(fabsf(x)) + 0x7fffffu) & 0x7f800000u);
 }
+SSD_DI int exponent_above(float x) { return (int)((__float_as_uint(fabsf(x)) + 0x7fffffu) >> 23) & 0xff; }
+// A row's maximum follows a value scale down to kBelow binades below vref / 4, and comes down
+// by kDown in all where vref grows.  With 8 of kRaise and 31 for a sum of rows these stay in
+// fp32's range.
+constexpr int kBelow = 42, kDown = 42;
+// kRaise for a tile: what its scores may pass a maximum by.  (log2(vref / scale) from the
+// numbers' bits, to 0.09.)
+SSD_DI float raise_of(bool eight, float scale, float vref) {
+  const float far = (float)((int)__float_as_uint(vref) - (int)__float_as_uint(fabsf(scale)));
+  return eight ? fminf(fmaf(far, 0x1p-23f, kRaise - 2), kBelow + kRaise) : kRaise;
+}
+constexpr float kFar = 0x1p22f;                  // from here on a maximum is the score alone: its steps are 1/2
 
 // How a row of V goes into the products: 0 as zeros (it is outside the tile's
 // run), 1 without what is not finite (0 x infinity is NaN, and some token of the
@@ -471,6 +487,17 @@ static __device__ __noinline__ float not_finite(const CacheAttnArgs& a, const Se
     }
   }
   return sum;
+}
+// Whether V rows j .. j + 31 of the pair, as far as they lie in [rs, re), hold zeros alone.
+SSD_DI bool rows_are_zero(const CacheAttnArgs& a, const Segment& s, int j, int rs, int re) {
+  j += threadIdx.x & 31;
+  uint32_t any = 0;
+  if (j >= rs && j < re) {
+    const uint4* row = reinterpret_cast<const uint4*>(a.v8 + (size_t)s.b * a.seq8_stride + ((size_t)s.h * a.max_seq + j) * a.dh);
+#pragma unroll 1
+    for (int i = 0; !any && i < a.dh / 16; ++i) any |= (row[i].x | row[i].y | row[i].z | row[i].w) & 0x7f7f7f7fu;
+  }
+  return !__any_sync(~0u, any);
 }
 // The CTA's rows as NaN: a wait gave up, and none is sure.
 static __device__ __noinline__ void mark_rows(const CacheAttnArgs& a, const Plan& plan, Place& place) {
@@ -940,14 +967,14 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
     const int q0 = TURNS ? 0 : group, q_step = TURNS ? 1 : kGroups;
     const int s0 = TURNS ? group : 0;            // where the rows' state lies: chunk s0 + q
     const uint32_t col_mine = col_o + (TURNS ? group * 16u : 0u);
-    // Columns of O of 8 rows times f, or all.
-    auto rescale = [&](int q, const float* f, float all) {
+    // Columns of O of 8 rows times f and all.
+    auto rescale = [&](int q, const float (&f)[8], float all) {
       uint32_t o[8];
       tmem_ld8_nw(trow + col_mine + q * 8, o);
       tmem_wait_ld();
       tmem_pin8(o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (f ? f[e] : all));
+      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (f[e] * all));
       tmem_st8(trow + col_mine + q * 8, o);
       tmem_wait_st();
     };
@@ -1015,7 +1042,9 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         if (lane == 0 && (!TURNS || group == 0)) mbar_arrive_cta(qready);
       }
       // ---- tiles
-      // O holds sums of 2^(score - m) v 2^7 / vref
+      // O holds sums of 2^(score - m) v 2^7 / vref.  m follows the largest score + log2(scale /
+      // (vref / 4)) of the row's keys, so that what P holds of a row's largest weight depends
+      // on no scale without weight.
       float vref = 0.f, unit = 0.f;              // (unit = 2^7 / vref)
       float c[8], nm[8], ls[8];                  // of the chunk; the sums of SMALL
       auto state = [&](int q) {
@@ -1060,7 +1089,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
       for (; i < sn; i += TURNS ? 2 : 1, n += TURNS ? 2 : 1) {
         const uint32_t buf = n & 1u;
         const bool eight = t.eight, edge = t.edge();
-        const float kc = ks, vc = eight ? vs : 1.f;
+        const float kc = ks;
+        float vc = eight ? vs : 1.f;
         // the rows that see the thread's key: [r0, r1); the warp's scale passes vref
         // (if any of its keys counts)
         int r0 = 0, r1 = NP;
@@ -1076,6 +1106,11 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
           if (j < t.rs || j >= t.re) r1 = 0;
           over = over && t.p0 + w4 * 32 < t.re && t.p0 + w4 * 32 + 32 > t.rs;
         }
+        // (a scale of 1 may be that of zeros, whose weight is none)
+        if (seldom(over && vc == 1.f) && rows_are_zero(a, s, t.p0 + w4 * 32, t.rs, t.re)) {
+          over = false;
+          vc = 0.f;
+        }
         if (i + (TURNS ? 2 : 1) < sn) {
           if (TURNS) step(t, place, a.window);
           step(t, place, a.window);
@@ -1090,6 +1125,10 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         tc_fence_after();
         if (!SMALL && lay.p_bufs == 1 && n > 0) wait_values(n);  // (its only one)
         float pv = vc * unit;
+        float most_over = raise_of(eight, vc, vref);
+        // vref's change: its inverse, what maxima come down by, so far (in the place of a chunk of
+        // the group's own, or of none)
+        float* grown = part + (group + (TURNS ? 4 : kGroups)) * 32;
         unsigned char* pto = psm + (lay.p_bufs == 2 ? buf * NP * 256 : 0) + key * 32;
         // More than 16 rows: the loop a second time for what nearly all tiles are, 8-bit rows
         // that all tokens see, without the questions after the others.  (72 rows 134.2 ->
@@ -1145,7 +1184,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
             };
             scores(true);
             const float top = tree_max3(tree_max3(d[0], d[1], d[2]), tree_max3(d[3], d[4], d[5]), fmaxf(d[6], d[7]));
-            if (seldom(any_group(group, top > kRaise || force))) {
+            if (seldom(any_group(group, top > most_over || force))) {
               if (q == q0) {
                 // the largest of the four warps' scales
                 if (lane == 0) gpart[w4] = over ? fabsf(vc) : 0.f;
@@ -1154,20 +1193,27 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
                 if (most > vref || vref == 0.f) {
                   // (2^7 / next: finite)
                   const float next = most > 0.f ? fmaxf(power_above(most) * 4.f, 0x1p-119f) : 1.f;
-                  if (i > i_first) {
-                    if (!TURNS) wait_values(n);
-#pragma unroll 1
-                    for (int z = q0; z < chunks; z += q_step) rescale(z, nullptr, vref / next);
+                  force = vref != 0.f;           // (then all chunks of this tile come through here)
+                  if (key == 0) {
+                    const float down = force ? grown[2] : 0.f;
+                    const float by = force ? (float)(exponent_above(next) - exponent_above(vref)) : 0.f;
+                    if (force) {
+                      grown[0] = vref / next;
+                      grown[1] = fminf(by, kDown - down);
+                    }
+                    grown[2] = fminf(down + by, kDown);
                   }
                   vref = next;
-                  unit = 0x1p7f / next;
+                  unit = __uint_as_float((261u << 23) - __float_as_uint(next));
                   pv = vc * unit;
+                  most_over = raise_of(eight, vc, vref);
+                } else {
+                  force = false;
                 }
-                over = false;
-                force = vref == 0.f;
                 bar_group(group);
               }
-              // the rows' largest scores of all keys; those that pass m + 8 become m
+              // the rows' largest scores of all keys, and what their scales lie below vref; those
+              // that pass m + 8 become m
               tmem_ld8_nw(scol, x);
               if (SMALL) tmem_ld8_nw(scol + 16, y);
               tmem_wait_ld();
@@ -1175,13 +1221,13 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
               tmem_pin8(y);
               scores(false);
               over_lanes(d, [](float u, float w) { return fmaxf(u, w); });
-              if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = d[0];
+              if (!(lane & 3)) gpart[w4 * 8 + (lane >> 2)] = fabsf(d[0]) < kFar ? d[0] + (kRaise - most_over) : d[0];
               bar_group(group);
               if (key < 8) {
                 const int at_row = (s0 + q) * 8 + key;
-                const float old = -row_nm[at_row];
+                const float old = -row_nm[at_row], low = force && fabsf(old) < kFar ? old - grown[1] : old;
                 const float z = fmaxf(fmaxf(gpart[key], gpart[8 + key]), fmaxf(gpart[16 + key], gpart[24 + key]));
-                const float m = z > old + kRaise ? z : old;
+                const float m = z > low + kRaise ? z : low;
                 row_f[at_row] = tree_ex2(old - m);
                 row_nm[at_row] = -m;
               }
@@ -1196,7 +1242,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
               }
               if (i > i_first) {                   // (O as the tile before left it)
                 if (!TURNS) wait_values(n);
-                rescale(q, g, 1.f);
+                rescale(q, g, force ? grown[0] : 1.f);
               }
               tmem_ld8_nw(scol, x);
               if (SMALL) tmem_ld8_nw(scol + 16, y);
@@ -1333,13 +1379,14 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         const bool bad = tree_flagged(odd);
         if (mine < chunks) {
           const float over_l = !final ? 1.f : l != 0.f ? __fdividef(1.f, l) : 0.f;
-          row_f[row] = row < live ? (TURNS ? 1.f : 0x1p-7f * vref) * over_l : 0.f;
+          row_f[row] = row < live ? over_l : 0.f;
           if (!final && row < rows) {
             a.part_m[slot * rows + row] = m;
             a.part_l[slot * rows + row] = row < live ? l : 0.f;
           }
         }
         bar_group(group);
+        const float out_unit = TURNS ? 1.f : 0x1p-7f * vref;  // (apart: times 1 / l it may be no normal number)
         if (DH == 128 || w4 < 2)
 #pragma unroll 1
           for (int q = q0; q < chunks; q += q_step) {
@@ -1349,7 +1396,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int row = q * 8 + e;
-              const float w = row < live ? __uint_as_float(o[e]) * row_f[row] : 0.f;
+              const float w = row < live ? __uint_as_float(o[e]) * row_f[row] * out_unit : 0.f;
               if (row < rows && final) out[row_at[row] * DH] = __float2bfloat16(w);
               if (row < rows && !final) po[e * DH] = w;
             }

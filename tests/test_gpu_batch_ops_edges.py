@@ -145,3 +145,197 @@ def test_values_that_some_tokens_see_reach_them(ops, B, Hkv, n, held, window, T,
             assert torch.equal(out[..., 7][~lost], clean[..., 7][~lost])
             cols = [i for i in range(dh) if i != 7]
             assert torch.equal(out[..., cols], clean[..., cols])
+
+
+# --------------------------------------------------------------------------
+# attention: value scales far apart
+
+
+def exact_rows(q, K, S, V8, length, scale, window=0):
+    """One sequence in 64 bits: q [T, H, dh], K [Hkv, n, dh] values, V = S[..., None] *
+    V8 -> the result, sum p |v|, and the largest p s of each row."""
+    T, H, dh = q.shape
+    Hkv, n = K.shape[:2]
+    x = q.double().view(T, Hkv, H // Hkv, dh).permute(1, 2, 0, 3)
+    s = scale * (x @ K[:, None].transpose(2, 3))
+    j, pos = torch.arange(n, device="cuda"), length + torch.arange(T, device="cuda")[:, None]
+    hidden = (j > pos) | ((j <= pos - window) if window else False)
+    p = torch.softmax(s.masked_fill(hidden, -float("inf")), -1)
+    back = lambda t: t.permute(2, 0, 1, 3).reshape(T, H, -1)  # noqa: E731
+    V = S[..., None] * V8
+    return back(p @ V[:, None]), back(p @ V.abs()[:, None]), back((p * S.abs()[:, None, None]).amax(-1, keepdim=True))
+
+
+def check_scales(ops, q, k8, v8, ks, vs, n, held, k, v, window=0, scale=None):
+    """The call against 64 bits.  Off by: the result's own rounding U |o|; each weight's
+    in fp16, 2^-11 of it, or (below 2^-18 of the largest) half a step of 2^-28 of the
+    largest; bf16 rows' weights U; scores 2^-16 with values of this size, a factor of
+    2^-15 on a probability and its sum."""
+    B, T, H, dh = q.shape
+    block = k8.shape[2] // ks.shape[2]
+    out = ops.cache_attention(q, k, v, whole([n] * B), k8=k8, v8=v8, k_scale=ks, v_scale=vs, held=whole([held] * B),
+                              window=window, scale=scale).double()
+    worst = 0.0
+    for b in range(B):
+        ring = torch.arange(held, n + T, device="cuda") % k.shape[2]
+        each = lambda s: s[b].double().repeat_interleave(block, 1)[:, :held]  # noqa: E731
+        K = torch.cat((k8[b, :, :held].double() * each(ks)[..., None], k[b, :, ring].double()), 1)
+        V8 = torch.cat((v8[b, :, :held].double(), v[b, :, ring].double()), 1)
+        S = torch.cat((each(vs), torch.ones_like(K[:, held:, 0])), 1)
+        ref, spread, most = exact_rows(q[b], K, S, V8, n, dh ** -0.5 if scale is None else scale, window)
+        tol = U * ref.abs() + (2.0 ** -11 + 2.0 ** -14 + (U if held < n + T else 0.0)) * spread + (
+            (n + T) * 2.0 ** -29 * most * V8.abs().amax())
+        off = (out[b] - ref).abs() / (tol + 1e-37)
+        worst = max(worst, off.max().item())
+    assert worst <= 1, worst
+
+
+ROWS = [(1, 1), (2, 2), (3, 4), (5, 3), (7, 4), (9, 8)]          # tokens, query heads a K/V head
+
+
+@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("heavy", ["first", "last", "middle"])
+@pytest.mark.parametrize("apart", [-38, -30, -12, 12, 30, 38])
+def test_weight_on_blocks_of_another_scale(ops, T, G, heavy, apart):
+    # all the weight lies in one block whose value scale is 2^apart of the others'
+    B, Hkv, dh, block, n = 3, 2, 64, 32, 1500
+    g = torch.Generator(device="cuda").manual_seed(abs(apart) + T)
+    held = (n + T) // block * block
+    k, v = (torch.randn(B, Hkv, 128, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k8 = torch.randn(B, Hkv, held, dh, generator=g, device="cuda").mul_(0.5)
+    v8 = torch.randn(B, Hkv, held, dh, generator=g, device="cuda").mul_(90).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    at = {"first": 0, "middle": held // block // 2, "last": held // block - 2}[heavy]
+    k8[..., 0] = -30.0                               # scores far below the block's
+    k8[:, :, at * block:(at + 1) * block, 0] = 30.0
+    k[..., 0] = -30.0
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda")
+    q[..., 0] = 8.0
+    ks = torch.ones(B, Hkv, held // block, device="cuda")
+    vs = torch.full((B, Hkv, held // block), 0.01, device="cuda")
+    vs[:, :, at] = 0.013 * 2.0 ** apart
+    v.mul_(1e-30)
+    check_scales(ops, q.bfloat16(), k8.to(torch.float8_e4m3fn), v8, ks, vs, n, held, k, v)
+
+
+@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("e", [3, 12, 19])
+@pytest.mark.parametrize("lengths", [40, 700, 5000])
+def test_scales_at_random(ops, T, G, e, lengths):
+    B, Hkv, dh, block = 2, 3, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(e + T)
+    held = lengths // block * block
+    max_seq = max(block, held)
+    k, v = (torch.randn(B, Hkv, 256, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k8, v8 = (torch.randn(B, Hkv, max_seq, dh, generator=g, device="cuda").mul_(a).clamp_(-448, 448).to(torch.float8_e4m3fn)
+              for a in (1.0, 90.0))
+    ks = torch.ones(B, Hkv, max_seq // block, device="cuda")
+    vs = torch.exp2(torch.randint(-e, e + 1, ks.shape, generator=g, device="cuda").float()) * (
+        1.0 + torch.rand(ks.shape, generator=g, device="cuda"))
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").mul_(2.0).bfloat16()
+    check_scales(ops, q, k8, v8, ks, vs, lengths, held, k, v)
+    if held:
+        check_scales(ops, q, k8, v8, ks, vs, held - T, held, k, v)
+
+
+@pytest.mark.parametrize("T,G", [(1, 2), (2, 8), (9, 8)])
+@pytest.mark.parametrize("large", ["first", "last"])
+def test_a_tail_of_small_weights_beside_a_large_scale(ops, T, G, large):
+    # a block of scale 1 without weight; the others 2^12 below, one key of which takes
+    # most, and the rest (12 below it) a tenth of that in all: none may be lost
+    n, dh, block = 20000, 64, 32
+    held = n + T + block - (n + T) % block
+    k8 = torch.zeros(1, 1, held, dh, device="cuda")
+    at = 0 if large == "first" else (n // block - 1)
+    k8[:, :, at * block:(at + 1) * block, 0] = -12.0
+    k8[:, :, 64, 0] = 12.0
+    v8 = torch.zeros_like(k8)
+    v8[..., 1] = 1.0
+    v8[:, :, 64, 1] = 0.0
+    v8[:, :, at * block:(at + 1) * block, 1] = 448.0
+    ks = torch.ones(1, 1, held // block, device="cuda")
+    vs = torch.full_like(ks, 2.0 ** -12)
+    vs[:, :, at] = 1.0
+    q = torch.zeros(1, T, G, dh, device="cuda").bfloat16()
+    q[..., 0] = 8.0
+    ring = torch.zeros(1, 1, 128, dh, device="cuda").bfloat16()
+    out = ops.cache_attention(q, ring, ring, whole([n]), k8=k8.to(torch.float8_e4m3fn), v8=v8.to(torch.float8_e4m3fn),
+                              k_scale=ks, v_scale=vs, held=whole([n]))
+    # (rows n .. are the ring's: scores and values of 0)
+    for t in range(T):
+        tail = n - 1 - block
+        total = 1 + (tail + t + 1) * np.exp(-12.0) + block * np.exp(-24.0)
+        want = 2.0 ** -12 * tail * np.exp(-12.0) / total + 448 * block * np.exp(-24.0) / total
+        off = (out[0, t, :, 1].double() - want).abs().max().item() / want
+        assert off <= 3 * U
+
+
+@pytest.mark.parametrize("T,G", [(1, 2), (2, 8), (3, 10), (9, 8)])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("at", [0, 3, 300])
+def test_a_block_of_zeros_takes_the_weight(ops, T, G, dh, at):
+    # zeros, whose scale is 1, take nearly all the weight; the rows beside them, whose
+    # scale is 2^-12, have e^-12 each, and are the result
+    n, block = 20000, 64
+    held = n + T + block - (n + T) % block
+    k8 = torch.zeros(1, 1, held, dh, device="cuda")
+    k8[:, :, at * block:(at + 1) * block, 0] = 12.0
+    v8 = torch.zeros_like(k8)
+    v8[..., 1] = 1.0
+    v8[:, :, at * block:(at + 1) * block] = 0.0
+    v8[:, :, at * block:(at + 1) * block, 5] = -0.0
+    ks = torch.ones(1, 1, held // block, device="cuda")
+    vs = torch.full_like(ks, 2.0 ** -12)
+    vs[:, :, at] = 1.0
+    q = torch.zeros(1, T, G, dh, device="cuda").bfloat16()
+    q[..., 0] = 8.0
+    ring = torch.zeros(1, 1, 128, dh, device="cuda").bfloat16()
+    out = ops.cache_attention(q, ring, ring, whole([n]), k8=k8.to(torch.float8_e4m3fn), v8=v8.to(torch.float8_e4m3fn),
+                              k_scale=ks, v_scale=vs, held=whole([n // block * block]), scale=0.125)
+    far = n // block * block                     # (rows from there on are the ring's: scores and values of 0)
+    for t in range(T):
+        tail = far - block
+        total = block + (n + t + 1 - block) * np.exp(-12.0)
+        want = 2.0 ** -12 * tail * np.exp(-12.0) / total
+        off = (out[0, t, :, 1].double() - want).abs().max().item() / want
+        assert off <= 3 * U and not out[0, t, :, 2:].any().item()
+
+
+@pytest.mark.parametrize("T,G", [(2, 1), (4, 2), (4, 4), (6, 5), (9, 8)])
+def test_a_large_scale_that_some_tokens_see(ops, T, G):
+    # a block of large scale leaves the window token by token
+    B, Hkv, dh, block, n, window = 2, 2, 64, 32, 1000, 601
+    g = torch.Generator(device="cuda").manual_seed(T)
+    held = 960
+    k, v = (torch.randn(B, Hkv, 256, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k8, v8 = (torch.randn(B, Hkv, held, dh, generator=g, device="cuda").mul_(a).clamp_(-448, 448).to(torch.float8_e4m3fn)
+              for a in (1.0, 90.0))
+    ks = torch.ones(B, Hkv, held // block, device="cuda")
+    vs = torch.full_like(ks, 0.01)
+    low = n + 1 - window                             # 400: the first token's first row
+    vs[:, :, low // block] = 2.0 ** 30
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").bfloat16()
+    v8.view(torch.uint8)[:, :, low + T:(low // block + 1) * block] = 0
+    check_scales(ops, q, k8, v8, ks, vs, n, held, k, v, window=window)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (2, 6), (3, 9), (4, 7), (5, 12)])
+@pytest.mark.parametrize("first", [2.0 ** -86, 2.0 ** -100, 2.0 ** -126])
+def test_means_of_many_rows_of_tiny_scales(ops, T, G, first):
+    # more pairs than SMs: each is one CTA's, and its sums are divided there
+    B, Hkv, dh, block, n = 20, 9, 64, 64, 4096     # (e^-128 2^40 is far below 2^-28)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k8 = torch.zeros(B, Hkv, n, dh, device="cuda").to(torch.float8_e4m3fn)
+    v8 = (torch.rand(B, Hkv, n, dh, generator=g, device="cuda") * 400 + 40).to(torch.float8_e4m3fn)
+    k8.view(torch.uint8)[:, :, :block] = 0xD8                    # -16 x 64: no weight
+    ks = torch.ones(B, Hkv, n // block, device="cuda")
+    vs = torch.full_like(ks, 2.0 ** -126)
+    vs[:, :, 0] = first
+    q = torch.ones(B, T, Hkv * G, dh, device="cuda").bfloat16()
+    ring = torch.full((B, Hkv, 128, dh), NAN, device="cuda").bfloat16()
+    out = ops.cache_attention(q, ring, ring, whole([n - T] * B), k8=k8, v8=v8, k_scale=ks, v_scale=vs,
+                              held=whole([n] * B)).double()
+    for t in range(T):
+        m = n - T + 1 + t
+        want = (v8[:, :, block:m].float().double().sum(2) / (m - block) * 2.0 ** -126).repeat_interleave(G, 1)
+        off = ((out[:, t] - want).abs() / want).max().item()
+        assert off <= U + 2.0 ** -10
