@@ -457,6 +457,7 @@ SSD_DI float raise_of(bool eight, float scale, float vref) {
   const float far = (float)((int)__float_as_uint(vref) - (int)__float_as_uint(fabsf(scale)));
   return eight ? fminf(fmaf(far, 0x1p-23f, kRaise - 2), kBelow + kRaise) : kRaise;
 }
+constexpr float kTiny = 0x1p-24f;
 constexpr float kFar = 0x1p22f;                  // from here on a maximum is the score alone: its steps are 1/2
 
 // How a row of V goes into the products: 0 as zeros (it is outside the tile's
@@ -1094,7 +1095,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         // the rows that see the thread's key: [r0, r1); the warp's scale passes vref
         // (if any of its keys counts)
         int r0 = 0, r1 = NP;
-        bool over = eight && fabsf(vc) > vref && fabsf(vc) < 0x1p124f;
+        // (bf16 rows: a unit far below their values' would take P and O out of fp32's range)
+        bool over = eight ? fabsf(vc) > vref && fabsf(vc) < 0x1p124f : vref < kTiny && vref != 0.f;
         if (seldom(edge)) {
           const int j = t.p0 + key;
           r0 = max(j - s.r.length, 0) * a.G;
@@ -1107,7 +1109,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
           over = over && t.p0 + w4 * 32 < t.re && t.p0 + w4 * 32 + 32 > t.rs;
         }
         // (a scale of 1 may be that of zeros, whose weight is none)
-        if (seldom(over && vc == 1.f) && rows_are_zero(a, s, t.p0 + w4 * 32, t.rs, t.re)) {
+        if (seldom(over && eight && vc == 1.f) && rows_are_zero(a, s, t.p0 + w4 * 32, t.rs, t.re)) {
           over = false;
           vc = 0.f;
         }
@@ -1191,8 +1193,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
                 bar_group(group);
                 const float most = fmaxf(fmaxf(gpart[0], gpart[1]), fmaxf(gpart[2], gpart[3]));
                 if (most > vref || vref == 0.f) {
-                  // (2^7 / next: finite)
-                  const float next = most > 0.f ? fmaxf(power_above(most) * 4.f, 0x1p-119f) : 1.f;
+                  // (2^7 / next: finite; 1 for bf16 rows alone)
+                  const float next = most > 0.f ? fmaxf(power_above(most) * 4.f, 0x1p-119f) : eight ? 1.f : 0x1p7f;
                   force = vref != 0.f;           // (then all chunks of this tile come through here)
                   if (key == 0) {
                     const float down = force ? grown[2] : 0.f;

@@ -339,3 +339,36 @@ def test_means_of_many_rows_of_tiny_scales(ops, T, G, first):
         want = (v8[:, :, block:m].float().double().sum(2) / (m - block) * 2.0 ** -126).repeat_interleave(G, 1)
         off = ((out[:, t] - want).abs() / want).max().item()
         assert off <= U + 2.0 ** -10
+
+
+@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("e", [-126, -115, -90, -60, -40, -25, -20])
+@pytest.mark.parametrize("n", [150, 900, 9000])
+def test_bf16_rows_behind_tiny_scales(ops, T, G, e, n):
+    B, Hkv, dh, block = 2, 2, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(T - e)
+    held = (n - 70) // block * block
+    k, v = (torch.randn(B, Hkv, 256, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k8, v8 = (torch.randn(B, Hkv, held, dh, generator=g, device="cuda").mul_(a).clamp_(-448, 448).to(torch.float8_e4m3fn)
+              for a in (1.0, 90.0))
+    ks = torch.ones(B, Hkv, held // block, device="cuda")
+    vs = torch.full_like(ks, 2.0 ** e)
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").bfloat16()
+    check_scales(ops, q, k8, v8, ks, vs, n, held, k, v)
+    # and larger ones than usual; and as tiny as the others
+    check_scales(ops, q, k8, v8, ks, vs, n, held, k, v * 2.0 ** 40)
+    v = v * 2.0 ** max(e + 6, -100)
+    check_scales(ops, q, k8, v8, ks, vs, n, held, k, v)
+
+
+@pytest.mark.parametrize("T,G", ROWS)
+def test_large_values_of_bf16_rows_alone(ops, T, G):
+    # 2^9 times their sum is below 2^127
+    B, Hkv, dh, n = 2, 2, 64, 1000
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(B, Hkv, 1024, dh, generator=g, device="cuda") for _ in range(2))
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").bfloat16()
+    k, v = k.bfloat16(), v.bfloat16()
+    want = ops.cache_attention(q, k, v, whole([n] * B))
+    out = ops.cache_attention(q, k, v * 2.0 ** 105, whole([n] * B))
+    assert torch.equal(out, want * 2.0 ** 105)
