@@ -175,8 +175,7 @@ def check_scales(ops, q, k8, v8, ks, vs, n, held, k, v, window=0, scale=None):
     block = k8.shape[2] // ks.shape[2]
     out = ops.cache_attention(q, k, v, whole([n] * B), k8=k8, v8=v8, k_scale=ks, v_scale=vs, held=whole([held] * B),
                               window=window, scale=scale).double()
-    worst = 0.0
-    for b in range(B):
+    for b in range(0, B, max(1, B // 5)):
         ring = torch.arange(held, n + T, device="cuda") % k.shape[2]
         each = lambda s: s[b].double().repeat_interleave(block, 1)[:, :held]  # noqa: E731
         K = torch.cat((k8[b, :, :held].double() * each(ks)[..., None], k[b, :, ring].double()), 1)
@@ -186,19 +185,20 @@ def check_scales(ops, q, k8, v8, ks, vs, n, held, k, v, window=0, scale=None):
         tol = U * ref.abs() + (2.0 ** -11 + 2.0 ** -14 + (U if held < n + T else 0.0)) * spread + (
             (n + T) * 2.0 ** -29 * most * V8.abs().amax())
         off = (out[b] - ref).abs() / (tol + 1e-37)
-        worst = max(worst, off.max().item())
-    assert worst <= 1, worst
+        assert (off <= 1).all().item(), (b, off.max().item())
 
 
 ROWS = [(1, 1), (2, 2), (3, 4), (5, 3), (7, 4), (9, 8)]          # tokens, query heads a K/V head
+PAIRS = [(3, 2), (40, 5)]              # sequences, heads: a CTA for each tile or so; all of a pair's tiles in one
 
 
+@pytest.mark.parametrize("B,Hkv", PAIRS)
 @pytest.mark.parametrize("T,G", ROWS)
 @pytest.mark.parametrize("heavy", ["first", "last", "middle"])
 @pytest.mark.parametrize("apart", [-38, -30, -12, 12, 30, 38])
-def test_weight_on_blocks_of_another_scale(ops, T, G, heavy, apart):
+def test_weight_on_blocks_of_another_scale(ops, B, Hkv, T, G, heavy, apart):
     # all the weight lies in one block whose value scale is 2^apart of the others'
-    B, Hkv, dh, block, n = 3, 2, 64, 32, 1500
+    dh, block, n = 64, 32, 1500
     g = torch.Generator(device="cuda").manual_seed(abs(apart) + T)
     held = (n + T) // block * block
     k, v = (torch.randn(B, Hkv, 128, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
@@ -217,11 +217,12 @@ def test_weight_on_blocks_of_another_scale(ops, T, G, heavy, apart):
     check_scales(ops, q.bfloat16(), k8.to(torch.float8_e4m3fn), v8, ks, vs, n, held, k, v)
 
 
+@pytest.mark.parametrize("B,Hkv", PAIRS)
 @pytest.mark.parametrize("T,G", ROWS)
 @pytest.mark.parametrize("e", [3, 12, 19])
 @pytest.mark.parametrize("lengths", [40, 700, 5000])
-def test_scales_at_random(ops, T, G, e, lengths):
-    B, Hkv, dh, block = 2, 3, 128, 64
+def test_scales_at_random(ops, B, Hkv, T, G, e, lengths):
+    dh, block = 128, 64
     g = torch.Generator(device="cuda").manual_seed(e + T)
     held = lengths // block * block
     max_seq = max(block, held)
@@ -300,10 +301,11 @@ def test_a_block_of_zeros_takes_the_weight(ops, T, G, dh, at):
         assert off <= 3 * U and not out[0, t, :, 2:].any().item()
 
 
+@pytest.mark.parametrize("B,Hkv", PAIRS)
 @pytest.mark.parametrize("T,G", [(2, 1), (4, 2), (4, 4), (6, 5), (9, 8)])
-def test_a_large_scale_that_some_tokens_see(ops, T, G):
+def test_a_large_scale_that_some_tokens_see(ops, B, Hkv, T, G):
     # a block of large scale leaves the window token by token
-    B, Hkv, dh, block, n, window = 2, 2, 64, 32, 1000, 601
+    dh, block, n, window = 64, 32, 1000, 601
     g = torch.Generator(device="cuda").manual_seed(T)
     held = 960
     k, v = (torch.randn(B, Hkv, 256, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
@@ -341,11 +343,12 @@ def test_means_of_many_rows_of_tiny_scales(ops, T, G, first):
         assert off <= U + 2.0 ** -10
 
 
+@pytest.mark.parametrize("B,Hkv", PAIRS)
 @pytest.mark.parametrize("T,G", ROWS)
 @pytest.mark.parametrize("e", [-126, -115, -90, -60, -40, -25, -20])
-@pytest.mark.parametrize("n", [150, 900, 9000])
-def test_bf16_rows_behind_tiny_scales(ops, T, G, e, n):
-    B, Hkv, dh, block = 2, 2, 64, 64
+@pytest.mark.parametrize("n", [150, 900])
+def test_bf16_rows_behind_tiny_scales(ops, B, Hkv, T, G, e, n):
+    dh, block = 64, 64
     g = torch.Generator(device="cuda").manual_seed(T - e)
     held = (n - 70) // block * block
     k, v = (torch.randn(B, Hkv, 256, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
