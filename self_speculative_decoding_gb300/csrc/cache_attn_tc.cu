@@ -1334,6 +1334,9 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         const float* p4 = part + (s0 + mine) * 32 + (key & 7);
         m = -row_nm[s0 * 8 + row];
         l = (p4[0] + p4[8]) + (p4[16] + p4[24]);
+        // a query that is not finite (bf16 rows do not see row_c, and an infinite element may
+        // make all their scores -infinity)
+        if (row < rows && isnan(row_c[row])) l = NAN;
       }
       uint32_t o[8];
       auto fetch_o = [&](int q) {

@@ -375,3 +375,29 @@ def test_large_values_of_bf16_rows_alone(ops, T, G):
     want = ops.cache_attention(q, k, v, whole([n] * B))
     out = ops.cache_attention(q, k, v * 2.0 ** 105, whole([n] * B))
     assert torch.equal(out, want * 2.0 ** 105)
+
+
+# --------------------------------------------------------------------------
+# queries that are not finite
+
+
+@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("n,held", [(0, None), (5, None), (900, None), (900, 0), (900, 832)])
+def test_queries_that_are_not_finite_are_nan(ops, T, G, n, held):
+    B, Hkv, dh, block = 40, 5, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(T + n)
+    k, v, kw = caches(g, B, Hkv, dh, 1024, 1024, block)
+    kw = {} if held is None else dict(kw, held=whole([held] * B))
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").bfloat16()
+    clean = ops.cache_attention(q, k, v, whole([n] * B), **kw)
+    rng = np.random.default_rng(T + n)
+    for what in (float("inf"), float("-inf"), NAN):
+        hit = torch.from_numpy(rng.random((B, T, Hkv * G)) < 0.3).cuda()
+        bad = q.clone()
+        bad[..., 11] = torch.where(hit, torch.full_like(q[..., 11], what), q[..., 11])
+        for scale in (0.125, -0.125):
+            out = ops.cache_attention(bad, k, v, whole([n] * B), scale=scale, **kw)
+            assert torch.isnan(out[hit]).all()
+            assert torch.isfinite(out[~hit]).all()
+            if scale > 0:
+                assert torch.equal(out[~hit], clean[~hit])
