@@ -359,7 +359,7 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
  * the last v with r_v > 0.  Entries that are negative or NaN count as 0.
  * tokens int32 [B][d + 1] = the accepted drafts, the drawn token, then -1;
  * n int32 [B] = the number of them (no drawn token where p_j has no entry over 0,
- * or an infinite one).  d >= 0 (0: one draw from p; q, drafts and accept_u are not
+ * or where the entries drawn from sum to more than fp32 holds).  d >= 0 (0: one draw from p; q, drafts and accept_u are not
  * read), d <= 1024, 1 <= V <= 2^30; 4-byte alignment. */
 ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* drafts,
                                 const int32_t* counts, const float* accept_u,

@@ -10,6 +10,8 @@
 // lies that near to a border.
 #include <cooperative_groups.h>
 
+#include <cfloat>
+
 #include "batch.cuh"
 #include "tree.cuh"
 
@@ -36,10 +38,12 @@ SSD_DI void rest_of(float p, float q, float& r, float& e) {
 }
 
 // u q < p without rounding: the product's rounding error decides where the rounded
-// product is p (scaled, so that the error of a small product is a normal number).
+// product is p (u and p scaled, so that the error of a small product is a normal number; a
+// product that overflows is above any p).  In 64 bits it took 0.6 us more.
 SSD_DI bool less(float u, float q, float p) {
-  q *= 0x1p64f;
-  p *= 0x1p64f;
+  const float up = p < 0x1p60f ? 0x1p64f : 1.f;
+  u *= up;
+  p *= up;
   const float h = __fmul_rn(u, q), l = __fmaf_rn(u, q, -h);
   return h < p || (h == p && l < 0.f);
 }
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
       if (lane == 0) {
         s_before = rank ? below : 0.0;
         s_total = all;
-        s_owner = !(all < INFINITY) ? -1 : past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
+        s_owner = !(all <= (double)FLT_MAX) ? -1 : past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
       }
     }
     __syncthreads();

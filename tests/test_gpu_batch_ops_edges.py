@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import batch as O
+
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -8                          # half a bf16 step, relative to the value
@@ -89,6 +91,31 @@ def test_verify_drafts_says_the_same_every_time(ops, B, d, V, given):
         for a, b in zip(ops.verify_drafts(p, drafts, au, su, q=q), first):
             same &= (a == b).all()
     assert same.item()
+
+
+@pytest.mark.parametrize("e", [-149, -130, -100, 0, 70, 100, 118])
+def test_verify_drafts_of_weights_of_any_size(ops, e):
+    # weights that sum to anything: what is accepted and drawn depends on their ratios; with
+    # e = 118 every row sums to more than fp32 holds, and nothing is drawn
+    B, d, V = 64, 3, 50
+    rng = np.random.default_rng(e + 200)
+    scale = 2.0 ** e
+    p = np.ldexp(rng.integers(1, 1 << 9, (B, d + 1, V)).astype(np.float32), e)
+    q = np.ldexp(rng.integers(1, 1 << 9, (B, d, V)).astype(np.float32), e)
+    drafts = rng.integers(0, V, (B, d))
+    au, su = rng.random((B, d)).astype(np.float32), rng.random(B).astype(np.float32)
+    # ties: u q = p exactly, and one step below
+    for b in range(0, B, 4):
+        q[b, 0], p[b, 0] = np.float32(scale * 256), np.float32(scale * 128)
+        au[b, 0] = 0.5 if b % 8 else np.nextafter(np.float32(0.5), np.float32(0))
+    on = lambda x, t: torch.from_numpy(np.ascontiguousarray(x)).to(t).cuda()  # noqa: E731
+    tokens, n = ops.verify_drafts(on(p, torch.float32), on(drafts, torch.int32), on(au, torch.float32),
+                                  on(su, torch.float32), q=on(q, torch.float32))
+    for b in range(B):
+        want = O.verify(p[b].astype(np.float64), q[b].astype(np.float64), drafts[b], au[b].astype(np.float64), float(su[b]))
+        want = want[:-1] if e == 118 else want
+        assert tokens[b].tolist() == want + [-1] * (d + 1 - len(want)), b
+        assert n[b].item() == len(want)
 
 
 # --------------------------------------------------------------------------
