@@ -355,7 +355,7 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
  * is not, one token is drawn from max(p_j - q_j, 0) (q NULL: p_j without y), or
  * from p_j where nothing is left; after the last, from p_counts: the lowest v with
  *   sum_{w <= v} r_w > sample_u sum r     (r: the entries drawn from)
- * the sums good to 2^-40; where rounding or a sample_u of 1 or more leaves none,
+ * the sums good to 2^-41 + V 2^-58 of the whole; where rounding or a sample_u of 1 or more leaves none,
  * the last v with r_v > 0.  Entries that are negative or NaN count as 0.
  * tokens int32 [B][d + 1] = the accepted drafts, the drawn token, then -1;
  * n int32 [B] = the number of them (no drawn token where p_j has no entry over 0,

@@ -1,6 +1,8 @@
 """The calls of several sequences on the GPU, at the edges of what they promise:
 equal calls, values that are not finite, scales far apart, the ends of fp32."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -116,6 +118,49 @@ def test_verify_drafts_of_weights_of_any_size(ops, e):
         want = want[:-1] if e == 118 else want
         assert tokens[b].tolist() == want + [-1] * (d + 1 - len(want)), b
         assert n[b].item() == len(want)
+
+
+def stubborn_entries(n, seed):
+    """n fp32 entries whose sum in order, with the rounding errors added up in
+    fp32, is off by some 2^-35 always to the same side."""
+    f, rng = np.float32, np.random.default_rng(seed)
+    some = (f(2.0 ** -20) * (1 + rng.integers(0, 1 << 23, 512) / f(1 << 23))).astype(f)
+    s, c, entries = f(1), f(0), [f(1)]
+    for _ in range(n - 1):
+        t = (s + some).astype(f)
+        part = (t - s).astype(f)
+        err = ((s - (t - part).astype(f)).astype(f) + (some - part).astype(f)).astype(f)
+        now = (c + err).astype(f)
+        k = int(np.argmax(now.astype(np.float64) - (np.float64(c) + err.astype(np.float64))))
+        entries.append(some[k])
+        s, c = t[k], now[k]
+    return np.array(entries, f), float(s) + float(c)
+
+
+@pytest.mark.parametrize("B", [1, 512])
+def test_verify_drafts_sums_many_entries(ops, B):
+    # a border as near to U sum p as 2^-36 of it: one CTA's 16 runs of 8000 entries, a
+    # lane's every 32nd; the runs of the second half sum to 256 times `lane`
+    V, n = 128000, 250
+    lane, by_fp32 = stubborn_entries(n, 5)
+    half = [Fraction(float(x)) for x in lane]
+    true = 256 * sum(half)
+    off = 256 * (Fraction(by_fp32) - sum(half))
+    assert abs(off) > 2.0 ** -36 * true
+    p = np.zeros(V, np.float32)
+    p[V // 2:] = np.repeat(lane, 32)[None].repeat(8, 0).reshape(-1)
+    # the first half: the same sum and half of what fp32 is off by, in a few entries
+    left, at = true + off / 2, 0
+    while left > true * Fraction(1, 2 ** 44):
+        p[at] = np.float32(np.nextafter(np.float32(left), np.float32(0)))
+        left -= Fraction(float(p[at]))
+        at += 1
+    first = sum(Fraction(float(x)) for x in p[:at])
+    want = at - 1 if first > (first + true) / 2 else V // 2
+    tokens, count = ops.verify_drafts(torch.from_numpy(p).cuda().expand(B, 1, V).contiguous(),
+                                      torch.zeros(B, 0, dtype=torch.int32, device="cuda"), torch.zeros(B, 0, device="cuda"),
+                                      torch.full((B,), 0.5, device="cuda"))
+    assert (count == 1).all().item() and (tokens == want).all().item(), (tokens[0].item(), want)
 
 
 # --------------------------------------------------------------------------
