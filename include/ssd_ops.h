@@ -313,7 +313,7 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * Rows j < held[b] are read from k8, v8, the others from k, v (held, k8, v8,
  * k_scale and v_scale NULL together: all from k, v; max_seq, block and the strides
  * then mean nothing).  q bf16 [B][T][H][dh]; query head h reads K/V head
- * h / (H / Hkv); 1 <= T, T H / Hkv <= 128.  counts as for ssd_op_rope_append but
+ * h / (H / Hkv); 1 <= T, T H / Hkv <= 128; |scale| <= 2^127.  counts as for ssd_op_rope_append but
  * not clamped; rows of out behind a sequence's tokens are zeros.  A row that
  * sees keys of score -infinity alone is zeros.  Rows that a token does not see
  * take no part in it, whatever they hold; of the rings only rows that some token

@@ -787,7 +787,8 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
   } else if (k8 || v8 || k_scale || v_scale) {
     return op_fail(SSD_ERR_INVALID_ARG, "cache_attention: 8-bit caches need held");
   }
-  if (window < 0 || sinks < 0 || !std::isfinite(scale))
+  const float scale_log2 = (float)(1.4426950408889634 * std::fabs((double)scale));
+  if (window < 0 || sinks < 0 || !std::isfinite(scale_log2))
     return op_fail(SSD_ERR_INVALID_ARG, "cache_attention: window / sinks / scale");
   if (!al16(q) || !al16(out) || !al4(lengths) || (counts && !al4(counts)) || (held && !al4(held)) || !workspace ||
       ((uintptr_t)workspace & 255u))
@@ -829,7 +830,7 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
   }
   a.window = window;
   a.sinks = sinks;
-  a.scale_log2 = (float)(1.4426950408889634 * std::fabs((double)scale));
+  a.scale_log2 = scale_log2;
   a.negate = scale < 0.f;
   a.out = (bf16*)out;
   a.give_up = t_cache_give_up;
