@@ -114,15 +114,6 @@ __host__ __device__ inline Layout layout_of(int rows, int dh, int B) {
   return l;
 }
 
-// Four columns of the thread's lane, waited for.
-SSD_DI void tmem_ld4(uint32_t taddr, float (&r)[4]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-      : "r"(taddr)
-      : "memory");
-}
 SSD_DI void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
