@@ -473,3 +473,115 @@ def test_queries_that_are_not_finite_are_nan(ops, T, G, n, held):
             assert torch.isfinite(out[~hit]).all()
             if scale > 0:
                 assert torch.equal(out[~hit], clean[~hit])
+
+
+# --------------------------------------------------------------------------
+# attention at random: odd lengths, any number of 8-bit rows, windows, rings, counts
+
+
+def seen_mask(length, T, n, window, sinks):
+    j, pos = torch.arange(n, device="cuda"), length + torch.arange(T, device="cuda")[:, None]
+    seen = j <= pos
+    return seen & ((j < sinks) | (j > pos - window)) if window else seen
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_attention_at_random(ops, seed):
+    rng = np.random.default_rng(1000 + seed)
+    pick = lambda *x: x[rng.integers(len(x))]  # noqa: E731
+    dh, block = int(pick(64, 128)), int(pick(32, 64, 128))
+    G = int(pick(1, 1, 2, 3, 4, 5, 8, 16))
+    T = int(rng.integers(1, max(2, min(17, 128 // G + 1))))
+    Hkv, B = int(pick(1, 2, 3, 5)), int(pick(1, 2, 3, 7, 40, 90))
+    most = int(pick(3, 60, 300, 1500, 4000))
+    lengths = rng.integers(0, most + 1, B)
+    counts = rng.integers(0, T + 1, B) if seed % 3 else np.full(B, T)
+    window = int(pick(0, 0, 1, 17, 130, 1000))
+    sinks = int(rng.integers(0, 300)) if window and seed % 2 else int(pick(0, 3))
+    ends = lengths + counts
+    tail = rng.integers(0, 200, B)
+    held = np.maximum(ends - tail, 0) if seed % 4 else np.maximum(lengths - tail, 0) // block * block
+    # a ring that holds what is in bf16, or rows for the longest
+    need = int(np.maximum(ends - held, 1).max())
+    rows = -(-need // 128) * 128 if seed % 2 else max(int(ends.max()), 1)
+    max_seq = -(-max(int(held.max()), 1) // block) * block
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    std = float(pick(0.5, 1.5, 4.0))
+    q = (torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda") * std).bfloat16()
+    k, v, kw = caches(g, B, Hkv, dh, rows, max_seq, block)
+    out = ops.cache_attention(q, k, v, whole(lengths.tolist()), held=whole(held.tolist()), counts=whole(counts.tolist()),
+                              window=window, sinks=sinks, **kw)
+    again = ops.cache_attention(q, k, v, whole(lengths.tolist()), held=whole(held.tolist()), counts=whole(counts.tolist()),
+                                window=window, sinks=sinks, **kw)
+    assert torch.equal(out, again)
+    out = out.double()
+    for b in range(0, B, max(1, B // 7)):
+        n, c, h = int(lengths[b]), int(counts[b]), int(held[b])
+        assert not out[b, c:].any().item()
+        if not c:
+            continue
+        at = torch.arange(h, n + c, device="cuda") % rows
+        each = lambda s: s[b].double().repeat_interleave(block, 1)[:, :h, None]  # noqa: E731
+        K, V = (torch.cat((kw[x + "8"][b, :, :h].double() * each(kw[x + "_scale"]), r[b, :, at].double()), 1)
+                for x, r in (("k", k), ("v", v)))
+        x = q[b, :c].double().view(c, Hkv, G, dh).permute(1, 2, 0, 3)
+        s = dh ** -0.5 * (x @ K[:, None].transpose(2, 3))
+        p = torch.softmax(s.masked_fill(~seen_mask(n, c, n + c, window, sinks), -float("inf")), -1)
+        back = lambda t: t.permute(2, 0, 1, 3).reshape(c, Hkv * G, dh)  # noqa: E731
+        ref, spread = back(p @ V[:, None]), back(p @ V[:, None].abs())
+        # (as the tolerance of check_scales: U for a bf16 row's weight; a score's error, doubled)
+        d = dh ** -0.5 * (2.0 ** -17 * x.abs().amax() * K.abs().sum(-1).amax() +
+                          2 * dh * 2.0 ** -24 * (x.abs() @ K[:, None].abs().transpose(2, 3)).amax()) + 1e-6
+        off = (out[b, :c] - ref).abs() / (U * ref.abs() + (U + 2 * d) * spread)
+        assert (off <= 1).all().item(), (b, off.max().item())
+
+
+def test_no_tokens_at_all(ops):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v, kw = caches(g, 5, 2, 64, 128, 256, 64)
+    q = torch.randn(5, 3, 8, 64, generator=g, device="cuda").bfloat16()
+    kw["held"] = whole([0, 64, 128, 0, 256])
+    out = ops.cache_attention(q, k, v, whole([0, 64, 130, 7, 256]), counts=whole([0] * 5), **kw)
+    assert not out.any().item()
+    out = ops.rope_append(torch.randn(5, 3, 12 * 64, generator=g, device="cuda"), whole([0] * 5), k, v, 8, 2, 64, 1e4,
+                          counts=whole([0] * 5))
+    assert not out.any().item()
+
+
+def test_calls_captured_from_streams_that_meet(ops):
+    # rotation on one stream, verification on another, behind a copy and a fill; the
+    # attention where the two meet
+    B, T, H, Hkv, dh, V = 2, 3, 8, 2, 64, 500
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v, kw = caches(g, B, Hkv, dh, 256, 256, 64)
+    kw["held"] = whole([64, 128])
+    qkv = torch.randn(B, T, (H + 2 * Hkv) * dh, generator=g, device="cuda")
+    p = torch.softmax(torch.randn(B, T + 1, V, generator=g, device="cuda"), -1)
+    drafts, au, su = whole([[1, 2, 3], [4, 5, 6]]), torch.zeros(B, T, device="cuda"), torch.rand(B, generator=g, device="cuda")
+    lengths, n_in, x_in = whole([100, 140]), whole([100, 140]), qkv.clone()
+
+    def calls(other):
+        main = torch.cuda.current_stream()
+        lengths.copy_(n_in)
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            qkv.copy_(x_in)
+            q = ops.rope_append(qkv, lengths, k, v, H, Hkv, dh, 1e4)
+        tokens, n = ops.verify_drafts(p, drafts, au, su)
+        main.wait_stream(other)
+        out = ops.cache_attention(q, k, v, lengths, **kw)
+        new = ops.cache_quantize(k, v, kw["held"], lengths + n, kw["k8"].clone(), kw["v8"].clone(), kw["k_scale"].clone(),
+                                 kw["v_scale"].clone())
+        q.record_stream(main)
+        return q, tokens, n, out, new
+
+    other = torch.cuda.Stream()
+    want = [x.clone() for x in calls(other)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(other)
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
