@@ -330,8 +330,8 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * a row's largest such weight, and steps of 2^-28 below; where the value scales that a
  * sequence's tokens see lie further than 2^40 apart, or scores beyond 2^21, the steps are
  * 2^-28 of the largest scale times the row's largest probability.  Value scales are below
- * 2^124).  Sums of values are divided in the end: where 2^9 times the sum of a row's
- * values (2^40 times that of its bf16 values, beside 8-bit rows) leaves fp32's range, so
+ * 2^124).  Sums of values are divided in the end: where 2^11 times the sum of a row's
+ * values (2^41 times that of its bf16 values, beside 8-bit rows) leaves fp32's range, so
  * may the result.  Equal calls give equal bits, but a
  * row's last bits depend on how the rows of all sequences of the call are divided among
  * the SMs. */

@@ -438,7 +438,7 @@ def test_bf16_rows_behind_tiny_scales(ops, B, Hkv, T, G, e, n):
 
 @pytest.mark.parametrize("T,G", ROWS)
 def test_large_values_of_bf16_rows_alone(ops, T, G):
-    # 2^9 times their sum is below 2^127
+    # 2^11 times their sum is below 2^127
     B, Hkv, dh, n = 2, 2, 64, 1000
     g = torch.Generator(device="cuda").manual_seed(T)
     k, v = (torch.randn(B, Hkv, 1024, dh, generator=g, device="cuda") for _ in range(2))
