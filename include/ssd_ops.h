@@ -356,7 +356,8 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
  * from p_j where nothing is left; after the last, from p_counts: the lowest v with
  *   sum_{w <= v} r_w > sample_u sum r     (r: the entries drawn from)
  * the sums good to 2^-41 + V 2^-58 of the whole; where rounding or a sample_u of 1 or more leaves none,
- * the last v with r_v > 0.  Entries that are negative or NaN count as 0.
+ * the last v with r_v > 0.  Entries that are negative or NaN count as 0, and so does such a
+ * sample_u.
  * tokens int32 [B][d + 1] = the accepted drafts, the drawn token, then -1;
  * n int32 [B] = the number of them (no drawn token where p_j has no entry over 0,
  * or where the entries drawn from sum to more than fp32 holds).  d >= 0 (0: one draw from p; q, drafts and accept_u are not

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
   pdl_wait();
   pdl_trigger();
   const int count = a.counts ? min(max(a.counts[b], 0), a.d) : a.d;
-  const float sample = a.sample_u[b];
+  const float sample = fmaxf(a.sample_u[b], 0.f);  // (NaN too: with it no sum would pass)
   // the drafts in order, 32 at a time (by each warp for itself)
   int taken = count;
 #pragma unroll 1

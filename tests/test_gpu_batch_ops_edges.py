@@ -120,6 +120,19 @@ def test_verify_drafts_of_weights_of_any_size(ops, e):
         assert n[b].item() == len(want)
 
 
+@pytest.mark.parametrize("V", [40, 3000, 40000])
+@pytest.mark.parametrize("u", [-1e-30, -0.5, -0.0, float("-inf"), NAN])
+def test_verify_drafts_below_the_range(ops, V, u):
+    # as 0: the first entry over 0, wherever it lies
+    p = torch.zeros(6, 1, V, device="cuda")
+    at = [0, 1, V // 3, V // 2, V - 2, V - 1]
+    for b, v in enumerate(at):
+        p[b, 0, v:] = torch.rand(V - v, device="cuda") + 0.1
+    tokens, n = ops.verify_drafts(p, torch.zeros(6, 0, dtype=torch.int32, device="cuda"), torch.zeros(6, 0, device="cuda"),
+                                  torch.full((6,), u, device="cuda"))
+    assert tokens[:, 0].tolist() == at and n.tolist() == [1] * 6
+
+
 def stubborn_entries(n, seed):
     """n fp32 entries whose sum in order, with the rounding errors added up in
     fp32, is off by some 2^-35 always to the same side."""
