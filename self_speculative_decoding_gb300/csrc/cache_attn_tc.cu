@@ -1401,6 +1401,7 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
               for (int e = 0; e < min(8, live - q * 8); ++e) {
                 const int row = q * 8 + e;
                 const float w = not_finite(a, s, s.r.length + row / a.G, key);
+                if (w == 0.f) continue;          // (-0 stays: whether the flag is set here may be another pair's doing)
                 if (final) out[row_at[row] * DH] = __float2bfloat16(__bfloat162float(out[row_at[row] * DH]) + w);
                 else po[e * DH] += w;
               }

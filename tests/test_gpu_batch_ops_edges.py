@@ -65,6 +65,26 @@ def test_rope_append_inputs_that_end_where_outputs_begin(ops, name, next_to):
 
 
 # --------------------------------------------------------------------------
+# rotation
+
+
+@pytest.mark.parametrize("H,Hkv,dh", [(40, 4, 128), (7, 3, 64)])
+@pytest.mark.parametrize("norms", [False, True])
+def test_rope_append_of_many_tokens_gives_each_token_alone(ops, H, Hkv, dh, norms):
+    # calls of few and of many tokens go by different grains
+    B, T = 3, 400
+    g = torch.Generator(device="cuda").manual_seed(dh)
+    qkv = torch.randn(B, T, (H + 2 * Hkv) * dh, generator=g, device="cuda")
+    gains = [torch.rand(dh, generator=g, device="cuda") + 0.5 for _ in range(2)] if norms else [None, None]
+    k, v, k1, v1 = (torch.zeros(B, Hkv, 1000, dh, device="cuda").bfloat16() for _ in range(4))
+    start = whole([0, 131, 600])
+    q = ops.rope_append(qkv, start, k, v, H, Hkv, dh, 1e4, *gains)
+    lone = [ops.rope_append(qkv[:, t:t + 1].contiguous(), start + t, k1, v1, H, Hkv, dh, 1e4, *gains) for t in range(T)]
+    assert torch.equal(torch.cat(lone, 1).view(torch.int16), q.view(torch.int16))
+    assert torch.equal(k1, k) and torch.equal(v1, v)
+
+
+# --------------------------------------------------------------------------
 # verification
 
 
@@ -231,6 +251,23 @@ def test_values_that_some_tokens_see_reach_them(ops, B, Hkv, n, held, window, T,
             cols = [i for i in range(dh) if i != 7]
             assert torch.equal(out[..., cols], clean[..., cols])
 
+
+@pytest.mark.parametrize("T,G", [(2, 1), (3, 4), (3, 9), (9, 8)])
+@pytest.mark.parametrize("B", [1, 90])
+def test_a_zero_keeps_its_sign_beside_them(ops, B, T, G):
+    # results that round to -0 stay -0 where other columns hold NaN
+    Hkv, dh, n = 2, 64, 300
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(B, Hkv, 384, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    v[..., 5] = -2.0 ** -133
+    v[:, :, :n - 1, 5] = 0.0
+    q = torch.randn(B, T, Hkv * G, dh, generator=g, device="cuda").bfloat16()
+    clean = ops.cache_attention(q, k, v, whole([n] * B))
+    v[:, :, n + T - 1, 7] = NAN                      # the last token's own
+    out = ops.cache_attention(q, k, v, whole([n] * B))
+    cols = [i for i in range(dh) if i != 7]
+    assert torch.equal(out[..., cols].view(torch.int16), clean[..., cols].view(torch.int16))
+    assert (clean[..., 5].view(torch.int16) == -32768).any().item()
 
 # --------------------------------------------------------------------------
 # attention: value scales far apart
