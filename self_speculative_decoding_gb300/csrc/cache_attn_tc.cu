@@ -1004,6 +1004,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (a.negate) w[k] ^= 0x80008000u;
+              // (a query that is not finite: NaN, as an infinite element may make all scores -infinity)
+              if (most >= 0x7f80u) w[k] = 0x7fff7fffu;
               const float2 f = make_float2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
               const uint32_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
               const __half2 b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
@@ -1325,9 +1327,6 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
         const float* p4 = part + (s0 + mine) * 32 + (key & 7);
         m = -row_nm[s0 * 8 + row];
         l = (p4[0] + p4[8]) + (p4[16] + p4[24]);
-        // a query that is not finite (bf16 rows do not see row_c, and an infinite element may
-        // make all their scores -infinity)
-        if (row < rows && isnan(row_c[row])) l = NAN;
       }
       uint32_t o[8];
       auto fetch_o = [&](int q) {
