@@ -268,9 +268,9 @@ ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* pare
  * Strides are in elements and at least what one sequence takes (so that a layer
  * of [B][layers][Hkv][rows][dh] can be given); seq_stride a multiple of 8,
  * seq8_stride of 16.  dh is 64 or 128, block 32, 64 or 128, max_seq a
- * multiple of block.  k and v of different sequences may alternate in memory, and
- * a call that only reads a pair of caches may be given one for both; buffers
- * overlap in no other way. */
+ * multiple of block.  The caches of different sequences may alternate in memory
+ * (all of one sequence behind one another, say), and a call that only reads a pair
+ * of caches may be given one for both; buffers overlap in no other way. */
 
 /* Norms of the query and key heads, rotation and append: token t < counts[b]
  * (counts NULL: T for all; clamped to 0..T) of sequence b goes to row

@@ -131,25 +131,27 @@ void tree_frequencies(float theta, int dh, double* out) {
   std::memcpy(out, table, sizeof(double) * (dh / 2));
 }
 
-// Whether what a call writes meets what it reads (NULL: not given).
+// What a call reads or writes: `runs` runs of n bytes, `stride` bytes apart (NULL: not given).
 struct Bytes {
   const void* at;
-  size_t n;
+  size_t n, runs = 1, stride = 0;
 };
+bool meet(const Bytes& a, const Bytes& b) {
+  if (!a.at || !b.at || !overlap(a.at, (a.runs - 1) * a.stride + a.n, b.at, (b.runs - 1) * b.stride + b.n)) return false;
+  const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+  for (size_t i = 0, j = 0; i < a.runs && j < b.runs;) {  // (the runs of each are in order)
+    if (x + i * a.stride + a.n <= y + j * b.stride) ++i;
+    else if (y + j * b.stride + b.n <= x + i * a.stride) ++j;
+    else return true;
+  }
+  return false;
+}
+// Whether what it writes meets what it reads.
 bool meets(std::initializer_list<Bytes> written, std::initializer_list<Bytes> read) {
   for (const Bytes& w : written)
     for (const Bytes& r : read)
-      if (w.at && r.at && overlap(w.at, w.n, r.at, r.n)) return true;
+      if (meet(w, r)) return true;
   return false;
-}
-
-// Whether two sets of n runs of `span` bytes, `stride` bytes apart, meet.
-bool runs_overlap(const void* a, const void* b, size_t n, size_t stride, size_t span) {
-  const size_t all = (n - 1) * stride + span;
-  if (!overlap(a, all, b, all)) return false;
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  const size_t d = (x < y ? y - x : x - y) % stride;
-  return d < span || stride - d < span;
 }
 
 // The caches of a call of many sequences: sizes, strides, pointers.
@@ -179,9 +181,9 @@ ssd_status check_eight(const char* call, const void* k8, const void* v8, const f
   return SSD_OK;
 }
 
-// Bytes from a cache's first element to the end of its last.
-size_t cache_span(int32_t B, size_t stride, size_t one, size_t element) {
-  return ((size_t)(B - 1) * stride + one) * element;
+// A cache of B sequences: `one` elements of each, `stride` elements apart.
+Bytes cache_bytes(const void* at, int32_t B, size_t stride, size_t one, size_t element) {
+  return {at, one * element, (size_t)B, stride * element};
 }
 
 ssd_status check_cache_attention(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh) {
@@ -678,11 +680,11 @@ ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int3
       (q_gain && !al16(q_gain)) || (k_gain && !al16(k_gain)))
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append pointers");
   const size_t tokens = (size_t)B * T, in = tokens * ((size_t)H + 2 * Hkv) * dh * 4, o = tokens * H * dh * 2;
-  const size_t one = (size_t)Hkv * rows * dh, cache = cache_span(B, seq_stride, one, 2);
-  const size_t n4 = (size_t)4 * B, gain = (size_t)4 * dh;
-  if (runs_overlap(k, v, B, seq_stride * 2, one * 2) || meets({{q_out, o}}, {{k, cache}, {v, cache}}) ||
-      meets({{q_out, o}, {k, cache}, {v, cache}}, {{qkv, in}, {lengths, n4}, {counts, n4}, {positions, n4},
-                                                   {q_gain, gain}, {k_gain, gain}}))
+  const size_t one = (size_t)Hkv * rows * dh, n4 = (size_t)4 * B, gain = (size_t)4 * dh;
+  const Bytes kb = cache_bytes(k, B, seq_stride, one, 2), vb = cache_bytes(v, B, seq_stride, one, 2);
+  if (meet(kb, vb) || meets({{q_out, o}}, {kb, vb}) ||
+      meets({{q_out, o}, kb, vb},
+            {{qkv, in}, {lengths, n4}, {counts, n4}, {positions, n4}, {q_gain, gain}, {k_gain, gain}}))
     return op_fail(SSD_ERR_INVALID_ARG, "rope_append: buffers overlap");
   RopeAppendArgs a;
   a.qkv = qkv;
@@ -723,15 +725,15 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
   if (r != SSD_OK) return r;
   if (!al4(held) || !al4(lengths) || !al4(held_out))
     return op_fail(SSD_ERR_INVALID_ARG, "cache_quantize pointers");
-  const size_t in = cache_span(B, seq_stride, (size_t)Hkv * rows * dh, 2);
-  const size_t one = (size_t)Hkv * max_seq * dh, scales = (size_t)4 * Hkv * (max_seq / block);
-  const size_t o = cache_span(B, seq8_stride, one, 1), n = (size_t)4 * B;
-  const size_t all_scales = cache_span(B, scale_stride, (size_t)Hkv * (max_seq / block), 4);
-  if (runs_overlap(k8, v8, B, seq8_stride, one) || runs_overlap(k_scale, v_scale, B, scale_stride * 4, scales) ||
-      meets({{k8, o}, {v8, o}, {k_scale, all_scales}, {v_scale, all_scales}, {held_out, n}},
-            {{k, in}, {v, in}, {held, n}, {lengths, n}}) ||
-      meets({{k8, o}, {v8, o}}, {{k_scale, all_scales}, {v_scale, all_scales}, {held_out, n}}) ||
-      meets({{held_out, n}}, {{k_scale, all_scales}, {v_scale, all_scales}}))
+  const size_t one = (size_t)Hkv * rows * dh, n = (size_t)4 * B;
+  const size_t one8 = (size_t)Hkv * max_seq * dh, scales = (size_t)Hkv * (max_seq / block);
+  const Bytes kb = cache_bytes(k, B, seq_stride, one, 2), vb = cache_bytes(v, B, seq_stride, one, 2);
+  const Bytes k8b = cache_bytes(k8, B, seq8_stride, one8, 1), v8b = cache_bytes(v8, B, seq8_stride, one8, 1);
+  const Bytes ksb = cache_bytes(k_scale, B, scale_stride, scales, 4);
+  const Bytes vsb = cache_bytes(v_scale, B, scale_stride, scales, 4);
+  if (meet(k8b, v8b) || meet(ksb, vsb) ||
+      meets({k8b, v8b, ksb, vsb, {held_out, n}}, {kb, vb, {held, n}, {lengths, n}}) ||
+      meets({k8b, v8b}, {ksb, vsb, {held_out, n}}) || meets({{held_out, n}}, {ksb, vsb}))
     return op_fail(SSD_ERR_INVALID_ARG, "cache_quantize: buffers overlap");
   QuantizeArgs a;
   a.k = (const bf16*)k;
@@ -803,11 +805,13 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
   const size_t need = cache_attn_workspace(a, workspace);
   if (need > workspace_bytes) return op_fail(SSD_ERR_CAPACITY, "cache_attention: workspace too small");
   const size_t o = (size_t)B * T * H * dh * 2, n4 = (size_t)4 * B;
-  const size_t in = cache_span(B, seq_stride, (size_t)Hkv * rows * dh, 2);
-  const size_t in8 = eight ? cache_span(B, seq8_stride, (size_t)Hkv * max_seq * dh, 1) : 0;
-  const size_t scales = eight ? cache_span(B, scale_stride, (size_t)Hkv * (max_seq / block), 4) : 0;
-  if (meets({{out, o}, {workspace, need}}, {{q, o}, {k, in}, {v, in}, {k8, in8}, {v8, in8}, {k_scale, scales},
-                                            {v_scale, scales}, {lengths, n4}, {counts, n4}, {held, n4}}) ||
+  const size_t one = (size_t)Hkv * rows * dh, one8 = (size_t)Hkv * max_seq * dh;
+  const size_t scales = eight ? (size_t)Hkv * (max_seq / block) : 0;
+  if (meets({{out, o}, {workspace, need}},
+            {{q, o}, cache_bytes(k, B, seq_stride, one, 2), cache_bytes(v, B, seq_stride, one, 2),
+             cache_bytes(k8, B, seq8_stride, one8, 1), cache_bytes(v8, B, seq8_stride, one8, 1),
+             cache_bytes(k_scale, B, scale_stride, scales, 4), cache_bytes(v_scale, B, scale_stride, scales, 4),
+             {lengths, n4}, {counts, n4}, {held, n4}}) ||
       meets({{out, o}}, {{workspace, need}}))
     return op_fail(SSD_ERR_INVALID_ARG, "cache_attention: buffers overlap");
   a.q = (const bf16*)q;

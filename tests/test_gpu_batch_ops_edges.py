@@ -64,6 +64,34 @@ def test_rope_append_inputs_that_end_where_outputs_begin(ops, name, next_to):
         assert torch.equal(a[k], want[k]), k
 
 
+def test_all_caches_of_a_sequence_in_one_piece(ops):
+    # k, v, their 8-bit rows and scales of each sequence one behind the other
+    B, T, H, Hkv, dh, rows, max_seq, block = 3, 90, 6, 2, 64, 128, 256, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    qkv = torch.randn(B, T, (H + 2 * Hkv) * dh, generator=g, device="cuda")
+    parts = [("k", torch.bfloat16, (Hkv, rows, dh)), ("v", torch.bfloat16, (Hkv, rows, dh)),
+             ("k8", torch.float8_e4m3fn, (Hkv, max_seq, dh)), ("v8", torch.float8_e4m3fn, (Hkv, max_seq, dh)),
+             ("ks", torch.float32, (Hkv, max_seq // block)), ("vs", torch.float32, (Hkv, max_seq // block))]
+    sizes = [torch.empty(0, dtype=t).element_size() * int(np.prod(shape)) for _, t, shape in parts]
+    piece = torch.zeros(B, sum(sizes), dtype=torch.uint8, device="cuda")
+    one = {n: x.view(t).view(B, *shape) for (n, t, shape), x in zip(parts, piece.split(sizes, 1))}
+    apart = {n: torch.zeros(B, *shape, device="cuda").to(t) for n, t, shape in parts}
+
+    def run(c):
+        start = whole([0, 7, 30])
+        q = ops.rope_append(qkv, start, c["k"], c["v"], H, Hkv, dh, 1e4)
+        held = ops.cache_quantize(c["k"], c["v"], whole([0, 0, 0]), start + T, c["k8"], c["v8"], c["ks"], c["vs"])
+        out = ops.cache_attention(q[:, -3:].contiguous(), c["k"], c["v"], start + T - 3, c["k8"], c["v8"], c["ks"], c["vs"], held)
+        return q, held, out, *(x.contiguous().view(torch.uint8) for x in c.values())
+
+    for x, y in zip(run(one), run(apart)):
+        assert torch.equal(x, y)
+    # in each other's way they are refused
+    bad = dict(one, k8=piece[:, 16:16 + sizes[2]].view(torch.float8_e4m3fn).view(B, Hkv, max_seq, dh))
+    with pytest.raises((ValueError, RuntimeError)):
+        ops.cache_quantize(bad["k"], bad["v"], whole([0, 0, 0]), whole([90] * 3), bad["k8"], bad["v8"], bad["ks"], bad["vs"])
+
+
 # --------------------------------------------------------------------------
 # rotation
 
