@@ -18,8 +18,9 @@
  *
  * Every kernel's reduction order is fixed by the element's own position and
  * never depends on M or on the other rows: row m of a call with M rows is
- * bit-identical to the same row computed alone.  ssd_op_tree_attention and
- * ssd_op_cache_attention are the exceptions (see there).
+ * bit-identical to the same row computed alone.  ssd_op_tree_attention,
+ * ssd_op_cache_attention and, where a draw lies as near to a border as its sums
+ * are good, ssd_op_verify_drafts are the exceptions (see there).
  */
 #ifndef SSD_OPS_H_
 #define SSD_OPS_H_
@@ -278,11 +279,13 @@ ssd_status ssd_op_beam_reorder(const void* k, const void* v, const int32_t* pare
  * qkv fp32 [B][T][(H + 2 Hkv) dh] holds the raw projections (q, k, v).  Heads of
  * q become x / sqrt(mean(x^2) + eps) * q_gain (fp32 [dh]; NULL: stay as they
  * are), heads of k the same with k_gain; both are then turned by rotate-half RoPE
- * (base theta), the angle exact for every position; bf16(q) goes to q_out
+ * (base theta), the angle good to 2^-22 of a half turn at every position (theta
+ * of 1 or more); the squares are summed in fp32.  bf16(q) goes to q_out
  * (bf16 [B][T][H][dh]), bf16(k) and bf16(v) to their rows.  A token that a
  * sequence does not have (t >= counts[b], or lengths[b] below 0 or beyond
  * 2^31 - 1 - T) has zeros in q_out and no row.  Other rows stay as they are.
- * 1 <= T <= rows; B T (H + 2 Hkv) dh <= 2^38.  A token's results do not depend on the other tokens. */
+ * 1 <= T <= rows; B T (H + 2 Hkv) dh <= 2^38.  A token's results do not depend on the
+ * other tokens. */
 ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int32_t* lengths,
                               const int32_t* counts, const int32_t* positions,
                               const float* q_gain, const float* k_gain, float eps, float theta,
@@ -295,7 +298,9 @@ ssd_status ssd_op_rope_append(const float* qkv, int32_t B, int32_t T, const int3
  * most 448; elements are rounded to nearest, ties to even.  Infinities and NaN
  * become NaN and do not enter the scale.  held_out[b] = held[b] + the rows moved
  * (held_out may not be held).  lengths is what is to stay: rows of drafts that
- * may yet be rejected are not in it.  A sequence whose numbers make no sense
+ * may yet be rejected are not in it, but a ring needs rows for them too (a draft
+ * appended `rows` rows behind held[b], or further, has taken the place of a row that
+ * is still to be moved, which lengths does not tell).  A sequence whose numbers make no sense
  * (held[b] negative, no multiple of block or beyond max_seq, lengths[b] beyond
  * max_seq), or of whose rows the ring has lost one (lengths[b] - held[b] > rows),
  * stays as it is. */
@@ -313,11 +318,11 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * Rows j < held[b] are read from k8, v8, the others from k, v (held, k8, v8,
  * k_scale and v_scale NULL together: all from k, v; max_seq, block and the strides
  * then mean nothing).  q bf16 [B][T][H][dh]; query head h reads K/V head
- * h / (H / Hkv); 1 <= T, T H / Hkv <= 128; |scale| <= 2^127.  counts as for ssd_op_rope_append but
- * not clamped; rows of out behind a sequence's tokens are zeros.  A row that
- * sees keys of score -infinity alone is zeros.  Rows that a token does not see
- * take no part in it, whatever they hold; of the rings only rows that some token
- * of the sequence sees are needed.  A sequence whose numbers make no sense
+ * h / (H / Hkv); 1 <= T, T H / Hkv <= 128; |scale| <= 2^127.  counts as for
+ * ssd_op_rope_append but not clamped; rows of out behind a sequence's tokens are
+ * zeros.  A row that sees keys of score -infinity alone is zeros.  Rows that a token
+ * does not see take no part in it, whatever they hold; of the rings only rows that
+ * some token of the sequence sees are needed.  A sequence whose numbers make no sense
  * (lengths[b] negative or beyond 2^31 - 257 - T, counts[b] outside 0..T, held[b]
  * outside 0..max_seq or beyond lengths[b] + counts[b]), or of whose rows the
  * ring no longer holds one that is needed, gives NaN in all of its rows of out;
@@ -326,15 +331,15 @@ ssd_status ssd_op_cache_quantize(const void* k, const void* v, int32_t rows, siz
  * fp32 (elements of q below 2^-9 of their row's largest are good to 2^-17 of
  * that; a query row with infinity or NaN gives NaN); probabilities are rounded to
  * bf16 for the product with bf16 rows of V, and, times the value's scale, to fp16
- * for the product with 8-bit rows (in units that keep 11 bits down to 2^-18 of
- * a row's largest such weight, and steps of 2^-28 below; where the value scales that a
- * sequence's tokens see lie further than 2^40 apart, or scores beyond 2^21, the steps are
- * 2^-28 of the largest scale times the row's largest probability.  Value scales are below
- * 2^124).  Sums of values are divided in the end: where 2^11 times the sum of a row's
- * values (2^41 times that of its bf16 values, beside 8-bit rows) leaves fp32's range, so
- * may the result.  Equal calls give equal bits, but a
- * row's last bits depend on how the rows of all sequences of the call are divided among
- * the SMs. */
+ * for the product with 8-bit rows, in units that keep 11 bits down to 2^-18 of a
+ * row's largest such weight (one of zeros under a scale of 1, as ssd_op_cache_quantize
+ * writes them, is none) and steps of 2^-28 of it below.  Where the value scales that a
+ * sequence's tokens see lie further than 2^40 apart, or scores beyond 2^21, the steps
+ * are 2^-28 of the largest scale times the row's largest probability.  Value scales
+ * are below 2^124.  Sums of values are divided in the end: where 2^11 times the sum of
+ * a row's values (2^41 times that of its bf16 values, beside 8-bit rows) leaves fp32's
+ * range, so may the result.  Equal calls give equal bits, but a row's last bits depend
+ * on how the rows of all sequences of the call are divided among the SMs. */
 size_t ssd_op_cache_attention_workspace(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dh);
 ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int32_t* lengths,
                                   const int32_t* counts, const void* k, const void* v,
@@ -355,13 +360,14 @@ ssd_status ssd_op_cache_attention(const void* q, int32_t B, int32_t T, const int
  * is not, one token is drawn from max(p_j - q_j, 0) (q NULL: p_j without y), or
  * from p_j where nothing is left; after the last, from p_counts: the lowest v with
  *   sum_{w <= v} r_w > sample_u sum r     (r: the entries drawn from)
- * the sums good to 2^-41 + V 2^-58 of the whole; where rounding or a sample_u of 1 or more leaves none,
- * the last v with r_v > 0.  Entries that are negative or NaN count as 0, and so does such a
- * sample_u.
+ * the sums good to 2^-41 + V 2^-58 of the whole; where rounding or a sample_u of 1 or
+ * more leaves none, the last v with r_v > 0.  Entries that are negative or NaN count
+ * as 0, and so does such a sample_u.
  * tokens int32 [B][d + 1] = the accepted drafts, the drawn token, then -1;
  * n int32 [B] = the number of them (no drawn token where p_j has no entry over 0,
- * or where the entries drawn from sum to more than fp32 holds).  d >= 0 (0: one draw from p; q, drafts and accept_u are not
- * read), d <= 1024, 1 <= V <= 2^30; 4-byte alignment. */
+ * or where the entries drawn from sum to more than fp32 holds).  0 <= d <= 1024 (0:
+ * one draw from p; q, drafts and accept_u are not read), 1 <= V <= 2^30; 4-byte
+ * alignment. */
 ssd_status ssd_op_verify_drafts(const float* p, const float* q, const int32_t* drafts,
                                 const int32_t* counts, const float* accept_u,
                                 const float* sample_u, int32_t B, int32_t d, int32_t V,

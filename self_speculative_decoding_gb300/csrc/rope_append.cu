@@ -5,9 +5,10 @@
 //   (x'_i, x'_{i + dh/2}) turned by the angle p theta^(-2 i / dh),
 // q rounded to bf16 into q, k' and v into row (length + t) % rows of the caches.
 //
-// Angles: a turn is 2^64, so that position * frequency wraps by itself and
-// keeps 2^-64 of a turn times the position, however far that is; the product's
-// upper half, exact to 2^-24 of a half turn as fp32, gives sine and cosine.
+// Angles: a turn is 2^64, so that position * frequency wraps by itself.  The
+// frequencies come from 64-bit floats and are good to 2^-54 of a turn (bases of 1 or
+// more), which is 2^-22 of a half turn at position 2^31; the product's upper half, as
+// fp32 good to 2^-25 of a half turn, gives sine and cosine.
 //
 // Bound by the bytes: fp32 in, bf16 out, once each.  8064 tokens of 120 heads: 743 MB
 // in 114 us, 6.5 TB/s, 97% of a plain copy's; one token: 2.3 us, a launch.  Roundings: q,
