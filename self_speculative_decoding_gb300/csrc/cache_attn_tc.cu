@@ -1103,7 +1103,8 @@ __global__ void __launch_bounds__(threads_of(kGroups), 1)
           if (j < t.rs || j >= t.re) r1 = 0;
           over = over && t.p0 + w4 * 32 < t.re && t.p0 + w4 * 32 + 32 > t.rs;
         }
-        // (a scale of 1 may be that of zeros, whose weight is none)
+        // (a scale of 1 may be that of zeros, whose weight is none; where all scales are 1 a pair's
+        // first tile is looked at for nothing, 1 us of 51 of one token over 131000 rows)
         if (seldom(over && eight && vc == 1.f) && rows_are_zero(a, s, t.p0 + w4 * 32, t.rs, t.re)) {
           over = false;
           vc = 0.f;
